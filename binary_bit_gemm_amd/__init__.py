@@ -380,6 +380,207 @@ def gemm_batched(problems: Sequence[Tuple["object", "object", "object", "object"
         _check(st, "lowbit_gemm_batched_ex")
 
 
+class QkProblem(ctypes.Structure):
+    """lowbit_qk_problem of include/lowbit.h."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "q_out", "k_out", "q_weight", "k_weight", "positions", "freqs")]
+                + [(n, ctypes.c_int64) for n in ("tokens", "q_token", "q_head", "k_token", "k_head", "q_out_token",
+                                                 "q_out_head", "k_out_token", "k_out_head")]
+                + [(n, ctypes.c_int32) for n in ("q_heads", "k_heads", "head_dim", "axes")]
+                + [("axis_dims", ctypes.c_int32 * 4), ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float)])
+
+
+def _heads(t, name: str, ndim: int):
+    """A bf16 device tensor [..., heads, head_dim] whose last dimension is contiguous (any other strides)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must be {ndim}-D, got shape {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU")
+    if t.stride(-1) != 1 and t.shape[-1] != 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+
+
+def _same_device(first, named) -> None:
+    """Every tensor of `named` on the device of `first` (the kernel runs there)."""
+    for name, t in named:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} must be on {first.device}, got {t.device}")
+
+
+def rope_freqs(axis_dims: Sequence[int], theta: float = 10000.0, device="cuda"):
+    """fp32 [sum(axis_dims) / 2]: theta^(-2i / axis_dims[a]) for pair i of each axis a, the usual choice of
+    qk_norm_rope's `freqs` (any other, e.g. scaled for longer contexts, can be passed as well)."""
+    torch = _torch()
+    parts = [theta ** (-torch.arange(0, d, 2, dtype=torch.float64) / d) for d in axis_dims]
+    return (torch.cat(parts) if parts else torch.empty(0, dtype=torch.float64)).to(torch.float32).to(device)
+
+
+def qk_norm_rope(q, k, positions, freqs, axis_dims: Sequence[int], q_weight=None, k_weight=None, eps: float = 1e-6,
+                 interleaved: bool = True, q_out=None, k_out=None):
+    """RMS norm of every head of q [tokens, q_heads, D] and k [tokens, k_heads, D] (bf16, any strides of
+    whole 16-byte pieces, e.g. views of a fused QKV output) and their rotation by `positions` (int32 [tokens, axes]) and `freqs`
+    (fp32, radians per unit position and pair), in one pass (lowbit_qk_norm_rope).
+
+    A weight of None leaves that tensor unnormed; axis_dims = () leaves both unturned (positions and
+    freqs may then be None).  `interleaved` pairs neighbouring elements, otherwise element i goes with i +
+    sum(axis_dims) / 2.  q_out / k_out may be q / k themselves.  Returns (q_out, k_out)."""
+    torch = _torch()
+    _heads(q, "q", 3)
+    _heads(k, "k", 3)
+    T, Hq, D = q.shape
+    Hk = k.shape[1]
+    if k.shape[0] != T or k.shape[2] != D:
+        raise ValueError(f"k must be [{T}, heads, {D}], got {tuple(k.shape)}")
+    axes = len(axis_dims)
+    if axes > 4:
+        raise ValueError("at most 4 axes")
+    if axes:
+        _require(positions, torch.int32, "positions")
+        _require(freqs, torch.float32, "freqs", ndim=1)
+        if tuple(positions.shape) != (T, axes):
+            raise ValueError(f"positions must be [{T}, {axes}], got {tuple(positions.shape)}")
+        if 2 * freqs.shape[0] != sum(axis_dims):
+            raise ValueError(f"freqs must hold sum(axis_dims) / 2 = {sum(axis_dims) // 2} values, got {freqs.shape[0]}")
+    else:
+        positions = freqs = None
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _require(w, torch.bfloat16, name, ndim=1)
+            if w.shape[0] != D:
+                raise ValueError(f"{name} must be [{D}]")
+    if q_out is None:
+        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    if k_out is None:
+        k_out = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=q.device)
+    for name, o, like in (("q_out", q_out, q), ("k_out", k_out, k)):
+        _heads(o, name, 3)
+        if o.shape != like.shape:
+            raise ValueError(f"{name} must be {tuple(like.shape)}")
+    _same_device(q, (("k", k), ("positions", positions), ("freqs", freqs), ("q_weight", q_weight), ("k_weight", k_weight),
+                     ("q_out", q_out), ("k_out", k_out)))
+
+    def ptr(t):
+        return None if t is None or t.numel() == 0 else t.data_ptr()
+
+    dims = (ctypes.c_int32 * 4)(*axis_dims)
+    p = QkProblem(ptr(q), ptr(k), ptr(q_out), ptr(k_out), ptr(q_weight), ptr(k_weight), ptr(positions), ptr(freqs), T,
+                  *_strides(q), *_strides(k), *_strides(q_out), *_strides(k_out), Hq, Hk, D, axes, dims,
+                  1 if interleaved else 0, eps)
+    with _on(q.device):
+        _check(lib().lowbit_qk_norm_rope(ctypes.byref(p), _stream_ptr(q.device)), "lowbit_qk_norm_rope")
+    return q_out, k_out
+
+
+def _strides(t):
+    """Strides of every dimension but the last, 0 for dimensions of one element (whose stride says nothing)."""
+    return [s if n > 1 else 0 for s, n in zip(t.stride()[:-1], t.shape[:-1])]
+
+
+class _on:
+    """The tensors' device made current for the call, where it is not already (a launch goes to the current device)."""
+
+    def __init__(self, device):
+        self.device = device
+        self.guard = None
+
+    def __enter__(self):
+        torch = _torch()
+        if self.device.index is not None and self.device.index != torch.cuda.current_device():
+            self.guard = torch.cuda.device(self.device)
+            self.guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self.guard is not None:
+            self.guard.__exit__(*exc)
+
+
+class AttentionProblem(ctypes.Structure):
+    """lowbit_attention_problem of include/lowbit.h."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "o", "key_mask", "key_lens", "q_start")]
+                + [(n, ctypes.c_int64) for n in ("batch", "q_len", "kv_len", "q_batch", "q_token", "q_head", "k_batch",
+                                                 "k_token", "k_head", "v_batch", "v_token", "v_head", "o_batch", "o_token",
+                                                 "o_head", "mask_batch")]
+                + [(n, ctypes.c_int32) for n in ("q_heads", "kv_heads", "head_dim", "causal")] + [("scale", ctypes.c_float)])
+
+
+def _attention_problem(q, k, v, key_mask, key_lens, causal, q_start, scale, out):
+    torch = _torch()
+    for name, t in (("q", q), ("k", k), ("v", v)):
+        _heads(t, name, 4)
+    B, Lq, Hq, D = q.shape
+    Lk, Hk = k.shape[1], k.shape[2]
+    if k.shape[0] != B or k.shape[3] != D or v.shape != k.shape:
+        raise ValueError(f"k and v must be [{B}, keys, kv_heads, {D}], got {tuple(k.shape)} and {tuple(v.shape)}")
+    if key_mask is not None:
+        if not isinstance(key_mask, torch.Tensor) or key_mask.dtype not in (torch.bool, torch.uint8):
+            raise TypeError("key_mask must be a bool or uint8 torch.Tensor")
+        if tuple(key_mask.shape) != (B, Lk) or (Lk > 1 and key_mask.stride(1) != 1):
+            raise ValueError(f"key_mask must be [{B}, {Lk}], contiguous along the keys")
+        if not key_mask.is_cuda:
+            raise ValueError("key_mask must be on a GPU")
+    for name, t in (("key_lens", key_lens), ("q_start", q_start)):
+        if t is not None:
+            _require(t, torch.int32, name, ndim=1)
+            if t.shape[0] != B:
+                raise ValueError(f"{name} must be [{B}]")
+    if q_start is not None and not causal:
+        q_start = None  # positions matter to the causal rule only
+    if out is not None:
+        _heads(out, "out", 4)
+        if out.shape != q.shape:
+            raise ValueError(f"out must be {tuple(q.shape)}")
+    _same_device(q, (("k", k), ("v", v), ("key_mask", key_mask), ("key_lens", key_lens), ("q_start", q_start), ("out", out)))
+
+    def ptr(t):
+        return None if t is None or t.numel() == 0 else t.data_ptr()
+
+    return AttentionProblem(
+        ptr(q), ptr(k), ptr(v), ptr(out), ptr(key_mask), ptr(key_lens), ptr(q_start), B, Lq, Lk,
+        *_strides(q), *_strides(k), *_strides(v), *(_strides(out) if out is not None else (Lq * Hq * D, Hq * D, D)),
+        _strides(key_mask)[0] if key_mask is not None else 0, Hq, Hk, D, 1 if causal else 0,
+        scale if scale is not None else (D ** -0.5 if D else 1.0))
+
+
+def attention_workspace_size(q, k, v) -> int:
+    """Bytes of workspace attention(q, k, v, ...) can use (0: none)."""
+    p = _attention_problem(q, k, v, None, None, False, None, None, None)
+    return int(lib().lowbit_attention_workspace_size(ctypes.byref(p)))
+
+
+def attention(q, k, v, key_mask=None, key_lens=None, causal: bool = False, q_start=None, scale=None, out=None,
+              workspace=None):
+    """softmax(scale * q k^T) v in bf16 (lowbit_attention): q [batch, q_len, q_heads, D], k and v [batch, kv_len,
+    kv_heads, D] with any strides of whole 16-byte pieces (views of a fused QKV output, a cache), D 64 or 128, q_heads a multiple of
+    kv_heads.  Query t takes key j where key_mask[b, j] (bool), j < key_lens[b] and, if causal, j <= q_start[b] + t (None: 0);
+    a query without keys gets zeros.  scale: 1 / sqrt(D) by default.
+
+    `workspace`: an optional device tensor of at least attention_workspace_size(q, k, v) bytes, with
+    which few rows over many keys run split along the keys; do not share it between calls that run
+    concurrently."""
+    torch = _torch()
+    if out is None:
+        _heads(q, "q", 4)
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    p = _attention_problem(q, k, v, key_mask, key_lens, causal, q_start, scale, out)
+    ws, nbytes = _workspace(workspace, q)
+    with _on(q.device):
+        _check(lib().lowbit_attention(ctypes.byref(p), ws, nbytes, _stream_ptr(q.device)), "lowbit_attention")
+    return out
+
+
+def _workspace(workspace, like):
+    if workspace is None:
+        return None, 0
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous device tensor")
+    _same_device(like, (("workspace", workspace),))
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def check_gemm_args(x_ptr: int, w_ptr: int, s_ptr: int, y_ptr: int, M: int, N: int, K: int, g: int,
                     bits: int) -> int:
     """Host-only validation (no HIP call); returns the status code lowbit_gemm would return."""

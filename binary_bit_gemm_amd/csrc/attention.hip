@@ -1,0 +1,418 @@
+// Attention over grouped heads: O = softmax(scale * Q K^T, over the allowed keys) V.
+//
+// Row r of a kv head's problem is query token r / G of its q head r % G (G q heads share a kv head), so
+// the heads of a group read each key and value once, also where there is one query token.  Keys go by
+// in tiles, with the running maximum m and sum l of the softmax per row (one pass):
+//     p = exp2(c s - c m),  l += sum p,  O += p v,      c = scale * log2(e);
+// where m grows, l and O are multiplied by exp2(c m_old - c m_new).
+//
+// The products are computed transposed, S^T = K Q^T and O^T = V^T P^T, with 32x32x16 MFMAs: a lane
+// then holds 16 scores of one query per 32 keys (lane l: query l % 32, keys 8 (i / 4) + 4 (l / 32) + i % 4),
+// so the row maximum is an in-lane maximum and one exchange between the two lane halves, the
+// factors of m and l are one number per lane, and the probabilities, rounded to bf16 in pairs, are
+// already the B operand of the second product: its K order is the order in which the lane holds
+// them, and V^T is read from LDS in that order by transposing reads (4 keys x 16 columns each).
+//
+// Rounding to bf16: the probabilities before the second product (the matrix cores' input; relative
+// 2^-8 each, averaged over the keys) and O at the store.  Scores, m, l and O are fp32.
+#include "lowbit_device.h"
+#include "lowbit_internal.h"
+
+namespace lowbit {
+namespace {
+
+typedef short s16x4_t __attribute__((ext_vector_type(4)));
+
+constexpr float kNegInf = -__builtin_inff();
+// A maximum that grows by less than this (in powers of two) leaves m as it is: p then reaches 2^8
+// instead of 1, which fp32 sums and the bf16 mantissa do not notice, and O is not rescaled.
+constexpr float kLazy = 8.f;
+
+// ---- layouts in LDS: rows of D elements in 16-byte chunks, chunk c of row r at position c ^ swz(r) ----
+// K is read 16 bytes per lane from 32 consecutive rows at one chunk; 16 rows must land in 16 different
+// 16-byte bank groups of the 256-byte line.
+template <int D>
+__device__ __forceinline__ int k_swz(int r) {
+    return D == 128 ? (r & 15) : ((r >> 1) & 7);
+}
+// V is read by transposing reads, 8 bytes per lane: 16 lanes take 4 rows x 32 bytes, the wave instruction
+// rows 4h .. 4h+3 x 64 bytes.  The four rows' 64-byte windows must not share banks.
+template <int D>
+__device__ __forceinline__ int v_swz(int r) {
+    return D == 128 ? (r & 3) << 2 : ((r >> 1) & 1) << 2;
+}
+
+// One wave's state for 32 rows.
+template <int D>
+struct Rows {
+    bf16x8_t q[D / 16];   // B operand: lane (query l % 32, h): elements 16 kk + 8 h ..
+    f32x16_t o[D / 32];   // O^T
+    float m, l;           // the softmax's maximum (raw scores) and the lane half's share of its sum
+};
+
+template <int D>
+__device__ __forceinline__ void rows_init(Rows<D>& w) {
+#pragma unroll
+    for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) w.o[b][i] = 0.f;
+    w.m = kNegInf;
+    w.l = 0.f;
+}
+
+__device__ __forceinline__ float other_half(float v) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+}
+
+__device__ __forceinline__ bool bf16_finite(short v) { return (v & 0x7F80) != 0x7F80; }
+
+// Infinities and NaN of a tile's V, which the matrix product left out (0 * inf is NaN there, also for the
+// queries that do not take the key): added to the queries that take them, one key after the other.
+// What a positive probability times an infinity or a NaN gives is that infinity or NaN.
+template <int D, int NKB>
+__device__ __forceinline__ void add_nonfinite(Rows<D>& w, const unsigned char* vt, uint64_t allowed) {
+    const int h = (int(threadIdx.x) >> 5) & 1;
+    for (int j = 0; j < 32 * NKB; ++j) {
+        const bool mine = (allowed >> j) & 1;
+        if (!__any(mine)) continue;
+#pragma unroll
+        for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const s16x4_t v = *reinterpret_cast<const s16x4_t*>(vt + j * (2 * D) + (((4 * b + e) ^ v_swz<D>(j)) << 4) + 8 * h);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (mine && !bf16_finite(v[i])) w.o[b][4 * e + i] += __uint_as_float(uint32_t(uint16_t(v[i])) << 16);
+            }
+    }
+}
+
+// NKB * 32 keys of a tile in LDS at kt, vt.  allowed: bit i of the lane's word says whether the lane's
+// query takes key i; PARTIAL: not all of them are set in every lane.  live: the keys that any
+// query may take (padding excluded); V rows of the others count as zeros, whatever they hold.
+template <int D, int NKB, bool PARTIAL>
+__device__ __forceinline__ void tile_step(Rows<D>& w, const unsigned char* kt, const unsigned char* vt, float c,
+                                          uint64_t allowed, uint64_t live) {
+    const int lane = int(threadIdx.x) & 63;
+    const int l32 = lane & 31, h = lane >> 5;
+    f32x16_t s[NKB];
+#pragma unroll
+    for (int kb = 0; kb < NKB; ++kb) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) s[kb][i] = 0.f;
+        const int r = 32 * kb + l32;
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+            const bf16x8_t a = *reinterpret_cast<const bf16x8_t*>(kt + r * (2 * D) + (((2 * kk + h) ^ k_swz<D>(r)) << 4));
+            s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, w.q[kk], s[kb], 0, 0, 0);
+        }
+    }
+    if constexpr (PARTIAL) {
+        const uint64_t mine = allowed >> (4 * h);
+#pragma unroll
+        for (int kb = 0; kb < NKB; ++kb) {
+            const uint32_t bits = uint32_t(mine >> (32 * kb));
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[kb][i] = (bits >> (8 * (i / 4) + i % 4)) & 1u ? s[kb][i] : kNegInf;
+        }
+    }
+    float top = s[0][0];
+#pragma unroll
+    for (int kb = 0; kb < NKB; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kb][i]);
+    top = fmaxf(top, other_half(top));
+    // grow m where a row of the wave needs it
+    if (__any((top - w.m) * c > kLazy || (w.m == kNegInf && top != kNegInf))) {
+        const float m = fmaxf(w.m, top);
+        const float f = m == kNegInf ? 1.f : __builtin_amdgcn_exp2f((w.m - m) * c);
+        w.m = m;
+        w.l *= f;
+#pragma unroll
+        for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) w.o[b][i] *= f;
+    }
+    const float mc = w.m == kNegInf ? 0.f : w.m * c;
+    float sum = 0.f;
+#pragma unroll
+    for (int kb = 0; kb < NKB; ++kb)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            s[kb][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i], c, -mc));
+            sum += s[kb][i];
+        }
+    w.l += sum;
+    const int i16 = lane & 15, dsel = (lane >> 4) & 1;
+    bool odd = false;  // an infinity or a NaN in a live row of V
+#pragma unroll
+    for (int k2 = 0; k2 < 2 * NKB; ++k2) {  // 16 keys each
+        bf16x8_t p;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) p[i] = static_cast<__bf16>(s[k2 / 2][8 * (k2 % 2) + i]);
+#pragma unroll
+        for (int b = 0; b < D / 32; ++b) {
+            s16x4_t v[2];
+#pragma unroll
+            for (int part = 0; part < 2; ++part) {
+                const int r = 16 * k2 + 8 * part + 4 * h + (i16 >> 2);
+                const int chunk = 4 * b + 2 * dsel + ((i16 & 3) >> 1);
+                v[part] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                    (__attribute__((address_space(3))) s16x4_t*)(vt + r * (2 * D) + ((chunk ^ v_swz<D>(r)) << 4) +
+                                                                  8 * (i16 & 1)));
+                if constexpr (PARTIAL) {
+                    const uint32_t keys = uint32_t(live >> (16 * k2 + 8 * part + 4 * h));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool take = (keys >> i) & 1u, fine = bf16_finite(v[part][i]);
+                        odd = odd || (take && !fine);
+                        v[part][i] = take && fine ? v[part][i] : short(0);
+                    }
+                }
+            }
+            typedef short s16x8_t __attribute__((ext_vector_type(8)));
+            const s16x8_t a = __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7);
+            w.o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), p, w.o[b], 0, 0, 0);
+        }
+    }
+    if constexpr (PARTIAL) {
+        if (__any(odd)) add_nonfinite<D, NKB>(w, vt, allowed);
+    }
+}
+
+// The rows' Q operands (rows past the last read as zeros).
+template <int D>
+__device__ __forceinline__ void load_q(Rows<D>& w, const AttnArgs& a, int b, int hk, int row) {
+    const int h = (int(threadIdx.x) >> 5) & 1;
+    const bool in = row < a.rows;
+    const int t = in ? row / a.group : 0, g = in ? row - t * a.group : 0;
+    const uint16_t* src = a.q + int64_t(b) * a.q_batch + int64_t(t) * a.q_token + int64_t(hk * a.group + g) * a.q_head;
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+        u32x4_t v = {0, 0, 0, 0};
+        if (in) v = *reinterpret_cast<const u32x4_t*>(src + 16 * kk + 8 * h);
+        w.q[kk] = __builtin_bit_cast(bf16x8_t, v);
+    }
+}
+
+// O of one row (its lane pair) to memory, scaled by f: 16 bytes per lane and 32 columns after an exchange
+// between the lane halves (each half holds 4 of every 8 consecutive columns).
+template <int D>
+__device__ __forceinline__ void store_o(const Rows<D>& w, const AttnArgs& a, int b, int hk, int row, float f) {
+    const int h = (int(threadIdx.x) >> 5) & 1;
+    const bool in = row < a.rows;
+    const int t = in ? row / a.group : 0, g = in ? row - t * a.group : 0;
+    uint16_t* dst = a.o + int64_t(b) * a.o_batch + int64_t(t) * a.o_token + int64_t(hk * a.group + g) * a.o_head;
+    auto pair = [&](float x, float y) {
+        return uint32_t(float_to_bf16_bits(x * f)) | (uint32_t(float_to_bf16_bits(y * f)) << 16);
+    };
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            // columns 32 d + 16 e + (0..7 | 8..15), four of each eight per half
+            const uint32_t x0 = pair(w.o[d][8 * e], w.o[d][8 * e + 1]), x1 = pair(w.o[d][8 * e + 2], w.o[d][8 * e + 3]);
+            const uint32_t y0 = pair(w.o[d][8 * e + 4], w.o[d][8 * e + 5]), y1 = pair(w.o[d][8 * e + 6], w.o[d][8 * e + 7]);
+            const auto s0 = __builtin_amdgcn_permlane32_swap(x0, y0, false, false);
+            const auto s1 = __builtin_amdgcn_permlane32_swap(x1, y1, false, false);
+            if (in) *reinterpret_cast<u32x4_t*>(dst + 32 * d + 16 * e + 8 * h) = u32x4_t{s0[0], s1[0], s0[1], s1[1]};
+        }
+}
+
+// Partial results of one row for the join: O unnormalised, then (c m, l).
+template <int D>
+__device__ __forceinline__ void store_part(const Rows<D>& w, const AttnArgs& a, int64_t part_row, bool in, float l) {
+    const int h = (int(threadIdx.x) >> 5) & 1;
+    if (!in) return;
+    float* dst = a.part + part_row * D;
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            *reinterpret_cast<f32x4_t*>(dst + 32 * d + 8 * e + 4 * h) =
+                f32x4_t{w.o[d][4 * e], w.o[d][4 * e + 1], w.o[d][4 * e + 2], w.o[d][4 * e + 3]};
+    if (h == 0) {
+        a.part_ml[2 * part_row] = w.m == kNegInf ? kNegInf : w.m * a.scale_log2;
+        a.part_ml[2 * part_row + 1] = l;
+    }
+}
+
+// Keys [0, n) that a batch entry holds at all.
+__device__ __forceinline__ int live_keys(const AttnArgs& a, int b) {
+    int n = a.kv_len;
+    if (a.lens != nullptr) {
+        const int v = a.lens[b];
+        n = v < 0 ? 0 : v < n ? v : n;
+    }
+    return n;
+}
+
+// Bits of the keys key0 .. key0 + width - 1 that the mask and the length leave (wave-uniform).
+__device__ __forceinline__ uint64_t live_bits(const AttnArgs& a, int b, int key0, int width, int n) {
+    const int lane = int(threadIdx.x) & 63;
+    const bool in = lane < width && key0 + lane < n;
+    if (a.mask == nullptr) return __ballot(in);
+    return __ballot(in && a.mask[int64_t(b) * a.mask_batch + key0 + lane] != 0);
+}
+
+// Bits 0 .. rel (none for rel < 0).
+__device__ __forceinline__ uint64_t up_to(int64_t rel) {
+    return rel < 0 ? 0ull : rel >= 63 ? ~0ull : (2ull << rel) - 1;
+}
+
+// Long rows: a workgroup of 4 waves takes 128 rows of one kv head, a wave 32 of them; tiles of 64 keys go
+// through LDS, double-buffered, by direct copies one tile ahead.
+template <int D>
+__global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
+    constexpr int kTile = 64 * D * 2;
+    constexpr int kRowsPerCopy = 512 / D;         // rows that one wave-wide 16-byte copy brings
+    constexpr int kCopies = 64 / kRowsPerCopy / 4;  // copies per wave and tile
+    __shared__ __attribute__((aligned(1024))) unsigned char kbuf[2][kTile];
+    __shared__ __attribute__((aligned(1024))) unsigned char vbuf[2][kTile];
+    const int lane = int(threadIdx.x) & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    // tiles of one head next to each other, heads of one XCD together
+    int id = xcd_remap(int(blockIdx.x), int(gridDim.x));
+    const int rt = id % a.row_tiles;
+    id /= a.row_tiles;
+    const int split = id % a.splits;
+    id /= a.splits;
+    const int hk = id % a.kv_heads, b = id / a.kv_heads;
+
+    const int n = live_keys(a, b);
+    const int row = rt * 128 + wave * 32 + (lane & 31);
+    const int64_t start = a.causal ? (a.start != nullptr ? a.start[b] : 0) : 0;
+    // the last key of the workgroup's and of the lane's rows
+    const int last_row = rt * 128 + 127 < a.rows ? rt * 128 + 127 : a.rows - 1;
+    const int64_t last = a.causal ? start + last_row / a.group : int64_t(n) - 1;
+    const int64_t mine = a.causal ? start + (row < a.rows ? row : a.rows - 1) / a.group : int64_t(1) << 40;
+    const int64_t end64 = last + 1 < n ? last + 1 : n;
+    const int end = end64 < 0 ? 0 : int(end64);
+    const int tiles = (end + 63) / 64;
+    const int t0 = split * a.tiles_per_split;
+    const int t1 = t0 + a.tiles_per_split < tiles ? t0 + a.tiles_per_split : tiles;
+
+    Rows<D> w;
+    rows_init(w);
+    load_q(w, a, b, hk, row);
+
+    const uint16_t* kb = a.k + int64_t(b) * a.k_batch + int64_t(hk) * a.k_head;
+    const uint16_t* vb = a.v + int64_t(b) * a.v_batch + int64_t(hk) * a.v_head;
+    uint32_t koff[kCopies], voff[kCopies];
+#pragma unroll
+    for (int i = 0; i < kCopies; ++i) {
+        const int r = (wave * kCopies + i) * kRowsPerCopy + lane / (D / 8), p = lane % (D / 8);
+        koff[i] = uint32_t(r) * uint32_t(a.k_token) * 2u + uint32_t(p ^ k_swz<D>(r)) * 16u;
+        voff[i] = uint32_t(r) * uint32_t(a.v_token) * 2u + uint32_t(p ^ v_swz<D>(r)) * 16u;
+    }
+    auto issue = [&](int t, int buf) __attribute__((always_inline)) {
+        const int have = n - 64 * t < 64 ? n - 64 * t : 64;  // rows past the last key come as zeros
+        const auto kr = make_rsrc(kb + int64_t(64) * t * a.k_token, uint32_t(have - 1) * uint32_t(a.k_token) * 2u + 2u * D);
+        const auto vr = make_rsrc(vb + int64_t(64) * t * a.v_token, uint32_t(have - 1) * uint32_t(a.v_token) * 2u + 2u * D);
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) dma16(kr, kbuf[buf] + (wave * kCopies + i) * 1024, koff[i], 0);
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) dma16(vr, vbuf[buf] + (wave * kCopies + i) * 1024, voff[i], 0);
+    };
+    if (t0 < t1) issue(t0, 0);
+    for (int t = t0; t < t1; ++t) {
+        const int buf = (t - t0) & 1;
+        wait_vmcnt<0>();
+        __syncthreads();  // tile t is there, and every wave is done with the other buffer
+        const uint64_t live = live_bits(a, b, 64 * t, 64, n);
+        if (t + 1 < t1) issue(t + 1, buf ^ 1);
+        const uint64_t allowed = live & up_to(mine - 64 * int64_t(t));
+        if (__all(allowed == ~0ull))
+            tile_step<D, 2, false>(w, kbuf[buf], vbuf[buf], a.scale_log2, 0, 0);
+        else if (__any(allowed != 0))
+            tile_step<D, 2, true>(w, kbuf[buf], vbuf[buf], a.scale_log2, allowed, live);
+    }
+    const float l = w.l + other_half(w.l);
+    if (a.splits == 1) {
+        store_o(w, a, b, hk, row, l > 0.f || l != l ? 1.f / l : 0.f);
+    } else {
+        const int64_t base = ((int64_t(b) * a.kv_heads + hk) * a.splits + split) * a.rows;
+        store_part(w, a, base + row, row < a.rows, l);
+    }
+}
+
+// Joins the splits' partial results of a row, in split order: a wave per row.
+template <int D>
+__global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
+    const int lane = int(threadIdx.x) & 63;
+    const int64_t id = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    if (id >= int64_t(a.batch) * a.kv_heads * a.rows) return;
+    const int row = int(id % a.rows);
+    const int64_t bh = id / a.rows;
+    const int64_t base = bh * a.splits * a.rows + row;
+    float m = kNegInf;
+    for (int s = 0; s < a.splits; ++s) m = fmaxf(m, a.part_ml[2 * (base + int64_t(s) * a.rows)]);
+    float l = 0.f, o[D / 64];
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) o[e] = 0.f;
+    for (int s = 0; s < a.splits; ++s) {
+        const int64_t r = base + int64_t(s) * a.rows;
+        const float ms = a.part_ml[2 * r];
+        const float f = ms == kNegInf ? 0.f : __builtin_amdgcn_exp2f(ms - m);
+        l += f * a.part_ml[2 * r + 1];
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e) o[e] = __builtin_fmaf(f, a.part[r * D + (D / 64) * lane + e], o[e]);
+    }
+    const float f = l > 0.f || l != l ? 1.f / l : 0.f;
+    const int b = int(bh / a.kv_heads), hk = int(bh % a.kv_heads);
+    const int t = row / a.group, g = row - t * a.group;
+    uint16_t* dst = a.o + int64_t(b) * a.o_batch + int64_t(t) * a.o_token + int64_t(hk * a.group + g) * a.o_head;
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) dst[(D / 64) * lane + e] = float_to_bf16_bits(o[e] * f);
+}
+
+template <int D>
+hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
+    const int64_t grid = int64_t(a.row_tiles) * a.splits * a.kv_heads * a.batch;
+    hipLaunchKernelGGL((attention_kernel<D>), dim3(unsigned(grid)), dim3(256), 0, stream, a);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.splits == 1) return e;
+    const int64_t rows = int64_t(a.batch) * a.kv_heads * a.rows;
+    hipLaunchKernelGGL((attention_join_kernel<D>), dim3(unsigned((rows + 3) / 4)), dim3(256), 0, stream, a);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+// Splits along the keys: where the row tiles leave compute units idle, about two workgroups per
+// compute unit, each with four key tiles at least.
+AttnPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t kv_len, int head_dim) {
+    AttnPlan p;
+    p.row_tiles = int(tiles_of(rows, 128));
+    const int64_t tiles = tiles_of(kv_len, 64), base = batch * kv_heads * p.row_tiles;
+    int64_t splits = base >= kComputeUnits ? 1 : 2 * kComputeUnits / base;
+    const int64_t most = tiles / 4;
+    splits = splits < most ? splits : most;
+    splits = splits < 1 ? 1 : splits;
+    p.tiles_per_split = int(tiles_of(tiles, splits));
+    p.splits = int(tiles_of(tiles, p.tiles_per_split > 0 ? p.tiles_per_split : 1));
+    if (p.splits < 1) p.splits = 1;
+    p.part_rows = p.splits > 1 ? batch * kv_heads * rows * p.splits : 0;
+    p.bytes = size_t(p.part_rows) * (size_t(head_dim) + 2) * 4u;
+    return p;
+}
+
+AttnPlan plan_attention_unsplit(AttnPlan p, int64_t kv_len) {
+    p.splits = 1;
+    p.tiles_per_split = int(tiles_of(kv_len, 64));
+    p.part_rows = 0;
+    p.bytes = 0;
+    return p;
+}
+
+hipError_t launch_attention(AttnArgs a, int head_dim, const AttnPlan& plan, void* workspace, hipStream_t stream) {
+    a.row_tiles = plan.row_tiles;
+    a.splits = plan.splits;
+    a.tiles_per_split = plan.tiles_per_split;
+    a.part = static_cast<float*>(workspace);
+    a.part_ml = a.part + plan.part_rows * head_dim;
+    return head_dim == 64 ? launch_d<64>(a, stream) : launch_d<128>(a, stream);
+}
+
+}  // namespace lowbit

@@ -1,0 +1,197 @@
+// C-ABI of the operators around the packed linears: argument checks and launch.  As in lowbit_api.cpp,
+// every check runs before any HIP call, and nothing here allocates or throws.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstring>
+
+#include "../../include/lowbit.h"
+#include "lowbit_internal.h"
+
+namespace {
+
+bool aligned(const void* p, uintptr_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
+constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxStride = int64_t(1) << 40;
+constexpr int kMaxHeads = 1 << 16;
+
+bool stride_ok(int64_t s) { return s >= 0 && s <= kMaxStride && s % 8 == 0; }
+
+// Whether [tokens, heads] rows of `dim` elements at these strides lie apart (outputs).
+bool apart(int64_t tokens, int64_t token, int64_t heads, int64_t head, int64_t dim) {
+    if (tokens <= 1 && heads <= 1) return true;
+    if (tokens <= 1) return head >= dim;
+    if (heads <= 1) return token >= dim;
+    return head <= token ? head >= dim && token >= (heads - 1) * head + dim
+                         : token >= dim && head >= (tokens - 1) * token + dim;
+}
+
+// The same for [batch, tokens, heads] rows.
+bool apart3(int64_t batch, int64_t batch_stride, int64_t tokens, int64_t token, int64_t heads, int64_t head, int64_t dim) {
+    int64_t n[3] = {batch, tokens, heads}, st[3] = {batch_stride, token, head};
+    for (int i = 0; i < 2; ++i)  // by stride, smallest first
+        for (int j = 0; j < 2 - i; ++j)
+            if (st[j] > st[j + 1]) {
+                const int64_t a = n[j], b = st[j];
+                n[j] = n[j + 1];
+                st[j] = st[j + 1];
+                n[j + 1] = a;
+                st[j + 1] = b;
+            }
+    int64_t span = dim;  // elements that the dimensions so far cover
+    for (int i = 0; i < 3; ++i) {
+        if (n[i] <= 1) continue;
+        if (st[i] < span) return false;
+        span += (n[i] - 1) * st[i];
+    }
+    return true;
+}
+
+constexpr int64_t kMaxTokenStride = int64_t(1) << 24;  // 64 rows of keys within a 32-bit byte range
+
+// The checks of lowbit_attention that read no tensor pointer, and the launch arguments.
+int attention_args(const lowbit_attention_problem* p, lowbit::AttnArgs& a) {
+    if (p == nullptr) return LOWBIT_E_INVALID;
+    if (p->head_dim != 64 && p->head_dim != 128) return LOWBIT_E_UNSUPPORTED;
+    if (p->batch < 0 || p->q_heads < 0 || p->kv_heads < 0 || p->q_len < 0 || p->kv_len < 0) return LOWBIT_E_INVALID;
+    if (p->q_len > kMaxDim || p->kv_len > kMaxDim - 64) return LOWBIT_E_UNSUPPORTED;
+    if (p->q_heads > kMaxHeads || p->batch > kMaxHeads) return LOWBIT_E_UNSUPPORTED;
+    if (p->kv_heads == 0 ? p->q_heads != 0 : p->q_heads % p->kv_heads != 0) return LOWBIT_E_INVALID;
+    if (!(p->scale > 0.f) || std::isinf(p->scale)) return LOWBIT_E_INVALID;
+    for (int64_t s : {p->q_batch, p->q_token, p->q_head, p->k_batch, p->k_token, p->k_head, p->v_batch, p->v_token,
+                      p->v_head, p->o_batch, p->o_token, p->o_head})
+        if (!stride_ok(s)) return LOWBIT_E_INVALID;
+    if (p->mask_batch < 0 || p->mask_batch > kMaxStride) return LOWBIT_E_INVALID;
+    if (p->kv_len > 1 && (p->k_token < p->head_dim || p->v_token < p->head_dim)) return LOWBIT_E_INVALID;
+    if (p->k_token > kMaxTokenStride || p->v_token > kMaxTokenStride) return LOWBIT_E_UNSUPPORTED;
+    if (!apart3(p->batch, p->o_batch, p->q_len, p->o_token, p->q_heads, p->o_head, p->head_dim)) return LOWBIT_E_INVALID;
+    a.group = p->kv_heads > 0 ? p->q_heads / p->kv_heads : 1;
+    const int64_t rows = int64_t(p->q_len) * a.group;
+    if (rows > kMaxDim - 128 || (rows + 127) / 128 * p->kv_heads * p->batch > kMaxDim / 64) return LOWBIT_E_UNSUPPORTED;
+    a.q_batch = p->q_batch;
+    a.q_token = p->q_token;
+    a.q_head = p->q_head;
+    a.k_batch = p->k_batch;
+    a.k_token = p->kv_len > 1 ? p->k_token : p->head_dim;
+    a.k_head = p->k_head;
+    a.v_batch = p->v_batch;
+    a.v_token = p->kv_len > 1 ? p->v_token : p->head_dim;
+    a.v_head = p->v_head;
+    a.o_batch = p->o_batch;
+    a.o_token = p->o_token;
+    a.o_head = p->o_head;
+    a.mask_batch = p->mask_batch;
+    a.batch = int(p->batch);
+    a.kv_heads = p->kv_heads;
+    a.rows = int(rows);
+    a.kv_len = int(p->kv_len);
+    a.causal = p->causal != 0;
+    a.scale_log2 = float(double(p->scale) * 1.4426950408889634074);
+    a.q = static_cast<const uint16_t*>(p->q);
+    a.k = static_cast<const uint16_t*>(p->k);
+    a.v = static_cast<const uint16_t*>(p->v);
+    a.o = static_cast<uint16_t*>(p->o);
+    a.mask = p->key_mask;
+    a.lens = p->key_lens;
+    a.start = p->q_start;
+    return LOWBIT_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t lowbit_attention_workspace_size(const lowbit_attention_problem* p) {
+    lowbit::AttnArgs a{};
+    if (attention_args(p, a) != LOWBIT_OK || a.batch == 0 || a.rows == 0) return 0;
+    return lowbit::plan_attention(a.batch, a.kv_heads, a.rows, a.kv_len, p->head_dim).bytes;
+}
+
+int lowbit_attention(const lowbit_attention_problem* p, void* workspace, size_t workspace_bytes, void* stream) {
+    lowbit::AttnArgs a{};
+    int st = attention_args(p, a);
+    if (st != LOWBIT_OK) return st;
+    if (a.batch == 0 || a.rows == 0) return LOWBIT_OK;
+    if (a.q == nullptr || a.o == nullptr) return LOWBIT_E_INVALID;
+    if (a.kv_len > 0 && (a.k == nullptr || a.v == nullptr)) return LOWBIT_E_INVALID;
+    for (const void* ptr : {p->q, p->k, p->v, static_cast<const void*>(p->o), static_cast<const void*>(workspace)})
+        if (!aligned(ptr, 16)) return LOWBIT_E_ALIGN;
+    if (!aligned(p->key_lens, 4) || !aligned(p->q_start, 4)) return LOWBIT_E_ALIGN;
+    st = lowbit::device_check();
+    if (st != LOWBIT_OK) return st;
+    lowbit::AttnPlan plan = lowbit::plan_attention(a.batch, a.kv_heads, a.rows, a.kv_len, p->head_dim);
+    if (plan.bytes > 0 && (workspace == nullptr || workspace_bytes < plan.bytes))
+        plan = lowbit::plan_attention_unsplit(plan, a.kv_len);
+    const hipError_t e = lowbit::launch_attention(a, p->head_dim, plan, workspace, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? LOWBIT_OK : lowbit::hip_fail(e);
+}
+
+int lowbit_qk_norm_rope(const lowbit_qk_problem* p, void* stream) {
+    if (p == nullptr) return LOWBIT_E_INVALID;
+    const int D = p->head_dim;
+    if (D != 32 && D != 64 && D != 128 && D != 256) return LOWBIT_E_UNSUPPORTED;
+    if (p->axes < 0 || p->axes > 4) return LOWBIT_E_UNSUPPORTED;
+    if (p->tokens < 0 || p->tokens > kMaxDim || p->q_heads < 0 || p->k_heads < 0) return LOWBIT_E_INVALID;
+    if (p->q_heads > kMaxHeads || p->k_heads > kMaxHeads) return LOWBIT_E_UNSUPPORTED;
+    lowbit::QkArgs a{};
+    int rot = 0;
+    for (int i = 0; i < p->axes; ++i) {
+        const int d = p->axis_dims[i];
+        if (d <= 0 || d % 2 != 0 || d > D) return LOWBIT_E_INVALID;
+        rot += d;
+        a.axis_end[i] = rot / 2;
+    }
+    if (rot % 16 != 0 || rot > D) return LOWBIT_E_INVALID;
+    for (int i = p->axes; i < 4; ++i) a.axis_end[i] = rot / 2;
+    if (!(p->eps >= 0.f) || std::isinf(p->eps)) return LOWBIT_E_INVALID;
+    for (int64_t s : {p->q_token, p->q_head, p->k_token, p->k_head, p->q_out_token, p->q_out_head, p->k_out_token,
+                      p->k_out_head})
+        if (!stride_ok(s)) return LOWBIT_E_INVALID;
+    if (p->tokens == 0 || p->q_heads + p->k_heads == 0) return LOWBIT_OK;
+    if (p->q_heads > 0 && (p->q == nullptr || p->q_out == nullptr)) return LOWBIT_E_INVALID;
+    if (p->k_heads > 0 && (p->k == nullptr || p->k_out == nullptr)) return LOWBIT_E_INVALID;
+    if (p->axes > 0 && (p->positions == nullptr || p->freqs == nullptr)) return LOWBIT_E_INVALID;
+    if (!apart(p->tokens, p->q_out_token, p->q_heads, p->q_out_head, D) ||
+        !apart(p->tokens, p->k_out_token, p->k_heads, p->k_out_head, D))
+        return LOWBIT_E_INVALID;
+    // in place: the same element order (a stride along a dimension of one element says nothing)
+    auto moved = [&](const void* in, const void* out, int heads, int64_t it, int64_t ih, int64_t ot, int64_t oh) {
+        return heads > 0 && in == out && ((p->tokens > 1 && it != ot) || (heads > 1 && ih != oh));
+    };
+    if (moved(p->q, p->q_out, p->q_heads, p->q_token, p->q_head, p->q_out_token, p->q_out_head) ||
+        moved(p->k, p->k_out, p->k_heads, p->k_token, p->k_head, p->k_out_token, p->k_out_head))
+        return LOWBIT_E_INVALID;
+    for (const void* ptr : {p->q, p->k, static_cast<const void*>(p->q_out), static_cast<const void*>(p->k_out),
+                            p->q_weight, p->k_weight})
+        if (!aligned(ptr, 16)) return LOWBIT_E_ALIGN;
+    if (!aligned(p->positions, 4) || !aligned(p->freqs, 4)) return LOWBIT_E_ALIGN;
+    const int st = lowbit::device_check();
+    if (st != LOWBIT_OK) return st;
+    a.q = static_cast<const uint16_t*>(p->q);
+    a.k = static_cast<const uint16_t*>(p->k);
+    a.q_out = static_cast<uint16_t*>(p->q_out);
+    a.k_out = static_cast<uint16_t*>(p->k_out);
+    a.q_weight = static_cast<const uint16_t*>(p->q_weight);
+    a.k_weight = static_cast<const uint16_t*>(p->k_weight);
+    a.positions = p->positions;
+    a.freqs = p->freqs;
+    a.tokens = p->tokens;
+    a.q_token = p->q_token;
+    a.q_head = p->q_head;
+    a.k_token = p->k_token;
+    a.k_head = p->k_head;
+    a.qo_token = p->q_out_token;
+    a.qo_head = p->q_out_head;
+    a.ko_token = p->k_out_token;
+    a.ko_head = p->k_out_head;
+    a.q_heads = p->q_heads;
+    a.k_heads = p->k_heads;
+    a.axes = p->axes;
+    a.rot = rot;
+    a.eps = p->eps;
+    const hipError_t e = lowbit::launch_qk_norm_rope(a, D, p->interleaved != 0, static_cast<hipStream_t>(stream));
+    return e == hipSuccess ? LOWBIT_OK : lowbit::hip_fail(e);
+}
+
+}  // extern "C"

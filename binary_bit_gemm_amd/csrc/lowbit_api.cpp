@@ -40,13 +40,31 @@ void trace_launch(const char* family, const char* config, int g, int bits, const
 }  // namespace lowbit
 
 namespace {
-
 thread_local int g_last_hip_error = 0;
+}
+
+namespace lowbit {
 
 int hip_fail(hipError_t e) {
     g_last_hip_error = int(e);
     return LOWBIT_E_HIP;
 }
+
+int device_check() {
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return hip_fail(e);
+    const int r = lowbit_device_supported(dev);
+    if (r < 0) return LOWBIT_E_HIP;
+    return r == 1 ? LOWBIT_OK : LOWBIT_E_UNSUPPORTED;
+}
+
+}  // namespace lowbit
+
+namespace {
+
+using lowbit::device_check;
+using lowbit::hip_fail;
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -73,15 +91,6 @@ int check_pack_args(const void* codes, const void* W, int64_t N, int64_t K, int 
 // Cached gfx950 check per device ordinal: 0 not yet probed, 1 no, 2 yes.  Threads that make
 // their first call at the same time may both probe; they store the same value.
 std::atomic<int> g_dev_ok[64];
-
-int device_check() {
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess) return hip_fail(e);
-    const int r = lowbit_device_supported(dev);
-    if (r < 0) return LOWBIT_E_HIP;
-    return r == 1 ? LOWBIT_OK : LOWBIT_E_UNSUPPORTED;
-}
 
 // Variant override for A/B runs and tests: LOWBIT_VARIANT = auto | skinny | resident | tile256 | tile256w |
 // tile128 | tile64 | tile288 | tile256n (256 x 192) | tile96 | tile96k2 | tile64k2 (the 16x16-block tiles,

@@ -133,4 +133,52 @@ hipError_t launch_gemm_tile16_group(const GemmProblem* probs, int count, int g, 
 hipError_t launch_gemm_tile16_affine(const GemmProblem* probs, int count, int g, int variant, hipStream_t stream);
 bool use_skinny(int64_t M, int64_t N, int64_t K, int g, int bits);
 
+// Host-side status helpers (lowbit_api.cpp): LOWBIT_E_HIP with the error kept for
+// lowbit_last_hip_error(); LOWBIT_OK where the current device is one the library runs on.
+int hip_fail(hipError_t e);
+int device_check();
+
+// Norms of queries and keys with the position rotation (qk_norm_rope.hip).  Strides in elements.
+struct QkArgs {
+    const uint16_t *q, *k;
+    uint16_t *q_out, *k_out;
+    const uint16_t *q_weight, *k_weight;  // null: no norm
+    const int32_t* positions;             // [tokens, axes]
+    const float* freqs;                   // [rot / 2]
+    int64_t tokens;
+    int64_t q_token, q_head, k_token, k_head, qo_token, qo_head, ko_token, ko_head;
+    int q_heads, k_heads, axes;
+    int rot;          // rotated elements
+    int axis_end[4];  // pairs of the axes so far (inclusive prefix sums; unused axes: rot / 2)
+    int chunks;       // waves per token (set by the launch)
+    float eps;
+};
+hipError_t launch_qk_norm_rope(const QkArgs& a, int head_dim, bool interleaved, hipStream_t stream);
+
+// Attention over grouped heads (attention.hip).  Strides in elements.
+struct AttnArgs {
+    const uint16_t *q, *k, *v;
+    uint16_t* o;
+    const uint8_t* mask;   // [batch, kv_len], null: every key
+    const int32_t* lens;   // [batch], null: kv_len
+    const int32_t* start;  // [batch], null: 0 (causal only)
+    int64_t q_batch, q_token, q_head, k_batch, k_token, k_head, v_batch, v_token, v_head, o_batch, o_token, o_head;
+    int64_t mask_batch;
+    int batch, kv_heads, group, rows, kv_len, causal;  // rows: query tokens x heads of a group
+    float scale_log2;                                  // scale * log2(e)
+    // set by the launch
+    int row_tiles, splits, tiles_per_split;
+    float *part, *part_ml;
+};
+// How a call is divided: row tiles of a kv head, ranges of key tiles, and the workspace of the ranges'
+// partial results (bytes 0: none; without one the call runs unsplit).
+struct AttnPlan {
+    int row_tiles, splits, tiles_per_split;
+    int64_t part_rows;
+    size_t bytes;
+};
+AttnPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t kv_len, int head_dim);
+AttnPlan plan_attention_unsplit(AttnPlan p, int64_t kv_len);
+hipError_t launch_attention(AttnArgs a, int head_dim, const AttnPlan& plan, void* workspace, hipStream_t stream);
+
 }  // namespace lowbit

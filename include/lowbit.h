@@ -310,6 +310,85 @@ int lowbit_gemm_affine_ex(const void* X, const uint32_t* W, const void* S, const
                           int64_t M, int64_t N, int64_t K, int g, void* workspace, size_t workspace_bytes,
                           void* stream);
 
+/*
+ * lowbit_qk_norm_rope -- norms of queries and keys for each head, with the position rotation (of one
+ * or several axes) in the same pass: what stands between a block's QKV linear and its attention.  The
+ * imagegen page lists it among its image path's kernels (qk_rmsnorm_rope, rope_2d_flux: "Implementation").
+ * For token t and head h of q (and of k alike), x = q[t, h, 0:D):
+ *     y[d] = x[d] * q_weight[d] / sqrt(mean(x^2) + eps)          (y = x where q_weight is NULL)
+ *     pair i < R/2 of y turns by the angle  positions[t, axis(i)] * freqs[i]  (radians):
+ *         (u, v) -> (u cos - v sin, u sin + v cos),
+ * with R = axis_dims[0] + .. + axis_dims[axes - 1]; axis a turns the next axis_dims[a] / 2 pairs.
+ *   interleaved != 0: pair i is (y[2i], y[2i+1]);  0: pair i is (y[i], y[i + R/2]).
+ *   Elements from R on are not turned.  axes = 0: the norms alone.
+ *   q, k            device bf16, element (t, h, d) at q[t * q_token + h * q_head + d]; strides in
+ *                   elements, multiples of 8 (columns of a fused QKV output need no copy).
+ *   q_out, k_out    device bf16, with their own strides; may be q (k) itself with the same strides
+ *                   (in place), and must not overlap the inputs in any other way.
+ *   q_weight, k_weight  device bf16 [D] or NULL;  positions  device int32 [tokens, axes], any sign;
+ *                   freqs  device fp32 [R / 2], radians per unit position.
+ *   head_dim D in {32, 64, 128, 256}; axes 0 .. 4; axis_dims even and > 0; R % 16 == 0, R <= D; eps >= 0.
+ * All arithmetic is fp32 (angles: fp64 up to the fraction of a turn), rounded to bf16 once.  q and k
+ * may have no heads (q_heads = 0 or k_heads = 0).  positions and freqs need 4-byte alignment, every other
+ * pointer 16.  The descriptor is read before the call returns.
+ */
+typedef struct lowbit_qk_problem {
+    const void *q, *k;
+    void *q_out, *k_out;
+    const void *q_weight, *k_weight;
+    const int32_t* positions;
+    const float* freqs;
+    int64_t tokens;
+    int64_t q_token, q_head, k_token, k_head;             /* input strides  */
+    int64_t q_out_token, q_out_head, k_out_token, k_out_head; /* output strides */
+    int32_t q_heads, k_heads, head_dim, axes;
+    int32_t axis_dims[4];
+    int32_t interleaved;
+    float eps;
+} lowbit_qk_problem;
+
+int lowbit_qk_norm_rope(const lowbit_qk_problem* problem, void* stream);
+
+/*
+ * lowbit_attention -- O = softmax(scale * Q K^T over the allowed keys) V, for grouped heads: a block's
+ * attention between its QKV and its output linear (joint over text and image tokens, or causal in the
+ * text encoder; the imagegen page's "Implementation" lists both: attention_flux_vt, attention_text_gqa).
+ *   q  device bf16, element (b, t, h, d) at q[b * q_batch + t * q_token + h * q_head + d]; k, v, o alike.
+ *      Strides in elements, multiples of 8 (columns of a fused QKV output need no copy); k_token and
+ *      v_token from head_dim to 2^24.  o must not overlap an input.
+ *   q_heads % kv_heads == 0: q head h reads kv head h / (q_heads / kv_heads).  head_dim 64 or 128.
+ *   scale > 0, e.g. 1 / sqrt(head_dim).
+ *   Query t of batch entry b takes key j where all of these hold:
+ *      key_lens NULL or j < key_lens[b]      (device int32 [batch]; a cache's filled part)
+ *      key_mask NULL or key_mask[b * mask_batch + j] != 0   (device uint8, 1 byte a key; padding)
+ *      causal == 0  or j <= q_start[b] + t   (device int32 [batch], NULL: 0; the first query's position)
+ *   A query that takes no key gets O = 0.  Keys and values that key_lens or key_mask leave out may hold
+ *   anything, infinities and NaN included.
+ * Scores, softmax statistics and sums are fp32; the probabilities are rounded to bf16 for the second
+ * product; O is rounded once.  Deterministic.
+ *   workspace  device memory of lowbit_attention_workspace_size(problem) bytes, 16-byte aligned, of any
+ *      content, with which a call of few rows and many keys splits the keys across workgroups.  With a
+ *      NULL or too small workspace the call runs unsplit.  Calls that share it must not run concurrently.
+ * The size depends on the shape only (0: no split, or invalid arguments).  The descriptor is read
+ * before the call returns.  key_lens and q_start need 4-byte alignment, q, k, v, o and workspace 16.
+ */
+typedef struct lowbit_attention_problem {
+    const void *q, *k, *v;
+    void* o;
+    const uint8_t* key_mask;
+    const int32_t* key_lens;
+    const int32_t* q_start;
+    int64_t batch, q_len, kv_len;
+    int64_t q_batch, q_token, q_head, k_batch, k_token, k_head;
+    int64_t v_batch, v_token, v_head, o_batch, o_token, o_head;
+    int64_t mask_batch;
+    int32_t q_heads, kv_heads, head_dim, causal;
+    float scale;
+} lowbit_attention_problem;
+
+size_t lowbit_attention_workspace_size(const lowbit_attention_problem* problem);
+int lowbit_attention(const lowbit_attention_problem* problem, void* workspace, size_t workspace_bytes, void* stream);
+
 /* Host-only argument check of lowbit_gemm (no HIP call): returns the status lowbit_gemm
  * would return before touching the device. */
 int lowbit_check_gemm_args(const void* X, const uint32_t* W, const void* S, const void* Y,
