@@ -380,6 +380,56 @@ def gemm_batched(problems: Sequence[Tuple["object", "object", "object", "object"
         _check(st, "lowbit_gemm_batched_ex")
 
 
+def lora_workspace_size(M: int, rank: int) -> int:
+    """Bytes of workspace that gemm_lora needs for M rows (0 for invalid arguments)."""
+    return int(lib().lowbit_lora_workspace_size(M, rank))
+
+
+def gemm_lora(x, words, scales, g: int, bits: int, lora_a, lora_b, alpha, rows, out=None, workspace=None):
+    """Y[m] = X[m] . dequant(W)^T + alpha[e] * (X[m] . A[e]^T) . B[e]^T with e = rows[m], in bf16
+    (lowbit_gemm_lora): low-rank adapters of many requests beside one packed weight.  lora_a bf16 [adapters, rank, K],
+    lora_b bf16 [adapters, N, rank], alpha fp32 [adapters], rows int32 [M] (-1: no adapter).
+
+    `workspace`: a device tensor of at least lora_workspace_size(M, rank) bytes, allocated for the call if None."""
+    torch = _torch()
+    _require(x, torch.bfloat16, "x")
+    _require(words, torch.int32, "words")
+    _require(scales, torch.float16, "scales")
+    _require(lora_a, torch.bfloat16, "lora_a", ndim=3)
+    _require(lora_b, torch.bfloat16, "lora_b", ndim=3)
+    _require(alpha, torch.float32, "alpha", ndim=1)
+    _require(rows, torch.int32, "rows", ndim=1)
+    M, K = x.shape
+    N = words.shape[0]
+    E, rank = lora_a.shape[0], lora_a.shape[1]
+    if words.shape[1] != words_per_row(K, bits):
+        raise ValueError(f"words must be [N, K*bits/32] = [{N}, {words_per_row(K, bits)}], got {tuple(words.shape)}")
+    if K % g or tuple(scales.shape) != (N, K // g):
+        raise ValueError(f"scales must be [N, K/g] = [{N}, {K // g if g else 0}], got {tuple(scales.shape)}")
+    if lora_a.shape[2] != K or tuple(lora_b.shape) != (E, N, rank):
+        raise ValueError(f"lora_a must be [adapters, rank, {K}] and lora_b [adapters, {N}, rank], got "
+                         f"{tuple(lora_a.shape)} and {tuple(lora_b.shape)}")
+    if alpha.shape[0] != E or rows.shape[0] != M:
+        raise ValueError(f"alpha must be [{E}] and rows [{M}]")
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+    else:
+        _require(out, torch.bfloat16, "out")
+        if tuple(out.shape) != (M, N):
+            raise ValueError("out must be [M, N]")
+    if workspace is None:
+        workspace = torch.empty(lora_workspace_size(M, rank), dtype=torch.uint8, device=x.device)
+    _same_device(x, (("words", words), ("scales", scales), ("lora_a", lora_a), ("lora_b", lora_b), ("alpha", alpha),
+                     ("rows", rows), ("out", out)))
+    ws, nbytes = _workspace(workspace, x)
+    with _on(x.device):
+        st = lib().lowbit_gemm_lora(x.data_ptr(), words.data_ptr(), scales.data_ptr(), out.data_ptr(), M, N, K, g, bits,
+                                    lora_a.data_ptr(), lora_b.data_ptr(), alpha.data_ptr(), rows.data_ptr(), E, rank, ws,
+                                    nbytes, _stream_ptr(x.device))
+        _check(st, "lowbit_gemm_lora")
+    return out
+
+
 class QkProblem(ctypes.Structure):
     """lowbit_qk_problem of include/lowbit.h."""
     _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "q_out", "k_out", "q_weight", "k_weight", "positions", "freqs")]

@@ -98,9 +98,48 @@ int attention_args(const lowbit_attention_problem* p, lowbit::AttnArgs& a) {
     return LOWBIT_OK;
 }
 
+constexpr int64_t kMaxAdapters = 1 << 16;
+
+bool lora_rank_ok(int64_t rank) { return rank >= 8 && rank <= 128 && rank % 8 == 0; }
+
 }  // namespace
 
 extern "C" {
+
+size_t lowbit_lora_workspace_size(int64_t M, int rank) {
+    if (M <= 0 || M > kMaxDim || !lora_rank_ok(rank)) return 0;
+    return (size_t(M) * size_t(rank) * 4u + 255u) & ~size_t(255);
+}
+
+int lowbit_gemm_lora(const void* X, const uint32_t* W, const void* S, void* Y, int64_t M, int64_t N, int64_t K, int g,
+                     int bits, const void* A, const void* B, const float* alpha, const int32_t* rows, int64_t adapters,
+                     int rank, void* workspace, size_t workspace_bytes, void* stream) {
+    int st = lowbit_check_gemm_args(X, W, S, Y, M, N, K, g, bits);
+    if (st != LOWBIT_OK) return st;
+    if (!lora_rank_ok(rank) || adapters > kMaxAdapters) return LOWBIT_E_UNSUPPORTED;
+    if (adapters < 0) return LOWBIT_E_INVALID;
+    if (!lowbit::tile16_supported(g, bits)) return LOWBIT_E_UNSUPPORTED;
+    if (N * int64_t(rank) * 2 > (int64_t(1) << 32) - 1) return LOWBIT_E_UNSUPPORTED;
+    if (M * N == 0) return LOWBIT_OK;
+    // no adapter, or an empty sum: the plain product
+    if (adapters == 0 || K == 0) return lowbit_gemm(X, W, S, Y, M, N, K, g, bits, stream);
+    if (A == nullptr || B == nullptr || alpha == nullptr || rows == nullptr) return LOWBIT_E_INVALID;
+    if (workspace == nullptr || workspace_bytes < lowbit_lora_workspace_size(M, rank)) return LOWBIT_E_INVALID;
+    if (!aligned(A, 16) || !aligned(B, 16) || !aligned(workspace, 16) || !aligned(alpha, 4) || !aligned(rows, 4))
+        return LOWBIT_E_ALIGN;
+    st = lowbit::device_check();
+    if (st != LOWBIT_OK) return st;
+    const hipStream_t s = static_cast<hipStream_t>(stream);
+    const lowbit::ShrinkArgs sh{static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(A), alpha, rows,
+                                static_cast<uint16_t*>(workspace), int(M), int(K), int(adapters), rank};
+    hipError_t e = lowbit::launch_lora_shrink(sh, s);
+    if (e != hipSuccess) return lowbit::hip_fail(e);
+    const lowbit::LoraArgs la{sh.u, static_cast<const uint16_t*>(B), rows, int(adapters), rank};
+    const lowbit::GemmProblem p{static_cast<const uint16_t*>(X), W, static_cast<const uint16_t*>(S),
+                                static_cast<uint16_t*>(Y), int(M), int(N), int(K)};
+    e = lowbit::launch_gemm_tile16_lora(p, g, bits, la, s);
+    return e == hipSuccess ? LOWBIT_OK : lowbit::hip_fail(e);
+}
 
 size_t lowbit_attention_workspace_size(const lowbit_attention_problem* p) {
     lowbit::AttnArgs a{};

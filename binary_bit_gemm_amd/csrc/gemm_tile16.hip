@@ -35,6 +35,9 @@
 // or bytes (q & 1) and (q & 1) + 2 of binary word q >> 1; one 8-byte read of the row's step
 // words and one byte permute gather them.  4-bit codes (8 per word) make each chunk one word:
 // the lane reads words phi(q, 0) and phi(q, 0) + 2 of the step (one two-dword LDS read).
+#include <type_traits>
+
+#include "lora_device.h"
 #include "lowbit_device.h"
 #include "lowbit_internal.h"
 
@@ -98,9 +101,14 @@ struct SplitK {
     int splits;
 };
 
+// EPI = kEpiLora: the second argument holds the adapters' operands instead, and the fp32 sums start at
+// their term.
+template <int EPI>
+using Extra = std::conditional_t<EPI == kEpiLora, LoraArgs, SplitK>;
+
 template <int G, int BITS, int BM, int BN, int WAVES_M, int WAVES_N, int KSPLIT, int EPI = kEpiPlain,
           bool AFFINE = false, bool XSPLIT = false>
-__global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KSPLIT, 1) void gemm_tile16_kernel(ProblemGroup grp, SplitK sk) {
+__global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KSPLIT, 1) void gemm_tile16_kernel(ProblemGroup grp, Extra<EPI> sk) {
     constexpr bool SWIGLU = EPI == kEpiSwiglu;
     static_assert(!AFFINE || (BITS == 4 && EPI == kEpiPlain), "affine groups: 4-bit levels, plain epilogue");
     using C = Cfg16<G, BITS, BM, BN, WAVES_M, WAVES_N>;
@@ -304,6 +312,9 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KSPLIT, 1) void gemm_tile1
         for (int mb = 0; mb < C::MB; ++mb)
 #pragma unroll
             for (int nb = 0; nb < C::NB; ++nb) acc[mb][nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        if constexpr (EPI == kEpiLora) {
+            if (kg == 0) lora_init<1>(acc, sk, M, N, m0 + wm0, n0 + wn0);
+        }
 
         // A step's words and scales are read from LDS before any copy of the step is issued (the
         // compiler cannot tell which of the two buffers a step reads).
@@ -668,8 +679,10 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KSPLIT, 1) void gemm_tile1
 
 template <int G, int BITS, int BM, int BN, int WAVES_M, int WAVES_N, int KSPLIT = 1, int EPI = kEpiPlain,
           bool AFFINE = false, bool XSPLIT = false>
-hipError_t launch_cfg16(const GemmProblem* probs, int count, hipStream_t stream, SplitK sk = SplitK{}) {
+hipError_t launch_cfg16(const GemmProblem* probs, int count, hipStream_t stream, Extra<EPI> sk = Extra<EPI>{}) {
     ProblemGroup grp{};
+    int splits = 1;
+    if constexpr (XSPLIT) splits = sk.splits;
     int total = 0;
     constexpr int kOutBn = EPI == kEpiSwiglu ? BN / 2 : BN;
     for (int i = 0; i < count; ++i) {
@@ -683,15 +696,15 @@ hipError_t launch_cfg16(const GemmProblem* probs, int count, hipStream_t stream,
     using Cf = Cfg16<G, BITS, BM, BN, WAVES_M, WAVES_N>;
     constexpr int kLds = KSPLIT * 2 * (Cf::X_TILE + Cf::W_BLOCK + Cf::S_BLOCK + (AFFINE ? Cf::S_BLOCK : 16));
     constexpr bool kPersistent = KSPLIT == 1 && kLds > 80 * 1024;
-    const int grid = XSPLIT ? total * sk.splits : kPersistent && total > kComputeUnits ? kComputeUnits : total;
+    const int grid = XSPLIT ? total * splits : kPersistent && total > kComputeUnits ? kComputeUnits : total;
     hipLaunchKernelGGL((gemm_tile16_kernel<G, BITS, BM, BN, WAVES_M, WAVES_N, KSPLIT, EPI, AFFINE, XSPLIT>), dim3(grid),
                        dim3(64 * WAVES_M * WAVES_N * KSPLIT), 0, stream, grp, sk);
     const hipError_t e = hipGetLastError();
     if (e == hipSuccess && trace_enabled()) {
         char cfg[96];
         snprintf(cfg, sizeof cfg, "%dx%d waves=%dx%dx%d epi=%s%s splits=%d", BM, BN, WAVES_M, WAVES_N, KSPLIT,
-                 EPI == kEpiSwiglu ? "swiglu" : EPI == kEpiResidual ? "residual" : "plain", AFFINE ? " affine" : "",
-                 XSPLIT ? sk.splits : 1);
+                 EPI == kEpiSwiglu ? "swiglu" : EPI == kEpiResidual ? "residual" : EPI == kEpiLora ? "lora" : "plain",
+                 AFFINE ? " affine" : "", splits);
         trace_launch("tile16", cfg, G, BITS, probs, count, unsigned(grid), 64u * WAVES_M * WAVES_N * KSPLIT, 0u);
     }
     return e;
@@ -750,6 +763,26 @@ hipError_t launch_gemm_tile16_epilogue(const GemmProblem* probs, int count, int 
     if (epi == kEpiSwiglu) return launch_epi16_gb<kEpiSwiglu>(probs, count, g, bits, stream);
     if (epi == kEpiResidual) return launch_epi16_gb<kEpiResidual>(probs, count, g, bits, stream);
     return hipErrorInvalidValue;
+}
+
+// The adapters' epilogue on the tile that the cost model picks among this kernel's.
+template <int G, int BITS>
+hipError_t launch_lora16(const GemmProblem& p, const LoraArgs& la, hipStream_t stream) {
+    const int variant = pick_tile_variant(&p, 1, G, BITS, true);
+    const bool even = (p.K / KS) % 2 == 0;
+    if (variant == TILE_64x128K2) return launch_cfg16<G, BITS, 64, 128, 1, 4, 2, kEpiLora>(&p, 1, stream, la);
+    if (variant == TILE_96x192K2 && even) return launch_cfg16<G, BITS, 96, 192, 1, 4, 2, kEpiLora>(&p, 1, stream, la);
+    if (variant == TILE_96x192 || variant == TILE_96x192K2)
+        return launch_cfg16<G, BITS, 96, 192, 1, 4, 1, kEpiLora>(&p, 1, stream, la);
+    if (variant == TILE_256x192) return launch_cfg16<G, BITS, 256, 192, 2, 6, 1, kEpiLora>(&p, 1, stream, la);
+    return launch_cfg16<G, BITS, 288, 192, 2, 6, 1, kEpiLora>(&p, 1, stream, la);
+}
+
+hipError_t launch_gemm_tile16_lora(const GemmProblem& p, int g, int bits, const LoraArgs& la, hipStream_t stream) {
+    if (!tile16_supported(g, bits)) return hipErrorInvalidValue;
+    if (bits == 2) return g == 64 ? launch_lora16<64, 2>(p, la, stream) : launch_lora16<128, 2>(p, la, stream);
+    if (bits == 4) return g == 64 ? launch_lora16<64, 4>(p, la, stream) : launch_lora16<128, 4>(p, la, stream);
+    return g == 64 ? launch_lora16<64, 1>(p, la, stream) : launch_lora16<128, 1>(p, la, stream);
 }
 
 // Affine 4-bit GEMMs whose 64 x 128 tile grid leaves a quarter of the compute units or more idle

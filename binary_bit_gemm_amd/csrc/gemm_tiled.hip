@@ -620,18 +620,19 @@ constexpr TileShape kTiles[] = {
 
 }  // namespace
 
-int pick_tile_variant(const GemmProblem* probs, int count, int g, int bits) {
-    int best = bits == 4 ? TILE_288x192 : TILE_64x256;
+int pick_tile_variant(const GemmProblem* probs, int count, int g, int bits, bool tile16_only) {
+    int best = bits == 4 || tile16_only ? TILE_288x192 : TILE_64x256;
     double best_cost = 0.0;
     for (const TileShape& t : kTiles) {
         if (is_tile16_variant(t.variant) && !tile16_supported(g, bits)) continue;
-        if (bits == 4 && !is_tile16_variant(t.variant)) continue;  // 4-bit codes: the 16x16-block tile only
+        // 4-bit codes and the adapters' epilogue: the 16x16-block tile only
+        if ((bits == 4 || tile16_only) && !is_tile16_variant(t.variant)) continue;
         if (t.variant == TILE_64x128K2) {
-            bool skip = bits != 4;
+            bool skip = bits != 4 && !tile16_only;
             for (int i = 0; i < count; ++i) skip = skip || (probs[i].K / 64) % 2 != 0;
             if (skip) continue;
         }
-        if ((t.variant == TILE_96x192 || t.variant == TILE_96x192K2) && bits != 4) {
+        if ((t.variant == TILE_96x192 || t.variant == TILE_96x192K2) && bits != 4 && !tile16_only) {
             // measured at M = 1536; below M = 1024 they stay unused.  The K split needs an even
             // number of 64-element steps.
             bool skip = false;

@@ -23,6 +23,25 @@ struct GemmProblem {
 constexpr int kEpiPlain = 0;     // Y = X . W^T
 constexpr int kEpiSwiglu = 1;    // W holds [gate | up] rows: Y = silu(X . Wg^T) * (X . Wu^T)
 constexpr int kEpiResidual = 2;  // Y = R + gate[n] * (X . W^T)
+constexpr int kEpiLora = 3;      // Y = X . W^T + U B_e^T (low-rank adapters, lora_device.h)
+
+// Adapters inside a GEMM: U [M, 2 rank] bf16 (hi and lo halves of alpha_e A_e X[m]), B [adapters, N,
+// rank] bf16, rows [M] (a row's adapter; outside [0, adapters): none).
+struct LoraArgs {
+    const uint16_t* u;
+    const uint16_t* b;
+    const int32_t* rows;
+    int adapters, rank;
+};
+// The first product, U = alpha_e A_e X[m] (lora.hip).
+struct ShrinkArgs {
+    const uint16_t *X, *A;  // bf16 [M, K], [adapters, rank, K]
+    const float* alpha;     // [adapters]
+    const int32_t* rows;
+    uint16_t* u;
+    int M, K, adapters, rank;
+};
+hipError_t launch_lora_shrink(const ShrinkArgs& a, hipStream_t stream);
 
 // Tiles of `b` rows or columns over a dimension of n (64-bit: M may be up to 2^31 - 1).
 inline int64_t tiles_of(int64_t n, int64_t b) { return (n + b - 1) / b; }
@@ -117,7 +136,8 @@ hipError_t launch_gemm_tiled_group(const GemmProblem* probs, int count, int g, i
 hipError_t launch_gemm_skinny_group(const GemmProblem* probs, int count, int g, int bits, hipStream_t stream);
 
 // Tile for a group of problems: fewest estimated rounds x tile work over the whole group.
-int pick_tile_variant(const GemmProblem* probs, int count, int g, int bits);
+// tile16_only: among the tiles of the 16x16-block kernel.
+int pick_tile_variant(const GemmProblem* probs, int count, int g, int bits, bool tile16_only = false);
 int pick_tile_variant(int64_t M, int64_t N, int64_t K, int g, int bits);
 const char* tile_variant_name(int variant);
 bool tile16_supported(int g, int bits);
@@ -128,6 +148,7 @@ hipError_t launch_gemm_tile16_epilogue(const GemmProblem* probs, int count, int 
                                        hipStream_t stream);
 hipError_t launch_gemm_tile16_group(const GemmProblem* probs, int count, int g, int bits, int variant,
                                     hipStream_t stream);
+hipError_t launch_gemm_tile16_lora(const GemmProblem& p, int g, int bits, const LoraArgs& la, hipStream_t stream);
 // Affine 4-bit groups (unsigned levels, w = s * q + b with each problem's B set) on a 16x16-block
 // tile; `variant` as for 4-bit codes.
 hipError_t launch_gemm_tile16_affine(const GemmProblem* probs, int count, int g, int variant, hipStream_t stream);

@@ -311,6 +311,26 @@ int lowbit_gemm_affine_ex(const void* X, const uint32_t* W, const void* S, const
                           void* stream);
 
 /*
+ * lowbit_gemm_lora -- lowbit_gemm with the low-rank adapters of many requests at once beside the shared
+ * packed weights (an adapter cannot be merged into ternary or binary codes):
+ *     Y[m] = X[m] . dequant(W)^T + alpha[e] * (X[m] . A[e]^T) . B[e]^T,   e = rows[m].
+ *   X, W, S, Y, M, N, K, g, bits  as lowbit_gemm; g = 64 or 128 (g = 32 returns LOWBIT_E_UNSUPPORTED).
+ *   A  device bf16 [adapters, rank, K];  B  device bf16 [adapters, N, rank];  alpha  device fp32 [adapters].
+ *   rows  device int32 [M]: the adapter of each row, in any order; a value outside [0, adapters) (e.g. -1)
+ *      means none.  Rows of different adapters do not affect each other, whatever an adapter holds.
+ *   rank  a multiple of 8 from 8 to 128 (pad smaller adapters with zeros).
+ *   workspace  device memory of lowbit_lora_workspace_size(M, rank) bytes, 16-byte aligned, of any
+ *      content (required: NULL or too small returns LOWBIT_E_INVALID).  Calls that share it must not
+ *      run concurrently.
+ * Both products are fp32 sums of bf16 products; X . A^T is kept to 16 significant bits between them; Y is rounded
+ * to bf16 once.  Deterministic.  A, B and workspace need 16-byte alignment, alpha and rows 4.
+ */
+size_t lowbit_lora_workspace_size(int64_t M, int rank);
+int lowbit_gemm_lora(const void* X, const uint32_t* W, const void* S, void* Y, int64_t M, int64_t N, int64_t K, int g,
+                     int bits, const void* A, const void* B, const float* alpha, const int32_t* rows, int64_t adapters,
+                     int rank, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * lowbit_qk_norm_rope -- norms of queries and keys for each head, with the position rotation (of one
  * or several axes) in the same pass: what stands between a block's QKV linear and its attention.  The
  * imagegen page lists it among its image path's kernels (qk_rmsnorm_rope, rope_2d_flux: "Implementation").

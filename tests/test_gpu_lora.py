@@ -1,0 +1,177 @@
+"""Low-rank adapters beside a packed GEMM, against the formula in 64 bits (the oracle's dequantised weights).
+
+Tolerance, per element: one rounding to bf16 (8 significant bits: 2^-8 of the result); the packed product's
+fp32 sums, groups of g products and then K / g group sums and a few more additions, (g + K / g + 32) * 2^-24 of the sum of magnitudes;
+the adapter's term, whose first sum of K products is kept to 16 bits: (K * 2^-24 + 2^-16) of alpha * sum_r
+(sum_k |x| |a|) |b|, plus its sum over the rank, 2 rank * 2^-24 of the same.
+"""
+import numpy as np
+import pytest
+import torch
+
+import binary_bit_gemm_amd as lb
+import oracle
+import workloads as W
+
+pytestmark = pytest.mark.gpu
+
+
+class Case:
+    def __init__(self, M, N, K, bits, g, rank, adapters, rows, seed=0):
+        rng = np.random.default_rng([seed, M, N, K, bits, g, rank, adapters])
+        self.bits, self.g, self.K, self.rank = bits, g, K, rank
+        inp = W.make_inputs(W.Problem("lora", M, N, K, bits, g, 0, 0), seed=seed)
+        self.x = torch.from_numpy(inp.x.view(np.int16)).view(torch.bfloat16).cuda()
+        self.words, bad = lb.pack(torch.from_numpy(inp.codes).cuda(), bits)
+        assert bad == 0
+        self.scales = torch.from_numpy(inp.scales).cuda()
+        self.w = oracle.dequant_f64(inp.codes, inp.scales, g)
+        self.a = torch.from_numpy(rng.standard_normal((adapters, rank, K)) / np.sqrt(K)).bfloat16().cuda()
+        self.b = torch.from_numpy(rng.standard_normal((adapters, N, rank)) * 0.2).bfloat16().cuda()
+        self.alpha = torch.from_numpy(rng.uniform(-2, 2, adapters)).float().cuda()
+        if rows == "one":
+            r = np.full(M, adapters - 1)
+        elif rows == "segments":
+            r = np.sort(rng.integers(0, adapters, M))
+        elif rows == "none":
+            r = np.full(M, -1)
+        else:  # scattered, some without an adapter, some out of range
+            r = rng.integers(-1, adapters + 1, M)
+        self.rows = torch.from_numpy(r.astype(np.int32)).cuda()
+
+    def run(self, **kw):
+        return lb.gemm_lora(self.x, self.words, self.scales, self.g, self.bits, self.a, self.b, self.alpha, self.rows, **kw)
+
+    def reference(self):
+        x = self.x.double().cpu().numpy()
+        y, mag = x @ self.w.T, np.abs(x) @ np.abs(self.w).T
+        lora = np.zeros_like(y)
+        for e in range(self.a.shape[0]):
+            m = self.rows.cpu().numpy() == e
+            if m.any():
+                a, b = self.a[e].double().cpu().numpy(), self.b[e].double().cpu().numpy()
+                al = float(self.alpha[e])
+                y[m] += al * (x[m] @ a.T) @ b.T
+                lora[m] = abs(al) * (np.abs(x[m]) @ np.abs(a).T) @ np.abs(b).T
+        bound = (self.g + self.K / self.g + 32) * 2.0 ** -24 * mag + ((self.K + 2 * self.rank) * 2.0 ** -24 + 2.0 ** -16) * lora
+        return y, bound
+
+    def check(self, got):
+        want, bound = self.reference()
+        got = got.double().cpu().numpy()
+        assert np.isfinite(got).all()
+        off = np.abs(got - want) - (2.0 ** -8 * (np.abs(want) + bound) + bound)
+        assert off.max(initial=-1) <= 0, f"worst element over its bound by {off.max()}"
+
+
+@pytest.mark.parametrize("bits,g", [(2, 64), (2, 128), (1, 64), (1, 128), (4, 64), (4, 128)])
+@pytest.mark.parametrize("M,N,K,rank,adapters,rows", [
+    (1, 16, 128, 8, 1, "one"), (1, 272, 512, 16, 3, "one"), (16, 256, 256, 16, 16, "scattered"), (15, 1040, 640, 24, 5, "segments"),
+    (33, 320, 768, 64, 4, "scattered"), (64, 128, 1024, 128, 2, "segments"), (300, 528, 384, 32, 3, "segments"),
+    (97, 192, 192, 40, 7, "scattered"), (130, 512, 1280, 16, 1, "none"), (289, 208, 256, 8, 20, "scattered"),
+])
+def test_parity(M, N, K, rank, adapters, rows, bits, g):
+    if K % g:
+        K = K // g * g + g
+    c = Case(M, N, K, bits, g, rank, adapters, rows)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("variant_m", [1025, 1536, 4608])
+@pytest.mark.parametrize("rows", ["one", "segments", "scattered"])
+def test_large_tiles(variant_m, rows):
+    c = Case(variant_m, 2304, 576, 2, 64, 32, 4, rows, seed=1)
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("bits", [1, 2])
+@pytest.mark.parametrize("M,N,K", [(1, 9216, 3072), (16, 3072, 9216), (16, 3072, 3072), (9, 512, 12288), (32, 9216, 3072), (20, 1024, 4096)])
+def test_skinny(M, N, K, bits):
+    """The shapes on which lowbit_gemm runs its skinny kernels."""
+    for rows in ("one", "scattered"):
+        c = Case(M, N, K, bits, 64, 16, 6, rows, seed=2)
+        c.check(c.run())
+
+
+def test_rows_without_an_adapter_are_the_plain_product():
+    c = Case(300, 512, 512, 2, 64, 16, 4, "none", seed=3)
+    plain = c.x.double().cpu().numpy() @ c.w.T
+    got = c.run().double().cpu().numpy()
+    assert (np.abs(got - plain) <= 2.0 ** -8 * np.abs(plain) + 2.0 ** -8).all()
+    c.rows[:] = 99
+    assert torch.equal(c.run(), c.run()) and np.array_equal(c.run().double().cpu().numpy(), got)
+
+
+@pytest.mark.parametrize("M", [7, 16, 32, 200, 1100])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_requests_do_not_touch_each_other(M, bad):
+    """An adapter and a row that hold no numbers reach their own rows only."""
+    c = Case(M, 400, 512, 2, 64, 16, 3, "scattered", seed=4)
+    c.rows[0], c.rows[1], c.rows[2] = 1, 0, 2
+    want = c.run()
+    c.a[1, :, 5] = bad
+    c.b[1, 7] = bad
+    got = c.run()
+    own = c.rows == 1
+    assert torch.equal(got[~own], want[~own])
+    assert not bool(torch.isfinite(got[own][:, 7]).any())
+    c = Case(M, 400, 512, 2, 64, 16, 3, "one", seed=5)
+    want = c.run()
+    c.x[M // 2, 3] = bad
+    got = c.run()
+    keep = torch.arange(M, device="cuda") != M // 2
+    assert torch.equal(got[keep], want[keep]) and not bool(torch.isfinite(got[M // 2]).any())
+
+
+def test_workspace_content_and_repeats():
+    c = Case(70, 512, 1024, 2, 64, 24, 5, "scattered", seed=6)
+    want = c.run()
+    ws = torch.full((lb.lora_workspace_size(70, 24),), 0xFF, dtype=torch.uint8, device="cuda")  # NaN patterns
+    for _ in range(3):
+        assert torch.equal(c.run(workspace=ws), want)
+
+
+def test_no_adapters_and_empty_calls():
+    c = Case(5, 256, 256, 2, 64, 8, 1, "one", seed=7)
+    plain = lb.gemm(c.x, c.words, c.scales, 64, 2)
+    none = lb.gemm_lora(c.x, c.words, c.scales, 64, 2, c.a[:0], c.b[:0], c.alpha[:0], c.rows)
+    assert torch.equal(none, plain)
+    assert lb.gemm_lora(c.x[:0], c.words, c.scales, 64, 2, c.a, c.b, c.alpha, c.rows[:0]).shape == (0, 256)
+
+
+def test_adapters_past_32_bits():
+    """A table of adapters longer than 2^32 bytes, of which the last is used."""
+    c = Case(40, 256, 4096, 2, 64, 128, 1, "one", seed=8)
+    want = c.run()
+    n = (1 << 32) // (128 * 4096 * 2) + 2
+    a = torch.empty(n, 128, 4096, dtype=torch.bfloat16, device="cuda")
+    b = torch.empty(n, 256, 128, dtype=torch.bfloat16, device="cuda")
+    a[-1], b[-1] = c.a[0], c.b[0]
+    c.a, c.b, c.alpha = a, b, c.alpha.expand(n).contiguous()
+    c.rows[:] = n - 1
+    assert torch.equal(c.run(), want)
+
+
+def test_on_another_stream_and_in_a_graph():
+    c = Case(64, 1024, 1024, 2, 64, 16, 4, "scattered", seed=9)
+    want = c.run()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = c.run()
+    s.synchronize()
+    assert torch.equal(got, want)
+    ws = torch.zeros(lb.lora_workspace_size(64, 16), dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(want)
+    c.run(out=out, workspace=ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        c.run(out=out, workspace=ws)
+    for k in range(3):
+        c.x.copy_(torch.randn(c.x.shape, generator=torch.Generator().manual_seed(k)).bfloat16())
+        want = c.run()
+        out.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
