@@ -22,6 +22,7 @@ namespace lowbit {
 namespace {
 
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
+typedef short s16x8_t __attribute__((ext_vector_type(8)));
 
 constexpr float kNegInf = -__builtin_inff();
 // A maximum that grows by less than this (in powers of two) leaves m as it is: p then reaches 2^8
@@ -65,58 +66,58 @@ __device__ __forceinline__ float other_half(float v) {
     return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
 }
 
-__device__ __forceinline__ bool bf16_finite(short v) { return (v & 0x7F80) != 0x7F80; }
+// The lane's byte offsets into a K and a V tile, without the constants that the compiler folds into the
+// instructions: K row l % 32 at chunk 2 kk + h (rows 32 apart have the same swizzle), V row 4 h +
+// (l % 16) / 4 at column block b (rows 4 apart as well).
+template <int D>
+struct Offsets {
+    int k[D / 16], v[D / 32];
+};
 
-// Infinities and NaN of a tile's V, which the matrix product left out (0 * inf is NaN there, also for the
-// queries that do not take the key): added to the queries that take them, one key after the other.
-// What a positive probability times an infinity or a NaN gives is that infinity or NaN.
-template <int D, int NKB>
-__device__ __forceinline__ void add_nonfinite(Rows<D>& w, const unsigned char* vt, uint64_t allowed) {
-    const int h = (int(threadIdx.x) >> 5) & 1;
-    for (int j = 0; j < 32 * NKB; ++j) {
-        const bool mine = (allowed >> j) & 1;
-        if (!__any(mine)) continue;
+template <int D>
+__device__ __forceinline__ Offsets<D> offsets() {
+    const int lane = int(threadIdx.x) & 63;
+    const int l32 = lane & 31, h = lane >> 5, i16 = lane & 15, dsel = (lane >> 4) & 1;
+    Offsets<D> f;
 #pragma unroll
-        for (int b = 0; b < D / 32; ++b)
+    for (int kk = 0; kk < D / 16; ++kk) f.k[kk] = l32 * (2 * D) + (((2 * kk + h) ^ k_swz<D>(l32)) << 4);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const s16x4_t v = *reinterpret_cast<const s16x4_t*>(vt + j * (2 * D) + (((4 * b + e) ^ v_swz<D>(j)) << 4) + 8 * h);
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (mine && !bf16_finite(v[i])) w.o[b][4 * e + i] += __uint_as_float(uint32_t(uint16_t(v[i])) << 16);
-            }
+    for (int b = 0; b < D / 32; ++b) {
+        const int r = 4 * h + (i16 >> 2), chunk = 4 * b + 2 * dsel + ((i16 & 3) >> 1);
+        f.v[b] = r * (2 * D) + ((chunk ^ v_swz<D>(r)) << 4) + 8 * (i16 & 1);
     }
+    return f;
 }
 
-// NKB * 32 keys of a tile in LDS at kt, vt.  allowed: bit i of the lane's word says whether the lane's
-// query takes key i; PARTIAL: not all of them are set in every lane.  live: the keys that any
-// query may take (padding excluded); V rows of the others count as zeros, whatever they hold.
-template <int D, int NKB, bool PARTIAL>
-__device__ __forceinline__ void tile_step(Rows<D>& w, const unsigned char* kt, const unsigned char* vt, float c,
-                                          uint64_t allowed, uint64_t live) {
-    const int lane = int(threadIdx.x) & 63;
-    const int l32 = lane & 31, h = lane >> 5;
-    f32x16_t s[NKB];
+// Scores of NKB * 32 keys of the K tile at kt.
+template <int D, int NKB>
+__device__ __forceinline__ void scores(const Rows<D>& w, const Offsets<D>& f, const unsigned char* kt, f32x16_t (&s)[NKB]) {
 #pragma unroll
     for (int kb = 0; kb < NKB; ++kb) {
 #pragma unroll
         for (int i = 0; i < 16; ++i) s[kb][i] = 0.f;
-        const int r = 32 * kb + l32;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-            const bf16x8_t a = *reinterpret_cast<const bf16x8_t*>(kt + r * (2 * D) + (((2 * kk + h) ^ k_swz<D>(r)) << 4));
-            s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, w.q[kk], s[kb], 0, 0, 0);
-        }
+        for (int kk = 0; kk < D / 16; ++kk)
+            s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+                *reinterpret_cast<const bf16x8_t*>(kt + f.k[kk] + kb * 32 * (2 * D)), w.q[kk], s[kb], 0, 0, 0);
     }
-    if constexpr (PARTIAL) {
-        const uint64_t mine = allowed >> (4 * h);
+}
+
+// Scores of keys that the lane's query does not take (bit of `allowed` clear) to -inf.
+template <int NKB>
+__device__ __forceinline__ void mask_scores(f32x16_t (&s)[NKB], uint64_t allowed) {
+    const uint64_t mine = allowed >> ((threadIdx.x & 32) >> 3);
 #pragma unroll
-        for (int kb = 0; kb < NKB; ++kb) {
-            const uint32_t bits = uint32_t(mine >> (32 * kb));
+    for (int kb = 0; kb < NKB; ++kb) {
+        const uint32_t bits = uint32_t(mine >> (32 * kb));
 #pragma unroll
-            for (int i = 0; i < 16; ++i) s[kb][i] = (bits >> (8 * (i / 4) + i % 4)) & 1u ? s[kb][i] : kNegInf;
-        }
+        for (int i = 0; i < 16; ++i) s[kb][i] = (bits >> (8 * (i / 4) + i % 4)) & 1u ? s[kb][i] : kNegInf;
     }
+}
+
+// The softmax's step: s becomes the probabilities (to the maximum so far), O, l and m follow.
+template <int D, int NKB>
+__device__ __forceinline__ void softmax_step(Rows<D>& w, f32x16_t (&s)[NKB], float c) {
     float top = s[0][0];
 #pragma unroll
     for (int kb = 0; kb < NKB; ++kb)
@@ -144,8 +145,11 @@ __device__ __forceinline__ void tile_step(Rows<D>& w, const unsigned char* kt, c
             sum += s[kb][i];
         }
     w.l += sum;
-    const int i16 = lane & 15, dsel = (lane >> 4) & 1;
-    bool odd = false;  // an infinity or a NaN in a live row of V
+}
+
+// O += P V for the V tile at vt.
+template <int D, int NKB>
+__device__ __forceinline__ void weighted(Rows<D>& w, const Offsets<D>& f, const unsigned char* vt, const f32x16_t (&s)[NKB]) {
 #pragma unroll
     for (int k2 = 0; k2 < 2 * NKB; ++k2) {  // 16 keys each
         bf16x8_t p;
@@ -155,29 +159,71 @@ __device__ __forceinline__ void tile_step(Rows<D>& w, const unsigned char* kt, c
         for (int b = 0; b < D / 32; ++b) {
             s16x4_t v[2];
 #pragma unroll
-            for (int part = 0; part < 2; ++part) {
-                const int r = 16 * k2 + 8 * part + 4 * h + (i16 >> 2);
-                const int chunk = 4 * b + 2 * dsel + ((i16 & 3) >> 1);
+            for (int part = 0; part < 2; ++part)
                 v[part] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) s16x4_t*)(vt + r * (2 * D) + ((chunk ^ v_swz<D>(r)) << 4) +
-                                                                  8 * (i16 & 1)));
-                if constexpr (PARTIAL) {
-                    const uint32_t keys = uint32_t(live >> (16 * k2 + 8 * part + 4 * h));
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const bool take = (keys >> i) & 1u, fine = bf16_finite(v[part][i]);
-                        odd = odd || (take && !fine);
-                        v[part][i] = take && fine ? v[part][i] : short(0);
-                    }
-                }
-            }
-            typedef short s16x8_t __attribute__((ext_vector_type(8)));
+                    (__attribute__((address_space(3))) s16x4_t*)(vt + f.v[b] + (16 * k2 + 8 * part) * (2 * D)));
             const s16x8_t a = __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7);
             w.o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), p, w.o[b], 0, 0, 0);
         }
     }
-    if constexpr (PARTIAL) {
-        if (__any(odd)) add_nonfinite<D, NKB>(w, vt, allowed);
+}
+
+__device__ __forceinline__ bool pair_finite(uint32_t v) { return (v & 0x7F80u) != 0x7F80u && (v & 0x7F800000u) != 0x7F800000u; }
+
+// Zero in a matrix product does not silence an infinity or a NaN, so tiles with keys that some query leaves
+// out are looked over first.  tidy_v: rows [first, first + rows) of the V tile, one wave: rows of
+// keys that nobody takes (bit of `live` clear) become zeros; says whether another row holds an infinity
+// or a NaN.  CLEAN: those become zeros as well.
+template <int D, bool CLEAN>
+__device__ __forceinline__ bool tidy_v(unsigned char* vt, int first, int rows, uint64_t live) {
+    int lane = int(threadIdx.x) & 63;
+    asm volatile("" : "+v"(lane));  // addresses computed here, not held through the main loop
+    bool odd = false;
+    for (int i = lane; i < rows * (D / 8); i += 64) {
+        const int r = first + i / (D / 8);  // any order within the row will do
+        u32x4_t* at = reinterpret_cast<u32x4_t*>(vt + first * (2 * D) + i * 16);
+        const bool take = (live >> r) & 1;
+        u32x4_t x = *at;
+        bool fine = true;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) fine = fine && pair_finite(x[e]);
+        if (!take) {
+            *at = u32x4_t{0, 0, 0, 0};
+        } else if (!fine) {
+            odd = true;
+            if constexpr (CLEAN) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    if ((x[e] & 0x7F80u) == 0x7F80u) x[e] &= 0xFFFF0000u;
+                    if ((x[e] & 0x7F800000u) == 0x7F800000u) x[e] &= 0xFFFFu;
+                }
+                *at = x;
+            }
+        }
+    }
+    return odd;
+}
+
+// The infinities and NaN of a V tile, before tidy_v cleans them away, added to the queries that take their
+// keys: what a positive probability times an infinity or a NaN gives is that infinity or NaN.
+template <int D>
+__device__ __forceinline__ void add_nonfinite(Rows<D>& w, const unsigned char* vt, int keys, uint64_t allowed) {
+    int h = (int(threadIdx.x) >> 5) & 1;
+    asm volatile("" : "+v"(h));
+    for (int j = 0; j < keys; ++j) {
+        const bool mine = (allowed >> j) & 1;
+        if (!__any(mine)) continue;
+#pragma unroll
+        for (int b = 0; b < D / 32; ++b)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const u32x2_t v = *reinterpret_cast<const u32x2_t*>(vt + j * (2 * D) + (((4 * b + e) ^ v_swz<D>(j)) << 4) + 8 * h);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t bits = i & 1 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16;
+                    if (mine && (bits & 0x7F800000u) == 0x7F800000u) w.o[b][4 * e + i] += __uint_as_float(bits);
+                }
+            }
     }
 }
 
@@ -268,8 +314,10 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
     constexpr int kTile = 64 * D * 2;
     constexpr int kRowsPerCopy = 512 / D;         // rows that one wave-wide 16-byte copy brings
     constexpr int kCopies = 64 / kRowsPerCopy / 4;  // copies per wave and tile
-    __shared__ __attribute__((aligned(1024))) unsigned char kbuf[2][kTile];
-    __shared__ __attribute__((aligned(1024))) unsigned char vbuf[2][kTile];
+    // an array per buffer, not one indexed by parity: the compiler then sees that a tile's reads do not
+    // depend on the copies still landing in the other buffer
+    __shared__ __attribute__((aligned(1024))) unsigned char kbuf0[kTile], kbuf1[kTile], vbuf0[kTile], vbuf1[kTile];
+    __shared__ int odd_tile;  // the last tile in which an infinity or a NaN was seen
     const int lane = int(threadIdx.x) & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
     // tiles of one head next to each other, heads of one XCD together
@@ -296,6 +344,7 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
     Rows<D> w;
     rows_init(w);
     load_q(w, a, b, hk, row);
+    const Offsets<D> f = offsets<D>();
 
     const uint16_t* kb = a.k + int64_t(b) * a.k_batch + int64_t(hk) * a.k_head;
     const uint16_t* vb = a.v + int64_t(b) * a.v_batch + int64_t(hk) * a.v_head;
@@ -306,28 +355,57 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
         koff[i] = uint32_t(r) * uint32_t(a.k_token) * 2u + uint32_t(p ^ k_swz<D>(r)) * 16u;
         voff[i] = uint32_t(r) * uint32_t(a.v_token) * 2u + uint32_t(p ^ v_swz<D>(r)) * 16u;
     }
-    auto issue = [&](int t, int buf) __attribute__((always_inline)) {
+    auto issue = [&](int t, unsigned char* kd, unsigned char* vd) __attribute__((always_inline)) {
         const int have = n - 64 * t < 64 ? n - 64 * t : 64;  // rows past the last key come as zeros
         const auto kr = make_rsrc(kb + int64_t(64) * t * a.k_token, uint32_t(have - 1) * uint32_t(a.k_token) * 2u + 2u * D);
         const auto vr = make_rsrc(vb + int64_t(64) * t * a.v_token, uint32_t(have - 1) * uint32_t(a.v_token) * 2u + 2u * D);
 #pragma unroll
-        for (int i = 0; i < kCopies; ++i) dma16(kr, kbuf[buf] + (wave * kCopies + i) * 1024, koff[i], 0);
+        for (int i = 0; i < kCopies; ++i) dma16(kr, kd + (wave * kCopies + i) * 1024, koff[i], 0);
 #pragma unroll
-        for (int i = 0; i < kCopies; ++i) dma16(vr, vbuf[buf] + (wave * kCopies + i) * 1024, voff[i], 0);
+        for (int i = 0; i < kCopies; ++i) dma16(vr, vd + (wave * kCopies + i) * 1024, voff[i], 0);
     };
-    if (t0 < t1) issue(t0, 0);
-    for (int t = t0; t < t1; ++t) {
-        const int buf = (t - t0) & 1;
+    // the first key that a row of the workgroup leaves out by the causal rule (all rows take those before)
+    const int64_t first = a.causal ? start + (rt * 128) / a.group + 1 : int64_t(1) << 40;
+    if (threadIdx.x == 0) odd_tile = -1;
+    // tile t is in (kc, vc); the next one goes to (kn, vn)
+    auto step = [&](int t, unsigned char* kc, unsigned char* vc, unsigned char* kn, unsigned char* vn)
+                    __attribute__((always_inline)) {
         wait_vmcnt<0>();
-        __syncthreads();  // tile t is there, and every wave is done with the other buffer
+        __syncthreads();  // tile t is there, and every wave is done with the other buffers
         const uint64_t live = live_bits(a, b, 64 * t, 64, n);
-        if (t + 1 < t1) issue(t + 1, buf ^ 1);
-        const uint64_t allowed = live & up_to(mine - 64 * int64_t(t));
-        if (__all(allowed == ~0ull))
-            tile_step<D, 2, false>(w, kbuf[buf], vbuf[buf], a.scale_log2, 0, 0);
-        else if (__any(allowed != 0))
-            tile_step<D, 2, true>(w, kbuf[buf], vbuf[buf], a.scale_log2, allowed, live);
+        if (live == 0) {  // the same in every wave
+            if (t + 1 < t1) issue(t + 1, kn, vn);
+            return;
+        }
+        const bool partial = live != ~0ull || 64 * int64_t(t) + 64 > first;  // for a row of the workgroup
+        uint64_t allowed = ~0ull;
+        bool odd = false;
+        if (partial) {
+            allowed = live & up_to(mine - 64 * int64_t(t));
+            if (tidy_v<D, false>(vc, wave * 16, 16, live)) odd_tile = t;
+            __syncthreads();
+            odd = odd_tile == t;
+        }
+        if (t + 1 < t1) issue(t + 1, kn, vn);
+        f32x16_t s[2];
+        scores<D, 2>(w, f, kc, s);
+        if (partial) mask_scores<2>(s, allowed);
+        softmax_step<D, 2>(w, s, a.scale_log2);
+        if (odd) {
+            add_nonfinite<D>(w, vc, 64, allowed);
+            __syncthreads();
+            tidy_v<D, true>(vc, wave * 16, 16, live);
+            __syncthreads();
+        }
+        weighted<D, 2>(w, f, vc, s);
+    };
+    if (t0 < t1) issue(t0, kbuf0, vbuf0);
+    int t = t0;
+    for (; t + 1 < t1; t += 2) {
+        step(t, kbuf0, vbuf0, kbuf1, vbuf1);
+        step(t + 1, kbuf1, vbuf1, kbuf0, vbuf0);
     }
+    if (t < t1) step(t, kbuf0, vbuf0, kbuf1, vbuf1);
     const float l = w.l + other_half(w.l);
     if (a.splits == 1) {
         store_o(w, a, b, hk, row, l > 0.f || l != l ? 1.f / l : 0.f);
