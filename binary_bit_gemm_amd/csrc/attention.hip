@@ -106,6 +106,7 @@ __device__ __forceinline__ void scores(const Rows<D>& w, const Offsets<D>& f, co
 // Scores of keys that the lane's query does not take (bit of `allowed` clear) to -inf.
 template <int NKB>
 __device__ __forceinline__ void mask_scores(f32x16_t (&s)[NKB], uint64_t allowed) {
+    asm volatile("");  // a branch, not a select in every tile
     const uint64_t mine = allowed >> ((threadIdx.x & 32) >> 3);
 #pragma unroll
     for (int kb = 0; kb < NKB; ++kb) {
@@ -284,6 +285,22 @@ __device__ __forceinline__ void store_part(const Rows<D>& w, const AttnArgs& a, 
     }
 }
 
+// Keeps a wave-uniform value in a scalar register: without it the compiler reloads kernel arguments inside
+// the loop, and a scalar load shares its wait with every LDS read in flight.
+template <class T>
+__device__ __forceinline__ T in_sgpr(T v) {
+    asm volatile("" : "+s"(v));
+    return v;
+}
+
+// Workgroup barrier after LDS reads and writes that leaves copies in flight (__syncthreads() waits for them).
+__device__ __forceinline__ void lds_writes_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0); vmcnt and expcnt left alone
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+
 // Keys [0, n) that a batch entry holds at all.
 __device__ __forceinline__ int live_keys(const AttnArgs& a, int b) {
     int n = a.kv_len;
@@ -294,12 +311,12 @@ __device__ __forceinline__ int live_keys(const AttnArgs& a, int b) {
     return n;
 }
 
-// Bits of the keys key0 .. key0 + width - 1 that the mask and the length leave (wave-uniform).
-__device__ __forceinline__ uint64_t live_bits(const AttnArgs& a, int b, int key0, int width, int n) {
+// Bits of the keys key0 .. key0 + 63 (key0 < n) that the mask and the length leave (wave-uniform).
+__device__ __forceinline__ uint64_t live_bits(const uint8_t* mask, int key0, int n) {
+    const uint64_t in = n - key0 >= 64 ? ~0ull : (1ull << (n - key0)) - 1;
+    if (mask == nullptr) return in;
     const int lane = int(threadIdx.x) & 63;
-    const bool in = lane < width && key0 + lane < n;
-    if (a.mask == nullptr) return __ballot(in);
-    return __ballot(in && a.mask[int64_t(b) * a.mask_batch + key0 + lane] != 0);
+    return __ballot(key0 + lane < n && mask[key0 + lane] != 0);
 }
 
 // Bits 0 .. rel (none for rel < 0).
@@ -328,74 +345,78 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
     id /= a.splits;
     const int hk = id % a.kv_heads, b = id / a.kv_heads;
 
-    const int n = live_keys(a, b);
+    const int n = in_sgpr(live_keys(a, b));
     const int row = rt * 128 + wave * 32 + (lane & 31);
     const int64_t start = a.causal ? (a.start != nullptr ? a.start[b] : 0) : 0;
     // the last key of the workgroup's and of the lane's rows
     const int last_row = rt * 128 + 127 < a.rows ? rt * 128 + 127 : a.rows - 1;
     const int64_t last = a.causal ? start + last_row / a.group : int64_t(n) - 1;
     const int64_t mine = a.causal ? start + (row < a.rows ? row : a.rows - 1) / a.group : int64_t(1) << 40;
+    // the first key that a row of the workgroup leaves out by the causal rule (all rows take those before)
+    const int64_t first64 = a.causal ? start + (rt * 128) / a.group + 1 : n;
     const int64_t end64 = last + 1 < n ? last + 1 : n;
     const int end = end64 < 0 ? 0 : int(end64);
+    const int first = in_sgpr(first64 < 0 ? 0 : first64 < n ? int(first64) : n);
     const int tiles = (end + 63) / 64;
     const int t0 = split * a.tiles_per_split;
-    const int t1 = t0 + a.tiles_per_split < tiles ? t0 + a.tiles_per_split : tiles;
+    const int t1 = in_sgpr(t0 + a.tiles_per_split < tiles ? t0 + a.tiles_per_split : tiles);
 
     Rows<D> w;
     rows_init(w);
     load_q(w, a, b, hk, row);
     const Offsets<D> f = offsets<D>();
 
-    const uint16_t* kb = a.k + int64_t(b) * a.k_batch + int64_t(hk) * a.k_head;
-    const uint16_t* vb = a.v + int64_t(b) * a.v_batch + int64_t(hk) * a.v_head;
+    // the next tile to copy, and its key and value rows
+    const uint32_t k_row = in_sgpr(uint32_t(a.k_token) * 2u), v_row = in_sgpr(uint32_t(a.v_token) * 2u);
+    const unsigned char* kp = reinterpret_cast<const unsigned char*>(a.k + int64_t(b) * a.k_batch + int64_t(hk) * a.k_head) + int64_t(64) * t0 * k_row;
+    const unsigned char* vp = reinterpret_cast<const unsigned char*>(a.v + int64_t(b) * a.v_batch + int64_t(hk) * a.v_head) + int64_t(64) * t0 * v_row;
+    const uint8_t* mask = in_sgpr(a.mask == nullptr ? nullptr : a.mask + int64_t(b) * a.mask_batch);
+    const float c = in_sgpr(a.scale_log2);
     uint32_t koff[kCopies], voff[kCopies];
 #pragma unroll
     for (int i = 0; i < kCopies; ++i) {
         const int r = (wave * kCopies + i) * kRowsPerCopy + lane / (D / 8), p = lane % (D / 8);
-        koff[i] = uint32_t(r) * uint32_t(a.k_token) * 2u + uint32_t(p ^ k_swz<D>(r)) * 16u;
-        voff[i] = uint32_t(r) * uint32_t(a.v_token) * 2u + uint32_t(p ^ v_swz<D>(r)) * 16u;
+        koff[i] = uint32_t(r) * k_row + uint32_t(p ^ k_swz<D>(r)) * 16u;
+        voff[i] = uint32_t(r) * v_row + uint32_t(p ^ v_swz<D>(r)) * 16u;
     }
     auto issue = [&](int t, unsigned char* kd, unsigned char* vd) __attribute__((always_inline)) {
-        const int have = n - 64 * t < 64 ? n - 64 * t : 64;  // rows past the last key come as zeros
-        const auto kr = make_rsrc(kb + int64_t(64) * t * a.k_token, uint32_t(have - 1) * uint32_t(a.k_token) * 2u + 2u * D);
-        const auto vr = make_rsrc(vb + int64_t(64) * t * a.v_token, uint32_t(have - 1) * uint32_t(a.v_token) * 2u + 2u * D);
+        const uint32_t rest = uint32_t(n - 64 * t < 64 ? n - 64 * t : 64) - 1u;  // rows past the last key come as zeros
+        const auto kr = make_rsrc(kp, rest * k_row + 2u * D);
+        const auto vr = make_rsrc(vp, rest * v_row + 2u * D);
+        kp += uint64_t(64) * k_row;
+        vp += uint64_t(64) * v_row;
 #pragma unroll
         for (int i = 0; i < kCopies; ++i) dma16(kr, kd + (wave * kCopies + i) * 1024, koff[i], 0);
 #pragma unroll
         for (int i = 0; i < kCopies; ++i) dma16(vr, vd + (wave * kCopies + i) * 1024, voff[i], 0);
     };
-    // the first key that a row of the workgroup leaves out by the causal rule (all rows take those before)
-    const int64_t first = a.causal ? start + (rt * 128) / a.group + 1 : int64_t(1) << 40;
     if (threadIdx.x == 0) odd_tile = -1;
     // tile t is in (kc, vc); the next one goes to (kn, vn)
     auto step = [&](int t, unsigned char* kc, unsigned char* vc, unsigned char* kn, unsigned char* vn)
                     __attribute__((always_inline)) {
         wait_vmcnt<0>();
         __syncthreads();  // tile t is there, and every wave is done with the other buffers
-        const uint64_t live = live_bits(a, b, 64 * t, 64, n);
-        if (live == 0) {  // the same in every wave
-            if (t + 1 < t1) issue(t + 1, kn, vn);
-            return;
-        }
-        const bool partial = live != ~0ull || 64 * int64_t(t) + 64 > first;  // for a row of the workgroup
+        const uint64_t live = live_bits(mask, 64 * t, n);
+        if (t + 1 < t1) issue(t + 1, kn, vn);
+        if (live == 0) return;  // the same in every wave
+        const bool partial = live != ~0ull || 64 * t + 64 > first;  // for a row of the workgroup
         uint64_t allowed = ~0ull;
         bool odd = false;
         if (partial) {
             allowed = live & up_to(mine - 64 * int64_t(t));
             if (tidy_v<D, false>(vc, wave * 16, 16, live)) odd_tile = t;
-            __syncthreads();
+            lds_writes_barrier();
             odd = odd_tile == t;
         }
-        if (t + 1 < t1) issue(t + 1, kn, vn);
         f32x16_t s[2];
         scores<D, 2>(w, f, kc, s);
         if (partial) mask_scores<2>(s, allowed);
-        softmax_step<D, 2>(w, s, a.scale_log2);
+        softmax_step<D, 2>(w, s, c);
         if (odd) {
             add_nonfinite<D>(w, vc, 64, allowed);
-            __syncthreads();
+            lds_writes_barrier();
             tidy_v<D, true>(vc, wave * 16, 16, live);
-            __syncthreads();
+            lds_writes_barrier();
         }
         weighted<D, 2>(w, f, vc, s);
     };
