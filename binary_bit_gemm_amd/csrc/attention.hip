@@ -116,16 +116,20 @@ __device__ __forceinline__ void mask_scores(f32x16_t (&s)[NKB], uint64_t allowed
     }
 }
 
-// The softmax's step: s becomes the probabilities (to the maximum so far), O, l and m follow.
-template <int D, int NKB>
-__device__ __forceinline__ void softmax_step(Rows<D>& w, f32x16_t (&s)[NKB], float c) {
+// Largest score of the lane's row among s.
+template <int NKB>
+__device__ __forceinline__ float row_max(const f32x16_t (&s)[NKB]) {
     float top = s[0][0];
 #pragma unroll
     for (int kb = 0; kb < NKB; ++kb)
 #pragma unroll
         for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kb][i]);
-    top = fmaxf(top, other_half(top));
-    // grow m where a row of the wave needs it
+    return fmaxf(top, other_half(top));
+}
+
+// m grows to `top` where a row of the wave needs it, and l and O follow.
+template <int D>
+__device__ __forceinline__ void grow(Rows<D>& w, float top, float c) {
     if (__any((top - w.m) * c > kLazy || (w.m == kNegInf && top != kNegInf))) {
         const float m = fmaxf(w.m, top);
         const float f = m == kNegInf ? 1.f : __builtin_amdgcn_exp2f((w.m - m) * c);
@@ -136,7 +140,18 @@ __device__ __forceinline__ void softmax_step(Rows<D>& w, f32x16_t (&s)[NKB], flo
 #pragma unroll
             for (int i = 0; i < 16; ++i) w.o[b][i] *= f;
     }
-    const float mc = w.m == kNegInf ? 0.f : w.m * c;
+}
+
+// What the exponents subtract: c m, and 0 for a row that has no key yet (its scores are -inf).
+template <int D>
+__device__ __forceinline__ float offset(const Rows<D>& w, float c) {
+    return w.m == kNegInf ? 0.f : w.m * c;
+}
+
+// s becomes the probabilities to the maximum so far, l their sum.
+template <int D, int NKB>
+__device__ __forceinline__ void probabilities(Rows<D>& w, f32x16_t (&s)[NKB], float c) {
+    const float mc = offset(w, c);
     float sum = 0.f;
 #pragma unroll
     for (int kb = 0; kb < NKB; ++kb)
@@ -170,6 +185,18 @@ __device__ __forceinline__ void weighted(Rows<D>& w, const Offsets<D>& f, const 
 }
 
 __device__ __forceinline__ bool pair_finite(uint32_t v) { return (v & 0x7F80u) != 0x7F80u && (v & 0x7F800000u) != 0x7F800000u; }
+
+// One tile's probabilities and values and the next tile's scores in one block of code, so that the matrix cores
+// have work while the vector unit takes the exponentials: s (scores of the tile whose values are at
+// vt) is used up, sn becomes the scores of the K tile at kt; the result is the rows' largest new score.
+template <int D>
+__device__ __forceinline__ float fused_step(Rows<D>& w, const Offsets<D>& f, const unsigned char* kt, const unsigned char* vt,
+                                            f32x16_t (&s)[2], f32x16_t (&sn)[2], float c) {
+    scores<D, 2>(w, f, kt, sn);
+    probabilities<D, 2>(w, s, c);
+    weighted<D, 2>(w, f, vt, s);
+    return row_max<2>(sn);
+}
 
 // Zero in a matrix product does not silence an infinity or a NaN, so tiles with keys that some query leaves
 // out are looked over first.  tidy_v: rows [first, first + rows) of the V tile, one wave: rows of
@@ -311,14 +338,6 @@ __device__ __forceinline__ int live_keys(const AttnArgs& a, int b) {
     return n;
 }
 
-// Bits of the keys key0 .. key0 + 63 (key0 < n) that the mask and the length leave (wave-uniform).
-__device__ __forceinline__ uint64_t live_bits(const uint8_t* mask, int key0, int n) {
-    const uint64_t in = n - key0 >= 64 ? ~0ull : (1ull << (n - key0)) - 1;
-    if (mask == nullptr) return in;
-    const int lane = int(threadIdx.x) & 63;
-    return __ballot(key0 + lane < n && mask[key0 + lane] != 0);
-}
-
 // Bits 0 .. rel (none for rel < 0).
 __device__ __forceinline__ uint64_t up_to(int64_t rel) {
     return rel < 0 ? 0ull : rel >= 63 ? ~0ull : (2ull << rel) - 1;
@@ -379,31 +398,62 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
         koff[i] = uint32_t(r) * k_row + uint32_t(p ^ k_swz<D>(r)) * 16u;
         voff[i] = uint32_t(r) * v_row + uint32_t(p ^ v_swz<D>(r)) * 16u;
     }
-    auto issue = [&](int t, unsigned char* kd, unsigned char* vd) __attribute__((always_inline)) {
+    // The tiles' copies, each K and V tile issued once, in order.
+    int k_next = t0, v_next = t0;
+    auto issue_k = [&](int t, unsigned char* kd) __attribute__((always_inline)) {
+        if (k_next != t || t >= t1) return;
+        ++k_next;
         const uint32_t rest = uint32_t(n - 64 * t < 64 ? n - 64 * t : 64) - 1u;  // rows past the last key come as zeros
         const auto kr = make_rsrc(kp, rest * k_row + 2u * D);
-        const auto vr = make_rsrc(vp, rest * v_row + 2u * D);
         kp += uint64_t(64) * k_row;
-        vp += uint64_t(64) * v_row;
 #pragma unroll
         for (int i = 0; i < kCopies; ++i) dma16(kr, kd + (wave * kCopies + i) * 1024, koff[i], 0);
+    };
+    auto issue_v = [&](int t, unsigned char* vd) __attribute__((always_inline)) {
+        if (v_next != t || t >= t1) return;
+        ++v_next;
+        const uint32_t rest = uint32_t(n - 64 * t < 64 ? n - 64 * t : 64) - 1u;
+        const auto vr = make_rsrc(vp, rest * v_row + 2u * D);
+        vp += uint64_t(64) * v_row;
 #pragma unroll
         for (int i = 0; i < kCopies; ++i) dma16(vr, vd + (wave * kCopies + i) * 1024, voff[i], 0);
     };
-    if (threadIdx.x == 0) odd_tile = -1;
-    // tile t is in (kc, vc); the next one goes to (kn, vn)
-    auto step = [&](int t, unsigned char* kc, unsigned char* vc, unsigned char* kn, unsigned char* vn)
-                    __attribute__((always_inline)) {
+    // Every copy issued so far is there, and every wave is done with the tiles before.
+    auto arrive = [&]() __attribute__((always_inline)) {
         wait_vmcnt<0>();
-        __syncthreads();  // tile t is there, and every wave is done with the other buffers
-        const uint64_t live = live_bits(mask, 64 * t, n);
-        if (t + 1 < t1) issue(t + 1, kn, vn);
+        __syncthreads();
+    };
+    // The lane's bytes of the mask for tiles t, t + 1 and t + 2, fetched before they are needed.
+    auto fetch = [&](int t) __attribute__((always_inline)) {
+        return mask != nullptr && 64 * t + lane < n ? mask[64 * t + lane] : uint8_t(0);
+    };
+    uint8_t m0 = fetch(t0), m1 = fetch(t0 + 1), m2 = fetch(t0 + 2);
+    // Whole tiles: all rows of the workgroup take all 64 keys.
+    const int whole_end = in_sgpr((first < 64 * t1 ? first : 64 * t1) / 64);
+    auto whole = [&](int t, uint8_t byte) __attribute__((always_inline)) {
+        return t < whole_end && (mask == nullptr || __ballot(byte != 0) == ~0ull);
+    };
+    if (threadIdx.x == 0) odd_tile = -1;
+    int t = t0;
+
+    // One tile of any kind, in (kc, vc); the next one goes to (kn, vn).
+    auto any_step = [&](unsigned char* kc, unsigned char* vc, unsigned char* kn, unsigned char* vn)
+                        __attribute__((always_inline)) {
+        arrive();
+        const uint64_t in = n - 64 * t >= 64 ? ~0ull : (1ull << (n - 64 * t)) - 1;
+        const uint64_t live = mask != nullptr ? __ballot(m0 != 0) : in;
+        const bool partial = !whole(t, m0);
+        m0 = m1;
+        m1 = m2;
+        m2 = fetch(t + 3);
+        issue_k(t + 1, kn);
+        issue_v(t + 1, vn);
+        ++t;
         if (live == 0) return;  // the same in every wave
-        const bool partial = live != ~0ull || 64 * t + 64 > first;  // for a row of the workgroup
         uint64_t allowed = ~0ull;
         bool odd = false;
         if (partial) {
-            allowed = live & up_to(mine - 64 * int64_t(t));
+            allowed = live & up_to(mine - 64 * int64_t(t - 1));
             if (tidy_v<D, false>(vc, wave * 16, 16, live)) odd_tile = t;
             lds_writes_barrier();
             odd = odd_tile == t;
@@ -411,7 +461,8 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
         f32x16_t s[2];
         scores<D, 2>(w, f, kc, s);
         if (partial) mask_scores<2>(s, allowed);
-        softmax_step<D, 2>(w, s, c);
+        grow(w, row_max<2>(s), c);
+        probabilities<D, 2>(w, s, c);
         if (odd) {
             add_nonfinite<D>(w, vc, 64, allowed);
             lds_writes_barrier();
@@ -420,13 +471,44 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
         }
         weighted<D, 2>(w, f, vc, s);
     };
-    if (t0 < t1) issue(t0, kbuf0, vbuf0);
-    int t = t0;
-    for (; t + 1 < t1; t += 2) {
-        step(t, kbuf0, vbuf0, kbuf1, vbuf1);
-        step(t + 1, kbuf1, vbuf1, kbuf0, vbuf0);
+
+    issue_k(t0, kbuf0);
+    issue_v(t0, vbuf0);
+    while (t < t1) {
+        if (whole(t, m0) && whole(t + 1, m1) && whole(t + 2, m2)) {
+            // a run of whole tiles, two per turn; the scores are one tile ahead of the values
+            arrive();
+            issue_k(t + 1, kbuf1);
+            f32x16_t s0[2], s1[2];
+            scores<D, 2>(w, f, kbuf0, s0);
+            grow(w, row_max<2>(s0), c);
+            do {
+                arrive();
+                issue_k(t + 2, kbuf0);
+                issue_v(t + 1, vbuf1);
+                grow(w, fused_step<D>(w, f, kbuf1, vbuf0, s0, s1, c), c);
+                arrive();
+                issue_k(t + 3, kbuf1);
+                issue_v(t + 2, vbuf0);
+                m0 = m2;
+                m1 = fetch(t + 3);
+                m2 = fetch(t + 4);
+                grow(w, fused_step<D>(w, f, kbuf0, vbuf1, s1, s0, c), c);
+                t += 2;
+            } while (whole(t + 1, m1) && whole(t + 2, m2));
+            arrive();
+            issue_v(t + 1, vbuf1);
+            probabilities<D, 2>(w, s0, c);
+            weighted<D, 2>(w, f, vbuf0, s0);
+            m0 = m1;
+            m1 = m2;
+            m2 = fetch(t + 3);
+            ++t;
+        } else {
+            any_step(kbuf0, vbuf0, kbuf1, vbuf1);
+        }
+        if (t < t1) any_step(kbuf1, vbuf1, kbuf0, vbuf0);
     }
-    if (t < t1) step(t, kbuf0, vbuf0, kbuf1, vbuf1);
     const float l = w.l + other_half(w.l);
     if (a.splits == 1) {
         store_o(w, a, b, hk, row, l > 0.f || l != l ? 1.f / l : 0.f);
