@@ -4,14 +4,22 @@
 // the heads of a group read each key and value once, also where there is one query token.  Keys go by
 // in tiles, with the running maximum m and sum l of the softmax per row (one pass):
 //     p = exp2(c s - c m),  l += sum p,  O += p v,      c = scale * log2(e);
-// where m grows, l and O are multiplied by exp2(c m_old - c m_new).
+// where m moves, l and O are multiplied by exp2(c m_old - c m_new).
 //
-// The products are computed transposed, S^T = K Q^T and O^T = V^T P^T, with 32x32x16 MFMAs: a lane
-// then holds 16 scores of one query per 32 keys (lane l: query l % 32, keys 8 (i / 4) + 4 (l / 32) + i % 4),
-// so the row maximum is an in-lane maximum and one exchange between the two lane halves, the
-// factors of m and l are one number per lane, and the probabilities, rounded to bf16 in pairs, are
-// already the B operand of the second product: its K order is the order in which the lane holds
-// them, and V^T is read from LDS in that order by transposing reads (4 keys x 16 columns each).
+// The products are computed transposed, S^T = K Q^T and O^T = V^T P^T, with 16x16x32 MFMAs: a lane then
+// holds scores of one query (lane (q, l16) of a 16x16 block: query l16, keys 4q .. 4q + 3), the factors of m
+// and l are one number per lane, and the probabilities, rounded to bf16 in pairs, are already
+// the B operand of the second product: its K order is the order in which the lane holds them (keys 4q ..
+// of one 16-key block, then of the next), and V^T is read from LDS in that order by transposing reads.
+// 16x16x32 and not 32x32x16: on this SIMD a 16x16x32 MFMA leaves room for two vector instructions, a
+// 32x32x16 one (2x the work) for none, and the exponentials are as long as the products.
+//
+// Vector instructions per score are what is saved on:
+//   * l is a matrix product too (P^T with ones), which also makes it the sum of the rounded probabilities;
+//   * m is not followed tile by tile.  It stays where it was, kHeadroom powers of two above the largest score
+//     then seen (fp32 and bf16 have the exponents for it), as long as every new p is below 2, which one
+//     OR over the packed probabilities tells (bit 14 of a positive bf16 is set from 2 on); only
+//     otherwise is the maximum taken, O and l rescaled and the probabilities computed again.
 //
 // Rounding to bf16: the probabilities before the second product (the matrix cores' input; relative
 // 2^-8 each, averaged over the keys) and O at the store.  Scores, m, l and O are fp32.
@@ -24,179 +32,209 @@ namespace {
 typedef short s16x4_t __attribute__((ext_vector_type(4)));
 typedef short s16x8_t __attribute__((ext_vector_type(8)));
 
+// Two bf16 in one word, rounded to nearest even (one instruction).
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    const bf16x2_t v = {static_cast<__bf16>(lo), static_cast<__bf16>(hi)};
+    return __builtin_bit_cast(uint32_t, v);
+}
+
 constexpr float kNegInf = -__builtin_inff();
-// A maximum that grows by less than this (in powers of two) leaves m as it is: p then reaches 2^8
-// instead of 1, which fp32 sums and the bf16 mantissa do not notice, and O is not rescaled.
-constexpr float kLazy = 8.f;
+constexpr float kHeadroom = 32.f;  // powers of two between the largest score and 1; p reaches 2^33 times as much before m moves
+constexpr uint32_t kTooLarge = 0x40004000u;  // a packed pair of p has one of 2 or more
 
 // ---- layouts in LDS: rows of D elements in 16-byte chunks, chunk c of row r at position c ^ swz(r) ----
-// K is read 16 bytes per lane from 32 consecutive rows at one chunk; 16 rows must land in 16 different
-// 16-byte bank groups of the 256-byte line.
+// K is read 16 bytes per lane from 16 consecutive rows at one chunk, which must land in 16 different
+// 16-byte bank groups of the 256-byte line (and lanes l and l + 16 in one 32-byte block: k_chunk).
 template <int D>
 __device__ __forceinline__ int k_swz(int r) {
     return D == 128 ? (r & 15) : ((r >> 1) & 7);
 }
-// V is read by transposing reads, 8 bytes per lane: 16 lanes take 4 rows x 32 bytes, the wave instruction
-// rows 4h .. 4h+3 x 64 bytes.  The four rows' 64-byte windows must not share banks.
+// The chunk of a row that lane quarter q multiplies in MFMA ks of a product over D (any order will do
+// that Q and K share).
+__device__ __forceinline__ int k_chunk(int ks, int q) { return 8 * (ks / 2) + 4 * (q >> 1) + (q & 1) + 2 * (ks % 2); }
+// V is read by transposing reads, 8 bytes per lane: 16 lanes take 4 rows x 32 bytes, half a wave 8
+// consecutive rows, whose 32-byte pieces must not share banks.
 template <int D>
 __device__ __forceinline__ int v_swz(int r) {
-    return D == 128 ? (r & 3) << 2 : ((r >> 1) & 1) << 2;
+    return D == 128 ? (r & 7) << 1 : ((r >> 1) & 3) << 1;
 }
 
-// One wave's state for 32 rows.
+// One wave's state for 32 rows, two blocks of 16.
 template <int D>
 struct Rows {
-    bf16x8_t q[D / 16];   // B operand: lane (query l % 32, h): elements 16 kk + 8 h ..
-    f32x16_t o[D / 32];   // O^T
-    float m, l;           // the softmax's maximum (raw scores) and the lane half's share of its sum
+    bf16x8_t q[D / 32][2];  // B operand: lane (q, query): chunk k_chunk(ks, q)
+    f32x4_t o[D / 16][2];   // O^T: lane (q, query), columns 16 db + 4q ..
+    f32x4_t l[2];           // the softmax's sum (four times the same)
+    float mc[2];            // what the exponents subtract: c times the maximum then seen + kHeadroom; -inf: no key yet
 };
+
+// Scores, then probabilities of a tile's 64 keys: [16-key block][row block], keys 16 kb + 4q ..
+typedef f32x4_t Scores[4][2];
+// Probabilities as B operands: [32-key block][row block].
+typedef u32x4_t Probs[2][2];
 
 template <int D>
 __device__ __forceinline__ void rows_init(Rows<D>& w) {
 #pragma unroll
-    for (int b = 0; b < D / 32; ++b)
+    for (int qb = 0; qb < 2; ++qb) {
 #pragma unroll
-        for (int i = 0; i < 16; ++i) w.o[b][i] = 0.f;
-    w.m = kNegInf;
-    w.l = 0.f;
-}
-
-__device__ __forceinline__ float other_half(float v) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    return __uint_as_float((threadIdx.x & 32) ? r[0] : r[1]);
+        for (int b = 0; b < D / 16; ++b) w.o[b][qb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        w.l[qb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        w.mc[qb] = kNegInf;
+    }
 }
 
 // The lane's byte offsets into a K and a V tile, without the constants that the compiler folds into the
-// instructions: K row l % 32 at chunk 2 kk + h (rows 32 apart have the same swizzle), V row 4 h +
-// (l % 16) / 4 at column block b (rows 4 apart as well).
+// instructions: K row l16 at chunk k_chunk (rows 16 apart have the same swizzle), V row 4q + l16 / 4 at
+// column block b (rows 16 apart as well).
 template <int D>
 struct Offsets {
-    int k[D / 16], v[D / 32];
+    int k[D / 32], v[D / 16];
 };
 
 template <int D>
 __device__ __forceinline__ Offsets<D> offsets() {
     const int lane = int(threadIdx.x) & 63;
-    const int l32 = lane & 31, h = lane >> 5, i16 = lane & 15, dsel = (lane >> 4) & 1;
+    const int q = lane >> 4, l16 = lane & 15;
     Offsets<D> f;
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) f.k[kk] = l32 * (2 * D) + (((2 * kk + h) ^ k_swz<D>(l32)) << 4);
+    for (int ks = 0; ks < D / 32; ++ks) f.k[ks] = l16 * (2 * D) + ((k_chunk(ks, q) ^ k_swz<D>(l16)) << 4);
 #pragma unroll
-    for (int b = 0; b < D / 32; ++b) {
-        const int r = 4 * h + (i16 >> 2), chunk = 4 * b + 2 * dsel + ((i16 & 3) >> 1);
-        f.v[b] = r * (2 * D) + ((chunk ^ v_swz<D>(r)) << 4) + 8 * (i16 & 1);
+    for (int b = 0; b < D / 16; ++b) {
+        const int r = 4 * q + (l16 >> 2), chunk = 2 * b + ((l16 & 3) >> 1);
+        f.v[b] = r * (2 * D) + ((chunk ^ v_swz<D>(r)) << 4) + 8 * (l16 & 1);
     }
     return f;
 }
 
-// Scores of NKB * 32 keys of the K tile at kt.
-template <int D, int NKB>
-__device__ __forceinline__ void scores(const Rows<D>& w, const Offsets<D>& f, const unsigned char* kt, f32x16_t (&s)[NKB]) {
-#pragma unroll
-    for (int kb = 0; kb < NKB; ++kb) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[kb][i] = 0.f;
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk)
-            s[kb] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                *reinterpret_cast<const bf16x8_t*>(kt + f.k[kk] + kb * 32 * (2 * D)), w.q[kk], s[kb], 0, 0, 0);
-    }
-}
-
-// Scores of keys that the lane's query does not take (bit of `allowed` clear) to -inf.
-template <int NKB>
-__device__ __forceinline__ void mask_scores(f32x16_t (&s)[NKB], uint64_t allowed) {
-    asm volatile("");  // a branch, not a select in every tile
-    const uint64_t mine = allowed >> ((threadIdx.x & 32) >> 3);
-#pragma unroll
-    for (int kb = 0; kb < NKB; ++kb) {
-        const uint32_t bits = uint32_t(mine >> (32 * kb));
-#pragma unroll
-        for (int i = 0; i < 16; ++i) s[kb][i] = (bits >> (8 * (i / 4) + i % 4)) & 1u ? s[kb][i] : kNegInf;
-    }
-}
-
-// Largest score of the lane's row among s.
-template <int NKB>
-__device__ __forceinline__ float row_max(const f32x16_t (&s)[NKB]) {
-    float top = s[0][0];
-#pragma unroll
-    for (int kb = 0; kb < NKB; ++kb)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kb][i]);
-    return fmaxf(top, other_half(top));
-}
-
-// m grows to `top` where a row of the wave needs it, and l and O follow.
+// Scores of the K tile at kt.
 template <int D>
-__device__ __forceinline__ void grow(Rows<D>& w, float top, float c) {
-    if (__any((top - w.m) * c > kLazy || (w.m == kNegInf && top != kNegInf))) {
-        const float m = fmaxf(w.m, top);
-        const float f = m == kNegInf ? 1.f : __builtin_amdgcn_exp2f((w.m - m) * c);
-        w.m = m;
-        w.l *= f;
+__device__ __forceinline__ void scores(const Rows<D>& w, const Offsets<D>& f, const unsigned char* kt, Scores& s) {
 #pragma unroll
-        for (int b = 0; b < D / 32; ++b)
+    for (int kb = 0; kb < 4; ++kb) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) w.o[b][i] *= f;
-    }
-}
-
-// What the exponents subtract: c m, and 0 for a row that has no key yet (its scores are -inf).
-template <int D>
-__device__ __forceinline__ float offset(const Rows<D>& w, float c) {
-    return w.m == kNegInf ? 0.f : w.m * c;
-}
-
-// s becomes the probabilities to the maximum so far, l their sum.
-template <int D, int NKB>
-__device__ __forceinline__ void probabilities(Rows<D>& w, f32x16_t (&s)[NKB], float c) {
-    const float mc = offset(w, c);
-    float sum = 0.f;
+        for (int qb = 0; qb < 2; ++qb) s[kb][qb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int kb = 0; kb < NKB; ++kb)
+        for (int ks = 0; ks < D / 32; ++ks) {
+            const bf16x8_t k = *reinterpret_cast<const bf16x8_t*>(kt + f.k[ks] + kb * 16 * (2 * D));
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            s[kb][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][i], c, -mc));
-            sum += s[kb][i];
+            for (int qb = 0; qb < 2; ++qb) s[kb][qb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, w.q[ks][qb], s[kb][qb], 0, 0, 0);
         }
-    w.l += sum;
+    }
 }
 
-// O += P V for the V tile at vt.
-template <int D, int NKB>
-__device__ __forceinline__ void weighted(Rows<D>& w, const Offsets<D>& f, const unsigned char* vt, const f32x16_t (&s)[NKB]) {
+// Scores of keys that a lane's query does not take (bit of its `allowed` clear) to -inf.
+__device__ __forceinline__ void mask_scores(Scores& s, const uint64_t (&allowed)[2]) {
+    asm volatile("");  // a branch, not a select in every tile
 #pragma unroll
-    for (int k2 = 0; k2 < 2 * NKB; ++k2) {  // 16 keys each
-        bf16x8_t p;
+    for (int qb = 0; qb < 2; ++qb) {
+        const uint64_t mine = allowed[qb] >> ((threadIdx.x & 48) >> 2);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) p[i] = static_cast<__bf16>(s[k2 / 2][8 * (k2 % 2) + i]);
+        for (int kb = 0; kb < 4; ++kb) {
+            const uint32_t bits = uint32_t(mine >> (16 * kb));
 #pragma unroll
-        for (int b = 0; b < D / 32; ++b) {
+            for (int i = 0; i < 4; ++i) s[kb][qb][i] = (bits >> i) & 1u ? s[kb][qb][i] : kNegInf;
+        }
+    }
+}
+
+// m follows the largest of the scores s where it has to, and l and O follow m.
+template <int D>
+__device__ __forceinline__ void grow(Rows<D>& w, const Scores& s, float c) {
+#pragma unroll
+    for (int qb = 0; qb < 2; ++qb) {
+        float top = kNegInf;
+#pragma unroll
+        for (int kb = 0; kb < 4; ++kb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, s[kb][qb][i]);
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32)) * c;
+        // p below 2: the packed test's bound, with its rounding
+        const bool move = top > kNegInf && !(top - w.mc[qb] < 0.99f);
+        if (__any(move)) {
+            const float mc = move ? top + kHeadroom : w.mc[qb];
+            const float f = move ? __builtin_amdgcn_exp2f(w.mc[qb] - mc) : 1.f;
+            w.mc[qb] = mc;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w.l[qb][i] *= f;
+#pragma unroll
+            for (int b = 0; b < D / 16; ++b)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w.o[b][qb][i] *= f;
+        }
+    }
+}
+
+// The probabilities of s; returns an OR of them all.
+template <int D>
+__device__ __forceinline__ uint32_t probabilities(const Rows<D>& w, const Scores& s, Probs& p, float c) {
+    uint32_t any = 0;
+#pragma unroll
+    for (int qb = 0; qb < 2; ++qb) {
+        const float mc = w.mc[qb] == kNegInf ? 0.f : w.mc[qb];  // without a key yet every score is -inf
+#pragma unroll
+        for (int kk = 0; kk < 2; ++kk)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const f32x4_t& x = s[2 * kk + e / 2][qb];
+                const float lo = __builtin_amdgcn_exp2f(__builtin_fmaf(x[2 * (e % 2)], c, -mc));
+                const float hi = __builtin_amdgcn_exp2f(__builtin_fmaf(x[2 * (e % 2) + 1], c, -mc));
+                const uint32_t v = pack_bf16(lo, hi);
+                p[kk][qb][e] = v;
+                any |= v;
+            }
+    }
+    return any;
+}
+
+// O += P V for the V tile at vt, and l.
+template <int D>
+__device__ __forceinline__ void weighted(Rows<D>& w, const Offsets<D>& f, const unsigned char* vt, const Probs& p) {
+    const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
+#pragma unroll
+    for (int kk = 0; kk < 2; ++kk) {  // 32 keys each
+#pragma unroll
+        for (int qb = 0; qb < 2; ++qb)
+            w.l[qb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, __builtin_bit_cast(bf16x8_t, p[kk][qb]), w.l[qb], 0, 0, 0);
+#pragma unroll
+        for (int b = 0; b < D / 16; ++b) {
             s16x4_t v[2];
 #pragma unroll
             for (int part = 0; part < 2; ++part)
                 v[part] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                    (__attribute__((address_space(3))) s16x4_t*)(vt + f.v[b] + (16 * k2 + 8 * part) * (2 * D)));
-            const s16x8_t a = __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7);
-            w.o[b] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a), p, w.o[b], 0, 0, 0);
+                    (__attribute__((address_space(3))) s16x4_t*)(vt + f.v[b] + (32 * kk + 16 * part) * (2 * D)));
+            const bf16x8_t a = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
+#pragma unroll
+            for (int qb = 0; qb < 2; ++qb)
+                w.o[b][qb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, p[kk][qb]), w.o[b][qb], 0, 0, 0);
         }
     }
 }
 
-__device__ __forceinline__ bool pair_finite(uint32_t v) { return (v & 0x7F80u) != 0x7F80u && (v & 0x7F800000u) != 0x7F800000u; }
-
-// One tile's probabilities and values and the next tile's scores in one block of code, so that the matrix cores
-// have work while the vector unit takes the exponentials: s (scores of the tile whose values are at
-// vt) is used up, sn becomes the scores of the K tile at kt; the result is the rows' largest new score.
+// Whether the wave's probabilities have to be computed again with a larger m.
 template <int D>
-__device__ __forceinline__ float fused_step(Rows<D>& w, const Offsets<D>& f, const unsigned char* kt, const unsigned char* vt,
-                                            f32x16_t (&s)[2], f32x16_t (&sn)[2], float c) {
-    scores<D, 2>(w, f, kt, sn);
-    probabilities<D, 2>(w, s, c);
-    weighted<D, 2>(w, f, vt, s);
-    return row_max<2>(sn);
+__device__ __forceinline__ bool outgrown(const Rows<D>& w, uint32_t any) {
+    return __any((any & kTooLarge) != 0 || w.mc[0] == kNegInf || w.mc[1] == kNegInf);
 }
+
+// One tile's values and the next tile's scores: the exponentials of s (scores of the tile whose values are
+// at vt) are taken while the matrix cores compute sn, the scores of the K tile at kt.
+template <int D>
+__device__ __forceinline__ void fused_step(Rows<D>& w, const Offsets<D>& f, const unsigned char* kt, const unsigned char* vt,
+                                           const Scores& s, Scores& sn, float c) {
+    Probs p;
+    scores<D>(w, f, kt, sn);
+    const uint32_t any = probabilities<D>(w, s, p, c);
+    if (outgrown(w, any)) {
+        grow(w, s, c);
+        probabilities<D>(w, s, p, c);
+    }
+    weighted<D>(w, f, vt, p);
+}
+
+__device__ __forceinline__ bool pair_finite(uint32_t v) { return (v & 0x7F80u) != 0x7F80u && (v & 0x7F800000u) != 0x7F800000u; }
 
 // Zero in a matrix product does not silence an infinity or a NaN, so tiles with keys that some query leaves
 // out are looked over first.  tidy_v: rows [first, first + rows) of the V tile, one wave: rows of
@@ -235,80 +273,85 @@ __device__ __forceinline__ bool tidy_v(unsigned char* vt, int first, int rows, u
 // The infinities and NaN of a V tile, before tidy_v cleans them away, added to the queries that take their
 // keys: what a positive probability times an infinity or a NaN gives is that infinity or NaN.
 template <int D>
-__device__ __forceinline__ void add_nonfinite(Rows<D>& w, const unsigned char* vt, int keys, uint64_t allowed) {
-    int h = (int(threadIdx.x) >> 5) & 1;
-    asm volatile("" : "+v"(h));
+__device__ __forceinline__ void add_nonfinite(Rows<D>& w, const unsigned char* vt, int keys, const uint64_t (&allowed)[2]) {
+    int q = (int(threadIdx.x) >> 4) & 3;
+    asm volatile("" : "+v"(q));
     for (int j = 0; j < keys; ++j) {
-        const bool mine = (allowed >> j) & 1;
-        if (!__any(mine)) continue;
+        const bool mine[2] = {bool((allowed[0] >> j) & 1), bool((allowed[1] >> j) & 1)};
+        if (!__any(mine[0] || mine[1])) continue;
 #pragma unroll
-        for (int b = 0; b < D / 32; ++b)
+        for (int b = 0; b < D / 16; ++b) {  // columns 16 b + 4 q ..
+            const u32x2_t v = *reinterpret_cast<const u32x2_t*>(
+                vt + j * (2 * D) + (((2 * b + (q >> 1)) ^ v_swz<D>(j)) << 4) + 8 * (q & 1));
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const u32x2_t v = *reinterpret_cast<const u32x2_t*>(vt + j * (2 * D) + (((4 * b + e) ^ v_swz<D>(j)) << 4) + 8 * h);
+            for (int i = 0; i < 4; ++i) {
+                const uint32_t bits = i & 1 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16;
+                const bool odd = (bits & 0x7F800000u) == 0x7F800000u;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint32_t bits = i & 1 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16;
-                    if (mine && (bits & 0x7F800000u) == 0x7F800000u) w.o[b][4 * e + i] += __uint_as_float(bits);
-                }
+                for (int qb = 0; qb < 2; ++qb)
+                    if (mine[qb] && odd) w.o[b][qb][i] += __uint_as_float(bits);
             }
-    }
-}
-
-// The rows' Q operands (rows past the last read as zeros).
-template <int D>
-__device__ __forceinline__ void load_q(Rows<D>& w, const AttnArgs& a, int b, int hk, int row) {
-    const int h = (int(threadIdx.x) >> 5) & 1;
-    const bool in = row < a.rows;
-    const int t = in ? row / a.group : 0, g = in ? row - t * a.group : 0;
-    const uint16_t* src = a.q + int64_t(b) * a.q_batch + int64_t(t) * a.q_token + int64_t(hk * a.group + g) * a.q_head;
-#pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-        u32x4_t v = {0, 0, 0, 0};
-        if (in) v = *reinterpret_cast<const u32x4_t*>(src + 16 * kk + 8 * h);
-        w.q[kk] = __builtin_bit_cast(bf16x8_t, v);
-    }
-}
-
-// O of one row (its lane pair) to memory, scaled by f: 16 bytes per lane and 32 columns after an exchange
-// between the lane halves (each half holds 4 of every 8 consecutive columns).
-template <int D>
-__device__ __forceinline__ void store_o(const Rows<D>& w, const AttnArgs& a, int b, int hk, int row, float f) {
-    const int h = (int(threadIdx.x) >> 5) & 1;
-    const bool in = row < a.rows;
-    const int t = in ? row / a.group : 0, g = in ? row - t * a.group : 0;
-    uint16_t* dst = a.o + int64_t(b) * a.o_batch + int64_t(t) * a.o_token + int64_t(hk * a.group + g) * a.o_head;
-    auto pair = [&](float x, float y) {
-        return uint32_t(float_to_bf16_bits(x * f)) | (uint32_t(float_to_bf16_bits(y * f)) << 16);
-    };
-#pragma unroll
-    for (int d = 0; d < D / 32; ++d)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            // columns 32 d + 16 e + (0..7 | 8..15), four of each eight per half
-            const uint32_t x0 = pair(w.o[d][8 * e], w.o[d][8 * e + 1]), x1 = pair(w.o[d][8 * e + 2], w.o[d][8 * e + 3]);
-            const uint32_t y0 = pair(w.o[d][8 * e + 4], w.o[d][8 * e + 5]), y1 = pair(w.o[d][8 * e + 6], w.o[d][8 * e + 7]);
-            const auto s0 = __builtin_amdgcn_permlane32_swap(x0, y0, false, false);
-            const auto s1 = __builtin_amdgcn_permlane32_swap(x1, y1, false, false);
-            if (in) *reinterpret_cast<u32x4_t*>(dst + 32 * d + 16 * e + 8 * h) = u32x4_t{s0[0], s1[0], s0[1], s1[1]};
         }
+    }
 }
 
-// Partial results of one row for the join: O unnormalised, then (c m, l).
+// The Q operands of rows row0 + 16 qb + l16 (rows past the last read as zeros).
 template <int D>
-__device__ __forceinline__ void store_part(const Rows<D>& w, const AttnArgs& a, int64_t part_row, bool in, float l) {
-    const int h = (int(threadIdx.x) >> 5) & 1;
-    if (!in) return;
-    float* dst = a.part + part_row * D;
+__device__ __forceinline__ void load_q(Rows<D>& w, const AttnArgs& a, int b, int hk, int row0) {
+    const int lane = int(threadIdx.x) & 63, q = lane >> 4;
 #pragma unroll
-    for (int d = 0; d < D / 32; ++d)
+    for (int qb = 0; qb < 2; ++qb) {
+        const int row = row0 + 16 * qb + (lane & 15);
+        const bool in = row < a.rows;
+        const int t = in ? row / a.group : 0, g = in ? row - t * a.group : 0;
+        const uint16_t* src = a.q + int64_t(b) * a.q_batch + int64_t(t) * a.q_token + int64_t(hk * a.group + g) * a.q_head;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            *reinterpret_cast<f32x4_t*>(dst + 32 * d + 8 * e + 4 * h) =
-                f32x4_t{w.o[d][4 * e], w.o[d][4 * e + 1], w.o[d][4 * e + 2], w.o[d][4 * e + 3]};
-    if (h == 0) {
-        a.part_ml[2 * part_row] = w.m == kNegInf ? kNegInf : w.m * a.scale_log2;
-        a.part_ml[2 * part_row + 1] = l;
+        for (int ks = 0; ks < D / 32; ++ks) {
+            u32x4_t v = {0, 0, 0, 0};
+            if (in) v = *reinterpret_cast<const u32x4_t*>(src + 8 * k_chunk(ks, q));
+            w.q[ks][qb] = __builtin_bit_cast(bf16x8_t, v);
+        }
+    }
+}
+
+// O of the rows to memory, divided by l: 16 bytes per lane and pair of column blocks after an exchange between
+// neighbouring lane quarters (each holds 4 of every 16 columns).  A row without keys has l = 0: zeros.
+template <int D>
+__device__ __forceinline__ void store_o(const Rows<D>& w, const AttnArgs& a, int b, int hk, int row0) {
+    const int lane = int(threadIdx.x) & 63, q = lane >> 4;
+#pragma unroll
+    for (int qb = 0; qb < 2; ++qb) {
+        const int row = row0 + 16 * qb + (lane & 15);
+        const bool in = row < a.rows;
+        const int t = in ? row / a.group : 0, g = in ? row - t * a.group : 0;
+        uint16_t* dst = a.o + int64_t(b) * a.o_batch + int64_t(t) * a.o_token + int64_t(hk * a.group + g) * a.o_head;
+        const float l = w.l[qb][0], f = l == 0.f ? 0.f : 1.f / l;
+        auto pair = [&](float x, float y) { return pack_bf16(x * f, y * f); };
+#pragma unroll
+        for (int d = 0; d < D / 16; d += 2) {
+            const f32x4_t x = w.o[d][qb], y = w.o[d + 1][qb];
+            const auto s0 = __builtin_amdgcn_permlane16_swap(pair(x[0], x[1]), pair(y[0], y[1]), false, false);
+            const auto s1 = __builtin_amdgcn_permlane16_swap(pair(x[2], x[3]), pair(y[2], y[3]), false, false);
+            if (in) *reinterpret_cast<u32x4_t*>(dst + 16 * (d + (q & 1)) + 8 * (q >> 1)) = u32x4_t{s0[0], s1[0], s0[1], s1[1]};
+        }
+    }
+}
+
+// Partial results of the rows for the join: O unnormalised, then (c m, l).
+template <int D>
+__device__ __forceinline__ void store_part(const Rows<D>& w, const AttnArgs& a, int64_t base, int row0) {
+    const int lane = int(threadIdx.x) & 63, q = lane >> 4;
+#pragma unroll
+    for (int qb = 0; qb < 2; ++qb) {
+        const int row = row0 + 16 * qb + (lane & 15);
+        if (row >= a.rows) continue;
+        float* dst = a.part + (base + row) * D;
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) *reinterpret_cast<f32x4_t*>(dst + 16 * d + 4 * q) = w.o[d][qb];
+        if (q == 0) {
+            a.part_ml[2 * (base + row)] = w.mc[qb];
+            a.part_ml[2 * (base + row) + 1] = w.l[qb][0];
+        }
     }
 }
 
@@ -365,12 +408,11 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
     const int hk = id % a.kv_heads, b = id / a.kv_heads;
 
     const int n = in_sgpr(live_keys(a, b));
-    const int row = rt * 128 + wave * 32 + (lane & 31);
+    const int row0 = rt * 128 + wave * 32;  // the wave's rows
     const int64_t start = a.causal ? (a.start != nullptr ? a.start[b] : 0) : 0;
-    // the last key of the workgroup's and of the lane's rows
+    // the last key of the workgroup's rows
     const int last_row = rt * 128 + 127 < a.rows ? rt * 128 + 127 : a.rows - 1;
     const int64_t last = a.causal ? start + last_row / a.group : int64_t(n) - 1;
-    const int64_t mine = a.causal ? start + (row < a.rows ? row : a.rows - 1) / a.group : int64_t(1) << 40;
     // the first key that a row of the workgroup leaves out by the causal rule (all rows take those before)
     const int64_t first64 = a.causal ? start + (rt * 128) / a.group + 1 : n;
     const int64_t end64 = last + 1 < n ? last + 1 : n;
@@ -382,7 +424,14 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
 
     Rows<D> w;
     rows_init(w);
-    load_q(w, a, b, hk, row);
+    load_q(w, a, b, hk, row0);
+    // the last key of the lane's rows
+    int64_t mine[2];
+#pragma unroll
+    for (int qb = 0; qb < 2; ++qb) {
+        const int row = row0 + 16 * qb + (lane & 15);
+        mine[qb] = a.causal ? start + (row < a.rows ? row : a.rows - 1) / a.group : int64_t(1) << 40;
+    }
     const Offsets<D> f = offsets<D>();
 
     // the next tile to copy, and its key and value rows
@@ -450,26 +499,28 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
         issue_v(t + 1, vn);
         ++t;
         if (live == 0) return;  // the same in every wave
-        uint64_t allowed = ~0ull;
+        uint64_t allowed[2] = {~0ull, ~0ull};
         bool odd = false;
         if (partial) {
-            allowed = live & up_to(mine - 64 * int64_t(t - 1));
+#pragma unroll
+            for (int qb = 0; qb < 2; ++qb) allowed[qb] = live & up_to(mine[qb] - 64 * int64_t(t - 1));
             if (tidy_v<D, false>(vc, wave * 16, 16, live)) odd_tile = t;
             lds_writes_barrier();
             odd = odd_tile == t;
         }
-        f32x16_t s[2];
-        scores<D, 2>(w, f, kc, s);
-        if (partial) mask_scores<2>(s, allowed);
-        grow(w, row_max<2>(s), c);
-        probabilities<D, 2>(w, s, c);
+        Scores s;
+        Probs p;
+        scores<D>(w, f, kc, s);
+        if (partial) mask_scores(s, allowed);
+        grow(w, s, c);
+        probabilities<D>(w, s, p, c);
         if (odd) {
             add_nonfinite<D>(w, vc, 64, allowed);
             lds_writes_barrier();
             tidy_v<D, true>(vc, wave * 16, 16, live);
             lds_writes_barrier();
         }
-        weighted<D, 2>(w, f, vc, s);
+        weighted<D>(w, f, vc, p);
     };
 
     issue_k(t0, kbuf0);
@@ -479,27 +530,29 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
             // a run of whole tiles, two per turn; the scores are one tile ahead of the values
             arrive();
             issue_k(t + 1, kbuf1);
-            f32x16_t s0[2], s1[2];
-            scores<D, 2>(w, f, kbuf0, s0);
-            grow(w, row_max<2>(s0), c);
+            Scores s0, s1;
+            scores<D>(w, f, kbuf0, s0);
+            grow(w, s0, c);
             do {
                 arrive();
                 issue_k(t + 2, kbuf0);
                 issue_v(t + 1, vbuf1);
-                grow(w, fused_step<D>(w, f, kbuf1, vbuf0, s0, s1, c), c);
+                fused_step<D>(w, f, kbuf1, vbuf0, s0, s1, c);
                 arrive();
                 issue_k(t + 3, kbuf1);
                 issue_v(t + 2, vbuf0);
                 m0 = m2;
                 m1 = fetch(t + 3);
                 m2 = fetch(t + 4);
-                grow(w, fused_step<D>(w, f, kbuf0, vbuf1, s1, s0, c), c);
+                fused_step<D>(w, f, kbuf0, vbuf1, s1, s0, c);
                 t += 2;
             } while (whole(t + 1, m1) && whole(t + 2, m2));
             arrive();
             issue_v(t + 1, vbuf1);
-            probabilities<D, 2>(w, s0, c);
-            weighted<D, 2>(w, f, vbuf0, s0);
+            Probs p;
+            grow(w, s0, c);
+            probabilities<D>(w, s0, p, c);
+            weighted<D>(w, f, vbuf0, p);
             m0 = m1;
             m1 = m2;
             m2 = fetch(t + 3);
@@ -509,12 +562,10 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
         }
         if (t < t1) any_step(kbuf1, vbuf1, kbuf0, vbuf0);
     }
-    const float l = w.l + other_half(w.l);
     if (a.splits == 1) {
-        store_o(w, a, b, hk, row, l > 0.f || l != l ? 1.f / l : 0.f);
+        store_o(w, a, b, hk, row0);
     } else {
-        const int64_t base = ((int64_t(b) * a.kv_heads + hk) * a.splits + split) * a.rows;
-        store_part(w, a, base + row, row < a.rows, l);
+        store_part(w, a, ((int64_t(b) * a.kv_heads + hk) * a.splits + split) * a.rows, row0);
     }
 }
 
@@ -540,7 +591,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
 #pragma unroll
         for (int e = 0; e < D / 64; ++e) o[e] = __builtin_fmaf(f, a.part[r * D + (D / 64) * lane + e], o[e]);
     }
-    const float f = l > 0.f || l != l ? 1.f / l : 0.f;
+    const float f = l == 0.f ? 0.f : 1.f / l;
     const int b = int(bh / a.kv_heads), hk = int(bh % a.kv_heads);
     const int t = row / a.group, g = row - t * a.group;
     uint16_t* dst = a.o + int64_t(b) * a.o_batch + int64_t(t) * a.o_token + int64_t(hk * a.group + g) * a.o_head;
