@@ -359,8 +359,16 @@ __device__ __forceinline__ void store_part(const Rows<D>& w, const AttnArgs& a, 
 // the loop, and a scalar load shares its wait with every LDS read in flight.
 template <class T>
 __device__ __forceinline__ T in_sgpr(T v) {
-    asm volatile("" : "+s"(v));
-    return v;
+    if constexpr (sizeof(T) == 8) {
+        const uint64_t x = __builtin_bit_cast(uint64_t, v);
+        uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(x)), hi = __builtin_amdgcn_readfirstlane(uint32_t(x >> 32));
+        asm volatile("" : "+s"(lo), "+s"(hi));
+        return __builtin_bit_cast(T, (uint64_t(hi) << 32) | lo);
+    } else {
+        uint32_t x = __builtin_amdgcn_readfirstlane(__builtin_bit_cast(uint32_t, v));
+        asm volatile("" : "+s"(x));
+        return __builtin_bit_cast(T, x);
+    }
 }
 
 // Workgroup barrier after LDS reads and writes that leaves copies in flight (__syncthreads() waits for them).
