@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import List, Optional, Sequence, Tuple
 
 from ._lib import LowbitError, lib, library_path  # noqa: F401
@@ -380,6 +381,99 @@ def gemm_batched(problems: Sequence[Tuple["object", "object", "object", "object"
         _check(st, "lowbit_gemm_batched_ex")
 
 
+# ---- operators around the packed linears ----
+# Their calls take a few microseconds on the device at small sizes, so the checks below look at the ordinary case first and
+# the descriptors are packed bytes: a call costs the host about as much as a torch operation.
+
+_get = None  # (torch.Tensor, current raw stream of a device index, current device index), once torch is there
+
+
+def _env():
+    global _get
+    if _get is None:
+        torch = _torch()
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda d: torch.cuda.current_stream(d).cuda_stream)
+        torch.cuda.init()
+        _get = (torch.Tensor, raw, getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device))
+    return _get
+
+
+def _heads(t, name: str, ndim: int) -> None:
+    """A bf16 device tensor [..., heads, head_dim] whose last dimension is contiguous (any other strides)."""
+    torch = _torch()
+    if isinstance(t, torch.Tensor) and t.dtype is torch.bfloat16 and t.dim() == ndim and t.is_cuda and (
+            t.stride(-1) == 1 or t.shape[-1] == 1):
+        return
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must be {ndim}-D, got shape {tuple(t.shape)}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be on a GPU")
+    raise ValueError(f"{name} must be contiguous along its last dimension")
+
+
+def _plain(t, dtype, name: str, ndim: int, like) -> int:
+    """The address of a contiguous tensor of that type on the device of `like`."""
+    if not (t.__class__ is like.__class__ and t.dtype is dtype and t.dim() == ndim and t.is_contiguous()
+            and t.get_device() == like.get_device() and t.is_cuda):
+        _require(t, dtype, name, ndim)
+        _same_device(like, ((name, t),))
+    return t.data_ptr()
+
+
+def _same_device(first, named) -> None:
+    """Every tensor of `named` on the device of `first` (the kernel runs there)."""
+    dev = first.get_device()
+    for name, t in named:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{name} must be on {first.device}, got {t.device}")
+
+
+def _call(function: str, like, *args) -> None:
+    """Calls the library with the current stream of the tensors' device, that device being current (a launch goes
+    to the current device)."""
+    _, raw_stream, current = _env()
+    dev = like.get_device()
+    if dev == current():
+        st = getattr(lib(), function)(*args, raw_stream(dev))
+    else:
+        with _torch().cuda.device(dev):
+            st = getattr(lib(), function)(*args, raw_stream(dev))
+    if st:
+        _check(st, function)
+
+
+def _strides(t):
+    """Strides of every dimension but the last, 0 for dimensions of one element (whose stride says nothing)."""
+    n, s = t.shape, t.stride()
+    if len(n) == 3:
+        return (s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0)
+    return (s[0] if n[0] > 1 else 0, s[1] if n[1] > 1 else 0, s[2] if n[2] > 1 else 0)
+
+
+def _workspace(workspace, like):
+    """(address, bytes) of an optional workspace."""
+    if workspace is None:
+        return 0, 0
+    if not workspace.is_cuda or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous device tensor")
+    _same_device(like, (("workspace", workspace),))
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _output(out, shape, like):
+    """`out`, checked, or a new bf16 tensor of that shape."""
+    torch = _torch()
+    if out is None:
+        return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+    if out.shape != shape:
+        raise ValueError(f"out must be {tuple(shape)}, got {tuple(out.shape)}")
+    return out
+
+
 def lora_workspace_size(M: int, rank: int) -> int:
     """Bytes of workspace that gemm_lora needs for M rows (0 for invalid arguments)."""
     return int(lib().lowbit_lora_workspace_size(M, rank))
@@ -392,73 +486,37 @@ def gemm_lora(x, words, scales, g: int, bits: int, lora_a, lora_b, alpha, rows, 
 
     `workspace`: a device tensor of at least lora_workspace_size(M, rank) bytes, allocated for the call if None."""
     torch = _torch()
-    _require(x, torch.bfloat16, "x")
-    _require(words, torch.int32, "words")
-    _require(scales, torch.float16, "scales")
-    _require(lora_a, torch.bfloat16, "lora_a", ndim=3)
-    _require(lora_b, torch.bfloat16, "lora_b", ndim=3)
-    _require(alpha, torch.float32, "alpha", ndim=1)
-    _require(rows, torch.int32, "rows", ndim=1)
+    bf16 = torch.bfloat16
+    _require(x, bf16, "x")
     M, K = x.shape
-    N = words.shape[0]
-    E, rank = lora_a.shape[0], lora_a.shape[1]
-    if words.shape[1] != words_per_row(K, bits):
+    px = x.data_ptr()
+    pw = _plain(words, torch.int32, "words", 2, x)
+    ps = _plain(scales, torch.float16, "scales", 2, x)
+    pa = _plain(lora_a, bf16, "lora_a", 3, x)
+    pb = _plain(lora_b, bf16, "lora_b", 3, x)
+    pl = _plain(alpha, torch.float32, "alpha", 1, x)
+    pr = _plain(rows, torch.int32, "rows", 1, x)
+    N, per_row = words.shape
+    E, rank, ka = lora_a.shape
+    if per_row != words_per_row(K, bits):
         raise ValueError(f"words must be [N, K*bits/32] = [{N}, {words_per_row(K, bits)}], got {tuple(words.shape)}")
-    if K % g or tuple(scales.shape) != (N, K // g):
+    if K % g or scales.shape != (N, K // g):
         raise ValueError(f"scales must be [N, K/g] = [{N}, {K // g if g else 0}], got {tuple(scales.shape)}")
-    if lora_a.shape[2] != K or tuple(lora_b.shape) != (E, N, rank):
+    if ka != K or lora_b.shape != (E, N, rank):
         raise ValueError(f"lora_a must be [adapters, rank, {K}] and lora_b [adapters, {N}, rank], got "
                          f"{tuple(lora_a.shape)} and {tuple(lora_b.shape)}")
     if alpha.shape[0] != E or rows.shape[0] != M:
         raise ValueError(f"alpha must be [{E}] and rows [{M}]")
-    if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
-    else:
-        _require(out, torch.bfloat16, "out")
-        if tuple(out.shape) != (M, N):
-            raise ValueError("out must be [M, N]")
+    out = _output(out, (M, N), x)
+    po = _plain(out, bf16, "out", 2, x)
     if workspace is None:
         workspace = torch.empty(lora_workspace_size(M, rank), dtype=torch.uint8, device=x.device)
-    _same_device(x, (("words", words), ("scales", scales), ("lora_a", lora_a), ("lora_b", lora_b), ("alpha", alpha),
-                     ("rows", rows), ("out", out)))
     ws, nbytes = _workspace(workspace, x)
-    with _on(x.device):
-        st = lib().lowbit_gemm_lora(x.data_ptr(), words.data_ptr(), scales.data_ptr(), out.data_ptr(), M, N, K, g, bits,
-                                    lora_a.data_ptr(), lora_b.data_ptr(), alpha.data_ptr(), rows.data_ptr(), E, rank, ws,
-                                    nbytes, _stream_ptr(x.device))
-        _check(st, "lowbit_gemm_lora")
+    _call("lowbit_gemm_lora", x, px, pw, ps, po, M, N, K, g, bits, pa, pb, pl, pr, E, rank, ws, nbytes)
     return out
 
 
-class QkProblem(ctypes.Structure):
-    """lowbit_qk_problem of include/lowbit.h."""
-    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "q_out", "k_out", "q_weight", "k_weight", "positions", "freqs")]
-                + [(n, ctypes.c_int64) for n in ("tokens", "q_token", "q_head", "k_token", "k_head", "q_out_token",
-                                                 "q_out_head", "k_out_token", "k_out_head")]
-                + [(n, ctypes.c_int32) for n in ("q_heads", "k_heads", "head_dim", "axes")]
-                + [("axis_dims", ctypes.c_int32 * 4), ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float)])
-
-
-def _heads(t, name: str, ndim: int):
-    """A bf16 device tensor [..., heads, head_dim] whose last dimension is contiguous (any other strides)."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
-        raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-    if t.dim() != ndim:
-        raise ValueError(f"{name} must be {ndim}-D, got shape {tuple(t.shape)}")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be on a GPU")
-    if t.stride(-1) != 1 and t.shape[-1] != 1:
-        raise ValueError(f"{name} must be contiguous along its last dimension")
-
-
-def _same_device(first, named) -> None:
-    """Every tensor of `named` on the device of `first` (the kernel runs there)."""
-    for name, t in named:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} must be on {first.device}, got {t.device}")
+_QK_PROBLEM = struct.Struct("@8P9q9if0q")  # lowbit_qk_problem of include/lowbit.h
 
 
 def rope_freqs(axis_dims: Sequence[int], theta: float = 10000.0, device="cuda"):
@@ -482,123 +540,83 @@ def qk_norm_rope(q, k, positions, freqs, axis_dims: Sequence[int], q_weight=None
     _heads(q, "q", 3)
     _heads(k, "k", 3)
     T, Hq, D = q.shape
-    Hk = k.shape[1]
-    if k.shape[0] != T or k.shape[2] != D:
+    Tk, Hk, Dk = k.shape
+    if Tk != T or Dk != D:
         raise ValueError(f"k must be [{T}, heads, {D}], got {tuple(k.shape)}")
     axes = len(axis_dims)
     if axes > 4:
         raise ValueError("at most 4 axes")
+    pp = pf = 0
     if axes:
-        _require(positions, torch.int32, "positions")
-        _require(freqs, torch.float32, "freqs", ndim=1)
-        if tuple(positions.shape) != (T, axes):
+        pp = _plain(positions, torch.int32, "positions", 2, q)
+        pf = _plain(freqs, torch.float32, "freqs", 1, q)
+        if positions.shape != (T, axes):
             raise ValueError(f"positions must be [{T}, {axes}], got {tuple(positions.shape)}")
         if 2 * freqs.shape[0] != sum(axis_dims):
             raise ValueError(f"freqs must hold sum(axis_dims) / 2 = {sum(axis_dims) // 2} values, got {freqs.shape[0]}")
-    else:
-        positions = freqs = None
-    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
-            _require(w, torch.bfloat16, name, ndim=1)
-            if w.shape[0] != D:
-                raise ValueError(f"{name} must be [{D}]")
-    if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
-    if k_out is None:
-        k_out = torch.empty((T, Hk, D), dtype=torch.bfloat16, device=q.device)
-    for name, o, like in (("q_out", q_out, q), ("k_out", k_out, k)):
-        _heads(o, name, 3)
-        if o.shape != like.shape:
-            raise ValueError(f"{name} must be {tuple(like.shape)}")
-    _same_device(q, (("k", k), ("positions", positions), ("freqs", freqs), ("q_weight", q_weight), ("k_weight", k_weight),
-                     ("q_out", q_out), ("k_out", k_out)))
-
-    def ptr(t):
-        return None if t is None or t.numel() == 0 else t.data_ptr()
-
-    dims = (ctypes.c_int32 * 4)(*axis_dims)
-    p = QkProblem(ptr(q), ptr(k), ptr(q_out), ptr(k_out), ptr(q_weight), ptr(k_weight), ptr(positions), ptr(freqs), T,
-                  *_strides(q), *_strides(k), *_strides(q_out), *_strides(k_out), Hq, Hk, D, axes, dims,
-                  1 if interleaved else 0, eps)
-    with _on(q.device):
-        _check(lib().lowbit_qk_norm_rope(ctypes.byref(p), _stream_ptr(q.device)), "lowbit_qk_norm_rope")
+    pwq = pwk = 0
+    if q_weight is not None:
+        pwq = _plain(q_weight, torch.bfloat16, "q_weight", 1, q)
+        if q_weight.shape[0] != D:
+            raise ValueError(f"q_weight must be [{D}]")
+    if k_weight is not None:
+        pwk = _plain(k_weight, torch.bfloat16, "k_weight", 1, q)
+        if k_weight.shape[0] != D:
+            raise ValueError(f"k_weight must be [{D}]")
+    q_out, k_out = _output(q_out, q.shape, q), _output(k_out, k.shape, q)
+    _heads(q_out, "q_out", 3)
+    _heads(k_out, "k_out", 3)
+    _same_device(q, (("k", k), ("q_out", q_out), ("k_out", k_out)))
+    dims = (*axis_dims, 0, 0, 0, 0)
+    p = _QK_PROBLEM.pack(q.data_ptr(), k.data_ptr(), q_out.data_ptr(), k_out.data_ptr(), pwq, pwk, pp, pf, T,
+                         *_strides(q), *_strides(k), *_strides(q_out), *_strides(k_out), Hq, Hk, D, axes,
+                         dims[0], dims[1], dims[2], dims[3], 1 if interleaved else 0, eps)
+    _call("lowbit_qk_norm_rope", q, p)
     return q_out, k_out
 
 
-def _strides(t):
-    """Strides of every dimension but the last, 0 for dimensions of one element (whose stride says nothing)."""
-    return [s if n > 1 else 0 for s, n in zip(t.stride()[:-1], t.shape[:-1])]
-
-
-class _on:
-    """The tensors' device made current for the call, where it is not already (a launch goes to the current device)."""
-
-    def __init__(self, device):
-        self.device = device
-        self.guard = None
-
-    def __enter__(self):
-        torch = _torch()
-        if self.device.index is not None and self.device.index != torch.cuda.current_device():
-            self.guard = torch.cuda.device(self.device)
-            self.guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self.guard is not None:
-            self.guard.__exit__(*exc)
-
-
-class AttentionProblem(ctypes.Structure):
-    """lowbit_attention_problem of include/lowbit.h."""
-    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "o", "key_mask", "key_lens", "q_start")]
-                + [(n, ctypes.c_int64) for n in ("batch", "q_len", "kv_len", "q_batch", "q_token", "q_head", "k_batch",
-                                                 "k_token", "k_head", "v_batch", "v_token", "v_head", "o_batch", "o_token",
-                                                 "o_head", "mask_batch")]
-                + [(n, ctypes.c_int32) for n in ("q_heads", "kv_heads", "head_dim", "causal")] + [("scale", ctypes.c_float)])
+_ATTENTION_PROBLEM = struct.Struct("@7P16q4if0q")  # lowbit_attention_problem of include/lowbit.h
 
 
 def _attention_problem(q, k, v, key_mask, key_lens, causal, q_start, scale, out):
     torch = _torch()
-    for name, t in (("q", q), ("k", k), ("v", v)):
-        _heads(t, name, 4)
+    _heads(q, "q", 4)
+    _heads(k, "k", 4)
+    _heads(v, "v", 4)
     B, Lq, Hq, D = q.shape
-    Lk, Hk = k.shape[1], k.shape[2]
-    if k.shape[0] != B or k.shape[3] != D or v.shape != k.shape:
+    _, Lk, Hk, _ = k.shape
+    if k.shape != (B, Lk, Hk, D) or v.shape != k.shape:
         raise ValueError(f"k and v must be [{B}, keys, kv_heads, {D}], got {tuple(k.shape)} and {tuple(v.shape)}")
+    pm = pn = pq = mask_batch = 0
     if key_mask is not None:
         if not isinstance(key_mask, torch.Tensor) or key_mask.dtype not in (torch.bool, torch.uint8):
             raise TypeError("key_mask must be a bool or uint8 torch.Tensor")
-        if tuple(key_mask.shape) != (B, Lk) or (Lk > 1 and key_mask.stride(1) != 1):
+        if key_mask.shape != (B, Lk) or (Lk > 1 and key_mask.stride(1) != 1):
             raise ValueError(f"key_mask must be [{B}, {Lk}], contiguous along the keys")
         if not key_mask.is_cuda:
             raise ValueError("key_mask must be on a GPU")
-    for name, t in (("key_lens", key_lens), ("q_start", q_start)):
-        if t is not None:
-            _require(t, torch.int32, name, ndim=1)
-            if t.shape[0] != B:
-                raise ValueError(f"{name} must be [{B}]")
-    if q_start is not None and not causal:
-        q_start = None  # positions matter to the causal rule only
+        pm, mask_batch = key_mask.data_ptr(), key_mask.stride(0) if B > 1 else 0
+    if key_lens is not None:
+        pn = _plain(key_lens, torch.int32, "key_lens", 1, q)
+        if key_lens.shape[0] != B:
+            raise ValueError(f"key_lens must be [{B}]")
+    if q_start is not None and causal:  # positions matter to the causal rule only
+        pq = _plain(q_start, torch.int32, "q_start", 1, q)
+        if q_start.shape[0] != B:
+            raise ValueError(f"q_start must be [{B}]")
+    po, so = 0, (Lq * Hq * D, Hq * D, D)
     if out is not None:
         _heads(out, "out", 4)
-        if out.shape != q.shape:
-            raise ValueError(f"out must be {tuple(q.shape)}")
-    _same_device(q, (("k", k), ("v", v), ("key_mask", key_mask), ("key_lens", key_lens), ("q_start", q_start), ("out", out)))
-
-    def ptr(t):
-        return None if t is None or t.numel() == 0 else t.data_ptr()
-
-    return AttentionProblem(
-        ptr(q), ptr(k), ptr(v), ptr(out), ptr(key_mask), ptr(key_lens), ptr(q_start), B, Lq, Lk,
-        *_strides(q), *_strides(k), *_strides(v), *(_strides(out) if out is not None else (Lq * Hq * D, Hq * D, D)),
-        _strides(key_mask)[0] if key_mask is not None else 0, Hq, Hk, D, 1 if causal else 0,
-        scale if scale is not None else (D ** -0.5 if D else 1.0))
+        po, so = out.data_ptr(), _strides(out)
+    _same_device(q, (("k", k), ("v", v), ("key_mask", key_mask), ("out", out)))
+    return _ATTENTION_PROBLEM.pack(q.data_ptr(), k.data_ptr(), v.data_ptr(), po, pm, pn, pq, B, Lq, Lk, *_strides(q),
+                                   *_strides(k), *_strides(v), *so, mask_batch, Hq, Hk, D, 1 if causal else 0,
+                                   scale if scale is not None else D ** -0.5 if D else 1.0)
 
 
 def attention_workspace_size(q, k, v) -> int:
     """Bytes of workspace attention(q, k, v, ...) can use (0: none)."""
-    p = _attention_problem(q, k, v, None, None, False, None, None, None)
-    return int(lib().lowbit_attention_workspace_size(ctypes.byref(p)))
+    return int(lib().lowbit_attention_workspace_size(_attention_problem(q, k, v, None, None, False, None, None, None)))
 
 
 def attention(q, k, v, key_mask=None, key_lens=None, causal: bool = False, q_start=None, scale=None, out=None,
@@ -611,24 +629,13 @@ def attention(q, k, v, key_mask=None, key_lens=None, causal: bool = False, q_sta
     `workspace`: an optional device tensor of at least attention_workspace_size(q, k, v) bytes, with
     which few rows over many keys run split along the keys; do not share it between calls that run
     concurrently."""
-    torch = _torch()
     if out is None:
         _heads(q, "q", 4)
-        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device)
+    out = _output(out, q.shape, q)
     p = _attention_problem(q, k, v, key_mask, key_lens, causal, q_start, scale, out)
     ws, nbytes = _workspace(workspace, q)
-    with _on(q.device):
-        _check(lib().lowbit_attention(ctypes.byref(p), ws, nbytes, _stream_ptr(q.device)), "lowbit_attention")
+    _call("lowbit_attention", q, p, ws, nbytes)
     return out
-
-
-def _workspace(workspace, like):
-    if workspace is None:
-        return None, 0
-    if not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous device tensor")
-    _same_device(like, (("workspace", workspace),))
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def check_gemm_args(x_ptr: int, w_ptr: int, s_ptr: int, y_ptr: int, M: int, N: int, K: int, g: int,
