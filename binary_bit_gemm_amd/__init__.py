@@ -23,9 +23,15 @@ BINARY = 1
 MAX_BATCH = 64
 
 
+_TORCH = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _TORCH
+    if _TORCH is None:
+        import torch
+        _TORCH = torch
+    return _TORCH
 
 
 def _stream_ptr(device) -> int:
@@ -626,9 +632,9 @@ def attention(q, k, v, key_mask=None, key_lens=None, causal: bool = False, q_sta
     kv_heads.  Query t takes key j where key_mask[b, j] (bool), j < key_lens[b] and, if causal, j <= q_start[b] + t (None: 0);
     a query without keys gets zeros.  scale: 1 / sqrt(D) by default.
 
-    `workspace`: an optional device tensor of at least attention_workspace_size(q, k, v) bytes, with
-    which few rows over many keys run split along the keys; do not share it between calls that run
-    concurrently."""
+    `workspace`: an optional device tensor of at least attention_workspace_size(q, k, v) bytes, zero-filled before its
+    first use, with which few rows over many keys run split along the keys.  Reuse it between calls;
+    do not share it between calls that run concurrently."""
     if out is None:
         _heads(q, "q", 4)
     out = _output(out, q.shape, q)

@@ -60,24 +60,30 @@ __device__ __forceinline__ int v_swz(int r) {
     return D == 128 ? (r & 7) << 1 : ((r >> 1) & 3) << 1;
 }
 
-// One wave's state for 32 rows, two blocks of 16.
-template <int D>
+// One wave's state for NQ blocks of 16 rows.
+template <int D, int NQ>
 struct Rows {
-    bf16x8_t q[D / 32][2];  // B operand: lane (q, query): chunk k_chunk(ks, q)
-    f32x4_t o[D / 16][2];   // O^T: lane (q, query), columns 16 db + 4q ..
-    f32x4_t l[2];           // the softmax's sum (four times the same)
-    float mc[2];            // what the exponents subtract: c times the maximum then seen + kHeadroom; -inf: no key yet
+    bf16x8_t q[D / 32][NQ];  // B operand: lane (q, query): chunk k_chunk(ks, q)
+    f32x4_t o[D / 16][NQ];   // O^T: lane (q, query), columns 16 db + 4q ..
+    f32x4_t l[NQ];           // the softmax's sum (four times the same)
+    float mc[NQ];            // what the exponents subtract: c times the maximum then seen + kHeadroom; -inf: no key yet
 };
 
-// Scores, then probabilities of a tile's 64 keys: [16-key block][row block], keys 16 kb + 4q ..
-typedef f32x4_t Scores[4][2];
-// Probabilities as B operands: [32-key block][row block].
-typedef u32x4_t Probs[2][2];
+// Scores of a tile of KB blocks of 16 keys: [key block][row block], keys 16 kb + 4q ..
+template <int KB, int NQ>
+struct Scores {
+    f32x4_t s[KB][NQ];
+};
+// Their probabilities as B operands: [32-key block][row block].
+template <int KB, int NQ>
+struct Probs {
+    u32x4_t p[KB / 2][NQ];
+};
 
-template <int D>
-__device__ __forceinline__ void rows_init(Rows<D>& w) {
+template <int D, int NQ>
+__device__ __forceinline__ void rows_init(Rows<D, NQ>& w) {
 #pragma unroll
-    for (int qb = 0; qb < 2; ++qb) {
+    for (int qb = 0; qb < NQ; ++qb) {
 #pragma unroll
         for (int b = 0; b < D / 16; ++b) w.o[b][qb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         w.l[qb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -109,46 +115,48 @@ __device__ __forceinline__ Offsets<D> offsets() {
 }
 
 // Scores of the K tile at kt.
-template <int D>
-__device__ __forceinline__ void scores(const Rows<D>& w, const Offsets<D>& f, const unsigned char* kt, Scores& s) {
+template <int D, int NQ, int KB>
+__device__ __forceinline__ void scores(const Rows<D, NQ>& w, const Offsets<D>& f, const unsigned char* kt, Scores<KB, NQ>& x) {
 #pragma unroll
-    for (int kb = 0; kb < 4; ++kb) {
+    for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll
-        for (int qb = 0; qb < 2; ++qb) s[kb][qb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        for (int qb = 0; qb < NQ; ++qb) x.s[kb][qb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int ks = 0; ks < D / 32; ++ks) {
             const bf16x8_t k = *reinterpret_cast<const bf16x8_t*>(kt + f.k[ks] + kb * 16 * (2 * D));
 #pragma unroll
-            for (int qb = 0; qb < 2; ++qb) s[kb][qb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, w.q[ks][qb], s[kb][qb], 0, 0, 0);
+            for (int qb = 0; qb < NQ; ++qb)
+                x.s[kb][qb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(k, w.q[ks][qb], x.s[kb][qb], 0, 0, 0);
         }
     }
 }
 
 // Scores of keys that a lane's query does not take (bit of its `allowed` clear) to -inf.
-__device__ __forceinline__ void mask_scores(Scores& s, const uint64_t (&allowed)[2]) {
+template <int KB, int NQ>
+__device__ __forceinline__ void mask_scores(Scores<KB, NQ>& x, const uint64_t (&allowed)[NQ]) {
     asm volatile("");  // a branch, not a select in every tile
 #pragma unroll
-    for (int qb = 0; qb < 2; ++qb) {
+    for (int qb = 0; qb < NQ; ++qb) {
         const uint64_t mine = allowed[qb] >> ((threadIdx.x & 48) >> 2);
 #pragma unroll
-        for (int kb = 0; kb < 4; ++kb) {
+        for (int kb = 0; kb < KB; ++kb) {
             const uint32_t bits = uint32_t(mine >> (16 * kb));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) s[kb][qb][i] = (bits >> i) & 1u ? s[kb][qb][i] : kNegInf;
+            for (int i = 0; i < 4; ++i) x.s[kb][qb][i] = (bits >> i) & 1u ? x.s[kb][qb][i] : kNegInf;
         }
     }
 }
 
-// m follows the largest of the scores s where it has to, and l and O follow m.
-template <int D>
-__device__ __forceinline__ void grow(Rows<D>& w, const Scores& s, float c) {
+// m follows the largest of the scores where it has to, and l and O follow m.
+template <int D, int NQ, int KB>
+__device__ __forceinline__ void grow(Rows<D, NQ>& w, const Scores<KB, NQ>& x, float c) {
 #pragma unroll
-    for (int qb = 0; qb < 2; ++qb) {
+    for (int qb = 0; qb < NQ; ++qb) {
         float top = kNegInf;
 #pragma unroll
-        for (int kb = 0; kb < 4; ++kb)
+        for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top = fmaxf(top, s[kb][qb][i]);
+            for (int i = 0; i < 4; ++i) top = fmaxf(top, x.s[kb][qb][i]);
         top = fmaxf(top, __shfl_xor(top, 16));
         top = fmaxf(top, __shfl_xor(top, 32)) * c;
         // p below 2: the packed test's bound, with its rounding
@@ -167,22 +175,22 @@ __device__ __forceinline__ void grow(Rows<D>& w, const Scores& s, float c) {
     }
 }
 
-// The probabilities of s; returns an OR of them all.
-template <int D>
-__device__ __forceinline__ uint32_t probabilities(const Rows<D>& w, const Scores& s, Probs& p, float c) {
+// The probabilities of x; returns an OR of them all.
+template <int D, int NQ, int KB>
+__device__ __forceinline__ uint32_t probabilities(const Rows<D, NQ>& w, const Scores<KB, NQ>& x, Probs<KB, NQ>& p, float c) {
     uint32_t any = 0;
 #pragma unroll
-    for (int qb = 0; qb < 2; ++qb) {
+    for (int qb = 0; qb < NQ; ++qb) {
         const float mc = w.mc[qb] == kNegInf ? 0.f : w.mc[qb];  // without a key yet every score is -inf
 #pragma unroll
-        for (int kk = 0; kk < 2; ++kk)
+        for (int kk = 0; kk < KB / 2; ++kk)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                const f32x4_t& x = s[2 * kk + e / 2][qb];
-                const float lo = __builtin_amdgcn_exp2f(__builtin_fmaf(x[2 * (e % 2)], c, -mc));
-                const float hi = __builtin_amdgcn_exp2f(__builtin_fmaf(x[2 * (e % 2) + 1], c, -mc));
+                const f32x4_t& s = x.s[2 * kk + e / 2][qb];
+                const float lo = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * (e % 2)], c, -mc));
+                const float hi = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * (e % 2) + 1], c, -mc));
                 const uint32_t v = pack_bf16(lo, hi);
-                p[kk][qb][e] = v;
+                p.p[kk][qb][e] = v;
                 any |= v;
             }
     }
@@ -190,14 +198,14 @@ __device__ __forceinline__ uint32_t probabilities(const Rows<D>& w, const Scores
 }
 
 // O += P V for the V tile at vt, and l.
-template <int D>
-__device__ __forceinline__ void weighted(Rows<D>& w, const Offsets<D>& f, const unsigned char* vt, const Probs& p) {
+template <int D, int NQ, int KB>
+__device__ __forceinline__ void weighted(Rows<D, NQ>& w, const Offsets<D>& f, const unsigned char* vt, const Probs<KB, NQ>& p) {
     const bf16x8_t ones = __builtin_bit_cast(bf16x8_t, u32x4_t{0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u});
 #pragma unroll
-    for (int kk = 0; kk < 2; ++kk) {  // 32 keys each
+    for (int kk = 0; kk < KB / 2; ++kk) {  // 32 keys each
 #pragma unroll
-        for (int qb = 0; qb < 2; ++qb)
-            w.l[qb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, __builtin_bit_cast(bf16x8_t, p[kk][qb]), w.l[qb], 0, 0, 0);
+        for (int qb = 0; qb < NQ; ++qb)
+            w.l[qb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(ones, __builtin_bit_cast(bf16x8_t, p.p[kk][qb]), w.l[qb], 0, 0, 0);
 #pragma unroll
         for (int b = 0; b < D / 16; ++b) {
             s16x4_t v[2];
@@ -207,31 +215,34 @@ __device__ __forceinline__ void weighted(Rows<D>& w, const Offsets<D>& f, const 
                     (__attribute__((address_space(3))) s16x4_t*)(vt + f.v[b] + (32 * kk + 16 * part) * (2 * D)));
             const bf16x8_t a = __builtin_bit_cast(bf16x8_t, __builtin_shufflevector(v[0], v[1], 0, 1, 2, 3, 4, 5, 6, 7));
 #pragma unroll
-            for (int qb = 0; qb < 2; ++qb)
-                w.o[b][qb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, p[kk][qb]), w.o[b][qb], 0, 0, 0);
+            for (int qb = 0; qb < NQ; ++qb)
+                w.o[b][qb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, p.p[kk][qb]), w.o[b][qb], 0, 0, 0);
         }
     }
 }
 
-// Whether the wave's probabilities have to be computed again with a larger m.
-template <int D>
-__device__ __forceinline__ bool outgrown(const Rows<D>& w, uint32_t any) {
-    return __any((any & kTooLarge) != 0 || w.mc[0] == kNegInf || w.mc[1] == kNegInf);
+// The probabilities of x, to a maximum that has moved if one of them would reach 2.
+template <int D, int NQ, int KB>
+__device__ __forceinline__ void probabilities_checked(Rows<D, NQ>& w, const Scores<KB, NQ>& x, Probs<KB, NQ>& p, float c) {
+    const uint32_t any = probabilities(w, x, p, c);
+    bool move = (any & kTooLarge) != 0;
+#pragma unroll
+    for (int qb = 0; qb < NQ; ++qb) move = move || w.mc[qb] == kNegInf;
+    if (__any(move)) {
+        grow(w, x, c);
+        probabilities(w, x, p, c);
+    }
 }
 
-// One tile's values and the next tile's scores: the exponentials of s (scores of the tile whose values are
-// at vt) are taken while the matrix cores compute sn, the scores of the K tile at kt.
-template <int D>
-__device__ __forceinline__ void fused_step(Rows<D>& w, const Offsets<D>& f, const unsigned char* kt, const unsigned char* vt,
-                                           const Scores& s, Scores& sn, float c) {
-    Probs p;
-    scores<D>(w, f, kt, sn);
-    const uint32_t any = probabilities<D>(w, s, p, c);
-    if (outgrown(w, any)) {
-        grow(w, s, c);
-        probabilities<D>(w, s, p, c);
-    }
-    weighted<D>(w, f, vt, p);
+// One tile's values and the next tile's scores: the exponentials of x (scores of the tile whose values are
+// at vt) are taken while the matrix cores compute xn, the scores of the K tile at kt.
+template <int D, int NQ, int KB>
+__device__ __forceinline__ void fused_step(Rows<D, NQ>& w, const Offsets<D>& f, const unsigned char* kt, const unsigned char* vt,
+                                           const Scores<KB, NQ>& x, Scores<KB, NQ>& xn, float c) {
+    Probs<KB, NQ> p;
+    scores(w, f, kt, xn);
+    probabilities_checked(w, x, p, c);
+    weighted(w, f, vt, p);
 }
 
 __device__ __forceinline__ bool pair_finite(uint32_t v) { return (v & 0x7F80u) != 0x7F80u && (v & 0x7F800000u) != 0x7F800000u; }
@@ -272,13 +283,18 @@ __device__ __forceinline__ bool tidy_v(unsigned char* vt, int first, int rows, u
 
 // The infinities and NaN of a V tile, before tidy_v cleans them away, added to the queries that take their
 // keys: what a positive probability times an infinity or a NaN gives is that infinity or NaN.
-template <int D>
-__device__ __forceinline__ void add_nonfinite(Rows<D>& w, const unsigned char* vt, int keys, const uint64_t (&allowed)[2]) {
+template <int D, int NQ>
+__device__ __forceinline__ void add_nonfinite(Rows<D, NQ>& w, const unsigned char* vt, int keys, const uint64_t (&allowed)[NQ]) {
     int q = (int(threadIdx.x) >> 4) & 3;
     asm volatile("" : "+v"(q));
     for (int j = 0; j < keys; ++j) {
-        const bool mine[2] = {bool((allowed[0] >> j) & 1), bool((allowed[1] >> j) & 1)};
-        if (!__any(mine[0] || mine[1])) continue;
+        bool mine[NQ], some = false;
+#pragma unroll
+        for (int qb = 0; qb < NQ; ++qb) {
+            mine[qb] = (allowed[qb] >> j) & 1;
+            some = some || mine[qb];
+        }
+        if (!__any(some)) continue;
 #pragma unroll
         for (int b = 0; b < D / 16; ++b) {  // columns 16 b + 4 q ..
             const u32x2_t v = *reinterpret_cast<const u32x2_t*>(
@@ -288,7 +304,7 @@ __device__ __forceinline__ void add_nonfinite(Rows<D>& w, const unsigned char* v
                 const uint32_t bits = i & 1 ? v[i / 2] & 0xFFFF0000u : v[i / 2] << 16;
                 const bool odd = (bits & 0x7F800000u) == 0x7F800000u;
 #pragma unroll
-                for (int qb = 0; qb < 2; ++qb)
+                for (int qb = 0; qb < NQ; ++qb)
                     if (mine[qb] && odd) w.o[b][qb][i] += __uint_as_float(bits);
             }
         }
@@ -296,11 +312,11 @@ __device__ __forceinline__ void add_nonfinite(Rows<D>& w, const unsigned char* v
 }
 
 // The Q operands of rows row0 + 16 qb + l16 (rows past the last read as zeros).
-template <int D>
-__device__ __forceinline__ void load_q(Rows<D>& w, const AttnArgs& a, int b, int hk, int row0) {
+template <int D, int NQ>
+__device__ __forceinline__ void load_q(Rows<D, NQ>& w, const AttnArgs& a, int b, int hk, int row0) {
     const int lane = int(threadIdx.x) & 63, q = lane >> 4;
 #pragma unroll
-    for (int qb = 0; qb < 2; ++qb) {
+    for (int qb = 0; qb < NQ; ++qb) {
         const int row = row0 + 16 * qb + (lane & 15);
         const bool in = row < a.rows;
         const int t = in ? row / a.group : 0, g = in ? row - t * a.group : 0;
@@ -317,7 +333,7 @@ __device__ __forceinline__ void load_q(Rows<D>& w, const AttnArgs& a, int b, int
 // O of the rows to memory, divided by l: 16 bytes per lane and pair of column blocks after an exchange between
 // neighbouring lane quarters (each holds 4 of every 16 columns).  A row without keys has l = 0: zeros.
 template <int D>
-__device__ __forceinline__ void store_o(const Rows<D>& w, const AttnArgs& a, int b, int hk, int row0) {
+__device__ __forceinline__ void store_o(const Rows<D, 2>& w, const AttnArgs& a, int b, int hk, int row0) {
     const int lane = int(threadIdx.x) & 63, q = lane >> 4;
 #pragma unroll
     for (int qb = 0; qb < 2; ++qb) {
@@ -339,7 +355,7 @@ __device__ __forceinline__ void store_o(const Rows<D>& w, const AttnArgs& a, int
 
 // Partial results of the rows for the join: O unnormalised, then (c m, l).
 template <int D>
-__device__ __forceinline__ void store_part(const Rows<D>& w, const AttnArgs& a, int64_t base, int row0) {
+__device__ __forceinline__ void store_part(const Rows<D, 2>& w, const AttnArgs& a, int64_t base, int row0) {
     const int lane = int(threadIdx.x) & 63, q = lane >> 4;
 #pragma unroll
     for (int qb = 0; qb < 2; ++qb) {
@@ -430,7 +446,7 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
     const int t0 = split * a.tiles_per_split;
     const int t1 = in_sgpr(t0 + a.tiles_per_split < tiles ? t0 + a.tiles_per_split : tiles);
 
-    Rows<D> w;
+    Rows<D, 2> w;
     rows_init(w);
     load_q(w, a, b, hk, row0);
     // the last key of the lane's rows
@@ -516,19 +532,18 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
             lds_writes_barrier();
             odd = odd_tile == t;
         }
-        Scores s;
-        Probs p;
-        scores<D>(w, f, kc, s);
+        Scores<4, 2> s;
+        Probs<4, 2> p;
+        scores(w, f, kc, s);
         if (partial) mask_scores(s, allowed);
-        grow(w, s, c);
-        probabilities<D>(w, s, p, c);
+        probabilities_checked(w, s, p, c);
         if (odd) {
             add_nonfinite<D>(w, vc, 64, allowed);
             lds_writes_barrier();
             tidy_v<D, true>(vc, wave * 16, 16, live);
             lds_writes_barrier();
         }
-        weighted<D>(w, f, vc, p);
+        weighted(w, f, vc, p);
     };
 
     issue_k(t0, kbuf0);
@@ -538,29 +553,27 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
             // a run of whole tiles, two per turn; the scores are one tile ahead of the values
             arrive();
             issue_k(t + 1, kbuf1);
-            Scores s0, s1;
-            scores<D>(w, f, kbuf0, s0);
-            grow(w, s0, c);
+            Scores<4, 2> s0, s1;
+            scores(w, f, kbuf0, s0);
             do {
                 arrive();
                 issue_k(t + 2, kbuf0);
                 issue_v(t + 1, vbuf1);
-                fused_step<D>(w, f, kbuf1, vbuf0, s0, s1, c);
+                fused_step(w, f, kbuf1, vbuf0, s0, s1, c);
                 arrive();
                 issue_k(t + 3, kbuf1);
                 issue_v(t + 2, vbuf0);
                 m0 = m2;
                 m1 = fetch(t + 3);
                 m2 = fetch(t + 4);
-                fused_step<D>(w, f, kbuf0, vbuf1, s1, s0, c);
+                fused_step(w, f, kbuf0, vbuf1, s1, s0, c);
                 t += 2;
             } while (whole(t + 1, m1) && whole(t + 2, m2));
             arrive();
             issue_v(t + 1, vbuf1);
-            Probs p;
-            grow(w, s0, c);
-            probabilities<D>(w, s0, p, c);
-            weighted<D>(w, f, vbuf0, p);
+            Probs<4, 2> p;
+            probabilities_checked(w, s0, p, c);
+            weighted(w, f, vbuf0, p);
             m0 = m1;
             m1 = m2;
             m2 = fetch(t + 3);
@@ -574,6 +587,240 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
         store_o(w, a, b, hk, row0);
     } else {
         store_part(w, a, ((int64_t(b) * a.kv_heads + hk) * a.splits + split) * a.rows, row0);
+    }
+}
+
+// Few rows (one or two blocks of 16: decoded tokens): bound by reading the keys and values once.  Every
+// wave takes its own tiles of 32 keys (tile w, w + 4, .. of the workgroup's range for wave w), copied into its own two LDS
+// stages, so no barrier stands between the copies and 64 KB are on their way per compute unit.  The
+// waves' results are joined through LDS; where the keys are also split across workgroups, each leaves
+// its partial result in the workspace and the last one to arrive joins them.  Both joins go in a fixed
+// order (wave 0 .., split 0 ..), so results do not depend on timing.
+constexpr int kShortKeys = 32;
+
+template <int D, int NQ>
+__global__ __launch_bounds__(256, 1) void attention_short_kernel(AttnArgs a) {
+    constexpr int kTile = kShortKeys * D * 2;
+    constexpr int kRowsPerCopy = 512 / D;
+    constexpr int kCopies = kShortKeys / kRowsPerCopy;  // of K and of V, per wave and tile
+    constexpr int kWaves = 4;
+    // an array per stage: the compiler then sees that a stage's reads do not depend on the other's copies
+    __shared__ __attribute__((aligned(1024))) unsigned char stage0[kWaves][2 * kTile], stage1[kWaves][2 * kTile];
+    __shared__ float join_mc[kWaves][NQ][16], join_l[kWaves][NQ][16];
+    __shared__ int last_split;
+    const int lane = int(threadIdx.x) & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    const int q = lane >> 4, l16 = lane & 15;
+    const int split = int(blockIdx.x) % a.splits, bh = int(blockIdx.x) / a.splits;
+    const int hk = bh % a.kv_heads, b = bh / a.kv_heads;
+
+    const int n = live_keys(a, b);
+    const int64_t start = a.causal ? (a.start != nullptr ? a.start[b] : 0) : 0;
+    const int64_t last = a.causal ? start + (a.rows - 1) / a.group : int64_t(n) - 1;
+    const int64_t end64 = last + 1 < n ? last + 1 : n;
+    const int end = end64 < 0 ? 0 : int(end64);
+    const int64_t first64 = a.causal ? start + 1 : n;  // the first key that some row leaves out
+    const int first = first64 < 0 ? 0 : first64 < n ? int(first64) : n;
+    // the splits share the keys there are, not the keys there could be
+    const int tiles = (end + kShortKeys - 1) / kShortKeys;
+    const int t0 = int(int64_t(tiles) * split / a.splits), t1 = int(int64_t(tiles) * (split + 1) / a.splits);
+
+    Rows<D, NQ> w;
+    rows_init(w);
+    load_q(w, a, b, hk, 0);
+    int64_t mine[NQ];
+#pragma unroll
+    for (int qb = 0; qb < NQ; ++qb) {
+        const int row = 16 * qb + l16;
+        mine[qb] = a.causal ? start + (row < a.rows ? row : a.rows - 1) / a.group : int64_t(1) << 40;
+    }
+    const Offsets<D> f = offsets<D>();
+
+    const uint32_t k_row = uint32_t(a.k_token) * 2u, v_row = uint32_t(a.v_token) * 2u;
+    const unsigned char* kp = reinterpret_cast<const unsigned char*>(a.k + int64_t(b) * a.k_batch + int64_t(hk) * a.k_head);
+    const unsigned char* vp = reinterpret_cast<const unsigned char*>(a.v + int64_t(b) * a.v_batch + int64_t(hk) * a.v_head);
+    const uint8_t* mask = a.mask == nullptr ? nullptr : a.mask + int64_t(b) * a.mask_batch;
+    // copy i of a wave brings rows i * kRowsPerCopy ..; their swizzles repeat every 16 rows
+    const int r0 = lane / (D / 8), p0 = lane % (D / 8);
+    auto issue = [&](int t, unsigned char* to) __attribute__((always_inline)) {
+        // a tile past the range is still issued, through empty ranges: the counted wait below holds for every tile
+        const bool there = t < t1;
+        const int key0 = there ? kShortKeys * t : 0;
+        const int have = n - key0 < kShortKeys ? n - key0 : kShortKeys;
+        const auto kr = make_rsrc(kp + int64_t(key0) * k_row, there ? uint32_t(have - 1) * k_row + 2u * D : 0u);
+        const auto vr = make_rsrc(vp + int64_t(key0) * v_row, there ? uint32_t(have - 1) * v_row + 2u * D : 0u);
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+            const int r = i * kRowsPerCopy + r0;
+            dma16(kr, to + i * 1024, uint32_t(r) * k_row + uint32_t(p0 ^ k_swz<D>(r)) * 16u, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+            const int r = i * kRowsPerCopy + r0;
+            dma16(vr, to + kTile + i * 1024, uint32_t(r) * v_row + uint32_t(p0 ^ v_swz<D>(r)) * 16u, 0);
+        }
+    };
+    auto step = [&](int t, unsigned char* at) __attribute__((always_inline)) {
+        const int key0 = kShortKeys * t;
+        uint64_t live = n - key0 >= kShortKeys ? 0xFFFFFFFFull : (1ull << (n - key0)) - 1;
+        if (mask != nullptr) live = __ballot(lane < kShortKeys && key0 + lane < n && mask[key0 + lane] != 0);
+        wait_vmcnt<2 * kCopies>();  // all but the other stage's copies
+        asm volatile("" ::: "memory");
+        if (live != 0) {
+            Scores<2, NQ> x;
+            Probs<2, NQ> p;
+            uint64_t allowed[NQ];
+            bool odd = false;
+            const bool partial = live != 0xFFFFFFFFull || key0 + kShortKeys > first;
+            if (partial) {
+#pragma unroll
+                for (int qb = 0; qb < NQ; ++qb) allowed[qb] = live & up_to(mine[qb] - key0);
+                odd = __any(tidy_v<D, false>(at + kTile, 0, kShortKeys, live));
+            }
+            scores(w, f, at, x);
+            if (partial) mask_scores(x, allowed);
+            probabilities_checked(w, x, p, a.scale_log2);
+            if (odd) {
+                add_nonfinite<D, NQ>(w, at + kTile, kShortKeys, allowed);
+                tidy_v<D, true>(at + kTile, 0, kShortKeys, live);
+            }
+            weighted(w, f, at + kTile, p);
+        }
+        // the stage's reads are done before its next copies may land
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+        asm volatile("" ::: "memory");
+    };
+    int t = t0 + wave;
+    if (t < t1) {
+        issue(t, stage0[wave]);
+        issue(t + kWaves, stage1[wave]);
+        for (;;) {
+            step(t, stage0[wave]);
+            t += kWaves;
+            if (t >= t1) break;
+            issue(t + kWaves, stage0[wave]);
+            step(t, stage1[wave]);
+            t += kWaves;
+            if (t >= t1) break;
+            issue(t + kWaves, stage1[wave]);
+        }
+    }
+    wait_vmcnt<0>();
+
+    // ---- the waves' results ----
+    // wave w's O in its stage 0 (16 bytes per lane, column block and row block)
+    f32x4_t* const mine_o = reinterpret_cast<f32x4_t*>(stage0[wave]);
+#pragma unroll
+    for (int d = 0; d < D / 16; ++d)
+#pragma unroll
+        for (int qb = 0; qb < NQ; ++qb) mine_o[(d * NQ + qb) * 64 + lane] = w.o[d][qb];
+    if (q == 0) {
+#pragma unroll
+        for (int qb = 0; qb < NQ; ++qb) {
+            join_mc[wave][qb][l16] = w.mc[qb];
+            join_l[wave][qb][l16] = w.l[qb][0];
+        }
+    }
+    __syncthreads();
+    const int rows = a.rows;
+    const int64_t part_base = (int64_t(bh) * a.splits) * rows;
+    const uint32_t part_bytes = uint32_t(a.splits) * uint32_t(rows) * (D + 2) * 4u;  // of this head
+    constexpr int kSc1 = 16;  // through to the device-coherent level: other workgroups' caches are elsewhere
+    const auto part_rs = make_rsrc(a.part + part_base * (D + 2), a.splits > 1 ? part_bytes : 0u);
+    auto row_factors = [&](const float* mc, const float* l, int count, int stride, float* factor, float& total) {
+        float top = kNegInf;
+        for (int i = 0; i < count; ++i) top = fmaxf(top, mc[i * stride]);
+        total = 0.f;
+        for (int i = 0; i < count; ++i) {
+            factor[i] = mc[i * stride] == kNegInf ? 0.f : __builtin_amdgcn_exp2f(mc[i * stride] - top);
+            total += factor[i] * l[i * stride];
+        }
+        return top;
+    };
+    // O of row `row`, columns col .. col + 3, divided by the sum l (0: a row without keys)
+    auto store4 = [&](int row, int col, f32x4_t v, float l) {
+        const int tok = row / a.group, g = row - tok * a.group;
+        uint16_t* dst = a.o + int64_t(b) * a.o_batch + int64_t(tok) * a.o_token + int64_t(hk * a.group + g) * a.o_head + col;
+        const float r = l == 0.f ? 0.f : 1.f / l;
+        *reinterpret_cast<u32x2_t*>(dst) = u32x2_t{pack_bf16(v[0] * r, v[1] * r), pack_bf16(v[2] * r, v[3] * r)};
+    };
+#pragma unroll
+    for (int qb = 0; qb < NQ; ++qb) {
+        const int row = 16 * qb + l16;
+        float factor[kWaves], total;
+        const float top = row_factors(&join_mc[0][qb][l16], &join_l[0][qb][l16], kWaves, NQ * 16, factor, total);
+#pragma unroll
+        for (int d0 = 0; d0 < D / 16; d0 += kWaves) {
+            const int d = d0 + wave;
+            f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int i = 0; i < kWaves; ++i) {
+                const f32x4_t u = reinterpret_cast<const f32x4_t*>(stage0[i])[(d * NQ + qb) * 64 + lane];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(factor[i], u[e], v[e]);
+            }
+            if (row < rows) {
+                if (a.splits == 1)
+                    store4(row, 16 * d + 4 * q, v, total);
+                else
+                    __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), part_rs,
+                                                           (uint32_t(split * rows + row) * (D + 2) + uint32_t(16 * d + 4 * q)) * 4u, 0, kSc1);
+            }
+        }
+        if (a.splits > 1 && wave == 0 && q == 0 && row < rows) {
+            const uint32_t at = (uint32_t(split * rows + row) * (D + 2) + D) * 4u;
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(top), part_rs, at, 0, kSc1);
+            __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(total), part_rs, at + 4u, 0, kSc1);
+        }
+    }
+    if (a.splits == 1) return;
+
+    // ---- the splits' results: the last workgroup of the head to arrive joins them ----
+    wait_vmcnt<0>();  // the partial result is there before the arrival counts
+    __syncthreads();
+    if (threadIdx.x == 0)
+        last_split = __hip_atomic_fetch_add(&a.counters[bh], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == uint32_t(a.splits - 1);
+    __syncthreads();
+    if (!last_split) return;
+    if (threadIdx.x == 0) __hip_atomic_store(&a.counters[bh], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    // every row's factors (kMaxShortSplits of them at most), then its columns
+    float* const factors = reinterpret_cast<float*>(stage1[0]);  // [rows][splits], then the sums [rows]
+    float* const totals = factors + rows * a.splits;
+    for (int row = wave; row < rows; row += kWaves) {  // a lane per split
+        const uint32_t at = (uint32_t(lane * rows + row) * (D + 2) + D) * 4u;
+        const bool in = lane < a.splits;
+        const float mc = in ? __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(part_rs, at, 0, kSc1)) : kNegInf;
+        const float l = in ? __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(part_rs, at + 4u, 0, kSc1)) : 0.f;
+        float top = mc;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+        const float fac = mc == kNegInf ? 0.f : __builtin_amdgcn_exp2f(mc - top);
+        float sum = fac * l;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
+        if (in) factors[row * a.splits + lane] = fac;
+        if (lane == 0) totals[row] = sum;
+    }
+    __syncthreads();
+    // (row, 4 columns) per thread; up to 8 splits' loads in flight
+    for (int i = int(threadIdx.x); i < rows * (D / 4); i += 64 * kWaves) {
+        const int row = i / (D / 4), col = 4 * (i % (D / 4));
+        f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+        for (int s0 = 0; s0 < a.splits; s0 += 8) {
+            f32x4_t u[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)  // a split past the last reads as zeros
+                u[j] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                       part_rs, s0 + j < a.splits ? (uint32_t((s0 + j) * rows + row) * (D + 2) + uint32_t(col)) * 4u : 0xFFFFFF00u,
+                                                       0, kSc1));
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float fac = s0 + j < a.splits ? factors[row * a.splits + s0 + j] : 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(fac, u[j][e], v[e]);
+            }
+        }
+        store4(row, col, v, totals[row]);
     }
 }
 
@@ -608,7 +855,15 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
 }
 
 template <int D>
-hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
+hipError_t launch_d(const AttnArgs& a, bool is_short, hipStream_t stream) {
+    if (is_short) {
+        const unsigned grid = unsigned(a.splits) * unsigned(a.kv_heads) * unsigned(a.batch);
+        if (a.rows <= 16)
+            hipLaunchKernelGGL((attention_short_kernel<D, 1>), dim3(grid), dim3(256), 0, stream, a);
+        else
+            hipLaunchKernelGGL((attention_short_kernel<D, 2>), dim3(grid), dim3(256), 0, stream, a);
+        return hipGetLastError();
+    }
     const int64_t grid = int64_t(a.row_tiles) * a.splits * a.kv_heads * a.batch;
     hipLaunchKernelGGL((attention_kernel<D>), dim3(unsigned(grid)), dim3(256), 0, stream, a);
     hipError_t e = hipGetLastError();
@@ -618,23 +873,39 @@ hipError_t launch_d(const AttnArgs& a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+constexpr int kMaxShortSplits = 64;     // a lane per split in the join
+constexpr size_t kCounterBytes = 4096;  // at the workspace's start: arrival counters, zero between calls
+
 }  // namespace
 
-// Splits along the keys: where the row tiles leave compute units idle, about two workgroups per
-// compute unit, each with four key tiles at least.
+// Short rows (two blocks of 16 at most) take the kernel for them, with the keys split so that every compute unit
+// has one workgroup, each wave two tiles at least.  Longer rows split where their tiles of 128 leave
+// compute units idle: about two workgroups per compute unit, each with four key tiles at least.
 AttnPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t kv_len, int head_dim) {
-    AttnPlan p;
-    p.row_tiles = int(tiles_of(rows, 128));
-    const int64_t tiles = tiles_of(kv_len, 64), base = batch * kv_heads * p.row_tiles;
-    int64_t splits = base >= kComputeUnits ? 1 : 2 * kComputeUnits / base;
-    const int64_t most = tiles / 4;
-    splits = splits < most ? splits : most;
-    splits = splits < 1 ? 1 : splits;
-    p.tiles_per_split = int(tiles_of(tiles, splits));
-    p.splits = int(tiles_of(tiles, p.tiles_per_split > 0 ? p.tiles_per_split : 1));
-    if (p.splits < 1) p.splits = 1;
+    AttnPlan p{};
+    p.is_short = rows <= 32;
+    int64_t splits, tiles;
+    if (p.is_short) {
+        const int64_t heads = batch * kv_heads;
+        tiles = tiles_of(kv_len, kShortKeys);
+        splits = heads >= kComputeUnits ? 1 : kComputeUnits / heads;
+        splits = splits < tiles / 8 ? splits : tiles / 8;
+        splits = splits < kMaxShortSplits ? splits : kMaxShortSplits;
+        p.splits = splits < 1 ? 1 : int(splits);
+        p.row_tiles = 1;
+        p.tiles_per_split = 0;
+    } else {
+        p.row_tiles = int(tiles_of(rows, 128));
+        tiles = tiles_of(kv_len, 64);
+        const int64_t base = batch * kv_heads * p.row_tiles;
+        splits = base >= kComputeUnits ? 1 : 2 * kComputeUnits / base;
+        splits = splits < tiles / 4 ? splits : tiles / 4;
+        splits = splits < 1 ? 1 : splits;
+        p.tiles_per_split = int(tiles_of(tiles, splits));
+        p.splits = p.tiles_per_split > 0 ? int(tiles_of(tiles, p.tiles_per_split)) : 1;
+    }
     p.part_rows = p.splits > 1 ? batch * kv_heads * rows * p.splits : 0;
-    p.bytes = size_t(p.part_rows) * (size_t(head_dim) + 2) * 4u;
+    p.bytes = p.splits > 1 ? kCounterBytes + size_t(p.part_rows) * (size_t(head_dim) + 2) * 4u : 0;
     return p;
 }
 
@@ -650,9 +921,10 @@ hipError_t launch_attention(AttnArgs a, int head_dim, const AttnPlan& plan, void
     a.row_tiles = plan.row_tiles;
     a.splits = plan.splits;
     a.tiles_per_split = plan.tiles_per_split;
-    a.part = static_cast<float*>(workspace);
+    a.counters = static_cast<uint32_t*>(workspace);
+    a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kCounterBytes);
     a.part_ml = a.part + plan.part_rows * head_dim;
-    return head_dim == 64 ? launch_d<64>(a, stream) : launch_d<128>(a, stream);
+    return head_dim == 64 ? launch_d<64>(a, plan.is_short, stream) : launch_d<128>(a, plan.is_short, stream);
 }
 
 }  // namespace lowbit

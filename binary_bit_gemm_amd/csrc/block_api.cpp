@@ -99,6 +99,7 @@ int attention_args(const lowbit_attention_problem* p, lowbit::AttnArgs& a) {
 }
 
 constexpr int64_t kMaxAdapters = 1 << 16;
+constexpr size_t kCounterBytes = 4096;  // of a workspace, for the calls that split sums
 
 bool lora_rank_ok(int64_t rank) { return rank >= 8 && rank <= 128 && rank % 8 == 0; }
 
@@ -108,7 +109,7 @@ extern "C" {
 
 size_t lowbit_lora_workspace_size(int64_t M, int rank) {
     if (M <= 0 || M > kMaxDim || !lora_rank_ok(rank)) return 0;
-    return (size_t(M) * size_t(rank) * 4u + 255u) & ~size_t(255);
+    return kCounterBytes + ((size_t(M) * size_t(rank) * 4u + 255u) & ~size_t(255));
 }
 
 int lowbit_gemm_lora(const void* X, const uint32_t* W, const void* S, void* Y, int64_t M, int64_t N, int64_t K, int g,
@@ -131,7 +132,7 @@ int lowbit_gemm_lora(const void* X, const uint32_t* W, const void* S, void* Y, i
     if (st != LOWBIT_OK) return st;
     const hipStream_t s = static_cast<hipStream_t>(stream);
     const lowbit::ShrinkArgs sh{static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(A), alpha, rows,
-                                static_cast<uint16_t*>(workspace), int(M), int(K), int(adapters), rank};
+                                reinterpret_cast<uint16_t*>(static_cast<unsigned char*>(workspace) + kCounterBytes), int(M), int(K), int(adapters), rank};
     hipError_t e = lowbit::launch_lora_shrink(sh, s);
     if (e != hipSuccess) return lowbit::hip_fail(e);
     const lowbit::LoraArgs la{sh.u, static_cast<const uint16_t*>(B), rows, int(adapters), rank};

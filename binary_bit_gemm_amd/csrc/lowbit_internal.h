@@ -189,11 +189,13 @@ struct AttnArgs {
     float scale_log2;                                  // scale * log2(e)
     // set by the launch
     int row_tiles, splits, tiles_per_split;
+    uint32_t* counters;  // arrivals of a head's splits (short rows), zero between calls
     float *part, *part_ml;
 };
 // How a call is divided: row tiles of a kv head, ranges of key tiles, and the workspace of the ranges'
 // partial results (bytes 0: none; without one the call runs unsplit).
 struct AttnPlan {
+    bool is_short;  // the kernel for few rows
     int row_tiles, splits, tiles_per_split;
     int64_t part_rows;
     size_t bytes;

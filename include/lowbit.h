@@ -319,9 +319,9 @@ int lowbit_gemm_affine_ex(const void* X, const uint32_t* W, const void* S, const
  *   rows  device int32 [M]: the adapter of each row, in any order; a value outside [0, adapters) (e.g. -1)
  *      means none.  Rows of different adapters do not affect each other, whatever an adapter holds.
  *   rank  a multiple of 8 from 8 to 128 (pad smaller adapters with zeros).
- *   workspace  device memory of lowbit_lora_workspace_size(M, rank) bytes, 16-byte aligned, of any
- *      content (required: NULL or too small returns LOWBIT_E_INVALID).  Calls that share it must not
- *      run concurrently.
+ *   workspace  device memory of lowbit_lora_workspace_size(M, rank) bytes, 16-byte aligned (required: NULL or
+ *      too small returns LOWBIT_E_INVALID).  Any content will do; the first 4096 bytes, where calls that
+ *      split K or keys keep their counters, are left alone.  Calls that share it must not run concurrently.
  * Both products are fp32 sums of bf16 products; X . A^T is kept to 16 significant bits between them; Y is rounded
  * to bf16 once.  Deterministic.  A, B and workspace need 16-byte alignment, alpha and rows 4.
  */
@@ -386,8 +386,10 @@ int lowbit_qk_norm_rope(const lowbit_qk_problem* problem, void* stream);
  *   anything, infinities and NaN included.
  * Scores, softmax statistics and sums are fp32; the probabilities are rounded to bf16 for the second
  * product; O is rounded once.  Deterministic.
- *   workspace  device memory of lowbit_attention_workspace_size(problem) bytes, 16-byte aligned, of any
- *      content, with which a call of few rows and many keys splits the keys across workgroups.  With a
+ *   workspace  device memory of lowbit_attention_workspace_size(problem) bytes, 16-byte aligned, ZERO-FILLED
+ *      before its first use, with which a call of few rows and many keys splits the keys across workgroups.  Its
+ *      first 4096 bytes hold arrival counters that every call leaves at zero, so one workspace serves calls
+ *      of any shapes in turn (and lowbit_gemm_ex's, lowbit_gemm_affine_ex's and lowbit_gemm_lora's).  With a
  *      NULL or too small workspace the call runs unsplit.  Calls that share it must not run concurrently.
  * The size depends on the shape only (0: no split, or invalid arguments).  The descriptor is read
  * before the call returns.  key_lens and q_start need 4-byte alignment, q, k, v, o and workspace 16.

@@ -69,7 +69,9 @@ def make(B, Lq, Lk, Hq, Hk, D, seed=0):
 
 def scratch(q, k, v):
     n = lb.attention_workspace_size(q, k, v)
-    return torch.full((n,), 0xAB, dtype=torch.uint8, device="cuda") if n else None
+    ws = torch.full((n,), 0xAB, dtype=torch.uint8, device="cuda")
+    ws[:4096] = 0  # the arrival counters; the rest may hold anything
+    return ws if n else None
 
 
 SHAPES = [  # B, Lq, Lk, Hq, Hk, D
@@ -224,6 +226,17 @@ def test_runs_repeat_bitwise_and_on_another_stream():
         got = lb.attention(q, k, v, workspace=ws)
     s.synchronize()
     assert torch.equal(got, want)
+
+
+def test_counters_are_left_at_zero_and_shapes_take_turns():
+    calls = [make(*shape, seed=20 + i) for i, shape in enumerate([(1, 1, 9000, 8, 2, 128), (4, 2, 1500, 16, 4, 64), (2, 40, 4000, 2, 2, 128)])]
+    ws = torch.zeros(max(lb.attention_workspace_size(*c) for c in calls), dtype=torch.uint8, device="cuda")
+    first = [lb.attention(*c, workspace=ws) for c in calls]
+    for _ in range(2):
+        for c, f in zip(calls, first):
+            got = lb.attention(*c, workspace=ws)
+            assert torch.equal(got, f) and not bool(ws[:4096].any())
+            check(got, *reference(*c))
 
 
 def test_in_a_graph():
