@@ -23,6 +23,9 @@
 //
 // Rounding to bf16: the probabilities before the second product (the matrix cores' input; relative
 // 2^-8 each, averaged over the keys) and O at the store.  Scores, m, l and O are fp32.
+#include <cstdlib>
+#include <cstring>
+
 #include "lowbit_device.h"
 #include "lowbit_internal.h"
 
@@ -496,9 +499,10 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
         wait_vmcnt<0>();
         __syncthreads();
     };
-    // The lane's bytes of the mask for tiles t, t + 1 and t + 2, fetched before they are needed.
+    // The lane's bytes of the mask for tiles t, t + 1 and t + 2, fetched before they are needed (0 past the last key).
     auto fetch = [&](int t) __attribute__((always_inline)) {
-        return mask != nullptr && 64 * t + lane < n ? mask[64 * t + lane] : uint8_t(0);
+        if (mask == nullptr) return uint8_t(0);
+        return uint8_t(__builtin_amdgcn_raw_buffer_load_b8(make_rsrc(mask, uint32_t(n)), uint32_t(64 * t + lane), 0, 0));
     };
     uint8_t m0 = fetch(t0), m1 = fetch(t0 + 1), m2 = fetch(t0 + 2);
     // Whole tiles: all rows of the workgroup take all 64 keys.
@@ -591,35 +595,41 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
 }
 
 // Few rows (one or two blocks of 16: decoded tokens): bound by reading the keys and values once.  Every
-// wave takes its own tiles of 32 keys (tile w, w + 4, .. of the workgroup's range for wave w), copied into its own two LDS
-// stages, so no barrier stands between the copies and 64 KB are on their way per compute unit.  The
-// waves' results are joined through LDS; where the keys are also split across workgroups, each leaves
+// wave takes its own tiles of 32 keys (tile w, w + 4, .. of the workgroup's range for wave w), copied into its own part of
+// LDS, so no barrier stands between the copies; two workgroups share a compute unit, and while one wave
+// computes the others' copies are on their way (up to 128 KB per compute unit).  The waves' results are joined through LDS; where the keys are also split across workgroups, each leaves
 // its partial result in the workspace and the last one to arrive joins them.  Both joins go in a fixed
 // order (wave 0 .., split 0 ..), so results do not depend on timing.
 constexpr int kShortKeys = 32;
 
 template <int D, int NQ>
-__global__ __launch_bounds__(256, 1) void attention_short_kernel(AttnArgs a) {
+__global__ __launch_bounds__(256, 2) void attention_short_kernel(AttnArgs a) {
     constexpr int kTile = kShortKeys * D * 2;
     constexpr int kRowsPerCopy = 512 / D;
     constexpr int kCopies = kShortKeys / kRowsPerCopy;  // of K and of V, per wave and tile
     constexpr int kWaves = 4;
-    // an array per stage: the compiler then sees that a stage's reads do not depend on the other's copies
-    __shared__ __attribute__((aligned(1024))) unsigned char stage0[kWaves][2 * kTile], stage1[kWaves][2 * kTile];
+    __shared__ __attribute__((aligned(1024))) unsigned char tiles_lds[kWaves][2 * kTile];  // K, then V
     __shared__ float join_mc[kWaves][NQ][16], join_l[kWaves][NQ][16];
     __shared__ int last_split;
     const int lane = int(threadIdx.x) & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
     const int q = lane >> 4, l16 = lane & 15;
-    const int split = int(blockIdx.x) % a.splits, bh = int(blockIdx.x) / a.splits;
-    const int hk = bh % a.kv_heads, b = bh / a.kv_heads;
+    // row tiles and splits of one head next to each other on one XCD
+    int id = xcd_remap(int(blockIdx.x), int(gridDim.x));
+    const int split = id % a.splits;
+    id /= a.splits;
+    const int rt = id % a.row_tiles;
+    id /= a.row_tiles;
+    const int hk = id % a.kv_heads, b = id / a.kv_heads;
+    const int group_of = (b * a.kv_heads + hk) * a.row_tiles + rt;  // of the workgroups that share rows
+    const int row0 = rt * 16 * NQ, rows = a.rows - row0 < 16 * NQ ? a.rows - row0 : 16 * NQ;
 
     const int n = live_keys(a, b);
     const int64_t start = a.causal ? (a.start != nullptr ? a.start[b] : 0) : 0;
-    const int64_t last = a.causal ? start + (a.rows - 1) / a.group : int64_t(n) - 1;
+    const int64_t last = a.causal ? start + (row0 + rows - 1) / a.group : int64_t(n) - 1;
     const int64_t end64 = last + 1 < n ? last + 1 : n;
     const int end = end64 < 0 ? 0 : int(end64);
-    const int64_t first64 = a.causal ? start + 1 : n;  // the first key that some row leaves out
+    const int64_t first64 = a.causal ? start + row0 / a.group + 1 : n;  // the first key that some row leaves out
     const int first = first64 < 0 ? 0 : first64 < n ? int(first64) : n;
     // the splits share the keys there are, not the keys there could be
     const int tiles = (end + kShortKeys - 1) / kShortKeys;
@@ -627,11 +637,11 @@ __global__ __launch_bounds__(256, 1) void attention_short_kernel(AttnArgs a) {
 
     Rows<D, NQ> w;
     rows_init(w);
-    load_q(w, a, b, hk, 0);
+    load_q(w, a, b, hk, row0);
     int64_t mine[NQ];
 #pragma unroll
     for (int qb = 0; qb < NQ; ++qb) {
-        const int row = 16 * qb + l16;
+        const int row = row0 + 16 * qb + l16;
         mine[qb] = a.causal ? start + (row < a.rows ? row : a.rows - 1) / a.group : int64_t(1) << 40;
     }
     const Offsets<D> f = offsets<D>();
@@ -642,36 +652,34 @@ __global__ __launch_bounds__(256, 1) void attention_short_kernel(AttnArgs a) {
     const uint8_t* mask = a.mask == nullptr ? nullptr : a.mask + int64_t(b) * a.mask_batch;
     // copy i of a wave brings rows i * kRowsPerCopy ..; their swizzles repeat every 16 rows
     const int r0 = lane / (D / 8), p0 = lane % (D / 8);
-    auto issue = [&](int t, unsigned char* to) __attribute__((always_inline)) {
-        // a tile past the range is still issued, through empty ranges: the counted wait below holds for every tile
-        const bool there = t < t1;
-        const int key0 = there ? kShortKeys * t : 0;
-        const int have = n - key0 < kShortKeys ? n - key0 : kShortKeys;
-        const auto kr = make_rsrc(kp + int64_t(key0) * k_row, there ? uint32_t(have - 1) * k_row + 2u * D : 0u);
-        const auto vr = make_rsrc(vp + int64_t(key0) * v_row, there ? uint32_t(have - 1) * v_row + 2u * D : 0u);
-#pragma unroll
-        for (int i = 0; i < kCopies; ++i) {
-            const int r = i * kRowsPerCopy + r0;
-            dma16(kr, to + i * 1024, uint32_t(r) * k_row + uint32_t(p0 ^ k_swz<D>(r)) * 16u, 0);
-        }
-#pragma unroll
-        for (int i = 0; i < kCopies; ++i) {
-            const int r = i * kRowsPerCopy + r0;
-            dma16(vr, to + kTile + i * 1024, uint32_t(r) * v_row + uint32_t(p0 ^ v_swz<D>(r)) * 16u, 0);
-        }
-    };
-    auto step = [&](int t, unsigned char* at) __attribute__((always_inline)) {
+    const auto mask_rs = make_rsrc(mask, mask != nullptr ? uint32_t(n) : 0u);
+    unsigned char* const at = tiles_lds[wave];
+    for (int t = t0 + wave; t < t1; t += kWaves) {
         const int key0 = kShortKeys * t;
-        uint64_t live = n - key0 >= kShortKeys ? 0xFFFFFFFFull : (1ull << (n - key0)) - 1;
-        if (mask != nullptr) live = __ballot(lane < kShortKeys && key0 + lane < n && mask[key0 + lane] != 0);
-        wait_vmcnt<2 * kCopies>();  // all but the other stage's copies
+        const int have = n - key0 < kShortKeys ? n - key0 : kShortKeys;  // rows past the last key come as zeros
+        const uint8_t byte = uint8_t(__builtin_amdgcn_raw_buffer_load_b8(mask_rs, uint32_t(key0 + lane), 0, 0));
+        const auto kr = make_rsrc(kp + int64_t(key0) * k_row, uint32_t(have - 1) * k_row + 2u * D);
+        const auto vr = make_rsrc(vp + int64_t(key0) * v_row, uint32_t(have - 1) * v_row + 2u * D);
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+            const int r = i * kRowsPerCopy + r0;
+            dma16(kr, at + i * 1024, uint32_t(r) * k_row + uint32_t(p0 ^ k_swz<D>(r)) * 16u, 0);
+        }
+#pragma unroll
+        for (int i = 0; i < kCopies; ++i) {
+            const int r = i * kRowsPerCopy + r0;
+            dma16(vr, at + kTile + i * 1024, uint32_t(r) * v_row + uint32_t(p0 ^ v_swz<D>(r)) * 16u, 0);
+        }
+        uint64_t live = have == kShortKeys ? 0xFFFFFFFFull : (1ull << have) - 1;
+        if (mask != nullptr) live = __ballot(lane < kShortKeys && byte != 0);
+        Scores<2, NQ> x;
+        Probs<2, NQ> p;
+        uint64_t allowed[NQ];
+        bool odd = false;
+        const bool partial = live != 0xFFFFFFFFull || key0 + kShortKeys > first;
+        wait_vmcnt<0>();
         asm volatile("" ::: "memory");
         if (live != 0) {
-            Scores<2, NQ> x;
-            Probs<2, NQ> p;
-            uint64_t allowed[NQ];
-            bool odd = false;
-            const bool partial = live != 0xFFFFFFFFull || key0 + kShortKeys > first;
             if (partial) {
 #pragma unroll
                 for (int qb = 0; qb < NQ; ++qb) allowed[qb] = live & up_to(mine[qb] - key0);
@@ -686,30 +694,14 @@ __global__ __launch_bounds__(256, 1) void attention_short_kernel(AttnArgs a) {
             }
             weighted(w, f, at + kTile, p);
         }
-        // the stage's reads are done before its next copies may land
+        // the tile's reads are done before the next copies may land
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
         asm volatile("" ::: "memory");
-    };
-    int t = t0 + wave;
-    if (t < t1) {
-        issue(t, stage0[wave]);
-        issue(t + kWaves, stage1[wave]);
-        for (;;) {
-            step(t, stage0[wave]);
-            t += kWaves;
-            if (t >= t1) break;
-            issue(t + kWaves, stage0[wave]);
-            step(t, stage1[wave]);
-            t += kWaves;
-            if (t >= t1) break;
-            issue(t + kWaves, stage1[wave]);
-        }
     }
-    wait_vmcnt<0>();
 
     // ---- the waves' results ----
-    // wave w's O in its stage 0 (16 bytes per lane, column block and row block)
-    f32x4_t* const mine_o = reinterpret_cast<f32x4_t*>(stage0[wave]);
+    // wave w's O in place of its tile (16 bytes per lane, column block and row block)
+    f32x4_t* const mine_o = reinterpret_cast<f32x4_t*>(at);
 #pragma unroll
     for (int d = 0; d < D / 16; ++d)
 #pragma unroll
@@ -722,9 +714,8 @@ __global__ __launch_bounds__(256, 1) void attention_short_kernel(AttnArgs a) {
         }
     }
     __syncthreads();
-    const int rows = a.rows;
-    const int64_t part_base = (int64_t(bh) * a.splits) * rows;
-    const uint32_t part_bytes = uint32_t(a.splits) * uint32_t(rows) * (D + 2) * 4u;  // of this head
+    const int64_t part_base = int64_t(group_of) * a.splits * (16 * NQ);
+    const uint32_t part_bytes = uint32_t(a.splits) * uint32_t(rows) * (D + 2) * 4u;  // of these rows
     constexpr int kSc1 = 16;  // through to the device-coherent level: other workgroups' caches are elsewhere
     const auto part_rs = make_rsrc(a.part + part_base * (D + 2), a.splits > 1 ? part_bytes : 0u);
     auto row_factors = [&](const float* mc, const float* l, int count, int stride, float* factor, float& total) {
@@ -737,8 +728,9 @@ __global__ __launch_bounds__(256, 1) void attention_short_kernel(AttnArgs a) {
         }
         return top;
     };
-    // O of row `row`, columns col .. col + 3, divided by the sum l (0: a row without keys)
-    auto store4 = [&](int row, int col, f32x4_t v, float l) {
+    // O of a row of the tile, columns col .. col + 3, divided by the sum l (0: a row without keys)
+    auto store4 = [&](int in_tile, int col, f32x4_t v, float l) {
+        const int row = row0 + in_tile;
         const int tok = row / a.group, g = row - tok * a.group;
         uint16_t* dst = a.o + int64_t(b) * a.o_batch + int64_t(tok) * a.o_token + int64_t(hk * a.group + g) * a.o_head + col;
         const float r = l == 0.f ? 0.f : 1.f / l;
@@ -755,7 +747,7 @@ __global__ __launch_bounds__(256, 1) void attention_short_kernel(AttnArgs a) {
             f32x4_t v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < kWaves; ++i) {
-                const f32x4_t u = reinterpret_cast<const f32x4_t*>(stage0[i])[(d * NQ + qb) * 64 + lane];
+                const f32x4_t u = reinterpret_cast<const f32x4_t*>(tiles_lds[i])[(d * NQ + qb) * 64 + lane];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(factor[i], u[e], v[e]);
             }
@@ -779,12 +771,12 @@ __global__ __launch_bounds__(256, 1) void attention_short_kernel(AttnArgs a) {
     wait_vmcnt<0>();  // the partial result is there before the arrival counts
     __syncthreads();
     if (threadIdx.x == 0)
-        last_split = __hip_atomic_fetch_add(&a.counters[bh], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == uint32_t(a.splits - 1);
+        last_split = __hip_atomic_fetch_add(&a.counters[group_of], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == uint32_t(a.splits - 1);
     __syncthreads();
     if (!last_split) return;
-    if (threadIdx.x == 0) __hip_atomic_store(&a.counters[bh], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (threadIdx.x == 0) __hip_atomic_store(&a.counters[group_of], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     // every row's factors (kMaxShortSplits of them at most), then its columns
-    float* const factors = reinterpret_cast<float*>(stage1[0]);  // [rows][splits], then the sums [rows]
+    float* const factors = reinterpret_cast<float*>(tiles_lds);  // [rows][splits], then the sums [rows]
     float* const totals = factors + rows * a.splits;
     for (int row = wave; row < rows; row += kWaves) {  // a lane per split
         const uint32_t at = (uint32_t(lane * rows + row) * (D + 2) + D) * 4u;
@@ -802,25 +794,47 @@ __global__ __launch_bounds__(256, 1) void attention_short_kernel(AttnArgs a) {
         if (lane == 0) totals[row] = sum;
     }
     __syncthreads();
-    // (row, 4 columns) per thread; up to 8 splits' loads in flight
-    for (int i = int(threadIdx.x); i < rows * (D / 4); i += 64 * kWaves) {
-        const int row = i / (D / 4), col = 4 * (i % (D / 4));
+    // (row, 4 columns) per thread, with the splits in `parts` ranges where threads are left over; kAhead loads in flight
+    constexpr int kAhead = 16;
+    const int items = rows * (D / 4);
+    int parts = 1;
+    while (parts < 4 && 2 * parts * items <= 64 * kWaves) parts *= 2;
+    const int span = (a.splits + parts - 1) / parts;
+    f32x4_t* const sums = reinterpret_cast<f32x4_t*>(tiles_lds[2]);  // [parts][items], read by the first range's threads
+    for (int i = int(threadIdx.x); i < items * parts; i += 64 * kWaves) {
+        const int part = i / items, item = i - part * items;
+        const int row = item / (D / 4), col = 4 * (item % (D / 4));
+        const int s1 = (part + 1) * span < a.splits ? (part + 1) * span : a.splits;
         f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-        for (int s0 = 0; s0 < a.splits; s0 += 8) {
-            f32x4_t u[8];
+        for (int s0 = part * span; s0 < s1; s0 += kAhead) {
+            f32x4_t u[kAhead];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)  // a split past the last reads as zeros
+            for (int j = 0; j < kAhead; ++j)  // a split past the range reads as zeros
                 u[j] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                                       part_rs, s0 + j < a.splits ? (uint32_t((s0 + j) * rows + row) * (D + 2) + uint32_t(col)) * 4u : 0xFFFFFF00u,
+                                                       part_rs, s0 + j < s1 ? (uint32_t((s0 + j) * rows + row) * (D + 2) + uint32_t(col)) * 4u : 0xFFFFFF00u,
                                                        0, kSc1));
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float fac = s0 + j < a.splits ? factors[row * a.splits + s0 + j] : 0.f;
+            for (int j = 0; j < kAhead; ++j) {
+                const float fac = s0 + j < s1 ? factors[row * a.splits + s0 + j] : 0.f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(fac, u[j][e], v[e]);
             }
         }
-        store4(row, col, v, totals[row]);
+        if (parts == 1)
+            store4(row, col, v, totals[row]);
+        else
+            sums[i] = v;
+    }
+    if (parts == 1) return;
+    __syncthreads();
+    for (int item = int(threadIdx.x); item < items; item += 64 * kWaves) {
+        f32x4_t v = sums[item];
+        for (int part = 1; part < parts; ++part) {
+            const f32x4_t u = sums[part * items + item];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += u[e];
+        }
+        store4(item / (D / 4), 4 * (item % (D / 4)), v, totals[item / (D / 4)]);
     }
 }
 
@@ -857,7 +871,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
 template <int D>
 hipError_t launch_d(const AttnArgs& a, bool is_short, hipStream_t stream) {
     if (is_short) {
-        const unsigned grid = unsigned(a.splits) * unsigned(a.kv_heads) * unsigned(a.batch);
+        const unsigned grid = unsigned(a.row_tiles) * unsigned(a.splits) * unsigned(a.kv_heads) * unsigned(a.batch);
         if (a.rows <= 16)
             hipLaunchKernelGGL((attention_short_kernel<D, 1>), dim3(grid), dim3(256), 0, stream, a);
         else
@@ -878,21 +892,32 @@ constexpr size_t kCounterBytes = 4096;  // at the workspace's start: arrival cou
 
 }  // namespace
 
-// Short rows (two blocks of 16 at most) take the kernel for them, with the keys split so that every compute unit
-// has one workgroup, each wave two tiles at least.  Longer rows split where their tiles of 128 leave
-// compute units idle: about two workgroups per compute unit, each with four key tiles at least.
+// Which kernel, and how the keys are split.
+//   The kernel for few rows (32 per workgroup, its waves over the keys) takes calls of up to 2^32 products: it has four
+// times the workgroups and no barriers, where the other kernel waits for copies.  Measured (us, few / many):
+// 512 x 512, 32 / 8 heads of 128: 14 / 29; 1024 x 1024, 24 heads of 128: 32 / 39; 2048 x 2048, 8 heads of 128:
+// 31 / 44; 128 x 32768, 8 heads of 128: 58 / 67; past the bound 1536 x 1536, 24 heads of 128: 61 / 52, and 2 x
+// 1533 x 1533, 16 heads of 64: 37 / 35.  One row block (16 or 32 rows) always takes it.
+//   Keys are split until every compute unit has a workgroup (few rows: 256 workgroups of four tiles a wave at least;
+// 512 were slower at 1024 rows, 27 against 17 us, and at 40007 keys, 33 against 32); the other
+// kernel, until there are two per compute unit, each with four tiles at least.
+//   LOWBIT_ATTENTION=few|many in the environment forces the kernel (A/B runs and tests).
 AttnPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t kv_len, int head_dim) {
     AttnPlan p{};
-    p.is_short = rows <= 32;
+    p.is_short = rows <= 32 || double(batch) * double(kv_heads) * double(rows) * double(kv_len) * head_dim <= 4294967296.0;
+    if (const char* force = std::getenv("LOWBIT_ATTENTION")) {
+        if (std::strcmp(force, "few") == 0) p.is_short = true;
+        if (std::strcmp(force, "many") == 0) p.is_short = false;
+    }
     int64_t splits, tiles;
     if (p.is_short) {
-        const int64_t heads = batch * kv_heads;
+        p.row_tiles = int(rows <= 16 ? 1 : tiles_of(rows, 32));
+        const int64_t heads = batch * kv_heads * p.row_tiles;
         tiles = tiles_of(kv_len, kShortKeys);
         splits = heads >= kComputeUnits ? 1 : kComputeUnits / heads;
-        splits = splits < tiles / 8 ? splits : tiles / 8;
+        splits = splits < tiles / 16 ? splits : tiles / 16;
         splits = splits < kMaxShortSplits ? splits : kMaxShortSplits;
         p.splits = splits < 1 ? 1 : int(splits);
-        p.row_tiles = 1;
         p.tiles_per_split = 0;
     } else {
         p.row_tiles = int(tiles_of(rows, 128));
@@ -904,7 +929,8 @@ AttnPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t k
         p.tiles_per_split = int(tiles_of(tiles, splits));
         p.splits = p.tiles_per_split > 0 ? int(tiles_of(tiles, p.tiles_per_split)) : 1;
     }
-    p.part_rows = p.splits > 1 ? batch * kv_heads * rows * p.splits : 0;
+    const int64_t padded = p.is_short ? int64_t(p.row_tiles) * (rows <= 16 ? 16 : 32) : rows;
+    p.part_rows = p.splits > 1 ? batch * kv_heads * padded * p.splits : 0;
     p.bytes = p.splits > 1 ? kCounterBytes + size_t(p.part_rows) * (size_t(head_dim) + 2) * 4u : 0;
     return p;
 }

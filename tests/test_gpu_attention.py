@@ -67,6 +67,14 @@ def make(B, Lq, Lk, Hq, Hk, D, seed=0):
     return q, k, v
 
 
+@pytest.fixture(params=["few", "many", "auto"])
+def kernel(request, monkeypatch):
+    """Each of the two kernels in turn, and the one that the library takes."""
+    if request.param != "auto":
+        monkeypatch.setenv("LOWBIT_ATTENTION", request.param)
+    return request.param
+
+
 def scratch(q, k, v):
     n = lb.attention_workspace_size(q, k, v)
     ws = torch.full((n,), 0xAB, dtype=torch.uint8, device="cuda")
@@ -83,7 +91,7 @@ SHAPES = [  # B, Lq, Lk, Hq, Hk, D
 
 @pytest.mark.parametrize("shape", SHAPES)
 @pytest.mark.parametrize("causal", [False, True])
-def test_shapes(shape, causal):
+def test_shapes(shape, causal, kernel):
     B, Lq, Lk = shape[:3]
     q, k, v = make(*shape)
     start = torch.full((B,), Lk - Lq, dtype=torch.int32, device="cuda") if causal else None
@@ -94,7 +102,7 @@ def test_shapes(shape, causal):
 
 @pytest.mark.parametrize("shape", [(2, 1, 777, 8, 2, 128), (3, 70, 70, 4, 4, 64), (2, 200, 333, 2, 2, 128), (4, 1, 64, 4, 4, 64)])
 @pytest.mark.parametrize("causal", [False, True])
-def test_masks_lengths_and_empty_rows(shape, causal):
+def test_masks_lengths_and_empty_rows(shape, causal, kernel):
     B, Lq, Lk, Hq, Hk, D = shape
     q, k, v = make(*shape, seed=1)
     g = torch.Generator().manual_seed(2)
@@ -116,7 +124,7 @@ def test_masks_lengths_and_empty_rows(shape, causal):
 
 
 @pytest.mark.parametrize("lens", [[0, 0], [-3, 1], [1, 500], [64, 65]])
-def test_lengths_out_of_range_and_short(lens):
+def test_lengths_out_of_range_and_short(lens, kernel):
     q, k, v = make(2, 3, 100, 4, 2, 128, seed=3)
     n = torch.tensor(lens, dtype=torch.int32).cuda()
     check(lb.attention(q, k, v, key_lens=n), *reference(q, k, v, lens=n))
@@ -124,7 +132,7 @@ def test_lengths_out_of_range_and_short(lens):
 
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), torch.finfo(torch.bfloat16).min])
-def test_anything_in_places_that_are_left_out(bad, D):
+def test_anything_in_places_that_are_left_out(bad, D, kernel):
     """Padding in the middle and past the length holds infinities, NaN or the type's lowest value."""
     q, k, v = make(2, 90, 200, 4, 2, D, seed=4)
     mask = torch.ones(2, 200, dtype=torch.bool)
@@ -145,7 +153,7 @@ def test_anything_in_places_that_are_left_out(bad, D):
 
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
-def test_later_keys_do_not_reach_earlier_queries(bad, D):
+def test_later_keys_do_not_reach_earlier_queries(bad, D, kernel):
     """Causal: a value that is no number at key j leaves queries before j alone and reaches the others."""
     q, k, v = make(1, 150, 150, 2, 2, D, seed=5)
     want = lb.attention(q, k, v, causal=True)
@@ -161,7 +169,7 @@ def test_later_keys_do_not_reach_earlier_queries(bad, D):
     assert torch.equal(got[0, :70], want[0, :70]) and bool(torch.isnan(got[0, 70:, 0]).all())
 
 
-def test_large_scores_and_growing_maxima():
+def test_large_scores_and_growing_maxima(kernel):
     """Scores that grow along the keys (the running maximum moves at every tile) and reach thousands."""
     q, k, v = make(1, 40, 1000, 2, 2, 128, seed=6)
     k = (k.float() * torch.linspace(0.1, 4, 1000, device="cuda")[None, :, None, None]).bfloat16()
@@ -174,7 +182,7 @@ def test_large_scores_and_growing_maxima():
     assert (off <= 2.0 ** -8 * np.abs(want) + (2.0 ** -8 + 2.0 ** -5) * mag + 1e-6).all()
 
 
-def test_views_of_a_fused_projection_and_other_layouts():
+def test_views_of_a_fused_projection_and_other_layouts(kernel):
     g = torch.Generator().manual_seed(7)
     B, L, Hq, Hk, D = 2, 77, 6, 2, 128
     qkv = torch.randn(B, L, Hq + 2 * Hk, D, generator=g).bfloat16().cuda()
@@ -192,7 +200,7 @@ def test_views_of_a_fused_projection_and_other_layouts():
     check(lb.attention(q, k, v, key_mask=mask), *reference(q, k, v, mask))
 
 
-def test_scale_and_empty_calls():
+def test_scale_and_empty_calls(kernel):
     q, k, v = make(1, 20, 50, 2, 2, 64, seed=8)
     check(lb.attention(q, k, v, scale=0.01), *reference(q, k, v, scale=0.01))
     assert not bool(lb.attention(q, k[:, :0], v[:, :0]).any())
@@ -200,7 +208,7 @@ def test_scale_and_empty_calls():
     assert lb.attention(q[:0], k[:0], v[:0]).shape == (0, 20, 2, 64)
 
 
-def test_offsets_past_32_bits():
+def test_offsets_past_32_bits(kernel):
     """A cache whose tokens lie 2^25 bytes apart: the last ones start past 2^32 bytes."""
     n, step = 200, 1 << 24
     g = torch.Generator().manual_seed(9)
@@ -214,7 +222,7 @@ def test_offsets_past_32_bits():
     assert torch.equal(lb.attention(q, k, v), lb.attention(q, k.contiguous(), v.contiguous()))
 
 
-def test_runs_repeat_bitwise_and_on_another_stream():
+def test_runs_repeat_bitwise_and_on_another_stream(kernel):
     q, k, v = make(1, 3, 6000, 16, 4, 128, seed=10)
     ws = scratch(q, k, v)
     want = lb.attention(q, k, v, workspace=ws)
@@ -228,7 +236,7 @@ def test_runs_repeat_bitwise_and_on_another_stream():
     assert torch.equal(got, want)
 
 
-def test_counters_are_left_at_zero_and_shapes_take_turns():
+def test_counters_are_left_at_zero_and_shapes_take_turns(kernel):
     calls = [make(*shape, seed=20 + i) for i, shape in enumerate([(1, 1, 9000, 8, 2, 128), (4, 2, 1500, 16, 4, 64), (2, 40, 4000, 2, 2, 128)])]
     ws = torch.zeros(max(lb.attention_workspace_size(*c) for c in calls), dtype=torch.uint8, device="cuda")
     first = [lb.attention(*c, workspace=ws) for c in calls]
@@ -239,7 +247,7 @@ def test_counters_are_left_at_zero_and_shapes_take_turns():
             check(got, *reference(*c))
 
 
-def test_in_a_graph():
+def test_in_a_graph(kernel):
     q, k, v = make(1, 2, 3000, 8, 8, 64, seed=11)
     ws = scratch(q, k, v)
     out = torch.empty_like(q)
