@@ -775,10 +775,28 @@ __global__ __launch_bounds__(256, 2) void attention_short_kernel(AttnArgs a) {
     __syncthreads();
     if (!last_split) return;
     if (threadIdx.x == 0) __hip_atomic_store(&a.counters[group_of], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    // every row's factors (kMaxShortSplits of them at most), then its columns
+    // (row, 4 columns) per thread, with the splits in `parts` ranges where threads are left over; kAhead loads in
+    // flight, the first of them while the rows' factors are worked out
+    constexpr int kAhead = 16;
+    const int items = rows * (D / 4);
+    int parts = 1;
+    while (parts < 4 && 2 * parts * items <= 64 * kWaves) parts *= 2;
+    const int span = (a.splits + parts - 1) / parts;
+    f32x4_t u[kAhead];
+    auto fetch = [&](int i, int s0, int s1) __attribute__((always_inline)) {
+        const int item = i % items;
+        const uint32_t at = (uint32_t(item / (D / 4)) * (D + 2) + 4u * uint32_t(item % (D / 4))) * 4u;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)  // a split past the range reads as zeros
+            u[j] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                   part_rs, s0 + j < s1 ? uint32_t((s0 + j) * rows) * (D + 2) * 4u + at : 0xFFFFFF00u, 0, kSc1));
+    };
+    auto range_end = [&](int part) { return (part + 1) * span < a.splits ? (part + 1) * span : a.splits; };
+    const int mine_i = int(threadIdx.x);
+    if (mine_i < items * parts) fetch(mine_i, mine_i / items * span, range_end(mine_i / items));
     float* const factors = reinterpret_cast<float*>(tiles_lds);  // [rows][splits], then the sums [rows]
     float* const totals = factors + rows * a.splits;
-    for (int row = wave; row < rows; row += kWaves) {  // a lane per split
+    for (int row = wave; row < rows; row += kWaves) {  // a lane per split (kMaxShortSplits at most)
         const uint32_t at = (uint32_t(lane * rows + row) * (D + 2) + D) * 4u;
         const bool in = lane < a.splits;
         const float mc = in ? __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(part_rs, at, 0, kSc1)) : kNegInf;
@@ -794,25 +812,14 @@ __global__ __launch_bounds__(256, 2) void attention_short_kernel(AttnArgs a) {
         if (lane == 0) totals[row] = sum;
     }
     __syncthreads();
-    // (row, 4 columns) per thread, with the splits in `parts` ranges where threads are left over; kAhead loads in flight
-    constexpr int kAhead = 16;
-    const int items = rows * (D / 4);
-    int parts = 1;
-    while (parts < 4 && 2 * parts * items <= 64 * kWaves) parts *= 2;
-    const int span = (a.splits + parts - 1) / parts;
-    f32x4_t* const sums = reinterpret_cast<f32x4_t*>(tiles_lds[2]);  // [parts][items], read by the first range's threads
-    for (int i = int(threadIdx.x); i < items * parts; i += 64 * kWaves) {
+    f32x4_t* const sums = reinterpret_cast<f32x4_t*>(tiles_lds[2]);  // [parts][items]
+    for (int i = mine_i; i < items * parts; i += 64 * kWaves) {
         const int part = i / items, item = i - part * items;
         const int row = item / (D / 4), col = 4 * (item % (D / 4));
-        const int s1 = (part + 1) * span < a.splits ? (part + 1) * span : a.splits;
+        const int s1 = range_end(part);
         f32x4_t v = {0.f, 0.f, 0.f, 0.f};
         for (int s0 = part * span; s0 < s1; s0 += kAhead) {
-            f32x4_t u[kAhead];
-#pragma unroll
-            for (int j = 0; j < kAhead; ++j)  // a split past the range reads as zeros
-                u[j] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                                       part_rs, s0 + j < s1 ? (uint32_t((s0 + j) * rows + row) * (D + 2) + uint32_t(col)) * 4u : 0xFFFFFF00u,
-                                                       0, kSc1));
+            if (i != mine_i || s0 != part * span) fetch(i, s0, s1);
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
                 const float fac = s0 + j < s1 ? factors[row * a.splits + s0 + j] : 0.f;
@@ -898,7 +905,7 @@ constexpr size_t kCounterBytes = 4096;  // at the workspace's start: arrival cou
 // 512 x 512, 32 / 8 heads of 128: 14 / 29; 1024 x 1024, 24 heads of 128: 32 / 39; 2048 x 2048, 8 heads of 128:
 // 31 / 44; 128 x 32768, 8 heads of 128: 58 / 67; past the bound 1536 x 1536, 24 heads of 128: 61 / 52, and 2 x
 // 1533 x 1533, 16 heads of 64: 37 / 35.  One row block (16 or 32 rows) always takes it.
-//   Keys are split until every compute unit has a workgroup (few rows: 256 workgroups of four tiles a wave at least;
+//   Keys are split until every compute unit has a workgroup (few rows: 256 workgroups of three tiles a wave at least;
 // 512 were slower at 1024 rows, 27 against 17 us, and at 40007 keys, 33 against 32); the other
 // kernel, until there are two per compute unit, each with four tiles at least.
 //   LOWBIT_ATTENTION=few|many in the environment forces the kernel (A/B runs and tests).
@@ -915,7 +922,7 @@ AttnPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t k
         const int64_t heads = batch * kv_heads * p.row_tiles;
         tiles = tiles_of(kv_len, kShortKeys);
         splits = heads >= kComputeUnits ? 1 : kComputeUnits / heads;
-        splits = splits < tiles / 16 ? splits : tiles / 16;
+        splits = splits < tiles / 12 ? splits : tiles / 12;
         splits = splits < kMaxShortSplits ? splits : kMaxShortSplits;
         p.splits = splits < 1 ? 1 : int(splits);
         p.tiles_per_split = 0;
