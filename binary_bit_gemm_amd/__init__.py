@@ -490,7 +490,8 @@ def gemm_lora(x, words, scales, g: int, bits: int, lora_a, lora_b, alpha, rows, 
     (lowbit_gemm_lora): low-rank adapters of many requests beside one packed weight.  lora_a bf16 [adapters, rank, K],
     lora_b bf16 [adapters, N, rank], alpha fp32 [adapters], rows int32 [M] (-1: no adapter).
 
-    `workspace`: a device tensor of at least lora_workspace_size(M, rank) bytes, allocated for the call if None."""
+    `workspace`: a device tensor of at least lora_workspace_size(M, rank) bytes, zero-filled before its first use (reuse
+    it between calls; do not share it between calls that run concurrently); allocated for the call if None."""
     torch = _torch()
     bf16 = torch.bfloat16
     _require(x, bf16, "x")
@@ -516,7 +517,7 @@ def gemm_lora(x, words, scales, g: int, bits: int, lora_a, lora_b, alpha, rows, 
     out = _output(out, (M, N), x)
     po = _plain(out, bf16, "out", 2, x)
     if workspace is None:
-        workspace = torch.empty(lora_workspace_size(M, rank), dtype=torch.uint8, device=x.device)
+        workspace = torch.zeros(lora_workspace_size(M, rank), dtype=torch.uint8, device=x.device)
     ws, nbytes = _workspace(workspace, x)
     _call("lowbit_gemm_lora", x, px, pw, ps, po, M, N, K, g, bits, pa, pb, pl, pr, E, rank, ws, nbytes)
     return out

@@ -895,7 +895,6 @@ hipError_t launch_d(const AttnArgs& a, bool is_short, hipStream_t stream) {
 }
 
 constexpr int kMaxShortSplits = 64;     // a lane per split in the join
-constexpr size_t kCounterBytes = 4096;  // at the workspace's start: arrival counters, zero between calls
 
 }  // namespace
 
@@ -938,7 +937,7 @@ AttnPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t k
     }
     const int64_t padded = p.is_short ? int64_t(p.row_tiles) * (rows <= 16 ? 16 : 32) : rows;
     p.part_rows = p.splits > 1 ? batch * kv_heads * padded * p.splits : 0;
-    p.bytes = p.splits > 1 ? kCounterBytes + size_t(p.part_rows) * (size_t(head_dim) + 2) * 4u : 0;
+    p.bytes = p.splits > 1 ? kWorkspaceCounterBytes + size_t(p.part_rows) * (size_t(head_dim) + 2) * 4u : 0;
     return p;
 }
 
@@ -955,7 +954,7 @@ hipError_t launch_attention(AttnArgs a, int head_dim, const AttnPlan& plan, void
     a.splits = plan.splits;
     a.tiles_per_split = plan.tiles_per_split;
     a.counters = static_cast<uint32_t*>(workspace);
-    a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kCounterBytes);
+    a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kWorkspaceCounterBytes);
     a.part_ml = a.part + plan.part_rows * head_dim;
     return head_dim == 64 ? launch_d<64>(a, plan.is_short, stream) : launch_d<128>(a, plan.is_short, stream);
 }

@@ -99,7 +99,6 @@ int attention_args(const lowbit_attention_problem* p, lowbit::AttnArgs& a) {
 }
 
 constexpr int64_t kMaxAdapters = 1 << 16;
-constexpr size_t kCounterBytes = 4096;  // of a workspace, for the calls that split sums
 
 bool lora_rank_ok(int64_t rank) { return rank >= 8 && rank <= 128 && rank % 8 == 0; }
 
@@ -109,7 +108,7 @@ extern "C" {
 
 size_t lowbit_lora_workspace_size(int64_t M, int rank) {
     if (M <= 0 || M > kMaxDim || !lora_rank_ok(rank)) return 0;
-    return kCounterBytes + ((size_t(M) * size_t(rank) * 4u + 255u) & ~size_t(255));
+    return lowbit::lora_workspace_bytes(M, rank);
 }
 
 int lowbit_gemm_lora(const void* X, const uint32_t* W, const void* S, void* Y, int64_t M, int64_t N, int64_t K, int g,
@@ -131,14 +130,25 @@ int lowbit_gemm_lora(const void* X, const uint32_t* W, const void* S, void* Y, i
     st = lowbit::device_check();
     if (st != LOWBIT_OK) return st;
     const hipStream_t s = static_cast<hipStream_t>(stream);
-    const lowbit::ShrinkArgs sh{static_cast<const uint16_t*>(X), static_cast<const uint16_t*>(A), alpha, rows,
-                                reinterpret_cast<uint16_t*>(static_cast<unsigned char*>(workspace) + kCounterBytes), int(M), int(K), int(adapters), rank};
-    hipError_t e = lowbit::launch_lora_shrink(sh, s);
+    lowbit::ShrinkArgs sh{};
+    sh.X = static_cast<const uint16_t*>(X);
+    sh.A = static_cast<const uint16_t*>(A);
+    sh.alpha = alpha;
+    sh.rows = rows;
+    sh.M = int(M);
+    sh.K = int(K);
+    sh.adapters = int(adapters);
+    sh.rank = rank;
+    hipError_t e = lowbit::launch_lora_shrink(sh, workspace, s);
     if (e != hipSuccess) return lowbit::hip_fail(e);
-    const lowbit::LoraArgs la{sh.u, static_cast<const uint16_t*>(B), rows, int(adapters), rank};
+    const lowbit::LoraArgs la{lowbit::lora_u(workspace), static_cast<const uint16_t*>(B), rows, int(adapters), rank};
     const lowbit::GemmProblem p{static_cast<const uint16_t*>(X), W, static_cast<const uint16_t*>(S),
                                 static_cast<uint16_t*>(Y), int(M), int(N), int(K)};
-    e = lowbit::launch_gemm_tile16_lora(p, g, bits, la, s);
+    // few rows: the kernels that lowbit_gemm takes for them, where they cover the shape
+    e = hipErrorNotSupported;
+    if (bits == 2 && M <= 16 && N / 16 >= 512) e = lowbit::launch_gemm_resident_epilogue(p, g, lowbit::kEpiLora, s, &la);
+    if (e == hipErrorNotSupported && lowbit::use_skinny(M, N, K, g, bits)) e = lowbit::launch_gemm_skinny_group(&p, 1, g, bits, s, &la);
+    if (e == hipErrorNotSupported) e = lowbit::launch_gemm_tile16_lora(p, g, bits, la, s);
     return e == hipSuccess ? LOWBIT_OK : lowbit::hip_fail(e);
 }
 

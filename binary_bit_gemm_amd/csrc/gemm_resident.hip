@@ -29,6 +29,7 @@
 #include <cstdio>
 #include <cstdlib>
 
+#include "lora_device.h"
 #include "lowbit_device.h"
 #include "lowbit_internal.h"
 
@@ -76,6 +77,7 @@ struct ResidentArgs {
     int tiles;            // tiles of the launch
     float* ws;            // [tiles][splits][cb][64][4] fp32 partial sums (splits > 1)
     uint32_t* counters;   // [tiles] arrival counters, zero between calls (splits > 1)
+    LoraArgs lora;        // adapters (kEpiLora)
 };
 
 // 4-byte direct-to-LDS copy: lane i's 4 bytes land at lds_wave_base + 4 * i.
@@ -88,7 +90,8 @@ __device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t rs, void* lds_wave_b
 // Y[M, N] = silu(X . Wgate^T) * (X . Wup^T).  A workgroup's CB (even) column blocks are then CB / 2
 // gate blocks and the up blocks of the same output columns; after the K-slice reduction the up
 // sums reach the gate blocks' waves through LDS.  EPI = kEpiResidual: Y = R + gate[n] * (X . W^T)
-// (Y may be R: each element is read and written by the same lane).  Both: whole K only (one split).
+// (Y may be R: each element is read and written by the same lane).  EPI = kEpiLora: the adapters' term is
+// added to the sums.  All three: whole K only (one split).
 template <int G, int LEN, int EPI = kEpiPlain>
 __global__ __launch_bounds__(64 * kMaxWaves, 1) void gemm_resident_kernel(ResidentArgs a) {
     constexpr bool SWIGLU = EPI == kEpiSwiglu;
@@ -294,11 +297,14 @@ __global__ __launch_bounds__(64 * kMaxWaves, 1) void gemm_resident_kernel(Reside
     if (S == 1) {
         if (ks == 0 && active) {
             const float gt = EPI == kEpiResidual ? static_cast<float>(__builtin_bit_cast(__bf16, p.gate[col])) : 0.f;
+            f32x4_t term = {0.f, 0.f, 0.f, 0.f};
+            if constexpr (EPI == kEpiLora) term = lora_term16(a.lora, M, N, 0, cb * 16);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int m = 4 * q + e;
                 if (m < M) {
                     float v = 0.5f * acc[e];  // operand holds 2c
+                    if constexpr (EPI == kEpiLora) v += term[e];
                     if constexpr (EPI == kEpiResidual)
                         v = __builtin_fmaf(gt, v, static_cast<float>(__builtin_bit_cast(__bf16, p.R[int64_t(m) * N + col])));
                     p.Y[int64_t(m) * N + col] = float_to_bf16_bits(v);
@@ -382,7 +388,8 @@ hipError_t launch_cfg(const ResidentArgs& a, uint32_t lds, hipStream_t stream) {
     if (e == hipSuccess && trace_enabled()) {
         char cfg[96];
         snprintf(cfg, sizeof cfg, "column_blocks=%d k_slices=%d steps=%d splits=%d tiles=%d epi=%s", a.cb, a.ks, LEN,
-                 a.splits, a.tiles, EPI == kEpiSwiglu ? "swiglu" : EPI == kEpiResidual ? "residual" : "plain");
+                 a.splits, a.tiles,
+                 EPI == kEpiSwiglu ? "swiglu" : EPI == kEpiResidual ? "residual" : EPI == kEpiLora ? "lora" : "plain");
         trace_launch("resident", cfg, G, 2, a.grp.p, a.grp.count, unsigned(a.tiles * a.splits), 64u * a.cb * a.ks, lds);
     }
     return e;
@@ -550,12 +557,12 @@ hipError_t launch_gemm_resident_group(const GemmProblem* probs, int count, int g
 // Fused epilogues, whole K only; hipErrorNotSupported where no plan fits (the caller then takes
 // the tile kernel).  SwiGLU (gate rows [0, N), up rows [N, 2N) of W and S; Y is [M, N]): the
 // workgroups hold an even number of column blocks -- half gate, half the up blocks of the same
-// output columns -- enough that the pairs fill one round over the compute units.  Residual: the
-// plain whole-K plan.
-hipError_t launch_gemm_resident_epilogue(const GemmProblem& p, int g, int epi, hipStream_t stream) {
+// output columns -- enough that the pairs fill one round over the compute units.  Residual and
+// adapters: the plain whole-K plan.
+hipError_t launch_gemm_resident_epilogue(const GemmProblem& p, int g, int epi, hipStream_t stream, const LoraArgs* lora) {
     const bool swiglu = epi == kEpiSwiglu;
     const int64_t w_rows = swiglu ? 2 * int64_t(p.N) : p.N;
-    if (!resident_supported(p.M, w_rows, p.K, g, 2) || (epi != kEpiSwiglu && epi != kEpiResidual))
+    if (!resident_supported(p.M, w_rows, p.K, g, 2) || (epi != kEpiSwiglu && epi != kEpiResidual && (epi != kEpiLora || lora == nullptr)))
         return hipErrorNotSupported;
     const int T = p.K / kStepCodes;
     const int64_t out_blocks = p.N / 16;
@@ -579,6 +586,10 @@ hipError_t launch_gemm_resident_epilogue(const GemmProblem& p, int g, int epi, h
     uint32_t lds = lds_bytes(T, g, cb);
     const uint32_t red = uint32_t(cb * ks) * 1024u;  // the K-slice reduction reuses the LDS
     lds = lds > red ? lds : red;
+    if (epi == kEpiLora) {
+        a.lora = *lora;
+        return g == 64 ? launch_g<64, kEpiLora>(a, lds, len, stream) : launch_g<128, kEpiLora>(a, lds, len, stream);
+    }
     if (swiglu) return g == 64 ? launch_g<64, kEpiSwiglu>(a, lds, len, stream) : launch_g<128, kEpiSwiglu>(a, lds, len, stream);
     return g == 64 ? launch_g<64, kEpiResidual>(a, lds, len, stream) : launch_g<128, kEpiResidual>(a, lds, len, stream);
 }

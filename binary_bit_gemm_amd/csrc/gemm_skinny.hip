@@ -27,7 +27,9 @@
 // Weight Representation: 1-bit g128"); the operand holds 2c (ternary) or -2c (binary) and
 // the factor +-1/2 is applied once to the final sum.
 #include <cstdlib>
+#include <type_traits>
 
+#include "lora_device.h"
 #include "lowbit_device.h"
 #include "lowbit_internal.h"
 
@@ -44,8 +46,11 @@ struct SkinnyFmt {
     static constexpr int XPS = 4 * MPC;             // activation operands per step and row block
 };
 
-template <int BITS, int G, int MB, int NCB, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, 2) void gemm_skinny_kernel(ProblemGroup grp) {
+struct NoLora {};
+
+// LORA: low-rank adapters' term added to the sums (one problem per launch).
+template <int BITS, int G, int MB, int NCB, int WAVES, bool LORA>
+__global__ __launch_bounds__(64 * WAVES, 2) void gemm_skinny_kernel(ProblemGroup grp, std::conditional_t<LORA, LoraArgs, NoLora> la) {
     using F = SkinnyFmt<BITS>;
     constexpr int GPS = F::STEP / G;                      // scale groups per step
     constexpr bool kSplitChunk = F::CHUNK > G;            // groups smaller than a chunk
@@ -309,15 +314,22 @@ __global__ __launch_bounds__(64 * WAVES, 2) void gemm_skinny_kernel(ProblemGroup
         // 16x16 MFMA result layout: lane l holds column l % 16, rows 4 * (l / 16) + i.
         const int col = n0 + 16 * cb + (l & 15);
 #pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] *= code_scale;
+        if constexpr (LORA) {  // a wave's 64 threads share cb and mb
+            const f32x4_t term = lora_term16(la, M, N, 16 * mb, n0 + 16 * cb);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += term[i];
+        }
+#pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int m = 16 * mb + 4 * (l >> 4) + i;
-            if (m < M) p.Y[int64_t(m) * N + col] = float_to_bf16_bits(v[i] * code_scale);
+            if (m < M) p.Y[int64_t(m) * N + col] = float_to_bf16_bits(v[i]);
         }
     }
 }
 
 template <int BITS, int G, int MB, int NCB>
-hipError_t launch_cfg(const GemmProblem* probs, int count, hipStream_t stream) {
+hipError_t launch_cfg(const GemmProblem* probs, int count, const LoraArgs* lora, hipStream_t stream) {
     constexpr int WAVES = 4;
     ProblemGroup grp{};
     int total = 0;
@@ -327,11 +339,20 @@ hipError_t launch_cfg(const GemmProblem* probs, int count, hipStream_t stream) {
         grp.tile_end[i] = total;
     }
     grp.count = count;
-    hipLaunchKernelGGL((gemm_skinny_kernel<BITS, G, MB, NCB, WAVES>), dim3(total), dim3(64 * WAVES), 0, stream, grp);
+    if (lora != nullptr) {
+        if constexpr (G != 32)
+            hipLaunchKernelGGL((gemm_skinny_kernel<BITS, G, MB, NCB, WAVES, true>), dim3(total), dim3(64 * WAVES), 0, stream,
+                               grp, *lora);
+        else
+            return hipErrorNotSupported;
+    } else {
+        hipLaunchKernelGGL((gemm_skinny_kernel<BITS, G, MB, NCB, WAVES, false>), dim3(total), dim3(64 * WAVES), 0, stream,
+                           grp, NoLora{});
+    }
     const hipError_t e = hipGetLastError();
     if (e == hipSuccess && trace_enabled()) {
         char cfg[64];
-        snprintf(cfg, sizeof cfg, "row_blocks=%d column_blocks=%d waves=%d", MB, NCB, WAVES);
+        snprintf(cfg, sizeof cfg, "row_blocks=%d column_blocks=%d waves=%d%s", MB, NCB, WAVES, lora ? " epi=lora" : "");
         trace_launch("skinny", cfg, G, BITS, probs, count, unsigned(total), 64u * WAVES, 0u);
     }
     return e;
@@ -341,23 +362,23 @@ hipError_t launch_cfg(const GemmProblem* probs, int count, hipStream_t stream) {
 // ternary codes, two for binary codes (twice the activation operands per step), one for two
 // row blocks and for binary codes with groups of 32 (four masked operand copies per chunk).
 template <int BITS, int G, int MB>
-hipError_t launch_mb(const GemmProblem* probs, int count, int ncb, hipStream_t stream) {
+hipError_t launch_mb(const GemmProblem* probs, int count, int ncb, const LoraArgs* lora, hipStream_t stream) {
     if constexpr (MB == 1 && BITS == 2) {
-        if (ncb >= 4) return launch_cfg<BITS, G, MB, 4>(probs, count, stream);
+        if (ncb >= 4) return launch_cfg<BITS, G, MB, 4>(probs, count, lora, stream);
     }
     if constexpr (MB == 1 && !(BITS == 1 && G == 32)) {
-        if (ncb >= 2) return launch_cfg<BITS, G, MB, 2>(probs, count, stream);
+        if (ncb >= 2) return launch_cfg<BITS, G, MB, 2>(probs, count, lora, stream);
     }
-    return launch_cfg<BITS, G, MB, 1>(probs, count, stream);
+    return launch_cfg<BITS, G, MB, 1>(probs, count, lora, stream);
 }
 
 template <int BITS, int G>
-hipError_t launch_bits_g(const GemmProblem* probs, int count, int max_m, int ncb, hipStream_t stream) {
+hipError_t launch_bits_g(const GemmProblem* probs, int count, int max_m, int ncb, const LoraArgs* lora, hipStream_t stream) {
     if constexpr (BITS == 1) {
-        return launch_mb<BITS, G, 1>(probs, count, ncb, stream);
+        return launch_mb<BITS, G, 1>(probs, count, ncb, lora, stream);
     } else {
-        return max_m <= 16 ? launch_mb<BITS, G, 1>(probs, count, ncb, stream)
-                           : launch_mb<BITS, G, 2>(probs, count, ncb, stream);
+        return max_m <= 16 ? launch_mb<BITS, G, 1>(probs, count, ncb, lora, stream)
+                           : launch_mb<BITS, G, 2>(probs, count, ncb, lora, stream);
     }
 }
 
@@ -398,21 +419,21 @@ bool use_skinny(int64_t M, int64_t N, int64_t K, int g, int bits) {
     return M <= (bits == 2 ? 32 : 16) && skinny_supported(g, bits) && K % step == 0;
 }
 
-hipError_t launch_gemm_skinny_group(const GemmProblem* probs, int count, int g, int bits, hipStream_t stream) {
+hipError_t launch_gemm_skinny_group(const GemmProblem* probs, int count, int g, int bits, hipStream_t stream, const LoraArgs* lora) {
     int max_m = 0;
     for (int i = 0; i < count; ++i) max_m = probs[i].M > max_m ? probs[i].M : max_m;
     const int ncb = pick_ncb(probs, count);
     if (bits == 2) {
         switch (g) {
-            case 32: return launch_bits_g<2, 32>(probs, count, max_m, ncb, stream);
-            case 64: return launch_bits_g<2, 64>(probs, count, max_m, ncb, stream);
-            default: return launch_bits_g<2, 128>(probs, count, max_m, ncb, stream);
+            case 32: return launch_bits_g<2, 32>(probs, count, max_m, ncb, lora, stream);
+            case 64: return launch_bits_g<2, 64>(probs, count, max_m, ncb, lora, stream);
+            default: return launch_bits_g<2, 128>(probs, count, max_m, ncb, lora, stream);
         }
     }
     switch (g) {
-        case 32: return launch_bits_g<1, 32>(probs, count, max_m, ncb, stream);
-        case 64: return launch_bits_g<1, 64>(probs, count, max_m, ncb, stream);
-        default: return launch_bits_g<1, 128>(probs, count, max_m, ncb, stream);
+        case 32: return launch_bits_g<1, 32>(probs, count, max_m, ncb, lora, stream);
+        case 64: return launch_bits_g<1, 64>(probs, count, max_m, ncb, lora, stream);
+        default: return launch_bits_g<1, 128>(probs, count, max_m, ncb, lora, stream);
     }
 }
 

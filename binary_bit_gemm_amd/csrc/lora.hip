@@ -2,121 +2,203 @@
 // row m, with X [M, K] bf16, A [adapters, rank, K] bf16 and alpha fp32.  The second product (U B_e^T) is where the packed GEMM's
 // sums start (lora_device.h).
 //
-// A workgroup takes 16 rows and one of the adapters among them (the j-th smallest; a workgroup whose j
-// is past the last one leaves at once), so rows of many requests cost more workgroups, not a longer one.
-// Its waves split K; every wave multiplies 16x16x32 blocks straight from global memory (16
-// bytes per lane: 64 consecutive bytes of each of 16 rows of X and of A per instruction), and the waves'
-// fp32 sums are added in wave order through LDS, scaled, and stored as hi + lo bf16 pairs.
-#include <type_traits>
-
+// A workgroup takes 16 rows, one of the adapters among them (the j-th smallest; a workgroup whose j is past
+// the last one leaves at once) and a range of K; rows of many requests cost more workgroups, not a
+// longer one.  Its waves take steps of 128 of K in turn.  A step's pieces of the 16 rows of X and the rank
+// rows of A, 256 bytes a row, are copied into the wave's part of LDS (four whole rows per instruction: loads straight into
+// operand registers would touch 16 rows each, and took 26 us where this takes 10: 509 rows, K = 9216,
+// rank 32) and multiplied in 16x16x32 blocks.  The waves' fp32 sums are added in wave order; where K is
+// split across workgroups (few rows, long K) each leaves its sums in the workspace and the last to arrive adds
+// them in order.  U is stored as hi + lo bf16 pairs.
 #include "lowbit_device.h"
 #include "lowbit_internal.h"
 
 namespace lowbit {
 namespace {
 
-constexpr int kWaves = 8;
+constexpr int kStepK = 128;             // of K per wave and step
+constexpr int kBlock = 16 * kStepK * 2;  // bytes of 16 rows' pieces: 4 KB
+constexpr int kMaxCounters = 1024;
 
-template <int RB>
-__global__ __launch_bounds__(64 * kWaves) void lora_shrink_kernel(ShrinkArgs a) {
-    __shared__ f32x4_t red[kWaves][RB][64];
+// Chunk c (16 bytes) of row r of a 16-row block sits at position c ^ r: the 16 rows that an operand read
+// touches at one chunk then lie in 16 different bank groups.
+__device__ __forceinline__ int chunk_of(int ks, int q) { return 8 * (ks / 2) + 4 * (q >> 1) + (q & 1) + 2 * (ks % 2); }
+
+__device__ __forceinline__ int min_of_16_lanes(int v) {
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2) {
+        const int o = __shfl_xor(v, d);
+        v = o < v ? o : v;
+    }
+    return __builtin_amdgcn_readfirstlane(v);
+}
+
+// RB: blocks of 16 of the rank (the last may be half used).
+template <int RB, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(ShrinkArgs a) {
+    __shared__ __attribute__((aligned(1024))) unsigned char lds[WAVES][(1 + RB) * kBlock];
+    __shared__ int last_split;
     const int lane = int(threadIdx.x) & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
     const int q = lane >> 4, l16 = lane & 15;
     const int64_t row0 = int64_t(blockIdx.x) * 16;
-    const int64_t m = row0 + l16;
-    int id = m < a.M ? a.rows[m] : -1;
+    const int have = a.M - row0 < 16 ? int(a.M - row0) : 16;
+    int id = l16 < have ? a.rows[row0 + l16] : -1;
     id = id >= 0 && id < a.adapters ? id : -1;
-    // the blockIdx.y-th adapter of the 16 rows
-    int cur = -1;
+    int cur = -1;  // the blockIdx.y-th adapter of the 16 rows
     for (int j = 0; j <= int(blockIdx.y); ++j) {
-        int next = id > cur ? id : 0x7FFFFFFF;
-#pragma unroll
-        for (int d = 1; d < 16; d *= 2) {
-            const int o = __shfl_xor(next, d);
-            next = o < next ? o : next;
-        }
-        next = __builtin_amdgcn_readfirstlane(next);
-        if (next == 0x7FFFFFFF) return;  // the same in every wave
-        cur = next;
+        cur = min_of_16_lanes(id > cur ? id : 0x7FFFFFFF);
+        if (cur == 0x7FFFFFFF) return;  // the same in every wave and every split
     }
-    const int steps = a.K / 32;
-    const int s0 = wave * steps / kWaves, s1 = (wave + 1) * steps / kWaves;
-    const bool mine = id == cur;
-    const uint16_t* x = a.X + (mine ? m : row0) * int64_t(a.K) + 8 * q;
-    const uint16_t* w[RB];
-    bool live[RB];
+    const uint32_t row_bytes = uint32_t(a.K) * 2u;
+    const int steps = (a.K + kStepK - 1) / kStepK;
+    const int s0 = int(int64_t(steps) * blockIdx.z / a.splits), s1 = int(int64_t(steps) * (blockIdx.z + 1) / a.splits);
+    const auto x_rs = make_rsrc(a.X + row0 * a.K, uint32_t(have) * row_bytes);
+    const auto a_rs = make_rsrc(a.A + int64_t(cur) * a.rank * a.K, uint32_t(a.rank) * row_bytes);  // rows past the rank: zeros
+    // copy i of a block brings rows 4 i + lane / 16; X's rows of other adapters come as zeros
+    constexpr uint32_t kNone = 0xFFFFFF00u;
+    uint32_t off[4];
+    bool mine[4];
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-        const int r = 16 * rb + l16;
-        live[rb] = r < a.rank;
-        w[rb] = a.A + (int64_t(cur) * a.rank + (live[rb] ? r : 0)) * int64_t(a.K) + 8 * q;
+    for (int i = 0; i < 4; ++i) {
+        const int r = 4 * i + q;
+        off[i] = uint32_t(r) * row_bytes + uint32_t(l16 ^ r) * 16u;
+        mine[i] = __shfl(id, r) == cur;
     }
+    unsigned char* const at = lds[wave];
+    int rd[4];
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) rd[ks] = l16 * (kStepK * 2) + ((chunk_of(ks, q) ^ l16) << 4);
     f32x4_t acc[RB];
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) acc[rb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    // kAhead steps' operands are loaded before the first is used
-    constexpr int kAhead = RB >= 8 ? 2 : 4;
-    auto steps_of = [&](int s, auto count) __attribute__((always_inline)) {
-        constexpr int n = decltype(count)::value;
-        bf16x8_t xf[n], wf[n][RB];
+    for (int s = s0 + wave; s < s1; s += WAVES) {
+        const uint32_t k0 = uint32_t(s) * (kStepK * 2u);
+        const uint32_t left = row_bytes - k0;  // of a row; the last step may have half its columns
 #pragma unroll
-        for (int j = 0; j < n; ++j) {
-            xf[j] = *reinterpret_cast<const bf16x8_t*>(x + 32 * int64_t(s + j));
+        for (int i = 0; i < 4; ++i) {
+            const bool in = uint32_t(l16 ^ (4 * i + q)) * 16u < left;
+            dma16(x_rs, at + i * 1024, in && mine[i] ? off[i] + k0 : kNone, 0);
 #pragma unroll
-            for (int rb = 0; rb < RB; ++rb) wf[j][rb] = *reinterpret_cast<const bf16x8_t*>(w[rb] + 32 * int64_t(s + j));
+            for (int rb = 0; rb < RB; ++rb)
+                dma16(a_rs, at + (1 + rb) * kBlock + i * 1024, in ? off[i] + k0 + uint32_t(16 * rb) * row_bytes : kNone, 0);
         }
+        wait_vmcnt<0>();
+        asm volatile("" ::: "memory");
 #pragma unroll
-        for (int j = 0; j < n; ++j)
+        for (int ks = 0; ks < 4; ++ks) {
+            const bf16x8_t xf = *reinterpret_cast<const bf16x8_t*>(at + rd[ks]);
 #pragma unroll
-            for (int rb = 0; rb < RB; ++rb) acc[rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[j], wf[j][rb], acc[rb], 0, 0, 0);
-    };
-    int s = s0;
-    for (; s + kAhead <= s1; s += kAhead) steps_of(s, std::integral_constant<int, kAhead>{});
-    for (; s < s1; ++s) steps_of(s, std::integral_constant<int, 1>{});
+            for (int rb = 0; rb < RB; ++rb)
+                acc[rb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                    xf, *reinterpret_cast<const bf16x8_t*>(at + (1 + rb) * kBlock + rd[ks]), acc[rb], 0, 0, 0);
+        }
+        // the step's reads are done before the next copies may land
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+        asm volatile("" ::: "memory");
+    }
+    // ---- the waves' sums, in wave order (each wave's in its own part of LDS: no copy is in flight) ----
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) red[wave][rb][lane] = acc[rb];
+    for (int rb = 0; rb < RB; ++rb) reinterpret_cast<f32x4_t*>(at)[rb * 64 + lane] = acc[rb];
     __syncthreads();
-    for (int rb = wave; rb < RB; rb += kWaves) {
-        f32x4_t v = red[0][rb][lane];
-#pragma unroll
-        for (int k = 1; k < kWaves; ++k) {
-            const f32x4_t o = red[k][rb][lane];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] += o[i];
-        }
+    const int group = int(blockIdx.x) * int(gridDim.y) + int(blockIdx.y);
+    constexpr int kSc1 = 16;  // through to the device-coherent level: other workgroups' caches are elsewhere
+    const auto part_rs = make_rsrc(a.part + int64_t(group) * a.splits * (RB * 256), a.splits > 1 ? uint32_t(a.splits) * (RB * 1024u) : 0u);
+    auto store = [&](int rb, f32x4_t v) __attribute__((always_inline)) {
         const int r = 16 * rb + l16;
         const float alpha = a.alpha[cur];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t row = row0 + 4 * q + i;
             const int owner = __shfl(id, 4 * q + i);
             if (owner == cur && r < a.rank) {
                 const float u = v[i] * alpha;
                 const __bf16 hi = static_cast<__bf16>(u);
                 const float h = static_cast<float>(hi);
                 const bool fine = __builtin_fabsf(h) < __builtin_inff();  // an infinity's rest would be a NaN
-                uint16_t* dst = a.u + row * (2 * a.rank) + r;
+                uint16_t* dst = a.u + (row0 + 4 * q + i) * (2 * a.rank) + r;
                 dst[0] = __builtin_bit_cast(uint16_t, hi);
                 dst[a.rank] = fine ? float_to_bf16_bits(u - h) : uint16_t(0);
             }
         }
+    };
+    for (int rb = wave; rb < RB; rb += WAVES) {
+        f32x4_t v = reinterpret_cast<const f32x4_t*>(lds[0])[rb * 64 + lane];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) {
+            const f32x4_t o = reinterpret_cast<const f32x4_t*>(lds[w])[rb * 64 + lane];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += o[i];
+        }
+        if (a.splits == 1)
+            store(rb, v);
+        else
+            __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u32x4_t, v), part_rs,
+                                                   (uint32_t(blockIdx.z) * RB + uint32_t(rb)) * 1024u + uint32_t(lane) * 16u, 0, kSc1);
     }
+    if (a.splits == 1) return;
+    // ---- the splits' sums: the last to arrive adds them in order ----
+    wait_vmcnt<0>();  // this one's sums are there before the arrival counts
+    __syncthreads();
+    if (threadIdx.x == 0)
+        last_split = __hip_atomic_fetch_add(&a.counters[group], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == uint32_t(a.splits - 1);
+    __syncthreads();
+    if (!last_split) return;
+    if (threadIdx.x == 0) __hip_atomic_store(&a.counters[group], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    for (int rb = wave; rb < RB; rb += WAVES) {
+        u32x4_t part[kMaxShrinkSplits];
+#pragma unroll
+        for (int z = 0; z < kMaxShrinkSplits; ++z)  // a split past the last reads as zeros
+            part[z] = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                      part_rs, (uint32_t(z) * RB + uint32_t(rb)) * 1024u + uint32_t(lane) * 16u, 0, kSc1));
+        f32x4_t v = __builtin_bit_cast(f32x4_t, part[0]);
+#pragma unroll
+        for (int z = 1; z < kMaxShrinkSplits; ++z) {
+            const f32x4_t o = __builtin_bit_cast(f32x4_t, part[z]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] += o[i];
+        }
+        store(rb, v);
+    }
+}
+
+int rank_blocks(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
+
+int slots_of(int64_t adapters) { return adapters < 16 ? int(adapters) : 16; }
+
+// K is split where the row tiles leave compute units idle and a workgroup would read more than 256 KB (about
+// 50 KB a microsecond arrive at a compute unit; the join costs 3 to 4 us): into pieces of 128 KB.
+int shrink_splits(int64_t M, int64_t K, int64_t adapters, int rank) {
+    const int64_t tiles = tiles_of(M, 16), bytes = (16 + int64_t(rank)) * K * 2;
+    if (bytes <= 256 * 1024 || tiles * slots_of(adapters) > kMaxCounters || 2 * tiles > kComputeUnits) return 1;
+    int64_t s = tiles_of(bytes, 128 * 1024);
+    s = s < kComputeUnits / tiles ? s : kComputeUnits / tiles;
+    return int(s < kMaxShrinkSplits ? s : kMaxShrinkSplits);
 }
 
 }  // namespace
 
-hipError_t launch_lora_shrink(const ShrinkArgs& a, hipStream_t stream) {
-    const dim3 grid(unsigned(tiles_of(a.M, 16)), unsigned(a.adapters < 16 ? a.adapters : 16));
-    const int rb = (a.rank + 15) / 16;
-    if (rb <= 1)
-        hipLaunchKernelGGL(lora_shrink_kernel<1>, grid, dim3(64 * kWaves), 0, stream, a);
-    else if (rb <= 2)
-        hipLaunchKernelGGL(lora_shrink_kernel<2>, grid, dim3(64 * kWaves), 0, stream, a);
-    else if (rb <= 4)
-        hipLaunchKernelGGL(lora_shrink_kernel<4>, grid, dim3(64 * kWaves), 0, stream, a);
-    else
-        hipLaunchKernelGGL(lora_shrink_kernel<8>, grid, dim3(64 * kWaves), 0, stream, a);
+// The fp32 sums of the splits lie behind U; their place is kept for every call that could split.
+size_t lora_u_bytes(int64_t M, int rank) { return (size_t(M) * size_t(rank) * 4u + 255u) & ~size_t(255); }
+size_t lora_workspace_bytes(int64_t M, int rank) {
+    const int64_t tiles = tiles_of(M, 16);
+    const int64_t most = tiles * kMaxShrinkSplits < kComputeUnits ? tiles * kMaxShrinkSplits : kComputeUnits;  // tiles x splits
+    const size_t parts = 2 * tiles > kComputeUnits ? 0 : size_t(most) * 16 * size_t(rank_blocks(rank)) * 1024u;
+    return kWorkspaceCounterBytes + lora_u_bytes(M, rank) + parts;
+}
+
+hipError_t launch_lora_shrink(ShrinkArgs a, void* workspace, hipStream_t stream) {
+    unsigned char* const base = static_cast<unsigned char*>(workspace);
+    a.counters = reinterpret_cast<uint32_t*>(base);
+    a.u = reinterpret_cast<uint16_t*>(base + kWorkspaceCounterBytes);
+    a.part = reinterpret_cast<float*>(base + kWorkspaceCounterBytes + lora_u_bytes(a.M, a.rank));
+    a.splits = shrink_splits(a.M, a.K, a.adapters, a.rank);
+    const dim3 grid(unsigned(tiles_of(a.M, 16)), unsigned(slots_of(a.adapters)), unsigned(a.splits));
+    switch (rank_blocks(a.rank)) {
+        case 1: hipLaunchKernelGGL((lora_shrink_kernel<1, 8>), grid, dim3(512), 0, stream, a); break;
+        case 2: hipLaunchKernelGGL((lora_shrink_kernel<2, 8>), grid, dim3(512), 0, stream, a); break;
+        case 4: hipLaunchKernelGGL((lora_shrink_kernel<4, 4>), grid, dim3(256), 0, stream, a); break;
+        default: hipLaunchKernelGGL((lora_shrink_kernel<8, 4>), grid, dim3(256), 0, stream, a); break;
+    }
     return hipGetLastError();
 }
 

@@ -13,6 +13,23 @@
 
 namespace lowbit {
 
+// Smallest of the 16 lanes' values of a lane quarter whose quarters are alike.
+__device__ __forceinline__ int min_of_16(int v) {
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2) {
+        const int o = __shfl_xor(v, d);
+        v = o < v ? o : v;
+    }
+    return __builtin_amdgcn_readfirstlane(v);
+}
+
+__device__ __forceinline__ bool all_finite(u32x4_t v) {
+    bool fine = true;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) fine = fine && (v[e] & 0x7F80u) != 0x7F80u && (v[e] & 0x7F800000u) != 0x7F800000u;
+    return fine;
+}
+
 // acc[mb][nb], in the layout of 16x16 MFMA results (lane (q, l16): column l16, rows 4q + i), becomes GAIN times
 // the adapters' term of rows row0 + 16 mb .. and output columns col0 + 16 nb .. (GAIN: the factor that some
 // kernels' code operands carry until their epilogue).
@@ -21,10 +38,8 @@ namespace lowbit {
 // places, hi then lo, against B's rank columns taken twice: the adapter's term is exact to fp32
 // sums of bf16 products, for one more matrix instruction per 16 of rank and block.
 //
-// Rows of one request (the ordinary case: a wave's rows have one adapter, or none) load all operands of a step
-// at once.  Mixed rows go block by block and adapter by adapter.  Requests must not touch each other:
-// rows of other adapters are left out of a product by a zero operand and, since zero times
-// another request's infinity or NaN is a NaN, by dropping their result as well.
+// Rows of one request (the ordinary case: a wave's rows have one adapter, or none) go straight through.  Mixed rows
+// take a turn per adapter, the smallest first, in which rows of others enter as zeros.
 template <int GAIN, int MB, int NB>
 __device__ __forceinline__ void lora_init(f32x4_t (&acc)[MB][NB], const LoraArgs& la, int M, int N, int row0, int col0) {
     int lane = int(threadIdx.x) & 63;
@@ -60,85 +75,103 @@ __device__ __forceinline__ void lora_init(f32x4_t (&acc)[MB][NB], const LoraArgs
     };
     const int b_block = 32 * la.rank;  // bytes of 16 rows of B
 
-    bool one = true;
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb) one = one && id[mb] == id[0];
-    const int first = __builtin_amdgcn_readfirstlane(id[0]);
     const int steps = (2 * chunks + 3) / 4;
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    if (__all(one && id[0] == first)) {
+    // one adapter's step ks: its products added to the sums
+    auto step = [&](__amdgpu_buffer_rsrc_t rs, int e, int ks) __attribute__((always_inline)) {
+        bf16x8_t bf[NB];
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) bf[nb] = load(rs, b_off(ks), nb * b_block);
+        const uint32_t uo = u_off(ks);
+        // kAhead row blocks' operands in flight at a time: what the sums leave room for
+        constexpr int kAhead = 5;
+#pragma unroll
+        for (int m0 = 0; m0 < MB; m0 += kAhead) {
+            bf16x8_t uf[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+                if (m0 + j < MB) uf[j] = load(u_rs, id[m0 + j] == e ? uo : kNone, (m0 + j) * 16 * int(u_row));
+            __builtin_amdgcn_sched_barrier(0);  // or the loads sink to their uses, and each is waited for
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb)
+                    if (m0 + j < MB)
+                        acc[m0 + j][nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(uf[j], bf[nb], acc[m0 + j][nb], 0, 0, 0);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        uint32_t odd = 0;
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) odd |= all_finite(__builtin_bit_cast(u32x4_t, bf[nb])) ? 0u : 1u;
+        return odd;
+    };
+    bool one = true;
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) one = one && id[mb] == id[0];
+    const int first = __builtin_amdgcn_readfirstlane(id[0]);
+    if (__all(one && id[0] == first)) {  // the ordinary case: one request's rows
         if (first < 0) return;
         const auto rs = b_rsrc(first);
-        auto run = [&](auto count) __attribute__((always_inline)) {
+        step(rs, first, 0);
+        if (steps > 1) step(rs, first, 1);
+        if (steps > 2) {
+            step(rs, first, 2);
+            step(rs, first, 3);  // past the rank: zeros
+        }
+        if (steps > 4) {
+            step(rs, first, 4);
+            step(rs, first, 5);
+            step(rs, first, 6);
+            step(rs, first, 7);
+        }
+    } else {
+        // A turn per adapter.  An infinity or a NaN in an adapter's B makes NaN of the other rows' zeros: it is noticed, and
+        // the block-by-block form below, which drops other rows' results, takes over from the start.
+        uint32_t odd = 0;
+        for (int cur = -1;;) {
+            int next = 0x7FFFFFFF;  // the wave's next adapter
 #pragma unroll
-            for (int ks = 0; ks < decltype(count)::value; ++ks) {
-                bf16x8_t bf[NB];
+            for (int mb = 0; mb < MB; ++mb) next = id[mb] > cur && id[mb] < next ? id[mb] : next;
+            next = min_of_16(next);
+            if (next == 0x7FFFFFFF) break;
+            cur = next;
+            const auto rs = b_rsrc(cur);
+#pragma nounroll
+            for (int ks = 0; ks < steps; ++ks) odd |= step(rs, cur, ks);
+        }
+        if (__any(odd != 0)) {
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) bf[nb] = load(rs, b_off(ks), nb * b_block);
-                // kAhead row blocks' operands in flight at a time: what the sums leave room for
-                constexpr int kAhead = 5;
+            for (int mb = 0; mb < MB; ++mb) {
+                f32x4_t sum[NB];
 #pragma unroll
-                for (int m0 = 0; m0 < MB; m0 += kAhead) {
-                    bf16x8_t uf[kAhead];
+                for (int nb = 0; nb < NB; ++nb) sum[nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                for (int cur = -1;;) {
+                    const int next = min_of_16(id[mb] > cur ? id[mb] : 0x7FFFFFFF);  // the block's next adapter
+                    if (next == 0x7FFFFFFF) break;
+                    cur = next;
+                    const auto rs = b_rsrc(cur);
+                    f32x4_t t[NB];
 #pragma unroll
-                    for (int j = 0; j < kAhead; ++j)
-                        if (m0 + j < MB) uf[j] = load(u_rs, u_off(ks), (m0 + j) * 16 * int(u_row));
-#pragma unroll
-                    for (int j = 0; j < kAhead; ++j)
+                    for (int nb = 0; nb < NB; ++nb) t[nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+                    for (int ks = 0; ks < steps; ++ks) {
+                        const bf16x8_t uf = load(u_rs, id[mb] == cur ? u_off(ks) : kNone, mb * 16 * int(u_row));
 #pragma unroll
                         for (int nb = 0; nb < NB; ++nb)
-                            if (m0 + j < MB)
-                                acc[m0 + j][nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(uf[j], bf[nb], acc[m0 + j][nb], 0, 0, 0);
-                    __builtin_amdgcn_sched_barrier(0);
+                            t[nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(uf, load(rs, b_off(ks), nb * b_block), t[nb], 0, 0, 0);
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool mine = __shfl(id[mb], 4 * q + i) == cur;
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) sum[nb][i] = mine ? t[nb][i] : sum[nb][i];
+                    }
                 }
+#pragma unroll
+                for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = sum[nb];
             }
-        };
-        if (steps <= 1)
-            run(std::integral_constant<int, 1>{});
-        else if (steps <= 2)
-            run(std::integral_constant<int, 2>{});
-        else if (steps <= 4)
-            run(std::integral_constant<int, 4>{});
-        else
-            run(std::integral_constant<int, 8>{});
-    } else {
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb) {
-            f32x4_t sum[NB];
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) sum[nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-            for (int cur = -1;;) {
-                int next = id[mb] > cur ? id[mb] : 0x7FFFFFFF;  // the block's next adapter
-#pragma unroll
-                for (int d = 1; d < 16; d *= 2) {
-                    const int o = __shfl_xor(next, d);
-                    next = o < next ? o : next;
-                }
-                next = __builtin_amdgcn_readfirstlane(next);
-                if (next == 0x7FFFFFFF) break;
-                cur = next;
-                const auto rs = b_rsrc(cur);
-                f32x4_t t[NB];
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) t[nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-                for (int ks = 0; ks < steps; ++ks) {
-                    const bf16x8_t uf = load(u_rs, id[mb] == cur ? u_off(ks) : kNone, mb * 16 * int(u_row));
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-                        t[nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(uf, load(rs, b_off(ks), nb * b_block), t[nb], 0, 0, 0);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bool mine = __shfl(id[mb], 4 * q + i) == cur;
-#pragma unroll
-                    for (int nb = 0; nb < NB; ++nb) sum[nb][i] = mine ? t[nb][i] : sum[nb][i];
-                }
-            }
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = sum[nb];
         }
     }
     if constexpr (GAIN != 1) {
@@ -149,6 +182,62 @@ __device__ __forceinline__ void lora_init(f32x4_t (&acc)[MB][NB], const LoraArgs
 #pragma unroll
                 for (int i = 0; i < 4; ++i) acc[mb][nb][i] *= float(GAIN);
     }
+}
+
+// The adapters' term of one 16x16 block (rows row0 .., columns col0 .. below N), for the kernels of few rows, where
+// each row may well belong to a request of its own.  Mixed rows take a turn each, with the loads of eight
+// turns in flight; a turn's product has one row that is not zero, and only that row of the result is
+// kept, so requests cannot touch each other.
+__device__ __forceinline__ f32x4_t lora_term16(const LoraArgs& la, int M, int N, int row0, int col0) {
+    const int lane = int(threadIdx.x) & 63;
+    const int q = lane >> 4, l16 = lane & 15;
+    const int have = M - row0 < 16 ? M - row0 : 16;
+    const int e = l16 < have ? la.rows[row0 + l16] : -1;
+    const int id = e >= 0 && e < la.adapters ? e : -1;
+    const int chunks = la.rank / 8, steps = (2 * chunks + 3) / 4;
+    const uint32_t u_row = uint32_t(la.rank) * 4u;
+    const auto u_rs = make_rsrc(la.u + int64_t(row0) * (2 * la.rank), uint32_t(have) * u_row);
+    constexpr uint32_t kNone = 0xFFF00000u;  // past every range: reads as zero
+    // 16 rows of B of adapter `ad`; none (an empty range) for -1
+    auto b_load = [&](int ad, uint32_t off) __attribute__((always_inline)) {
+        const auto rs = make_rsrc(la.b + (int64_t(ad < 0 ? 0 : ad) * N + col0) * la.rank, ad < 0 ? 0u : 32u * uint32_t(la.rank));
+        return __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0);
+    };
+    const int first = __builtin_amdgcn_readfirstlane(id);
+    const bool one = __all(id == first);
+    f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
+    if (one && first < 0) return sum;
+    for (int ks = 0; ks < steps; ++ks) {
+        const int c = 4 * ks + q;  // the lane's chunk of the 2 rank places
+        const bool in = c < 2 * chunks;
+        const u32x4_t uf = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                           u_rs, in && id >= 0 ? uint32_t(l16) * u_row + uint32_t(c) * 16u : kNone, 0, 0));
+        const uint32_t b_off = in ? uint32_t(l16 * chunks + (c < chunks ? c : c - chunks)) * 16u : kNone;
+        if (one) {
+            sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, uf), __builtin_bit_cast(bf16x8_t, b_load(first, b_off)),
+                                                          sum, 0, 0, 0);
+            continue;
+        }
+#pragma unroll
+        for (int r0 = 0; r0 < 16; r0 += 8) {
+            if (r0 >= have) break;
+            bf16x8_t bf[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                bf[j] = __builtin_bit_cast(bf16x8_t, b_load(__builtin_amdgcn_readlane(id, r0 + j), b_off));
+            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int r = r0 + j;
+                u32x4_t row;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) row[i] = l16 == r ? uf[i] : 0u;
+                const f32x4_t t = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, row), bf[j], f32x4_t{0.f, 0.f, 0.f, 0.f}, 0, 0, 0);
+                sum[r % 4] += q == r / 4 ? t[r % 4] : 0.f;
+            }
+        }
+    }
+    return sum;
 }
 
 }  // namespace lowbit

@@ -33,15 +33,25 @@ struct LoraArgs {
     const int32_t* rows;
     int adapters, rank;
 };
-// The first product, U = alpha_e A_e X[m] (lora.hip).
+// The first product, U = alpha_e A_e X[m] (lora.hip), at lora_u(workspace).
+constexpr size_t kWorkspaceCounterBytes = 4096;  // at a workspace's start: arrival counters, zero between calls
+constexpr int kMaxShrinkSplits = 8;
 struct ShrinkArgs {
     const uint16_t *X, *A;  // bf16 [M, K], [adapters, rank, K]
     const float* alpha;     // [adapters]
     const int32_t* rows;
-    uint16_t* u;
     int M, K, adapters, rank;
+    // set by the launch
+    uint16_t* u;
+    int splits;          // workgroups along K
+    uint32_t* counters;  // [row tiles x adapters of a tile] arrivals (splits > 1)
+    float* part;         // their fp32 sums
 };
-hipError_t launch_lora_shrink(const ShrinkArgs& a, hipStream_t stream);
+size_t lora_workspace_bytes(int64_t M, int rank);
+inline const uint16_t* lora_u(const void* workspace) {
+    return reinterpret_cast<const uint16_t*>(static_cast<const unsigned char*>(workspace) + kWorkspaceCounterBytes);
+}
+hipError_t launch_lora_shrink(ShrinkArgs a, void* workspace, hipStream_t stream);
 
 // Tiles of `b` rows or columns over a dimension of n (64-bit: M may be up to 2^31 - 1).
 inline int64_t tiles_of(int64_t n, int64_t b) { return (n + b - 1) / b; }
@@ -124,7 +134,8 @@ bool resident_preferred(const GemmProblem* probs, int count, int g, bool may_spl
 hipError_t launch_gemm_resident_group(const GemmProblem* probs, int count, int g, const ResidentPlan& plan,
                                       void* workspace, hipStream_t stream);
 // Fused epilogues on the resident kernel (whole K); hipErrorNotSupported where no plan applies.
-hipError_t launch_gemm_resident_epilogue(const GemmProblem& p, int g, int epi, hipStream_t stream);
+hipError_t launch_gemm_resident_epilogue(const GemmProblem& p, int g, int epi, hipStream_t stream,
+                                         const LoraArgs* lora = nullptr);
 
 // Grouped launch: problems of one (g, bits) class; one launch per kernel family and per
 // kMaxGroup problems.
@@ -133,7 +144,9 @@ hipError_t launch_gemm_grouped(const GemmProblem* probs, int count, int g, int b
 size_t grouped_workspace_bytes(const GemmProblem* probs, int count, int g, int bits);
 hipError_t launch_gemm_tiled_group(const GemmProblem* probs, int count, int g, int bits, int variant,
                                    hipStream_t stream);
-hipError_t launch_gemm_skinny_group(const GemmProblem* probs, int count, int g, int bits, hipStream_t stream);
+// lora: low-rank adapters of the one problem (g = 64 or 128).
+hipError_t launch_gemm_skinny_group(const GemmProblem* probs, int count, int g, int bits, hipStream_t stream,
+                                    const LoraArgs* lora = nullptr);
 
 // Tile for a group of problems: fewest estimated rounds x tile work over the whole group.
 // tile16_only: among the tiles of the 16x16-block kernel.

@@ -320,8 +320,9 @@ int lowbit_gemm_affine_ex(const void* X, const uint32_t* W, const void* S, const
  *      means none.  Rows of different adapters do not affect each other, whatever an adapter holds.
  *   rank  a multiple of 8 from 8 to 128 (pad smaller adapters with zeros).
  *   workspace  device memory of lowbit_lora_workspace_size(M, rank) bytes, 16-byte aligned (required: NULL or
- *      too small returns LOWBIT_E_INVALID).  Any content will do; the first 4096 bytes, where calls that
- *      split K or keys keep their counters, are left alone.  Calls that share it must not run concurrently.
+ *      too small returns LOWBIT_E_INVALID), ZERO-FILLED before its first use.  Its first 4096 bytes hold arrival
+ *      counters that every call leaves at zero, as in lowbit_gemm_ex; one workspace serves all such calls
+ *      in turn.  Calls that share it must not run concurrently.
  * Both products are fp32 sums of bf16 products; X . A^T is kept to 16 significant bits between them; Y is rounded
  * to bf16 once.  Deterministic.  A, B and workspace need 16-byte alignment, alpha and rows 4.
  */

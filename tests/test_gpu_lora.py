@@ -127,8 +127,15 @@ def test_workspace_content_and_repeats():
     c = Case(70, 512, 1024, 2, 64, 24, 5, "scattered", seed=6)
     want = c.run()
     ws = torch.full((lb.lora_workspace_size(70, 24),), 0xFF, dtype=torch.uint8, device="cuda")  # NaN patterns
+    ws[:4096] = 0  # the arrival counters
     for _ in range(3):
-        assert torch.equal(c.run(workspace=ws), want)
+        assert torch.equal(c.run(workspace=ws), want) and not bool(ws[:4096].any())
+    long = Case(50, 256, 16384, 2, 64, 64, 3, "scattered", seed=6)  # K split across workgroups
+    ws = torch.zeros(lb.lora_workspace_size(50, 64), dtype=torch.uint8, device="cuda")
+    want = long.run(workspace=ws)
+    long.check(want)
+    for _ in range(3):
+        assert torch.equal(long.run(workspace=ws), want) and not bool(ws[:4096].any())
 
 
 def test_no_adapters_and_empty_calls():
