@@ -29,6 +29,7 @@ bool apart(int64_t tokens, int64_t token, int64_t heads, int64_t head, int64_t d
 
 // The same for [batch, tokens, heads] rows.
 bool apart3(int64_t batch, int64_t batch_stride, int64_t tokens, int64_t token, int64_t heads, int64_t head, int64_t dim) {
+    if (batch == 0 || tokens == 0 || heads == 0) return true;
     int64_t n[3] = {batch, tokens, heads}, st[3] = {batch_stride, token, head};
     for (int i = 0; i < 2; ++i)  // by stride, smallest first
         for (int j = 0; j < 2 - i; ++j)
@@ -63,10 +64,11 @@ int attention_args(const lowbit_attention_problem* p, lowbit::AttnArgs& a) {
                       p->v_head, p->o_batch, p->o_token, p->o_head})
         if (!stride_ok(s)) return LOWBIT_E_INVALID;
     if (p->mask_batch < 0 || p->mask_batch > kMaxStride) return LOWBIT_E_INVALID;
+    if (p->batch == 0 || p->q_len == 0 || p->q_heads == 0) return LOWBIT_OK;  // nothing to do: a.rows stays 0
     if (p->kv_len > 1 && (p->k_token < p->head_dim || p->v_token < p->head_dim)) return LOWBIT_E_INVALID;
     if (p->k_token > kMaxTokenStride || p->v_token > kMaxTokenStride) return LOWBIT_E_UNSUPPORTED;
     if (!apart3(p->batch, p->o_batch, p->q_len, p->o_token, p->q_heads, p->o_head, p->head_dim)) return LOWBIT_E_INVALID;
-    a.group = p->kv_heads > 0 ? p->q_heads / p->kv_heads : 1;
+    a.group = p->q_heads / p->kv_heads;
     const int64_t rows = int64_t(p->q_len) * a.group;
     if (rows > kMaxDim - 128 || (rows + 127) / 128 * p->kv_heads * p->batch > kMaxDim / 64) return LOWBIT_E_UNSUPPORTED;
     a.q_batch = p->q_batch;

@@ -18,7 +18,6 @@ namespace {
 
 constexpr int kStepK = 128;             // of K per wave and step
 constexpr int kBlock = 16 * kStepK * 2;  // bytes of 16 rows' pieces: 4 KB
-constexpr int kMaxCounters = 1024;
 
 // Chunk c (16 bytes) of row r of a 16-row block sits at position c ^ r: the 16 rows that an operand read
 // touches at one chunk then lie in 16 different bank groups.
@@ -166,24 +165,26 @@ int rank_blocks(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 
 int slots_of(int64_t adapters) { return adapters < 16 ? int(adapters) : 16; }
 
 // K is split where the row tiles leave compute units idle and a workgroup would read more than 256 KB (about
-// 50 KB a microsecond arrive at a compute unit; the join costs 3 to 4 us): into pieces of 128 KB.
+// 50 KB a microsecond arrive at a compute unit; the join costs 3 to 4 us): into pieces of 128 KB, and into
+// kMaxParts pieces in all.
+constexpr int kMaxParts = 1024;
 int shrink_splits(int64_t M, int64_t K, int64_t adapters, int rank) {
-    const int64_t tiles = tiles_of(M, 16), bytes = (16 + int64_t(rank)) * K * 2;
-    if (bytes <= 256 * 1024 || tiles * slots_of(adapters) > kMaxCounters || 2 * tiles > kComputeUnits) return 1;
+    const int64_t tiles = tiles_of(M, 16), groups = tiles * slots_of(adapters), bytes = (16 + int64_t(rank)) * K * 2;
+    if (bytes <= 256 * 1024 || 2 * tiles > kComputeUnits || 2 * groups > kMaxParts) return 1;
     int64_t s = tiles_of(bytes, 128 * 1024);
     s = s < kComputeUnits / tiles ? s : kComputeUnits / tiles;
+    s = s < kMaxParts / groups ? s : kMaxParts / groups;
     return int(s < kMaxShrinkSplits ? s : kMaxShrinkSplits);
 }
 
 }  // namespace
 
-// The fp32 sums of the splits lie behind U; their place is kept for every call that could split.
+// The fp32 sums of the splits lie behind U.  Room for them is kept at every M, so that a workspace for
+// some number of rows serves fewer as well.
 size_t lora_u_bytes(int64_t M, int rank) { return (size_t(M) * size_t(rank) * 4u + 255u) & ~size_t(255); }
 size_t lora_workspace_bytes(int64_t M, int rank) {
-    const int64_t tiles = tiles_of(M, 16);
-    const int64_t most = tiles * kMaxShrinkSplits < kComputeUnits ? tiles * kMaxShrinkSplits : kComputeUnits;  // tiles x splits
-    const size_t parts = 2 * tiles > kComputeUnits ? 0 : size_t(most) * 16 * size_t(rank_blocks(rank)) * 1024u;
-    return kWorkspaceCounterBytes + lora_u_bytes(M, rank) + parts;
+    const int64_t most = tiles_of(M, 16) * 16 * kMaxShrinkSplits, parts = most < kMaxParts ? most : kMaxParts;
+    return kWorkspaceCounterBytes + lora_u_bytes(M, rank) + size_t(parts) * size_t(rank_blocks(rank)) * 1024u;
 }
 
 hipError_t launch_lora_shrink(ShrinkArgs a, void* workspace, hipStream_t stream) {

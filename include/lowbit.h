@@ -322,7 +322,7 @@ int lowbit_gemm_affine_ex(const void* X, const uint32_t* W, const void* S, const
  *   workspace  device memory of lowbit_lora_workspace_size(M, rank) bytes, 16-byte aligned (required: NULL or
  *      too small returns LOWBIT_E_INVALID), ZERO-FILLED before its first use.  Its first 4096 bytes hold arrival
  *      counters that every call leaves at zero, as in lowbit_gemm_ex; one workspace serves all such calls
- *      in turn.  Calls that share it must not run concurrently.
+ *      in turn (one for M rows serves fewer rows).  Calls that share it must not run concurrently.
  * Both products are fp32 sums of bf16 products; X . A^T is kept to 16 significant bits between them; Y is rounded
  * to bf16 once.  Deterministic.  A, B and workspace need 16-byte alignment, alpha and rows 4.
  */
