@@ -2,9 +2,9 @@
 // row m, with X [M, K] bf16, A [adapters, rank, K] bf16 and alpha fp32.  The second product (U B_e^T) is where the packed GEMM's
 // sums start (lora_device.h).
 //
-// A workgroup takes 16 rows, one of the adapters among them (the j-th smallest; a workgroup whose j is past
-// the last one leaves at once) and a range of K; rows of many requests cost more workgroups, not a
-// longer one.  Its waves take steps of 128 of K in turn.  A step's pieces of the 16 rows of X and the rank
+// A workgroup takes 16 rows, `stack` of the adapters among them (in ascending order, blockIdx.y counting the groups; one
+// past the last leaves at once), whose rank rows it stacks, and a range of K; rows of many requests cost
+// more workgroups, not a longer one.  Its waves take steps of 128 of K in turn.  A step's pieces of the 16 rows of X and the rank
 // rows of A, 256 bytes a row, are copied into the wave's part of LDS (four whole rows per instruction: loads straight into
 // operand registers would touch 16 rows each, and took 26 us where this takes 10: 509 rows, K = 9216,
 // rank 32) and multiplied in 16x16x32 blocks.  The waves' fp32 sums are added in wave order; where K is
@@ -18,6 +18,7 @@ namespace {
 
 constexpr int kStepK = 128;             // of K per wave and step
 constexpr int kBlock = 16 * kStepK * 2;  // bytes of 16 rows' pieces: 4 KB
+constexpr int kMaxStack = 4;            // adapters of a workgroup
 
 // Chunk c (16 bytes) of row r of a 16-row block sits at position c ^ r: the 16 rows that an operand read
 // touches at one chunk then lie in 16 different bank groups.
@@ -44,25 +45,56 @@ __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(ShrinkArgs a) {
     const int have = a.M - row0 < 16 ? int(a.M - row0) : 16;
     int id = l16 < have ? a.rows[row0 + l16] : -1;
     id = id >= 0 && id < a.adapters ? id : -1;
-    int cur = -1;  // the blockIdx.y-th adapter of the 16 rows
-    for (int j = 0; j <= int(blockIdx.y); ++j) {
+    // the workgroup's adapters: those of the 16 rows from the (blockIdx.y * stack)-th on; the last repeats where there are fewer
+    int cur = -1, list[kMaxStack], mine_at = -1;  // mine_at: where the lane's row finds its adapter
+#pragma unroll
+    for (int j = 0; j < kMaxStack; ++j) list[j] = -1;
+    for (int j = 0; j < int(blockIdx.y) * a.stack; ++j) {
         cur = min_of_16_lanes(id > cur ? id : 0x7FFFFFFF);
         if (cur == 0x7FFFFFFF) return;  // the same in every wave and every split
+    }
+#pragma unroll
+    for (int j = 0; j < kMaxStack; ++j) {
+        if (j >= a.stack) break;
+        const int next = min_of_16_lanes(id > cur ? id : 0x7FFFFFFF);
+        if (next == 0x7FFFFFFF) {
+            if (j == 0) return;
+            break;
+        }
+        cur = next;
+        list[j] = cur;
+        if (id == cur) mine_at = j;
     }
     const uint32_t row_bytes = uint32_t(a.K) * 2u;
     const int steps = (a.K + kStepK - 1) / kStepK;
     const int s0 = int(int64_t(steps) * blockIdx.z / a.splits), s1 = int(int64_t(steps) * (blockIdx.z + 1) / a.splits);
     const auto x_rs = make_rsrc(a.X + row0 * a.K, uint32_t(have) * row_bytes);
-    const auto a_rs = make_rsrc(a.A + int64_t(cur) * a.rank * a.K, uint32_t(a.rank) * row_bytes);  // rows past the rank: zeros
+    // a single adapter from its own 64-bit address (rows past the rank come as zeros), stacked ones by offsets into the
+    // whole table (the host stacks where that is below 4 GiB)
+    const bool stacked = a.stack > 1;
+    const auto a_rs = make_rsrc(a.A + (stacked ? int64_t(0) : int64_t(list[0]) * a.rank * a.K),
+                                (stacked ? uint32_t(a.adapters) : 1u) * uint32_t(a.rank) * row_bytes);
     // copy i of a block brings rows 4 i + lane / 16; X's rows of other adapters come as zeros
     constexpr uint32_t kNone = 0xFFFFFF00u;
-    uint32_t off[4];
-    bool mine[4];
+    uint32_t x_off[4], a_off[RB][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = 4 * i + q;
-        off[i] = uint32_t(r) * row_bytes + uint32_t(l16 ^ r) * 16u;
-        mine[i] = __shfl(id, r) == cur;
+        const uint32_t column = uint32_t(l16 ^ r) * 16u;
+        x_off[i] = __shfl(mine_at, r) >= 0 ? uint32_t(r) * row_bytes + column : kNone;
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) {
+            const int row = 16 * rb + r;
+            if (!stacked) {
+                a_off[rb][i] = row < a.rank ? uint32_t(row) * row_bytes + column : kNone;
+            } else {
+                const int j = row / a.rank;
+                int e = -1;
+#pragma unroll
+                for (int k = 0; k < kMaxStack; ++k) e = j == k && k < a.stack ? list[k] : e;
+                a_off[rb][i] = e >= 0 ? (uint32_t(e) * uint32_t(a.rank) + uint32_t(row - j * a.rank)) * row_bytes + column : kNone;
+            }
+        }
     }
     unsigned char* const at = lds[wave];
     int rd[4];
@@ -77,10 +109,10 @@ __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(ShrinkArgs a) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const bool in = uint32_t(l16 ^ (4 * i + q)) * 16u < left;
-            dma16(x_rs, at + i * 1024, in && mine[i] ? off[i] + k0 : kNone, 0);
+            dma16(x_rs, at + i * 1024, in && x_off[i] != kNone ? x_off[i] + k0 : kNone, 0);
 #pragma unroll
             for (int rb = 0; rb < RB; ++rb)
-                dma16(a_rs, at + (1 + rb) * kBlock + i * 1024, in ? off[i] + k0 + uint32_t(16 * rb) * row_bytes : kNone, 0);
+                dma16(a_rs, at + (1 + rb) * kBlock + i * 1024, in && a_off[rb][i] != kNone ? a_off[rb][i] + k0 : kNone, 0);
         }
         wait_vmcnt<0>();
         asm volatile("" ::: "memory");
@@ -104,12 +136,16 @@ __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(ShrinkArgs a) {
     constexpr int kSc1 = 16;  // through to the device-coherent level: other workgroups' caches are elsewhere
     const auto part_rs = make_rsrc(a.part + int64_t(group) * a.splits * (RB * 256), a.splits > 1 ? uint32_t(a.splits) * (RB * 1024u) : 0u);
     auto store = [&](int rb, f32x4_t v) __attribute__((always_inline)) {
-        const int r = 16 * rb + l16;
-        const float alpha = a.alpha[cur];
+        const int row = 16 * rb + l16, j = stacked ? row / a.rank : 0, r = row - j * a.rank;
+        int adapter = -1;
+#pragma unroll
+        for (int k = 0; k < kMaxStack; ++k) adapter = j == k && k < a.stack ? list[k] : adapter;
+        const bool in = adapter >= 0 && r < a.rank;
+        const float alpha = in ? a.alpha[adapter] : 0.f;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int owner = __shfl(id, 4 * q + i);
-            if (owner == cur && r < a.rank) {
+            if (in && owner == adapter) {
                 const float u = v[i] * alpha;
                 const __bf16 hi = static_cast<__bf16>(u);
                 const float h = static_cast<float>(hi);
@@ -162,14 +198,26 @@ __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(ShrinkArgs a) {
 
 int rank_blocks(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
 
-int slots_of(int64_t adapters) { return adapters < 16 ? int(adapters) : 16; }
+// Adapters that a workgroup stacks: as many as 32 rows of A hold (a second block costs little, and X is read for fewer
+// workgroups) where that leaves a workgroup per compute unit.  1021 rows of 12 interleaved adapters of rank 8: 14 us with one, 9
+// with four.
+int stack_of(int64_t M, int64_t K, int64_t adapters, int rank) {
+    int64_t stack = 32 / rank < 1 ? 1 : 32 / rank;
+    stack = stack < kMaxStack ? stack : kMaxStack;
+    const int64_t among = adapters < 16 ? adapters : 16;  // in 16 rows
+    if (adapters * rank * K * 2 > (int64_t(1) << 32) - 1) return 1;
+    while (stack > 1 && (stack / 2 >= among || tiles_of(M, 16) * tiles_of(among, stack) < kComputeUnits * 3 / 4)) stack /= 2;
+    return int(stack);
+}
+
+int slots_of(int64_t adapters, int stack) { return int(tiles_of(adapters < 16 ? adapters : 16, stack)); }
 
 // K is split where the row tiles leave compute units idle and a workgroup would read more than 256 KB (about
 // 50 KB a microsecond arrive at a compute unit; the join costs 3 to 4 us): into pieces of 128 KB, and into
 // kMaxParts pieces in all.
 constexpr int kMaxParts = 1024;
-int shrink_splits(int64_t M, int64_t K, int64_t adapters, int rank) {
-    const int64_t tiles = tiles_of(M, 16), groups = tiles * slots_of(adapters), bytes = (16 + int64_t(rank)) * K * 2;
+int shrink_splits(int64_t M, int64_t K, int64_t adapters, int rank, int stack) {
+    const int64_t tiles = tiles_of(M, 16), groups = tiles * slots_of(adapters, stack), bytes = (16 + int64_t(rank)) * K * 2;
     if (bytes <= 256 * 1024 || 2 * tiles > kComputeUnits || 2 * groups > kMaxParts) return 1;
     int64_t s = tiles_of(bytes, 128 * 1024);
     s = s < kComputeUnits / tiles ? s : kComputeUnits / tiles;
@@ -184,7 +232,7 @@ int shrink_splits(int64_t M, int64_t K, int64_t adapters, int rank) {
 size_t lora_u_bytes(int64_t M, int rank) { return (size_t(M) * size_t(rank) * 4u + 255u) & ~size_t(255); }
 size_t lora_workspace_bytes(int64_t M, int rank) {
     const int64_t most = tiles_of(M, 16) * 16 * kMaxShrinkSplits, parts = most < kMaxParts ? most : kMaxParts;
-    return kWorkspaceCounterBytes + lora_u_bytes(M, rank) + size_t(parts) * size_t(rank_blocks(rank)) * 1024u;
+    return kWorkspaceCounterBytes + lora_u_bytes(M, rank) + size_t(parts) * size_t(rank_blocks(rank < 32 ? 32 : rank)) * 1024u;
 }
 
 hipError_t launch_lora_shrink(ShrinkArgs a, void* workspace, hipStream_t stream) {
@@ -192,9 +240,10 @@ hipError_t launch_lora_shrink(ShrinkArgs a, void* workspace, hipStream_t stream)
     a.counters = reinterpret_cast<uint32_t*>(base);
     a.u = reinterpret_cast<uint16_t*>(base + kWorkspaceCounterBytes);
     a.part = reinterpret_cast<float*>(base + kWorkspaceCounterBytes + lora_u_bytes(a.M, a.rank));
-    a.splits = shrink_splits(a.M, a.K, a.adapters, a.rank);
-    const dim3 grid(unsigned(tiles_of(a.M, 16)), unsigned(slots_of(a.adapters)), unsigned(a.splits));
-    switch (rank_blocks(a.rank)) {
+    a.stack = stack_of(a.M, a.K, a.adapters, a.rank);
+    a.splits = shrink_splits(a.M, a.K, a.adapters, a.rank, a.stack);
+    const dim3 grid(unsigned(tiles_of(a.M, 16)), unsigned(slots_of(a.adapters, a.stack)), unsigned(a.splits));
+    switch (rank_blocks(a.rank * a.stack)) {
         case 1: hipLaunchKernelGGL((lora_shrink_kernel<1, 8>), grid, dim3(512), 0, stream, a); break;
         case 2: hipLaunchKernelGGL((lora_shrink_kernel<2, 8>), grid, dim3(512), 0, stream, a); break;
         case 4: hipLaunchKernelGGL((lora_shrink_kernel<4, 4>), grid, dim3(256), 0, stream, a); break;

@@ -23,6 +23,12 @@ __device__ __forceinline__ int min_of_16(int v) {
     return __builtin_amdgcn_readfirstlane(v);
 }
 
+__device__ __forceinline__ uint32_t or_of_16(uint32_t v) {
+#pragma unroll
+    for (int d = 1; d < 16; d *= 2) v |= uint32_t(__shfl_xor(int(v), d));
+    return __builtin_amdgcn_readfirstlane(v);
+}
+
 __device__ __forceinline__ bool all_finite(u32x4_t v) {
     bool fine = true;
 #pragma unroll
@@ -39,7 +45,7 @@ __device__ __forceinline__ bool all_finite(u32x4_t v) {
 // sums of bf16 products, for one more matrix instruction per 16 of rank and block.
 //
 // Rows of one request (the ordinary case: a wave's rows have one adapter, or none) go straight through.  Mixed rows
-// take a turn per adapter, the smallest first, in which rows of others enter as zeros.
+// take a turn per adapter, in ascending order, in which rows of others enter as zeros.
 template <int GAIN, int MB, int NB>
 __device__ __forceinline__ void lora_init(f32x4_t (&acc)[MB][NB], const LoraArgs& la, int M, int N, int row0, int col0) {
     int lane = int(threadIdx.x) & 63;
@@ -80,20 +86,20 @@ __device__ __forceinline__ void lora_init(f32x4_t (&acc)[MB][NB], const LoraArgs
     for (int mb = 0; mb < MB; ++mb)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    // one adapter's step ks: its products added to the sums
-    auto step = [&](__amdgpu_buffer_rsrc_t rs, int e, int ks) __attribute__((always_inline)) {
+    // One adapter's step ks, the wave's rows all being its own: the products added to the sums.
+    // kAhead row blocks' operands in flight at a time: what the sums leave room for
+    constexpr int kAhead = 5;
+    auto step = [&](__amdgpu_buffer_rsrc_t rs, int ks) __attribute__((always_inline)) {
         bf16x8_t bf[NB];
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) bf[nb] = load(rs, b_off(ks), nb * b_block);
         const uint32_t uo = u_off(ks);
-        // kAhead row blocks' operands in flight at a time: what the sums leave room for
-        constexpr int kAhead = 5;
 #pragma unroll
         for (int m0 = 0; m0 < MB; m0 += kAhead) {
             bf16x8_t uf[kAhead];
 #pragma unroll
             for (int j = 0; j < kAhead; ++j)
-                if (m0 + j < MB) uf[j] = load(u_rs, id[m0 + j] == e ? uo : kNone, (m0 + j) * 16 * int(u_row));
+                if (m0 + j < MB) uf[j] = load(u_rs, uo, (m0 + j) * 16 * int(u_row));
             __builtin_amdgcn_sched_barrier(0);  // or the loads sink to their uses, and each is waited for
 #pragma unroll
             for (int j = 0; j < kAhead; ++j)
@@ -103,10 +109,6 @@ __device__ __forceinline__ void lora_init(f32x4_t (&acc)[MB][NB], const LoraArgs
                         acc[m0 + j][nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(uf[j], bf[nb], acc[m0 + j][nb], 0, 0, 0);
             __builtin_amdgcn_sched_barrier(0);
         }
-        uint32_t odd = 0;
-#pragma unroll
-        for (int nb = 0; nb < NB; ++nb) odd |= all_finite(__builtin_bit_cast(u32x4_t, bf[nb])) ? 0u : 1u;
-        return odd;
     };
     bool one = true;
 #pragma unroll
@@ -115,32 +117,84 @@ __device__ __forceinline__ void lora_init(f32x4_t (&acc)[MB][NB], const LoraArgs
     if (__all(one && id[0] == first)) {  // the ordinary case: one request's rows
         if (first < 0) return;
         const auto rs = b_rsrc(first);
-        step(rs, first, 0);
-        if (steps > 1) step(rs, first, 1);
+        step(rs, 0);
+        if (steps > 1) step(rs, 1);
         if (steps > 2) {
-            step(rs, first, 2);
-            step(rs, first, 3);  // past the rank: zeros
+            step(rs, 2);
+            step(rs, 3);  // past the rank: zeros
         }
         if (steps > 4) {
-            step(rs, first, 4);
-            step(rs, first, 5);
-            step(rs, first, 6);
-            step(rs, first, 7);
+            step(rs, 4);
+            step(rs, 5);
+            step(rs, 6);
+            step(rs, 7);
         }
     } else {
-        // A turn per adapter.  An infinity or a NaN in an adapter's B makes NaN of the other rows' zeros: it is noticed, and
-        // the block-by-block form below, which drops other rows' results, takes over from the start.
+        // A turn per adapter.  The rows' U operands are loaded once a step and masked per turn; the adapters of the wave
+        // are the bits of a scalar word (64 at a time), and the next turn's part of B is on its way
+        // during a turn.  An infinity or a NaN in it makes NaN of the other rows' zeros: it is noticed, and the
+        // block-by-block form below, which drops other rows' results, takes over from the start.
         uint32_t odd = 0;
-        for (int cur = -1;;) {
-            int next = 0x7FFFFFFF;  // the wave's next adapter
+        for (int base = 0;;) {
+            int lowest = 0x7FFFFFFF;
 #pragma unroll
-            for (int mb = 0; mb < MB; ++mb) next = id[mb] > cur && id[mb] < next ? id[mb] : next;
-            next = min_of_16(next);
-            if (next == 0x7FFFFFFF) break;
-            cur = next;
-            const auto rs = b_rsrc(cur);
+            for (int mb = 0; mb < MB; ++mb) lowest = id[mb] >= base && id[mb] < lowest ? id[mb] : lowest;
+            lowest = min_of_16(lowest);
+            if (lowest == 0x7FFFFFFF) break;
+            base = lowest & ~63;
+            uint32_t lo = 0, hi = 0;
+#pragma unroll
+            for (int mb = 0; mb < MB; ++mb) {
+                const int d = id[mb] - base;
+                lo |= d >= 0 && d < 32 ? 1u << d : 0u;
+                hi |= d >= 32 && d < 64 ? 1u << (d - 32) : 0u;
+            }
+            const uint64_t present = (uint64_t(or_of_16(hi)) << 32) | or_of_16(lo);
 #pragma nounroll
-            for (int ks = 0; ks < steps; ++ks) odd |= step(rs, cur, ks);
+            for (int ks = 0; ks < steps; ++ks) {
+                const uint32_t uo = u_off(ks), bo = b_off(ks);
+                // row blocks in two halves: their operands stay in registers through the turns
+                constexpr int kHalf = (MB + 1) / 2;
+#pragma unroll
+                for (int m0 = 0; m0 < MB; m0 += kHalf) {
+                    u32x4_t uf[kHalf];
+#pragma unroll
+                    for (int j = 0; j < kHalf; ++j)
+                        if (m0 + j < MB) uf[j] = __builtin_bit_cast(u32x4_t, load(u_rs, uo, (m0 + j) * 16 * int(u_row)));
+                    uint64_t left = present;
+                    int cur = base + __builtin_ctzll(left);
+                    bf16x8_t bf[NB];
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb) bf[nb] = load(b_rsrc(cur), bo, nb * b_block);
+#pragma nounroll
+                    for (;;) {
+                        left &= left - 1;
+                        const int next = left != 0 ? base + __builtin_ctzll(left) : cur;
+                        bf16x8_t bn[NB];
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) bn[nb] = load(b_rsrc(next), bo, nb * b_block);
+                        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) odd |= all_finite(__builtin_bit_cast(u32x4_t, bf[nb])) ? 0u : 1u;
+#pragma unroll
+                        for (int j = 0; j < kHalf; ++j) {
+                            if (m0 + j >= MB) continue;
+                            u32x4_t mine;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) mine[i] = id[m0 + j] == cur ? uf[j][i] : 0u;
+#pragma unroll
+                            for (int nb = 0; nb < NB; ++nb)
+                                acc[m0 + j][nb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, mine), bf[nb],
+                                                                                          acc[m0 + j][nb], 0, 0, 0);
+                        }
+                        if (left == 0) break;
+                        cur = next;
+#pragma unroll
+                        for (int nb = 0; nb < NB; ++nb) bf[nb] = bn[nb];
+                    }
+                }
+            }
+            base += 64;
         }
         if (__any(odd != 0)) {
 #pragma unroll

@@ -43,6 +43,7 @@ struct ShrinkArgs {
     int M, K, adapters, rank;
     // set by the launch
     uint16_t* u;
+    int stack;           // adapters of a workgroup
     int splits;          // workgroups along K
     uint32_t* counters;  // [row tiles x adapters of a tile] arrivals (splits > 1)
     float* part;         // their fp32 sums

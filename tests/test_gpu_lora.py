@@ -138,6 +138,15 @@ def test_workspace_content_and_repeats():
         assert torch.equal(long.run(workspace=ws), want) and not bool(ws[:4096].any())
 
 
+@pytest.mark.parametrize("M", [12, 30, 150, 700])
+def test_many_adapters(M):
+    """More adapters than a scalar word has bits, far apart in the table, every row with its own."""
+    c = Case(M, 208, 256, 2, 64, 8, 3000, "one", seed=10)
+    g = torch.Generator().manual_seed(M)
+    c.rows.copy_(torch.randint(-1, 3000, (M,), generator=g, dtype=torch.int32))
+    c.check(c.run())
+
+
 def test_no_adapters_and_empty_calls():
     c = Case(5, 256, 256, 2, 64, 8, 1, "one", seed=7)
     plain = lb.gemm(c.x, c.words, c.scales, 64, 2)
