@@ -480,9 +480,12 @@ def _output(out, shape, like):
     return out
 
 
-def lora_workspace_size(M: int, rank: int) -> int:
-    """Bytes of workspace that gemm_lora needs for M rows (0 for invalid arguments)."""
-    return int(lib().lowbit_lora_workspace_size(M, rank))
+def lora_workspace_size(M: int, rank: int, N: Optional[int] = None, K: Optional[int] = None, g: int = 64, bits: int = 2) -> int:
+    """Bytes of workspace that gemm_lora needs for M rows (0 for invalid arguments); with N and K, the bytes with which it
+    can also split K across workgroups (lowbit_lora_split_workspace_size)."""
+    if N is None or K is None:
+        return int(lib().lowbit_lora_workspace_size(M, rank))
+    return int(lib().lowbit_lora_split_workspace_size(M, N, K, g, bits, rank))
 
 
 def gemm_lora(x, words, scales, g: int, bits: int, lora_a, lora_b, alpha, rows, out=None, workspace=None):

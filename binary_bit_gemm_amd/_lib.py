@@ -29,6 +29,7 @@ SIGNATURES = {
     "lowbit_batched_workspace_size": (ctypes.c_size_t, [_VP, _INT]),
     "lowbit_gemm_batched_ex": (_INT, [_VP, _INT, _VP, ctypes.c_size_t, _VP]),
     "lowbit_lora_workspace_size": (ctypes.c_size_t, [_I64, _INT]),
+    "lowbit_lora_split_workspace_size": (ctypes.c_size_t, [_I64, _I64, _I64, _INT, _INT, _INT]),
     "lowbit_gemm_lora": (_INT, [_VP, _VP, _VP, _VP, _I64, _I64, _I64, _INT, _INT, _VP, _VP, _VP, _VP, _I64, _INT, _VP,
                                 ctypes.c_size_t, _VP]),
     "lowbit_qk_norm_rope": (_INT, [_VP, _VP]),

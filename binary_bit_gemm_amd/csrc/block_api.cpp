@@ -113,6 +113,16 @@ size_t lowbit_lora_workspace_size(int64_t M, int rank) {
     return lowbit::lora_workspace_bytes(M, rank);
 }
 
+size_t lowbit_lora_split_workspace_size(int64_t M, int64_t N, int64_t K, int g, int bits, int rank) {
+    if (M <= 0 || N <= 0 || K <= 0 || !lora_rank_ok(rank) ||
+        lowbit_check_gemm_args(nullptr, nullptr, nullptr, nullptr, 0, N, K, g, bits) != LOWBIT_OK || M > kMaxDim ||
+        !lowbit::tile16_supported(g, bits))
+        return 0;
+    const lowbit::GemmProblem p{nullptr, nullptr, nullptr, nullptr, int(M), int(N), int(K)};
+    const bool few = lowbit::use_skinny(M, N, K, g, bits);  // those kernels split K inside a workgroup
+    return lowbit::lora_workspace_bytes(M, rank) + (few ? 0 : lowbit::lora_split_bytes(p, g, bits));
+}
+
 int lowbit_gemm_lora(const void* X, const uint32_t* W, const void* S, void* Y, int64_t M, int64_t N, int64_t K, int g,
                      int bits, const void* A, const void* B, const float* alpha, const int32_t* rows, int64_t adapters,
                      int rank, void* workspace, size_t workspace_bytes, void* stream) {
@@ -150,7 +160,11 @@ int lowbit_gemm_lora(const void* X, const uint32_t* W, const void* S, void* Y, i
     e = hipErrorNotSupported;
     if (bits == 2 && M <= 16 && N / 16 >= 512) e = lowbit::launch_gemm_resident_epilogue(p, g, lowbit::kEpiLora, s, &la);
     if (e == hipErrorNotSupported && lowbit::use_skinny(M, N, K, g, bits)) e = lowbit::launch_gemm_skinny_group(&p, 1, g, bits, s, &la);
-    if (e == hipErrorNotSupported) e = lowbit::launch_gemm_tile16_lora(p, g, bits, la, s);
+    if (e == hipErrorNotSupported) {
+        const size_t least = lowbit::lora_workspace_bytes(M, rank), sums = lowbit::lora_split_bytes(p, g, bits);
+        void* const at = sums > 0 && workspace_bytes >= least + sums ? static_cast<unsigned char*>(workspace) + least : nullptr;
+        e = lowbit::launch_gemm_tile16_lora(p, g, bits, la, workspace, at, s);
+    }
     return e == hipSuccess ? LOWBIT_OK : lowbit::hip_fail(e);
 }
 

@@ -101,14 +101,15 @@ struct SplitK {
     int splits;
 };
 
-// EPI = kEpiLora: the second argument holds the adapters' operands instead, and the fp32 sums start at
+// EPI = kEpiLora: the second argument holds the adapters' operands (too), and the fp32 sums start at
 // their term.
-template <int EPI>
-using Extra = std::conditional_t<EPI == kEpiLora, LoraArgs, SplitK>;
+struct LoraSplitK : SplitK, LoraArgs {};
+template <int EPI, bool XSPLIT>
+using Extra = std::conditional_t<EPI == kEpiLora, std::conditional_t<XSPLIT, LoraSplitK, LoraArgs>, SplitK>;
 
 template <int G, int BITS, int BM, int BN, int WAVES_M, int WAVES_N, int KSPLIT, int EPI = kEpiPlain,
           bool AFFINE = false, bool XSPLIT = false>
-__global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KSPLIT, 1) void gemm_tile16_kernel(ProblemGroup grp, Extra<EPI> sk) {
+__global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KSPLIT, 1) void gemm_tile16_kernel(ProblemGroup grp, Extra<EPI, XSPLIT> sk) {
     constexpr bool SWIGLU = EPI == kEpiSwiglu;
     static_assert(!AFFINE || (BITS == 4 && EPI == kEpiPlain), "affine groups: 4-bit levels, plain epilogue");
     using C = Cfg16<G, BITS, BM, BN, WAVES_M, WAVES_N>;
@@ -313,7 +314,9 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KSPLIT, 1) void gemm_tile1
 #pragma unroll
             for (int nb = 0; nb < C::NB; ++nb) acc[mb][nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         if constexpr (EPI == kEpiLora) {
-            if (kg == 0) lora_init<1>(acc, sk, M, N, m0 + wm0, n0 + wn0);
+            // K ranges that are added up later: the term belongs to one of them, or a half of it to each of two
+            const bool owner = !XSPLIT || int(blockIdx.x) < total_tiles;
+            if (owner) lora_init<1>(acc, sk, M, N, m0 + wm0, n0 + wn0, KSPLIT == 2 ? kg : -1);
         }
 
         // A step's words and scales are read from LDS before any copy of the step is issued (the
@@ -679,7 +682,8 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KSPLIT, 1) void gemm_tile1
 
 template <int G, int BITS, int BM, int BN, int WAVES_M, int WAVES_N, int KSPLIT = 1, int EPI = kEpiPlain,
           bool AFFINE = false, bool XSPLIT = false>
-hipError_t launch_cfg16(const GemmProblem* probs, int count, hipStream_t stream, Extra<EPI> sk = Extra<EPI>{}) {
+hipError_t launch_cfg16(const GemmProblem* probs, int count, hipStream_t stream,
+                        Extra<EPI, XSPLIT> sk = Extra<EPI, XSPLIT>{}) {
     ProblemGroup grp{};
     int splits = 1;
     if constexpr (XSPLIT) splits = sk.splits;
@@ -765,9 +769,27 @@ hipError_t launch_gemm_tile16_epilogue(const GemmProblem* probs, int count, int 
     return hipErrorInvalidValue;
 }
 
+// K split across kTileSplits workgroups of a 64 x 128 tile: bytes of the splits' fp32 sums, 0 where the tile grid
+// fills the compute units or K is short.  With adapters (509 binary rows at K = 9216, 192 tiles, two of rank 32): 66 us
+// without the split, 59 with it.
+constexpr int kTileSplits = 3;
+size_t tile_split_bytes(const GemmProblem& p) {
+    const int64_t tiles = tiles_of(p.M, 64) * tiles_of(p.N, 128);
+    if (tiles * 4 > int64_t(kComputeUnits) * 3 || tiles > 1024 || p.K / KS < 8 * kTileSplits) return 0;
+    using Cf = Cfg16<64, 4, 64, 128, 1, 4>;
+    return size_t(tiles) * kTileSplits * Cf::WAVES * Cf::MB * Cf::NB * 1024u;
+}
+
 // The adapters' epilogue on the tile that the cost model picks among this kernel's.
 template <int G, int BITS>
-hipError_t launch_lora16(const GemmProblem& p, const LoraArgs& la, hipStream_t stream) {
+hipError_t launch_lora16(const GemmProblem& p, const LoraArgs& la, void* workspace, size_t workspace_bytes, void* sums,
+                         hipStream_t stream) {
+    if (workspace_bytes > 0) {  // the caller's workspace has room for a K split that pays
+        LoraSplitK sk;
+        static_cast<SplitK&>(sk) = SplitK{static_cast<float*>(sums), static_cast<uint32_t*>(workspace), kTileSplits};
+        static_cast<LoraArgs&>(sk) = la;
+        return launch_cfg16<G, BITS, 64, 128, 1, 4, 1, kEpiLora, false, true>(&p, 1, stream, sk);
+    }
     const int variant = pick_tile_variant(&p, 1, G, BITS, true);
     const bool even = (p.K / KS) % 2 == 0;
     if (variant == TILE_64x128K2) return launch_cfg16<G, BITS, 64, 128, 1, 4, 2, kEpiLora>(&p, 1, stream, la);
@@ -778,25 +800,31 @@ hipError_t launch_lora16(const GemmProblem& p, const LoraArgs& la, hipStream_t s
     return launch_cfg16<G, BITS, 288, 192, 2, 6, 1, kEpiLora>(&p, 1, stream, la);
 }
 
-hipError_t launch_gemm_tile16_lora(const GemmProblem& p, int g, int bits, const LoraArgs& la, hipStream_t stream) {
+size_t lora_split_bytes(const GemmProblem& p, int g, int bits) {
+    if (!tile16_supported(g, bits) || pick_tile_variant(&p, 1, g, bits, true) != TILE_64x128K2) return 0;
+    return tile_split_bytes(p);
+}
+
+hipError_t launch_gemm_tile16_lora(const GemmProblem& p, int g, int bits, const LoraArgs& la, void* workspace, void* sums,
+                                   hipStream_t stream) {
     if (!tile16_supported(g, bits)) return hipErrorInvalidValue;
-    if (bits == 2) return g == 64 ? launch_lora16<64, 2>(p, la, stream) : launch_lora16<128, 2>(p, la, stream);
-    if (bits == 4) return g == 64 ? launch_lora16<64, 4>(p, la, stream) : launch_lora16<128, 4>(p, la, stream);
-    return g == 64 ? launch_lora16<64, 1>(p, la, stream) : launch_lora16<128, 1>(p, la, stream);
+    const size_t split = sums != nullptr ? lora_split_bytes(p, g, bits) : 0;
+    if (bits == 2)
+        return g == 64 ? launch_lora16<64, 2>(p, la, workspace, split, sums, stream) : launch_lora16<128, 2>(p, la, workspace, split, sums, stream);
+    if (bits == 4)
+        return g == 64 ? launch_lora16<64, 4>(p, la, workspace, split, sums, stream) : launch_lora16<128, 4>(p, la, workspace, split, sums, stream);
+    return g == 64 ? launch_lora16<64, 1>(p, la, workspace, split, sums, stream) : launch_lora16<128, 1>(p, la, workspace, split, sums, stream);
 }
 
 // Affine 4-bit GEMMs whose 64 x 128 tile grid leaves a quarter of the compute units or more idle
 // (the text encoder's 512 x 2560 down projection: 160 tiles) split K three ways across workgroups
 // through a caller workspace: three 4-wave workgroups of 48 KB LDS share a compute unit, so the
 // 480 workgroups run in one round.  0 where no split applies.
-constexpr int kAffineSplits = 3;
 constexpr size_t kAffineCounterBytes = 4096;  // 1024 tile counters, at the workspace's start
 size_t affine_split_bytes(const GemmProblem& p, int g) {
     if (!tile16_supported(g, 4) || pick_tile_variant(&p, 1, g, 4) != TILE_64x128K2) return 0;
-    const int64_t tiles = tiles_of(p.M, 64) * tiles_of(p.N, 128);
-    if (tiles * 4 > int64_t(kComputeUnits) * 3 || tiles > 1024 || p.K / KS < 8 * kAffineSplits) return 0;
-    using Cf = Cfg16<64, 4, 64, 128, 1, 4>;
-    return kAffineCounterBytes + size_t(tiles) * kAffineSplits * Cf::WAVES * Cf::MB * Cf::NB * 1024u;
+    const size_t sums = tile_split_bytes(p);
+    return sums == 0 ? 0 : kAffineCounterBytes + sums;
 }
 
 size_t affine_workspace_bytes(const GemmProblem& p, int g) { return affine_split_bytes(p, g); }
@@ -806,7 +834,7 @@ hipError_t launch_gemm_tile16_affine_ex(const GemmProblem& p, int g, void* works
     const size_t need = affine_split_bytes(p, g);
     if (need == 0 || workspace == nullptr || workspace_bytes < need) return hipErrorNotSupported;
     SplitK sk{reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kAffineCounterBytes),
-              static_cast<uint32_t*>(workspace), kAffineSplits};
+              static_cast<uint32_t*>(workspace), kTileSplits};
     return g == 64 ? launch_cfg16<64, 4, 64, 128, 1, 4, 1, kEpiPlain, true, true>(&p, 1, stream, sk)
                    : launch_cfg16<128, 4, 64, 128, 1, 4, 1, kEpiPlain, true, true>(&p, 1, stream, sk);
 }

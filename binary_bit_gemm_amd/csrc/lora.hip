@@ -199,7 +199,7 @@ __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(ShrinkArgs a) {
 int rank_blocks(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
 
 // Adapters that a workgroup stacks: as many as 32 rows of A hold (a second block costs little, and X is read for fewer
-// workgroups) where that leaves a workgroup per compute unit.  1021 rows of 12 interleaved adapters of rank 8: 14 us with one, 9
+// workgroups) where that leaves a workgroup per compute unit.  1021 rows of 12 interleaved adapters of rank 8: 14 us with one, 10
 // with four.
 int stack_of(int64_t M, int64_t K, int64_t adapters, int rank) {
     int64_t stack = 32 / rank < 1 ? 1 : 32 / rank;

@@ -46,8 +46,10 @@ __device__ __forceinline__ bool all_finite(u32x4_t v) {
 //
 // Rows of one request (the ordinary case: a wave's rows have one adapter, or none) go straight through.  Mixed rows
 // take a turn per adapter, in ascending order, in which rows of others enter as zeros.
+//   half: two waves whose sums are added later share the work on mixed rows (0: the first half of the row blocks,
+// and all of one request's rows; 1: the second half; -1: a wave by itself).
 template <int GAIN, int MB, int NB>
-__device__ __forceinline__ void lora_init(f32x4_t (&acc)[MB][NB], const LoraArgs& la, int M, int N, int row0, int col0) {
+__device__ __forceinline__ void lora_init(f32x4_t (&acc)[MB][NB], const LoraArgs& la, int M, int N, int row0, int col0, int half = -1) {
     int lane = int(threadIdx.x) & 63;
     asm volatile("" : "+v"(lane));  // what follows from it is computed here, not held through the main loop
     const int q = lane >> 4, l16 = lane & 15;
@@ -110,12 +112,13 @@ __device__ __forceinline__ void lora_init(f32x4_t (&acc)[MB][NB], const LoraArgs
             __builtin_amdgcn_sched_barrier(0);
         }
     };
+    constexpr int kHalf = (MB + 1) / 2;
     bool one = true;
 #pragma unroll
     for (int mb = 0; mb < MB; ++mb) one = one && id[mb] == id[0];
     const int first = __builtin_amdgcn_readfirstlane(id[0]);
     if (__all(one && id[0] == first)) {  // the ordinary case: one request's rows
-        if (first < 0) return;
+        if (first < 0 || half == 1) return;
         const auto rs = b_rsrc(first);
         step(rs, 0);
         if (steps > 1) step(rs, 1);
@@ -154,9 +157,9 @@ __device__ __forceinline__ void lora_init(f32x4_t (&acc)[MB][NB], const LoraArgs
             for (int ks = 0; ks < steps; ++ks) {
                 const uint32_t uo = u_off(ks), bo = b_off(ks);
                 // row blocks in two halves: their operands stay in registers through the turns
-                constexpr int kHalf = (MB + 1) / 2;
 #pragma unroll
                 for (int m0 = 0; m0 < MB; m0 += kHalf) {
+                    if (half >= 0 && half != m0 / kHalf) continue;
                     u32x4_t uf[kHalf];
 #pragma unroll
                     for (int j = 0; j < kHalf; ++j)
@@ -199,6 +202,7 @@ __device__ __forceinline__ void lora_init(f32x4_t (&acc)[MB][NB], const LoraArgs
         if (__any(odd != 0)) {
 #pragma unroll
             for (int mb = 0; mb < MB; ++mb) {
+                if (half >= 0 && half != mb / kHalf) continue;
                 f32x4_t sum[NB];
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) sum[nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};

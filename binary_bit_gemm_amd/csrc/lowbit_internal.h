@@ -162,7 +162,11 @@ hipError_t launch_gemm_tile16_epilogue(const GemmProblem* probs, int count, int 
                                        hipStream_t stream);
 hipError_t launch_gemm_tile16_group(const GemmProblem* probs, int count, int g, int bits, int variant,
                                     hipStream_t stream);
-hipError_t launch_gemm_tile16_lora(const GemmProblem& p, int g, int bits, const LoraArgs& la, hipStream_t stream);
+// Adapters on a 16x16-block tile.  sums: lora_split_bytes(...) bytes for the fp32 sums of a K split across workgroups
+// (0: the shape takes none; null: not split), with the tiles' arrival counters at the start of `workspace`.
+size_t lora_split_bytes(const GemmProblem& p, int g, int bits);
+hipError_t launch_gemm_tile16_lora(const GemmProblem& p, int g, int bits, const LoraArgs& la, void* workspace, void* sums,
+                                   hipStream_t stream);
 // Affine 4-bit groups (unsigned levels, w = s * q + b with each problem's B set) on a 16x16-block
 // tile; `variant` as for 4-bit codes.
 hipError_t launch_gemm_tile16_affine(const GemmProblem* probs, int count, int g, int variant, hipStream_t stream);

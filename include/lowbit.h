@@ -323,10 +323,13 @@ int lowbit_gemm_affine_ex(const void* X, const uint32_t* W, const void* S, const
  *      too small returns LOWBIT_E_INVALID), ZERO-FILLED before its first use.  Its first 4096 bytes hold arrival
  *      counters that every call leaves at zero, as in lowbit_gemm_ex; one workspace serves all such calls
  *      in turn (one for M rows serves fewer rows).  Calls that share it must not run concurrently.
+ *      With lowbit_lora_split_workspace_size(...) bytes, shapes whose output tiles leave compute units idle also
+ *      split the packed product along K (as lowbit_gemm_affine_ex does; the last bits can differ).
  * Both products are fp32 sums of bf16 products; X . A^T is kept to 16 significant bits between them; Y is rounded
  * to bf16 once.  Deterministic.  A, B and workspace need 16-byte alignment, alpha and rows 4.
  */
 size_t lowbit_lora_workspace_size(int64_t M, int rank);
+size_t lowbit_lora_split_workspace_size(int64_t M, int64_t N, int64_t K, int g, int bits, int rank);
 int lowbit_gemm_lora(const void* X, const uint32_t* W, const void* S, void* Y, int64_t M, int64_t N, int64_t K, int g,
                      int bits, const void* A, const void* B, const float* alpha, const int32_t* rows, int64_t adapters,
                      int rank, void* workspace, size_t workspace_bytes, void* stream);

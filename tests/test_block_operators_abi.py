@@ -51,6 +51,10 @@ def test_lora_workspace_size():
         assert sizes == sorted(sizes) and sizes[-1] <= 4096 + 4 * 5000 * rank + (9 << 20)
     n = size(64, 16)
     assert lora(bytes=n - 1) == INVALID
+    assert size(509, 32, 3072, 9216, 128, 1) > size(509, 32)            # 192 tiles of 64 x 128: K is split
+    assert size(4608, 32, 9216, 3072) == size(4608, 32)                 # enough tiles
+    assert size(16, 32, 3072, 9216) == size(16, 32)                     # few rows
+    assert size(64, 12, 256, 256) == size(64, 16, 250, 256) == size(64, 16, 256, 256, 32) == size(0, 16, 256, 256) == 0
 
 
 # ---- lowbit_qk_norm_rope ----

@@ -147,6 +147,21 @@ def test_many_adapters(M):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("bits,g", [(2, 64), (1, 128), (4, 64), (4, 128)])
+@pytest.mark.parametrize("M,N,K,rows", [(509, 1024, 2048, "segments"), (100, 320, 4096, "scattered"), (64, 128, 1536, "one"), (190, 2048, 1664, "scattered")])
+def test_k_split_across_workgroups(M, N, K, rows, bits, g):
+    c = Case(M, N, K, bits, g, 16, 5, rows, seed=11)
+    n = lb.lora_workspace_size(M, 16, N, K, g, bits)
+    assert n > lb.lora_workspace_size(M, 16)
+    ws = torch.full((n,), 0xFF, dtype=torch.uint8, device="cuda")
+    ws[:4096] = 0
+    got = c.run(workspace=ws)
+    c.check(got)
+    for _ in range(2):
+        assert torch.equal(c.run(workspace=ws), got) and not bool(ws[:4096].any())
+    c.check(c.run())
+
+
 def test_no_adapters_and_empty_calls():
     c = Case(5, 256, 256, 2, 64, 8, 1, "one", seed=7)
     plain = lb.gemm(c.x, c.words, c.scales, 64, 2)
