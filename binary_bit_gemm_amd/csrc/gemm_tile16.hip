@@ -315,8 +315,10 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KSPLIT, 1) void gemm_tile1
             for (int nb = 0; nb < C::NB; ++nb) acc[mb][nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
         if constexpr (EPI == kEpiLora) {
             // K ranges that are added up later: the term belongs to one of them, or a half of it to each of two
-            const bool owner = !XSPLIT || int(blockIdx.x) < total_tiles;
-            if (owner) lora_init<1>(acc, sk, M, N, m0 + wm0, n0 + wn0, KSPLIT == 2 ? kg : -1);
+            const int part = XSPLIT ? int(blockIdx.x) / total_tiles : kg;
+            bool shared = KSPLIT == 2;
+            if constexpr (XSPLIT) shared = sk.splits > 1;
+            if (part < 2) lora_init<1>(acc, sk, M, N, m0 + wm0, n0 + wn0, shared ? part : -1);
         }
 
         // A step's words and scales are read from LDS before any copy of the step is issued (the
@@ -560,7 +562,9 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KSPLIT, 1) void gemm_tile1
         // (16-byte loads and stores with the sc1 cache policy: through to the device-coherent
         // level, since the L2 of one XCD is not coherent with the others; the stores complete
         // before the arrival is counted)
-        if constexpr (XSPLIT) {
+        bool joins = false;
+        if constexpr (XSPLIT) joins = sk.splits > 1;
+        if constexpr (XSPLIT) if (joins) {
             constexpr int kSc1 = 16;
             constexpr int kBlocks = C::MB * C::NB;
             const int t = xcd_remap(vt, total_tiles);
@@ -769,24 +773,45 @@ hipError_t launch_gemm_tile16_epilogue(const GemmProblem* probs, int count, int 
     return hipErrorInvalidValue;
 }
 
-// K split across kTileSplits workgroups of a 64 x 128 tile: bytes of the splits' fp32 sums, 0 where the tile grid
-// fills the compute units or K is short.  With adapters (509 binary rows at K = 9216, 192 tiles, two of rank 32): 66 us
-// without the split, 59 with it.
-constexpr int kTileSplits = 3;
-size_t tile_split_bytes(const GemmProblem& p) {
-    const int64_t tiles = tiles_of(p.M, 64) * tiles_of(p.N, 128);
-    if (tiles * 4 > int64_t(kComputeUnits) * 3 || tiles > 1024 || p.K / KS < 8 * kTileSplits) return 0;
-    using Cf = Cfg16<64, 4, 64, 128, 1, 4>;
-    return size_t(tiles) * kTileSplits * Cf::WAVES * Cf::MB * Cf::NB * 1024u;
+// Adapters, 64 x 128 tiles of four waves and 48 KB of LDS, three to a compute unit, with K split `splits` ways across
+// workgroups where that helps to fill them: the splits (1: unsplit), or 0 where the cost model's own tiles take less.
+// Costs are in pick_tile_variant's unit.  A compute unit that holds n workgroups does 0.30 (n = 1), 0.47 (2) or 0.56
+// (3 and more) of a 256 x 256 tile's work per unit time; the splits' fp32 sums go out and come back, 64 KB a
+// workgroup.  All splits of a call are resident together (at most 3 workgroups per compute unit).  Measured, with a
+// first product of 5 to 10 us in each figure, other tiles -> this one: 509 x 3072 binary at K = 9216 65 -> 53 us (4
+// splits), 512 x 9216 at K = 3072 74 -> 53 (1), 1021 x 2560 4-bit at K = 4096 57 -> 52 (2), 64 x 3072 at K = 9216 54 ->
+// 25 (8); not taken: 1000 x 4096 at K = 4096 49 -> 58, 1536 x 3072 at K = 3072 40 -> 56.
+constexpr int kMaxTileSplits = 8;
+int lora_splits(const GemmProblem& p, int g, int bits) {
+    double best = 0.0;
+    pick_tile_variant(&p, 1, g, bits, true, &best);
+    const int64_t tiles = tiles_of(p.M, 64) * tiles_of(p.N, 128), ksteps = p.K / KS;
+    int splits = 0;
+    for (int s = 1; s <= kMaxTileSplits && tiles * s <= 3 * kComputeUnits && (s == 1 || ksteps >= 6 * s); ++s) {
+        const int64_t n = tiles_of(tiles * s, kComputeUnits);
+        const double eff = n == 1 ? 0.30 : n == 2 ? 0.47 : 0.56;
+        const double join = s == 1 ? 0.0 : double(tiles * s) * 34000.0 / double(p.K);
+        const double cost = double(n) * 64 * 128 / (s * eff) + join;
+        if (cost < best) {
+            best = cost;
+            splits = s;
+        }
+    }
+    return splits;
 }
 
-// The adapters' epilogue on the tile that the cost model picks among this kernel's.
+size_t lora_split_bytes(const GemmProblem& p, int g, int bits) {
+    const int splits = tile16_supported(g, bits) ? lora_splits(p, g, bits) : 0;
+    using Cf = Cfg16<64, 4, 64, 128, 1, 4>;
+    return splits < 2 ? 0 : size_t(tiles_of(p.M, 64) * tiles_of(p.N, 128)) * splits * Cf::WAVES * Cf::MB * Cf::NB * 1024u;
+}
+
+// The adapters' epilogue on that tile, or on the one that the cost model picks among this kernel's others.
 template <int G, int BITS>
-hipError_t launch_lora16(const GemmProblem& p, const LoraArgs& la, void* workspace, size_t workspace_bytes, void* sums,
-                         hipStream_t stream) {
-    if (workspace_bytes > 0) {  // the caller's workspace has room for a K split that pays
+hipError_t launch_lora16(const GemmProblem& p, const LoraArgs& la, int splits, void* counters, void* sums, hipStream_t stream) {
+    if (splits > 0) {
         LoraSplitK sk;
-        static_cast<SplitK&>(sk) = SplitK{static_cast<float*>(sums), static_cast<uint32_t*>(workspace), kTileSplits};
+        static_cast<SplitK&>(sk) = SplitK{static_cast<float*>(sums), static_cast<uint32_t*>(counters), splits};
         static_cast<LoraArgs&>(sk) = la;
         return launch_cfg16<G, BITS, 64, 128, 1, 4, 1, kEpiLora, false, true>(&p, 1, stream, sk);
     }
@@ -800,31 +825,30 @@ hipError_t launch_lora16(const GemmProblem& p, const LoraArgs& la, void* workspa
     return launch_cfg16<G, BITS, 288, 192, 2, 6, 1, kEpiLora>(&p, 1, stream, la);
 }
 
-size_t lora_split_bytes(const GemmProblem& p, int g, int bits) {
-    if (!tile16_supported(g, bits) || pick_tile_variant(&p, 1, g, bits, true) != TILE_64x128K2) return 0;
-    return tile_split_bytes(p);
-}
-
-hipError_t launch_gemm_tile16_lora(const GemmProblem& p, int g, int bits, const LoraArgs& la, void* workspace, void* sums,
+hipError_t launch_gemm_tile16_lora(const GemmProblem& p, int g, int bits, const LoraArgs& la, void* counters, void* sums,
                                    hipStream_t stream) {
     if (!tile16_supported(g, bits)) return hipErrorInvalidValue;
-    const size_t split = sums != nullptr ? lora_split_bytes(p, g, bits) : 0;
+    int splits = lora_splits(p, g, bits);
+    if (splits > 1 && sums == nullptr) splits = 0;
     if (bits == 2)
-        return g == 64 ? launch_lora16<64, 2>(p, la, workspace, split, sums, stream) : launch_lora16<128, 2>(p, la, workspace, split, sums, stream);
+        return g == 64 ? launch_lora16<64, 2>(p, la, splits, counters, sums, stream) : launch_lora16<128, 2>(p, la, splits, counters, sums, stream);
     if (bits == 4)
-        return g == 64 ? launch_lora16<64, 4>(p, la, workspace, split, sums, stream) : launch_lora16<128, 4>(p, la, workspace, split, sums, stream);
-    return g == 64 ? launch_lora16<64, 1>(p, la, workspace, split, sums, stream) : launch_lora16<128, 1>(p, la, workspace, split, sums, stream);
+        return g == 64 ? launch_lora16<64, 4>(p, la, splits, counters, sums, stream) : launch_lora16<128, 4>(p, la, splits, counters, sums, stream);
+    return g == 64 ? launch_lora16<64, 1>(p, la, splits, counters, sums, stream) : launch_lora16<128, 1>(p, la, splits, counters, sums, stream);
 }
 
 // Affine 4-bit GEMMs whose 64 x 128 tile grid leaves a quarter of the compute units or more idle
 // (the text encoder's 512 x 2560 down projection: 160 tiles) split K three ways across workgroups
 // through a caller workspace: three 4-wave workgroups of 48 KB LDS share a compute unit, so the
 // 480 workgroups run in one round.  0 where no split applies.
+constexpr int kAffineSplits = 3;
 constexpr size_t kAffineCounterBytes = 4096;  // 1024 tile counters, at the workspace's start
 size_t affine_split_bytes(const GemmProblem& p, int g) {
     if (!tile16_supported(g, 4) || pick_tile_variant(&p, 1, g, 4) != TILE_64x128K2) return 0;
-    const size_t sums = tile_split_bytes(p);
-    return sums == 0 ? 0 : kAffineCounterBytes + sums;
+    const int64_t tiles = tiles_of(p.M, 64) * tiles_of(p.N, 128);
+    if (tiles * 4 > int64_t(kComputeUnits) * 3 || tiles > 1024 || p.K / KS < 8 * kAffineSplits) return 0;
+    using Cf = Cfg16<64, 4, 64, 128, 1, 4>;
+    return kAffineCounterBytes + size_t(tiles) * kAffineSplits * Cf::WAVES * Cf::MB * Cf::NB * 1024u;
 }
 
 size_t affine_workspace_bytes(const GemmProblem& p, int g) { return affine_split_bytes(p, g); }
@@ -834,7 +858,7 @@ hipError_t launch_gemm_tile16_affine_ex(const GemmProblem& p, int g, void* works
     const size_t need = affine_split_bytes(p, g);
     if (need == 0 || workspace == nullptr || workspace_bytes < need) return hipErrorNotSupported;
     SplitK sk{reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kAffineCounterBytes),
-              static_cast<uint32_t*>(workspace), kTileSplits};
+              static_cast<uint32_t*>(workspace), kAffineSplits};
     return g == 64 ? launch_cfg16<64, 4, 64, 128, 1, 4, 1, kEpiPlain, true, true>(&p, 1, stream, sk)
                    : launch_cfg16<128, 4, 64, 128, 1, 4, 1, kEpiPlain, true, true>(&p, 1, stream, sk);
 }

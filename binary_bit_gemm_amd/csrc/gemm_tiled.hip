@@ -620,7 +620,7 @@ constexpr TileShape kTiles[] = {
 
 }  // namespace
 
-int pick_tile_variant(const GemmProblem* probs, int count, int g, int bits, bool tile16_only) {
+int pick_tile_variant(const GemmProblem* probs, int count, int g, int bits, bool tile16_only, double* best_cost_out) {
     int best = bits == 4 || tile16_only ? TILE_288x192 : TILE_64x256;
     double best_cost = 0.0;
     for (const TileShape& t : kTiles) {
@@ -652,6 +652,7 @@ int pick_tile_variant(const GemmProblem* probs, int count, int g, int bits, bool
             best_cost = cost;
         }
     }
+    if (best_cost_out != nullptr) *best_cost_out = best_cost;
     return best;
 }
 

@@ -151,7 +151,8 @@ hipError_t launch_gemm_skinny_group(const GemmProblem* probs, int count, int g, 
 
 // Tile for a group of problems: fewest estimated rounds x tile work over the whole group.
 // tile16_only: among the tiles of the 16x16-block kernel.
-int pick_tile_variant(const GemmProblem* probs, int count, int g, int bits, bool tile16_only = false);
+int pick_tile_variant(const GemmProblem* probs, int count, int g, int bits, bool tile16_only = false,
+                      double* best_cost_out = nullptr);
 int pick_tile_variant(int64_t M, int64_t N, int64_t K, int g, int bits);
 const char* tile_variant_name(int variant);
 bool tile16_supported(int g, int bits);
@@ -163,9 +164,9 @@ hipError_t launch_gemm_tile16_epilogue(const GemmProblem* probs, int count, int 
 hipError_t launch_gemm_tile16_group(const GemmProblem* probs, int count, int g, int bits, int variant,
                                     hipStream_t stream);
 // Adapters on a 16x16-block tile.  sums: lora_split_bytes(...) bytes for the fp32 sums of a K split across workgroups
-// (0: the shape takes none; null: not split), with the tiles' arrival counters at the start of `workspace`.
+// (0: the shape takes none; null: not split), counters: the tiles' arrival counters.
 size_t lora_split_bytes(const GemmProblem& p, int g, int bits);
-hipError_t launch_gemm_tile16_lora(const GemmProblem& p, int g, int bits, const LoraArgs& la, void* workspace, void* sums,
+hipError_t launch_gemm_tile16_lora(const GemmProblem& p, int g, int bits, const LoraArgs& la, void* counters, void* sums,
                                    hipStream_t stream);
 // Affine 4-bit groups (unsigned levels, w = s * q + b with each problem's B set) on a 16x16-block
 // tile; `variant` as for 4-bit codes.

@@ -324,7 +324,7 @@ int lowbit_gemm_affine_ex(const void* X, const uint32_t* W, const void* S, const
  *      counters that every call leaves at zero, as in lowbit_gemm_ex; one workspace serves all such calls
  *      in turn (one for M rows serves fewer rows).  Calls that share it must not run concurrently.
  *      With lowbit_lora_split_workspace_size(...) bytes, shapes whose output tiles leave compute units idle also
- *      split the packed product along K (as lowbit_gemm_affine_ex does; the last bits can differ).
+ *      split the packed product along K (the last bits can differ from the other form's).
  * Both products are fp32 sums of bf16 products; X . A^T is kept to 16 significant bits between them; Y is rounded
  * to bf16 once.  Deterministic.  A, B and workspace need 16-byte alignment, alpha and rows 4.
  */

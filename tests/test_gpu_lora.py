@@ -162,6 +162,13 @@ def test_k_split_across_workgroups(M, N, K, rows, bits, g):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("bits,g", [(2, 64), (1, 128), (4, 64)])
+@pytest.mark.parametrize("rows", ["segments", "scattered"])
+def test_many_small_tiles(rows, bits, g):  # 640 tiles of 64 x 128, not split
+    c = Case(260, 16384, 512, bits, g, 16, 5, rows, seed=12)
+    c.check(c.run())
+
+
 def test_no_adapters_and_empty_calls():
     c = Case(5, 256, 256, 2, 64, 8, 1, "one", seed=7)
     plain = lb.gemm(c.x, c.words, c.scales, 64, 2)
