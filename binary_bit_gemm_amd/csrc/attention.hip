@@ -898,40 +898,68 @@ constexpr int kMaxShortSplits = 64;     // a lane per split in the join
 
 }  // namespace
 
-// Which kernel, and how the keys are split.
-//   The kernel for few rows (32 per workgroup, its waves over the keys) takes calls of up to 2^32 products: it has four
-// times the workgroups and no barriers, where the other kernel waits for copies.  Measured (us, few / many):
-// 512 x 512, 32 / 8 heads of 128: 14 / 29; 1024 x 1024, 24 heads of 128: 32 / 39; 2048 x 2048, 8 heads of 128:
-// 31 / 44; 128 x 32768, 8 heads of 128: 58 / 67; past the bound 1536 x 1536, 24 heads of 128: 61 / 52, and 2 x
-// 1533 x 1533, 16 heads of 64: 37 / 35.  One row block (16 or 32 rows) always takes it.
-//   Keys are split until every compute unit has a workgroup (few rows: 256 workgroups of three tiles a wave at least;
-// 512 were slower at 1024 rows, 27 against 17 us, and at 40007 keys, 33 against 32); the other
-// kernel, until there are two per compute unit, each with four tiles at least.
+// Which kernel, and how the keys are split: the one whose estimated time is less (one row block, 16 or 32 rows,
+// always goes to the few-rows kernel).  The estimates (us, D = 64 / 128) are fits to measured calls of 8 to 96 heads, 64 to
+// 2048 rows and 200 to 8192 keys: in five of 92 of them the other kernel is 7% to 12% faster, in the rest less or
+// not.  Measured (few / many, us): 512 x 512, 24 heads of 128: 14 / 17; 512 x 2048, 16 heads
+// of 128: 26 / 33; 1024 x 1024, 24 heads of 128: 33 / 28, of 64: 17 / 18; 4 x 512 x 512, 24 heads of 128: 38 / 26.
 //   LOWBIT_ATTENTION=few|many in the environment forces the kernel (A/B runs and tests).
+//
+// The few-rows kernel (32 rows per workgroup, its waves over the keys, two or three workgroups per compute unit):
+// 5, 0.0049 / 0.0093 a key for a workgroup alone on its compute unit, 0.45 of that for each beside it, and 4.5 / 6
+// for each further round.  Keys are split until every compute unit has a workgroup of three tiles a wave at least
+// (512 workgroups were slower at 1024 rows, 27 against 17, and at 40007 keys, 33 against 32); the join costs 10 / 12.
+double few_us(int64_t groups, int64_t keys, bool joins, int head_dim) {
+    const int64_t room = kComputeUnits * (head_dim == 64 ? 3 : 2);
+    auto load = [](int64_t n) { return n <= kComputeUnits ? 1.0 : 0.55 + 0.45 * double(n) / kComputeUnits; };
+    const int64_t rounds = groups == 0 ? 0 : (groups - 1) / room;  // full ones before the last
+    return 5.0 + (joins ? head_dim == 64 ? 10.0 : 12.0 : 0.0) + double(rounds) * (head_dim == 64 ? 4.5 : 6.0) +
+           double(keys) * (head_dim == 64 ? 0.0049 : 0.0093) * (double(rounds) * load(room) + load(groups - rounds * room));
+}
+// The other kernel (128 rows per workgroup): 5 / 9, and 0.79 / 1.16 a tile of 64 keys, times 0.75 for each workgroup on
+// a compute unit that has more than one.  Split, it runs two workgroups per compute unit, of four tiles at least, and
+// the join costs 6, 0.4 / 0.15 a split, and 7 / 14 for 512 workgroups' parts to go to memory and back.
+double many_us(int64_t groups, int64_t tiles, int64_t splits, int head_dim) {
+    const double load = groups <= kComputeUnits ? 1.0 : 0.75 * double(tiles_of(groups, kComputeUnits));
+    return (head_dim == 64 ? 5.0 : 9.0) + double(tiles) * (head_dim == 64 ? 0.79 : 1.16) * load +
+           (splits > 1 ? 6.0 + (head_dim == 64 ? 0.4 : 0.15) * double(splits) +
+                             (head_dim == 64 ? 7.0 : 14.0) * double(groups) / (2 * kComputeUnits)
+                       : 0.0);
+}
+
 AttnPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t kv_len, int head_dim) {
+    // few rows
+    const int64_t few_rows = rows <= 16 ? 16 : 32, few_groups = batch * kv_heads * tiles_of(rows, few_rows);
+    const int64_t few_tiles = tiles_of(kv_len, kShortKeys);
+    int64_t few_splits = few_groups >= kComputeUnits || few_groups == 0 ? 1 : kComputeUnits / few_groups;
+    few_splits = few_splits < few_tiles / 12 ? few_splits : few_tiles / 12;
+    few_splits = few_splits < kMaxShortSplits ? few_splits : kMaxShortSplits;
+    few_splits = few_splits < 1 ? 1 : few_splits;
+    const double few = few_us(few_groups * few_splits, tiles_of(few_tiles, few_splits) * kShortKeys, few_splits > 1, head_dim);
+    // many rows
+    const int64_t groups = batch * kv_heads * tiles_of(rows, 128), tiles = tiles_of(kv_len, 64);
+    int64_t splits = groups >= kComputeUnits || groups == 0 ? 1 : 2 * kComputeUnits / groups;
+    splits = splits < tiles / 4 ? splits : tiles / 4;
+    splits = splits < 1 ? 1 : splits;
+    double many = many_us(groups * splits, tiles_of(tiles, splits), splits, head_dim);
+    const double whole = many_us(groups, tiles, 1, head_dim);
+    if (whole <= many) {
+        splits = 1;
+        many = whole;
+    }
+
     AttnPlan p{};
-    p.is_short = rows <= 32 || double(batch) * double(kv_heads) * double(rows) * double(kv_len) * head_dim <= 4294967296.0;
+    p.is_short = rows <= 32 || few <= many;
     if (const char* force = std::getenv("LOWBIT_ATTENTION")) {
         if (std::strcmp(force, "few") == 0) p.is_short = true;
         if (std::strcmp(force, "many") == 0) p.is_short = false;
     }
-    int64_t splits, tiles;
     if (p.is_short) {
-        p.row_tiles = int(rows <= 16 ? 1 : tiles_of(rows, 32));
-        const int64_t heads = batch * kv_heads * p.row_tiles;
-        tiles = tiles_of(kv_len, kShortKeys);
-        splits = heads >= kComputeUnits ? 1 : kComputeUnits / heads;
-        splits = splits < tiles / 12 ? splits : tiles / 12;
-        splits = splits < kMaxShortSplits ? splits : kMaxShortSplits;
-        p.splits = splits < 1 ? 1 : int(splits);
+        p.row_tiles = int(tiles_of(rows, few_rows));
+        p.splits = int(few_splits);
         p.tiles_per_split = 0;
     } else {
         p.row_tiles = int(tiles_of(rows, 128));
-        tiles = tiles_of(kv_len, 64);
-        const int64_t base = batch * kv_heads * p.row_tiles;
-        splits = base >= kComputeUnits ? 1 : 2 * kComputeUnits / base;
-        splits = splits < tiles / 4 ? splits : tiles / 4;
-        splits = splits < 1 ? 1 : splits;
         p.tiles_per_split = int(tiles_of(tiles, splits));
         p.splits = p.tiles_per_split > 0 ? int(tiles_of(tiles, p.tiles_per_split)) : 1;
     }
