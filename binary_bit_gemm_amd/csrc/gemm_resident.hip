@@ -28,6 +28,7 @@
 #include <atomic>
 #include <cstdio>
 #include <cstdlib>
+#include <type_traits>
 
 #include "lora_device.h"
 #include "lowbit_device.h"
@@ -77,8 +78,14 @@ struct ResidentArgs {
     int tiles;            // tiles of the launch
     float* ws;            // [tiles][splits][cb][64][4] fp32 partial sums (splits > 1)
     uint32_t* counters;   // [tiles] arrival counters, zero between calls (splits > 1)
-    LoraArgs lora;        // adapters (kEpiLora)
 };
+
+// EPI = kEpiLora: with the adapters' operands (apart, so that the other launches' arguments stay short).
+struct ResidentLoraArgs : ResidentArgs {
+    LoraArgs lora;
+};
+template <int EPI>
+using Args = std::conditional_t<EPI == kEpiLora, ResidentLoraArgs, ResidentArgs>;
 
 // 4-byte direct-to-LDS copy: lane i's 4 bytes land at lds_wave_base + 4 * i.
 __device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t rs, void* lds_wave_base, uint32_t voff) {
@@ -93,7 +100,7 @@ __device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t rs, void* lds_wave_b
 // (Y may be R: each element is read and written by the same lane).  EPI = kEpiLora: the adapters' term is
 // added to the sums.  All three: whole K only (one split).
 template <int G, int LEN, int EPI = kEpiPlain>
-__global__ __launch_bounds__(64 * kMaxWaves, 1) void gemm_resident_kernel(ResidentArgs a) {
+__global__ __launch_bounds__(64 * kMaxWaves, 1) void gemm_resident_kernel(Args<EPI> a) {
     constexpr bool SWIGLU = EPI == kEpiSwiglu;
     constexpr int GPS = kStepCodes / G;  // scale groups per step: 4 or 2
     extern __shared__ __attribute__((aligned(1024))) unsigned char lds[];
@@ -368,7 +375,7 @@ __global__ __launch_bounds__(64 * kMaxWaves, 1) void gemm_resident_kernel(Reside
 }
 
 template <int G, int LEN, int EPI = kEpiPlain>
-hipError_t launch_cfg(const ResidentArgs& a, uint32_t lds, hipStream_t stream) {
+hipError_t launch_cfg(const Args<EPI>& a, uint32_t lds, hipStream_t stream) {
     // allow the dynamic LDS of the largest plan, once per kernel and device (threads that get here
     // first at the same time may both set it; the value is the same)
     static std::atomic<int> attr_set[64];
@@ -396,7 +403,7 @@ hipError_t launch_cfg(const ResidentArgs& a, uint32_t lds, hipStream_t stream) {
 }
 
 template <int G, int EPI = kEpiPlain>
-hipError_t launch_g(const ResidentArgs& a, uint32_t lds, int len, hipStream_t stream) {
+hipError_t launch_g(const Args<EPI>& a, uint32_t lds, int len, hipStream_t stream) {
     switch (len) {
         case 1: return launch_cfg<G, 1, EPI>(a, lds, stream);
         case 2: return launch_cfg<G, 2, EPI>(a, lds, stream);
@@ -587,8 +594,10 @@ hipError_t launch_gemm_resident_epilogue(const GemmProblem& p, int g, int epi, h
     const uint32_t red = uint32_t(cb * ks) * 1024u;  // the K-slice reduction reuses the LDS
     lds = lds > red ? lds : red;
     if (epi == kEpiLora) {
-        a.lora = *lora;
-        return g == 64 ? launch_g<64, kEpiLora>(a, lds, len, stream) : launch_g<128, kEpiLora>(a, lds, len, stream);
+        ResidentLoraArgs al;
+        static_cast<ResidentArgs&>(al) = a;
+        al.lora = *lora;
+        return g == 64 ? launch_g<64, kEpiLora>(al, lds, len, stream) : launch_g<128, kEpiLora>(al, lds, len, stream);
     }
     if (swiglu) return g == 64 ? launch_g<64, kEpiSwiglu>(a, lds, len, stream) : launch_g<128, kEpiSwiglu>(a, lds, len, stream);
     return g == 64 ? launch_g<64, kEpiResidual>(a, lds, len, stream) : launch_g<128, kEpiResidual>(a, lds, len, stream);

@@ -27,7 +27,6 @@
 // Weight Representation: 1-bit g128"); the operand holds 2c (ternary) or -2c (binary) and
 // the factor +-1/2 is applied once to the final sum.
 #include <cstdlib>
-#include <type_traits>
 
 #include "lora_device.h"
 #include "lowbit_device.h"
@@ -46,11 +45,9 @@ struct SkinnyFmt {
     static constexpr int XPS = 4 * MPC;             // activation operands per step and row block
 };
 
-struct NoLora {};
-
-// LORA: low-rank adapters' term added to the sums (one problem per launch).
-template <int BITS, int G, int MB, int NCB, int WAVES, bool LORA>
-__global__ __launch_bounds__(64 * WAVES, 2) void gemm_skinny_kernel(ProblemGroup grp, std::conditional_t<LORA, LoraArgs, NoLora> la) {
+// Lora: nothing, or LoraArgs: low-rank adapters' term added to the sums (one problem per launch).
+template <int BITS, int G, int MB, int NCB, int WAVES, class... Lora>
+__global__ __launch_bounds__(64 * WAVES, 2) void gemm_skinny_kernel(ProblemGroup grp, Lora... la) {
     using F = SkinnyFmt<BITS>;
     constexpr int GPS = F::STEP / G;                      // scale groups per step
     constexpr bool kSplitChunk = F::CHUNK > G;            // groups smaller than a chunk
@@ -315,8 +312,8 @@ __global__ __launch_bounds__(64 * WAVES, 2) void gemm_skinny_kernel(ProblemGroup
         const int col = n0 + 16 * cb + (l & 15);
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] *= code_scale;
-        if constexpr (LORA) {  // a wave's 64 threads share cb and mb
-            const f32x4_t term = lora_term16(la, M, N, 16 * mb, n0 + 16 * cb);
+        if constexpr (sizeof...(Lora) > 0) {  // a wave's 64 threads share cb and mb
+            const f32x4_t term = lora_term16(la..., M, N, 16 * mb, n0 + 16 * cb);
 #pragma unroll
             for (int i = 0; i < 4; ++i) v[i] += term[i];
         }
@@ -341,13 +338,12 @@ hipError_t launch_cfg(const GemmProblem* probs, int count, const LoraArgs* lora,
     grp.count = count;
     if (lora != nullptr) {
         if constexpr (G != 32)
-            hipLaunchKernelGGL((gemm_skinny_kernel<BITS, G, MB, NCB, WAVES, true>), dim3(total), dim3(64 * WAVES), 0, stream,
+            hipLaunchKernelGGL((gemm_skinny_kernel<BITS, G, MB, NCB, WAVES, LoraArgs>), dim3(total), dim3(64 * WAVES), 0, stream,
                                grp, *lora);
         else
             return hipErrorNotSupported;
     } else {
-        hipLaunchKernelGGL((gemm_skinny_kernel<BITS, G, MB, NCB, WAVES, false>), dim3(total), dim3(64 * WAVES), 0, stream,
-                           grp, NoLora{});
+        hipLaunchKernelGGL((gemm_skinny_kernel<BITS, G, MB, NCB, WAVES>), dim3(total), dim3(64 * WAVES), 0, stream, grp);
     }
     const hipError_t e = hipGetLastError();
     if (e == hipSuccess && trace_enabled()) {
