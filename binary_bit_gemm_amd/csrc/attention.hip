@@ -927,20 +927,21 @@ double many_us(int64_t groups, int64_t tiles, int64_t splits, int head_dim) {
                        : 0.0);
 }
 
-AttnPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t kv_len, int head_dim) {
+// may_split false: no workspace to split with.
+AttnPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t kv_len, int head_dim, bool may_split) {
     // few rows
     const int64_t few_rows = rows <= 16 ? 16 : 32, few_groups = batch * kv_heads * tiles_of(rows, few_rows);
     const int64_t few_tiles = tiles_of(kv_len, kShortKeys);
     int64_t few_splits = few_groups >= kComputeUnits || few_groups == 0 ? 1 : kComputeUnits / few_groups;
     few_splits = few_splits < few_tiles / 12 ? few_splits : few_tiles / 12;
     few_splits = few_splits < kMaxShortSplits ? few_splits : kMaxShortSplits;
-    few_splits = few_splits < 1 ? 1 : few_splits;
+    few_splits = few_splits < 1 || !may_split ? 1 : few_splits;
     const double few = few_us(few_groups * few_splits, tiles_of(few_tiles, few_splits) * kShortKeys, few_splits > 1, head_dim);
     // many rows
     const int64_t groups = batch * kv_heads * tiles_of(rows, 128), tiles = tiles_of(kv_len, 64);
     int64_t splits = groups >= kComputeUnits || groups == 0 ? 1 : 2 * kComputeUnits / groups;
     splits = splits < tiles / 4 ? splits : tiles / 4;
-    splits = splits < 1 ? 1 : splits;
+    splits = splits < 1 || !may_split ? 1 : splits;
     double many = many_us(groups * splits, tiles_of(tiles, splits), splits, head_dim);
     const double whole = many_us(groups, tiles, 1, head_dim);
     if (whole <= many) {
@@ -949,7 +950,7 @@ AttnPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t k
     }
 
     AttnPlan p{};
-    p.is_short = rows <= 32 || few <= many;
+    p.is_short = rows <= 32 || (few <= many && few_groups <= kMaxGrid256);
     if (const char* force = std::getenv("LOWBIT_ATTENTION")) {
         if (std::strcmp(force, "few") == 0) p.is_short = true;
         if (std::strcmp(force, "many") == 0) p.is_short = false;
@@ -966,14 +967,6 @@ AttnPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t k
     const int64_t padded = p.is_short ? int64_t(p.row_tiles) * (rows <= 16 ? 16 : 32) : rows;
     p.part_rows = p.splits > 1 ? batch * kv_heads * padded * p.splits : 0;
     p.bytes = p.splits > 1 ? kWorkspaceCounterBytes + size_t(p.part_rows) * (size_t(head_dim) + 2) * 4u : 0;
-    return p;
-}
-
-AttnPlan plan_attention_unsplit(AttnPlan p, int64_t kv_len) {
-    p.splits = 1;
-    p.tiles_per_split = int(tiles_of(kv_len, 64));
-    p.part_rows = 0;
-    p.bytes = 0;
     return p;
 }
 

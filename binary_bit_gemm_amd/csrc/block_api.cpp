@@ -70,7 +70,7 @@ int attention_args(const lowbit_attention_problem* p, lowbit::AttnArgs& a) {
     if (!apart3(p->batch, p->o_batch, p->q_len, p->o_token, p->q_heads, p->o_head, p->head_dim)) return LOWBIT_E_INVALID;
     a.group = p->q_heads / p->kv_heads;
     const int64_t rows = int64_t(p->q_len) * a.group;
-    if (rows > kMaxDim - 128 || (rows + 127) / 128 * p->kv_heads * p->batch > kMaxDim / 64) return LOWBIT_E_UNSUPPORTED;
+    if (rows > kMaxDim - 128 || (rows + 127) / 128 * p->kv_heads * p->batch > lowbit::kMaxGrid256) return LOWBIT_E_UNSUPPORTED;
     a.q_batch = p->q_batch;
     a.q_token = p->q_token;
     a.q_head = p->q_head;
@@ -188,7 +188,7 @@ int lowbit_attention(const lowbit_attention_problem* p, void* workspace, size_t 
     if (st != LOWBIT_OK) return st;
     lowbit::AttnPlan plan = lowbit::plan_attention(a.batch, a.kv_heads, a.rows, a.kv_len, p->head_dim);
     if (plan.bytes > 0 && (workspace == nullptr || workspace_bytes < plan.bytes))
-        plan = lowbit::plan_attention_unsplit(plan, a.kv_len);
+        plan = lowbit::plan_attention(a.batch, a.kv_heads, a.rows, a.kv_len, p->head_dim, false);
     const hipError_t e = lowbit::launch_attention(a, p->head_dim, plan, workspace, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? LOWBIT_OK : lowbit::hip_fail(e);
 }

@@ -242,14 +242,23 @@ hipError_t launch_lora_shrink(ShrinkArgs a, void* workspace, hipStream_t stream)
     a.part = reinterpret_cast<float*>(base + kWorkspaceCounterBytes + lora_u_bytes(a.M, a.rank));
     a.stack = stack_of(a.M, a.K, a.adapters, a.rank);
     a.splits = shrink_splits(a.M, a.K, a.adapters, a.rank, a.stack);
-    const dim3 grid(unsigned(tiles_of(a.M, 16)), unsigned(slots_of(a.adapters, a.stack)), unsigned(a.splits));
-    switch (rank_blocks(a.rank * a.stack)) {
-        case 1: hipLaunchKernelGGL((lora_shrink_kernel<1, 8>), grid, dim3(512), 0, stream, a); break;
-        case 2: hipLaunchKernelGGL((lora_shrink_kernel<2, 8>), grid, dim3(512), 0, stream, a); break;
-        case 4: hipLaunchKernelGGL((lora_shrink_kernel<4, 4>), grid, dim3(256), 0, stream, a); break;
-        default: hipLaunchKernelGGL((lora_shrink_kernel<8, 4>), grid, dim3(256), 0, stream, a); break;
+    // a launch has at most 2^32 threads: more rows take several (not split, so without counters)
+    const int64_t most = ((int64_t(1) << 23) - 1) * 16;
+    for (int64_t left = a.M;; left -= most) {
+        a.M = int(left < most ? left : most);
+        const dim3 grid(unsigned(tiles_of(a.M, 16)), unsigned(slots_of(a.adapters, a.stack)), unsigned(a.splits));
+        switch (rank_blocks(a.rank * a.stack)) {
+            case 1: hipLaunchKernelGGL((lora_shrink_kernel<1, 8>), grid, dim3(512), 0, stream, a); break;
+            case 2: hipLaunchKernelGGL((lora_shrink_kernel<2, 8>), grid, dim3(512), 0, stream, a); break;
+            case 4: hipLaunchKernelGGL((lora_shrink_kernel<4, 4>), grid, dim3(256), 0, stream, a); break;
+            default: hipLaunchKernelGGL((lora_shrink_kernel<8, 4>), grid, dim3(256), 0, stream, a); break;
+        }
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess || left <= most) return e;
+        a.X += most * a.K;
+        a.rows += most;
+        a.u += most * 2 * a.rank;
     }
-    return hipGetLastError();
 }
 
 }  // namespace lowbit

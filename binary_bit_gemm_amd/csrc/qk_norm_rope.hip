@@ -160,13 +160,26 @@ template <int D>
 hipError_t launch_d(QkArgs a, bool interleaved, hipStream_t stream) {
     constexpr int kHeads = kHeadRounds * (64 / (D / 8));  // heads of one wave
     a.chunks = (a.q_heads + a.k_heads + kHeads - 1) / kHeads;
-    const int64_t grid = (a.tokens * a.chunks + kWaves - 1) / kWaves;
-    if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-    if (interleaved)
-        hipLaunchKernelGGL((qk_norm_rope_kernel<D, true>), dim3(unsigned(grid)), dim3(64 * kWaves), 0, stream, a);
-    else
-        hipLaunchKernelGGL((qk_norm_rope_kernel<D, false>), dim3(unsigned(grid)), dim3(64 * kWaves), 0, stream, a);
-    return hipGetLastError();
+    // a launch has at most 2^32 threads: more tokens take several
+    const int64_t most = kMaxGrid256 * kWaves / a.chunks;
+    auto skip = [&](auto*& ptr, int64_t stride) {
+        if (ptr != nullptr) ptr += most * stride;
+    };
+    for (int64_t left = a.tokens;; left -= most) {
+        a.tokens = left < most ? left : most;
+        const unsigned grid = unsigned((a.tokens * a.chunks + kWaves - 1) / kWaves);
+        if (interleaved)
+            hipLaunchKernelGGL((qk_norm_rope_kernel<D, true>), dim3(grid), dim3(64 * kWaves), 0, stream, a);
+        else
+            hipLaunchKernelGGL((qk_norm_rope_kernel<D, false>), dim3(grid), dim3(64 * kWaves), 0, stream, a);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess || left <= most) return e;
+        skip(a.q, a.q_token);
+        skip(a.k, a.k_token);
+        skip(a.q_out, a.qo_token);
+        skip(a.k_out, a.ko_token);
+        skip(a.positions, a.axes);
+    }
 }
 
 }  // namespace

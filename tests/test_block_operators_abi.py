@@ -112,7 +112,8 @@ def attention(ws=0, nbytes=0, **kw):
     (dict(head_dim=96), UNSUPPORTED), (dict(head_dim=256), UNSUPPORTED), (dict(batch=-1), INVALID), (dict(q_len=-1), INVALID),
     (dict(kv_len=-1), INVALID), (dict(q_heads=-8), INVALID), (dict(q_heads=9), INVALID), (dict(kv_heads=3), INVALID),
     (dict(kv_heads=0), INVALID), (dict(kv_len=(1 << 31) - 1), UNSUPPORTED), (dict(q_len=1 << 31), UNSUPPORTED),
-    (dict(q_len=1 << 30, q_heads=8), UNSUPPORTED), (dict(batch=1 << 17), UNSUPPORTED), (dict(q_heads=1 << 17, kv_heads=1 << 17), UNSUPPORTED),
+    (dict(q_len=1 << 30, q_heads=8), UNSUPPORTED), (dict(batch=1 << 16, q_heads=256, kv_heads=256), UNSUPPORTED),
+    (dict(batch=1 << 17), UNSUPPORTED), (dict(q_heads=1 << 17, kv_heads=1 << 17), UNSUPPORTED),
     (dict(scale=0.0), INVALID), (dict(scale=-1.0), INVALID), (dict(scale=float("nan")), INVALID), (dict(scale=float("inf")), INVALID),
     (dict(q_token=1020), INVALID), (dict(k_head=-128), INVALID), (dict(v_batch=1 << 41), INVALID), (dict(mask_batch=-1), INVALID),
     (dict(k_token=64), INVALID), (dict(v_token=0), INVALID), (dict(k_token=(1 << 24) + 8), UNSUPPORTED),

@@ -147,6 +147,22 @@ def test_offsets_past_32_bits():
     assert torch.equal(q, want)
 
 
+def test_more_tokens_than_a_launch_has_waves():
+    """2^26 + 77 tokens, one head of 32 each (the input is one row, read again for every token)."""
+    T = (1 << 26) + 77
+    g = torch.Generator().manual_seed(9)
+    row = torch.randn(1, 1, 32, generator=g).bfloat16().cuda()
+    none = row.new_empty(T, 0, 32)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")[:, None] % 4099
+    freqs = lb.rope_freqs((32,))
+    got, _ = lb.qk_norm_rope(row.expand(T, 1, 32), none, pos, freqs, (32,))
+    first = torch.arange(300, device="cuda")
+    for at in (first, first + (1 << 25), first + (1 << 26) - 270, first + T - 300):
+        q = row.expand(300, 1, 32)
+        want, _ = lb.qk_norm_rope(q, none[:300], pos[at], freqs, (32,))
+        assert torch.equal(got[at], want)
+
+
 def test_on_another_stream():
     q, k, w, pos, freqs = make(300, 8, 8, 128, (128,), seed=8)
     want = lb.qk_norm_rope(q, k, pos, freqs, (128,), *w)
