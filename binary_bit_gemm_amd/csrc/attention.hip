@@ -335,11 +335,11 @@ __device__ __forceinline__ void load_q(Rows<D, NQ>& w, const AttnArgs& a, int b,
 
 // O of the rows to memory, divided by l: 16 bytes per lane and pair of column blocks after an exchange between
 // neighbouring lane quarters (each holds 4 of every 16 columns).  A row without keys has l = 0: zeros.
-template <int D>
-__device__ __forceinline__ void store_o(const Rows<D, 2>& w, const AttnArgs& a, int b, int hk, int row0) {
+template <int D, int NQ>
+__device__ __forceinline__ void store_o(const Rows<D, NQ>& w, const AttnArgs& a, int b, int hk, int row0) {
     const int lane = int(threadIdx.x) & 63, q = lane >> 4;
 #pragma unroll
-    for (int qb = 0; qb < 2; ++qb) {
+    for (int qb = 0; qb < NQ; ++qb) {
         const int row = row0 + 16 * qb + (lane & 15);
         const bool in = row < a.rows;
         const int t = in ? row / a.group : 0, g = in ? row - t * a.group : 0;
@@ -413,10 +413,11 @@ __device__ __forceinline__ uint64_t up_to(int64_t rel) {
     return rel < 0 ? 0ull : rel >= 63 ? ~0ull : (2ull << rel) - 1;
 }
 
-// Long rows: a workgroup of 4 waves takes 128 rows of one kv head, a wave 32 of them; tiles of 64 keys go
+// Many rows: a workgroup of 4 waves takes 64 NQ rows of one kv head, a wave 16 NQ of them; tiles of 64 keys go
 // through LDS, double-buffered, by direct copies one tile ahead.
-template <int D>
-__global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
+template <int D, int NQ>
+__global__ __launch_bounds__(256, D == 64 && NQ == 1 ? 4 : 2) void attention_kernel(AttnArgs a) {
+    constexpr int kRows = 64 * NQ;                // of a workgroup
     constexpr int kTile = 64 * D * 2;
     constexpr int kRowsPerCopy = 512 / D;         // rows that one wave-wide 16-byte copy brings
     constexpr int kCopies = 64 / kRowsPerCopy / 4;  // copies per wave and tile
@@ -426,22 +427,23 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
     __shared__ int odd_tile;  // the last tile in which an infinity or a NaN was seen
     const int lane = int(threadIdx.x) & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
-    // tiles of one head next to each other, heads of one XCD together
+    // tiles of one head next to each other, heads of one XCD together; causal: those with the most keys first (4608
+    // tokens, 24 heads of 128: 161 us, last 191)
     int id = xcd_remap(int(blockIdx.x), int(gridDim.x));
-    const int rt = id % a.row_tiles;
+    const int rt = a.causal ? a.row_tiles - 1 - id % a.row_tiles : id % a.row_tiles;
     id /= a.row_tiles;
     const int split = id % a.splits;
     id /= a.splits;
     const int hk = id % a.kv_heads, b = id / a.kv_heads;
 
     const int n = in_sgpr(live_keys(a, b));
-    const int row0 = rt * 128 + wave * 32;  // the wave's rows
+    const int row0 = rt * kRows + wave * (16 * NQ);  // the wave's rows
     const int64_t start = a.causal ? (a.start != nullptr ? a.start[b] : 0) : 0;
     // the last key of the workgroup's rows
-    const int last_row = rt * 128 + 127 < a.rows ? rt * 128 + 127 : a.rows - 1;
+    const int last_row = rt * kRows + kRows - 1 < a.rows ? rt * kRows + kRows - 1 : a.rows - 1;
     const int64_t last = a.causal ? start + last_row / a.group : int64_t(n) - 1;
     // the first key that a row of the workgroup leaves out by the causal rule (all rows take those before)
-    const int64_t first64 = a.causal ? start + (rt * 128) / a.group + 1 : n;
+    const int64_t first64 = a.causal ? start + (rt * kRows) / a.group + 1 : n;
     const int64_t end64 = last + 1 < n ? last + 1 : n;
     const int end = end64 < 0 ? 0 : int(end64);
     const int first = in_sgpr(first64 < 0 ? 0 : first64 < n ? int(first64) : n);
@@ -449,13 +451,13 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
     const int t0 = split * a.tiles_per_split;
     const int t1 = in_sgpr(t0 + a.tiles_per_split < tiles ? t0 + a.tiles_per_split : tiles);
 
-    Rows<D, 2> w;
+    Rows<D, NQ> w;
     rows_init(w);
     load_q(w, a, b, hk, row0);
     // the last key of the lane's rows
-    int64_t mine[2];
+    int64_t mine[NQ];
 #pragma unroll
-    for (int qb = 0; qb < 2; ++qb) {
+    for (int qb = 0; qb < NQ; ++qb) {
         const int row = row0 + 16 * qb + (lane & 15);
         mine[qb] = a.causal ? start + (row < a.rows ? row : a.rows - 1) / a.group : int64_t(1) << 40;
     }
@@ -527,17 +529,19 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
         issue_v(t + 1, vn);
         ++t;
         if (live == 0) return;  // the same in every wave
-        uint64_t allowed[2] = {~0ull, ~0ull};
+        uint64_t allowed[NQ];
+#pragma unroll
+        for (int qb = 0; qb < NQ; ++qb) allowed[qb] = ~0ull;
         bool odd = false;
         if (partial) {
 #pragma unroll
-            for (int qb = 0; qb < 2; ++qb) allowed[qb] = live & up_to(mine[qb] - 64 * int64_t(t - 1));
+            for (int qb = 0; qb < NQ; ++qb) allowed[qb] = live & up_to(mine[qb] - 64 * int64_t(t - 1));
             if (tidy_v<D, false>(vc, wave * 16, 16, live)) odd_tile = t;
             lds_writes_barrier();
             odd = odd_tile == t;
         }
-        Scores<4, 2> s;
-        Probs<4, 2> p;
+        Scores<4, NQ> s;
+        Probs<4, NQ> p;
         scores(w, f, kc, s);
         if (partial) mask_scores(s, allowed);
         probabilities_checked(w, s, p, c);
@@ -557,7 +561,7 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
             // a run of whole tiles, two per turn; the scores are one tile ahead of the values
             arrive();
             issue_k(t + 1, kbuf1);
-            Scores<4, 2> s0, s1;
+            Scores<4, NQ> s0, s1;
             scores(w, f, kbuf0, s0);
             do {
                 arrive();
@@ -575,7 +579,7 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
             } while (whole(t + 1, m1) && whole(t + 2, m2));
             arrive();
             issue_v(t + 1, vbuf1);
-            Probs<4, 2> p;
+            Probs<4, NQ> p;
             probabilities_checked(w, s0, p, c);
             weighted(w, f, vbuf0, p);
             m0 = m1;
@@ -587,11 +591,13 @@ __global__ __launch_bounds__(256, 2) void attention_kernel(AttnArgs a) {
         }
         if (t < t1) any_step(kbuf1, vbuf1, kbuf0, vbuf0);
     }
-    if (a.splits == 1) {
-        store_o(w, a, b, hk, row0);
-    } else {
-        store_part(w, a, ((int64_t(b) * a.kv_heads + hk) * a.splits + split) * a.rows, row0);
+    if constexpr (NQ == 2) {  // 64 rows are taken unsplit only
+        if (a.splits > 1) {
+            store_part(w, a, ((int64_t(b) * a.kv_heads + hk) * a.splits + split) * a.rows, row0);
+            return;
+        }
     }
+    store_o(w, a, b, hk, row0);
 }
 
 // Few rows (one or two blocks of 16: decoded tokens): bound by reading the keys and values once.  Every
@@ -876,8 +882,8 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
 }
 
 template <int D>
-hipError_t launch_d(const AttnArgs& a, bool is_short, hipStream_t stream) {
-    if (is_short) {
+hipError_t launch_d(const AttnArgs& a, const AttnPlan& plan, hipStream_t stream) {
+    if (plan.is_short) {
         const unsigned grid = unsigned(a.row_tiles) * unsigned(a.splits) * unsigned(a.kv_heads) * unsigned(a.batch);
         if (a.rows <= 16)
             hipLaunchKernelGGL((attention_short_kernel<D, 1>), dim3(grid), dim3(256), 0, stream, a);
@@ -886,7 +892,10 @@ hipError_t launch_d(const AttnArgs& a, bool is_short, hipStream_t stream) {
         return hipGetLastError();
     }
     const int64_t grid = int64_t(a.row_tiles) * a.splits * a.kv_heads * a.batch;
-    hipLaunchKernelGGL((attention_kernel<D>), dim3(unsigned(grid)), dim3(256), 0, stream, a);
+    if (plan.tile_rows == 64)
+        hipLaunchKernelGGL((attention_kernel<D, 1>), dim3(unsigned(grid)), dim3(256), 0, stream, a);
+    else
+        hipLaunchKernelGGL((attention_kernel<D, 2>), dim3(unsigned(grid)), dim3(256), 0, stream, a);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
     const int64_t rows = int64_t(a.batch) * a.kv_heads * a.rows;
@@ -900,35 +909,43 @@ constexpr int kMaxShortSplits = 64;     // a lane per split in the join
 
 // Which kernel, and how the keys are split: the one whose estimated time is less (one row block, 16 or 32 rows,
 // always goes to the few-rows kernel).  The estimates (us, D = 64 / 128) are fits to measured calls of 8 to 96 heads, 64 to
-// 2048 rows and 200 to 8192 keys: in five of 92 of them the other kernel is 7% to 12% faster, in the rest less or
-// not.  Measured (few / many, us): 512 x 512, 24 heads of 128: 14 / 17; 512 x 2048, 16 heads
-// of 128: 26 / 33; 1024 x 1024, 24 heads of 128: 33 / 28, of 64: 17 / 18; 4 x 512 x 512, 24 heads of 128: 38 / 26.
-//   LOWBIT_ATTENTION=few|many in the environment forces the kernel (A/B runs and tests).
+// 4608 rows and 200 to 8192 keys: in seven of 108 of them the other kernel is 7% to 11% faster, in the rest less or
+// not.  Measured (few / many, us): 256 x 1024, 24 heads of 128: 14 / 24; 512 x 2048, 16 heads of 128: 25 / 30; 512 x 512, 24
+// heads of 128: 14 / 12; 1024 x 1024, 24 heads of 128: 33 / 25, of 64: 16 / 17; 4 x 512 x 512, 24 heads of 128: 37 / 24.
+//   LOWBIT_ATTENTION=few|many|many64|many128 in the environment forces the kernel, or also its rows (A/B runs and tests).
 //
 // The few-rows kernel (32 rows per workgroup, its waves over the keys, two or three workgroups per compute unit):
-// 5, 0.0049 / 0.0093 a key for a workgroup alone on its compute unit, 0.45 of that for each beside it, and 4.5 / 6
+// 6.2 / 7, 0.0049 / 0.0093 a key for a workgroup alone on its compute unit, 0.45 of that for each beside it, and 4.5 / 6
 // for each further round.  Keys are split until every compute unit has a workgroup of three tiles a wave at least
 // (512 workgroups were slower at 1024 rows, 27 against 17, and at 40007 keys, 33 against 32); the join costs 10 / 12.
 double few_us(int64_t groups, int64_t keys, bool joins, int head_dim) {
     const int64_t room = kComputeUnits * (head_dim == 64 ? 3 : 2);
     auto load = [](int64_t n) { return n <= kComputeUnits ? 1.0 : 0.55 + 0.45 * double(n) / kComputeUnits; };
     const int64_t rounds = groups == 0 ? 0 : (groups - 1) / room;  // full ones before the last
-    return 5.0 + (joins ? head_dim == 64 ? 10.0 : 12.0 : 0.0) + double(rounds) * (head_dim == 64 ? 4.5 : 6.0) +
+    return (head_dim == 64 ? 6.2 : 7.0) + (joins ? head_dim == 64 ? 10.0 : 12.0 : 0.0) + double(rounds) * (head_dim == 64 ? 4.5 : 6.0) +
            double(keys) * (head_dim == 64 ? 0.0049 : 0.0093) * (double(rounds) * load(room) + load(groups - rounds * room));
 }
-// The other kernel (128 rows per workgroup): 5 / 9, and 0.79 / 1.16 a tile of 64 keys, times 0.75 for each workgroup on
-// a compute unit that has more than one.  Split, it runs two workgroups per compute unit, of four tiles at least, and
-// the join costs 6, 0.4 / 0.15 a split, and 7 / 14 for 512 workgroups' parts to go to memory and back.
-double many_us(int64_t groups, int64_t tiles, int64_t splits, int head_dim) {
-    const double load = groups <= kComputeUnits ? 1.0 : 0.75 * double(tiles_of(groups, kComputeUnits));
-    return (head_dim == 64 ? 5.0 : 9.0) + double(tiles) * (head_dim == 64 ? 0.79 : 1.16) * load +
-           (splits > 1 ? 6.0 + (head_dim == 64 ? 0.4 : 0.15) * double(splits) +
-                             (head_dim == 64 ? 7.0 : 14.0) * double(groups) / (2 * kComputeUnits)
-                       : 0.0);
+// The other kernel: a start, and a time per tile of 64 keys for a compute unit that has up to n = ceil(groups / 256)
+// workgroups: 5 / 9 and 0.79 / 1.16 of one of 128 rows alone, times 0.75 n from two on.  With 64 rows at a time 5 / 5.5,
+// and as in the table: they fill the units more evenly, and four of them of D = 64 fit one; but they read twice as
+// much LDS per product.  Measured (128 / 64 rows, us): 2 x 1533 x 1533, 16 heads of 64: 33 / 30; 4 x 300 x 300, 24
+// heads of 128: 21 / 14; 4608 x 4608, 24 heads of 128: 267 / 313; causal 1533 x 1533, 24 heads of 128: 43 / 31, 4608 x
+// 4608: 161 / 174.
+double many_us(int64_t tiles, int64_t groups, int tile_rows, int head_dim) {
+    const double n = double(tiles_of(groups, kComputeUnits)), whole = head_dim == 64 ? 0.79 : 1.16;
+    if (tile_rows == 128) return (head_dim == 64 ? 5.0 : 9.0) + double(tiles) * whole * (n <= 1 ? 1.0 : 0.75 * n);
+    if (head_dim == 64) return 5.0 + double(tiles) * whole * (0.1 + 0.42 * n);
+    return 5.5 + double(tiles) * whole * (n <= 1 ? 0.7 : n <= 2 ? 1.0 : 0.3 + 0.48 * n);
+}
+// Keys split: two workgroups of 128 rows per compute unit, of four tiles at least; the join costs 8 / 7, 0.4 / 0.15 a
+// split, and 7 / 14 for 512 workgroups' parts to go to memory and back.
+double join_us(int64_t groups, int64_t splits, int head_dim) {
+    return (head_dim == 64 ? 8.0 : 7.0) + (head_dim == 64 ? 0.4 : 0.15) * double(splits) + (head_dim == 64 ? 7.0 : 14.0) * double(groups) / (2 * kComputeUnits);
 }
 
 // may_split false: no workspace to split with.
-AttnPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t kv_len, int head_dim, bool may_split) {
+AttnPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t kv_len, int head_dim, bool causal,
+                        bool may_split) {
     // few rows
     const int64_t few_rows = rows <= 16 ? 16 : 32, few_groups = batch * kv_heads * tiles_of(rows, few_rows);
     const int64_t few_tiles = tiles_of(kv_len, kShortKeys);
@@ -938,29 +955,43 @@ AttnPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t k
     few_splits = few_splits < 1 || !may_split ? 1 : few_splits;
     const double few = few_us(few_groups * few_splits, tiles_of(few_tiles, few_splits) * kShortKeys, few_splits > 1, head_dim);
     // many rows
-    const int64_t groups = batch * kv_heads * tiles_of(rows, 128), tiles = tiles_of(kv_len, 64);
-    int64_t splits = groups >= kComputeUnits || groups == 0 ? 1 : 2 * kComputeUnits / groups;
+    const int64_t groups = batch * kv_heads * tiles_of(rows, 128), halves = batch * kv_heads * tiles_of(rows, 64);
+    const int64_t tiles = tiles_of(kv_len, 64);
+    const double full = many_us(tiles, groups, 128, head_dim), half = many_us(tiles, halves, 64, head_dim);
+    // causal: the row tiles with the most keys decide where all are resident at once
+    int tile_rows = halves <= kMaxGrid256 && (half < full || (causal && groups <= 2 * kComputeUnits)) ? 64 : 128;
+    double many = tile_rows == 64 ? half : full;
+    int64_t splits = groups >= kComputeUnits || groups == 0 || !may_split ? 1 : 2 * kComputeUnits / groups;
     splits = splits < tiles / 4 ? splits : tiles / 4;
-    splits = splits < 1 || !may_split ? 1 : splits;
-    double many = many_us(groups * splits, tiles_of(tiles, splits), splits, head_dim);
-    const double whole = many_us(groups, tiles, 1, head_dim);
-    if (whole <= many) {
-        splits = 1;
-        many = whole;
+    if (splits > 1) {
+        const double joined = many_us(tiles_of(tiles, splits), groups * splits, 128, head_dim) + join_us(groups * splits, splits, head_dim);
+        if (joined < many) {
+            many = joined;
+            tile_rows = 128;
+        } else {
+            splits = 1;
+        }
     }
+    splits = splits < 1 ? 1 : splits;
 
     AttnPlan p{};
     p.is_short = rows <= 32 || (few <= many && few_groups <= kMaxGrid256);
     if (const char* force = std::getenv("LOWBIT_ATTENTION")) {
         if (std::strcmp(force, "few") == 0) p.is_short = true;
-        if (std::strcmp(force, "many") == 0) p.is_short = false;
+        if (std::strncmp(force, "many", 4) == 0) p.is_short = false;
+        if (std::strcmp(force, "many128") == 0) tile_rows = 128;
+        if (std::strcmp(force, "many64") == 0 && halves <= kMaxGrid256) {
+            tile_rows = 64;
+            splits = 1;
+        }
     }
     if (p.is_short) {
         p.row_tiles = int(tiles_of(rows, few_rows));
         p.splits = int(few_splits);
         p.tiles_per_split = 0;
     } else {
-        p.row_tiles = int(tiles_of(rows, 128));
+        p.tile_rows = tile_rows;
+        p.row_tiles = int(tiles_of(rows, tile_rows));
         p.tiles_per_split = int(tiles_of(tiles, splits));
         p.splits = p.tiles_per_split > 0 ? int(tiles_of(tiles, p.tiles_per_split)) : 1;
     }
@@ -977,7 +1008,7 @@ hipError_t launch_attention(AttnArgs a, int head_dim, const AttnPlan& plan, void
     a.counters = static_cast<uint32_t*>(workspace);
     a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kWorkspaceCounterBytes);
     a.part_ml = a.part + plan.part_rows * head_dim;
-    return head_dim == 64 ? launch_d<64>(a, plan.is_short, stream) : launch_d<128>(a, plan.is_short, stream);
+    return head_dim == 64 ? launch_d<64>(a, plan, stream) : launch_d<128>(a, plan, stream);
 }
 
 }  // namespace lowbit

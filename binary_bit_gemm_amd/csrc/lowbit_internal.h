@@ -214,13 +214,15 @@ struct AttnArgs {
 // How a call is divided: row tiles of a kv head, ranges of key tiles, and the workspace of the ranges'
 // partial results (bytes 0: none; without one the call runs unsplit).
 struct AttnPlan {
+    int tile_rows;  // of a workgroup of the kernel for many rows: 64 or 128
     bool is_short;  // the kernel for few rows
     int row_tiles, splits, tiles_per_split;
     int64_t part_rows;
     size_t bytes;
 };
 constexpr int64_t kMaxGrid256 = (int64_t(1) << 24) - 1;  // workgroups of 256 threads in a launch (2^32 threads)
-AttnPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t kv_len, int head_dim, bool may_split = true);
+AttnPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t kv_len, int head_dim, bool causal,
+                        bool may_split = true);
 hipError_t launch_attention(AttnArgs a, int head_dim, const AttnPlan& plan, void* workspace, hipStream_t stream);
 
 }  // namespace lowbit

@@ -395,8 +395,8 @@ int lowbit_qk_norm_rope(const lowbit_qk_problem* problem, void* stream);
  *      first 4096 bytes hold arrival counters that every call leaves at zero, so one workspace serves calls
  *      of any shapes in turn (and lowbit_gemm_ex's, lowbit_gemm_affine_ex's and lowbit_gemm_lora's).  With a
  *      NULL or too small workspace the call runs unsplit.  Calls that share it must not run concurrently.
- * The size depends on the shape only (0: no split, or invalid arguments).  LOWBIT_ATTENTION=few|many in the
- * environment forces one of the two kernels (for A/B runs and tests).  The descriptor is read
+ * The size depends on the shape only (0: no split, or invalid arguments).  LOWBIT_ATTENTION=few|many|many64|many128
+ * in the environment forces one of the kernels, or also its rows per workgroup (for A/B runs and tests).  The descriptor is read
  * before the call returns.  key_lens and q_start need 4-byte alignment, q, k, v, o and workspace 16.
  */
 typedef struct lowbit_attention_problem {

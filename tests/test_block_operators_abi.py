@@ -133,7 +133,7 @@ def test_null_problems():
     assert L.lowbit_attention_workspace_size(None) == 0
 
 
-@pytest.mark.parametrize("kernel", [None, "few", "many"])
+@pytest.mark.parametrize("kernel", [None, "few", "many", "many64", "many128"])
 def test_attention_plans(kernel, monkeypatch):
     """Workspace sizes over many shapes: none where keys are not split, room for every split's rows otherwise."""
     if kernel:

@@ -67,9 +67,9 @@ def make(B, Lq, Lk, Hq, Hk, D, seed=0):
     return q, k, v
 
 
-@pytest.fixture(params=["few", "many", "auto"])
+@pytest.fixture(params=["few", "many", "many64", "many128", "auto"])
 def kernel(request, monkeypatch):
-    """Each of the two kernels in turn, and the one that the library takes."""
+    """Each of the kernels in turn (many rows: 64 and 128 per workgroup), and the one that the library takes."""
     if request.param != "auto":
         monkeypatch.setenv("LOWBIT_ATTENTION", request.param)
     return request.param
