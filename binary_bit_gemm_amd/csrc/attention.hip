@@ -414,7 +414,10 @@ __device__ __forceinline__ uint64_t up_to(int64_t rel) {
 }
 
 // Many rows: a workgroup of 4 waves takes 64 NQ rows of one kv head, a wave 16 NQ of them; tiles of 64 keys go
-// through LDS, double-buffered, by direct copies one tile ahead.
+// through LDS, double-buffered, by direct copies one tile ahead.  Bound by the two products and the exponentials beside them,
+// then by power: 4608 x 4608, 24 heads of 128: 264 us = 988 TFLOP/s, the clock at 1.7 GHz and the matrix cores
+// busy for 66% of the steady state's cycles; the rest is 864 workgroups in 512 places (two rounds for 1.7).  Heads of 64 have
+// half the products per exponential: 4608 x 4608, 24 heads: 159 us = 820 TFLOP/s.
 template <int D, int NQ>
 __global__ __launch_bounds__(256, D == 64 && NQ == 1 ? 4 : 2) void attention_kernel(AttnArgs a) {
     constexpr int kRows = 64 * NQ;                // of a workgroup
@@ -603,8 +606,9 @@ __global__ __launch_bounds__(256, D == 64 && NQ == 1 ? 4 : 2) void attention_ker
 // Few rows (one or two blocks of 16: decoded tokens): bound by reading the keys and values once.  Every
 // wave takes its own tiles of 32 keys (tile w, w + 4, .. of the workgroup's range for wave w), copied into its own part of
 // LDS, so no barrier stands between the copies; two workgroups share a compute unit, and while one wave
-// computes the others' copies are on their way (up to 128 KB per compute unit).  The waves' results are joined through LDS; where the keys are also split across workgroups, each leaves
-// its partial result in the workspace and the last one to arrive joins them.  Both joins go in a fixed
+// computes the others' copies are on their way (up to 128 KB per compute unit).  Measured: 1 x 40007 keys, 32 / 8 heads of
+// 128: 36 us = 4.5 TB/s (31 us and 5.3 TB/s in the kernel); 4 x 4099 keys: 17 us.  The waves' results are joined through LDS;
+// where the keys are also split across workgroups, each leaves its partial result in the workspace and the last one to arrive joins them.  Both joins go in a fixed
 // order (wave 0 .., split 0 ..), so results do not depend on timing.
 constexpr int kShortKeys = 32;
 
@@ -909,7 +913,7 @@ constexpr int kMaxShortSplits = 64;     // a lane per split in the join
 
 // Which kernel, and how the keys are split: the one whose estimated time is less (one row block, 16 or 32 rows,
 // always goes to the few-rows kernel).  The estimates (us, D = 64 / 128) are fits to measured calls of 8 to 96 heads, 64 to
-// 4608 rows and 200 to 8192 keys: in seven of 108 of them the other kernel is 7% to 11% faster, in the rest less or
+// 4608 rows and 200 to 8192 keys: in seven of 108 of them the other kernel is 7% to 14% faster, in the rest less or
 // not.  Measured (few / many, us): 256 x 1024, 24 heads of 128: 14 / 24; 512 x 2048, 16 heads of 128: 25 / 30; 512 x 512, 24
 // heads of 128: 14 / 12; 1024 x 1024, 24 heads of 128: 33 / 25, of 64: 16 / 17; 4 x 512 x 512, 24 heads of 128: 37 / 24.
 //   LOWBIT_ATTENTION=few|many|many64|many128 in the environment forces the kernel, or also its rows (A/B runs and tests).
@@ -958,8 +962,7 @@ AttnPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t k
     const int64_t groups = batch * kv_heads * tiles_of(rows, 128), halves = batch * kv_heads * tiles_of(rows, 64);
     const int64_t tiles = tiles_of(kv_len, 64);
     const double full = many_us(tiles, groups, 128, head_dim), half = many_us(tiles, halves, 64, head_dim);
-    // causal: the row tiles with the most keys decide where all are resident at once
-    int tile_rows = halves <= kMaxGrid256 && (half < full || (causal && groups <= 2 * kComputeUnits)) ? 64 : 128;
+    int tile_rows = halves <= kMaxGrid256 && half < full ? 64 : 128;
     double many = tile_rows == 64 ? half : full;
     int64_t splits = groups >= kComputeUnits || groups == 0 || !may_split ? 1 : 2 * kComputeUnits / groups;
     splits = splits < tiles / 4 ? splits : tiles / 4;
@@ -973,6 +976,9 @@ AttnPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t k
         }
     }
     splits = splits < 1 ? 1 : splits;
+    // causal: the row tiles with the most keys decide where all are resident at once (the workspace's size and the
+    // kernel do not depend on it)
+    if (causal && splits == 1 && groups <= 2 * kComputeUnits && halves <= kMaxGrid256) tile_rows = 64;
 
     AttnPlan p{};
     p.is_short = rows <= 32 || (few <= many && few_groups <= kMaxGrid256);

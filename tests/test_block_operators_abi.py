@@ -148,6 +148,7 @@ def test_attention_plans(kernel, monkeypatch):
                 for hq, hk in ((1, 1), (32, 8), (24, 24), (64, 1)):
                     for D in (64, 128):
                         n = size(batch=batch, q_len=q_len, kv_len=kv_len, q_heads=hq, kv_heads=hk, head_dim=D)
+                        assert n == size(batch=batch, q_len=q_len, kv_len=kv_len, q_heads=hq, kv_heads=hk, head_dim=D, causal=1)
                         if n:
                             rows = batch * hq * q_len
                             assert (n - 4096) % ((D + 2) * 4) == 0 and n >= 4096 + 2 * rows * (D + 2) * 4
