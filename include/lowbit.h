@@ -16,6 +16,8 @@
  *     (mlx-vlm Prism Bonsai ternary 2-bit guide, section 运行前提 / prerequisites);
  *   - weights kept as packed uint32 words plus scales ("backend/ -- FastAPI Mac backend",
  *     section "Checkpoint layout").
+ * Around these linears: low-rank adapters (lowbit_gemm_lora), norms and rotation of queries and keys
+ * (lowbit_qk_norm_rope) and attention (lowbit_attention), at the end.
  *
  * ---------------------------------------------------------------------------------
  * Packed weight format (the pages leave the bit layout open; this is the library's):
