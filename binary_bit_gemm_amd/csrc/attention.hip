@@ -20,6 +20,9 @@
 //     then seen (fp32 and bf16 have the exponents for it), as long as every new p is below 2, which one
 //     OR over the packed probabilities tells (bit 14 of a positive bf16 is set from 2 on); only
 //     otherwise is the maximum taken, O and l rescaled and the probabilities computed again.
+// The exponents c s - c m are one fused operation each, exact before its one rounding.  Past kLarge the rounding of c m alone is
+// worth more than the headroom, so c s is rounded too, the same way, and equal scores have equal exponents again
+// (the row's other scores are then a unit of c m, 32 powers of two, or more away).
 //
 // Rounding to bf16: the probabilities before the second product (the matrix cores' input; relative
 // 2^-8 each, averaged over the keys) and O at the store.  Scores, m, l and O are fp32.
@@ -44,6 +47,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 constexpr float kNegInf = -__builtin_inff();
 constexpr float kHeadroom = 32.f;  // powers of two between the largest score and 1; p reaches 2^33 times as much before m moves
+constexpr float kLarge = 0x1p28f;  // of |c m|: its last place is worth 32 from here on
 constexpr uint32_t kTooLarge = 0x40004000u;  // a packed pair of p has one of 2 or more
 
 // ---- layouts in LDS: rows of D elements in 16-byte chunks, chunk c of row r at position c ^ swz(r) ----
@@ -153,6 +157,7 @@ __device__ __forceinline__ void mask_scores(Scores<KB, NQ>& x, const uint64_t (&
 // m follows the largest of the scores where it has to, and l and O follow m.
 template <int D, int NQ, int KB>
 __device__ __forceinline__ void grow(Rows<D, NQ>& w, const Scores<KB, NQ>& x, float c) {
+#pragma clang fp contract(off)  // c m is the rounded product, as in probabilities()
 #pragma unroll
     for (int qb = 0; qb < NQ; ++qb) {
         float top = kNegInf;
@@ -178,20 +183,27 @@ __device__ __forceinline__ void grow(Rows<D, NQ>& w, const Scores<KB, NQ>& x, fl
     }
 }
 
-// The probabilities of x; returns an OR of them all.
-template <int D, int NQ, int KB>
+// The probabilities of x; returns an OR of them all.  ANY: rows whose |c m| is kLarge or more among them, which subtract it
+// after the product's rounding.
+template <bool ANY, int D, int NQ, int KB>
 __device__ __forceinline__ uint32_t probabilities(const Rows<D, NQ>& w, const Scores<KB, NQ>& x, Probs<KB, NQ>& p, float c) {
     uint32_t any = 0;
 #pragma unroll
     for (int qb = 0; qb < NQ; ++qb) {
-        const float mc = w.mc[qb] == kNegInf ? 0.f : w.mc[qb];  // without a key yet every score is -inf
+        const float all = w.mc[qb] == kNegInf ? 0.f : w.mc[qb];  // without a key yet every score is -inf
+        const bool large = ANY && !(__builtin_fabsf(all) < kLarge);
+        const float mc = large ? 0.f : all, after = large ? all : 0.f;
+        auto power = [&](float s) __attribute__((always_inline)) {
+            const float e = __builtin_fmaf(s, c, -mc);
+            return __builtin_amdgcn_exp2f(ANY ? e - after : e);
+        };
 #pragma unroll
         for (int kk = 0; kk < KB / 2; ++kk)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const f32x4_t& s = x.s[2 * kk + e / 2][qb];
-                const float lo = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * (e % 2)], c, -mc));
-                const float hi = __builtin_amdgcn_exp2f(__builtin_fmaf(s[2 * (e % 2) + 1], c, -mc));
+                const float lo = power(s[2 * (e % 2)]);
+                const float hi = power(s[2 * (e % 2) + 1]);
                 const uint32_t v = pack_bf16(lo, hi);
                 p.p[kk][qb][e] = v;
                 any |= v;
@@ -227,13 +239,19 @@ __device__ __forceinline__ void weighted(Rows<D, NQ>& w, const Offsets<D>& f, co
 // The probabilities of x, to a maximum that has moved if one of them would reach 2.
 template <int D, int NQ, int KB>
 __device__ __forceinline__ void probabilities_checked(Rows<D, NQ>& w, const Scores<KB, NQ>& x, Probs<KB, NQ>& p, float c) {
-    const uint32_t any = probabilities(w, x, p, c);
-    bool move = (any & kTooLarge) != 0;
+    const uint32_t any = probabilities<false>(w, x, p, c);
+    bool again = (any & kTooLarge) != 0;
 #pragma unroll
-    for (int qb = 0; qb < NQ; ++qb) move = move || w.mc[qb] == kNegInf;
-    if (__any(move)) {
+    for (int qb = 0; qb < NQ; ++qb) again = again || !(__builtin_fabsf(w.mc[qb]) < kLarge);  // no key yet (-inf) among them
+    if (__any(again)) {
         grow(w, x, c);
-        probabilities(w, x, p, c);
+        bool large = false;
+#pragma unroll
+        for (int qb = 0; qb < NQ; ++qb) large = large || (w.mc[qb] != kNegInf && !(__builtin_fabsf(w.mc[qb]) < kLarge));
+        if (__any(large))
+            probabilities<true>(w, x, p, c);
+        else
+            probabilities<false>(w, x, p, c);
     }
 }
 

@@ -264,3 +264,29 @@ def test_in_a_graph(kernel):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("power", [16, 24, 27, 28, 29, 31, 34, 40, 60, 90])
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("shape", [(1, 40, 1000, 2, 2, 128), (2, 90, 300, 4, 2, 64), (1, 1, 5000, 8, 2, 64), (1, 40, 4000, 2, 2, 128)])
+def test_scores_of_any_size(shape, sign, power, kernel):
+    """Queries times a power of two: a row's largest score then takes all of the softmax, and every key is there twice, so its
+    result is the mean of two values.  Rows whose largest scores lie closer than an fp32 sum of 128 products is off (2^-12 of
+    the power, see above) or closer than 2^-4 of the power (an exponent of 2^12 at the least) are left out."""
+    B, Lq, Lk, Hq, Hk, D = shape
+    q, k, v = make(B, Lq, Lk, Hq, Hk, D, seed=30)
+    if sign < 0:  # every score below zero
+        q, k = q.abs(), -k.abs()
+    k[:, Lk // 2:] = k[:, :Lk // 2]
+    s = torch.einsum("bthd,bjhd->bhtj", q.double().cpu(), k.double().cpu()[:, :Lk // 2].repeat_interleave(Hq // Hk, 2))
+    top, at = s.topk(2, -1)
+    clear = (top[..., 0] - top[..., 1] > 2.0 ** -4 * math.sqrt(D)).transpose(1, 2)  # [B, Lq, Hq]
+    assert clear.float().mean() > 0.5
+    vd = v.double().cpu().repeat_interleave(Hq // Hk, 2).transpose(1, 2)  # [B, Hq, Lk, D]
+    first = at[..., :1].expand(-1, -1, -1, D)
+    a, b = vd.gather(2, first), vd.gather(2, first + Lk // 2)
+    want, mag = ((a + b) / 2).transpose(1, 2), ((a.abs() + b.abs()) / 2).transpose(1, 2)
+    q = (q.float() * 2.0 ** power).bfloat16()
+    for ws in (None, scratch(q, k, v)):
+        got = lb.attention(q, k, v, workspace=ws)
+        check(got[clear], want[clear].numpy(), mag[clear].numpy())
