@@ -4,6 +4,7 @@
 
 #include <cmath>
 #include <cstring>
+#include <limits>
 
 #include "../../include/lowbit.h"
 #include "lowbit_internal.h"
@@ -15,6 +16,7 @@ bool aligned(const void* p, uintptr_t bytes) { return reinterpret_cast<uintptr_t
 constexpr int64_t kMaxDim = (int64_t(1) << 31) - 1;
 constexpr int64_t kMaxStride = int64_t(1) << 40;
 constexpr int kMaxHeads = 1 << 16;
+constexpr double kLog2E = 1.4426950408889634074;
 
 bool stride_ok(int64_t s) { return s >= 0 && s <= kMaxStride && s % 8 == 0; }
 
@@ -59,7 +61,8 @@ int attention_args(const lowbit_attention_problem* p, lowbit::AttnArgs& a) {
     if (p->q_len > kMaxDim || p->kv_len > kMaxDim - 64) return LOWBIT_E_UNSUPPORTED;
     if (p->q_heads > kMaxHeads || p->batch > kMaxHeads) return LOWBIT_E_UNSUPPORTED;
     if (p->kv_heads == 0 ? p->q_heads != 0 : p->q_heads % p->kv_heads != 0) return LOWBIT_E_INVALID;
-    if (!(p->scale > 0.f) || std::isinf(p->scale)) return LOWBIT_E_INVALID;
+    // the kernels take scale * log2(e), which has to be finite as well
+    if (!(p->scale > 0.f) || double(p->scale) * kLog2E > double(std::numeric_limits<float>::max())) return LOWBIT_E_INVALID;
     for (int64_t s : {p->q_batch, p->q_token, p->q_head, p->k_batch, p->k_token, p->k_head, p->v_batch, p->v_token,
                       p->v_head, p->o_batch, p->o_token, p->o_head})
         if (!stride_ok(s)) return LOWBIT_E_INVALID;
@@ -89,7 +92,7 @@ int attention_args(const lowbit_attention_problem* p, lowbit::AttnArgs& a) {
     a.rows = int(rows);
     a.kv_len = int(p->kv_len);
     a.causal = p->causal != 0;
-    a.scale_log2 = float(double(p->scale) * 1.4426950408889634074);
+    a.scale_log2 = float(double(p->scale) * kLog2E);
     a.q = static_cast<const uint16_t*>(p->q);
     a.k = static_cast<const uint16_t*>(p->k);
     a.v = static_cast<const uint16_t*>(p->v);

@@ -383,7 +383,7 @@ int lowbit_qk_norm_rope(const lowbit_qk_problem* problem, void* stream);
  *      Strides in elements, multiples of 8 (columns of a fused QKV output need no copy); k_token and
  *      v_token from head_dim to 2^24.  o must not overlap an input.
  *   q_heads % kv_heads == 0: q head h reads kv head h / (q_heads / kv_heads).  head_dim 64 or 128.
- *   scale > 0, e.g. 1 / sqrt(head_dim).  batch * kv_heads * ceil(q_len * q_heads / kv_heads / 128) < 2^24.
+ *   0 < scale <= 2^127, e.g. 1 / sqrt(head_dim).  batch * kv_heads * ceil(q_len * q_heads / kv_heads / 128) < 2^24.
  *   Query t of batch entry b takes key j where all of these hold:
  *      key_lens NULL or j < key_lens[b]      (device int32 [batch]; a cache's filled part)
  *      key_mask NULL or key_mask[b * mask_batch + j] != 0   (device uint8, 1 byte a key; padding)

@@ -127,6 +127,14 @@ def test_attention_refusals(change, want):
     assert attention(**change) == want
 
 
+def test_attention_scale_limits():
+    """scale * log2(e) is what the kernels multiply by: it has to be a number too."""
+    assert attention(scale=3.0e38) == INVALID and attention(scale=2.0 ** 127 * 1.4) == INVALID
+    # past the scale's check the next one answers
+    assert attention(scale=2.0 ** 127, q=0) == INVALID and attention(scale=2.0 ** 127, q=A + 8) == ALIGN
+    assert attention(scale=1e-38, q=A + 8) == ALIGN
+
+
 def test_null_problems():
     L = _lib.lib()
     assert L.lowbit_qk_norm_rope(None, None) == INVALID and L.lowbit_attention(None, None, 0, None) == INVALID
