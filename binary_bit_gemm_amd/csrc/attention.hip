@@ -26,6 +26,7 @@
 //
 // Rounding to bf16: the probabilities before the second product (the matrix cores' input; relative
 // 2^-8 each, averaged over the keys) and O at the store.  Scores, m, l and O are fp32.
+#include <cstdio>
 #include <cstdlib>
 #include <cstring>
 
@@ -903,6 +904,13 @@ __global__ __launch_bounds__(256) void attention_join_kernel(AttnArgs a) {
     for (int e = 0; e < D / 64; ++e) dst[(D / 64) * lane + e] = float_to_bf16_bits(o[e] * f);
 }
 
+// The launch log's line of an attention kernel.
+void trace_attention(const char* form, int tile_rows, const AttnArgs& a, int head_dim, unsigned grid) {
+    std::fprintf(stderr, "lowbit: attention %s rows=%d splits=%d grid=%u block=256 problem=%dx%dx%dx%d kv_heads=%d dim=%d%s\n", form,
+                 tile_rows, a.splits, grid, a.batch, a.rows / a.group, a.kv_len, a.kv_heads * a.group, a.kv_heads, head_dim,
+                 a.causal ? " causal" : "");
+}
+
 template <int D>
 hipError_t launch_d(const AttnArgs& a, const AttnPlan& plan, hipStream_t stream) {
     if (plan.is_short) {
@@ -911,7 +919,9 @@ hipError_t launch_d(const AttnArgs& a, const AttnPlan& plan, hipStream_t stream)
             hipLaunchKernelGGL((attention_short_kernel<D, 1>), dim3(grid), dim3(256), 0, stream, a);
         else
             hipLaunchKernelGGL((attention_short_kernel<D, 2>), dim3(grid), dim3(256), 0, stream, a);
-        return hipGetLastError();
+        const hipError_t e = hipGetLastError();
+        if (e == hipSuccess && trace_enabled()) trace_attention("few", a.rows <= 16 ? 16 : 32, a, D, grid);
+        return e;
     }
     const int64_t grid = int64_t(a.row_tiles) * a.splits * a.kv_heads * a.batch;
     if (plan.tile_rows == 64)
@@ -919,6 +929,7 @@ hipError_t launch_d(const AttnArgs& a, const AttnPlan& plan, hipStream_t stream)
     else
         hipLaunchKernelGGL((attention_kernel<D, 2>), dim3(unsigned(grid)), dim3(256), 0, stream, a);
     hipError_t e = hipGetLastError();
+    if (e == hipSuccess && trace_enabled()) trace_attention("many", plan.tile_rows, a, D, unsigned(grid));
     if (e != hipSuccess || a.splits == 1) return e;
     const int64_t rows = int64_t(a.batch) * a.kv_heads * a.rows;
     hipLaunchKernelGGL((attention_join_kernel<D>), dim3(unsigned((rows + 3) / 4)), dim3(256), 0, stream, a);
@@ -965,9 +976,9 @@ double join_us(int64_t groups, int64_t splits, int head_dim) {
     return (head_dim == 64 ? 8.0 : 7.0) + (head_dim == 64 ? 0.4 : 0.15) * double(splits) + (head_dim == 64 ? 7.0 : 14.0) * double(groups) / (2 * kComputeUnits);
 }
 
-// may_split false: no workspace to split with.
-AttnPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t kv_len, int head_dim, bool causal,
-                        bool may_split) {
+// may_split false: no workspace to split with.  Of a's arrays only whether they are there counts.
+AttnPlan plan_attention(const AttnArgs& a, int head_dim, bool may_split) {
+    const int64_t batch = a.batch, kv_heads = a.kv_heads, rows = a.rows, kv_len = a.kv_len;
     // few rows
     const int64_t few_rows = rows <= 16 ? 16 : 32, few_groups = batch * kv_heads * tiles_of(rows, few_rows);
     const int64_t few_tiles = tiles_of(kv_len, kShortKeys);
@@ -994,9 +1005,16 @@ AttnPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t k
         }
     }
     splits = splits < 1 ? 1 : splits;
-    // causal: the row tiles with the most keys decide where all are resident at once (the workspace's size and the
-    // kernel do not depend on it)
-    if (causal && splits == 1 && groups <= 2 * kComputeUnits && halves <= kMaxGrid256) tile_rows = 64;
+    // Causal, all row tiles resident at once: those with the most keys decide, and 64 rows share the keys out more evenly,
+    // while the keys are few beside the queries.  In a chunk of queries after a long cache every tile has about as many
+    // keys, and the estimates above hold.  Measured, queries at the end of 1, 1.5, 2, 3, 4 and 8 times as many keys (64 / 128
+    // rows, us): 2560 queries, 24 heads of 128 69 / 77, 109 / 113, 155 / 148, 248 / 218, 337 / 288, 710 / 580; 4096, 16 of 128 92 / 121, 171 / 178,
+    // 248 / 237, 401 / 355, 544 / 470, 1177 / 948; 2560, 24 of 64 40 / 47, 63 / 69, 86 / 90, 134 / 134, 184 / 176, 380 / 348.  (The
+    // workspace's size and the kernel do not depend on it.)
+    const int64_t queries = rows / a.group, reach = a.start == nullptr && queries < kv_len ? queries : kv_len;
+    if (a.causal && splits == 1 && groups <= 2 * kComputeUnits && halves <= kMaxGrid256 &&
+        4 * reach <= (head_dim == 64 ? 12 : 7) * queries)
+        tile_rows = 64;
 
     AttnPlan p{};
     p.is_short = rows <= 32 || (few <= many && few_groups <= kMaxGrid256);

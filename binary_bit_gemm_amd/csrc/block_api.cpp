@@ -174,7 +174,7 @@ int lowbit_gemm_lora(const void* X, const uint32_t* W, const void* S, void* Y, i
 size_t lowbit_attention_workspace_size(const lowbit_attention_problem* p) {
     lowbit::AttnArgs a{};
     if (attention_args(p, a) != LOWBIT_OK || a.batch == 0 || a.rows == 0) return 0;
-    return lowbit::plan_attention(a.batch, a.kv_heads, a.rows, a.kv_len, p->head_dim, a.causal).bytes;
+    return lowbit::plan_attention(a, p->head_dim).bytes;
 }
 
 int lowbit_attention(const lowbit_attention_problem* p, void* workspace, size_t workspace_bytes, void* stream) {
@@ -189,9 +189,9 @@ int lowbit_attention(const lowbit_attention_problem* p, void* workspace, size_t 
     if (!aligned(p->key_lens, 4) || !aligned(p->q_start, 4)) return LOWBIT_E_ALIGN;
     st = lowbit::device_check();
     if (st != LOWBIT_OK) return st;
-    lowbit::AttnPlan plan = lowbit::plan_attention(a.batch, a.kv_heads, a.rows, a.kv_len, p->head_dim, a.causal);
+    lowbit::AttnPlan plan = lowbit::plan_attention(a, p->head_dim);
     if (plan.bytes > 0 && (workspace == nullptr || workspace_bytes < plan.bytes))
-        plan = lowbit::plan_attention(a.batch, a.kv_heads, a.rows, a.kv_len, p->head_dim, a.causal, false);
+        plan = lowbit::plan_attention(a, p->head_dim, false);
     const hipError_t e = lowbit::launch_attention(a, p->head_dim, plan, workspace, static_cast<hipStream_t>(stream));
     return e == hipSuccess ? LOWBIT_OK : lowbit::hip_fail(e);
 }

@@ -221,8 +221,7 @@ struct AttnPlan {
     size_t bytes;
 };
 constexpr int64_t kMaxGrid256 = (int64_t(1) << 24) - 1;  // workgroups of 256 threads in a launch (2^32 threads)
-AttnPlan plan_attention(int64_t batch, int64_t kv_heads, int64_t rows, int64_t kv_len, int head_dim, bool causal,
-                        bool may_split = true);
+AttnPlan plan_attention(const AttnArgs& a, int head_dim, bool may_split = true);
 hipError_t launch_attention(AttnArgs a, int head_dim, const AttnPlan& plan, void* workspace, hipStream_t stream);
 
 }  // namespace lowbit

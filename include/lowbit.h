@@ -430,7 +430,9 @@ int lowbit_check_gemm_args(const void* X, const uint32_t* W, const void* S, cons
  *   lowbit: <family> <configuration> g=<g> bits=<bits> grid=<workgroups> block=<threads>
  *           lds=<dynamic LDS bytes> problems=<M>x<N>x<K>[,<M>x<N>x<K>...]
  * (one line; family resident, skinny, tile16 or tiled32; the configuration names the tile and
- * wave layout, or the resident plan's column blocks, K slices, steps, splits and tiles). */
+ * wave layout, or the resident plan's column blocks, K slices, steps, splits and tiles).  lowbit_attention's line:
+ *   lowbit: attention <few|many> rows=<of a workgroup> splits=<of the keys> grid=<workgroups> block=256
+ *           problem=<batch>x<q_len>x<kv_len>x<q_heads> kv_heads=<kv_heads> dim=<head_dim>[ causal] */
 const char* lowbit_gemm_variant(int64_t M, int64_t N, int64_t K, int g, int bits);
 
 /* Human-readable text for a status code. */

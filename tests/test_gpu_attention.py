@@ -290,3 +290,27 @@ def test_scores_of_any_size(shape, sign, power, kernel):
     for ws in (None, scratch(q, k, v)):
         got = lb.attention(q, k, v, workspace=ws)
         check(got[clear], want[clear].numpy(), mag[clear].numpy())
+
+
+@pytest.mark.parametrize("heads,D,queries,keys,start,rows", [
+    (24, 128, 2560, 2560, "end", 64), (24, 128, 2560, 3840, "end", 64), (24, 128, 2560, 7680, "end", 128),
+    (24, 128, 2560, 20480, "end", 128), (16, 128, 4096, 16384, "end", 128), (24, 128, 2560, 20480, None, 64),
+    (24, 64, 2560, 7680, "end", 64), (24, 64, 2560, 20480, "end", 128),
+    (24, 128, 1100, 8800, "end", 64), (16, 128, 2048, 16384, "end", 64),  # 64 rows fill the compute units better
+])
+def test_rows_of_a_workgroup_for_a_chunk_after_a_long_cache(heads, D, queries, keys, start, rows, capfd, monkeypatch):
+    """A causal prompt takes 64 rows at a time; a chunk of queries after many keys, of which every row tile has about as many, what
+    a call without the causal rule takes.  (Last queries only: their results against the formula.)"""
+    q, k, v = make(1, queries, keys, heads, 1, D, seed=40)
+    k, v = (x.expand(-1, -1, heads, -1) for x in (k, v))
+    first = keys - queries if start else 0
+    s = torch.tensor([first], dtype=torch.int32, device="cuda") if start else None
+    monkeypatch.setenv("LOWBIT_TRACE", "1")
+    capfd.readouterr()
+    got = lb.attention(q, k, v, causal=True, q_start=s)
+    torch.cuda.synchronize()
+    lines = [l for l in capfd.readouterr().err.splitlines() if l.startswith("lowbit: attention ")]
+    assert len(lines) == 1 and f"many rows={rows} splits=1 " in lines[0], lines
+    assert f"problem=1x{queries}x{keys}x{heads} kv_heads={heads} dim={D} causal" in lines[0]
+    last = torch.tensor([first + queries - 3], dtype=torch.int32, device="cuda")
+    check(got[:, -3:, :2], *reference(q[:, -3:, :2], k[:, :, :2], v[:, :, :2], causal=True, start=last))
