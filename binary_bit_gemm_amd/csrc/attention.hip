@@ -470,8 +470,10 @@ __global__ __launch_bounds__(256, D == 64 && NQ == 1 ? 4 : 2) void attention_ker
     const int end = end64 < 0 ? 0 : int(end64);
     const int first = in_sgpr(first64 < 0 ? 0 : first64 < n ? int(first64) : n);
     const int tiles = (end + 63) / 64;
-    const int t0 = split * a.tiles_per_split;
-    const int t1 = in_sgpr(t0 + a.tiles_per_split < tiles ? t0 + a.tiles_per_split : tiles);
+    // the splits share the keys there are, not the keys there could be
+    const int share = a.splits == 1 ? tiles : int(uint32_t(tiles + a.splits - 1) / uint32_t(a.splits));
+    const int t0 = split * share;
+    const int t1 = in_sgpr(t0 + share < tiles ? t0 + share : tiles);
 
     Rows<D, NQ> w;
     rows_init(w);
@@ -1030,12 +1032,11 @@ AttnPlan plan_attention(const AttnArgs& a, int head_dim, bool may_split) {
     if (p.is_short) {
         p.row_tiles = int(tiles_of(rows, few_rows));
         p.splits = int(few_splits);
-        p.tiles_per_split = 0;
     } else {
         p.tile_rows = tile_rows;
         p.row_tiles = int(tiles_of(rows, tile_rows));
-        p.tiles_per_split = int(tiles_of(tiles, splits));
-        p.splits = p.tiles_per_split > 0 ? int(tiles_of(tiles, p.tiles_per_split)) : 1;
+        const int64_t share = tiles_of(tiles, splits);  // no more splits than have a tile
+        p.splits = share > 0 ? int(tiles_of(tiles, share)) : 1;
     }
     const int64_t padded = p.is_short ? int64_t(p.row_tiles) * (rows <= 16 ? 16 : 32) : rows;
     p.part_rows = p.splits > 1 ? batch * kv_heads * padded * p.splits : 0;
@@ -1046,7 +1047,6 @@ AttnPlan plan_attention(const AttnArgs& a, int head_dim, bool may_split) {
 hipError_t launch_attention(AttnArgs a, int head_dim, const AttnPlan& plan, void* workspace, hipStream_t stream) {
     a.row_tiles = plan.row_tiles;
     a.splits = plan.splits;
-    a.tiles_per_split = plan.tiles_per_split;
     a.counters = static_cast<uint32_t*>(workspace);
     a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kWorkspaceCounterBytes);
     a.part_ml = a.part + plan.part_rows * head_dim;

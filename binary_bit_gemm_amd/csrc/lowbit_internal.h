@@ -207,16 +207,16 @@ struct AttnArgs {
     int batch, kv_heads, group, rows, kv_len, causal;  // rows: query tokens x heads of a group
     float scale_log2;                                  // scale * log2(e)
     // set by the launch
-    int row_tiles, splits, tiles_per_split;
+    int row_tiles, splits;
     uint32_t* counters;  // arrivals of a head's splits (short rows), zero between calls
     float *part, *part_ml;
 };
-// How a call is divided: row tiles of a kv head, ranges of key tiles, and the workspace of the ranges'
+// How a call is divided: row tiles of a kv head, ranges of its keys, and the workspace of the ranges'
 // partial results (bytes 0: none; without one the call runs unsplit).
 struct AttnPlan {
     int tile_rows;  // of a workgroup of the kernel for many rows: 64 or 128
     bool is_short;  // the kernel for few rows
-    int row_tiles, splits, tiles_per_split;
+    int row_tiles, splits;
     int64_t part_rows;
     size_t bytes;
 };

@@ -314,3 +314,26 @@ def test_rows_of_a_workgroup_for_a_chunk_after_a_long_cache(heads, D, queries, k
     assert f"problem=1x{queries}x{keys}x{heads} kv_heads={heads} dim={D} causal" in lines[0]
     last = torch.tensor([first + queries - 3], dtype=torch.int32, device="cuda")
     check(got[:, -3:, :2], *reference(q[:, -3:, :2], k[:, :, :2], v[:, :, :2], causal=True, start=last))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("causal", [False, True])
+def test_splits_share_the_keys_there_are(causal, D, monkeypatch):
+    """Many rows, keys split, lengths and positions far below the cache's: the partial results (behind the counters: O, then the
+    maximum and the sum of each row) show that the splits took even shares of the keys that a row has."""
+    monkeypatch.setenv("LOWBIT_ATTENTION", "many")
+    B, Lq, Lk, H = 2, 40, 4000, 2
+    q, k, v = make(B, Lq, Lk, H, H, D, seed=41)
+    ws = scratch(q, k, v)
+    rows = (ws.numel() - 4096) // ((D + 2) * 4)
+    splits = rows // (B * H * Lq)
+    assert rows == B * H * Lq * splits and splits >= 8
+    keys = torch.tensor([1000, 3000], dtype=torch.int32).cuda()
+    mask = dict(causal=True, q_start=keys - Lq) if causal else dict(key_lens=keys)
+    got = lb.attention(q, k, v, workspace=ws, **mask)
+    check(got, *reference(q, k, v, lens=mask.get("key_lens"), causal=causal, start=mask.get("q_start")))
+    sums = ws[4096 + rows * D * 4:].view(torch.float32).view(B, H, splits, Lq, 2)[..., 1]
+    for b in range(B):
+        tiles = -(-int(keys[b]) // 64)
+        taken = -(-tiles // -(-tiles // splits))  # splits that an even share reaches
+        assert bool((sums[b, :, :taken - 1] > 0).all()) and not bool(sums[b, :, taken:].any())
