@@ -116,11 +116,11 @@ __device__ __forceinline__ void lora_init(f32x4_t (&acc)[MB][NB], const LoraArgs
         }
     };
     constexpr int kHalf = (MB + 1) / 2;
-    bool one = true;
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb) one = one && id[mb] == id[0];
     const int first = __builtin_amdgcn_readfirstlane(id[0]);
-    if (__all(one && id[0] == first)) {  // the ordinary case: one request's rows
+    bool one = true;  // rows past the last belong to any request: their operands are zeros, and nothing of them is kept
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) one = one && (id[mb] == first || 16 * mb + l16 >= have);
+    if (__all(one)) {  // the ordinary case: one request's rows
         if (first < 0 || half == 1) return;
         const auto rs = b_rsrc(first);
         step(rs, 0);
@@ -265,7 +265,7 @@ __device__ __forceinline__ f32x4_t lora_term16(const LoraArgs& la, int M, int N,
         return __builtin_amdgcn_raw_buffer_load_b128(rs, off, 0, 0);
     };
     const int first = __builtin_amdgcn_readfirstlane(id);
-    const bool one = __all(id == first);
+    const bool one = __all(id == first || l16 >= have);  // rows past the last belong to any request
     f32x4_t sum = {0.f, 0.f, 0.f, 0.f};
     if (one && first < 0) return sum;
     for (int ks = 0; ks < steps; ++ks) {

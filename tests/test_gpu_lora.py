@@ -213,3 +213,28 @@ def test_on_another_stream_and_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("bits,N,K", [(2, 9216, 3072), (2, 1040, 1024), (1, 3072, 1024)])
+@pytest.mark.parametrize("M", [1, 7, 13, 15])
+def test_one_request_of_any_length_has_the_same_bits(M, bits, N, K):
+    """Fewer rows of one request than a block of 16 go the same way as a whole block: the sums over the rank are taken in the same
+    order (an adapter's term far above the packed product shows another order's last bits)."""
+    c = Case(16, N, K, bits, 64, 128, 2, "one", seed=13)
+    c.b.mul_(64)
+    whole = c.run()
+    c.check(whole)
+    c.x, c.rows = c.x[:M].contiguous(), c.rows[:M].contiguous()
+    assert torch.equal(c.run(), whole[:M])
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+@pytest.mark.parametrize("M,N,K", [(5, 9216, 512), (30, 512, 512), (509, 1024, 1024), (1100, 2304, 512)])
+def test_one_request_with_an_adapter_that_holds_no_numbers(M, N, K, bad):
+    """Rows past the last of a call whose rows all have such an adapter: the other columns stay as they were."""
+    c = Case(M, N, K, 2, 64, 16, 3, "one", seed=14)
+    want = c.run()
+    c.b[2, 7] = bad
+    got = c.run()
+    other = torch.arange(N, device="cuda") != 7
+    assert torch.equal(got[:, other], want[:, other]) and not bool(torch.isfinite(got[:, 7]).any())
