@@ -238,3 +238,34 @@ def test_one_request_with_an_adapter_that_holds_no_numbers(M, N, K, bad):
     got = c.run()
     other = torch.arange(N, device="cuda") != 7
     assert torch.equal(got[:, other], want[:, other]) and not bool(torch.isfinite(got[:, 7]).any())
+
+
+# Several adapters of 16 rows share a workgroup of the first product from about 200 workgroups on.
+SHARED = [(1021, 256, 512, 8, 12), (1100, 208, 1280, 8, 40), (520, 256, 320, 8, 16), (3100, 256, 256, 8, 2), (1533, 256, 256, 8, 5),
+          (500, 256, 512, 16, 12), (1021, 256, 384, 16, 30)]
+
+
+@pytest.mark.parametrize("bits,g", [(2, 64), (1, 128), (4, 64)])
+@pytest.mark.parametrize("M,N,K,rank,adapters", SHARED)
+def test_adapters_that_share_a_workgroup(M, N, K, rank, adapters, bits, g):
+    c = Case(M, N, K // g * g, bits, g, rank, adapters, "scattered", seed=15)
+    got = c.run()
+    c.check(got)
+    order = torch.randperm(M, generator=torch.Generator().manual_seed(15)).cuda()  # other neighbours, the same sums
+    c.x, c.rows = c.x[order].contiguous(), c.rows[order].contiguous()
+    c.check(c.run())
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("M,N,K,rank,adapters", SHARED)
+def test_adapters_that_share_a_workgroup_do_not_touch_each_other(M, N, K, rank, adapters, bad):
+    for e in (0, adapters // 2, adapters - 1):
+        c = Case(M, N, K, 2, 64, rank, adapters, "scattered", seed=16)
+        c.x[:, 5] = 1  # the bad element takes part in every row's sum
+        want = c.run()
+        c.a[e, rank // 2, 5] = bad
+        c.b[e, :, rank // 2] = 1
+        got = c.run()
+        own = c.rows == e
+        assert bool(own.any()) and torch.equal(got[~own], want[~own])
+        assert not bool(torch.isfinite(got[own]).any())
