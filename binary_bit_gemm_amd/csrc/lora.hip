@@ -18,7 +18,7 @@ namespace {
 
 constexpr int kStepK = 128;             // of K per wave and step
 constexpr int kBlock = 16 * kStepK * 2;  // bytes of 16 rows' pieces: 4 KB
-constexpr int kMaxStack = 4;            // adapters of a workgroup
+constexpr int kMaxStack = 2;            // adapters of a workgroup
 
 // Chunk c (16 bytes) of row r of a 16-row block sits at position c ^ r: the 16 rows that an operand read
 // touches at one chunk then lie in 16 different bank groups.
@@ -71,7 +71,7 @@ __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(ShrinkArgs a) {
     const auto x_rs = make_rsrc(a.X + row0 * a.K, uint32_t(have) * row_bytes);
     // a single adapter from its own 64-bit address (rows past the rank come as zeros), stacked ones by offsets into the
     // whole table (the host stacks where that is below 4 GiB)
-    const bool stacked = a.stack > 1;
+    const bool stacked = RB == 1 && a.stack > 1;  // in one block (stack_of)
     const auto a_rs = make_rsrc(a.A + (stacked ? int64_t(0) : int64_t(list[0]) * a.rank * a.K),
                                 (stacked ? uint32_t(a.adapters) : 1u) * uint32_t(a.rank) * row_bytes);
     // copy i of a block brings rows 4 i + lane / 16; X's rows of other adapters come as zeros
@@ -198,16 +198,16 @@ __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(ShrinkArgs a) {
 
 int rank_blocks(int rank) { return rank <= 16 ? 1 : rank <= 32 ? 2 : rank <= 64 ? 4 : 8; }
 
-// Adapters that a workgroup stacks: as many as 32 rows of A hold (a second block costs little, and X is read for fewer
-// workgroups) where that leaves a workgroup per compute unit.  1021 rows of 12 interleaved adapters of rank 8: 14 us with one, 10
-// with four.
+// Adapters that a workgroup stacks: as many as one block of 16 rows of A holds (X is then read by fewer workgroups and
+// the block multiplied whole) where three workgroups for every four compute units are left.  K = 3072, first and second product,
+// stacked / not: rank 8, 12 adapters, 400 rows (150 workgroups) 24.0 / 24.9 us, 512 (192) 23.8 / 24.7, 4608 50 / 66; 2 adapters,
+// 2048 (128) 22.4 / 21.5, 4608 (288) 30.3 / 32.5.  A second block does not pay: rank 8, 12 adapters, 4608 rows 55 us with four;
+// rank 16, 900 rows 33.3 / 29.9, 4608 70 / 65.
 int stack_of(int64_t M, int64_t K, int64_t adapters, int rank) {
-    int64_t stack = 32 / rank < 1 ? 1 : 32 / rank;
-    stack = stack < kMaxStack ? stack : kMaxStack;
+    const int64_t stack = 16 / rank < kMaxStack ? 16 / rank : kMaxStack;
     const int64_t among = adapters < 16 ? adapters : 16;  // in 16 rows
-    if (adapters * rank * K * 2 > (int64_t(1) << 32) - 1) return 1;
-    while (stack > 1 && (stack / 2 >= among || tiles_of(M, 16) * tiles_of(among, stack) < kComputeUnits * 3 / 4)) stack /= 2;
-    return int(stack);
+    if (stack < 2 || among < 2 || adapters * rank * K * 2 > (int64_t(1) << 32) - 1) return 1;
+    return tiles_of(M, 16) * tiles_of(among, stack) < kComputeUnits * 3 / 4 ? 1 : int(stack);
 }
 
 int slots_of(int64_t adapters, int stack) { return int(tiles_of(adapters < 16 ? adapters : 16, stack)); }
