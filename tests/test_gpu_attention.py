@@ -337,3 +337,95 @@ def test_splits_share_the_keys_there_are(causal, D, monkeypatch):
         tiles = -(-int(keys[b]) // 64)
         taken = -(-tiles // -(-tiles // splits))  # splits that an even share reaches
         assert bool((sums[b, :, :taken - 1] > 0).all()) and not bool(sums[b, :, taken:].any())
+
+
+# Keys split across workgroups in both kernels, with a workspace: 2 x 40 queries over 4000 keys.
+SPLIT = [(2, 40, 4000, 2, 2, 128), (2, 40, 4000, 4, 2, 64), (3, 33, 5000, 2, 1, 128)]
+
+
+def split_scratch(q, k, v, kernel):
+    ws = scratch(q, k, v)
+    if kernel != "many64":  # 64 rows are taken unsplit
+        assert ws is not None
+    return ws
+
+
+@pytest.mark.parametrize("shape", SPLIT)
+@pytest.mark.parametrize("causal", [False, True])
+def test_masks_lengths_and_empty_rows_of_split_keys(shape, causal, kernel):
+    """Empty partial results: rows without a key in some splits and in all of them."""
+    B, Lq, Lk, Hq, Hk, D = shape
+    q, k, v = make(*shape, seed=50)
+    g = torch.Generator().manual_seed(51)
+    ws = split_scratch(q, k, v, kernel)
+    sparse = torch.rand(B, Lk, generator=g) < 0.02
+    sparse[0] = False  # nothing left for a whole batch entry
+    middle = torch.zeros(B, Lk, dtype=torch.bool)
+    middle[:, 1500:1600] = True  # one split's keys, or two's
+    middle[1, Lk - 1] = True
+    end = torch.full((B,), Lk, dtype=torch.int32)
+    end[0] = 3
+    short = torch.tensor([0, 70, -1][:B], dtype=torch.int32)
+    starts = [None, torch.tensor([-20, 0, 5][:B], dtype=torch.int32), torch.tensor([Lk - Lq, 100, 2000][:B], dtype=torch.int32)]
+    for start in starts if causal else [None]:
+        start = None if start is None else start.cuda()
+        for m, n in ((sparse, None), (middle, None), (None, short), (None, end), (middle, end), (sparse, short), (None, None)):
+            m, n = (None if x is None else x.cuda() for x in (m, n))
+            got = lb.attention(q, k, v, key_mask=m, key_lens=n, causal=causal, q_start=start, workspace=ws)
+            check(got, *reference(q, k, v, m, n, causal, start))
+            ok = torch.from_numpy(allowed(B, Lq, Lk, m, n, causal, start).any(-1)).cuda()
+            assert not bool(got[~ok].any())
+            if ws is not None:
+                assert not bool(ws[:4096].any())
+
+
+@pytest.mark.parametrize("shape", SPLIT[:2])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), torch.finfo(torch.bfloat16).min])
+def test_anything_in_places_that_split_keys_leave_out(bad, shape, kernel):
+    B, Lq, Lk = shape[:3]
+    q, k, v = make(*shape, seed=52)
+    ws = split_scratch(q, k, v, kernel)
+    mask = torch.ones(B, Lk, dtype=torch.bool)
+    mask[0, 300:2777] = False  # whole splits
+    mask[1, 0] = mask[1, 640:650] = mask[1, Lk - 1] = False
+    mask = mask.cuda()
+    lens = torch.tensor([Lk, 1850], dtype=torch.int32).cuda()
+    want = lb.attention(q, k, v, key_mask=mask, key_lens=lens, workspace=ws)
+    check(want, *reference(q, k, v, mask, lens))
+    out = ~mask | (torch.arange(Lk, device="cuda") >= lens[:, None])
+    k[out] = bad
+    v[out] = bad
+    assert torch.equal(lb.attention(q, k, v, key_mask=mask, key_lens=lens, workspace=ws), want)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_later_keys_do_not_reach_earlier_queries_of_split_keys(bad, D, kernel):
+    q, k, v = make(1, 40, 4000, 2, 2, D, seed=53)
+    ws = split_scratch(q, k, v, kernel)
+    start = torch.tensor([3000], dtype=torch.int32, device="cuda")
+    call = lambda k, v: lb.attention(q, k, v, causal=True, q_start=start, workspace=ws)  # noqa: E731
+    want = call(k, v)
+    check(want, *reference(q, k, v, causal=True, start=start))
+    v2 = v.clone()
+    v2[0, 3017, 0, 5] = bad  # the 17th query on
+    got = call(k, v2)
+    assert torch.equal(got[0, :17], want[0, :17]) and torch.equal(got[0, :, 1], want[0, :, 1])
+    seen = got[0, 17:, 0, 5]
+    assert bool(torch.isnan(seen).all()) if math.isnan(bad) else bool((seen == bad).all())
+    k2 = k.clone()
+    k2[0, 3017, 0] = float("nan")
+    got = call(k2, v)
+    assert torch.equal(got[0, :17], want[0, :17]) and bool(torch.isnan(got[0, 17:, 0]).all())
+
+
+def test_a_workspace_that_is_too_small_is_not_used(kernel):
+    """The call runs unsplit, as without one, and leaves the buffer alone."""
+    for shape in SPLIT[:2]:
+        q, k, v = make(*shape, seed=54)
+        n = lb.attention_workspace_size(q, k, v)
+        want = lb.attention(q, k, v)
+        for size in (n - 1, 4096, 16):
+            if size > 0:
+                ws = torch.full((size,), 0xAB, dtype=torch.uint8, device="cuda")
+                assert torch.equal(lb.attention(q, k, v, workspace=ws), want) and bool((ws == 0xAB).all())

@@ -269,3 +269,45 @@ def test_adapters_that_share_a_workgroup_do_not_touch_each_other(M, N, K, rank, 
         own = c.rows == e
         assert bool(own.any()) and torch.equal(got[~own], want[~own])
         assert not bool(torch.isfinite(got[own]).any())
+
+
+@pytest.mark.parametrize("M", [1, 16, 130])
+@pytest.mark.parametrize("N,bits,g", [(18432, 2, 64), (27648, 2, 64), (27648, 1, 128), (18432, 4, 64)])
+@pytest.mark.parametrize("rows", ["one", "scattered"])
+def test_the_widest_linears(rows, N, bits, g, M):
+    c = Case(M, N, 384, bits, g, 16, 5, rows, seed=17)
+    c.check(c.run())
+
+
+def test_a_workspace_that_is_too_small():
+    c = Case(70, 512, 1024, 2, 64, 24, 5, "scattered", seed=18)
+    for n in (lb.lora_workspace_size(70, 24) - 1, 4096, 0):
+        with pytest.raises(lb.LowbitError):
+            c.run(workspace=torch.zeros(n, dtype=torch.uint8, device="cuda"))
+    # too small to split the product along K: unsplit, as with the least
+    c = Case(509, 1024, 2048, 2, 64, 16, 5, "segments", seed=18)
+    most, least = lb.lora_workspace_size(509, 16, 1024, 2048, 64, 2), lb.lora_workspace_size(509, 16)
+    assert most > least
+    want = c.run(workspace=torch.zeros(least, dtype=torch.uint8, device="cuda"))
+    ws = torch.zeros(most - 16, dtype=torch.uint8, device="cuda")
+    assert torch.equal(c.run(workspace=ws), want)
+
+
+def test_split_adapters_and_split_attention_take_turns_on_a_workspace():
+    c = Case(509, 1024, 2048, 2, 64, 16, 5, "segments", seed=19)      # the product split along K
+    few = Case(50, 256, 16384, 2, 64, 64, 3, "scattered", seed=19)    # the first product split along K
+    g = torch.Generator().manual_seed(19)
+    q = torch.randn(2, 40, 2, 128, generator=g).bfloat16().cuda()
+    k, v = (torch.randn(2, 4000, 2, 128, generator=g).bfloat16().cuda() for _ in range(2))
+    sizes = [lb.lora_workspace_size(509, 16, 1024, 2048, 64, 2), lb.lora_workspace_size(50, 64, 256, 16384, 64, 2),
+             lb.attention_workspace_size(q, k, v), lb.attention_workspace_size(q[:, :1], k, v)]
+    assert sizes[0] > lb.lora_workspace_size(509, 16) and min(sizes) > 4096
+    calls = [lambda ws: c.run(workspace=ws), lambda ws: lb.attention(q, k, v, workspace=ws), lambda ws: few.run(workspace=ws),
+             lambda ws: lb.attention(q[:, :1], k, v, workspace=ws)]
+    alone = [f(torch.zeros(max(sizes), dtype=torch.uint8, device="cuda")) for f in calls]
+    c.check(alone[0])
+    few.check(alone[2])
+    ws = torch.zeros(max(sizes), dtype=torch.uint8, device="cuda")
+    for turn in ((0, 1, 2, 3), (3, 2, 1, 0), (1, 0, 3, 2), (2, 0, 1, 1)):
+        for i in turn:
+            assert torch.equal(calls[i](ws), alone[i]) and not bool(ws[:4096].any())
