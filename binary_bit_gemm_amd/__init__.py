@@ -475,6 +475,8 @@ def _output(out, shape, like):
     torch = _torch()
     if out is None:
         return torch.empty(shape, dtype=torch.bfloat16, device=like.device)
+    if not isinstance(out, torch.Tensor):
+        raise TypeError("out must be a torch.Tensor")
     if out.shape != shape:
         raise ValueError(f"out must be {tuple(shape)}, got {tuple(out.shape)}")
     return out

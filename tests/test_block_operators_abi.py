@@ -177,6 +177,16 @@ def test_binding_refuses_before_the_device():
     assert lb.rope_freqs((8, 4), 100.0, device="cpu").tolist() == pytest.approx([1, 100 ** -0.25, 0.1, 100 ** -0.75, 1, 0.1])
 
 
+def test_binding_refuses_an_output_that_is_no_tensor():
+    torch = pytest.importorskip("torch")
+    like = torch.zeros(1, 2, dtype=torch.bfloat16)
+    with pytest.raises(TypeError, match="out must be a torch.Tensor"):
+        lb._output([[0.0, 0.0]], like.shape, like)
+    with pytest.raises(ValueError, match="out must be"):
+        lb._output(like, (2, 2), like)
+    assert lb._output(like, like.shape, like) is like
+
+
 def test_under_sanitizers():
     """This file's checks against the library built with AddressSanitizer and UndefinedBehaviorSanitizer on its host code."""
     from binary_bit_gemm_amd import build as B
