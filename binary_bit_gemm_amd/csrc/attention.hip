@@ -58,9 +58,6 @@ template <int D>
 __device__ __forceinline__ int k_swz(int r) {
     return D == 128 ? (r & 15) : ((r >> 1) & 7);
 }
-// The chunk of a row that lane quarter q multiplies in MFMA ks of a product over D (any order will do
-// that Q and K share).
-__device__ __forceinline__ int k_chunk(int ks, int q) { return 8 * (ks / 2) + 4 * (q >> 1) + (q & 1) + 2 * (ks % 2); }
 // V is read by transposing reads, 8 bytes per lane: 16 lanes take 4 rows x 32 bytes, half a wave 8
 // consecutive rows, whose 32-byte pieces must not share banks.
 template <int D>

@@ -318,7 +318,7 @@ __global__ __launch_bounds__(64 * WAVES_M * WAVES_N * KSPLIT, 1) void gemm_tile1
             const int part = XSPLIT ? int(blockIdx.x) / total_tiles : kg;
             bool shared = KSPLIT == 2;
             if constexpr (XSPLIT) shared = sk.splits > 1;
-            if (part < 2) lora_init<1>(acc, sk, M, N, m0 + wm0, n0 + wn0, shared ? part : -1);
+            if (part < 2) lora_init(acc, sk, M, N, m0 + wm0, n0 + wn0, shared ? part : -1);
         }
 
         // A step's words and scales are read from LDS before any copy of the step is issued (the

@@ -613,8 +613,8 @@ constexpr TileShape kTiles[] = {
     {TILE_64x256, 64, 256, 2, 0.75f, 0.75f},
     {TILE_96x192, 96, 192, 1, 0.54f, 0.51f},
     {TILE_96x192K2, 96, 192, 1, 0.65f, 0.62f},
-    // 4-bit codes only (the one kernel they run on): fills the chip where 96 x 192 leaves most
-    // compute units idle, e.g. the text encoder's 512 x 2560 down projection (160 vs 84 tiles)
+    // 4-bit codes and calls with adapters (which run on the 16x16-block kernel alone): fills the chip where 96 x 192
+    // leaves most compute units idle, e.g. the text encoder's 512 x 2560 down projection (160 vs 84 tiles)
     {TILE_64x128K2, 64, 128, 1, 0.40f, 0.40f},
 };
 

@@ -10,6 +10,7 @@
 // rank 32) and multiplied in 16x16x32 blocks.  The waves' fp32 sums are added in wave order; where K is
 // split across workgroups (few rows, long K) each leaves its sums in the workspace and the last to arrive adds
 // them in order.  U is stored as hi + lo bf16 pairs.
+#include "lora_device.h"
 #include "lowbit_device.h"
 #include "lowbit_internal.h"
 
@@ -21,17 +22,7 @@ constexpr int kBlock = 16 * kStepK * 2;  // bytes of 16 rows' pieces: 4 KB
 constexpr int kMaxStack = 2;            // adapters of a workgroup
 
 // Chunk c (16 bytes) of row r of a 16-row block sits at position c ^ r: the 16 rows that an operand read
-// touches at one chunk then lie in 16 different bank groups.
-__device__ __forceinline__ int chunk_of(int ks, int q) { return 8 * (ks / 2) + 4 * (q >> 1) + (q & 1) + 2 * (ks % 2); }
-
-__device__ __forceinline__ int min_of_16_lanes(int v) {
-#pragma unroll
-    for (int d = 1; d < 16; d *= 2) {
-        const int o = __shfl_xor(v, d);
-        v = o < v ? o : v;
-    }
-    return __builtin_amdgcn_readfirstlane(v);
-}
+// touches at one chunk (k_chunk) then lie in 16 different bank groups.
 
 // RB: blocks of 16 of the rank (the last may be half used).
 template <int RB, int WAVES>
@@ -50,13 +41,13 @@ __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(ShrinkArgs a) {
 #pragma unroll
     for (int j = 0; j < kMaxStack; ++j) list[j] = -1;
     for (int j = 0; j < int(blockIdx.y) * a.stack; ++j) {
-        cur = min_of_16_lanes(id > cur ? id : 0x7FFFFFFF);
+        cur = min_of_16(id > cur ? id : 0x7FFFFFFF);
         if (cur == 0x7FFFFFFF) return;  // the same in every wave and every split
     }
 #pragma unroll
     for (int j = 0; j < kMaxStack; ++j) {
         if (j >= a.stack) break;
-        const int next = min_of_16_lanes(id > cur ? id : 0x7FFFFFFF);
+        const int next = min_of_16(id > cur ? id : 0x7FFFFFFF);
         if (next == 0x7FFFFFFF) {
             if (j == 0) return;
             break;
@@ -99,7 +90,7 @@ __global__ __launch_bounds__(64 * WAVES) void lora_shrink_kernel(ShrinkArgs a) {
     unsigned char* const at = lds[wave];
     int rd[4];
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) rd[ks] = l16 * (kStepK * 2) + ((chunk_of(ks, q) ^ l16) << 4);
+    for (int ks = 0; ks < 4; ++ks) rd[ks] = l16 * (kStepK * 2) + ((k_chunk(ks, q) ^ l16) << 4);
     f32x4_t acc[RB];
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) acc[rb] = f32x4_t{0.f, 0.f, 0.f, 0.f};

@@ -39,9 +39,8 @@ __device__ __forceinline__ bool all_finite(u32x4_t v) {
     return fine;
 }
 
-// acc[mb][nb], in the layout of 16x16 MFMA results (lane (q, l16): column l16, rows 4q + i), becomes GAIN times
-// the adapters' term of rows row0 + 16 mb .. and output columns col0 + 16 nb .. (GAIN: the factor that some
-// kernels' code operands carry until their epilogue).
+// acc[mb][nb], in the layout of 16x16 MFMA results (lane (q, l16): column l16, rows 4q + i), becomes
+// the adapters' term of rows row0 + 16 mb .. and output columns col0 + 16 nb ..
 //
 // U is held as two bf16 halves per number, hi + lo (2^-16 of it is lost), and the product runs over 2 rank
 // places, hi then lo, against B's rank columns taken twice: the adapter's term is exact to fp32
@@ -51,7 +50,7 @@ __device__ __forceinline__ bool all_finite(u32x4_t v) {
 // take a turn per adapter, in ascending order, in which rows of others enter as zeros.
 //   half: two waves whose sums are added later share the work on mixed rows (0: the first half of the row blocks,
 // and all of one request's rows; 1: the second half; -1: a wave by itself).
-template <int GAIN, int MB, int NB>
+template <int MB, int NB>
 __device__ __forceinline__ void lora_init(f32x4_t (&acc)[MB][NB], const LoraArgs& la, int M, int N, int row0, int col0, int half = -1) {
     int lane = int(threadIdx.x) & 63;
     asm volatile("" : "+v"(lane));  // what follows from it is computed here, not held through the main loop
@@ -234,14 +233,6 @@ __device__ __forceinline__ void lora_init(f32x4_t (&acc)[MB][NB], const LoraArgs
                 for (int nb = 0; nb < NB; ++nb) acc[mb][nb] = sum[nb];
             }
         }
-    }
-    if constexpr (GAIN != 1) {
-#pragma unroll
-        for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[mb][nb][i] *= float(GAIN);
     }
 }
 

@@ -195,4 +195,8 @@ __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rs, void* lds_wave_
                                             soff, 0, 0);
 }
 
+// Which 16-byte chunk of a row's K run lane quarter q holds for 16x16x32 MFMA ks (any order will do that both operands
+// share): the quarters of lanes l and l + 16 then read one 32-byte block.
+__device__ __forceinline__ int k_chunk(int ks, int q) { return 8 * (ks / 2) + 4 * (q >> 1) + (q & 1) + 2 * (ks % 2); }
+
 }  // namespace lowbit
