@@ -468,7 +468,10 @@ __global__ __launch_bounds__(256, D == 64 && NQ == 1 ? 4 : 2) void attention_ker
     const int first = in_sgpr(first64 < 0 ? 0 : first64 < n ? int(first64) : n);
     const int tiles = (end + 63) / 64;
     // the splits share the keys there are, not the keys there could be
-    const int share = a.splits == 1 ? tiles : int(uint32_t(tiles + a.splits - 1) / uint32_t(a.splits));
+    int share = tiles;
+    if constexpr (NQ == 2) {  // 64 rows are taken unsplit only
+        if (a.splits > 1) share = int(uint32_t(tiles + a.splits - 1) / uint32_t(a.splits));
+    }
     const int t0 = split * share;
     const int t1 = in_sgpr(t0 + share < tiles ? t0 + share : tiles);
 
