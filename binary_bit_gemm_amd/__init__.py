@@ -496,7 +496,8 @@ def gemm_lora(x, words, scales, g: int, bits: int, lora_a, lora_b, alpha, rows, 
     lora_b bf16 [adapters, N, rank], alpha fp32 [adapters], rows int32 [M] (-1: no adapter).
 
     `workspace`: a device tensor of at least lora_workspace_size(M, rank) bytes, zero-filled before its first use (reuse
-    it between calls; do not share it between calls that run concurrently); allocated for the call if None."""
+    it between calls; do not share it between calls that run concurrently); that much is allocated for the call if None.
+    With the bytes that lora_workspace_size says for N and K too, K can be split (509 x 3072 x 9216 binary: 55 us, 68 without)."""
     torch = _torch()
     bf16 = torch.bfloat16
     _require(x, bf16, "x")
@@ -639,8 +640,8 @@ def attention(q, k, v, key_mask=None, key_lens=None, causal: bool = False, q_sta
     a query without keys gets zeros.  scale: 1 / sqrt(D) by default.
 
     `workspace`: an optional device tensor of at least attention_workspace_size(q, k, v) bytes, zero-filled before its
-    first use, with which few rows over many keys run split along the keys.  Reuse it between calls;
-    do not share it between calls that run concurrently."""
+    first use, with which few rows over many keys run split along the keys: pass one when decoding (one token over 40007 keys, 8 kv
+    heads of 128: 36 us, 411 without).  Reuse it between calls; do not share it between calls that run concurrently."""
     if out is None:
         _heads(q, "q", 4)
     out = _output(out, q.shape, q)

@@ -25,7 +25,8 @@
 // (the row's other scores are then a unit of c m, 32 powers of two, or more away).
 //
 // Rounding to bf16: the probabilities before the second product (the matrix cores' input; relative
-// 2^-8 each, averaged over the keys) and O at the store.  Scores, m, l and O are fp32.
+// 2^-8 each, averaged over the keys) and O at the store.  Scores, m, l and O are fp32.  O is kept undivided, with the
+// largest p anywhere from 2^-32 to 2: values v below 2^-70 or above 2^90 in magnitude leave fp32's range there.
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
@@ -430,10 +431,13 @@ __device__ __forceinline__ uint64_t up_to(int64_t rel) {
 }
 
 // Many rows: a workgroup of 4 waves takes 64 NQ rows of one kv head, a wave 16 NQ of them; tiles of 64 keys go
-// through LDS, double-buffered, by direct copies one tile ahead.  Bound by the two products and the exponentials beside them,
-// then by power: 4608 x 4608, 24 heads of 128: 264 us = 988 TFLOP/s, the clock at 1.7 GHz and the matrix cores
-// busy for 66% of the steady state's cycles; the rest is 864 workgroups in 512 places (two rounds for 1.7).  Heads of 64 have
-// half the products per exponential: 4608 x 4608, 24 heads: 159 us = 820 TFLOP/s.
+// through LDS, double-buffered, by direct copies one tile ahead.  4608 x 4608, 24 heads of 128: 262 to 273 us = 956 to 996 TFLOP/s
+// on different cards, of which 864 workgroups in 512 places (two rounds for 1.7) are the largest loss: 16 heads, 4096 x 16384, an exact
+// round, run at 1121 TFLOP/s.  There the matrix cores are busy for 52% of the SIMD cycles at least and vector
+// instructions (matrix ones' issue included) active for 44% (profiles/block_operators_kernel_trace_and_counters.txt):
+// two waves per SIMD do not keep either full.  Power takes the rest of what is seen: with zeros for inputs, the same
+// instructions, 250 for 267 us and 433 for 490.  Heads of 64 have half the products per exponential: 4608 x 4608, 24
+// heads: 161 us = 811 TFLOP/s.
 template <int D, int NQ>
 __global__ __launch_bounds__(256, D == 64 && NQ == 1 ? 4 : 2) void attention_kernel(AttnArgs a) {
     constexpr int kRows = 64 * NQ;                // of a workgroup
@@ -447,7 +451,7 @@ __global__ __launch_bounds__(256, D == 64 && NQ == 1 ? 4 : 2) void attention_ker
     const int lane = int(threadIdx.x) & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
     // tiles of one head next to each other, heads of one XCD together; causal: those with the most keys first (4608
-    // tokens, 24 heads of 128: 161 us, last 191)
+    // tokens, 24 heads of 128: 163 us, last 191)
     int id = xcd_remap(int(blockIdx.x), int(gridDim.x));
     const int rt = a.causal ? a.row_tiles - 1 - id % a.row_tiles : id % a.row_tiles;
     id /= a.row_tiles;
@@ -944,9 +948,11 @@ constexpr int kMaxShortSplits = 64;     // a lane per split in the join
 
 // Which kernel, and how the keys are split: the one whose estimated time is less (one row block, 16 or 32 rows,
 // always goes to the few-rows kernel).  The estimates (us, D = 64 / 128) are fits to measured calls of 8 to 96 heads, 64 to
-// 4608 rows and 200 to 8192 keys: in seven of 108 of them the other kernel is 7% to 14% faster, in the rest less or
-// not.  Measured (few / many, us): 256 x 1024, 24 heads of 128: 14 / 24; 512 x 2048, 16 heads of 128: 25 / 30; 512 x 512, 24
-// heads of 128: 14 / 12; 1024 x 1024, 24 heads of 128: 33 / 25, of 64: 16 / 17; 4 x 512 x 512, 24 heads of 128: 37 / 24.
+// 4608 rows and 200 to 8192 keys: in five of 108 of them the other kernel is 9% to 13% faster, in the rest less or
+// not (profiles/attention_plan_estimates.txt).  They plan with kv_len: with key_lens far below it the few-rows kernel may
+// be the faster one, and 1000 causal queries at the end of 2000 to 8000 keys, 16 heads, without a workspace, are 10% to 20%
+// slower than there.  Measured (few / many, us): 256 x 1024, 24 heads of 128: 15 / 18; 512 x 2048, 16 heads of 128: 26 / 30; 512 x 512, 24
+// heads of 128: 14 / 12; 1024 x 1024, 24 heads of 128: 32 / 25, of 64: 17 / 16; 4 x 512 x 512, 24 heads of 128: 37 / 25.
 //   LOWBIT_ATTENTION=few|many|many64|many128 in the environment forces the kernel, or also its rows (A/B runs and tests).
 //
 // The few-rows kernel (32 rows per workgroup, its waves over the keys, two or three workgroups per compute unit):
@@ -964,8 +970,8 @@ double few_us(int64_t groups, int64_t keys, bool joins, int head_dim) {
 // workgroups: 5 / 9 and 0.79 / 1.16 of one of 128 rows alone, times 0.75 n from two on.  With 64 rows at a time 5 / 5.5,
 // and as in the table: they fill the units more evenly, and four of them of D = 64 fit one; but they read twice as
 // much LDS per product.  Measured (128 / 64 rows, us): 2 x 1533 x 1533, 16 heads of 64: 33 / 30; 4 x 300 x 300, 24
-// heads of 128: 21 / 14; 4608 x 4608, 24 heads of 128: 267 / 313; causal 1533 x 1533, 24 heads of 128: 43 / 31, 4608 x
-// 4608: 161 / 174.
+// heads of 128: 21 / 14; 4608 x 4608, 24 heads of 128: 267 / 313; causal 1533 x 1533, 24 heads of 128: 44 / 31, 4608 x
+// 4608: 163 / 174.
 double many_us(int64_t tiles, int64_t groups, int tile_rows, int head_dim) {
     const double n = double(tiles_of(groups, kComputeUnits)), whole = head_dim == 64 ? 0.79 : 1.16;
     if (tile_rows == 128) return (head_dim == 64 ? 5.0 : 9.0) + double(tiles) * whole * (n <= 1 ? 1.0 : 0.75 * n);

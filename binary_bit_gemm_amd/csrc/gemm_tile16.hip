@@ -778,9 +778,9 @@ hipError_t launch_gemm_tile16_epilogue(const GemmProblem* probs, int count, int 
 // Costs are in pick_tile_variant's unit.  A compute unit that holds n workgroups does 0.30 (n = 1), 0.47 (2) or 0.56
 // (3 and more) of a 256 x 256 tile's work per unit time; the splits' fp32 sums go out and come back, 64 KB a
 // workgroup.  All splits of a call are resident together (at most 3 workgroups per compute unit).  Measured, with a
-// first product of 5 to 10 us in each figure, other tiles -> this one: 509 x 3072 binary at K = 9216 65 -> 53 us (4
-// splits), 512 x 9216 at K = 3072 74 -> 53 (1), 1021 x 2560 4-bit at K = 4096 57 -> 52 (2), 64 x 3072 at K = 9216 54 ->
-// 25 (8); not taken: 1000 x 4096 at K = 4096 49 -> 58, 1536 x 3072 at K = 3072 40 -> 56.
+// first product of 5 to 10 us in each figure, other tiles -> this one: 509 x 3072 binary at K = 9216 67 -> 56 us (4
+// splits), 512 x 9216 at K = 3072 80 -> 59 (1), 1021 x 2560 4-bit at K = 4096 64 -> 57 (2), 64 x 3072 at K = 9216 53 ->
+// 24 (8); not taken: 1000 x 4096 at K = 4096 49 -> 55, 1536 x 3072 at K = 3072 40 -> 52.
 constexpr int kMaxTileSplits = 8;
 int lora_splits(const GemmProblem& p, int g, int bits) {
     double best = 0.0;

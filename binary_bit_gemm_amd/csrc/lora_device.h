@@ -2,8 +2,8 @@
 // U B_e^T instead of zero, where U[m] = alpha_e A_e X[m] was laid down by the first kernel (lora.hip) and e is
 // row m's adapter.
 //
-// Costs, 4608 x 9216 at K = 3072, ternary, beside lowbit_gemm's 251 us (first product of 13 us included): one adapter of
-// rank 32 265 us, three in turn 264, rows of three interleaved 291; of rank 128 361, 384 and 507.
+// Costs, 4608 x 9216 at K = 3072, ternary, beside lowbit_gemm's 235 us (first product of 13 us included): one adapter of
+// rank 32 262 us, three in turn 262, rows of three interleaved 291; of rank 128 352, 368 and 493.
 //
 // At the start and not at the end: the loads then overlap the tile's first copies, and the sums are
 // only written (added to in loops at the end, they took twice their registers and spilled).

@@ -391,12 +391,14 @@ int lowbit_qk_norm_rope(const lowbit_qk_problem* problem, void* stream);
  *   A query that takes no key gets O = 0.  Keys and values that key_lens or key_mask leave out may hold
  *   anything, infinities and NaN included.
  * Scores, softmax statistics and sums are fp32; the probabilities are rounded to bf16 for the second
- * product; O is rounded once.  Deterministic.
+ * product (error against 64 bits 2.3e-3 where the rounding of O alone gives 1.7e-3); O is rounded once.
+ * Values v from 2^-70 to 2^90 in magnitude (and 0) stay inside fp32's range on the way.  Deterministic.
  *   workspace  device memory of lowbit_attention_workspace_size(problem) bytes, 16-byte aligned, ZERO-FILLED
  *      before its first use, with which a call of few rows and many keys splits the keys across workgroups.  Its
  *      first 4096 bytes hold arrival counters that every call leaves at zero, so one workspace serves calls
  *      of any shapes in turn (and lowbit_gemm_ex's, lowbit_gemm_affine_ex's and lowbit_gemm_lora's).  With a
- *      NULL or too small workspace the call runs unsplit.  Calls that share it must not run concurrently.
+ *      NULL or too small workspace the call runs unsplit (one token over 40007 keys, 8 kv heads of 128: 411 us
+ *      instead of 36).  Calls that share it must not run concurrently.
  * The size depends on the shape only (0: no split, or invalid arguments).  LOWBIT_ATTENTION=few|many|many64|many128
  * in the environment forces one of the kernels, or also its rows per workgroup (for A/B runs and tests).  The descriptor is read
  * before the call returns.  key_lens and q_start need 4-byte alignment, q, k, v, o and workspace 16.

@@ -429,3 +429,16 @@ def test_a_workspace_that_is_too_small_is_not_used(kernel):
             if size > 0:
                 ws = torch.full((size,), 0xAB, dtype=torch.uint8, device="cuda")
                 assert torch.equal(lb.attention(q, k, v, workspace=ws), want) and bool((ws == 0xAB).all())
+
+
+@pytest.mark.parametrize("power", [-70, 90])
+@pytest.mark.parametrize("shape", [(1, 40, 1000, 2, 2, 128), (1, 1, 5000, 8, 2, 64), (2, 200, 333, 2, 2, 128)])
+def test_values_of_any_size(shape, power, kernel):
+    """O is kept undivided, the largest probability anywhere from 2^-32 to 2: at the ends of the range that is promised for values,
+    with scores that grow along the keys, what fp32 loses is below 2^-126 of a sum of at least 2^-102."""
+    q, k, v = make(*shape, seed=60)
+    Lk = shape[2]
+    k = (k.float() * torch.linspace(0.1, 4, Lk, device="cuda")[None, :, None, None]).bfloat16()
+    v = (v.float().abs().clamp(0.5, 2) * v.float().sign() * 2.0 ** power).bfloat16()
+    for ws in (None, scratch(q, k, v)):
+        check(lb.attention(q, k, v, workspace=ws), *reference(q, k, v))
