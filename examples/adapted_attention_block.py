@@ -1,8 +1,10 @@
-"""The attention half of a double-stream block with low-rank adapters of several requests, on packed weights.
+"""The attention half of a double-stream block, and one decoded token of a causal layer, with low-rank adapters of several
+requests on packed weights.
 
     python examples/adapted_attention_block.py [--image-tokens 4096] [--text-tokens 512] [--heads 24] [--check]
+    python examples/adapted_attention_block.py --decode [--requests 16] [--cached-tokens 4096] [--check]
 
-Every request brings an image stream and a text stream (padded prompt) of one length each and its own adapter:
+In the block every request brings an image stream and a text stream (padded prompt) of one length each and its own adapter:
 
     QKV      lowbit_gemm_lora       packed ternary QKV linear of the stream + the request's adapter, written
                                     into the request's rows of one joint [text | image] buffer
@@ -10,6 +12,10 @@ Every request brings an image stream and a text stream (padded prompt) of one le
                                     positions, in place in that buffer
     mixing   lowbit_attention       text and image tokens together, padding masked out
     output   lowbit_gemm_residual   packed output linear, gated and added to the residual stream
+
+A decoded token (--decode) is a row of all requests together: one lowbit_gemm_lora per linear takes every row with its own
+request's adapter, lowbit_qk_norm_rope turns it by its request's position, and lowbit_attention reads each request's cache to its
+own length.
 
 Weights, adapters and activations are random (there are no checkpoints here); the shapes are those of the
 FLUX.2 Klein 4B transformer's double-stream blocks by default: hidden size 3072, 24 heads of 128.
@@ -92,6 +98,79 @@ def attention_half(block, x, adapter, mask, pos, workspace):
     return result
 
 
+class Layer:
+    """The attention half of a causal layer with grouped heads: QKV and output linear, both with adapters, and the caches."""
+
+    def __init__(self, requests, capacity, heads, kv_heads, adapters, rank, seed=0):
+        gen = torch.Generator(device="cuda").manual_seed(seed)
+        self.heads, self.kv_heads, self.dim = heads, kv_heads, 128 * heads
+        width = 128 * (heads + 2 * kv_heads)
+        self.qkv, self.out = Linear(width, self.dim, gen), Linear(self.dim, self.dim, gen)
+        rand = lambda *shape: torch.randn(*shape, generator=gen, device="cuda")  # noqa: E731
+        self.a = [(rand(adapters, rank, self.dim) / math.sqrt(self.dim)).bfloat16() for _ in range(2)]
+        self.b = [(rand(adapters, n, rank) * 0.1).bfloat16() for n in (width, self.dim)]
+        self.alpha = torch.ones(adapters, device="cuda")
+        self.norm = tuple((1 + 0.1 * rand(128)).bfloat16() for _ in range(2))
+        self.freqs = lb.rope_freqs((128,))
+        self.keys, self.values = (rand(requests, capacity, kv_heads, 128).bfloat16() for _ in range(2))
+
+
+def decode_step(layer, x, adapter, filled, workspace):
+    """x: bf16 [requests, dim], one new token of each; adapter: int32 [requests] (-1: none); filled: int32 [requests], the tokens that
+    each cache holds already.  Stores the new keys and values and returns x plus the layer's attention."""
+    requests, heads, kv = x.shape[0], layer.heads, layer.kv_heads
+    lora = lambda x, lin, i: lb.gemm_lora(x, lin.words, lin.scales, G, BITS, layer.a[i], layer.b[i], layer.alpha, adapter,  # noqa: E731
+                                          workspace=workspace)
+    qkv = lora(x, layer.qkv, 0).view(requests, heads + 2 * kv, 128)
+    q, k, v = qkv[:, :heads], qkv[:, heads:heads + kv], qkv[:, heads + kv:]
+    lb.qk_norm_rope(q, k, filled[:, None], layer.freqs, (128,), *layer.norm, interleaved=False, q_out=q, k_out=k)
+    at = torch.arange(requests, device="cuda"), filled.long()
+    layer.keys[at], layer.values[at] = k, v
+    mixed = lb.attention(q[:, None], layer.keys, layer.values, key_lens=filled + 1, workspace=workspace)
+    return x + lora(mixed.view(requests, -1), layer.out, 1)
+
+
+def decode_reference(layer, x, adapter, filled):
+    """The same in 64 bits from the caches before the step, without the roundings to bf16 in between."""
+    group = layer.heads // layer.kv_heads
+    dense = layer.qkv.dense(), layer.out.dense()
+    result = []
+    for r in range(x.shape[0]):
+        e, n = int(adapter[r]), int(filled[r])
+
+        def linear(y, i):
+            z = dense[i] @ y
+            return z if e < 0 else z + float(layer.alpha[e]) * (layer.b[i][e].double() @ (layer.a[i][e].double() @ y))
+        qkv = linear(x[r].double(), 0).view(-1, 128)
+        q, k, v = qkv.split([layer.heads, layer.kv_heads, layer.kv_heads])
+        c, s = (n * layer.freqs.double()).cos(), (n * layer.freqs.double()).sin()
+        turned = []
+        for y, w in zip((q, k), layer.norm):
+            y = y / (y.square().mean(-1, keepdim=True) + 1e-6).sqrt() * w.double()
+            turned.append(torch.cat([y[:, :64] * c - y[:, 64:] * s, y[:, :64] * s + y[:, 64:] * c], -1))
+        keys = torch.cat([layer.keys[r, :n].double(), turned[1][None]]).repeat_interleave(group, 1)
+        values = torch.cat([layer.values[r, :n].double(), v[None]]).repeat_interleave(group, 1)
+        p = torch.softmax((turned[0] * keys).sum(-1) / math.sqrt(128), 0)  # [tokens, heads]
+        result.append(x[r].double() + linear((p[..., None] * values).sum(0).flatten(), 1))
+    return torch.stack(result)
+
+
+def decode_example(requests, capacity, heads, kv_heads, rank=16, seed=0):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    layer = Layer(requests, capacity, heads, kv_heads, adapters=max(1, requests // 2), rank=rank, seed=seed + 1)
+    x = torch.randn(requests, layer.dim, generator=gen, device="cuda").bfloat16()
+    adapter = torch.arange(requests, dtype=torch.int32, device="cuda") % (layer.alpha.shape[0] + 1) - 1  # some have none
+    filled = torch.randint(0, capacity, (requests,), generator=gen, device="cuda", dtype=torch.int32)
+    filled[0] = 0
+    return layer, x, adapter, filled
+
+
+def decode_workspace(layer, requests, rank=16):
+    q = torch.empty(requests, 1, layer.heads, 128, dtype=torch.bfloat16, device="cuda")
+    need = max(lb.attention_workspace_size(q, layer.keys, layer.values), lb.lora_workspace_size(requests, rank))
+    return torch.zeros(need, dtype=torch.uint8, device="cuda")
+
+
 def reference(block, x, adapter, mask, pos):
     """The same in 64 bits, without the roundings to bf16 in between."""
     requests, text, dim = x["text"].shape
@@ -134,14 +213,37 @@ def example(requests, text, image, heads, rank=16, seed=0):
     return block, x, adapter, mask, positions(text, image)
 
 
+def decode_main(a):
+    requests = a.requests or 16
+    kv_heads = max(1, a.heads // 3) if a.heads % 3 == 0 else a.heads
+    layer, x, adapter, filled = args = decode_example(requests, a.cached_tokens + 1, a.heads, kv_heads)
+    workspace = decode_workspace(layer, requests)
+    want = decode_reference(*args) if a.check else None
+    got = decode_step(*args, workspace)
+    torch.cuda.synchronize()
+    t = time.perf_counter()
+    for _ in range(50):
+        decode_step(*args, workspace)
+    torch.cuda.synchronize()
+    print(f"one token of {requests} requests, caches of up to {a.cached_tokens} tokens, {a.heads} / {kv_heads} heads, hidden size "
+          f"{layer.dim}: {(time.perf_counter() - t) * 2e4:.0f} us")
+    if a.check:
+        print(f"relative error against 64 bits {float((got.double() - want).norm() / want.norm()):.2e}")
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
-    ap.add_argument("--requests", type=int, default=2)
+    ap.add_argument("--requests", type=int, help="default 2, or 16 with --decode")
     ap.add_argument("--text-tokens", type=int, default=512)
     ap.add_argument("--image-tokens", type=int, default=4096)
     ap.add_argument("--heads", type=int, default=24)
     ap.add_argument("--check", action="store_true", help="compare with the same computation in 64 bits")
+    ap.add_argument("--decode", action="store_true", help="one token of each request through a causal layer")
+    ap.add_argument("--cached-tokens", type=int, default=4096)
     a = ap.parse_args()
+    if a.decode:
+        return decode_main(a)
+    a.requests = a.requests or 2
     args = example(a.requests, a.text_tokens, a.image_tokens, a.heads)
     tokens = a.text_tokens + a.image_tokens
     block = args[0]

@@ -40,3 +40,25 @@ def test_the_block_in_one_piece(requests, text, image, heads):
     again = m.attention_half(*args, ws)
     assert all(torch.equal(again[s], got[s]) for s in got)
     assert block.dim == 128 * heads
+
+
+@pytest.mark.parametrize("requests,capacity,heads,kv_heads", [(16, 700, 6, 2), (1, 3000, 4, 4), (5, 40, 4, 1), (33, 130, 2, 2)])
+def test_a_decoded_token_of_many_requests(requests, capacity, heads, kv_heads):
+    """One call per linear with every request's own adapter.  Rounded to bf16 on the way: QKV, the turned q and k, the mixed values,
+    the output linear's result and the sum, each by 2^-8 at most; scores of a few units move the probabilities by a few
+    per cent at most: 5 * 2^-8 for the roundings and as much again for the scores."""
+    m = load()
+    layer, x, adapter, filled = m.decode_example(requests, capacity, heads, kv_heads)
+    assert requests == 1 or len(set(adapter.tolist())) > 1
+    ws = m.decode_workspace(layer, requests)
+    want = m.decode_reference(layer, x, adapter, filled)
+    got = m.decode_step(layer, x, adapter, filled, ws)
+    assert bool(torch.isfinite(got).all())
+    assert float((got.double() - want).norm() / want.norm()) <= 10 * 2.0 ** -8
+    assert torch.equal(m.decode_step(layer, x, adapter, filled, ws), got)
+    for r in range(requests):  # a request by itself, from its own cache
+        one = m.Layer.__new__(m.Layer)
+        one.__dict__.update(layer.__dict__)
+        one.keys, one.values = layer.keys[r:r + 1], layer.values[r:r + 1]
+        alone = m.decode_step(one, x[r:r + 1], adapter[r:r + 1], filled[r:r + 1], m.decode_workspace(one, 1))
+        assert float((alone.double() - want[r:r + 1]).norm() / want[r:r + 1].norm()) <= 10 * 2.0 ** -8
