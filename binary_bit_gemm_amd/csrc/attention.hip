@@ -433,10 +433,10 @@ __device__ __forceinline__ uint64_t up_to(int64_t rel) {
 // Many rows: a workgroup of 4 waves takes 64 NQ rows of one kv head, a wave 16 NQ of them; tiles of 64 keys go
 // through LDS, double-buffered, by direct copies one tile ahead.  4608 x 4608, 24 heads of 128: 262 to 273 us = 956 to 996 TFLOP/s
 // on different cards, of which 864 workgroups in 512 places (two rounds for 1.7) are the largest loss: 16 heads, 4096 x 16384, an exact
-// round, run at 1121 TFLOP/s.  There the matrix cores are busy for 52% of the SIMD cycles at least and vector
-// instructions (matrix ones' issue included) active for 44% (profiles/block_operators_kernel_trace_and_counters.txt):
-// two waves per SIMD do not keep either full.  Power takes the rest of what is seen: with zeros for inputs, the same
-// instructions, 250 for 267 us and 433 for 490.  Heads of 64 have half the products per exponential: 4608 x 4608, 24
+// round, run at 1121 TFLOP/s.  There the matrix cores are busy for 53% of the SIMD cycles at least and vector
+// instructions (matrix ones' issue included) active for 45% (profiles/block_operators_kernel_trace_and_counters.txt):
+// two waves per SIMD do not keep either full.  Power takes 6% and 11%: with zeros for inputs, the same instructions, 250 for
+// 267 us and 433 for 490.  Heads of 64 have half the products per exponential: 4608 x 4608, 24
 // heads: 161 us = 811 TFLOP/s.
 template <int D, int NQ>
 __global__ __launch_bounds__(256, D == 64 && NQ == 1 ? 4 : 2) void attention_kernel(AttnArgs a) {
