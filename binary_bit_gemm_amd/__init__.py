@@ -651,6 +651,191 @@ def attention(q, k, v, key_mask=None, key_lens=None, causal: bool = False, q_sta
     return out
 
 
+# ---- decoding: a paged cache, attention over it, matrix-vector products ----
+
+_CACHE = struct.Struct("@4Pq4i0q")  # lowbit_cache of include/lowbit.h
+_CACHE_ATTENTION_PROBLEM = struct.Struct("@4Pq4i6P10qif0q")  # lowbit_cache_attention_problem
+
+
+class KVCache:
+    """Keys and values of many requests in pages (lowbit_cache): k and v [pages, kv_heads, page_size, row], uint8 with head_dim * bits / 8
+    bytes a row at 8 and 4 bits, bf16 with head_dim elements at 16; k_scales and v_scales bf16, [pages, kv_heads, page_size] at 8 bits,
+    [pages, kv_heads, page_size, head_dim / 64, 2] at 4, None at 16.  page_size 16 .. 256 (a power of two), head_dim 64 or 128.
+    kv_cache() allocates one.  The order inside a page's head is the library's: cache_write and cache_read convert."""
+
+    __slots__ = ("k", "v", "k_scales", "v_scales", "bits", "shape")
+
+    def __init__(self, k, v, k_scales=None, v_scales=None, bits: int = 8):
+        torch = _torch()
+        if bits not in (4, 8, 16):
+            raise ValueError(f"bits must be 4, 8 or 16, got {bits}")
+        dtype = torch.bfloat16 if bits == 16 else torch.uint8
+        _require(k, dtype, "k", 4)
+        _plain(v, dtype, "v", 4, k)
+        pages, heads, page, row = k.shape
+        if v.shape != k.shape:
+            raise ValueError(f"v must be {tuple(k.shape)}, got {tuple(v.shape)}")
+        dim = row if bits == 16 else row * 8 // bits
+        if bits == 16:
+            if k_scales is not None or v_scales is not None:
+                raise ValueError("a 16-bit cache has no scales")
+        else:
+            want = (pages, heads, page) if bits == 8 else (pages, heads, page, dim // 64, 2)
+            for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+                _plain(t, torch.bfloat16, name, len(want), k)
+                if t.shape != want:
+                    raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
+        self.k, self.v, self.k_scales, self.v_scales, self.bits = k, v, k_scales, v_scales, bits
+        self.shape = (pages, heads, page, dim)
+
+    def _fields(self):
+        pages, heads, page, dim = self.shape
+        ks, vs = self.k_scales, self.v_scales
+        return (self.k.data_ptr(), self.v.data_ptr(), ks.data_ptr() if ks is not None else 0, vs.data_ptr() if vs is not None else 0,
+                pages, page, heads, dim, self.bits)
+
+
+def kv_cache(pages: int, kv_heads: int, head_dim: int, bits: int = 8, page_size: int = 64, device="cuda") -> KVCache:
+    """A new cache of zeros."""
+    torch = _torch()
+    if bits not in (4, 8, 16):
+        raise ValueError(f"bits must be 4, 8 or 16, got {bits}")
+    if head_dim not in (64, 128):
+        raise ValueError(f"head_dim must be 64 or 128, got {head_dim}")
+    row = (pages, kv_heads, page_size, head_dim if bits == 16 else head_dim * bits // 8)
+    k, v = (torch.zeros(row, dtype=torch.bfloat16 if bits == 16 else torch.uint8, device=device) for _ in range(2))
+    if bits == 16:
+        return KVCache(k, v, bits=16)
+    scales = row[:3] if bits == 8 else (*row[:3], head_dim // 64, 2)
+    return KVCache(k, v, *(torch.zeros(scales, dtype=torch.bfloat16, device=device) for _ in range(2)), bits=bits)
+
+
+def _cache_rows(function: str, cache: KVCache, k, v, slots) -> None:
+    _heads(k, "k", 3)
+    _heads(v, "v", 3)
+    _, heads, _, dim = cache.shape
+    T = slots.shape[0]
+    if k.shape != (T, heads, dim) or v.shape != k.shape:
+        raise ValueError(f"k and v must be [{T}, {heads}, {dim}], got {tuple(k.shape)} and {tuple(v.shape)}")
+    _same_device(cache.k, (("k", k), ("v", v)))
+    _call(function, cache.k, _CACHE.pack(*cache._fields()), k.data_ptr(), v.data_ptr(), T, *_strides(k), *_strides(v), slots.data_ptr())
+
+
+def cache_write(cache: KVCache, k, v, slots) -> None:
+    """Quantises k and v [tokens, kv_heads, head_dim] (bf16, any strides of whole 16-byte pieces, e.g. views of a fused QKV output) into the
+    cache's slots (int32 [tokens]: page * page_size + place; -1 leaves a row out; those of one call differ) (lowbit_cache_write)."""
+    _plain(slots, _torch().int32, "slots", 1, cache.k)
+    _cache_rows("lowbit_cache_write", cache, k, v, slots)
+
+
+def cache_read(cache: KVCache, slots, k_out=None, v_out=None):
+    """The rows at `slots` (int32 [tokens]) as bf16 [tokens, kv_heads, head_dim] (lowbit_cache_read): (k_out, v_out).  Rows whose slot
+    is outside the cache are left as they were (zeros where the output is made here)."""
+    torch = _torch()
+    _plain(slots, torch.int32, "slots", 1, cache.k)
+    _, heads, _, dim = cache.shape
+    shape = (slots.shape[0], heads, dim)
+    k_out, v_out = (torch.zeros(shape, dtype=torch.bfloat16, device=cache.k.device) if t is None else t for t in (k_out, v_out))
+    _cache_rows("lowbit_cache_read", cache, k_out, v_out, slots)
+    return k_out, v_out
+
+
+def _cache_attention_problem(q, cache, page_table, key_lens, q_lens, tree, kv_len, scale, out):
+    torch = _torch()
+    _heads(q, "q", 4)
+    B, Lq, Hq, D = q.shape
+    pages, heads, page, dim = cache.shape
+    if D != dim:
+        raise ValueError(f"q must be [batch, q_len, q_heads, {dim}], got {tuple(q.shape)}")
+    pt = pk = pq = ptree = po = stride = 0
+    so = (Lq * Hq * D, Hq * D, D)
+    if page_table is not None:
+        pt = _plain(page_table, torch.int32, "page_table", 2, q)
+        pk = _plain(key_lens, torch.int32, "key_lens", 1, q)
+        if page_table.shape[0] != B or key_lens.shape[0] != B:
+            raise ValueError(f"page_table must be [{B}, pages] and key_lens [{B}]")
+        stride = page_table.shape[1]
+        if kv_len is None:
+            kv_len = stride * page
+        elif kv_len > stride * page:
+            raise ValueError(f"page_table holds {stride * page} keys of a request, fewer than kv_len = {kv_len}")
+    if q_lens is not None:
+        pq = _plain(q_lens, torch.int32, "q_lens", 1, q)
+        if q_lens.shape[0] != B:
+            raise ValueError(f"q_lens must be [{B}]")
+    if tree is not None:
+        ptree = _plain(tree, torch.int64, "tree", 2, q)
+        if tree.shape != (B, Lq):
+            raise ValueError(f"tree must be [{B}, {Lq}]")
+    if out is not None:
+        _heads(out, "out", 4)
+        po, so = out.data_ptr(), _strides(out)
+    _same_device(q, (("cache", cache.k), ("out", out)))
+    return _CACHE_ATTENTION_PROBLEM.pack(*cache._fields(), q.data_ptr(), po, pt, pk, pq, ptree, B, Lq, kv_len, *_strides(q), *so, stride, Hq,
+                                         scale if scale is not None else D ** -0.5)
+
+
+def cache_attention_workspace_size(q, cache: KVCache, kv_len: int) -> int:
+    """Bytes of workspace that cache_attention can use for q and this many keys at most (0: none)."""
+    return int(lib().lowbit_cache_attention_workspace_size(_cache_attention_problem(q, cache, None, None, None, None, kv_len, None, None)))
+
+
+def cache_attention(q, cache: KVCache, page_table, key_lens, q_lens=None, tree=None, kv_len: Optional[int] = None, scale=None, out=None,
+                    workspace=None):
+    """Attention of each request's last tokens over its keys and values in the cache, in bf16 (lowbit_cache_attention): q [batch, q_len,
+    q_heads, head_dim] (any strides of whole 16-byte pieces), page_table int32 [batch, pages of a request], key_lens int32 [batch]: keys, the new
+    tokens' among them (cache_write puts them there first).  Every new token takes the keys before the new ones and, of those, the ones up to
+    itself, or where bit i of tree[b, t] (int64 [batch, q_len], q_len <= 64) is set: a tree of drafted tokens, each with its
+    ancestors and itself.  q_lens int32 [batch]: requests with fewer new tokens than q_len; rows of `out` past them are left as they
+    were (zeros where the output is made here).  kv_len: the most keys a request has in this call, if that is less than the table holds (it only
+    chooses how the keys are split).  scale: 1 / sqrt(head_dim) by default.
+
+    `workspace`: an optional device tensor of at least cache_attention_workspace_size(q, cache, kv_len) bytes, zero-filled before its first use, with
+    which few rows over many keys run split along the keys: pass one when decoding.  Reuse it between calls; do not
+    share it between calls that run concurrently."""
+    if page_table is None or key_lens is None:
+        raise TypeError("page_table and key_lens must be int32 tensors")
+    if out is None:
+        _heads(q, "q", 4)
+        torch = _torch()
+        out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device) if q_lens is None else torch.zeros(q.shape, dtype=torch.bfloat16, device=q.device)
+    else:
+        out = _output(out, q.shape, q)
+    p = _cache_attention_problem(q, cache, page_table, key_lens, q_lens, tree, kv_len, scale, out)
+    ws, nbytes = _workspace(workspace, q)
+    _call("lowbit_cache_attention", q, p, ws, nbytes)
+    return out
+
+
+def gemv_affine(x, words, scales, biases, g: int, residual=None, swiglu: bool = False, out=None):
+    """gemm_affine for up to 16 rows (lowbit_gemv_affine): Y = X . W^T (+ residual), W = S * u + B with `words` from pack_u4.  swiglu: words,
+    scales and biases hold 2N rows, gate then up, and Y = silu(X . Wg^T) * (X . Wu^T) (+ residual).  residual bf16 [M, N], may be `out`."""
+    torch = _torch()
+    _require(x, torch.bfloat16, "x")
+    M, K = x.shape
+    pw = _plain(words, torch.int32, "words", 2, x)
+    ps = _plain(scales, torch.float16, "scales", 2, x)
+    pb = _plain(biases, torch.float16, "biases", 2, x)
+    rows, per_row = words.shape
+    if g not in (64, 128):
+        raise ValueError(f"g must be 64 or 128, got {g}")
+    if per_row != K // 8 or K % g or scales.shape != (rows, K // g) or biases.shape != scales.shape:
+        raise ValueError(f"words must be [{rows}, K/8], scales and biases [{rows}, K/g] with K = {K}, got {tuple(words.shape)}, "
+                         f"{tuple(scales.shape)} and {tuple(biases.shape)}")
+    if swiglu and rows % 2:
+        raise ValueError(f"words must hold 2N rows (gate then up), got {rows}")
+    N = rows // 2 if swiglu else rows
+    pr = 0
+    if residual is not None:
+        pr = _plain(residual, torch.bfloat16, "residual", 2, x)
+        if residual.shape != (M, N):
+            raise ValueError(f"residual must be [{M}, {N}]")
+    out = _output(out, (M, N), x)
+    po = _plain(out, torch.bfloat16, "out", 2, x)
+    _call("lowbit_gemv_affine", x, x.data_ptr(), pw, ps, pb, pr, po, M, N, K, g, 1 if swiglu else 0)
+    return out
+
+
 def check_gemm_args(x_ptr: int, w_ptr: int, s_ptr: int, y_ptr: int, M: int, N: int, K: int, g: int,
                     bits: int) -> int:
     """Host-only validation (no HIP call); returns the status code lowbit_gemm would return."""

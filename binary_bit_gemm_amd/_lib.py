@@ -35,6 +35,11 @@ SIGNATURES = {
     "lowbit_qk_norm_rope": (_INT, [_VP, _VP]),
     "lowbit_attention_workspace_size": (ctypes.c_size_t, [_VP]),
     "lowbit_attention": (_INT, [_VP, _VP, ctypes.c_size_t, _VP]),
+    "lowbit_cache_write": (_INT, [_VP, _VP, _VP] + [_I64] * 5 + [_VP, _VP]),
+    "lowbit_cache_read": (_INT, [_VP, _VP, _VP] + [_I64] * 5 + [_VP, _VP]),
+    "lowbit_cache_attention_workspace_size": (ctypes.c_size_t, [_VP]),
+    "lowbit_cache_attention": (_INT, [_VP, _VP, ctypes.c_size_t, _VP]),
+    "lowbit_gemv_affine": (_INT, [_VP, _VP, _VP, _VP, _VP, _VP, _I64, _I64, _I64, _INT, _INT, _VP]),
     "lowbit_check_gemm_args": (_INT, [_VP, _VP, _VP, _VP, _I64, _I64, _I64, _INT, _INT]),
     "lowbit_gemm_variant": (ctypes.c_char_p, [_I64, _I64, _I64, _INT, _INT]),
     "lowbit_status_string": (ctypes.c_char_p, [_INT]),

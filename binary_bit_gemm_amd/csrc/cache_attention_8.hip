@@ -1,0 +1,11 @@
+// Attention over a cache of 8-bit codes (cache_attention.h holds the kernel).
+#include "cache_attention.h"
+
+namespace lowbit {
+
+hipError_t launch_cache_attention_8(const CacheAttnArgs& a, int row_blocks, hipStream_t stream) {
+    return a.cache.head_dim == 64 ? launch_cache_attention_as<64, 8>(a, row_blocks, stream)
+                                  : launch_cache_attention_as<128, 8>(a, row_blocks, stream);
+}
+
+}  // namespace lowbit

@@ -17,7 +17,8 @@
  *   - weights kept as packed uint32 words plus scales ("backend/ -- FastAPI Mac backend",
  *     section "Checkpoint layout").
  * Around these linears: low-rank adapters (lowbit_gemm_lora), norms and rotation of queries and keys
- * (lowbit_qk_norm_rope) and attention (lowbit_attention), at the end.
+ * (lowbit_qk_norm_rope) and attention (lowbit_attention), at the end; and for decoding a quantised, paged cache
+ * (lowbit_cache_write, _read, lowbit_cache_attention) and matrix-vector products (lowbit_gemv_affine).
  *
  * ---------------------------------------------------------------------------------
  * Packed weight format (the pages leave the bit layout open; this is the library's):
@@ -419,6 +420,90 @@ typedef struct lowbit_attention_problem {
 
 size_t lowbit_attention_workspace_size(const lowbit_attention_problem* problem);
 int lowbit_attention(const lowbit_attention_problem* problem, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * ---- Decoding: a paged cache of keys and values, attention over it, and matrix-vector products ----
+ *
+ * lowbit_cache -- keys and values of many requests in pages of page_size tokens, in 16, 8 or 4 bits.  A token's slot is
+ * page * page_size + place; which pages a request has is the caller's table.
+ *   k, v    device, [pages, kv_heads, page_size, head_dim * bits / 8] bytes: bf16 at 16 bits, codes otherwise, in an order that suits
+ *           the attention kernel's lanes (csrc/kv_cache.h; rows come back in the usual order through lowbit_cache_read).
+ *   k_scales, v_scales  device bf16: 8 bits [pages, kv_heads, page_size], one scale per token and head; 4 bits [pages, kv_heads,
+ *           page_size, head_dim / 64, 2], scale and smallest value per 64 elements; 16 bits: unused.
+ *   page_size 16, 32, 64, 128 or 256; head_dim 64 or 128; pages * page_size < 2^31; pointers 16-byte aligned.
+ * What an element x stands for once written, with up(t) the smallest bf16 not below t:
+ *   8 bits: s * c,  s = up(max|x| * (1/127)) over the head's row, c = x / s rounded to even;
+ *   4 bits: s * u + b,  b = min x, s = up((max x - b) * (1/15)) over the 64 elements, u = (x - b) / s rounded to even, 0 .. 15
+ *   (in fp32, 1/127 and 1/15 rounded to it).
+ * Elements of a row (4 bits: of its 64) that holds an infinity or a NaN, or at 4 bits spans more than fp32's range, read back as NaN.
+ *
+ * lowbit_cache_write -- rows k, v [tokens, kv_heads, head_dim] (bf16, element (t, h, d) at k[t * k_token + h * k_head + d];
+ * strides in elements, multiples of 8) into slots[t] (device int32).  A slot outside [0, pages * page_size), e.g. -1, leaves
+ * that row out.  The slots of one call that are inside must differ from each other.
+ * lowbit_cache_read -- the rows at slots[t] as bf16 (rounded once at 8 bits; at 4 bits s u + b to fp32, then to bf16; slots may
+ * repeat).  Rows whose slot is outside the cache are left as they were.
+ */
+typedef struct lowbit_cache {
+    void *k, *v, *k_scales, *v_scales;
+    int64_t pages;
+    int32_t page_size, kv_heads, head_dim, bits;
+} lowbit_cache;
+
+int lowbit_cache_write(const lowbit_cache* cache, const void* k, const void* v, int64_t tokens, int64_t k_token, int64_t k_head,
+                       int64_t v_token, int64_t v_head, const int32_t* slots, void* stream);
+int lowbit_cache_read(const lowbit_cache* cache, void* k, void* v, int64_t tokens, int64_t k_token, int64_t k_head, int64_t v_token,
+                      int64_t v_head, const int32_t* slots, void* stream);
+
+/*
+ * lowbit_cache_attention -- O = softmax(scale * Q K^T over the allowed keys) V for the last tokens of each request, drafted ones
+ * as a tree among them, over the keys and values of a lowbit_cache (what they stand for, above; nothing is unpacked in memory).
+ *   q, o   device bf16, element (b, t, h, d) at q[b * q_batch + t * q_token + h * q_head + d]; strides in elements, multiples of
+ *          8.  q_heads % kv_heads == 0: q head h reads kv head h / (q_heads / kv_heads).  o must not overlap q.
+ *   page_table  device int32, page of keys j * page_size .. of request b at page_table[b * table_stride + j].  The keys of an entry
+ *          outside [0, pages) are left out.
+ *   key_lens  device int32 [batch]: the request's keys, its new tokens' (written before) being the last of them; more than kv_len
+ *          counts as kv_len.  kv_len: the most keys that a request can have here (host; the table's rows hold that many).
+ *   q_lens  device int32 [batch] or NULL (q_len each): a request's new tokens.  Rows of o past them are left as they were.
+ *   tree   device uint64 [batch, q_len] or NULL: new token t takes new token i where bit i of tree[b, t] is set (its ancestors and
+ *          itself; q_len <= 64).  NULL: those up to itself.  Every new token takes all keys before the new ones.
+ *   A row that takes no key gets zeros.  Slots that no row takes may hold anything; a NaN in a key or value reaches the rows that take it.
+ * Scores, softmax statistics and sums are fp32; a probability times its value's scale is rounded to fp16 (16 bits: the
+ * probability to bf16) for the second product, O to bf16 once.  q up to 2^100, values from 2^-80 to 2^100 in magnitude (and 0)
+ * stay inside fp32's range on the way.  Deterministic.
+ *   workspace  as for lowbit_attention: lowbit_cache_attention_workspace_size(problem) bytes (0: none), 16-byte aligned,
+ *          zero-filled before its first use, shared by calls that do not run at once; with none or too little the keys are not split
+ *          across workgroups.
+ * Meant for few new tokens; a prompt's long chunks go through lowbit_cache_read and lowbit_attention.
+ * page_table, key_lens and q_lens need 4-byte alignment, tree 8, q, o and workspace 16.
+ */
+typedef struct lowbit_cache_attention_problem {
+    lowbit_cache cache;
+    const void* q;
+    void* o;
+    const int32_t* page_table;
+    const int32_t* key_lens;
+    const int32_t* q_lens;
+    const uint64_t* tree;
+    int64_t batch, q_len, kv_len;
+    int64_t q_batch, q_token, q_head, o_batch, o_token, o_head, table_stride;
+    int32_t q_heads;
+    float scale;
+} lowbit_cache_attention_problem;
+
+size_t lowbit_cache_attention_workspace_size(const lowbit_cache_attention_problem* problem);
+int lowbit_cache_attention(const lowbit_cache_attention_problem* problem, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * lowbit_gemv_affine -- lowbit_gemm_affine for up to 16 rows (decoded or drafted tokens), bound by reading the weights once:
+ *     Y[m, n] = X[m] . W[n] (+ residual[m, n]),   W[n, k] = S[n, k/g] * u[n, k] + B[n, k/g].
+ *   swiglu != 0: W, S and B hold 2N rows, gate rows then up rows, and Y = silu(X . Wg^T) * (X . Wu^T) (+ residual), as
+ *       lowbit_gemm_swiglu.
+ *   residual  device bf16 [M, N] or NULL; may be Y itself.
+ * Other arguments, checks and errors as lowbit_gemm_affine; M > 16 returns LOWBIT_E_UNSUPPORTED.  Sums are fp32 with no weight
+ * rounded, Y is rounded to bf16 once (the last bits can differ from lowbit_gemm_affine's).
+ */
+int lowbit_gemv_affine(const void* X, const uint32_t* W, const void* S, const void* B, const void* residual, void* Y, int64_t M,
+                       int64_t N, int64_t K, int g, int swiglu, void* stream);
 
 /* Host-only argument check of lowbit_gemm (no HIP call): returns the status lowbit_gemm
  * would return before touching the device. */
