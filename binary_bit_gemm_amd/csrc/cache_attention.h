@@ -42,13 +42,28 @@ constexpr float kMostWeight = 0x1p12f;  // of p s: past it the row's factor move
 constexpr float kFirstFactor = 0x1p120f;  // of a row before its first keys: they set it
 constexpr float kCodeUnit = 0x1p24f;    // 1 / the value of code 1 as an fp16
 
-// A wave's tile as it comes from memory: per block of 16 keys the lane's words of K and V, and the scales of its four keys.
+// What a lane has of a tile: per block of 16 keys its words of K (a quarter of key l16's row) and of V (piece l16 of keys 4q ..).
 template <int D, int BITS>
-struct CacheTile {
-    static constexpr int kWords = CacheFmt<D, BITS>::kRow / 16;  // of K (a quarter of a row), and of V (a piece of four rows)
-    static constexpr int kScales = CacheFmt<D, BITS>::kScaleBytes;  // words of four keys
-    uint32_t k[2][kWords], v[2][kWords];
-    uint32_t ks[2][kScales > 0 ? kScales : 1], vs[2][kScales > 0 ? kScales : 1];
+struct TileShape {
+    static constexpr int kWords = CacheFmt<D, BITS>::kRow / 16;     // of K, and of V, per block
+    static constexpr int kScales = CacheFmt<D, BITS>::kScaleBytes;  // words that hold the scales of four keys
+    static constexpr int kUnit = kWords >= 4 ? 4 : 1;               // words of a copy to LDS
+    static constexpr int kCopies = 4 * kWords / kUnit;              // of a tile: K then V, block by block
+};
+template <int W>
+struct Words {
+    uint32_t w[W];
+};
+// The scales (4 bits: and smallest values) of the lane's keys 4q .. of a tile's two blocks, of K or of V.
+template <int D, int BITS>
+struct KeyScales {
+    static constexpr int kN = TileShape<D, BITS>::kScales > 0 ? TileShape<D, BITS>::kScales : 1;
+    uint32_t w[2][kN];
+};
+// K or V of a tile.
+template <int D, int BITS>
+struct TileWords {
+    Words<TileShape<D, BITS>::kWords> block[2];
 };
 
 // Running state of a wave for NB blocks of 16 rows.
@@ -98,46 +113,37 @@ __device__ __forceinline__ int o_column(int j, int m) {
     return BITS == 4 ? 64 * (j / 4) + 4 * m + j % 4 : D / 16 * m + j;
 }
 
-// The score operand ks of block kb: lane (q, l16) has eight codes of key l16.
+// The score operand ks of a block from the lane's words: eight codes of key l16.
 template <int D, int BITS>
-__device__ __forceinline__ u32x4_t k_operand(const CacheTile<D, BITS>& t, int kb, int ks) {
+__device__ __forceinline__ u32x4_t k_operand(const Words<TileShape<D, BITS>::kWords>& k, int ks) {
     if constexpr (BITS == 16) {
-        return u32x4_t{t.k[kb][4 * ks], t.k[kb][4 * ks + 1], t.k[kb][4 * ks + 2], t.k[kb][4 * ks + 3]};
+        return u32x4_t{k.w[4 * ks], k.w[4 * ks + 1], k.w[4 * ks + 2], k.w[4 * ks + 3]};
     } else if constexpr (BITS == 8) {
-        const uint32_t a = t.k[kb][2 * ks], b = t.k[kb][2 * ks + 1];
+        const uint32_t a = k.w[2 * ks], b = k.w[2 * ks + 1];
         return u32x4_t{perm_b32(0, a, 0x0C010C00u), perm_b32(0, a, 0x0C030C02u), perm_b32(0, b, 0x0C010C00u), perm_b32(0, b, 0x0C030C02u)};
     } else {
-        const uint32_t w = t.k[kb][ks], h = w >> 8;  // the second and fourth pair come 16 times too large
+        const uint32_t w = k.w[ks], h = w >> 8;  // the second and fourth pair come 16 times too large
         return u32x4_t{w & 0x000F000Fu, w & 0x00F000F0u, h & 0x000F000Fu, h & 0x00F000F0u};
     }
 }
 
-// The value operand j of a tile: lane (q, l16) has column o_column(j, l16) of keys 4q .. of block 0, then of block 1.
-// Odd columns of 4-bit codes come 16 times too large.
+// Keys 2p and 2p + 1 of a block in column o_column(j, l16): half of a word of the value operand.  Odd columns of 4-bit codes come
+// 16 times too large.
 template <int D, int BITS>
-__device__ __forceinline__ u32x4_t v_operand(const CacheTile<D, BITS>& t, int j) {
-    u32x4_t a;
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int p = 0; p < 2; ++p) {  // keys 2p and 2p + 1
-            constexpr int kPiece = CacheFmt<D, BITS>::kPiece;
-            uint32_t x;
-            if constexpr (BITS == 16) {
-                const int at = kPiece / 4 * 2 * p + j / 2;
-                x = perm_b32(t.v[kb][at + kPiece / 4], t.v[kb][at], j % 2 ? 0x07060302u : 0x05040100u);
-            } else if constexpr (BITS == 8) {
-                const int at = kPiece / 4 * 2 * p + j / 4;
-                x = perm_b32(t.v[kb][at + kPiece / 4], t.v[kb][at], 0x0C040C00u + 0x00010001u * (j % 4));
-            } else if constexpr (kPiece == 4) {
-                const int byte = 2 * (j / 4) + j % 4 / 2;
-                x = perm_b32(t.v[kb][2 * p + 1], t.v[kb][2 * p], 0x0C040C00u + 0x00010001u * byte) & (j % 2 ? 0x00F000F0u : 0x000F000Fu);
-            } else {
-                x = (j / 2 ? t.v[kb][p] >> 8 : t.v[kb][p]) & (j % 2 ? 0x00F000F0u : 0x000F000Fu);
-            }
-            a[2 * kb + p] = x;
-        }
-    return a;
+__device__ __forceinline__ uint32_t v_pair(const Words<TileShape<D, BITS>::kWords>& v, int j, int p) {
+    constexpr int kPiece = CacheFmt<D, BITS>::kPiece;
+    if constexpr (BITS == 16) {
+        const int at = kPiece / 4 * 2 * p + j / 2;
+        return perm_b32(v.w[at + kPiece / 4], v.w[at], j % 2 ? 0x07060302u : 0x05040100u);
+    } else if constexpr (BITS == 8) {
+        const int at = kPiece / 4 * 2 * p + j / 4;
+        return perm_b32(v.w[at + kPiece / 4], v.w[at], 0x0C040C00u + 0x00010001u * (j % 4));
+    } else if constexpr (kPiece == 4) {
+        const int byte = 2 * (j / 4) + j % 4 / 2;
+        return perm_b32(v.w[2 * p + 1], v.w[2 * p], 0x0C040C00u + 0x00010001u * byte) & (j % 2 ? 0x00F000F0u : 0x000F000Fu);
+    } else {
+        return (j / 2 ? v.w[p] >> 8 : v.w[p]) & (j % 2 ? 0x00F000F0u : 0x000F000Fu);
+    }
 }
 
 // A value of the lanes that share l16 (and so a row).
@@ -222,72 +228,132 @@ __device__ __forceinline__ void load_queries(CacheRowsState<D, BITS, NB>& w, con
     }
 }
 
-// Where the 16 keys of a block lie: (page * heads + head) * page_size + place of the first in its page; -1: no such page.
-__device__ __forceinline__ int64_t block_place(const CacheAttnArgs& a, const CacheWork& at, int key0, int end) {
-    if (key0 >= end) return -1;
-    const int page = __builtin_amdgcn_readfirstlane(a.table[int64_t(at.b) * a.table_stride + (key0 >> a.cache.page_shift)]);
-    if (uint32_t(page) >= uint32_t(a.cache.pages)) return -1;
-    return ((int64_t(page) * a.cache.heads + at.hk) << a.cache.page_shift) + (key0 & ((1 << a.cache.page_shift) - 1));
+// Where a tile's two blocks of 16 keys lie: (page * heads + head) * page_size + the place of the first in its page; 0 and not `ok`
+// where there is no such page or key.
+struct Places {
+    int64_t at[2];
+    bool ok[2];
+};
+// `end` > 0; t may be past the last tile.
+__device__ __forceinline__ Places tile_places(const CacheAttnArgs& a, const CacheWork& at, int t, int end) {
+    Places p;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb) {
+        const int64_t key = int64_t(kCacheTile) * t + 16 * kb;
+        const int in = key < end ? int(key) : end - 1;
+        const int page = __builtin_amdgcn_readfirstlane(a.table[int64_t(at.b) * a.table_stride + (in >> a.cache.page_shift)]);
+        p.ok[kb] = key < end && uint32_t(page) < uint32_t(a.cache.pages);
+        const int64_t row = ((int64_t(page) * a.cache.heads + at.hk) << a.cache.page_shift) + (in & ((1 << a.cache.page_shift) - 16));
+        p.at[kb] = p.ok[kb] ? row : 0;
+    }
+    return p;
 }
 
+// Rows of `size` bytes of a block; an empty resource (zeros without a read) where it is not there.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t block_rows(const unsigned char* base, const Places& p, int kb, int size) {
+    return make_rsrc(base + p.at[kb] * size, p.ok[kb] ? 16u * uint32_t(size) : 0u);
+}
+
+// The lane's byte in a block of K or V for copy or load i.
 template <int D, int BITS>
-__device__ __forceinline__ void load_block(CacheTile<D, BITS>& t, const CacheAttnArgs& a, int kb, int64_t place) {
+__device__ __forceinline__ uint32_t unit_offset(bool is_v, int i) {
     using F = CacheFmt<D, BITS>;
-    const int lane = int(threadIdx.x) & 63, q = lane >> 4, l16 = lane & 15;
-    const uint32_t none = place < 0 ? 0u : 1u;  // an empty resource: zeros without a read
-    const int64_t p = place < 0 ? 0 : place;
-    const auto kr = make_rsrc(a.cache.k + p * F::kRow, none * 16u * F::kRow);
-    const auto vr = make_rsrc(a.cache.v + p * F::kRow, none * 16u * F::kRow);
-    constexpr int kW = CacheTile<D, BITS>::kWords;
-    if constexpr (kW >= 4) {
+    const uint32_t lane = threadIdx.x & 63u, q = lane >> 4, l16 = lane & 15u;
+    constexpr uint32_t kT = F::kBlock;
+    if constexpr (TileShape<D, BITS>::kUnit == 4)
+        return is_v ? 4u * q / kT * (kT * F::kRow) + 16u * l16 + kT * F::kRow * i : l16 * F::kRow + 16u * q + 64u * i;
+    else
+        return (is_v ? q * (4u * F::kRow) + 8u * l16 : l16 * F::kRow + 8u * q) + 4u * i;
+}
+
+// K or V of a tile into registers.
+template <int D, int BITS, bool IS_V>
+__device__ __forceinline__ void load_words(TileWords<D, BITS>& t, const CacheAttnArgs& a, const Places& p) {
+    constexpr int kW = TileShape<D, BITS>::kWords;
 #pragma unroll
-        for (int i = 0; i < kW / 4; ++i) {
-            const u32x4_t x = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(kr, uint32_t(l16 * F::kRow + 16 * q) + 64u * i, 0, 0));
+    for (int kb = 0; kb < 2; ++kb) {
+        const auto rs = block_rows(IS_V ? a.cache.v : a.cache.k, p, kb, CacheFmt<D, BITS>::kRow);
+        if constexpr (kW >= 4) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) t.k[kb][4 * i + e] = x[e];
-        }
-        constexpr int kT = F::kBlock;
+            for (int i = 0; i < kW / 4; ++i) {
+                const u32x4_t x = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, unit_offset<D, BITS>(IS_V, i), 0, 0));
 #pragma unroll
-        for (int i = 0; i < kW / 4; ++i) {  // 16 bytes: kBlock keys
-            const u32x4_t x = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                                              vr, uint32_t(4 * q / kT * (kT * F::kRow) + 16 * l16) + uint32_t(kT * F::kRow * i), 0, 0));
-#pragma unroll
-            for (int e = 0; e < 4; ++e) t.v[kb][4 * i + e] = x[e];
-        }
-    } else {
-        const u32x2_t x = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(kr, uint32_t(l16 * F::kRow + 8 * q), 0, 0));
-        const u32x2_t y = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(vr, uint32_t(q * (4 * F::kRow) + 8 * l16), 0, 0));
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            t.k[kb][e] = x[e];
-            t.v[kb][e] = y[e];
-        }
-    }
-    if constexpr (BITS != 16) {
-        constexpr int kS = F::kScaleBytes;
-        const auto ksr = make_rsrc(a.cache.k_scales + p * kS, none * 16u * kS);
-        const auto vsr = make_rsrc(a.cache.v_scales + p * kS, none * 16u * kS);
-        if constexpr (kS == 2) {
-            const u32x2_t x = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(ksr, uint32_t(8 * q), 0, 0));
-            const u32x2_t y = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(vsr, uint32_t(8 * q), 0, 0));
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                t.ks[kb][e] = x[e];
-                t.vs[kb][e] = y[e];
+                for (int e = 0; e < 4; ++e) t.block[kb].w[4 * i + e] = x[e];
             }
         } else {
+            const u32x2_t x = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(rs, unit_offset<D, BITS>(IS_V, 0), 0, 0));
+            t.block[kb].w[0] = x[0];
+            t.block[kb].w[1] = x[1];
+        }
+    }
+}
+
+template <int D, int BITS, bool IS_V>
+__device__ __forceinline__ void load_scales(KeyScales<D, BITS>& s, const CacheAttnArgs& a, const Places& p) {
+    constexpr int kS = CacheFmt<D, BITS>::kScaleBytes;
+    if constexpr (kS > 0) {
+        const uint32_t q = (threadIdx.x & 63u) >> 4;
 #pragma unroll
-            for (int i = 0; i < kS / 4; ++i) {
-                const u32x4_t x = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(ksr, uint32_t(4 * kS * q + 16 * i), 0, 0));
-                const u32x4_t y = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(vsr, uint32_t(4 * kS * q + 16 * i), 0, 0));
+        for (int kb = 0; kb < 2; ++kb) {
+            const auto rs = block_rows(IS_V ? a.cache.v_scales : a.cache.k_scales, p, kb, kS);
+            if constexpr (kS == 2) {
+                const u32x2_t x = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(rs, 8u * q, 0, 0));
+                s.w[kb][0] = x[0];
+                s.w[kb][1] = x[1];
+            } else {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    t.ks[kb][4 * i + e] = x[e];
-                    t.vs[kb][4 * i + e] = y[e];
+                for (int i = 0; i < kS / 4; ++i) {
+                    const u32x4_t x = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, 4u * kS * q + 16u * i, 0, 0));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s.w[kb][4 * i + e] = x[e];
                 }
             }
         }
     }
+}
+
+// The wave's quarter of a tile's copies to LDS, lane by lane.
+template <int D, int BITS>
+__device__ __forceinline__ void copy_tile(unsigned char* lds, const CacheAttnArgs& a, const Places& p, int wave) {
+    using S = TileShape<D, BITS>;
+    constexpr int kPer = S::kWords / S::kUnit;  // copies of a block of K or V
+#pragma unroll
+    for (int c = 0; c < S::kCopies / 4; ++c) {
+        const int copy = wave * (S::kCopies / 4) + c;  // the same for the wave
+        const bool is_v = copy >= 2 * kPer;
+        const int kb = copy / kPer % 2, i = copy % kPer;
+        Places one = p;
+        one.at[0] = kb ? p.at[1] : p.at[0];
+        one.ok[0] = kb ? p.ok[1] : p.ok[0];
+        const auto rs = block_rows(is_v ? a.cache.v : a.cache.k, one, 0, CacheFmt<D, BITS>::kRow);
+        unsigned char* const to = lds + copy * (256 * S::kUnit);
+        const uint32_t from = unit_offset<D, BITS>(is_v, i);
+        if constexpr (S::kUnit == 4)
+            dma16(rs, to, from, 0);
+        else
+            dma4(rs, to, from, 0);
+    }
+}
+
+// K or V of a tile from there: a lane reads the 16 (or 4) bytes that its number brought.
+template <int D, int BITS, bool IS_V>
+__device__ __forceinline__ void read_words(TileWords<D, BITS>& t, const unsigned char* lds) {
+    using S = TileShape<D, BITS>;
+    constexpr int kPer = S::kWords / S::kUnit;
+    const unsigned char* const at = lds + (threadIdx.x & 63u) * (4 * S::kUnit);
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            const unsigned char* const from = at + ((IS_V ? 2 : 0) + kb) * kPer * (256 * S::kUnit) + i * (256 * S::kUnit);
+            if constexpr (S::kUnit == 4) {
+                const u32x4_t x = *reinterpret_cast<const u32x4_t*>(from);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) t.block[kb].w[4 * i + e] = x[e];
+            } else {
+                t.block[kb].w[i] = *reinterpret_cast<const uint32_t*>(from);
+            }
+        }
 }
 
 // The scale of the lane's key i of block kb, and (4 bits, group g) its smallest value.
@@ -305,29 +371,29 @@ __device__ __forceinline__ float low_at(const uint32_t* s, int i, int g) {
 
 __device__ __forceinline__ bool odd_bf16(uint32_t half) { return (half & 0x7F80u) == 0x7F80u; }
 
-// 16-bit values that are an infinity or a NaN, in a tile with keys that some row leaves out (zero in a product does not silence them):
-// they are added to the rows that take their keys, and become zeros in the operand.
+// The pair without its infinities and NaN.
+__device__ __forceinline__ uint32_t finite_pair(uint32_t x) {
+    if (odd_bf16(x)) x &= 0xFFFF0000u;
+    if (odd_bf16(x >> 16)) x &= 0xFFFFu;
+    return x;
+}
+
+// 16-bit values that are an infinity or a NaN, in a tile with keys that some row leaves out (zero in a product does not silence them, so
+// they are zeros in the operands): added to the rows that take their keys.
 template <int D, int NB>
-__device__ __forceinline__ void set_odd_values_aside(CacheRowsState<D, 16, NB>& w, CacheTile<D, 16>& t, const CacheAttnArgs& a,
-                                                     const int64_t (&place)[2], const uint32_t (&allowed)[NB]) {
+__device__ __forceinline__ void add_odd_values(CacheRowsState<D, 16, NB>& w, const CacheAttnArgs& a, const Places& place,
+                                               const uint32_t (&allowed)[NB]) {
     using F = CacheFmt<D, 16>;
-    constexpr int kW = CacheTile<D, 16>::kWords;
-    const int lane = int(threadIdx.x) & 63, q = lane >> 4;
-    bool odd = false;
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int e = 0; e < kW; ++e) odd = odd || odd_bf16(t.v[kb][e]) || odd_bf16(t.v[kb][e] >> 16);
-    if (!__any(odd)) return;
+    const uint32_t q = (threadIdx.x & 63u) >> 4;
     for (int key = 0; key < kCacheTile; ++key) {
-        const int64_t p = key < 16 ? place[0] : place[1];
-        bool some = false;
+        const int64_t p = key < 16 ? place.at[0] : place.at[1];
+        bool some = false;  // (a key that is not there is allowed to no row)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) some = some || ((allowed[nb] >> key) & 1);
-        if (p < 0 || !__any(some)) continue;
+        if (!__any(some)) continue;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {  // the lane's columns: pieces 4q + i
-            const unsigned char* src = a.cache.v + p * F::kRow + F::v_offset(uint32_t(key & 15), uint32_t(4 * q + i));
+            const unsigned char* src = a.cache.v + p * F::kRow + F::v_offset(uint32_t(key & 15), 4u * q + i);
 #pragma unroll
             for (int j = 0; j < D / 16; ++j) {
                 const uint32_t b = reinterpret_cast<const uint16_t*>(src)[j];
@@ -337,200 +403,235 @@ __device__ __forceinline__ void set_odd_values_aside(CacheRowsState<D, 16, NB>& 
             }
         }
     }
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int e = 0; e < kW; ++e) {
-            if (odd_bf16(t.v[kb][e])) t.v[kb][e] &= 0xFFFF0000u;
-            if (odd_bf16(t.v[kb][e] >> 16)) t.v[kb][e] &= 0xFFFFu;
-        }
 }
 
-// One tile.  PARTIAL: some row leaves out some of its keys (bit of `allowed` clear; bit of `live` clear: a key that is not there).
-template <bool PARTIAL, int D, int BITS, int NB>
-__device__ __forceinline__ void cache_step(CacheRowsState<D, BITS, NB>& w, CacheTile<D, BITS>& t, const CacheAttnArgs& a,
-                                           const int64_t (&place)[2], uint32_t live, const uint32_t (&allowed)[NB]) {
-    constexpr int kGroups = CacheFmt<D, BITS>::kGroups;
-    const int lane = int(threadIdx.x) & 63, q = lane >> 4;
-    if constexpr (PARTIAL) {  // what lies where no key is may be anything
-        constexpr int kW = CacheTile<D, BITS>::kWords;
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (!((live >> (16 * kb + 4 * q + i)) & 1)) {
-                    if constexpr (BITS == 16) {
-#pragma unroll
-                        for (int e = 0; e < kW / 4; ++e) t.v[kb][kW / 4 * i + e] = 0;
-                    } else if constexpr (BITS == 8) {
-                        t.vs[kb][i / 2] &= i % 2 ? 0xFFFFu : 0xFFFF0000u;
-                    } else {
-#pragma unroll
-                        for (int g = 0; g < kGroups; ++g) t.vs[kb][i * kGroups + g] = 0;
-                    }
-                }
-        if constexpr (BITS == 16) set_odd_values_aside<D, NB>(w, t, a, place, allowed);
-    }
-    // scores, in powers of two
+// Scores of a tile, in powers of two: [block][row block], keys 16 kb + 4q ..
+template <int NB>
+struct TileScores {
     f32x4_t s[2][NB];
-    if constexpr (BITS == 4) {
+};
+
+template <int D, int BITS, int NB>
+__device__ __forceinline__ void tile_scores(const CacheRowsState<D, BITS, NB>& w, const TileWords<D, BITS>& k, const KeyScales<D, BITS>& ks,
+                                            TileScores<NB>& x) {
+    constexpr int kGroups = CacheFmt<D, BITS>::kGroups;
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
+    for (int kb = 0; kb < 2; ++kb) {
+        if constexpr (BITS == 4) {
             f32x4_t raw[kGroups][NB];
 #pragma unroll
             for (int g = 0; g < kGroups; ++g)
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) raw[g][nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int ks = 0; ks < D / 32; ++ks) {
-                const u32x4_t k = k_operand<D, BITS>(t, kb, ks);
+            for (int ks32 = 0; ks32 < D / 32; ++ks32) {
+                const u32x4_t op = k_operand<D, BITS>(k.block[kb], ks32);
 #pragma unroll
-                for (int nb = 0; nb < NB; ++nb) raw[ks / 2][nb] = cache_mfma<BITS>(k, w.q[ks][nb], raw[ks / 2][nb]);
+                for (int nb = 0; nb < NB; ++nb) raw[ks32 / 2][nb] = cache_mfma<BITS>(op, w.q[ks32][nb], raw[ks32 / 2][nb]);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
-                    float x = 0.f, y = 0.f;
-#pragma unroll
-                    for (int g = 0; g < kGroups; ++g) {
-                        x = __builtin_fmaf(raw[g][nb][i], scale_at<D, BITS>(t.ks[kb], i, g), x);
-                        y = __builtin_fmaf(w.qsum[nb][g], low_at<D, BITS>(t.ks[kb], i, g), y);
+                    float sum = raw[0][nb][i] * scale_at<D, BITS>(ks.w[kb], i, 0), low = w.qsum[nb][0] * low_at<D, BITS>(ks.w[kb], i, 0);
+                    if constexpr (kGroups == 2) {
+                        sum = __builtin_fmaf(raw[1][nb][i], scale_at<D, BITS>(ks.w[kb], i, 1), sum);
+                        low = __builtin_fmaf(w.qsum[nb][1], low_at<D, BITS>(ks.w[kb], i, 1), low);
                     }
-                    s[kb][nb][i] = __builtin_fmaf(x, w.gain[nb], y);
+                    x.s[kb][nb][i] = __builtin_fmaf(sum, w.gain[nb], low);
                 }
-        }
-    } else {
+        } else {
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
+            for (int nb = 0; nb < NB; ++nb) x.s[kb][nb] = f32x4_t{w.start[nb], w.start[nb], w.start[nb], w.start[nb]};
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) s[kb][nb] = f32x4_t{w.start[nb], w.start[nb], w.start[nb], w.start[nb]};
+            for (int ks32 = 0; ks32 < D / 32; ++ks32) {
+                const u32x4_t op = k_operand<D, BITS>(k.block[kb], ks32);
 #pragma unroll
-            for (int ks = 0; ks < D / 32; ++ks) {
-                const u32x4_t k = k_operand<D, BITS>(t, kb, ks);
-#pragma unroll
-                for (int nb = 0; nb < NB; ++nb) s[kb][nb] = cache_mfma<BITS>(k, w.q[ks][nb], s[kb][nb]);
+                for (int nb = 0; nb < NB; ++nb) x.s[kb][nb] = cache_mfma<BITS>(op, w.q[ks32][nb], x.s[kb][nb]);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
-                    s[kb][nb][i] *= BITS == 16 ? w.gain[nb] : w.gain[nb] * scale_at<D, 8>(t.ks[kb], i, 0);
+                    x.s[kb][nb][i] *= BITS == 16 ? w.gain[nb] : w.gain[nb] * scale_at<D, 8>(ks.w[kb], i, 0);
         }
     }
-    bool takes[2][NB][4];
-    if constexpr (PARTIAL) {
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    takes[kb][nb][i] = (allowed[nb] >> (16 * kb + 4 * q + i)) & 1;
-                    s[kb][nb][i] = takes[kb][nb][i] ? s[kb][nb][i] : kNegInf;
-                }
-    }
-    // the maximum follows where a score is more than kRise above it
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-        float top = kNegInf;
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top = fmaxf(top, s[kb][nb][i]);
-        if (__any(top > w.m[nb] + kRise)) {
-            top = row_max(top);
-            const bool move = top > w.m[nb] + kRise;
-            const float f = move ? __builtin_amdgcn_exp2f(w.m[nb] - top) : 1.f;
-            w.m[nb] = move ? top : w.m[nb];
-            w.l[nb] *= f;
-            w.low[nb][0] *= f;
-            w.low[nb][1] *= f;
-            float fo = f;
-            if constexpr (BITS != 16) {  // the values that now count may be far smaller: let p s set the row's factor anew
-                const float r = move ? fminf(w.r[nb] * 0x1p30f, kFirstFactor) : w.r[nb];
-                fo *= r / w.r[nb];
-                w.r[nb] = r;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w.sum[nb][i] *= fo;
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w.o[j][nb][i] *= fo;
-        }
-    }
-    // probabilities, and their products with the values' scales
-    u32x4_t p[NB][kGroups];
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-        const float m = w.m[nb] == kNegInf ? 0.f : w.m[nb];  // without a key yet every score is -inf
+}
+
+// Whether the lane's row takes its key i of block kb.
+__device__ __forceinline__ bool takes(uint32_t allowed, int kb, int i) {
+    return (allowed >> (16 * kb + 4 * ((threadIdx.x & 63u) >> 4) + i)) & 1;
+}
+
+// Maximum and factor of row block nb to what the scores x and the values' scales need, and the sums with them.
+template <int D, int BITS, int NB>
+__device__ __forceinline__ void rebase(CacheRowsState<D, BITS, NB>& w, int nb, const TileScores<NB>& x, const KeyScales<D, BITS>& vs, float top) {
+    top = row_max(top);
+    const bool move = top > w.m[nb] + kRise;
+    const float f = move ? __builtin_amdgcn_exp2f(w.m[nb] - top) : 1.f;
+    w.m[nb] = move ? top : w.m[nb];
+    w.l[nb] *= f;
+    float fo = f;
+    if constexpr (BITS != 16) {
+        w.low[nb][0] *= f;
+        w.low[nb][1] *= f;
+        // where the maximum moved, the values that now count may be far smaller: p s sets the factor anew
+        float r = move ? fminf(w.r[nb] * 0x1p30f, kFirstFactor) : w.r[nb];
+        const float m = w.m[nb] == kNegInf ? 0.f : w.m[nb];
+        float most = 0.f;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                s[kb][nb][i] = __builtin_amdgcn_exp2f(s[kb][nb][i] - m);
-                w.l[nb] += s[kb][nb][i];
+                const float p = __builtin_amdgcn_exp2f(x.s[kb][nb][i] - m);
+#pragma unroll
+                for (int g = 0; g < CacheFmt<D, BITS>::kGroups; ++g) most = fmaxf(most, p * scale_at<D, BITS>(vs.w[kb], i, g));
             }
-        if constexpr (BITS == 16) {
+        most = row_max(most);
+        if (most * r > kMostWeight) {  // such that the largest of these lies in [1, 2)
+            int up = 127 - int(__float_as_uint(most) >> 23);
+            up = up < -126 ? -126 : up > 120 ? 120 : up;
+            r = power_of_two(up);
+        }
+        fo *= r / w.r[nb];
+        w.r[nb] = r;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w.sum[nb][i] *= fo;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) w.o[j][nb][i] *= fo;
+}
+
+template <int D, int BITS, int NB>
+struct TileWeights {
+    u32x4_t p[NB][CacheFmt<D, BITS>::kGroups];  // operands: p s (16 bits: p), keys 4q .. of block 0, then of block 1
+};
+
+// The probabilities of a tile's scores, times the values' scales.  PARTIAL: a row leaves out its keys whose bit of `allowed` is clear.
+template <bool PARTIAL, int D, int BITS, int NB>
+__device__ __forceinline__ void tile_weights(CacheRowsState<D, BITS, NB>& w, TileScores<NB>& x, const KeyScales<D, BITS>& vs,
+                                             const uint32_t (&allowed)[NB], TileWeights<D, BITS, NB>& p) {
+    constexpr int kGroups = CacheFmt<D, BITS>::kGroups;
+    float most = 0.f;  // of the values' scales
+    if constexpr (BITS != 16) {
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) most = fmaxf(most, scale_at<D, BITS>(vs.w[kb], i, g));
+    }
+    float top[NB];
+    bool again = false;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        top[nb] = kNegInf;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (PARTIAL) x.s[kb][nb][i] = takes(allowed[nb], kb, i) ? x.s[kb][nb][i] : kNegInf;
+                top[nb] = fmaxf(top[nb], x.s[kb][nb][i]);
+            }
+        again = again || top[nb] > w.m[nb] + kRise;
+        // (a bound: the largest score and the largest scale need not be one key's)
+        if constexpr (BITS != 16) again = again || __builtin_amdgcn_exp2f(top[nb] - w.m[nb]) * most * w.r[nb] > kMostWeight;
+    }
+    if (__any(again)) {
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) rebase(w, nb, x, vs, top[nb]);
+    }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        const float m = w.m[nb] == kNegInf ? 0.f : w.m[nb];  // without a key yet every score is -inf
+        float y[2][4];
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                y[kb][i] = __builtin_amdgcn_exp2f(x.s[kb][nb][i] - m);
+                w.l[nb] += y[kb][i];
+            }
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g)
 #pragma unroll
             for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
-                for (int i = 0; i < 4; i += 2) p[nb][0][2 * kb + i / 2] = pack_bf16(s[kb][nb][i], s[kb][nb][i + 1]);
-        } else {
-            // a probability times a NaN scale: in the rows that take the key only
-            auto weight = [&](int kb, int i, int g) __attribute__((always_inline)) {
-                const float x = s[kb][nb][i] * scale_at<D, BITS>(t.vs[kb], i, g);
-                return PARTIAL && !takes[kb][nb][i] ? 0.f : x;
-            };
-            float top = 0.f, x[kGroups][2][4];
+                for (int i = 0; i < 4; i += 2) {
+                    if constexpr (BITS == 16) {
+                        p.p[nb][0][2 * kb + i / 2] = pack_bf16(y[kb][i], y[kb][i + 1]);
+                    } else {
+                        float z[2];
 #pragma unroll
-            for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        x[g][kb][i] = weight(kb, i, g);
-                        top = fmaxf(top, x[g][kb][i]);
-                        if constexpr (BITS == 4) {
-                            const float y = s[kb][nb][i] * low_at<D, BITS>(t.vs[kb], i, g);
-                            w.low[nb][g] += PARTIAL && !takes[kb][nb][i] ? 0.f : y;
+                        for (int e = 0; e < 2; ++e) {
+                            // a probability times a NaN scale: in the rows that take the key only
+                            const bool in = !PARTIAL || takes(allowed[nb], kb, i + e);
+                            z[e] = y[kb][i + e] * (scale_at<D, BITS>(vs.w[kb], i + e, g) * w.r[nb]);
+                            z[e] = in ? z[e] : 0.f;
+                            if constexpr (BITS == 4) {
+                                const float low = y[kb][i + e] * low_at<D, BITS>(vs.w[kb], i + e, g);
+                                w.low[nb][g] += in ? low : 0.f;
+                            }
                         }
+                        p.p[nb][g][2 * kb + i / 2] = pack_f16(z[0], z[1]);
                     }
-            if (__any(top * w.r[nb] > kMostWeight)) {  // the row's factor: such that the largest of these lies in [1, 2)
-                top = row_max(top);
-                const bool move = top * w.r[nb] > kMostWeight;
-                int up = 127 - int(__float_as_uint(top) >> 23);
-                up = up < -126 ? -126 : up > 120 ? 120 : up;
-                const float r = move ? power_of_two(up) : w.r[nb], f = r / w.r[nb];
-                w.r[nb] = r;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w.sum[nb][i] *= f;
-#pragma unroll
-                for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) w.o[j][nb][i] *= f;
-            }
-#pragma unroll
-            for (int g = 0; g < kGroups; ++g)
-#pragma unroll
-                for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-                    for (int i = 0; i < 4; i += 2) p[nb][g][2 * kb + i / 2] = pack_f16(x[g][kb][i] * w.r[nb], x[g][kb][i + 1] * w.r[nb]);
-        }
+                }
     }
-    // values
+}
+
+// O += V^T P^T of a tile.
+template <bool PARTIAL, int D, int BITS, int NB>
+__device__ __forceinline__ void tile_values(CacheRowsState<D, BITS, NB>& w, const TileWords<D, BITS>& v, const TileWeights<D, BITS, NB>& p,
+                                            const CacheAttnArgs& a, const Places& place, uint32_t live, const uint32_t (&allowed)[NB]) {
+    uint32_t here[4];  // 16 bits: the pairs' keys that are there
+    if constexpr (PARTIAL && BITS == 16) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) here[e] = (takes(live, e / 2, 2 * (e % 2)) ? 0xFFFFu : 0u) | (takes(live, e / 2, 2 * (e % 2) + 1) ? 0xFFFF0000u : 0u);
+    }
     if constexpr (BITS == 8) {
         const u32x4_t ones = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) w.sum[nb] = cache_mfma<BITS>(ones, p[nb][0], w.sum[nb]);
+        for (int nb = 0; nb < NB; ++nb) w.sum[nb] = cache_mfma<BITS>(ones, p.p[nb][0], w.sum[nb]);
     }
+    bool odd = false;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) {
-        const u32x4_t v = v_operand<D, BITS>(t, j);
+        u32x4_t op;
 #pragma unroll
-        for (int nb = 0; nb < NB; ++nb) w.o[j][nb] = cache_mfma<BITS>(v, p[nb][BITS == 4 ? j / 4 : 0], w.o[j][nb]);
+        for (int e = 0; e < 4; ++e) {
+            op[e] = v_pair<D, BITS>(v.block[e / 2], j, e % 2);
+            if constexpr (PARTIAL && BITS == 16) {
+                const uint32_t there = op[e] & here[e];
+                op[e] = finite_pair(there);
+                odd = odd || op[e] != there;
+            }
+        }
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb) w.o[j][nb] = cache_mfma<BITS>(op, p.p[nb][BITS == 4 ? j / 4 : 0], w.o[j][nb]);
     }
+    if constexpr (PARTIAL && BITS == 16) {
+        if (__any(odd)) add_odd_values<D, NB>(w, a, place, allowed);
+    }
+}
+
+// The scales of keys that are not there, which may be anything, to zeros.
+template <int D, int BITS>
+__device__ __forceinline__ void clear_scales(KeyScales<D, BITS>& s, uint32_t live) {
+    constexpr int kGroups = CacheFmt<D, BITS>::kGroups;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const bool is = takes(live, kb, i);
+            if constexpr (BITS == 8) {
+                if (!is) s.w[kb][i / 2] &= i % 2 ? 0xFFFFu : 0xFFFF0000u;
+            } else if constexpr (BITS == 4) {
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) s.w[kb][i * kGroups + g] = is ? s.w[kb][i * kGroups + g] : 0u;
+            }
+        }
 }
 
 // Bits 0 .. rel (none for rel < 0) of 32.
@@ -546,8 +647,114 @@ __device__ __forceinline__ uint32_t taken(bool tree, uint64_t own, int token, in
     return uint32_t(own << int(-rel)) | first_bits(-rel - 1);
 }
 
+// Which rows and keys a workgroup has; false: none.
+struct CacheRange {
+    CacheWork at;
+    int group_of;    // of the workgroups that share rows
+    int split, end;  // keys that some row takes: [0, end)
+    int first;       // that every row takes: [0, first)
+    int t0, t1;      // tiles
+    bool tree;
+};
+__device__ __forceinline__ bool cache_range(CacheRange& r, const CacheAttnArgs& a, int rows_of_tile) {
+    // row tiles of one range of keys next to each other on one XCD, then the ranges of one head
+    int id = xcd_remap(int(blockIdx.x), int(gridDim.x));
+    const int rt = id % a.row_tiles;
+    id /= a.row_tiles;
+    r.split = id % a.splits;
+    id /= a.splits;
+    r.at.hk = id % a.cache.heads;
+    r.at.b = id / a.cache.heads;
+    r.group_of = (r.at.b * a.cache.heads + r.at.hk) * a.row_tiles + rt;
+    int n = a.lens[r.at.b];
+    n = n < 0 ? 0 : n < a.kv_len ? n : a.kv_len;
+    int ql = a.q_len;
+    if (a.q_lens != nullptr) {
+        const int v = a.q_lens[r.at.b];
+        ql = v < 0 ? 0 : v < ql ? v : ql;
+    }
+    r.at.n = n = __builtin_amdgcn_readfirstlane(n);
+    ql = __builtin_amdgcn_readfirstlane(ql);
+    r.at.base = n - ql;
+    r.at.row0 = rt * rows_of_tile;
+    const int64_t left = int64_t(ql) * a.group - r.at.row0;
+    if (left <= 0) return false;  // rows past the request's last token, in every range of keys
+    r.at.rows = left < rows_of_tile ? int(left) : rows_of_tile;
+    r.tree = a.tree != nullptr;
+    const int64_t last = r.tree ? n : int64_t(r.at.base) + (r.at.row0 + r.at.rows - 1) / a.group + 1;
+    r.end = last < 0 ? 0 : last < n ? int(last) : n;
+    const int64_t first = r.tree ? r.at.base : int64_t(r.at.base) + r.at.row0 / a.group + 1;
+    r.first = first < 0 ? 0 : first < n ? int(first) : n;
+    const int tiles = (r.end + kCacheTile - 1) / kCacheTile;
+    // the ranges share the keys there are, not the keys there could be
+    r.t0 = int(int64_t(tiles) * r.split / a.splits);
+    r.t1 = int(int64_t(tiles) * (r.split + 1) / a.splits);
+    return true;
+}
+
+// The token of each of the lane's rows (those past the last: the tile's first), and its tree.
+template <int NB>
+struct RowTokens {
+    int token[NB];
+    uint64_t own[NB];
+};
+template <int NB>
+__device__ __forceinline__ RowTokens<NB> row_tokens(const CacheRange& r, const CacheAttnArgs& a, const CacheWork& at) {
+    RowTokens<NB> k;
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        const int in_tile = 16 * nb + (int(threadIdx.x) & 15);
+        const int row = in_tile < at.rows ? at.row0 + in_tile : r.at.row0;
+        k.token[nb] = row / a.group;
+        k.own[nb] = r.tree ? a.tree[int64_t(at.b) * a.q_len + k.token[nb]] : 0;
+    }
+    return k;
+}
+
+// Keys of tile t that are there, and those that each of the lane's rows takes.
+template <int NB>
+__device__ __forceinline__ uint32_t tile_keys(uint32_t (&allowed)[NB], const CacheRange& r, const RowTokens<NB>& k, const Places& place, int t) {
+    const int key0 = kCacheTile * t;
+    const uint32_t live = first_bits(int64_t(r.at.n) - key0 - 1) & ((place.ok[0] ? 0xFFFFu : 0u) | (place.ok[1] ? 0xFFFF0000u : 0u));
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) allowed[nb] = live & taken(r.tree, k.own[nb], k.token[nb], r.at.base, key0);
+    return live;
+}
+
+// Every row takes every key of tile t, and they are there.
+__device__ __forceinline__ bool whole_tile(const CacheRange& r, const Places& place, int t) {
+    return kCacheTile * (t + 1) <= r.first && place.ok[0] && place.ok[1];
+}
+
+// O of the lane's row in block nb: element [j][i], column o_column(j, 4q + i), as a number.
+template <int D, int BITS, int NB, class F>
+__device__ __forceinline__ void each_o(const CacheRowsState<D, BITS, NB>& w, int nb, F f) {
+    float low[2] = {0.f, 0.f};
+    if constexpr (BITS == 4) {
+        low[0] = row_sum(w.low[nb][0]);
+        low[1] = row_sum(w.low[nb][1]);
+    }
+    const float unit = BITS == 16 ? 1.f : kCodeUnit / w.r[nb], minus = BITS == 8 ? 128.f / w.r[nb] : 0.f;
+#pragma unroll
+    for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float v = w.o[j][nb][i] * (BITS == 4 && j % 2 ? unit * 0.0625f : unit);
+            if constexpr (BITS == 8) v -= minus * w.sum[nb][i];
+            if constexpr (BITS == 4) v += low[j / 4];
+            f(j, i, v);
+        }
+}
+
+__device__ __forceinline__ uint16_t* o_row(const CacheAttnArgs& a, const CacheWork& at, int in_tile) {
+    const int row = at.row0 + in_tile;
+    const int tok = row / a.group, g = row - tok * a.group;
+    return a.o + int64_t(at.b) * a.o_batch + int64_t(tok) * a.o_token + int64_t(at.hk * a.group + g) * a.o_head;
+}
+
+// Few rows (decoded tokens): the waves take tiles in turn.
 template <int D, int BITS, int NB>
-__global__ __launch_bounds__(256, NB == 4 ? 1 : 2) void cache_attention_kernel(CacheAttnArgs a) {
+__global__ __launch_bounds__(256, 2) void cache_attention_kernel(CacheAttnArgs a) {
     constexpr int kWaves = 4, kRows = 16 * NB;
     __shared__ __attribute__((aligned(16))) float lds_o[kWaves][kRows * D];
     __shared__ float lds_m[kWaves][kRows], lds_l[kWaves][kRows];
@@ -555,91 +762,68 @@ __global__ __launch_bounds__(256, NB == 4 ? 1 : 2) void cache_attention_kernel(C
     const int lane = int(threadIdx.x) & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
     const int q = lane >> 4, l16 = lane & 15;
-    // row tiles of one range of keys next to each other on one XCD, then the ranges of one head
-    int id = xcd_remap(int(blockIdx.x), int(gridDim.x));
-    const int rt = id % a.row_tiles;
-    id /= a.row_tiles;
-    const int split = id % a.splits;
-    id /= a.splits;
-    CacheWork at;
-    at.hk = id % a.cache.heads;
-    at.b = id / a.cache.heads;
-    const int group_of = (at.b * a.cache.heads + at.hk) * a.row_tiles + rt;  // of the workgroups that share rows
-    int n = a.lens[at.b];
-    n = n < 0 ? 0 : n < a.kv_len ? n : a.kv_len;
-    int ql = a.q_len;
-    if (a.q_lens != nullptr) {
-        const int v = a.q_lens[at.b];
-        ql = v < 0 ? 0 : v < ql ? v : ql;
-    }
-    n = __builtin_amdgcn_readfirstlane(n);
-    ql = __builtin_amdgcn_readfirstlane(ql);
-    at.n = n;
-    at.base = n - ql;
-    at.row0 = rt * kRows;
-    const int64_t left = int64_t(ql) * a.group - at.row0;
-    if (left <= 0) return;  // rows past the request's last token: none of this tile's workgroups counts
-    at.rows = left < kRows ? int(left) : kRows;
-
-    // keys that some row takes: [0, end); that every row takes: [0, first)
-    const bool tree = a.tree != nullptr;
-    const int64_t last = tree ? n : int64_t(at.base) + (at.row0 + at.rows - 1) / a.group + 1;
-    const int end = last < 0 ? 0 : last < n ? int(last) : n;
-    const int64_t first64 = tree ? at.base : int64_t(at.base) + at.row0 / a.group + 1;
-    const int first = first64 < 0 ? 0 : first64 < n ? int(first64) : n;
-    const int tiles = (end + kCacheTile - 1) / kCacheTile;
-    // the ranges share the keys there are, not the keys there could be
-    const int t0 = int(int64_t(tiles) * split / a.splits), t1 = int(int64_t(tiles) * (split + 1) / a.splits);
+    CacheRange r;
+    if (!cache_range(r, a, kRows)) return;
+    const CacheWork& at = r.at;
+    const int group_of = r.group_of, split = r.split;
 
     CacheRowsState<D, BITS, NB> w;
     load_queries(w, a, at);
-    int token[NB];
-    uint64_t own[NB];
-#pragma unroll
-    for (int nb = 0; nb < NB; ++nb) {
-        const int row = 16 * nb + l16 < at.rows ? at.row0 + 16 * nb + l16 : at.row0;
-        token[nb] = row / a.group;
-        own[nb] = 0;
-        if (tree) own[nb] = a.tree[int64_t(at.b) * a.q_len + token[nb]];
-    }
-
-    for (int t = t0 + wave; t < t1; t += kWaves) {
-        const int key0 = kCacheTile * t;
-        CacheTile<D, BITS> x;
-        const int64_t place[2] = {block_place(a, at, key0, end), block_place(a, at, key0 + 16, end)};
-        load_block(x, a, 0, place[0]);
-        load_block(x, a, 1, place[1]);
-        uint32_t live = first_bits(int64_t(n) - key0 - 1);
-        live &= (place[0] < 0 ? 0u : 0xFFFFu) | (place[1] < 0 ? 0u : 0xFFFF0000u);
-        uint32_t allowed[NB];
-        if (live != ~0u || key0 + kCacheTile > first) {
-#pragma unroll
-            for (int nb = 0; nb < NB; ++nb) allowed[nb] = live & taken(tree, own[nb], token[nb], at.base, key0);
-            cache_step<true>(w, x, a, place, live, allowed);
-        } else {
-            cache_step<false>(w, x, a, place, live, allowed);
+    const RowTokens<NB> rows = row_tokens<NB>(r, a, at);
+    int t = r.t0 + wave;
+    if (t < r.t1) {
+        TileWords<D, BITS> k, v;
+        KeyScales<D, BITS> ks, vs;
+        TileScores<NB> x;
+        TileWeights<D, BITS, NB> p;
+        uint32_t allowed[NB] = {};
+        // (past the wave's last tile: a tile of the next range, or empty resources at the end; it is not used)
+        auto places = [&](int tile) __attribute__((always_inline)) { return tile_places(a, at, tile, r.end); };
+        Places here = places(t), next = places(t + kWaves);
+        load_words<D, BITS, false>(k, a, here);
+        load_scales<D, BITS, false>(ks, a, here);
+        load_words<D, BITS, true>(v, a, here);
+        load_scales<D, BITS, true>(vs, a, here);
+        // the next tile's keys are on their way from the end of this one's scores on, its values from the end of this one's values
+        while (t < r.t1 && whole_tile(r, here, t)) {
+            tile_scores(w, k, ks, x);
+            if (t + kWaves < r.t1) {
+                load_words<D, BITS, false>(k, a, next);
+                load_scales<D, BITS, false>(ks, a, next);
+            }
+            tile_weights<false>(w, x, vs, allowed, p);
+            tile_values<false>(w, v, p, a, here, ~0u, allowed);
+            t += kWaves;
+            if (t < r.t1) {
+                load_words<D, BITS, true>(v, a, next);
+                load_scales<D, BITS, true>(vs, a, next);
+            }
+            here = next;
+            next = places(t + kWaves);
+        }
+        while (t < r.t1) {
+            const uint32_t live = tile_keys(allowed, r, rows, here, t);
+            tile_scores(w, k, ks, x);
+            clear_scales(vs, live);
+            tile_weights<true>(w, x, vs, allowed, p);
+            tile_values<true>(w, v, p, a, here, live, allowed);
+            t += kWaves;
+            if (t >= r.t1) break;
+            here = places(t);
+            load_words<D, BITS, false>(k, a, here);
+            load_scales<D, BITS, false>(ks, a, here);
+            load_words<D, BITS, true>(v, a, here);
+            load_scales<D, BITS, true>(vs, a, here);
         }
     }
 
     // ---- the waves' results, as numbers: row by row in LDS ----
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
+        each_o(w, nb, [&](int j, int i, float v) __attribute__((always_inline)) {
+            lds_o[wave][(16 * nb + l16) * D + o_column<D, BITS>(j, 4 * q + i)] = v;
+        });
         const float l = row_sum(w.l[nb]);
-        float low[2] = {0.f, 0.f};
-        if constexpr (BITS == 4) {
-            low[0] = row_sum(w.low[nb][0]);
-            low[1] = row_sum(w.low[nb][1]);
-        }
-        const float f = BITS == 16 ? 1.f : kCodeUnit / w.r[nb], minus = BITS == 8 ? 128.f / w.r[nb] : 0.f;
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float v = w.o[j][nb][i] * (BITS == 4 && j % 2 ? f * 0.0625f : f);
-                if constexpr (BITS == 8) v -= minus * w.sum[nb][i];
-                if constexpr (BITS == 4) v += low[j / 4];
-                lds_o[wave][(16 * nb + l16) * D + o_column<D, BITS>(j, 4 * q + i)] = v;
-            }
         if (q == 0) {
             lds_m[wave][16 * nb + l16] = w.m[nb];
             lds_l[wave][16 * nb + l16] = l;
@@ -648,11 +832,8 @@ __global__ __launch_bounds__(256, NB == 4 ? 1 : 2) void cache_attention_kernel(C
     __syncthreads();
     // O of a row of the tile, columns col .. col + 3, divided by the sum l (0: a row without keys)
     auto store4 = [&](int in_tile, int col, f32x4_t v, float l) {
-        const int row = at.row0 + in_tile;
-        const int tok = row / a.group, g = row - tok * a.group;
-        uint16_t* dst = a.o + int64_t(at.b) * a.o_batch + int64_t(tok) * a.o_token + int64_t(at.hk * a.group + g) * a.o_head + col;
-        const float r = l == 0.f ? 0.f : 1.f / l;
-        *reinterpret_cast<u32x2_t*>(dst) = u32x2_t{pack_bf16(v[0] * r, v[1] * r), pack_bf16(v[2] * r, v[3] * r)};
+        const float f = l == 0.f ? 0.f : 1.f / l;
+        *reinterpret_cast<u32x2_t*>(o_row(a, at, in_tile) + col) = u32x2_t{pack_bf16(v[0] * f, v[1] * f), pack_bf16(v[2] * f, v[3] * f)};
     };
     constexpr int kSc1 = 16;  // through to the device-coherent level: other workgroups' caches are elsewhere
     constexpr uint32_t kPart = uint32_t(D + 2) * 4u;  // bytes of a row's partial result: O, then maximum and sum
@@ -737,15 +918,165 @@ __global__ __launch_bounds__(256, NB == 4 ? 1 : 2) void cache_attention_kernel(C
     }
 }
 
+// Many rows (trees, chunks): the waves share the tiles, through LDS, and each takes its own 16 NB rows.  The copy of the
+// next tile is on its way while one is computed.
+template <int D, int BITS, int NB>
+__global__ __launch_bounds__(256, 2) void cache_attention_rows_kernel(CacheAttnArgs a) {
+    constexpr int kRows = 64 * NB;
+    constexpr int kBytes = TileShape<D, BITS>::kCopies * 256 * TileShape<D, BITS>::kUnit;
+    // an array per buffer: the compiler then sees that a tile's reads do not depend on the copies landing in the other
+    __shared__ __attribute__((aligned(1024))) unsigned char buf0[kBytes], buf1[kBytes];
+    const int lane = int(threadIdx.x) & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
+    const int q = lane >> 4, l16 = lane & 15;
+    CacheRange r;
+    if (!cache_range(r, a, kRows)) return;
+    CacheWork at = r.at;  // of the wave's rows
+    at.row0 += 16 * NB * wave;
+    at.rows = at.rows - 16 * NB * wave;
+    at.rows = at.rows < 0 ? 0 : at.rows < 16 * NB ? at.rows : 16 * NB;
+    CacheRowsState<D, BITS, NB> w;
+    load_queries(w, a, at);
+    const RowTokens<NB> rows = row_tokens<NB>(r, a, at);
+    TileWords<D, BITS> words;
+    KeyScales<D, BITS> ks, vs;
+    TileScores<NB> x;
+    TileWeights<D, BITS, NB> p;
+    uint32_t allowed[NB] = {};
+    int t = r.t0;
+    if (t < r.t1) {
+        auto places = [&](int tile) __attribute__((always_inline)) { return tile_places(a, at, tile, r.end); };
+        Places here = places(t), next = places(t + 1);
+        // A whole tile in `cur`, with the copy of the next one to `other` under way meanwhile.
+        auto step = [&](unsigned char* cur, unsigned char* other) __attribute__((always_inline)) {
+            wait_vmcnt<0>();
+            __syncthreads();  // the tile is there, and no wave reads `other` any more
+            if (t + 1 < r.t1) copy_tile<D, BITS>(other, a, next, wave);
+            read_words<D, BITS, false>(words, cur);
+            tile_scores(w, words, ks, x);
+            if (t + 1 < r.t1) load_scales<D, BITS, false>(ks, a, next);
+            tile_weights<false>(w, x, vs, allowed, p);
+            if (t + 1 < r.t1) load_scales<D, BITS, true>(vs, a, next);
+            read_words<D, BITS, true>(words, cur);
+            tile_values<false>(w, words, p, a, here, ~0u, allowed);
+            ++t;
+            here = next;
+            next = places(t + 1);
+        };
+        copy_tile<D, BITS>(buf0, a, here, wave);
+        load_scales<D, BITS, false>(ks, a, here);
+        load_scales<D, BITS, true>(vs, a, here);
+        bool second = false;  // which buffer holds tile t
+        while (t < r.t1 && whole_tile(r, here, t)) {
+            step(buf0, buf1);
+            second = true;
+            if (!(t < r.t1 && whole_tile(r, here, t))) break;
+            step(buf1, buf0);
+            second = false;
+        }
+        while (t < r.t1) {
+            wait_vmcnt<0>();
+            __syncthreads();
+            const unsigned char* const cur = second ? buf1 : buf0;
+            const uint32_t live = tile_keys(allowed, r, rows, here, t);
+            read_words<D, BITS, false>(words, cur);
+            tile_scores(w, words, ks, x);
+            clear_scales(vs, live);
+            tile_weights<true>(w, x, vs, allowed, p);
+            read_words<D, BITS, true>(words, cur);
+            tile_values<true>(w, words, p, a, here, live, allowed);
+            if (++t >= r.t1) break;
+            here = places(t);
+            second = false;
+            __syncthreads();  // every wave is done with the buffers
+            copy_tile<D, BITS>(buf0, a, here, wave);
+            load_scales<D, BITS, false>(ks, a, here);
+            load_scales<D, BITS, true>(vs, a, here);
+        }
+    }
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
+        const float l = row_sum(w.l[nb]);
+        const int in_tile = 16 * nb + l16;
+        const bool in = in_tile < at.rows;
+        if (a.splits == 1) {
+            const float f = l == 0.f ? 0.f : 1.f / l;
+            uint16_t* const dst = o_row(a, at, in ? in_tile : 0);
+            each_o(w, nb, [&](int j, int i, float v) __attribute__((always_inline)) {
+                if (in) dst[o_column<D, BITS>(j, 4 * q + i)] = float_to_bf16_bits(v * f);
+            });
+        } else {
+            float* const dst = a.part + (int64_t(r.group_of * a.splits + r.split) * kRows + 16 * NB * wave + in_tile) * (D + 2);
+            each_o(w, nb, [&](int j, int i, float v) __attribute__((always_inline)) {
+                if (in) dst[o_column<D, BITS>(j, 4 * q + i)] = v;
+            });
+            if (in && q == 0) {
+                dst[D] = w.m[nb];
+                dst[D + 1] = l;
+            }
+        }
+    }
+}
+
+// Joins the ranges' results of a row, in order: a wave per row of the padded tiles.
+template <int D>
+__global__ __launch_bounds__(256) void cache_join_kernel(CacheAttnArgs a, int rows_of_tile) {
+    const int lane = int(threadIdx.x) & 63;
+    const int64_t id = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    const int64_t groups = int64_t(a.batch) * a.cache.heads * a.row_tiles;
+    if (id >= groups * rows_of_tile) return;
+    const int64_t group_of = id / rows_of_tile;
+    const int in_tile = int(id - group_of * rows_of_tile);
+    CacheWork at;
+    at.row0 = int(group_of % a.row_tiles) * rows_of_tile;
+    const int64_t bh = group_of / a.row_tiles;
+    at.hk = int(bh % a.cache.heads);
+    at.b = int(bh / a.cache.heads);
+    int ql = a.q_len;
+    if (a.q_lens != nullptr) ql = min(max(a.q_lens[at.b], 0), ql);
+    if (int64_t(at.row0) + in_tile >= int64_t(ql) * a.group) return;
+    const float* const part = a.part + (group_of * a.splits * rows_of_tile + in_tile) * (D + 2);
+    const int64_t step = int64_t(rows_of_tile) * (D + 2);
+    const float m = lane < a.splits ? part[lane * step + D] : kNegInf, ls = lane < a.splits ? part[lane * step + D + 1] : 0.f;
+    float top = m;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
+    const float f = m == kNegInf ? 0.f : __builtin_amdgcn_exp2f(m - top);
+    float l = m == kNegInf ? ls : f * ls;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) l += __shfl_xor(l, d);
+    float o[D / 64];
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) o[e] = 0.f;
+    for (int s = 0; s < a.splits; ++s) {
+        const float fs = __shfl(f, s);
+#pragma unroll
+        for (int e = 0; e < D / 64; ++e) o[e] = __builtin_fmaf(fs, part[s * step + (D / 64) * lane + e], o[e]);
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    uint16_t* const dst = o_row(a, at, in_tile) + (D / 64) * lane;
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) dst[e] = float_to_bf16_bits(o[e] * inv);
+}
+
 template <int D, int BITS>
-hipError_t launch_cache_attention_as(const CacheAttnArgs& a, int row_blocks, hipStream_t stream) {
+hipError_t launch_cache_attention_as(const CacheAttnArgs& a, const CacheAttnPlan& plan, hipStream_t stream) {
     const unsigned grid = unsigned(a.row_tiles) * unsigned(a.splits) * unsigned(a.cache.heads) * unsigned(a.batch);
-    if (row_blocks == 1)
-        hipLaunchKernelGGL((cache_attention_kernel<D, BITS, 1>), dim3(grid), dim3(256), 0, stream, a);
-    else if (row_blocks == 2)
-        hipLaunchKernelGGL((cache_attention_kernel<D, BITS, 2>), dim3(grid), dim3(256), 0, stream, a);
+    if (!plan.share_tiles) {
+        if (plan.tile_rows == 16)
+            hipLaunchKernelGGL((cache_attention_kernel<D, BITS, 1>), dim3(grid), dim3(256), 0, stream, a);
+        else
+            hipLaunchKernelGGL((cache_attention_kernel<D, BITS, 2>), dim3(grid), dim3(256), 0, stream, a);
+        return hipGetLastError();
+    }
+    if (plan.tile_rows == 64)
+        hipLaunchKernelGGL((cache_attention_rows_kernel<D, BITS, 1>), dim3(grid), dim3(256), 0, stream, a);
     else
-        hipLaunchKernelGGL((cache_attention_kernel<D, BITS, 4>), dim3(grid), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((cache_attention_rows_kernel<D, BITS, 2>), dim3(grid), dim3(256), 0, stream, a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || a.splits == 1) return e;
+    const int64_t rows = int64_t(a.batch) * a.cache.heads * a.row_tiles * plan.tile_rows;
+    hipLaunchKernelGGL((cache_join_kernel<D>), dim3(unsigned((rows + 3) / 4)), dim3(256), 0, stream, a, plan.tile_rows);
     return hipGetLastError();
 }
 

@@ -5,9 +5,9 @@
 
 namespace lowbit {
 
-hipError_t launch_cache_attention_4(const CacheAttnArgs& a, int row_blocks, hipStream_t stream);
-hipError_t launch_cache_attention_8(const CacheAttnArgs& a, int row_blocks, hipStream_t stream);
-hipError_t launch_cache_attention_16(const CacheAttnArgs& a, int row_blocks, hipStream_t stream);
+hipError_t launch_cache_attention_4(const CacheAttnArgs& a, const CacheAttnPlan& plan, hipStream_t stream);
+hipError_t launch_cache_attention_8(const CacheAttnArgs& a, const CacheAttnPlan& plan, hipStream_t stream);
+hipError_t launch_cache_attention_16(const CacheAttnArgs& a, const CacheAttnPlan& plan, hipStream_t stream);
 
 namespace {
 constexpr int kTileKeys = 32, kMostSplits = 64;
@@ -17,14 +17,15 @@ constexpr int kTileKeys = 32, kMostSplits = 64;
 CacheAttnPlan plan_cache_attention(const CacheAttnArgs& a, bool may_split) {
     CacheAttnPlan p{};
     const int64_t rows = int64_t(a.q_len) * a.group;
-    p.row_blocks = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-    p.row_tiles = int(tiles_of(rows, 16 * p.row_blocks));
+    p.share_tiles = rows > 32;
+    p.tile_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
+    p.row_tiles = int(tiles_of(rows, p.tile_rows));
     const int64_t groups = int64_t(a.batch) * a.cache.heads * p.row_tiles, tiles = tiles_of(a.kv_len, kTileKeys);
     int64_t splits = groups == 0 || !may_split ? 1 : kComputeUnits / groups;
     splits = splits < tiles / 12 ? splits : tiles / 12;
     splits = splits < kMostSplits ? splits : kMostSplits;
     p.splits = splits < 1 ? 1 : int(splits);
-    p.bytes = p.splits > 1 ? kWorkspaceCounterBytes + size_t(groups) * p.splits * (16 * p.row_blocks) * (size_t(a.cache.head_dim) + 2) * 4u : 0;
+    p.bytes = p.splits > 1 ? kWorkspaceCounterBytes + size_t(groups) * p.splits * p.tile_rows * (size_t(a.cache.head_dim) + 2) * 4u : 0;
     return p;
 }
 
@@ -33,13 +34,13 @@ hipError_t launch_cache_attention(CacheAttnArgs a, const CacheAttnPlan& plan, vo
     a.splits = plan.splits;
     a.counters = static_cast<uint32_t*>(workspace);
     a.part = reinterpret_cast<float*>(static_cast<unsigned char*>(workspace) + kWorkspaceCounterBytes);
-    const hipError_t e = a.cache.bits == 4   ? launch_cache_attention_4(a, plan.row_blocks, stream)
-                         : a.cache.bits == 8 ? launch_cache_attention_8(a, plan.row_blocks, stream)
-                                             : launch_cache_attention_16(a, plan.row_blocks, stream);
+    const hipError_t e = a.cache.bits == 4   ? launch_cache_attention_4(a, plan, stream)
+                         : a.cache.bits == 8 ? launch_cache_attention_8(a, plan, stream)
+                                             : launch_cache_attention_16(a, plan, stream);
     if (e == hipSuccess && trace_enabled())
-        std::fprintf(stderr, "lowbit: cache_attention rows=%d splits=%d grid=%lld block=256 problem=%dx%dx%dx%d kv_heads=%d dim=%d bits=%d page=%d%s\n",
-                     16 * plan.row_blocks, a.splits, (long long)(int64_t(a.row_tiles) * a.splits * a.cache.heads * a.batch), a.batch, a.q_len,
-                     a.kv_len, a.cache.heads * a.group, a.cache.heads, a.cache.head_dim, a.cache.bits, 1 << a.cache.page_shift,
+        std::fprintf(stderr, "lowbit: cache_attention %s rows=%d splits=%d grid=%lld block=256 problem=%dx%dx%dx%d kv_heads=%d dim=%d bits=%d page=%d%s\n",
+                     plan.share_tiles ? "many" : "few", plan.tile_rows, a.splits,
+                     (long long)(int64_t(a.row_tiles) * a.splits * a.cache.heads * a.batch), a.batch, a.q_len, a.kv_len, a.cache.heads * a.group, a.cache.heads, a.cache.head_dim, a.cache.bits, 1 << a.cache.page_shift,
                      a.tree != nullptr ? " tree" : "");
     return e;
 }

@@ -3,9 +3,9 @@
 
 namespace lowbit {
 
-hipError_t launch_cache_attention_8(const CacheAttnArgs& a, int row_blocks, hipStream_t stream) {
-    return a.cache.head_dim == 64 ? launch_cache_attention_as<64, 8>(a, row_blocks, stream)
-                                  : launch_cache_attention_as<128, 8>(a, row_blocks, stream);
+hipError_t launch_cache_attention_8(const CacheAttnArgs& a, const CacheAttnPlan& plan, hipStream_t stream) {
+    return a.cache.head_dim == 64 ? launch_cache_attention_as<64, 8>(a, plan, stream)
+                                  : launch_cache_attention_as<128, 8>(a, plan, stream);
 }
 
 }  // namespace lowbit

@@ -256,7 +256,8 @@ struct CacheAttnArgs {
     float* part;
 };
 struct CacheAttnPlan {
-    int row_blocks;  // of 16 rows, of a workgroup: 1, 2 or 4
+    bool share_tiles;  // many rows: the waves share the tiles and split the rows; few: the other way round
+    int tile_rows;     // of a workgroup: 16 or 32 (few), 64 or 128 (many)
     int row_tiles, splits;
     size_t bytes;  // of workspace (0: none)
 };
