@@ -23,7 +23,7 @@
 // Rounding: p s to fp16 (2^-11 of each; 16 bits: p to bf16, 2^-8 of each) and O to bf16; all else is fp32.
 #pragma once
 
-#include <cstdio>
+#include <type_traits>
 
 #include "kv_cache.h"
 #include "lowbit_device.h"
@@ -32,6 +32,7 @@
 namespace lowbit {
 namespace {
 
+typedef float f32x2_t __attribute__((__vector_size__(2 * sizeof(float))));
 typedef _Float16 f16x8_t __attribute__((__vector_size__(8 * sizeof(_Float16))));
 
 constexpr float kNegInf = -__builtin_inff();
@@ -753,9 +754,9 @@ __device__ __forceinline__ uint16_t* o_row(const CacheAttnArgs& a, const CacheWo
 }
 
 // Few rows (decoded tokens): the waves take tiles in turn.
-template <int D, int BITS, int NB>
-__global__ __launch_bounds__(256, 2) void cache_attention_kernel(CacheAttnArgs a) {
-    constexpr int kWaves = 4, kRows = 16 * NB;
+template <int D, int BITS, int NB, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void cache_attention_kernel(CacheAttnArgs a) {
+    constexpr int kWaves = WAVES, kRows = 16 * NB;
     __shared__ __attribute__((aligned(16))) float lds_o[kWaves][kRows * D];
     __shared__ float lds_m[kWaves][kRows], lds_l[kWaves][kRows];
     __shared__ int last_split;
@@ -947,18 +948,22 @@ __global__ __launch_bounds__(256, 2) void cache_attention_rows_kernel(CacheAttnA
     if (t < r.t1) {
         auto places = [&](int tile) __attribute__((always_inline)) { return tile_places(a, at, tile, r.end); };
         Places here = places(t), next = places(t + 1);
-        // A whole tile in `cur`, with the copy of the next one to `other` under way meanwhile.
-        auto step = [&](unsigned char* cur, unsigned char* other) __attribute__((always_inline)) {
+        // The tile in `cur`, with the copy of the next one to `other` under way meanwhile.
+        auto step = [&](auto partial, unsigned char* cur, unsigned char* other) __attribute__((always_inline)) {
+            constexpr bool kPartial = decltype(partial)::value;
             wait_vmcnt<0>();
             __syncthreads();  // the tile is there, and no wave reads `other` any more
             if (t + 1 < r.t1) copy_tile<D, BITS>(other, a, next, wave);
+            uint32_t live = ~0u;
+            if constexpr (kPartial) live = tile_keys(allowed, r, rows, here, t);
             read_words<D, BITS, false>(words, cur);
             tile_scores(w, words, ks, x);
             if (t + 1 < r.t1) load_scales<D, BITS, false>(ks, a, next);
-            tile_weights<false>(w, x, vs, allowed, p);
+            if constexpr (kPartial) clear_scales(vs, live);
+            tile_weights<kPartial>(w, x, vs, allowed, p);
             if (t + 1 < r.t1) load_scales<D, BITS, true>(vs, a, next);
             read_words<D, BITS, true>(words, cur);
-            tile_values<false>(w, words, p, a, here, ~0u, allowed);
+            tile_values<kPartial>(w, words, p, a, here, live, allowed);
             ++t;
             here = next;
             next = places(t + 1);
@@ -968,30 +973,17 @@ __global__ __launch_bounds__(256, 2) void cache_attention_rows_kernel(CacheAttnA
         load_scales<D, BITS, true>(vs, a, here);
         bool second = false;  // which buffer holds tile t
         while (t < r.t1 && whole_tile(r, here, t)) {
-            step(buf0, buf1);
+            step(std::false_type{}, buf0, buf1);
             second = true;
             if (!(t < r.t1 && whole_tile(r, here, t))) break;
-            step(buf1, buf0);
+            step(std::false_type{}, buf1, buf0);
             second = false;
         }
-        while (t < r.t1) {
-            wait_vmcnt<0>();
-            __syncthreads();
-            const unsigned char* const cur = second ? buf1 : buf0;
-            const uint32_t live = tile_keys(allowed, r, rows, here, t);
-            read_words<D, BITS, false>(words, cur);
-            tile_scores(w, words, ks, x);
-            clear_scales(vs, live);
-            tile_weights<true>(w, x, vs, allowed, p);
-            read_words<D, BITS, true>(words, cur);
-            tile_values<true>(w, words, p, a, here, live, allowed);
-            if (++t >= r.t1) break;
-            here = places(t);
-            second = false;
-            __syncthreads();  // every wave is done with the buffers
-            copy_tile<D, BITS>(buf0, a, here, wave);
-            load_scales<D, BITS, false>(ks, a, here);
-            load_scales<D, BITS, true>(vs, a, here);
+        for (; t < r.t1; second = !second) {
+            if (second)
+                step(std::true_type{}, buf1, buf0);
+            else
+                step(std::true_type{}, buf0, buf1);
         }
     }
 #pragma unroll
@@ -1018,7 +1010,7 @@ __global__ __launch_bounds__(256, 2) void cache_attention_rows_kernel(CacheAttnA
     }
 }
 
-// Joins the ranges' results of a row, in order: a wave per row of the padded tiles.
+// Joins the ranges' results of a row, in a fixed order: a wave per row of the padded tiles.
 template <int D>
 __global__ __launch_bounds__(256) void cache_join_kernel(CacheAttnArgs a, int rows_of_tile) {
     const int lane = int(threadIdx.x) & 63;
@@ -1037,6 +1029,20 @@ __global__ __launch_bounds__(256) void cache_join_kernel(CacheAttnArgs a, int ro
     if (int64_t(at.row0) + in_tile >= int64_t(ql) * a.group) return;
     const float* const part = a.part + (group_of * a.splits * rows_of_tile + in_tile) * (D + 2);
     const int64_t step = int64_t(rows_of_tile) * (D + 2);
+    // four columns a lane, the ranges shared out over kParts groups of lanes, kAhead loads of each in flight
+    constexpr int kLanes = D / 4, kParts = 64 / kLanes, kAhead = 8;
+    const int col = 4 * (lane % kLanes), first = lane / kLanes;
+    f32x2_t u[kAhead][2];
+    auto fetch = [&](int s0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            const int s = s0 + i * kParts;
+            const float* const from = part + (s < a.splits ? s : 0) * step + col;  // rows lie on 8 bytes
+            u[i][0] = *reinterpret_cast<const f32x2_t*>(from);
+            u[i][1] = *reinterpret_cast<const f32x2_t*>(from + 2);
+        }
+    };
+    fetch(first);
     const float m = lane < a.splits ? part[lane * step + D] : kNegInf, ls = lane < a.splits ? part[lane * step + D + 1] : 0.f;
     float top = m;
 #pragma unroll
@@ -1045,28 +1051,39 @@ __global__ __launch_bounds__(256) void cache_join_kernel(CacheAttnArgs a, int ro
     float l = m == kNegInf ? ls : f * ls;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) l += __shfl_xor(l, d);
-    float o[D / 64];
+    f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+    for (int s0 = 0; s0 < a.splits; s0 += kAhead * kParts) {
+        if (s0 > 0) fetch(s0 + first);
 #pragma unroll
-    for (int e = 0; e < D / 64; ++e) o[e] = 0.f;
-    for (int s = 0; s < a.splits; ++s) {
-        const float fs = __shfl(f, s);
+        for (int i = 0; i < kAhead; ++i) {
+            const int s = s0 + first + i * kParts;
+            const float fs = __shfl(f, s & 63);
 #pragma unroll
-        for (int e = 0; e < D / 64; ++e) o[e] = __builtin_fmaf(fs, part[s * step + (D / 64) * lane + e], o[e]);
+            for (int e = 0; e < 4; ++e) o[e] = s < a.splits ? __builtin_fmaf(fs, u[i][e / 2][e % 2], o[e]) : o[e];
+        }
     }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-    uint16_t* const dst = o_row(a, at, in_tile) + (D / 64) * lane;
 #pragma unroll
-    for (int e = 0; e < D / 64; ++e) dst[e] = float_to_bf16_bits(o[e] * inv);
+    for (int d = kLanes; d < 64; d *= 2)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] += __shfl_xor(o[e], d);
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    if (first == 0)
+        *reinterpret_cast<u32x2_t*>(o_row(a, at, in_tile) + col) = u32x2_t{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
 }
 
 template <int D, int BITS>
 hipError_t launch_cache_attention_as(const CacheAttnArgs& a, const CacheAttnPlan& plan, hipStream_t stream) {
     const unsigned grid = unsigned(a.row_tiles) * unsigned(a.splits) * unsigned(a.cache.heads) * unsigned(a.batch);
     if (!plan.share_tiles) {
-        if (plan.tile_rows == 16)
-            hipLaunchKernelGGL((cache_attention_kernel<D, BITS, 1>), dim3(grid), dim3(256), 0, stream, a);
+        const dim3 block(64 * plan.waves);
+        if (plan.tile_rows == 16 && plan.waves == 4)
+            hipLaunchKernelGGL((cache_attention_kernel<D, BITS, 1, 4>), dim3(grid), block, 0, stream, a);
+        else if (plan.tile_rows == 16)
+            hipLaunchKernelGGL((cache_attention_kernel<D, BITS, 1, 8>), dim3(grid), block, 0, stream, a);
+        else if (plan.waves == 4)
+            hipLaunchKernelGGL((cache_attention_kernel<D, BITS, 2, 4>), dim3(grid), block, 0, stream, a);
         else
-            hipLaunchKernelGGL((cache_attention_kernel<D, BITS, 2>), dim3(grid), dim3(256), 0, stream, a);
+            hipLaunchKernelGGL((cache_attention_kernel<D, BITS, 2, 8>), dim3(grid), block, 0, stream, a);
         return hipGetLastError();
     }
     if (plan.tile_rows == 64)
