@@ -16,8 +16,9 @@
 //       sum p s c = sum p s u - 128 sum p s, with the same rounded p s (a product with ones).
 //     4 bits, x = s u + b per group: s (q.u) + b sum q for the scores, sum p s u + sum p b for the values (the latter in fp32).
 //   * Q is a power of two per row (2^14 over its largest exponent) times fp16: exact for bf16 elements down to 2^-28 of the largest.
-//   * p s is kept in fp16's range by a power of two per row, moved only when p s passes 2^12; p by the maximum, moved
-//     only when a score passes it by 2^8.
+//   * Everything that a row sums (p, p s, p b) carries one factor 2^-e, which the division at the end takes out.  e is the largest score plus
+//     the power of two of its value's scale when it was last set, so that the weights p s lie in fp16's range; it
+//     stays as long as they are below 2^12 (which the tile's largest score and largest scale tell), and the sums with it.
 // 16-bit caches take the same path with bf16 operands and no scales.
 //
 // Rounding: p s to fp16 (2^-11 of each; 16 bits: p to bf16, 2^-8 of each) and O to bf16; all else is fp32.
@@ -38,9 +39,8 @@ typedef _Float16 f16x8_t __attribute__((__vector_size__(8 * sizeof(_Float16))));
 constexpr float kNegInf = -__builtin_inff();
 constexpr int kCacheTile = 32;      // keys of a wave's tile
 constexpr int kMaxCacheSplits = 64;  // a lane per split in the join
-constexpr float kRise = 8.f;        // powers of two that a score may lie above the maximum in use
-constexpr float kMostWeight = 0x1p12f;  // of p s: past it the row's factor moves
-constexpr float kFirstFactor = 0x1p120f;  // of a row before its first keys: they set it
+constexpr float kMostWeight = 0x1p12f;    // of p s 2^-e: past it e moves
+constexpr float kMostProbability = 0x1p100f;  // of p 2^-e (values of scale 0 do not bound it)
 constexpr float kCodeUnit = 0x1p24f;    // 1 / the value of code 1 as an fp16
 
 // What a lane has of a tile: per block of 16 keys its words of K (a quarter of key l16's row) and of V (piece l16 of keys 4q ..).
@@ -73,9 +73,9 @@ struct CacheRowsState {
     u32x4_t q[D / 32][NB];  // B operands (bf16, or fp16 times the row's power of two)
     f32x4_t o[D / 16][NB];  // O^T: lane (q, l16): row l16, columns column(j, 4q + i)
     f32x4_t sum[NB];        // 8 bits: the sum of the rounded p s
-    float m[NB], l[NB];     // maximum in use (-inf: no key yet), the lane's own keys' sum of p
-    float r[NB];            // power of two on p s
-    float low[NB][2];       // 4 bits: the lane's own keys' sum of p b
+    float e[NB], l[NB];     // the row's exponent, the lane's own keys' sum of p 2^-e
+    uint32_t seen[NB];      // 1: the row has taken a key (e is 0 before)
+    float low[NB][2];       // 4 bits: the lane's own keys' sum of p b 2^-e
     float gain[NB];         // scores in powers of two per unit of (scale * sum)
     float start[NB];        // 8 bits: where sums of scores start from
     float qsum[NB][2];      // 4 bits: scale * log2(e) * the group's sum of q
@@ -220,9 +220,8 @@ __device__ __forceinline__ void load_queries(CacheRowsState<D, BITS, NB>& w, con
                 for (int g64 = 0; g64 < D / 64; ++g64) w.qsum[nb][g64] = row_sum(sum[g64]) * (a.scale_log2 * power_of_two(-up));
             }
         }
-        w.m[nb] = kNegInf;
-        w.l[nb] = w.low[nb][0] = w.low[nb][1] = 0.f;
-        w.r[nb] = kFirstFactor;
+        w.seen[nb] = 0;
+        w.e[nb] = w.l[nb] = w.low[nb][0] = w.low[nb][1] = 0.f;
         w.sum[nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int j = 0; j < D / 16; ++j) w.o[j][nb] = f32x4_t{0.f, 0.f, 0.f, 0.f};
@@ -406,7 +405,7 @@ __device__ __forceinline__ void add_odd_values(CacheRowsState<D, 16, NB>& w, con
     }
 }
 
-// Scores of a tile, in powers of two: [block][row block], keys 16 kb + 4q ..
+// Scores of a tile, in powers of two above the row's e: [block][row block], keys 16 kb + 4q ..
 template <int NB>
 struct TileScores {
     f32x4_t s[2][NB];
@@ -434,7 +433,8 @@ __device__ __forceinline__ void tile_scores(const CacheRowsState<D, BITS, NB>& w
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb) {
-                    float sum = raw[0][nb][i] * scale_at<D, BITS>(ks.w[kb], i, 0), low = w.qsum[nb][0] * low_at<D, BITS>(ks.w[kb], i, 0);
+                    float sum = raw[0][nb][i] * scale_at<D, BITS>(ks.w[kb], i, 0);
+                    float low = __builtin_fmaf(w.qsum[nb][0], low_at<D, BITS>(ks.w[kb], i, 0), -w.e[nb]);
                     if constexpr (kGroups == 2) {
                         sum = __builtin_fmaf(raw[1][nb][i], scale_at<D, BITS>(ks.w[kb], i, 1), sum);
                         low = __builtin_fmaf(w.qsum[nb][1], low_at<D, BITS>(ks.w[kb], i, 1), low);
@@ -454,7 +454,7 @@ __device__ __forceinline__ void tile_scores(const CacheRowsState<D, BITS, NB>& w
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
-                    x.s[kb][nb][i] *= BITS == 16 ? w.gain[nb] : w.gain[nb] * scale_at<D, 8>(ks.w[kb], i, 0);
+                    x.s[kb][nb][i] = __builtin_fmaf(x.s[kb][nb][i], BITS == 16 ? w.gain[nb] : w.gain[nb] * scale_at<D, 8>(ks.w[kb], i, 0), -w.e[nb]);
         }
     }
 }
@@ -464,45 +464,41 @@ __device__ __forceinline__ bool takes(uint32_t allowed, int kb, int i) {
     return (allowed >> (16 * kb + 4 * ((threadIdx.x & 63u) >> 4) + i)) & 1;
 }
 
-// Maximum and factor of row block nb to what the scores x and the values' scales need, and the sums with them.
+// Row block nb's e to what its scores x and the values' scales need, and x and the sums with it.
 template <int D, int BITS, int NB>
-__device__ __forceinline__ void rebase(CacheRowsState<D, BITS, NB>& w, int nb, const TileScores<NB>& x, const KeyScales<D, BITS>& vs, float top) {
+__device__ __forceinline__ void rebase(CacheRowsState<D, BITS, NB>& w, int nb, TileScores<NB>& x, const KeyScales<D, BITS>& vs, float top) {
     top = row_max(top);
-    const bool move = top > w.m[nb] + kRise;
-    const float f = move ? __builtin_amdgcn_exp2f(w.m[nb] - top) : 1.f;
-    w.m[nb] = move ? top : w.m[nb];
-    w.l[nb] *= f;
-    float fo = f;
+    float up = BITS == 16 ? top : kNegInf;  // of the new e above the old one
     if constexpr (BITS != 16) {
-        w.low[nb][0] *= f;
-        w.low[nb][1] *= f;
-        // where the maximum moved, the values that now count may be far smaller: p s sets the factor anew
-        float r = move ? fminf(w.r[nb] * 0x1p30f, kFirstFactor) : w.r[nb];
-        const float m = w.m[nb] == kNegInf ? 0.f : w.m[nb];
-        float most = 0.f;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float p = __builtin_amdgcn_exp2f(x.s[kb][nb][i] - m);
+                float most = 0.f;
 #pragma unroll
-                for (int g = 0; g < CacheFmt<D, BITS>::kGroups; ++g) most = fmaxf(most, p * scale_at<D, BITS>(vs.w[kb], i, g));
+                for (int g = 0; g < CacheFmt<D, BITS>::kGroups; ++g) most = fmaxf(most, scale_at<D, BITS>(vs.w[kb], i, g));
+                up = fmaxf(up, x.s[kb][nb][i] + __builtin_amdgcn_logf(most));
             }
-        most = row_max(most);
-        if (most * r > kMostWeight) {  // such that the largest of these lies in [1, 2)
-            int up = 127 - int(__float_as_uint(most) >> 23);
-            up = up < -126 ? -126 : up > 120 ? 120 : up;
-            r = power_of_two(up);
-        }
-        fo *= r / w.r[nb];
-        w.r[nb] = r;
+        up = fmaxf(row_max(up), top - 64.f);  // all scales 0, or nearly
     }
+    // a row without a key stays as it is, one with its first key takes any e, others a larger one
+    up = top > kNegInf && (up > 0.f || w.seen[nb] == 0) ? __builtin_ceilf(up) : 0.f;  // whole, so that e stays exact
+    const float f = w.seen[nb] != 0 ? __builtin_amdgcn_exp2f(-up) : 0.f;  // (sums of nothing are zeros)
+    w.seen[nb] = top > kNegInf ? 1u : w.seen[nb];
+    w.e[nb] += up;
+    w.l[nb] *= f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w.sum[nb][i] *= fo;
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) x.s[kb][nb][i] -= up;
+    w.low[nb][0] *= f;
+    w.low[nb][1] *= f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w.sum[nb][i] *= f;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) w.o[j][nb][i] *= fo;
+        for (int i = 0; i < 4; ++i) w.o[j][nb][i] *= f;
 }
 
 template <int D, int BITS, int NB>
@@ -536,9 +532,9 @@ __device__ __forceinline__ void tile_weights(CacheRowsState<D, BITS, NB>& w, Til
                 if constexpr (PARTIAL) x.s[kb][nb][i] = takes(allowed[nb], kb, i) ? x.s[kb][nb][i] : kNegInf;
                 top[nb] = fmaxf(top[nb], x.s[kb][nb][i]);
             }
-        again = again || top[nb] > w.m[nb] + kRise;
+        const float p = __builtin_amdgcn_exp2f(top[nb]);
         // (a bound: the largest score and the largest scale need not be one key's)
-        if constexpr (BITS != 16) again = again || __builtin_amdgcn_exp2f(top[nb] - w.m[nb]) * most * w.r[nb] > kMostWeight;
+        again = again || (w.seen[nb] == 0 && top[nb] > kNegInf) || p > kMostProbability || p * (BITS == 16 ? 1.f : most) > kMostWeight;
     }
     if (__any(again)) {
 #pragma unroll
@@ -546,13 +542,12 @@ __device__ __forceinline__ void tile_weights(CacheRowsState<D, BITS, NB>& w, Til
     }
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-        const float m = w.m[nb] == kNegInf ? 0.f : w.m[nb];  // without a key yet every score is -inf
         float y[2][4];
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                y[kb][i] = __builtin_amdgcn_exp2f(x.s[kb][nb][i] - m);
+                y[kb][i] = __builtin_amdgcn_exp2f(x.s[kb][nb][i]);
                 w.l[nb] += y[kb][i];
             }
 #pragma unroll
@@ -569,11 +564,15 @@ __device__ __forceinline__ void tile_weights(CacheRowsState<D, BITS, NB>& w, Til
                         for (int e = 0; e < 2; ++e) {
                             // a probability times a NaN scale: in the rows that take the key only
                             const bool in = !PARTIAL || takes(allowed[nb], kb, i + e);
-                            z[e] = y[kb][i + e] * (scale_at<D, BITS>(vs.w[kb], i + e, g) * w.r[nb]);
+                            z[e] = y[kb][i + e] * scale_at<D, BITS>(vs.w[kb], i + e, g);
                             z[e] = in ? z[e] : 0.f;
                             if constexpr (BITS == 4) {
-                                const float low = y[kb][i + e] * low_at<D, BITS>(vs.w[kb], i + e, g);
-                                w.low[nb][g] += in ? low : 0.f;
+                                if constexpr (PARTIAL) {
+                                    const float low = y[kb][i + e] * low_at<D, BITS>(vs.w[kb], i + e, g);
+                                    w.low[nb][g] += in ? low : 0.f;
+                                } else {
+                                    w.low[nb][g] = __builtin_fmaf(y[kb][i + e], low_at<D, BITS>(vs.w[kb], i + e, g), w.low[nb][g]);
+                                }
                             }
                         }
                         p.p[nb][g][2 * kb + i / 2] = pack_f16(z[0], z[1]);
@@ -735,13 +734,13 @@ __device__ __forceinline__ void each_o(const CacheRowsState<D, BITS, NB>& w, int
         low[0] = row_sum(w.low[nb][0]);
         low[1] = row_sum(w.low[nb][1]);
     }
-    const float unit = BITS == 16 ? 1.f : kCodeUnit / w.r[nb], minus = BITS == 8 ? 128.f / w.r[nb] : 0.f;
+    const float unit = BITS == 16 ? 1.f : kCodeUnit;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             float v = w.o[j][nb][i] * (BITS == 4 && j % 2 ? unit * 0.0625f : unit);
-            if constexpr (BITS == 8) v -= minus * w.sum[nb][i];
+            if constexpr (BITS == 8) v = __builtin_fmaf(-128.f, w.sum[nb][i], v);
             if constexpr (BITS == 4) v += low[j / 4];
             f(j, i, v);
         }
@@ -757,8 +756,9 @@ __device__ __forceinline__ uint16_t* o_row(const CacheAttnArgs& a, const CacheWo
 template <int D, int BITS, int NB, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 2) void cache_attention_kernel(CacheAttnArgs a) {
     constexpr int kWaves = WAVES, kRows = 16 * NB;
-    __shared__ __attribute__((aligned(16))) float lds_o[kWaves][kRows * D];
-    __shared__ float lds_m[kWaves][kRows], lds_l[kWaves][kRows];
+    constexpr int kPitch = D + 4;  // floats of a row: neighbouring rows 4 banks apart
+    __shared__ __attribute__((aligned(16))) float lds_o[kWaves][kRows * kPitch];
+    __shared__ float lds_m[kWaves][kRows], lds_l[kWaves][kRows];  // e (-inf: no key), and the sum
     __shared__ int last_split;
     const int lane = int(threadIdx.x) & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
@@ -822,11 +822,11 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_attention_kernel(CacheAtt
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
         each_o(w, nb, [&](int j, int i, float v) __attribute__((always_inline)) {
-            lds_o[wave][(16 * nb + l16) * D + o_column<D, BITS>(j, 4 * q + i)] = v;
+            lds_o[wave][(16 * nb + l16) * kPitch + o_column<D, BITS>(j, 4 * q + i)] = v;
         });
         const float l = row_sum(w.l[nb]);
         if (q == 0) {
-            lds_m[wave][16 * nb + l16] = w.m[nb];
+            lds_m[wave][16 * nb + l16] = l != 0.f ? w.e[nb] : kNegInf;  // (a NaN goes along)
             lds_l[wave][16 * nb + l16] = l;
         }
     }
@@ -848,13 +848,10 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_attention_kernel(CacheAtt
         f32x4_t v = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < kWaves; ++i) {
-            if (lds_m[i][row] == kNegInf) {  // no key (a sum of 0) or a NaN score
-                total += lds_l[i][row];
-                continue;
-            }
+            if (lds_m[i][row] == kNegInf) continue;
             const float f = __builtin_amdgcn_exp2f(lds_m[i][row] - top);
             total += f * lds_l[i][row];
-            const f32x4_t u = *reinterpret_cast<const f32x4_t*>(&lds_o[i][row * D + col]);
+            const f32x4_t u = *reinterpret_cast<const f32x4_t*>(&lds_o[i][row * kPitch + col]);
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(f, u[e], v[e]);
         }
@@ -890,7 +887,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_attention_kernel(CacheAtt
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
         const float f = m == kNegInf ? 0.f : __builtin_amdgcn_exp2f(m - top);
-        float sum = m == kNegInf ? l : f * l;
+        float sum = m == kNegInf ? 0.f : f * l;
 #pragma unroll
         for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
         if (in) factors[row * kMaxCacheSplits + lane] = f;
@@ -927,6 +924,8 @@ __global__ __launch_bounds__(256, 2) void cache_attention_rows_kernel(CacheAttnA
     constexpr int kBytes = TileShape<D, BITS>::kCopies * 256 * TileShape<D, BITS>::kUnit;
     // an array per buffer: the compiler then sees that a tile's reads do not depend on the copies landing in the other
     __shared__ __attribute__((aligned(1024))) unsigned char buf0[kBytes], buf1[kBytes];
+    constexpr int kPitch = D + 4;  // floats of a row: neighbouring rows 4 banks apart
+    __shared__ __attribute__((aligned(16))) float out[4][16 * kPitch];
     const int lane = int(threadIdx.x) & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
     const int q = lane >> 4, l16 = lane & 15;
@@ -986,27 +985,35 @@ __global__ __launch_bounds__(256, 2) void cache_attention_rows_kernel(CacheAttnA
                 step(std::true_type{}, buf0, buf1);
         }
     }
+    // 16 rows at a time through the wave's part of LDS, so that neighbouring lanes store neighbouring columns
+    float* const slab = out[wave];
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
         const float l = row_sum(w.l[nb]);
-        const int in_tile = 16 * nb + l16;
-        const bool in = in_tile < at.rows;
-        if (a.splits == 1) {
-            const float f = l == 0.f ? 0.f : 1.f / l;
-            uint16_t* const dst = o_row(a, at, in ? in_tile : 0);
-            each_o(w, nb, [&](int j, int i, float v) __attribute__((always_inline)) {
-                if (in) dst[o_column<D, BITS>(j, 4 * q + i)] = float_to_bf16_bits(v * f);
-            });
-        } else {
-            float* const dst = a.part + (int64_t(r.group_of * a.splits + r.split) * kRows + 16 * NB * wave + in_tile) * (D + 2);
-            each_o(w, nb, [&](int j, int i, float v) __attribute__((always_inline)) {
-                if (in) dst[o_column<D, BITS>(j, 4 * q + i)] = v;
-            });
-            if (in && q == 0) {
-                dst[D] = w.m[nb];
-                dst[D + 1] = l;
+        const float f = a.splits > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
+        each_o(w, nb, [&](int j, int i, float v) __attribute__((always_inline)) { slab[l16 * kPitch + o_column<D, BITS>(j, 4 * q + i)] = v * f; });
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0); the wave's own writes, so no barrier
+        asm volatile("" ::: "memory");
+        const int64_t part_row = int64_t(r.group_of * a.splits + r.split) * kRows + 16 * NB * wave + 16 * nb;
+        for (int item = lane; item < 16 * (D / 4); item += 64) {
+            const int row = item / (D / 4), col = 4 * (item % (D / 4));
+            if (16 * nb + row >= at.rows) break;  // rows only grow
+            const f32x4_t v = *reinterpret_cast<const f32x4_t*>(slab + row * kPitch + col);
+            if (a.splits == 1) {
+                *reinterpret_cast<u32x2_t*>(o_row(a, at, 16 * nb + row) + col) = u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+            } else {
+                f32x2_t* const dst = reinterpret_cast<f32x2_t*>(a.part + (part_row + row) * (D + 2) + col);  // rows lie on 8 bytes
+                dst[0] = f32x2_t{v[0], v[1]};
+                dst[1] = f32x2_t{v[2], v[3]};
             }
         }
+        if (a.splits > 1 && q == 0 && 16 * nb + l16 < at.rows) {
+            float* const dst = a.part + (part_row + l16) * (D + 2) + D;
+            dst[0] = l != 0.f ? w.e[nb] : kNegInf;  // (a NaN goes along)
+            dst[1] = l;
+        }
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // the slab's reads are done
+        asm volatile("" ::: "memory");
     }
 }
 
@@ -1048,7 +1055,7 @@ __global__ __launch_bounds__(256) void cache_join_kernel(CacheAttnArgs a, int ro
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
     const float f = m == kNegInf ? 0.f : __builtin_amdgcn_exp2f(m - top);
-    float l = m == kNegInf ? ls : f * ls;
+    float l = m == kNegInf ? 0.f : f * ls;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) l += __shfl_xor(l, d);
     f32x4_t o = {0.f, 0.f, 0.f, 0.f};
