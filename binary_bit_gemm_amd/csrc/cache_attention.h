@@ -24,8 +24,6 @@
 // Rounding: p s to fp16 (2^-11 of each; 16 bits: p to bf16, 2^-8 of each) and O to bf16; all else is fp32.
 #pragma once
 
-#include <type_traits>
-
 #include "kv_cache.h"
 #include "lowbit_device.h"
 #include "lowbit_internal.h"
@@ -166,34 +164,47 @@ struct CacheWork {
     int n, base;            // keys, and those before the new tokens (negative: more new tokens than keys)
 };
 
+// The lane's pieces of its rows of q as they lie (rows past the last read as zeros).
 template <int D, int BITS, int NB>
-__device__ __forceinline__ void load_queries(CacheRowsState<D, BITS, NB>& w, const CacheAttnArgs& a, const CacheWork& at) {
+struct RawQueries {
+    u32x4_t w[D / 32][NB];
+};
+template <int D, int BITS, int NB>
+__device__ __forceinline__ void load_queries(RawQueries<D, BITS, NB>& raw, const CacheAttnArgs& a, const CacheWork& at) {
     const int lane = int(threadIdx.x) & 63, q = lane >> 4, l16 = lane & 15;
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-        const int row = at.row0 + 16 * nb + l16;
+        const uint32_t row = uint32_t(at.row0 + 16 * nb + l16), group = uint32_t(a.group);
         const bool in = 16 * nb + l16 < at.rows;
-        const int t = in ? row / a.group : 0, g = in ? row - t * a.group : 0;
-        const uint16_t* src = a.q + int64_t(at.b) * a.q_batch + int64_t(t) * a.q_token + int64_t(at.hk * a.group + g) * a.q_head;
-        u32x4_t raw[D / 32];
+        const uint32_t t = in ? row / group : 0u, g = in ? row - t * group : 0u;
+        const uint16_t* src = a.q + int64_t(at.b) * a.q_batch + int64_t(t) * a.q_token + int64_t(at.hk * a.group + int(g)) * a.q_head;
 #pragma unroll
         for (int ks = 0; ks < D / 32; ++ks) {
-            raw[ks] = u32x4_t{0, 0, 0, 0};
-            if (in) raw[ks] = *reinterpret_cast<const u32x4_t*>(src + q_element<BITS>(ks, q));
+            raw.w[ks][nb] = u32x4_t{0, 0, 0, 0};
+            if (in) raw.w[ks][nb] = *reinterpret_cast<const u32x4_t*>(src + q_element<BITS>(ks, q));
         }
+    }
+}
+
+// Operands from them, and what goes with a row.
+template <int D, int BITS, int NB>
+__device__ __forceinline__ void start_rows(CacheRowsState<D, BITS, NB>& w, const RawQueries<D, BITS, NB>& raw, const CacheAttnArgs& a) {
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) {
         w.gain[nb] = a.scale_log2;
         w.start[nb] = w.qsum[nb][0] = w.qsum[nb][1] = 0.f;
         if constexpr (BITS == 16) {
 #pragma unroll
-            for (int ks = 0; ks < D / 32; ++ks) w.q[ks][nb] = raw[ks];
+            for (int ks = 0; ks < D / 32; ++ks) w.q[ks][nb] = raw.w[ks][nb];
         } else {
-            float top = 0.f;
+            uint32_t most = 0;  // the largest magnitude's bits
 #pragma unroll
             for (int ks = 0; ks < D / 32; ++ks)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) top = fmaxf(top, fmaxf(__builtin_fabsf(bf16_low(raw[ks][e])), __builtin_fabsf(bf16_high(raw[ks][e]))));
-            top = row_max(top);
-            int up = 14 - (int((__float_as_uint(top) >> 23) & 255u) - 127);  // the largest element comes to lie in [2^14, 2^15)
+                for (int e = 0; e < 4; ++e) most = max(max(most, raw.w[ks][nb][e] & 0x7FFF0000u), (raw.w[ks][nb][e] << 16) & 0x7FFF0000u);
+            most = max(most, uint32_t(__shfl_xor(int(most), 16)));
+            most = max(most, uint32_t(__shfl_xor(int(most), 32)));
+            int up = 14 - (int(most >> 23) - 127);  // the largest element comes to lie in [2^14, 2^15)
             up = up > 126 ? 126 : up < -113 ? -113 : up;  // (infinite or NaN: they stay that)
             const float f = power_of_two(up);
             float sum[D / 64];
@@ -203,7 +214,7 @@ __device__ __forceinline__ void load_queries(CacheRowsState<D, BITS, NB>& w, con
             for (int ks = 0; ks < D / 32; ++ks) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float x = bf16_low(raw[ks][e]) * f, y = bf16_high(raw[ks][e]) * f;
+                    const float x = bf16_low(raw.w[ks][nb][e]) * f, y = bf16_high(raw.w[ks][nb][e]) * f;
                     sum[ks / 2] += x + y;
                     const float share = BITS == 4 && e % 2 ? 0.0625f : 1.f;
                     w.q[ks][nb][e] = pack_f16(x * share, y * share);
@@ -234,24 +245,25 @@ struct Places {
     int64_t at[2];
     bool ok[2];
 };
-// `end` > 0; t may be past the last tile.
+// `end` > 0: the keys that count; t may be past the last tile.
 __device__ __forceinline__ Places tile_places(const CacheAttnArgs& a, const CacheWork& at, int t, int end) {
     Places p;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-        const int64_t key = int64_t(kCacheTile) * t + 16 * kb;
-        const int in = key < end ? int(key) : end - 1;
-        const int page = __builtin_amdgcn_readfirstlane(a.table[int64_t(at.b) * a.table_stride + (in >> a.cache.page_shift)]);
-        p.ok[kb] = key < end && uint32_t(page) < uint32_t(a.cache.pages);
-        const int64_t row = ((int64_t(page) * a.cache.heads + at.hk) << a.cache.page_shift) + (in & ((1 << a.cache.page_shift) - 16));
+        const uint32_t key = uint32_t(kCacheTile) * uint32_t(t) + 16u * kb;  // below 2^32: t is at most 32 past 2^26
+        const bool in = key < uint32_t(end);
+        const uint32_t last = in ? key : uint32_t(end) - 1u;
+        const int page = __builtin_amdgcn_readfirstlane(a.table[int64_t(at.b) * a.table_stride + (last >> a.cache.page_shift)]);
+        p.ok[kb] = in && uint32_t(page) < uint32_t(a.cache.pages);
+        const int64_t row = ((int64_t(page) * a.cache.heads + at.hk) << a.cache.page_shift) + (last & ((1u << a.cache.page_shift) - 16u));
         p.at[kb] = p.ok[kb] ? row : 0;
     }
     return p;
 }
 
 // Rows of `size` bytes of a block; an empty resource (zeros without a read) where it is not there.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t block_rows(const unsigned char* base, const Places& p, int kb, int size) {
-    return make_rsrc(base + p.at[kb] * size, p.ok[kb] ? 16u * uint32_t(size) : 0u);
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t block_rows(const unsigned char* base, int64_t at, bool ok, int size) {
+    return make_rsrc(base + at * size, ok ? 16u * uint32_t(size) : 0u);
 }
 
 // The lane's byte in a block of K or V for copy or load i.
@@ -272,7 +284,7 @@ __device__ __forceinline__ void load_words(TileWords<D, BITS>& t, const CacheAtt
     constexpr int kW = TileShape<D, BITS>::kWords;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-        const auto rs = block_rows(IS_V ? a.cache.v : a.cache.k, p, kb, CacheFmt<D, BITS>::kRow);
+        const auto rs = block_rows(IS_V ? a.cache.v : a.cache.k, p.at[kb], p.ok[kb], CacheFmt<D, BITS>::kRow);
         if constexpr (kW >= 4) {
 #pragma unroll
             for (int i = 0; i < kW / 4; ++i) {
@@ -295,7 +307,7 @@ __device__ __forceinline__ void load_scales(KeyScales<D, BITS>& s, const CacheAt
         const uint32_t q = (threadIdx.x & 63u) >> 4;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
-            const auto rs = block_rows(IS_V ? a.cache.v_scales : a.cache.k_scales, p, kb, kS);
+            const auto rs = block_rows(IS_V ? a.cache.v_scales : a.cache.k_scales, p.at[kb], p.ok[kb], kS);
             if constexpr (kS == 2) {
                 const u32x2_t x = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(rs, 8u * q, 0, 0));
                 s.w[kb][0] = x[0];
@@ -312,6 +324,14 @@ __device__ __forceinline__ void load_scales(KeyScales<D, BITS>& s, const CacheAt
     }
 }
 
+// A tile in LDS: its words as lanes take them, then the scales of K's two blocks and of V's.
+template <int D, int BITS>
+struct LdsTile {
+    static constexpr int kWords = TileShape<D, BITS>::kCopies * 256 * TileShape<D, BITS>::kUnit;
+    static constexpr int kSegment = 16 * CacheFmt<D, BITS>::kScaleBytes;
+    static constexpr int kBytes = kWords + 4 * kSegment;
+};
+
 // The wave's quarter of a tile's copies to LDS, lane by lane.
 template <int D, int BITS>
 __device__ __forceinline__ void copy_tile(unsigned char* lds, const CacheAttnArgs& a, const Places& p, int wave) {
@@ -322,16 +342,26 @@ __device__ __forceinline__ void copy_tile(unsigned char* lds, const CacheAttnArg
         const int copy = wave * (S::kCopies / 4) + c;  // the same for the wave
         const bool is_v = copy >= 2 * kPer;
         const int kb = copy / kPer % 2, i = copy % kPer;
-        Places one = p;
-        one.at[0] = kb ? p.at[1] : p.at[0];
-        one.ok[0] = kb ? p.ok[1] : p.ok[0];
-        const auto rs = block_rows(is_v ? a.cache.v : a.cache.k, one, 0, CacheFmt<D, BITS>::kRow);
+        const auto rs = block_rows(is_v ? a.cache.v : a.cache.k, kb ? p.at[1] : p.at[0], kb ? p.ok[1] : p.ok[0], CacheFmt<D, BITS>::kRow);
         unsigned char* const to = lds + copy * (256 * S::kUnit);
         const uint32_t from = unit_offset<D, BITS>(is_v, i);
         if constexpr (S::kUnit == 4)
             dma16(rs, to, from, 0);
         else
             dma4(rs, to, from, 0);
+    }
+    if constexpr (BITS != 16) {
+        constexpr int kS = CacheFmt<D, BITS>::kScaleBytes, kSegment = LdsTile<D, BITS>::kSegment;
+        constexpr int kBytes = BITS == 8 ? 4 : 16;  // of a lane
+        const int lane = int(threadIdx.x) & 63, kb = wave & 1;
+        const auto rs = block_rows(wave & 2 ? a.cache.v_scales : a.cache.k_scales, kb ? p.at[1] : p.at[0], kb ? p.ok[1] : p.ok[0], kS);
+        unsigned char* const to = lds + LdsTile<D, BITS>::kWords + wave * kSegment;
+        if (lane < kSegment / kBytes) {
+            if constexpr (kBytes == 4)
+                dma4(rs, to, 4u * uint32_t(lane), 0);
+            else
+                dma16(rs, to, 16u * uint32_t(lane), 0);
+        }
     }
 }
 
@@ -345,7 +375,7 @@ __device__ __forceinline__ void read_words(TileWords<D, BITS>& t, const unsigned
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
-            const unsigned char* const from = at + ((IS_V ? 2 : 0) + kb) * kPer * (256 * S::kUnit) + i * (256 * S::kUnit);
+            const unsigned char* const from = at + (((IS_V ? 2 : 0) + kb) * kPer + i) * (256 * S::kUnit);
             if constexpr (S::kUnit == 4) {
                 const u32x4_t x = *reinterpret_cast<const u32x4_t*>(from);
 #pragma unroll
@@ -354,6 +384,29 @@ __device__ __forceinline__ void read_words(TileWords<D, BITS>& t, const unsigned
                 t.block[kb].w[i] = *reinterpret_cast<const uint32_t*>(from);
             }
         }
+}
+template <int D, int BITS, bool IS_V>
+__device__ __forceinline__ void read_scales(KeyScales<D, BITS>& s, const unsigned char* lds) {
+    constexpr int kS = CacheFmt<D, BITS>::kScaleBytes;
+    if constexpr (kS > 0) {
+        const unsigned char* const at = lds + LdsTile<D, BITS>::kWords + (IS_V ? 2 : 0) * LdsTile<D, BITS>::kSegment + ((threadIdx.x & 63u) >> 4) * (4 * kS);
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb) {
+            const unsigned char* const from = at + kb * LdsTile<D, BITS>::kSegment;
+            if constexpr (kS == 2) {
+                const u32x2_t x = *reinterpret_cast<const u32x2_t*>(from);
+                s.w[kb][0] = x[0];
+                s.w[kb][1] = x[1];
+            } else {
+#pragma unroll
+                for (int i = 0; i < kS / 4; ++i) {
+                    const u32x4_t x = *reinterpret_cast<const u32x4_t*>(from + 16 * i);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s.w[kb][4 * i + e] = x[e];
+                }
+            }
+        }
+    }
 }
 
 // The scale of the lane's key i of block kb, and (4 bits, group g) its smallest value.
@@ -369,22 +422,26 @@ __device__ __forceinline__ float low_at(const uint32_t* s, int i, int g) {
     return bf16_high(s[i * CacheFmt<D, BITS>::kGroups + g]);
 }
 
-__device__ __forceinline__ bool odd_bf16(uint32_t half) { return (half & 0x7F80u) == 0x7F80u; }
-
-// The pair without its infinities and NaN.
-__device__ __forceinline__ uint32_t finite_pair(uint32_t x) {
-    if (odd_bf16(x)) x &= 0xFFFF0000u;
-    if (odd_bf16(x >> 16)) x &= 0xFFFFu;
-    return x;
-}
-
-// 16-bit values that are an infinity or a NaN, in a tile with keys that some row leaves out (zero in a product does not silence them, so
-// they are zeros in the operands): added to the rows that take their keys.
+// 16-bit values of a tile with keys that some row leaves out or that are not there.  Zero in a product does not silence an infinity or a NaN, so
+// these become zeros, and what is there is added to the rows that take it.
 template <int D, int NB>
-__device__ __forceinline__ void add_odd_values(CacheRowsState<D, 16, NB>& w, const CacheAttnArgs& a, const Places& place,
-                                               const uint32_t (&allowed)[NB]) {
+__device__ __forceinline__ void clean_values(CacheRowsState<D, 16, NB>& w, TileWords<D, 16>& v, const CacheAttnArgs& a, const Places& place, uint32_t live,
+                                             const uint32_t (&allowed)[NB]) {
     using F = CacheFmt<D, 16>;
+    constexpr int kW = TileShape<D, 16>::kWords;
     const uint32_t q = (threadIdx.x & 63u) >> 4;
+    uint32_t odd = 0;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < kW; ++i) {
+            const uint32_t x = (live >> (16 * kb + 4 * q + i / (kW / 4))) & 1 ? v.block[kb].w[i] : 0u;
+            const uint32_t y = (x & 0x7F80u) == 0x7F80u ? x & 0xFFFF0000u : x;
+            const uint32_t z = (y & 0x7F800000u) == 0x7F800000u ? y & 0xFFFFu : y;
+            odd |= x ^ z;
+            v.block[kb].w[i] = z;
+        }
+    if (!__any(odd != 0)) return;
     for (int key = 0; key < kCacheTile; ++key) {
         const int64_t p = key < 16 ? place.at[0] : place.at[1];
         bool some = false;  // (a key that is not there is allowed to no row)
@@ -399,7 +456,7 @@ __device__ __forceinline__ void add_odd_values(CacheRowsState<D, 16, NB>& w, con
                 const uint32_t b = reinterpret_cast<const uint16_t*>(src)[j];
 #pragma unroll
                 for (int nb = 0; nb < NB; ++nb)
-                    if (odd_bf16(b) && ((allowed[nb] >> key) & 1)) w.o[j][nb][i] += bf16_low(b);
+                    if ((b & 0x7F80u) == 0x7F80u && ((allowed[nb] >> key) & 1)) w.o[j][nb][i] += bf16_low(b);
             }
         }
     }
@@ -506,10 +563,10 @@ struct TileWeights {
     u32x4_t p[NB][CacheFmt<D, BITS>::kGroups];  // operands: p s (16 bits: p), keys 4q .. of block 0, then of block 1
 };
 
-// The probabilities of a tile's scores, times the values' scales.  PARTIAL: a row leaves out its keys whose bit of `allowed` is clear.
-template <bool PARTIAL, int D, int BITS, int NB>
+// The probabilities of a tile's scores, times the values' scales.
+template <int D, int BITS, int NB>
 __device__ __forceinline__ void tile_weights(CacheRowsState<D, BITS, NB>& w, TileScores<NB>& x, const KeyScales<D, BITS>& vs,
-                                             const uint32_t (&allowed)[NB], TileWeights<D, BITS, NB>& p) {
+                                             TileWeights<D, BITS, NB>& p) {
     constexpr int kGroups = CacheFmt<D, BITS>::kGroups;
     float most = 0.f;  // of the values' scales
     if constexpr (BITS != 16) {
@@ -529,7 +586,6 @@ __device__ __forceinline__ void tile_weights(CacheRowsState<D, BITS, NB>& w, Til
         for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                if constexpr (PARTIAL) x.s[kb][nb][i] = takes(allowed[nb], kb, i) ? x.s[kb][nb][i] : kNegInf;
                 top[nb] = fmaxf(top[nb], x.s[kb][nb][i]);
             }
         const float p = __builtin_amdgcn_exp2f(top[nb]);
@@ -562,18 +618,9 @@ __device__ __forceinline__ void tile_weights(CacheRowsState<D, BITS, NB>& w, Til
                         float z[2];
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            // a probability times a NaN scale: in the rows that take the key only
-                            const bool in = !PARTIAL || takes(allowed[nb], kb, i + e);
                             z[e] = y[kb][i + e] * scale_at<D, BITS>(vs.w[kb], i + e, g);
-                            z[e] = in ? z[e] : 0.f;
-                            if constexpr (BITS == 4) {
-                                if constexpr (PARTIAL) {
-                                    const float low = y[kb][i + e] * low_at<D, BITS>(vs.w[kb], i + e, g);
-                                    w.low[nb][g] += in ? low : 0.f;
-                                } else {
-                                    w.low[nb][g] = __builtin_fmaf(y[kb][i + e], low_at<D, BITS>(vs.w[kb], i + e, g), w.low[nb][g]);
-                                }
-                            }
+                            if constexpr (BITS == 4)
+                                w.low[nb][g] = __builtin_fmaf(y[kb][i + e], low_at<D, BITS>(vs.w[kb], i + e, g), w.low[nb][g]);
                         }
                         p.p[nb][g][2 * kb + i / 2] = pack_f16(z[0], z[1]);
                     }
@@ -582,56 +629,21 @@ __device__ __forceinline__ void tile_weights(CacheRowsState<D, BITS, NB>& w, Til
 }
 
 // O += V^T P^T of a tile.
-template <bool PARTIAL, int D, int BITS, int NB>
-__device__ __forceinline__ void tile_values(CacheRowsState<D, BITS, NB>& w, const TileWords<D, BITS>& v, const TileWeights<D, BITS, NB>& p,
-                                            const CacheAttnArgs& a, const Places& place, uint32_t live, const uint32_t (&allowed)[NB]) {
-    uint32_t here[4];  // 16 bits: the pairs' keys that are there
-    if constexpr (PARTIAL && BITS == 16) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) here[e] = (takes(live, e / 2, 2 * (e % 2)) ? 0xFFFFu : 0u) | (takes(live, e / 2, 2 * (e % 2) + 1) ? 0xFFFF0000u : 0u);
-    }
+template <int D, int BITS, int NB>
+__device__ __forceinline__ void tile_values(CacheRowsState<D, BITS, NB>& w, const TileWords<D, BITS>& v, const TileWeights<D, BITS, NB>& p) {
     if constexpr (BITS == 8) {
         const u32x4_t ones = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) w.sum[nb] = cache_mfma<BITS>(ones, p.p[nb][0], w.sum[nb]);
     }
-    bool odd = false;
 #pragma unroll
     for (int j = 0; j < D / 16; ++j) {
         u32x4_t op;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            op[e] = v_pair<D, BITS>(v.block[e / 2], j, e % 2);
-            if constexpr (PARTIAL && BITS == 16) {
-                const uint32_t there = op[e] & here[e];
-                op[e] = finite_pair(there);
-                odd = odd || op[e] != there;
-            }
-        }
+        for (int e = 0; e < 4; ++e) op[e] = v_pair<D, BITS>(v.block[e / 2], j, e % 2);
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) w.o[j][nb] = cache_mfma<BITS>(op, p.p[nb][BITS == 4 ? j / 4 : 0], w.o[j][nb]);
     }
-    if constexpr (PARTIAL && BITS == 16) {
-        if (__any(odd)) add_odd_values<D, NB>(w, a, place, allowed);
-    }
-}
-
-// The scales of keys that are not there, which may be anything, to zeros.
-template <int D, int BITS>
-__device__ __forceinline__ void clear_scales(KeyScales<D, BITS>& s, uint32_t live) {
-    constexpr int kGroups = CacheFmt<D, BITS>::kGroups;
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const bool is = takes(live, kb, i);
-            if constexpr (BITS == 8) {
-                if (!is) s.w[kb][i / 2] &= i % 2 ? 0xFFFFu : 0xFFFF0000u;
-            } else if constexpr (BITS == 4) {
-#pragma unroll
-                for (int g = 0; g < kGroups; ++g) s.w[kb][i * kGroups + g] = is ? s.w[kb][i * kGroups + g] : 0u;
-            }
-        }
 }
 
 // Bits 0 .. rel (none for rel < 0) of 32.
@@ -651,20 +663,21 @@ __device__ __forceinline__ uint32_t taken(bool tree, uint64_t own, int token, in
 struct CacheRange {
     CacheWork at;
     int group_of;    // of the workgroups that share rows
-    int split, end;  // keys that some row takes: [0, end)
+    int split, end;  // keys that some row takes and this or an earlier range has: [0, end)
     int first;       // that every row takes: [0, first)
     int t0, t1;      // tiles
     bool tree;
 };
 __device__ __forceinline__ bool cache_range(CacheRange& r, const CacheAttnArgs& a, int rows_of_tile) {
     // row tiles of one range of keys next to each other on one XCD, then the ranges of one head
-    int id = xcd_remap(int(blockIdx.x), int(gridDim.x));
-    const int rt = id % a.row_tiles;
-    id /= a.row_tiles;
-    r.split = id % a.splits;
-    id /= a.splits;
-    r.at.hk = id % a.cache.heads;
-    r.at.b = id / a.cache.heads;
+    uint32_t id = uint32_t(xcd_remap(int(blockIdx.x), int(gridDim.x)));
+    uint32_t next = id / uint32_t(a.row_tiles);
+    const int rt = int(id - next * uint32_t(a.row_tiles));
+    id = next;
+    next = id / uint32_t(a.splits);
+    r.split = int(id - next * uint32_t(a.splits));
+    r.at.b = int(next / uint32_t(a.cache.heads));
+    r.at.hk = int(next - uint32_t(r.at.b) * uint32_t(a.cache.heads));
     r.group_of = (r.at.b * a.cache.heads + r.at.hk) * a.row_tiles + rt;
     int n = a.lens[r.at.b];
     n = n < 0 ? 0 : n < a.kv_len ? n : a.kv_len;
@@ -681,14 +694,15 @@ __device__ __forceinline__ bool cache_range(CacheRange& r, const CacheAttnArgs& 
     if (left <= 0) return false;  // rows past the request's last token, in every range of keys
     r.at.rows = left < rows_of_tile ? int(left) : rows_of_tile;
     r.tree = a.tree != nullptr;
-    const int64_t last = r.tree ? n : int64_t(r.at.base) + (r.at.row0 + r.at.rows - 1) / a.group + 1;
+    const int64_t last = r.tree ? n : int64_t(r.at.base) + uint32_t(r.at.row0 + r.at.rows - 1) / uint32_t(a.group) + 1;
     r.end = last < 0 ? 0 : last < n ? int(last) : n;
-    const int64_t first = r.tree ? r.at.base : int64_t(r.at.base) + r.at.row0 / a.group + 1;
+    const int64_t first = r.tree ? r.at.base : int64_t(r.at.base) + uint32_t(r.at.row0) / uint32_t(a.group) + 1;
     r.first = first < 0 ? 0 : first < n ? int(first) : n;
-    const int tiles = (r.end + kCacheTile - 1) / kCacheTile;
+    const uint32_t tiles = uint32_t(r.end + kCacheTile - 1) / kCacheTile;  // below 2^26, and 64 ranges at most
     // the ranges share the keys there are, not the keys there could be
-    r.t0 = int(int64_t(tiles) * r.split / a.splits);
-    r.t1 = int(int64_t(tiles) * (r.split + 1) / a.splits);
+    r.t0 = int(tiles * uint32_t(r.split) / uint32_t(a.splits));
+    r.t1 = int(tiles * uint32_t(r.split + 1) / uint32_t(a.splits));
+    r.end = r.end < r.t1 * kCacheTile ? r.end : r.t1 * kCacheTile;
     return true;
 }
 
@@ -705,7 +719,7 @@ __device__ __forceinline__ RowTokens<NB> row_tokens(const CacheRange& r, const C
     for (int nb = 0; nb < NB; ++nb) {
         const int in_tile = 16 * nb + (int(threadIdx.x) & 15);
         const int row = in_tile < at.rows ? at.row0 + in_tile : r.at.row0;
-        k.token[nb] = row / a.group;
+        k.token[nb] = int(uint32_t(row) / uint32_t(a.group));
         k.own[nb] = r.tree ? a.tree[int64_t(at.b) * a.q_len + k.token[nb]] : 0;
     }
     return k;
@@ -724,6 +738,35 @@ __device__ __forceinline__ uint32_t tile_keys(uint32_t (&allowed)[NB], const Cac
 // Every row takes every key of tile t, and they are there.
 __device__ __forceinline__ bool whole_tile(const CacheRange& r, const Places& place, int t) {
     return kCacheTile * (t + 1) <= r.first && place.ok[0] && place.ok[1];
+}
+
+// A tile with keys that some row leaves out or that are not there: their scores to -inf.  Scales of keys that are not there may be anything;
+// those of the others may be NaN (or infinite), which is for the rows that take the key alone, and zero in a product does not silence it: both
+// become zeros, and the sums of those rows NaN.
+template <int D, int BITS, int NB>
+__device__ __forceinline__ void trim_tile(CacheRowsState<D, BITS, NB>& w, TileScores<NB>& x, KeyScales<D, BITS>& vs, uint32_t live,
+                                          const uint32_t (&allowed)[NB]) {
+    constexpr int kGroups = CacheFmt<D, BITS>::kGroups;
+#pragma unroll
+    for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+#pragma unroll
+            for (int nb = 0; nb < NB; ++nb) x.s[kb][nb][i] = takes(allowed[nb], kb, i) ? x.s[kb][nb][i] : kNegInf;
+            if constexpr (BITS != 16) {
+#pragma unroll
+                for (int g = 0; g < kGroups; ++g) {
+                    uint32_t& word = vs.w[kb][BITS == 8 ? i / 2 : i * kGroups + g];
+                    const uint32_t exponent = BITS == 8 && i % 2 ? 0x7F800000u : 0x7F80u;
+                    const uint32_t others = BITS == 4 ? 0u : i % 2 ? 0xFFFFu : 0xFFFF0000u;  // of the word: not this key's
+                    const bool odd = (word & exponent) == exponent;
+                    word = odd || !takes(live, kb, i) ? word & others : word;
+#pragma unroll
+                    for (int nb = 0; nb < NB; ++nb)
+                        if (odd && takes(allowed[nb], kb, i)) (BITS == 4 ? w.low[nb][g] : w.l[nb]) = __builtin_nanf("");
+                }
+            }
+        }
 }
 
 // O of the lane's row in block nb: element [j][i], column o_column(j, 4q + i), as a number.
@@ -747,8 +790,9 @@ __device__ __forceinline__ void each_o(const CacheRowsState<D, BITS, NB>& w, int
 }
 
 __device__ __forceinline__ uint16_t* o_row(const CacheAttnArgs& a, const CacheWork& at, int in_tile) {
-    const int row = at.row0 + in_tile;
-    const int tok = row / a.group, g = row - tok * a.group;
+    const uint32_t row = uint32_t(at.row0 + in_tile);
+    const uint32_t tok = row / uint32_t(a.group);
+    const int g = int(row - tok * uint32_t(a.group));
     return a.o + int64_t(at.b) * a.o_batch + int64_t(tok) * a.o_token + int64_t(at.hk * a.group + g) * a.o_head;
 }
 
@@ -769,53 +813,68 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_attention_kernel(CacheAtt
     const int group_of = r.group_of, split = r.split;
 
     CacheRowsState<D, BITS, NB> w;
-    load_queries(w, a, at);
-    const RowTokens<NB> rows = row_tokens<NB>(r, a, at);
+    RawQueries<D, BITS, NB> raw;
+    load_queries(raw, a, at);
     int t = r.t0 + wave;
-    if (t < r.t1) {
+    // A tile on its way or in work.  With 16 rows two of them: the next tile's loads run beside this one's work, and the registers of
+    // this one's keys (values) are loaded anew, for the tile after the next, as soon as its scores (products) are there.
+    constexpr int kSets = NB == 1 ? 2 : 1;
+    struct Set {
         TileWords<D, BITS> k, v;
         KeyScales<D, BITS> ks, vs;
-        TileScores<NB> x;
-        TileWeights<D, BITS, NB> p;
-        uint32_t allowed[NB] = {};
-        // (past the wave's last tile: a tile of the next range, or empty resources at the end; it is not used)
-        auto places = [&](int tile) __attribute__((always_inline)) { return tile_places(a, at, tile, r.end); };
-        Places here = places(t), next = places(t + kWaves);
-        load_words<D, BITS, false>(k, a, here);
-        load_scales<D, BITS, false>(ks, a, here);
-        load_words<D, BITS, true>(v, a, here);
-        load_scales<D, BITS, true>(vs, a, here);
-        // the next tile's keys are on their way from the end of this one's scores on, its values from the end of this one's values
-        while (t < r.t1 && whole_tile(r, here, t)) {
-            tile_scores(w, k, ks, x);
-            if (t + kWaves < r.t1) {
-                load_words<D, BITS, false>(k, a, next);
-                load_scales<D, BITS, false>(ks, a, next);
-            }
-            tile_weights<false>(w, x, vs, allowed, p);
-            tile_values<false>(w, v, p, a, here, ~0u, allowed);
-            t += kWaves;
-            if (t < r.t1) {
-                load_words<D, BITS, true>(v, a, next);
-                load_scales<D, BITS, true>(vs, a, next);
-            }
-            here = next;
-            next = places(t + kWaves);
+        Places at;
+    };
+    auto load_keys = [&](Set& s, const Places& p) __attribute__((always_inline)) {
+        load_words<D, BITS, false>(s.k, a, p);
+        load_scales<D, BITS, false>(s.ks, a, p);
+    };
+    auto load_values = [&](Set& s, const Places& p) __attribute__((always_inline)) {
+        load_words<D, BITS, true>(s.v, a, p);
+        load_scales<D, BITS, true>(s.vs, a, p);
+    };
+    if (t < r.t1) {
+        auto places = [&](int tile) __attribute__((always_inline)) { return tile_places(a, at, tile, r.end); };  // past the range: none
+        Set set[kSets];
+#pragma unroll
+        for (int i = 0; i < kSets; ++i) {
+            set[i].at = places(t + i * kWaves);
+            load_keys(set[i], set[i].at);
+            load_values(set[i], set[i].at);
         }
-        while (t < r.t1) {
-            const uint32_t live = tile_keys(allowed, r, rows, here, t);
-            tile_scores(w, k, ks, x);
-            clear_scales(vs, live);
-            tile_weights<true>(w, x, vs, allowed, p);
-            tile_values<true>(w, v, p, a, here, live, allowed);
+        Places ahead = places(t + kSets * kWaves);
+        start_rows(w, raw, a);
+        const RowTokens<NB> rows = row_tokens<NB>(r, a, at);
+        auto step = [&](Set& s) __attribute__((always_inline)) {
+            TileScores<NB> x;
+            TileWeights<D, BITS, NB> p;
+            const bool whole = whole_tile(r, s.at, t);
+            tile_scores(w, s.k, s.ks, x);
+            load_keys(s, ahead);
+            __builtin_amdgcn_sched_barrier(0);  // the loads stay where they are
+            if (!whole) {
+                uint32_t allowed[NB];
+                const uint32_t live = tile_keys(allowed, r, rows, s.at, t);
+                trim_tile(w, x, s.vs, live, allowed);
+                if constexpr (BITS == 16) clean_values(w, s.v, a, s.at, live, allowed);
+            }
+            tile_weights(w, x, s.vs, p);
+            tile_values(w, s.v, p);
+            load_values(s, ahead);
+            __builtin_amdgcn_sched_barrier(0);
+            s.at = ahead;
             t += kWaves;
+            ahead = places(t + kSets * kWaves);
+        };
+        while (true) {
+            step(set[0]);
             if (t >= r.t1) break;
-            here = places(t);
-            load_words<D, BITS, false>(k, a, here);
-            load_scales<D, BITS, false>(ks, a, here);
-            load_words<D, BITS, true>(v, a, here);
-            load_scales<D, BITS, true>(vs, a, here);
+            if constexpr (kSets == 2) {
+                step(set[1]);
+                if (t >= r.t1) break;
+            }
         }
+    } else {
+        start_rows(w, raw, a);
     }
 
     // ---- the waves' results, as numbers: row by row in LDS ----
@@ -876,9 +935,28 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_attention_kernel(CacheAtt
     __syncthreads();
     if (!last_split) return;
     if (threadIdx.x == 0) __hip_atomic_store(&a.counters[group_of], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    float* const factors = &lds_o[0][0];  // [rows][splits], then the sums [rows]
+    // (row, 4 columns) per thread, with the ranges shared out over `parts` threads where threads are left over; kAhead loads in flight,
+    // the first of them while the rows' factors are worked out
+    constexpr int kAhead = 16;
+    int parts = 1;
+    while (parts < 8 && 2 * parts * items <= 64 * kWaves) parts *= 2;
+    const int span = (a.splits + parts - 1) / parts;
+    const int first_item = int(threadIdx.x) % items, part = int(threadIdx.x) / items;  // (threads past items * parts have nothing)
+    f32x4_t u[kAhead];
+    auto fetch = [&](int item, int s0, int s1) __attribute__((always_inline)) {
+        const uint32_t from = uint32_t(item / (D / 4)) * kPart + 16u * uint32_t(item % (D / 4));
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i)  // a range past the last reads as zeros
+            u[i] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
+                                                   part_rs, s0 + i < s1 ? uint32_t((s0 + i) * kRows) * kPart + from : 0xFFFFFF00u, 0, kSc1));
+    };
+    const int s_end = (part + 1) * span < a.splits ? (part + 1) * span : a.splits;
+    if (part < parts) fetch(first_item, part * span, s_end);
+    float* const factors = &lds_o[0][0];  // [rows][splits], then the sums [rows], then the parts' sums
     float* const totals = factors + kRows * kMaxCacheSplits;
-    for (int row = wave; row < at.rows; row += kWaves) {  // a lane per split
+    f32x4_t* const sums = reinterpret_cast<f32x4_t*>(totals + kRows);  // [threads]
+    static_assert(kRows * kMaxCacheSplits + kRows + 4 * 64 * kWaves <= kWaves * kRows * kPitch, "they fit the waves' results");
+    for (int row = wave; row < at.rows; row += kWaves) {  // a lane per range
         const uint32_t from = uint32_t(lane * kRows + row) * kPart + 4u * D;
         const bool in = lane < a.splits;
         const float m = in ? __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(part_rs, from, 0, kSc1)) : kNegInf;
@@ -894,38 +972,44 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_attention_kernel(CacheAtt
         if (lane == 0) totals[row] = sum;
     }
     __syncthreads();
-    constexpr int kAhead = 8;
-    for (int item = int(threadIdx.x); item < items; item += 64 * kWaves) {
-        const int row = item / (D / 4), col = 4 * (item % (D / 4));
+    for (int item = first_item; item < items && part < parts; item += 64 * kWaves) {  // more than one turn only with one part
+        const int row = item / (D / 4);
         f32x4_t v = {0.f, 0.f, 0.f, 0.f};
-        for (int s0 = 0; s0 < a.splits; s0 += kAhead) {
-            f32x4_t u[kAhead];
-#pragma unroll
-            for (int i = 0; i < kAhead; ++i)  // a split past the last reads as zeros
-                u[i] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                                       part_rs, s0 + i < a.splits ? uint32_t((s0 + i) * kRows + row) * kPart + 4u * uint32_t(col) : 0xFFFFFF00u,
-                                                       0, kSc1));
+        for (int s0 = part * span; s0 < s_end; s0 += kAhead) {
+            if (item != first_item || s0 != part * span) fetch(item, s0, s_end);
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                const float f = s0 + i < a.splits ? factors[row * kMaxCacheSplits + s0 + i] : 0.f;
+                const float f = s0 + i < s_end ? factors[row * kMaxCacheSplits + s0 + i] : 0.f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(f, u[i][e], v[e]);
             }
         }
-        store4(row, col, v, totals[row]);
+        if (parts == 1)
+            store4(row, 4 * (item % (D / 4)), v, totals[row]);
+        else
+            sums[part * items + item] = v;
+    }
+    if (parts == 1) return;
+    __syncthreads();
+    if (int(threadIdx.x) < items) {
+        f32x4_t v = sums[first_item];
+        for (int i = 1; i < parts; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] += sums[i * items + first_item][e];
+        store4(first_item / (D / 4), 4 * (first_item % (D / 4)), v, totals[first_item / (D / 4)]);
     }
 }
 
-// Many rows (trees, chunks): the waves share the tiles, through LDS, and each takes its own 16 NB rows.  The copy of the
-// next tile is on its way while one is computed.
+// Many rows (trees, chunks): the waves share the tiles, through LDS, and each takes its own 16 NB rows.  A turn is kTurn tiles; the
+// copies of the next turn's are on their way meanwhile.
 template <int D, int BITS, int NB>
 __global__ __launch_bounds__(256, 2) void cache_attention_rows_kernel(CacheAttnArgs a) {
-    constexpr int kRows = 64 * NB;
-    constexpr int kBytes = TileShape<D, BITS>::kCopies * 256 * TileShape<D, BITS>::kUnit;
+    constexpr int kRows = 64 * NB, kTurn = 2;
+    constexpr int kPitch = D + 4;  // floats of a result's row: neighbouring rows 4 banks apart
+    constexpr int kTile = LdsTile<D, BITS>::kBytes, kSlab = 16 * kPitch * 4;
+    constexpr int kBytes = kTurn * kTile > 4 * kSlab ? kTurn * kTile : 4 * kSlab;
     // an array per buffer: the compiler then sees that a tile's reads do not depend on the copies landing in the other
-    __shared__ __attribute__((aligned(1024))) unsigned char buf0[kBytes], buf1[kBytes];
-    constexpr int kPitch = D + 4;  // floats of a row: neighbouring rows 4 banks apart
-    __shared__ __attribute__((aligned(16))) float out[4][16 * kPitch];
+    __shared__ __attribute__((aligned(1024))) unsigned char buf0[kBytes], buf1[kTurn * kTile];
     const int lane = int(threadIdx.x) & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
     const int q = lane >> 4, l16 = lane & 15;
@@ -936,57 +1020,75 @@ __global__ __launch_bounds__(256, 2) void cache_attention_rows_kernel(CacheAttnA
     at.rows = at.rows - 16 * NB * wave;
     at.rows = at.rows < 0 ? 0 : at.rows < 16 * NB ? at.rows : 16 * NB;
     CacheRowsState<D, BITS, NB> w;
-    load_queries(w, a, at);
-    const RowTokens<NB> rows = row_tokens<NB>(r, a, at);
-    TileWords<D, BITS> words;
-    KeyScales<D, BITS> ks, vs;
-    TileScores<NB> x;
-    TileWeights<D, BITS, NB> p;
-    uint32_t allowed[NB] = {};
+    RawQueries<D, BITS, NB> raw;
+    load_queries(raw, a, at);
     int t = r.t0;
     if (t < r.t1) {
-        auto places = [&](int tile) __attribute__((always_inline)) { return tile_places(a, at, tile, r.end); };
-        Places here = places(t), next = places(t + 1);
-        // The tile in `cur`, with the copy of the next one to `other` under way meanwhile.
-        auto step = [&](auto partial, unsigned char* cur, unsigned char* other) __attribute__((always_inline)) {
-            constexpr bool kPartial = decltype(partial)::value;
-            wait_vmcnt<0>();
-            __syncthreads();  // the tile is there, and no wave reads `other` any more
-            if (t + 1 < r.t1) copy_tile<D, BITS>(other, a, next, wave);
-            uint32_t live = ~0u;
-            if constexpr (kPartial) live = tile_keys(allowed, r, rows, here, t);
-            read_words<D, BITS, false>(words, cur);
-            tile_scores(w, words, ks, x);
-            if (t + 1 < r.t1) load_scales<D, BITS, false>(ks, a, next);
-            if constexpr (kPartial) clear_scales(vs, live);
-            tile_weights<kPartial>(w, x, vs, allowed, p);
-            if (t + 1 < r.t1) load_scales<D, BITS, true>(vs, a, next);
-            read_words<D, BITS, true>(words, cur);
-            tile_values<kPartial>(w, words, p, a, here, live, allowed);
-            ++t;
-            here = next;
-            next = places(t + 1);
+        struct Turn {
+            Places at[kTurn];
         };
-        copy_tile<D, BITS>(buf0, a, here, wave);
-        load_scales<D, BITS, false>(ks, a, here);
-        load_scales<D, BITS, true>(vs, a, here);
-        bool second = false;  // which buffer holds tile t
-        while (t < r.t1 && whole_tile(r, here, t)) {
-            step(std::false_type{}, buf0, buf1);
-            second = true;
-            if (!(t < r.t1 && whole_tile(r, here, t))) break;
-            step(std::false_type{}, buf1, buf0);
-            second = false;
+        auto places = [&](int tile) __attribute__((always_inline)) {  // past the range: none
+            Turn u;
+#pragma unroll
+            for (int i = 0; i < kTurn; ++i) u.at[i] = tile_places(a, at, tile + i, r.end);
+            return u;
+        };
+        auto copy = [&](unsigned char* to, const Turn& u) __attribute__((always_inline)) {
+#pragma unroll
+            for (int i = 0; i < kTurn; ++i) copy_tile<D, BITS>(to + i * kTile, a, u.at[i], wave);
+        };
+        Turn here = places(t), next = places(t + kTurn);
+        copy(buf0, here);
+        start_rows(w, raw, a);
+        const RowTokens<NB> rows = row_tokens<NB>(r, a, at);
+        // The turn in `cur`, with the copies of the next one to `other` under way meanwhile.
+        auto turn = [&](unsigned char* cur, unsigned char* other) __attribute__((always_inline)) {
+            wait_vmcnt<0>();
+            __syncthreads();  // the tiles are there, and no wave reads `other` any more
+            if (t + kTurn < r.t1) copy(other, next);
+#pragma unroll 1
+            for (int i = 0; i < kTurn; ++i) {
+                if (t + i >= r.t1) break;
+                const unsigned char* const tile = cur + i * kTile;
+                TileWords<D, BITS> words;
+                KeyScales<D, BITS> sc;
+                TileScores<NB> x;
+                TileWeights<D, BITS, NB> p;
+                Places place = here.at[0];
+                if (i == 1) place = here.at[1];
+                const bool whole = whole_tile(r, place, t + i);
+                uint32_t allowed[NB], live = 0;
+                read_words<D, BITS, false>(words, tile);
+                read_scales<D, BITS, false>(sc, tile);
+                tile_scores(w, words, sc, x);
+                read_scales<D, BITS, true>(sc, tile);
+                if (!whole) {
+                    live = tile_keys(allowed, r, rows, place, t + i);
+                    trim_tile(w, x, sc, live, allowed);
+                }
+                tile_weights(w, x, sc, p);
+                read_words<D, BITS, true>(words, tile);
+                if constexpr (BITS == 16) {
+                    if (!whole) clean_values(w, words, a, place, live, allowed);
+                }
+                tile_values(w, words, p);
+            }
+            t += kTurn;
+            here = next;
+            next = places(t + kTurn);
+        };
+        while (true) {
+            turn(buf0, buf1);
+            if (t >= r.t1) break;
+            turn(buf1, buf0);
+            if (t >= r.t1) break;
         }
-        for (; t < r.t1; second = !second) {
-            if (second)
-                step(std::true_type{}, buf1, buf0);
-            else
-                step(std::true_type{}, buf0, buf1);
-        }
+    } else {
+        start_rows(w, raw, a);
     }
+    __syncthreads();  // the buffers have been read
     // 16 rows at a time through the wave's part of LDS, so that neighbouring lanes store neighbouring columns
-    float* const slab = out[wave];
+    float* const slab = reinterpret_cast<float*>(buf0 + wave * kSlab);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
         const float l = row_sum(w.l[nb]);
