@@ -19,7 +19,7 @@ int cache_shape(const lowbit_cache* c, lowbit::CacheArgs& a) {
     while (shift < 8 && (1 << shift) != c->page_size) ++shift;
     if ((1 << shift) != c->page_size) return LOWBIT_E_UNSUPPORTED;
     if (c->pages < 0 || c->kv_heads < 0) return LOWBIT_E_INVALID;
-    if (c->kv_heads > kMaxHeads || c->pages > kMaxDim >> shift) return LOWBIT_E_UNSUPPORTED;
+    if (c->kv_heads > kMaxHeads || c->pages > kMaxDim >> shift || c->pages * c->kv_heads > kMaxDim) return LOWBIT_E_UNSUPPORTED;
     a.k = static_cast<unsigned char*>(c->k);
     a.v = static_cast<unsigned char*>(c->v);
     a.k_scales = static_cast<unsigned char*>(c->k_scales);
@@ -111,7 +111,7 @@ int attention_args(const lowbit_cache_attention_problem* p, lowbit::CacheAttnArg
     a.table_stride = p->table_stride;
     a.batch = int(p->batch);
     a.q_len = int(p->q_len);
-    a.kv_len = int(p->kv_len);
+    a.kv_len = a.cache.pages > 0 ? int(p->kv_len) : 0;  // without pages there are no keys (and nothing to read)
     a.scale_log2 = float(double(p->scale) * kLog2E);
     return LOWBIT_OK;
 }

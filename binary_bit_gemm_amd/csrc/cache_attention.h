@@ -239,31 +239,52 @@ __device__ __forceinline__ void start_rows(CacheRowsState<D, BITS, NB>& w, const
     }
 }
 
-// Where a tile's two blocks of 16 keys lie: (page * heads + head) * page_size + the place of the first in its page; 0 and not `ok`
-// where there is no such page or key.
+// Where a tile's two blocks of 16 keys lie: (page * heads + head) * page_size + the place of the first in its page; somewhere in the first page's
+// first head and not `ok` where there is no such page or key (what is read there is not used).
 struct Places {
-    int64_t at[2];
-    bool ok[2];
+    uint64_t at0, at1;
+    bool ok0, ok1;
+    __device__ __forceinline__ uint64_t at(int kb) const { return kb == 0 ? at0 : at1; }
 };
+// A word that nothing writes meanwhile, at an address that the wave shares: a scalar load, whose wait leaves vector loads in flight.
+__device__ __forceinline__ int scalar_word(const int32_t* p) {
+    typedef const __attribute__((address_space(4))) int32_t* Constant;
+    const uint64_t x = reinterpret_cast<uint64_t>(p);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(x)), hi = __builtin_amdgcn_readfirstlane(uint32_t(x >> 32));
+    return *reinterpret_cast<Constant>((uint64_t(hi) << 32) | lo);
+}
+
 // `end` > 0: the keys that count; t may be past the last tile.
 __device__ __forceinline__ Places tile_places(const CacheAttnArgs& a, const CacheWork& at, int t, int end) {
     Places p;
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb) {
-        const uint32_t key = uint32_t(kCacheTile) * uint32_t(t) + 16u * kb;  // below 2^32: t is at most 32 past 2^26
+    auto block = [&](uint32_t key, uint64_t& place, bool& ok) __attribute__((always_inline)) {
         const bool in = key < uint32_t(end);
         const uint32_t last = in ? key : uint32_t(end) - 1u;
-        const int page = __builtin_amdgcn_readfirstlane(a.table[int64_t(at.b) * a.table_stride + (last >> a.cache.page_shift)]);
-        p.ok[kb] = in && uint32_t(page) < uint32_t(a.cache.pages);
-        const int64_t row = ((int64_t(page) * a.cache.heads + at.hk) << a.cache.page_shift) + (last & ((1u << a.cache.page_shift) - 16u));
-        p.at[kb] = p.ok[kb] ? row : 0;
-    }
+        const int page = scalar_word(a.table + int64_t(at.b) * a.table_stride + (last >> a.cache.page_shift));
+        ok = in && uint32_t(page) < uint32_t(a.cache.pages);
+        // (page * heads fits 31 bits)
+        const uint32_t head = ok ? uint32_t(page) * uint32_t(a.cache.heads) + uint32_t(at.hk) : 0u;
+        place = (uint64_t(head) << a.cache.page_shift) + (last & ((1u << a.cache.page_shift) - 16u));
+    };
+    const uint32_t key = uint32_t(kCacheTile) * uint32_t(t);  // below 2^32: t is at most 32 past 2^26
+    block(key, p.at0, p.ok0);
+    block(key + 16u, p.at1, p.ok1);
     return p;
 }
 
-// Rows of `size` bytes of a block; an empty resource (zeros without a read) where it is not there.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t block_rows(const unsigned char* base, int64_t at, bool ok, int size) {
-    return make_rsrc(base + at * size, ok ? 16u * uint32_t(size) : 0u);
+// The resource of a block's rows of `size` bytes.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t block_rows(const unsigned char* base, uint64_t at, int size) {
+    return make_rsrc(base + at * size, 16u * uint32_t(size));
+}
+
+// 16 or 8 bytes of the lane at `offset` of a block's rows of `size` bytes: one scalar base, a 32-bit offset.
+template <class T>
+__device__ __forceinline__ T load_at(const unsigned char* base, uint64_t at, int size, uint32_t offset) {
+    const uint64_t from = reinterpret_cast<uint64_t>(base) + at * uint32_t(size);
+    const uint32_t lo = __builtin_amdgcn_readfirstlane(uint32_t(from)), hi = __builtin_amdgcn_readfirstlane(uint32_t(from >> 32));
+    typedef const __attribute__((address_space(1))) unsigned char* Global;
+    const Global scalar = reinterpret_cast<Global>((uint64_t(hi) << 32) | lo);
+    return *reinterpret_cast<const __attribute__((address_space(1))) T*>(scalar + offset);
 }
 
 // The lane's byte in a block of K or V for copy or load i.
@@ -284,16 +305,16 @@ __device__ __forceinline__ void load_words(TileWords<D, BITS>& t, const CacheAtt
     constexpr int kW = TileShape<D, BITS>::kWords;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-        const auto rs = block_rows(IS_V ? a.cache.v : a.cache.k, p.at[kb], p.ok[kb], CacheFmt<D, BITS>::kRow);
+        const unsigned char* const base = IS_V ? a.cache.v : a.cache.k;
         if constexpr (kW >= 4) {
 #pragma unroll
             for (int i = 0; i < kW / 4; ++i) {
-                const u32x4_t x = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, unit_offset<D, BITS>(IS_V, i), 0, 0));
+                const u32x4_t x = load_at<u32x4_t>(base, p.at(kb), CacheFmt<D, BITS>::kRow, unit_offset<D, BITS>(IS_V, i));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) t.block[kb].w[4 * i + e] = x[e];
             }
         } else {
-            const u32x2_t x = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(rs, unit_offset<D, BITS>(IS_V, 0), 0, 0));
+            const u32x2_t x = load_at<u32x2_t>(base, p.at(kb), CacheFmt<D, BITS>::kRow, unit_offset<D, BITS>(IS_V, 0));
             t.block[kb].w[0] = x[0];
             t.block[kb].w[1] = x[1];
         }
@@ -307,15 +328,15 @@ __device__ __forceinline__ void load_scales(KeyScales<D, BITS>& s, const CacheAt
         const uint32_t q = (threadIdx.x & 63u) >> 4;
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
-            const auto rs = block_rows(IS_V ? a.cache.v_scales : a.cache.k_scales, p.at[kb], p.ok[kb], kS);
+            const unsigned char* const base = IS_V ? a.cache.v_scales : a.cache.k_scales;
             if constexpr (kS == 2) {
-                const u32x2_t x = __builtin_bit_cast(u32x2_t, __builtin_amdgcn_raw_buffer_load_b64(rs, 8u * q, 0, 0));
+                const u32x2_t x = load_at<u32x2_t>(base, p.at(kb), kS, 8u * q);
                 s.w[kb][0] = x[0];
                 s.w[kb][1] = x[1];
             } else {
 #pragma unroll
                 for (int i = 0; i < kS / 4; ++i) {
-                    const u32x4_t x = __builtin_bit_cast(u32x4_t, __builtin_amdgcn_raw_buffer_load_b128(rs, 4u * kS * q + 16u * i, 0, 0));
+                    const u32x4_t x = load_at<u32x4_t>(base, p.at(kb), kS, 4u * kS * q + 16u * i);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) s.w[kb][4 * i + e] = x[e];
                 }
@@ -337,12 +358,15 @@ template <int D, int BITS>
 __device__ __forceinline__ void copy_tile(unsigned char* lds, const CacheAttnArgs& a, const Places& p, int wave) {
     using S = TileShape<D, BITS>;
     constexpr int kPer = S::kWords / S::kUnit;  // copies of a block of K or V
+    // (values, not a choice of addresses, which would put the places in memory)
+    const uint64_t first = p.at0, apart = p.at0 ^ p.at1;
+    auto place = [&](int kb) __attribute__((always_inline)) { return first ^ (apart & (kb != 0 ? ~uint64_t(0) : uint64_t(0))); };
 #pragma unroll
     for (int c = 0; c < S::kCopies / 4; ++c) {
         const int copy = wave * (S::kCopies / 4) + c;  // the same for the wave
         const bool is_v = copy >= 2 * kPer;
         const int kb = copy / kPer % 2, i = copy % kPer;
-        const auto rs = block_rows(is_v ? a.cache.v : a.cache.k, kb ? p.at[1] : p.at[0], kb ? p.ok[1] : p.ok[0], CacheFmt<D, BITS>::kRow);
+        const auto rs = block_rows(is_v ? a.cache.v : a.cache.k, place(kb), CacheFmt<D, BITS>::kRow);
         unsigned char* const to = lds + copy * (256 * S::kUnit);
         const uint32_t from = unit_offset<D, BITS>(is_v, i);
         if constexpr (S::kUnit == 4)
@@ -354,7 +378,7 @@ __device__ __forceinline__ void copy_tile(unsigned char* lds, const CacheAttnArg
         constexpr int kS = CacheFmt<D, BITS>::kScaleBytes, kSegment = LdsTile<D, BITS>::kSegment;
         constexpr int kBytes = BITS == 8 ? 4 : 16;  // of a lane
         const int lane = int(threadIdx.x) & 63, kb = wave & 1;
-        const auto rs = block_rows(wave & 2 ? a.cache.v_scales : a.cache.k_scales, kb ? p.at[1] : p.at[0], kb ? p.ok[1] : p.ok[0], kS);
+        const auto rs = block_rows(wave & 2 ? a.cache.v_scales : a.cache.k_scales, place(kb), kS);
         unsigned char* const to = lds + LdsTile<D, BITS>::kWords + wave * kSegment;
         if (lane < kSegment / kBytes) {
             if constexpr (kBytes == 4)
@@ -443,7 +467,7 @@ __device__ __forceinline__ void clean_values(CacheRowsState<D, 16, NB>& w, TileW
         }
     if (!__any(odd != 0)) return;
     for (int key = 0; key < kCacheTile; ++key) {
-        const int64_t p = key < 16 ? place.at[0] : place.at[1];
+        const uint64_t p = place.at0 ^ ((place.at0 ^ place.at1) & (key < 16 ? uint64_t(0) : ~uint64_t(0)));
         bool some = false;  // (a key that is not there is allowed to no row)
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) some = some || ((allowed[nb] >> key) & 1);
@@ -516,10 +540,8 @@ __device__ __forceinline__ void tile_scores(const CacheRowsState<D, BITS, NB>& w
     }
 }
 
-// Whether the lane's row takes its key i of block kb.
-__device__ __forceinline__ bool takes(uint32_t allowed, int kb, int i) {
-    return (allowed >> (16 * kb + 4 * ((threadIdx.x & 63u) >> 4) + i)) & 1;
-}
+// All ones or zeros: bit (kb, i) of the lane's keys (bits from the lane's quarter on).
+__device__ __forceinline__ uint32_t taken_mask(uint32_t mine, int kb, int i) { return uint32_t(int32_t(mine << (31 - 16 * kb - i)) >> 31); }
 
 // Row block nb's e to what its scores x and the values' scales need, and x and the sums with it.
 template <int D, int BITS, int NB>
@@ -679,15 +701,14 @@ __device__ __forceinline__ bool cache_range(CacheRange& r, const CacheAttnArgs& 
     r.at.b = int(next / uint32_t(a.cache.heads));
     r.at.hk = int(next - uint32_t(r.at.b) * uint32_t(a.cache.heads));
     r.group_of = (r.at.b * a.cache.heads + r.at.hk) * a.row_tiles + rt;
-    int n = a.lens[r.at.b];
+    int n = scalar_word(a.lens + r.at.b);
     n = n < 0 ? 0 : n < a.kv_len ? n : a.kv_len;
     int ql = a.q_len;
     if (a.q_lens != nullptr) {
-        const int v = a.q_lens[r.at.b];
+        const int v = scalar_word(a.q_lens + r.at.b);
         ql = v < 0 ? 0 : v < ql ? v : ql;
     }
-    r.at.n = n = __builtin_amdgcn_readfirstlane(n);
-    ql = __builtin_amdgcn_readfirstlane(ql);
+    r.at.n = n;
     r.at.base = n - ql;
     r.at.row0 = rt * rows_of_tile;
     const int64_t left = int64_t(ql) * a.group - r.at.row0;
@@ -729,7 +750,7 @@ __device__ __forceinline__ RowTokens<NB> row_tokens(const CacheRange& r, const C
 template <int NB>
 __device__ __forceinline__ uint32_t tile_keys(uint32_t (&allowed)[NB], const CacheRange& r, const RowTokens<NB>& k, const Places& place, int t) {
     const int key0 = kCacheTile * t;
-    const uint32_t live = first_bits(int64_t(r.at.n) - key0 - 1) & ((place.ok[0] ? 0xFFFFu : 0u) | (place.ok[1] ? 0xFFFF0000u : 0u));
+    const uint32_t live = first_bits(int64_t(r.at.n) - key0 - 1) & ((place.ok0 ? 0xFFFFu : 0u) | (place.ok1 ? 0xFFFF0000u : 0u));
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) allowed[nb] = live & taken(r.tree, k.own[nb], k.token[nb], r.at.base, key0);
     return live;
@@ -737,7 +758,7 @@ __device__ __forceinline__ uint32_t tile_keys(uint32_t (&allowed)[NB], const Cac
 
 // Every row takes every key of tile t, and they are there.
 __device__ __forceinline__ bool whole_tile(const CacheRange& r, const Places& place, int t) {
-    return kCacheTile * (t + 1) <= r.first && place.ok[0] && place.ok[1];
+    return kCacheTile * (t + 1) <= r.first && place.ok0 && place.ok1;
 }
 
 // A tile with keys that some row leaves out or that are not there: their scores to -inf.  Scales of keys that are not there may be anything;
@@ -747,23 +768,33 @@ template <int D, int BITS, int NB>
 __device__ __forceinline__ void trim_tile(CacheRowsState<D, BITS, NB>& w, TileScores<NB>& x, KeyScales<D, BITS>& vs, uint32_t live,
                                           const uint32_t (&allowed)[NB]) {
     constexpr int kGroups = CacheFmt<D, BITS>::kGroups;
+    const uint32_t shift = 4u * ((threadIdx.x & 63u) >> 4);
+    const uint32_t there = live >> shift;
+    uint32_t mine[NB];
+#pragma unroll
+    for (int nb = 0; nb < NB; ++nb) mine[nb] = allowed[nb] >> shift;
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
 #pragma unroll
-            for (int nb = 0; nb < NB; ++nb) x.s[kb][nb][i] = takes(allowed[nb], kb, i) ? x.s[kb][nb][i] : kNegInf;
+            for (int nb = 0; nb < NB; ++nb) {
+                const uint32_t all = taken_mask(mine[nb], kb, i);
+                x.s[kb][nb][i] = __uint_as_float((__float_as_uint(x.s[kb][nb][i]) & all) | (0xFF800000u & ~all));
+            }
             if constexpr (BITS != 16) {
 #pragma unroll
                 for (int g = 0; g < kGroups; ++g) {
                     uint32_t& word = vs.w[kb][BITS == 8 ? i / 2 : i * kGroups + g];
-                    const uint32_t exponent = BITS == 8 && i % 2 ? 0x7F800000u : 0x7F80u;
-                    const uint32_t others = BITS == 4 ? 0u : i % 2 ? 0xFFFFu : 0xFFFF0000u;  // of the word: not this key's
-                    const bool odd = (word & exponent) == exponent;
-                    word = odd || !takes(live, kb, i) ? word & others : word;
+                    const int up = BITS == 8 && i % 2 ? 16 : 0;                       // the scale's half of the word
+                    const uint32_t half = BITS == 4 ? ~0u : up != 0 ? 0xFFFF0000u : 0xFFFFu;  // what goes with it
+                    const uint32_t odd = (word & (0x7F80u << up)) == (0x7F80u << up) ? ~0u : 0u;
+                    word &= ~half | (taken_mask(there, kb, i) & ~odd);
 #pragma unroll
-                    for (int nb = 0; nb < NB; ++nb)
-                        if (odd && takes(allowed[nb], kb, i)) (BITS == 4 ? w.low[nb][g] : w.l[nb]) = __builtin_nanf("");
+                    for (int nb = 0; nb < NB; ++nb) {
+                        float& to = BITS == 4 ? w.low[nb][g] : w.l[nb];
+                        to = __uint_as_float(__float_as_uint(to) | (odd & taken_mask(mine[nb], kb, i) & 0x7FFFFFFFu));  // NaN, or as it was
+                    }
                 }
             }
         }
@@ -1025,17 +1056,14 @@ __global__ __launch_bounds__(256, 2) void cache_attention_rows_kernel(CacheAttnA
     int t = r.t0;
     if (t < r.t1) {
         struct Turn {
-            Places at[kTurn];
+            Places first, second;
         };
         auto places = [&](int tile) __attribute__((always_inline)) {  // past the range: none
-            Turn u;
-#pragma unroll
-            for (int i = 0; i < kTurn; ++i) u.at[i] = tile_places(a, at, tile + i, r.end);
-            return u;
+            return Turn{tile_places(a, at, tile, r.end), tile_places(a, at, tile + 1, r.end)};
         };
         auto copy = [&](unsigned char* to, const Turn& u) __attribute__((always_inline)) {
-#pragma unroll
-            for (int i = 0; i < kTurn; ++i) copy_tile<D, BITS>(to + i * kTile, a, u.at[i], wave);
+            copy_tile<D, BITS>(to, a, u.first, wave);
+            copy_tile<D, BITS>(to + kTile, a, u.second, wave);
         };
         Turn here = places(t), next = places(t + kTurn);
         copy(buf0, here);
@@ -1046,16 +1074,18 @@ __global__ __launch_bounds__(256, 2) void cache_attention_rows_kernel(CacheAttnA
             wait_vmcnt<0>();
             __syncthreads();  // the tiles are there, and no wave reads `other` any more
             if (t + kTurn < r.t1) copy(other, next);
+            const uint32_t ok = (here.first.ok0 ? 1u : 0u) | (here.first.ok1 ? 2u : 0u) | (here.second.ok0 ? 4u : 0u) | (here.second.ok1 ? 8u : 0u);
+            const uint64_t at0 = here.first.at0, at1 = here.first.at1, apart0 = at0 ^ here.second.at0, apart1 = at1 ^ here.second.at1;
 #pragma unroll 1
             for (int i = 0; i < kTurn; ++i) {
                 if (t + i >= r.t1) break;
+                const uint64_t other_tile = uint64_t(0) - uint64_t(i);
+                const Places place{at0 ^ (apart0 & other_tile), at1 ^ (apart1 & other_tile), ((ok >> (2 * i)) & 1) != 0, ((ok >> (2 * i)) & 2) != 0};
                 const unsigned char* const tile = cur + i * kTile;
                 TileWords<D, BITS> words;
                 KeyScales<D, BITS> sc;
                 TileScores<NB> x;
                 TileWeights<D, BITS, NB> p;
-                Places place = here.at[0];
-                if (i == 1) place = here.at[1];
                 const bool whole = whole_tile(r, place, t + i);
                 uint32_t allowed[NB], live = 0;
                 read_words<D, BITS, false>(words, tile);

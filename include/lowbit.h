@@ -430,7 +430,8 @@ int lowbit_attention(const lowbit_attention_problem* problem, void* workspace, s
  *           the attention kernel's lanes (csrc/kv_cache.h; rows come back in the usual order through lowbit_cache_read).
  *   k_scales, v_scales  device bf16: 8 bits [pages, kv_heads, page_size], one scale per token and head; 4 bits [pages, kv_heads,
  *           page_size, head_dim / 64, 2], scale and smallest value per 64 elements; 16 bits: unused.
- *   page_size 16, 32, 64, 128 or 256; head_dim 64 or 128; pages * page_size < 2^31; pointers 16-byte aligned.
+ *   page_size 16, 32, 64, 128 or 256; head_dim 64 or 128; pages * page_size and pages * kv_heads < 2^31; pointers
+ *           16-byte aligned.
  * What an element x stands for once written, with up(t) the smallest bf16 not below t:
  *   8 bits: s * c,  s = up(max|x| * (1/127)) over the head's row, c = x / s rounded to even;
  *   4 bits: s * u + b,  b = min x, s = up((max x - b) * (1/15)) over the 64 elements, u = (x - b) / s rounded to even, 0 .. 15
