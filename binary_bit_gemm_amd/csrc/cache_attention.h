@@ -46,8 +46,6 @@ template <int D, int BITS>
 struct TileShape {
     static constexpr int kWords = CacheFmt<D, BITS>::kRow / 16;     // of K, and of V, per block
     static constexpr int kScales = CacheFmt<D, BITS>::kScaleBytes;  // words that hold the scales of four keys
-    static constexpr int kUnit = kWords >= 4 ? 4 : 1;               // words of a copy to LDS
-    static constexpr int kCopies = 4 * kWords / kUnit;              // of a tile: K then V, block by block
 };
 template <int W>
 struct Words {
@@ -287,13 +285,13 @@ __device__ __forceinline__ T load_at(const unsigned char* base, uint64_t at, int
     return *reinterpret_cast<const __attribute__((address_space(1))) T*>(scalar + offset);
 }
 
-// The lane's byte in a block of K or V for copy or load i.
+// The lane's byte in a block of K or V for load i.
 template <int D, int BITS>
 __device__ __forceinline__ uint32_t unit_offset(bool is_v, int i) {
     using F = CacheFmt<D, BITS>;
     const uint32_t lane = threadIdx.x & 63u, q = lane >> 4, l16 = lane & 15u;
     constexpr uint32_t kT = F::kBlock;
-    if constexpr (TileShape<D, BITS>::kUnit == 4)
+    if constexpr (TileShape<D, BITS>::kWords >= 4)
         return is_v ? 4u * q / kT * (kT * F::kRow) + 16u * l16 + kT * F::kRow * i : l16 * F::kRow + 16u * q + 64u * i;
     else
         return (is_v ? q * (4u * F::kRow) + 8u * l16 : l16 * F::kRow + 8u * q) + 4u * i;
@@ -345,78 +343,80 @@ __device__ __forceinline__ void load_scales(KeyScales<D, BITS>& s, const CacheAt
     }
 }
 
-// A tile in LDS: its words as lanes take them, then the scales of K's two blocks and of V's.
+// A tile in LDS: its two blocks of K and two of V as they lie in memory, each row of K with its 16-byte chunk c at position c ^ swizzle(row), so
+// that the 16 rows of an operand read fall into different banks; then the scales of K's blocks and of V's.
 template <int D, int BITS>
 struct LdsTile {
-    static constexpr int kWords = TileShape<D, BITS>::kCopies * 256 * TileShape<D, BITS>::kUnit;
+    static constexpr int kRow = CacheFmt<D, BITS>::kRow;
+    static constexpr int kBlock = 16 * kRow;
     static constexpr int kSegment = 16 * CacheFmt<D, BITS>::kScaleBytes;
-    static constexpr int kBytes = kWords + 4 * kSegment;
+    static constexpr int kBytes = 4 * kBlock + 4 * kSegment;
+    static constexpr int kCopy = kBlock < 1024 ? kBlock : 1024;  // bytes that one wave-wide copy brings, neighbouring lanes on neighbouring chunks
+    static constexpr int kCopies = 4 * kBlock / kCopy;           // of a tile: K's blocks, then V's
+    static constexpr int swizzle(int row) { return kRow == 256 ? row & 15 : kRow == 128 ? (row >> 1) & 7 : kRow == 64 ? (row >> 2) & 3 : 0; }
 };
 
-// The wave's quarter of a tile's copies to LDS, lane by lane.
+// Copy c of a tile (the same for the wave): `at` is its block's place.
 template <int D, int BITS>
-__device__ __forceinline__ void copy_tile(unsigned char* lds, const CacheAttnArgs& a, const Places& p, int wave) {
-    using S = TileShape<D, BITS>;
-    constexpr int kPer = S::kWords / S::kUnit;  // copies of a block of K or V
-    // (values, not a choice of addresses, which would put the places in memory)
-    const uint64_t first = p.at0, apart = p.at0 ^ p.at1;
-    auto place = [&](int kb) __attribute__((always_inline)) { return first ^ (apart & (kb != 0 ? ~uint64_t(0) : uint64_t(0))); };
-#pragma unroll
-    for (int c = 0; c < S::kCopies / 4; ++c) {
-        const int copy = wave * (S::kCopies / 4) + c;  // the same for the wave
-        const bool is_v = copy >= 2 * kPer;
-        const int kb = copy / kPer % 2, i = copy % kPer;
-        const auto rs = block_rows(is_v ? a.cache.v : a.cache.k, place(kb), CacheFmt<D, BITS>::kRow);
-        unsigned char* const to = lds + copy * (256 * S::kUnit);
-        const uint32_t from = unit_offset<D, BITS>(is_v, i);
-        if constexpr (S::kUnit == 4)
-            dma16(rs, to, from, 0);
+__device__ __forceinline__ void copy_words(unsigned char* tile, const CacheAttnArgs& a, int c, uint64_t at) {
+    using L = LdsTile<D, BITS>;
+    constexpr int kPer = L::kBlock / L::kCopy;  // copies of a block
+    const bool is_v = c >= 2 * kPer;
+    const auto rs = block_rows(is_v ? a.cache.v : a.cache.k, at, L::kRow);
+    const int lane = int(threadIdx.x) & 63, chunk = c % kPer * (L::kCopy / 16) + lane;  // of the block, in LDS
+    const int row = chunk / (L::kRow / 16);
+    const int from = is_v ? chunk : chunk ^ L::swizzle(row);
+    if (L::kCopy == 1024 || lane < L::kCopy / 16) dma16(rs, tile + c * L::kCopy, 16u * uint32_t(from), 0);
+}
+// Segment s of its scales: K's blocks 0 and 1, then V's.
+template <int D, int BITS>
+__device__ __forceinline__ void copy_scales(unsigned char* tile, const CacheAttnArgs& a, int s, uint64_t at) {
+    using L = LdsTile<D, BITS>;
+    constexpr int kBytes = BITS == 8 ? 4 : 16;  // of a lane
+    const int lane = int(threadIdx.x) & 63;
+    const auto rs = block_rows(s >= 2 ? a.cache.v_scales : a.cache.k_scales, at, CacheFmt<D, BITS>::kScaleBytes);
+    unsigned char* const to = tile + 4 * L::kBlock + s * L::kSegment;
+    if (lane < L::kSegment / kBytes) {
+        if constexpr (kBytes == 4)
+            dma4(rs, to, 4u * uint32_t(lane), 0);
         else
-            dma4(rs, to, from, 0);
-    }
-    if constexpr (BITS != 16) {
-        constexpr int kS = CacheFmt<D, BITS>::kScaleBytes, kSegment = LdsTile<D, BITS>::kSegment;
-        constexpr int kBytes = BITS == 8 ? 4 : 16;  // of a lane
-        const int lane = int(threadIdx.x) & 63, kb = wave & 1;
-        const auto rs = block_rows(wave & 2 ? a.cache.v_scales : a.cache.k_scales, place(kb), kS);
-        unsigned char* const to = lds + LdsTile<D, BITS>::kWords + wave * kSegment;
-        if (lane < kSegment / kBytes) {
-            if constexpr (kBytes == 4)
-                dma4(rs, to, 4u * uint32_t(lane), 0);
-            else
-                dma16(rs, to, 16u * uint32_t(lane), 0);
-        }
+            dma16(rs, to, 16u * uint32_t(lane), 0);
     }
 }
 
-// K or V of a tile from there: a lane reads the 16 (or 4) bytes that its number brought.
+// K or V of a tile from there.
 template <int D, int BITS, bool IS_V>
-__device__ __forceinline__ void read_words(TileWords<D, BITS>& t, const unsigned char* lds) {
+__device__ __forceinline__ void read_words(TileWords<D, BITS>& t, const unsigned char* tile) {
     using S = TileShape<D, BITS>;
-    constexpr int kPer = S::kWords / S::kUnit;
-    const unsigned char* const at = lds + (threadIdx.x & 63u) * (4 * S::kUnit);
+    using L = LdsTile<D, BITS>;
+    const int l16 = int(threadIdx.x) & 15;
 #pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
+    for (int kb = 0; kb < 2; ++kb) {
+        const unsigned char* const block = tile + ((IS_V ? 2 : 0) + kb) * L::kBlock;
+        if constexpr (S::kWords >= 4) {
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) {
-            const unsigned char* const from = at + (((IS_V ? 2 : 0) + kb) * kPer + i) * (256 * S::kUnit);
-            if constexpr (S::kUnit == 4) {
-                const u32x4_t x = *reinterpret_cast<const u32x4_t*>(from);
+            for (int i = 0; i < S::kWords / 4; ++i) {
+                const uint32_t from = unit_offset<D, BITS>(IS_V, i);  // within a row of K: an aligned chunk
+                const u32x4_t x = *reinterpret_cast<const u32x4_t*>(block + (IS_V ? from : from ^ uint32_t(L::swizzle(l16) << 4)));
 #pragma unroll
                 for (int e = 0; e < 4; ++e) t.block[kb].w[4 * i + e] = x[e];
-            } else {
-                t.block[kb].w[i] = *reinterpret_cast<const uint32_t*>(from);
             }
+        } else {
+            const u32x2_t x = *reinterpret_cast<const u32x2_t*>(block + unit_offset<D, BITS>(IS_V, 0));
+            t.block[kb].w[0] = x[0];
+            t.block[kb].w[1] = x[1];
         }
+    }
 }
 template <int D, int BITS, bool IS_V>
-__device__ __forceinline__ void read_scales(KeyScales<D, BITS>& s, const unsigned char* lds) {
+__device__ __forceinline__ void read_scales(KeyScales<D, BITS>& s, const unsigned char* tile) {
+    using L = LdsTile<D, BITS>;
     constexpr int kS = CacheFmt<D, BITS>::kScaleBytes;
     if constexpr (kS > 0) {
-        const unsigned char* const at = lds + LdsTile<D, BITS>::kWords + (IS_V ? 2 : 0) * LdsTile<D, BITS>::kSegment + ((threadIdx.x & 63u) >> 4) * (4 * kS);
+        const unsigned char* const at = tile + 4 * L::kBlock + (IS_V ? 2 : 0) * L::kSegment + ((threadIdx.x & 63u) >> 4) * (4 * kS);
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
-            const unsigned char* const from = at + kb * LdsTile<D, BITS>::kSegment;
+            const unsigned char* const from = at + kb * L::kSegment;
             if constexpr (kS == 2) {
                 const u32x2_t x = *reinterpret_cast<const u32x2_t*>(from);
                 s.w[kb][0] = x[0];
@@ -449,8 +449,8 @@ __device__ __forceinline__ float low_at(const uint32_t* s, int i, int g) {
 // 16-bit values of a tile with keys that some row leaves out or that are not there.  Zero in a product does not silence an infinity or a NaN, so
 // these become zeros, and what is there is added to the rows that take it.
 template <int D, int NB>
-__device__ __forceinline__ void clean_values(CacheRowsState<D, 16, NB>& w, TileWords<D, 16>& v, const CacheAttnArgs& a, const Places& place, uint32_t live,
-                                             const uint32_t (&allowed)[NB]) {
+__device__ __forceinline__ void clean_values(CacheRowsState<D, 16, NB>& w, TileWords<D, 16>& v, const CacheAttnArgs& a, const CacheWork& at, int t, int end,
+                                             uint32_t live, const uint32_t (&allowed)[NB]) {
     using F = CacheFmt<D, 16>;
     constexpr int kW = TileShape<D, 16>::kWords;
     const uint32_t q = (threadIdx.x & 63u) >> 4;
@@ -466,6 +466,7 @@ __device__ __forceinline__ void clean_values(CacheRowsState<D, 16, NB>& w, TileW
             v.block[kb].w[i] = z;
         }
     if (!__any(odd != 0)) return;
+    const Places place = tile_places(a, at, t, end);
     for (int key = 0; key < kCacheTile; ++key) {
         const uint64_t p = place.at0 ^ ((place.at0 ^ place.at1) & (key < 16 ? uint64_t(0) : ~uint64_t(0)));
         bool some = false;  // (a key that is not there is allowed to no row)
@@ -748,9 +749,9 @@ __device__ __forceinline__ RowTokens<NB> row_tokens(const CacheRange& r, const C
 
 // Keys of tile t that are there, and those that each of the lane's rows takes.
 template <int NB>
-__device__ __forceinline__ uint32_t tile_keys(uint32_t (&allowed)[NB], const CacheRange& r, const RowTokens<NB>& k, const Places& place, int t) {
+__device__ __forceinline__ uint32_t tile_keys(uint32_t (&allowed)[NB], const CacheRange& r, const RowTokens<NB>& k, uint32_t blocks, int t) {
     const int key0 = kCacheTile * t;
-    const uint32_t live = first_bits(int64_t(r.at.n) - key0 - 1) & ((place.ok0 ? 0xFFFFu : 0u) | (place.ok1 ? 0xFFFF0000u : 0u));
+    const uint32_t live = first_bits(int64_t(r.at.n) - key0 - 1) & ((blocks & 1u ? 0xFFFFu : 0u) | (blocks & 2u ? 0xFFFF0000u : 0u));
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) allowed[nb] = live & taken(r.tree, k.own[nb], k.token[nb], r.at.base, key0);
     return live;
@@ -884,9 +885,9 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_attention_kernel(CacheAtt
             __builtin_amdgcn_sched_barrier(0);  // the loads stay where they are
             if (!whole) {
                 uint32_t allowed[NB];
-                const uint32_t live = tile_keys(allowed, r, rows, s.at, t);
+                const uint32_t live = tile_keys(allowed, r, rows, (s.at.ok0 ? 1u : 0u) | (s.at.ok1 ? 2u : 0u), t);
                 trim_tile(w, x, s.vs, live, allowed);
-                if constexpr (BITS == 16) clean_values(w, s.v, a, s.at, live, allowed);
+                if constexpr (BITS == 16) clean_values(w, s.v, a, at, t, r.end, live, allowed);
             }
             tile_weights(w, x, s.vs, p);
             tile_values(w, s.v, p);
@@ -1033,14 +1034,16 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_attention_kernel(CacheAtt
 
 // Many rows (trees, chunks): the waves share the tiles, through LDS, and each takes its own 16 NB rows.  A turn is kTurn tiles; the
 // copies of the next turn's are on their way meanwhile.
-template <int D, int BITS, int NB>
-__global__ __launch_bounds__(256, 2) void cache_attention_rows_kernel(CacheAttnArgs a) {
-    constexpr int kRows = 64 * NB, kTurn = 2;
+template <int D, int BITS, int NB, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, 2) void cache_attention_rows_kernel(CacheAttnArgs a) {
+    using L = LdsTile<D, BITS>;
+    constexpr int kRows = 16 * NB * WAVES;
+    constexpr int kTurn = D == 128 && BITS == 16 && WAVES == 4 ? 2 : 4;  // two workgroups of 4 waves fit a compute unit
     constexpr int kPitch = D + 4;  // floats of a result's row: neighbouring rows 4 banks apart
-    constexpr int kTile = LdsTile<D, BITS>::kBytes, kSlab = 16 * kPitch * 4;
-    constexpr int kBytes = kTurn * kTile > 4 * kSlab ? kTurn * kTile : 4 * kSlab;
+    constexpr int kSlab = 16 * kPitch * 4;
+    constexpr int kBytes = kTurn * L::kBytes > WAVES * kSlab ? kTurn * L::kBytes : WAVES * kSlab;
     // an array per buffer: the compiler then sees that a tile's reads do not depend on the copies landing in the other
-    __shared__ __attribute__((aligned(1024))) unsigned char buf0[kBytes], buf1[kTurn * kTile];
+    __shared__ __attribute__((aligned(1024))) unsigned char buf0[kBytes], buf1[kTurn * L::kBytes];
     const int lane = int(threadIdx.x) & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
     const int q = lane >> 4, l16 = lane & 15;
@@ -1055,57 +1058,79 @@ __global__ __launch_bounds__(256, 2) void cache_attention_rows_kernel(CacheAttnA
     load_queries(raw, a, at);
     int t = r.t0;
     if (t < r.t1) {
-        struct Turn {
-            Places first, second;
+        // Lane b has the page of block b of a turn's 2 kTurn (those after repeat).  Fetched a turn before its copies are issued.
+        const int32_t* const table = a.table + int64_t(at.b) * a.table_stride;
+        auto key_of = [&](int tile) __attribute__((always_inline)) { return uint32_t(kCacheTile) * uint32_t(tile) + 16u * uint32_t(lane & (2 * kTurn - 1)); };
+        auto fetch_pages = [&](int tile) __attribute__((always_inline)) {
+            const uint32_t key = key_of(tile), last = key < uint32_t(r.end) ? key : uint32_t(r.end) - 1u;
+            return table[last >> a.cache.page_shift];
         };
-        auto places = [&](int tile) __attribute__((always_inline)) {  // past the range: none
-            return Turn{tile_places(a, at, tile, r.end), tile_places(a, at, tile + 1, r.end)};
+        auto there = [&](int page, int tile) __attribute__((always_inline)) {  // bit b: block b's keys are there
+            return __ballot(key_of(tile) < uint32_t(r.end) && uint32_t(page) < uint32_t(a.cache.pages));
         };
-        auto copy = [&](unsigned char* to, const Turn& u) __attribute__((always_inline)) {
-            copy_tile<D, BITS>(to, a, u.first, wave);
-            copy_tile<D, BITS>(to + kTile, a, u.second, wave);
+        auto copy = [&](unsigned char* to, int page, uint64_t ok, int tile) __attribute__((always_inline)) {
+            auto place = [&](int b) __attribute__((always_inline)) {  // (blocks that are not there: the first page's, and what comes is not used)
+                const uint32_t head = (ok >> b) & 1 ? uint32_t(__builtin_amdgcn_readlane(page, b)) * uint32_t(a.cache.heads) + uint32_t(at.hk) : 0u;
+                return (uint64_t(head) << a.cache.page_shift) + ((uint32_t(kCacheTile) * uint32_t(tile) + 16u * uint32_t(b)) & ((1u << a.cache.page_shift) - 16u));
+            };
+            constexpr int kAll = kTurn * L::kCopies;
+#pragma unroll
+            for (int j = 0; j < (kAll + WAVES - 1) / WAVES; ++j) {
+                const int c = wave + j * WAVES, i = c / L::kCopies, in_tile = c % L::kCopies;
+                if (kAll % WAVES == 0 || c < kAll) copy_words<D, BITS>(to + i * L::kBytes, a, in_tile, place(2 * i + in_tile / (L::kCopies / 4) % 2));
+            }
+            if constexpr (BITS != 16) {
+#pragma unroll
+                for (int j = 0; j < 4 * kTurn / WAVES; ++j) {
+                    const int c = wave + j * WAVES, i = c / 4;
+                    copy_scales<D, BITS>(to + i * L::kBytes, a, c % 4, place(2 * i + c % 2));
+                }
+            }
         };
-        Turn here = places(t), next = places(t + kTurn);
-        copy(buf0, here);
+        int page = fetch_pages(t);
+        uint64_t ok = there(page, t);
+        copy(buf0, page, ok, t);
+        page = fetch_pages(t + kTurn);
         start_rows(w, raw, a);
         const RowTokens<NB> rows = row_tokens<NB>(r, a, at);
         // The turn in `cur`, with the copies of the next one to `other` under way meanwhile.
         auto turn = [&](unsigned char* cur, unsigned char* other) __attribute__((always_inline)) {
             wait_vmcnt<0>();
             __syncthreads();  // the tiles are there, and no wave reads `other` any more
-            if (t + kTurn < r.t1) copy(other, next);
-            const uint32_t ok = (here.first.ok0 ? 1u : 0u) | (here.first.ok1 ? 2u : 0u) | (here.second.ok0 ? 4u : 0u) | (here.second.ok1 ? 8u : 0u);
-            const uint64_t at0 = here.first.at0, at1 = here.first.at1, apart0 = at0 ^ here.second.at0, apart1 = at1 ^ here.second.at1;
+            const uint64_t ok_next = there(page, t + kTurn);
+            if (t + kTurn < r.t1) {
+                const int of_next = page;
+                page = fetch_pages(t + 2 * kTurn);
+                copy(other, of_next, ok_next, t + kTurn);
+            }
 #pragma unroll 1
             for (int i = 0; i < kTurn; ++i) {
                 if (t + i >= r.t1) break;
-                const uint64_t other_tile = uint64_t(0) - uint64_t(i);
-                const Places place{at0 ^ (apart0 & other_tile), at1 ^ (apart1 & other_tile), ((ok >> (2 * i)) & 1) != 0, ((ok >> (2 * i)) & 2) != 0};
-                const unsigned char* const tile = cur + i * kTile;
+                const unsigned char* const tile = cur + i * L::kBytes;
                 TileWords<D, BITS> words;
                 KeyScales<D, BITS> sc;
                 TileScores<NB> x;
                 TileWeights<D, BITS, NB> p;
-                const bool whole = whole_tile(r, place, t + i);
+                const uint32_t blocks = uint32_t(ok >> (2 * i)) & 3u;
+                const bool whole = blocks == 3u && kCacheTile * (t + i + 1) <= r.first;
                 uint32_t allowed[NB], live = 0;
                 read_words<D, BITS, false>(words, tile);
                 read_scales<D, BITS, false>(sc, tile);
                 tile_scores(w, words, sc, x);
                 read_scales<D, BITS, true>(sc, tile);
                 if (!whole) {
-                    live = tile_keys(allowed, r, rows, place, t + i);
+                    live = tile_keys(allowed, r, rows, blocks, t + i);
                     trim_tile(w, x, sc, live, allowed);
                 }
                 tile_weights(w, x, sc, p);
                 read_words<D, BITS, true>(words, tile);
                 if constexpr (BITS == 16) {
-                    if (!whole) clean_values(w, words, a, place, live, allowed);
+                    if (!whole) clean_values(w, words, a, at, t + i, r.end, live, allowed);
                 }
                 tile_values(w, words, p);
             }
             t += kTurn;
-            here = next;
-            next = places(t + kTurn);
+            ok = ok_next;
         };
         while (true) {
             turn(buf0, buf1);
@@ -1225,10 +1250,15 @@ hipError_t launch_cache_attention_as(const CacheAttnArgs& a, const CacheAttnPlan
             hipLaunchKernelGGL((cache_attention_kernel<D, BITS, 2, 8>), dim3(grid), block, 0, stream, a);
         return hipGetLastError();
     }
+    const dim3 block(64 * plan.waves);
     if (plan.tile_rows == 64)
-        hipLaunchKernelGGL((cache_attention_rows_kernel<D, BITS, 1>), dim3(grid), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((cache_attention_rows_kernel<D, BITS, 1, 4>), dim3(grid), block, 0, stream, a);
+    else if (plan.tile_rows == 128 && plan.waves == 4)
+        hipLaunchKernelGGL((cache_attention_rows_kernel<D, BITS, 2, 4>), dim3(grid), block, 0, stream, a);
+    else if (plan.tile_rows == 128)
+        hipLaunchKernelGGL((cache_attention_rows_kernel<D, BITS, 1, 8>), dim3(grid), block, 0, stream, a);
     else
-        hipLaunchKernelGGL((cache_attention_rows_kernel<D, BITS, 2>), dim3(grid), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((cache_attention_rows_kernel<D, BITS, 2, 8>), dim3(grid), block, 0, stream, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
     const int64_t rows = int64_t(a.batch) * a.cache.heads * a.row_tiles * plan.tile_rows;

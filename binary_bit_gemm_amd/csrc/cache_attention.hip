@@ -22,7 +22,7 @@ CacheAttnPlan plan_cache_attention(const CacheAttnArgs& a, bool may_split) {
     p.tile_rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128;
     if (getenv("CA_ROWS") && p.share_tiles) p.tile_rows = atoi(getenv("CA_ROWS"));
     p.row_tiles = int(tiles_of(rows, p.tile_rows));
-    p.waves = getenv("CA_WAVES") ? atoi(getenv("CA_WAVES")) : 4;
+    p.waves = p.share_tiles ? (p.tile_rows == 256 ? 8 : p.tile_rows == 64 ? 4 : getenv("CA_WAVES") ? atoi(getenv("CA_WAVES")) : 4) : getenv("CA_WAVES") ? atoi(getenv("CA_WAVES")) : 4;
     const int64_t groups = int64_t(a.batch) * a.cache.heads * p.row_tiles, tiles = tiles_of(a.kv_len, kTileKeys);
     int64_t splits = groups == 0 || !may_split ? 1 : kComputeUnits / groups;
     splits = splits < tiles / 12 ? splits : tiles / 12;
@@ -44,7 +44,7 @@ hipError_t launch_cache_attention(CacheAttnArgs a, const CacheAttnPlan& plan, vo
     if (e == hipSuccess && trace_enabled())
         std::fprintf(stderr, "lowbit: cache_attention %s rows=%d splits=%d grid=%lld block=%d problem=%dx%dx%dx%d kv_heads=%d dim=%d bits=%d page=%d%s\n",
                      plan.share_tiles ? "many" : "few", plan.tile_rows, a.splits,
-                     (long long)(int64_t(a.row_tiles) * a.splits * a.cache.heads * a.batch), plan.share_tiles ? 256 : 64 * plan.waves, a.batch, a.q_len, a.kv_len, a.cache.heads * a.group, a.cache.heads, a.cache.head_dim, a.cache.bits, 1 << a.cache.page_shift,
+                     (long long)(int64_t(a.row_tiles) * a.splits * a.cache.heads * a.batch), 64 * plan.waves, a.batch, a.q_len, a.kv_len, a.cache.heads * a.group, a.cache.heads, a.cache.head_dim, a.cache.bits, 1 << a.cache.page_shift,
                      a.tree != nullptr ? " tree" : "");
     return e;
 }
