@@ -464,10 +464,11 @@ def _workspace(workspace, like):
     """(address, bytes) of an optional workspace."""
     if workspace is None:
         return 0, 0
-    if not workspace.is_cuda or not workspace.is_contiguous():
-        raise ValueError("workspace must be a contiguous device tensor")
-    _same_device(like, (("workspace", workspace),))
-    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
+        if not workspace.is_cuda or not workspace.is_contiguous():
+            raise ValueError("workspace must be a contiguous device tensor")
+        _same_device(like, (("workspace", workspace),))
+    return workspace.data_ptr(), workspace.nbytes
 
 
 def _output(out, shape, like):
@@ -671,28 +672,37 @@ class KVCache:
             raise ValueError(f"bits must be 4, 8 or 16, got {bits}")
         dtype = torch.bfloat16 if bits == 16 else torch.uint8
         _require(k, dtype, "k", 4)
-        _plain(v, dtype, "v", 4, k)
-        pages, heads, page, row = k.shape
-        if v.shape != k.shape:
-            raise ValueError(f"v must be {tuple(k.shape)}, got {tuple(v.shape)}")
+        shape = k.shape
+        pages, heads, page, row = shape
+        dev = k.get_device()
+        if not (_fits(v, dtype, dev) and v.shape == shape):
+            _plain(v, dtype, "v", 4, k)
+            raise ValueError(f"v must be {tuple(shape)}, got {tuple(v.shape)}")
         dim = row if bits == 16 else row * 8 // bits
         if bits == 16:
             if k_scales is not None or v_scales is not None:
                 raise ValueError("a 16-bit cache has no scales")
         else:
             want = (pages, heads, page) if bits == 8 else (pages, heads, page, dim // 64, 2)
-            for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-                _plain(t, torch.bfloat16, name, len(want), k)
-                if t.shape != want:
-                    raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
+            bf16 = torch.bfloat16
+            if not (_fits(k_scales, bf16, dev) and _fits(v_scales, bf16, dev) and k_scales.shape == want and v_scales.shape == want):
+                for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+                    _plain(t, bf16, name, len(want), k)
+                    if t.shape != want:
+                        raise ValueError(f"{name} must be {want}, got {tuple(t.shape)}")
         self.k, self.v, self.k_scales, self.v_scales, self.bits = k, v, k_scales, v_scales, bits
         self.shape = (pages, heads, page, dim)
 
     def _fields(self):
         pages, heads, page, dim = self.shape
-        ks, vs = self.k_scales, self.v_scales
-        return (self.k.data_ptr(), self.v.data_ptr(), ks.data_ptr() if ks is not None else 0, vs.data_ptr() if vs is not None else 0,
-                pages, page, heads, dim, self.bits)
+        if self.bits == 16:
+            return self.k.data_ptr(), self.v.data_ptr(), 0, 0, pages, page, heads, dim, 16
+        return (self.k.data_ptr(), self.v.data_ptr(), self.k_scales.data_ptr(), self.v_scales.data_ptr(), pages, page, heads, dim, self.bits)
+
+
+def _fits(t, dtype, dev: int) -> bool:
+    """Whether t is a contiguous tensor of that type on that device."""
+    return t.__class__.__name__ != "NoneType" and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
 
 
 def kv_cache(pages: int, kv_heads: int, head_dim: int, bits: int = 8, page_size: int = 64, device="cuda") -> KVCache:
@@ -710,68 +720,95 @@ def kv_cache(pages: int, kv_heads: int, head_dim: int, bits: int = 8, page_size:
     return KVCache(k, v, *(torch.zeros(scales, dtype=torch.bfloat16, device=device) for _ in range(2)), bits=bits)
 
 
+def _row_strides(t, name: str, shape, dev: int):
+    """(token, head) strides of bf16 rows `shape` = [tokens, heads, D] whose elements lie together, 0 for dimensions of one."""
+    if t.dtype is not _torch().bfloat16 or t.get_device() != dev or t.shape != shape:
+        _heads(t, name, 3)
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {tuple(t.shape)}")
+        raise ValueError(f"{name} must be on the cache's device, got {t.device}")
+    token, head, one = t.stride()
+    if one != 1:
+        _heads(t, name, 3)
+    return token if shape[0] > 1 else 0, head if shape[1] > 1 else 0
+
+
 def _cache_rows(function: str, cache: KVCache, k, v, slots) -> None:
-    _heads(k, "k", 3)
-    _heads(v, "v", 3)
+    like = cache.k
+    dev = like.get_device()
+    at = _plain(slots, _torch().int32, "slots", 1, like)
     _, heads, _, dim = cache.shape
-    T = slots.shape[0]
-    if k.shape != (T, heads, dim) or v.shape != k.shape:
-        raise ValueError(f"k and v must be [{T}, {heads}, {dim}], got {tuple(k.shape)} and {tuple(v.shape)}")
-    _same_device(cache.k, (("k", k), ("v", v)))
-    _call(function, cache.k, _CACHE.pack(*cache._fields()), k.data_ptr(), v.data_ptr(), T, *_strides(k), *_strides(v), slots.data_ptr())
+    shape = (slots.shape[0], heads, dim)
+    for name, t in (("k", k), ("v", v)):
+        if not isinstance(t, _TORCH.Tensor):
+            raise TypeError(f"{name} must be a torch.Tensor")
+    ks, vs = _row_strides(k, "k", shape, dev), _row_strides(v, "v", shape, dev)
+    _call(function, like, _CACHE.pack(*cache._fields()), k.data_ptr(), v.data_ptr(), shape[0], *ks, *vs, at)
 
 
 def cache_write(cache: KVCache, k, v, slots) -> None:
     """Quantises k and v [tokens, kv_heads, head_dim] (bf16, any strides of whole 16-byte pieces, e.g. views of a fused QKV output) into the
     cache's slots (int32 [tokens]: page * page_size + place; -1 leaves a row out; those of one call differ) (lowbit_cache_write)."""
-    _plain(slots, _torch().int32, "slots", 1, cache.k)
     _cache_rows("lowbit_cache_write", cache, k, v, slots)
 
 
 def cache_read(cache: KVCache, slots, k_out=None, v_out=None):
     """The rows at `slots` (int32 [tokens]) as bf16 [tokens, kv_heads, head_dim] (lowbit_cache_read): (k_out, v_out).  Rows whose slot
     is outside the cache are left as they were (zeros where the output is made here)."""
-    torch = _torch()
-    _plain(slots, torch.int32, "slots", 1, cache.k)
-    _, heads, _, dim = cache.shape
-    shape = (slots.shape[0], heads, dim)
-    k_out, v_out = (torch.zeros(shape, dtype=torch.bfloat16, device=cache.k.device) if t is None else t for t in (k_out, v_out))
+    if k_out is None or v_out is None:
+        torch = _torch()
+        _plain(slots, torch.int32, "slots", 1, cache.k)
+        shape = (slots.shape[0], cache.shape[1], cache.shape[3])
+        k_out, v_out = (torch.zeros(shape, dtype=torch.bfloat16, device=cache.k.device) if t is None else t for t in (k_out, v_out))
     _cache_rows("lowbit_cache_read", cache, k_out, v_out, slots)
     return k_out, v_out
 
 
 def _cache_attention_problem(q, cache, page_table, key_lens, q_lens, tree, kv_len, scale, out):
     torch = _torch()
+    int32 = torch.int32
     _heads(q, "q", 4)
-    B, Lq, Hq, D = q.shape
-    pages, heads, page, dim = cache.shape
+    B, Lq, Hq, D = shape = q.shape
+    _, _, page, dim = cache.shape
+    dev = q.get_device()
     if D != dim:
-        raise ValueError(f"q must be [batch, q_len, q_heads, {dim}], got {tuple(q.shape)}")
-    pt = pk = pq = ptree = po = stride = 0
-    so = (Lq * Hq * D, Hq * D, D)
+        raise ValueError(f"q must be [batch, q_len, q_heads, {dim}], got {tuple(shape)}")
+    if cache.k.get_device() != dev:
+        raise ValueError(f"cache must be on {q.device}, got {cache.k.device}")
+    pt = pk = pq = ptree = po = pages = 0
     if page_table is not None:
-        pt = _plain(page_table, torch.int32, "page_table", 2, q)
-        pk = _plain(key_lens, torch.int32, "key_lens", 1, q)
-        if page_table.shape[0] != B or key_lens.shape[0] != B:
+        pt = page_table.data_ptr() if _fits(page_table, int32, dev) and page_table.dim() == 2 else _plain(page_table, int32, "page_table", 2, q)
+        pk = key_lens.data_ptr() if _fits(key_lens, int32, dev) and key_lens.dim() == 1 else _plain(key_lens, int32, "key_lens", 1, q)
+        rows, pages = page_table.shape
+        if rows != B or key_lens.shape[0] != B:
             raise ValueError(f"page_table must be [{B}, pages] and key_lens [{B}]")
-        stride = page_table.shape[1]
         if kv_len is None:
-            kv_len = stride * page
-        elif kv_len > stride * page:
-            raise ValueError(f"page_table holds {stride * page} keys of a request, fewer than kv_len = {kv_len}")
+            kv_len = pages * page
+        elif kv_len > pages * page:
+            raise ValueError(f"page_table holds {pages * page} keys of a request, fewer than kv_len = {kv_len}")
     if q_lens is not None:
-        pq = _plain(q_lens, torch.int32, "q_lens", 1, q)
+        pq = _plain(q_lens, int32, "q_lens", 1, q)
         if q_lens.shape[0] != B:
             raise ValueError(f"q_lens must be [{B}]")
     if tree is not None:
         ptree = _plain(tree, torch.int64, "tree", 2, q)
         if tree.shape != (B, Lq):
             raise ValueError(f"tree must be [{B}, {Lq}]")
+    qb, qt, qh, _ = q.stride()
+    ob, ot, oh = Lq * Hq * D, Hq * D, D
     if out is not None:
-        _heads(out, "out", 4)
-        po, so = out.data_ptr(), _strides(out)
-    _same_device(q, (("cache", cache.k), ("out", out)))
-    return _CACHE_ATTENTION_PROBLEM.pack(*cache._fields(), q.data_ptr(), po, pt, pk, pq, ptree, B, Lq, kv_len, *_strides(q), *so, stride, Hq,
+        if out.dtype is not torch.bfloat16 or out.get_device() != dev or out.stride(3) != 1:
+            _heads(out, "out", 4)
+            _same_device(q, (("out", out),))
+        po = out.data_ptr()
+        ob, ot, oh, _ = out.stride()
+    if B <= 1:  # strides along dimensions of one say nothing
+        qb = ob = 0
+    if Lq <= 1:
+        qt = ot = 0
+    if Hq <= 1:
+        qh = oh = 0
+    return _CACHE_ATTENTION_PROBLEM.pack(*cache._fields(), q.data_ptr(), po, pt, pk, pq, ptree, B, Lq, kv_len, qb, qt, qh, ob, ot, oh, pages, Hq,
                                          scale if scale is not None else D ** -0.5)
 
 
@@ -799,7 +836,8 @@ def cache_attention(q, cache: KVCache, page_table, key_lens, q_lens=None, tree=N
         _heads(q, "q", 4)
         torch = _torch()
         out = torch.empty(q.shape, dtype=torch.bfloat16, device=q.device) if q_lens is None else torch.zeros(q.shape, dtype=torch.bfloat16, device=q.device)
-    else:
+    elif out.__class__ is not q.__class__ or out.shape != q.shape:
+        _heads(q, "q", 4)
         out = _output(out, q.shape, q)
     p = _cache_attention_problem(q, cache, page_table, key_lens, q_lens, tree, kv_len, scale, out)
     ws, nbytes = _workspace(workspace, q)

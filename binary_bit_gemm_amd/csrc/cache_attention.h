@@ -829,9 +829,9 @@ __device__ __forceinline__ uint16_t* o_row(const CacheAttnArgs& a, const CacheWo
 }
 
 // Few rows (decoded tokens): the waves take tiles in turn.
-template <int D, int BITS, int NB, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, 2) void cache_attention_kernel(CacheAttnArgs a) {
-    constexpr int kWaves = WAVES, kRows = 16 * NB;
+template <int D, int BITS, int NB>
+__global__ __launch_bounds__(256, 2) void cache_attention_kernel(CacheAttnArgs a) {
+    constexpr int kWaves = 4, kRows = 16 * NB;
     constexpr int kPitch = D + 4;  // floats of a row: neighbouring rows 4 banks apart
     __shared__ __attribute__((aligned(16))) float lds_o[kWaves][kRows * kPitch];
     __shared__ float lds_m[kWaves][kRows], lds_l[kWaves][kRows];  // e (-inf: no key), and the sum
@@ -1038,7 +1038,7 @@ template <int D, int BITS, int NB, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, 2) void cache_attention_rows_kernel(CacheAttnArgs a) {
     using L = LdsTile<D, BITS>;
     constexpr int kRows = 16 * NB * WAVES;
-    constexpr int kTurn = D == 128 && BITS == 16 && WAVES == 4 ? 2 : 4;  // two workgroups of 4 waves fit a compute unit
+    constexpr int kTurn = D == 128 && BITS == 16 && WAVES == 4 ? 2 : 4;  // so that two workgroups of 4 waves fit a compute unit
     constexpr int kPitch = D + 4;  // floats of a result's row: neighbouring rows 4 banks apart
     constexpr int kSlab = 16 * kPitch * 4;
     constexpr int kBytes = kTurn * L::kBytes > WAVES * kSlab ? kTurn * L::kBytes : WAVES * kSlab;
@@ -1239,22 +1239,15 @@ template <int D, int BITS>
 hipError_t launch_cache_attention_as(const CacheAttnArgs& a, const CacheAttnPlan& plan, hipStream_t stream) {
     const unsigned grid = unsigned(a.row_tiles) * unsigned(a.splits) * unsigned(a.cache.heads) * unsigned(a.batch);
     if (!plan.share_tiles) {
-        const dim3 block(64 * plan.waves);
-        if (plan.tile_rows == 16 && plan.waves == 4)
-            hipLaunchKernelGGL((cache_attention_kernel<D, BITS, 1, 4>), dim3(grid), block, 0, stream, a);
-        else if (plan.tile_rows == 16)
-            hipLaunchKernelGGL((cache_attention_kernel<D, BITS, 1, 8>), dim3(grid), block, 0, stream, a);
-        else if (plan.waves == 4)
-            hipLaunchKernelGGL((cache_attention_kernel<D, BITS, 2, 4>), dim3(grid), block, 0, stream, a);
+        if (plan.tile_rows == 16)
+            hipLaunchKernelGGL((cache_attention_kernel<D, BITS, 1>), dim3(grid), dim3(256), 0, stream, a);
         else
-            hipLaunchKernelGGL((cache_attention_kernel<D, BITS, 2, 8>), dim3(grid), block, 0, stream, a);
+            hipLaunchKernelGGL((cache_attention_kernel<D, BITS, 2>), dim3(grid), dim3(256), 0, stream, a);
         return hipGetLastError();
     }
     const dim3 block(64 * plan.waves);
     if (plan.tile_rows == 64)
         hipLaunchKernelGGL((cache_attention_rows_kernel<D, BITS, 1, 4>), dim3(grid), block, 0, stream, a);
-    else if (plan.tile_rows == 128 && plan.waves == 4)
-        hipLaunchKernelGGL((cache_attention_rows_kernel<D, BITS, 2, 4>), dim3(grid), block, 0, stream, a);
     else if (plan.tile_rows == 128)
         hipLaunchKernelGGL((cache_attention_rows_kernel<D, BITS, 1, 8>), dim3(grid), block, 0, stream, a);
     else
