@@ -21,7 +21,8 @@
 //     stays as long as they are below 2^12 (which the tile's largest score and largest scale tell), and the sums with it.
 // 16-bit caches take the same path with bf16 operands and no scales.
 //
-// Rounding: p s to fp16 (2^-11 of each; 16 bits: p to bf16, 2^-8 of each) and O to bf16; all else is fp32.
+// Rounding: p s to fp16 (2^-11 of each; 16 bits: p to bf16, 2^-8 of each) and O to bf16; all else is fp32.  fp16 holds 24 bits below its normal
+// range: a weight is off by 2^-25 of the row's largest at least, which shows only where one group's scales are 2^12 below the other's.
 #pragma once
 
 #include "kv_cache.h"
@@ -38,7 +39,7 @@ constexpr float kNegInf = -__builtin_inff();
 constexpr int kCacheTile = 32;      // keys of a wave's tile
 constexpr int kMaxCacheSplits = 64;  // a lane per split in the join
 constexpr float kMostWeight = 0x1p12f;    // of p s 2^-e: past it e moves
-constexpr float kMostProbability = 0x1p100f;  // of p 2^-e (values of scale 0 do not bound it)
+constexpr float kMostProbability = 0x1p70f;   // of p 2^-e, which values of scale 0 do not bound: times their smallest value it stays in fp32
 constexpr float kCodeUnit = 0x1p24f;    // 1 / the value of code 1 as an fp16
 
 // What a lane has of a tile: per block of 16 keys its words of K (a quarter of key l16's row) and of V (piece l16 of keys 4q ..).
@@ -563,7 +564,7 @@ __device__ __forceinline__ void rebase(CacheRowsState<D, BITS, NB>& w, int nb, T
     }
     // a row without a key stays as it is, one with its first key takes any e, others a larger one
     up = top > kNegInf && (up > 0.f || w.seen[nb] == 0) ? __builtin_ceilf(up) : 0.f;  // whole, so that e stays exact
-    const float f = w.seen[nb] != 0 ? __builtin_amdgcn_exp2f(-up) : 0.f;  // (sums of nothing are zeros)
+    const float f = w.seen[nb] != 0 ? __builtin_amdgcn_exp2f(-up) : 1.f;  // (sums of nothing are zeros, or what clean_values put there)
     w.seen[nb] = top > kNegInf ? 1u : w.seen[nb];
     w.e[nb] += up;
     w.l[nb] *= f;

@@ -467,10 +467,11 @@ int lowbit_cache_read(const lowbit_cache* cache, void* k, void* v, int64_t token
  *   q_lens  device int32 [batch] or NULL (q_len each): a request's new tokens.  Rows of o past them are left as they were.
  *   tree   device uint64 [batch, q_len] or NULL: new token t takes new token i where bit i of tree[b, t] is set (its ancestors and
  *          itself; q_len <= 64).  NULL: those up to itself.  Every new token takes all keys before the new ones.
- *   A row that takes no key gets zeros.  Slots that no row takes may hold anything; a NaN in a key or value reaches the rows that take it.
+ *   A row that takes no key gets zeros.  Slots that no row takes may hold anything; a NaN in a key or value reaches the rows that take it,
+ * an infinite value too (as an infinity or, where its weight underflows, a NaN).
  * Scores, softmax statistics and sums are fp32; a probability times its value's scale is rounded to fp16 (16 bits: the
- * probability to bf16) for the second product, O to bf16 once.  q up to 2^100, values from 2^-80 to 2^100 in magnitude (and 0)
- * stay inside fp32's range on the way.  Deterministic.
+ * probability to bf16) for the second product, O to bf16 once.  At 8 and 4 bits fp32's range holds what arises on the way for rows of V whose
+ * largest magnitudes lie between 2^-50 and 2^30 (or are 0), and scores inside it.  Deterministic.
  *   workspace  as for lowbit_attention: lowbit_cache_attention_workspace_size(problem) bytes (0: none), 16-byte aligned,
  *          zero-filled before its first use, shared by calls that do not run at once; with none or too little the keys are not split
  *          across workgroups.

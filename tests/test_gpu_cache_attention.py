@@ -103,10 +103,12 @@ class Problem:
         self.answers[scale] = answers
         return answers
 
-    def check(self, got, scale=None):
+    def check(self, got, scale=None, rows=None):
+        """rows: (request) -> the new tokens to look at (bool [q_len])."""
         got = R.bf16(got)
         for (b, h), (want, bound) in self.wanted(scale if scale is not None else 1 / math.sqrt(self.dim)).items():
-            live = slice(0, self.q_lens[b])
+            live = np.arange(self.q_len) < self.q_lens[b]
+            live = live if rows is None else live & rows(b)
             off = np.abs(got[b, live, h] - want[live]) - bound[live]
             assert np.isfinite(got[b, live, h]).all()
             assert off.max(initial=-1) <= 0, f"request {b}, head {h}: over its bound by {off.max()}"
