@@ -1033,6 +1033,12 @@ __global__ __launch_bounds__(256, 2) void cache_attention_kernel(CacheAttnArgs a
     }
 }
 
+// Behind the ranges' sums of O [heads][ranges][rows][D]: [heads][ranges][rows] of (e, sum).
+template <int D>
+__device__ __forceinline__ f32x2_t* row_stats(const CacheAttnArgs& a, int rows_of_tile) {
+    return reinterpret_cast<f32x2_t*>(a.part + int64_t(a.batch) * a.cache.heads * a.row_tiles * a.splits * rows_of_tile * D);
+}
+
 // Many rows (trees, chunks): the waves share the tiles, through LDS, and each takes its own 16 NB rows.  A turn is kTurn tiles; the
 // copies of the next turn's are on their way meanwhile.
 template <int D, int BITS, int NB, int WAVES>
@@ -1160,26 +1166,22 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_attention_rows_kernel(Cac
             if (a.splits == 1) {
                 *reinterpret_cast<u32x2_t*>(o_row(a, at, 16 * nb + row) + col) = u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
             } else {
-                f32x2_t* const dst = reinterpret_cast<f32x2_t*>(a.part + (part_row + row) * (D + 2) + col);  // rows lie on 8 bytes
-                dst[0] = f32x2_t{v[0], v[1]};
-                dst[1] = f32x2_t{v[2], v[3]};
+                *reinterpret_cast<f32x4_t*>(a.part + (part_row + row) * D + col) = v;
             }
         }
-        if (a.splits > 1 && q == 0 && 16 * nb + l16 < at.rows) {
-            float* const dst = a.part + (part_row + l16) * (D + 2) + D;
-            dst[0] = l != 0.f ? w.e[nb] : kNegInf;  // (a NaN goes along)
-            dst[1] = l;
-        }
+        if (a.splits > 1 && q == 0 && 16 * nb + l16 < at.rows)  // e (a NaN goes along) and the sum
+            row_stats<D>(a, kRows)[part_row + l16] = f32x2_t{l != 0.f ? w.e[nb] : kNegInf, l};
         __builtin_amdgcn_s_waitcnt(0xC07F);  // the slab's reads are done
         asm volatile("" ::: "memory");
     }
 }
 
-// Joins the ranges' results of a row, in a fixed order: a wave per row of the padded tiles.
+// Joins the ranges' results of a row, in a fixed order: a wave per row of the padded tiles, on the XCD whose cache the row's ranges were written
+// through (a head's ranges lie on one, and the remapping is the same).
 template <int D>
 __global__ __launch_bounds__(256) void cache_join_kernel(CacheAttnArgs a, int rows_of_tile) {
     const int lane = int(threadIdx.x) & 63;
-    const int64_t id = int64_t(blockIdx.x) * 4 + (threadIdx.x >> 6);
+    const int64_t id = int64_t(xcd_remap(int(blockIdx.x), int(gridDim.x))) * 4 + (threadIdx.x >> 6);
     const int64_t groups = int64_t(a.batch) * a.cache.heads * a.row_tiles;
     if (id >= groups * rows_of_tile) return;
     const int64_t group_of = id / rows_of_tile;
@@ -1192,23 +1194,25 @@ __global__ __launch_bounds__(256) void cache_join_kernel(CacheAttnArgs a, int ro
     int ql = a.q_len;
     if (a.q_lens != nullptr) ql = min(max(a.q_lens[at.b], 0), ql);
     if (int64_t(at.row0) + in_tile >= int64_t(ql) * a.group) return;
-    const float* const part = a.part + (group_of * a.splits * rows_of_tile + in_tile) * (D + 2);
-    const int64_t step = int64_t(rows_of_tile) * (D + 2);
+    const int64_t part_row = group_of * a.splits * rows_of_tile + in_tile;
+    const float* const part = a.part + part_row * D;
+    const int64_t step = int64_t(rows_of_tile) * D;
     // four columns a lane, the ranges shared out over kParts groups of lanes, kAhead loads of each in flight
     constexpr int kLanes = D / 4, kParts = 64 / kLanes, kAhead = 8;
     const int col = 4 * (lane % kLanes), first = lane / kLanes;
-    f32x2_t u[kAhead][2];
+    f32x4_t u[kAhead];
     auto fetch = [&](int s0) __attribute__((always_inline)) {
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
             const int s = s0 + i * kParts;
-            const float* const from = part + (s < a.splits ? s : 0) * step + col;  // rows lie on 8 bytes
-            u[i][0] = *reinterpret_cast<const f32x2_t*>(from);
-            u[i][1] = *reinterpret_cast<const f32x2_t*>(from + 2);
+            u[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            if (s < a.splits) u[i] = *reinterpret_cast<const f32x4_t*>(part + s * step + col);
         }
     };
     fetch(first);
-    const float m = lane < a.splits ? part[lane * step + D] : kNegInf, ls = lane < a.splits ? part[lane * step + D + 1] : 0.f;
+    f32x2_t stats = {kNegInf, 0.f};
+    if (lane < a.splits) stats = row_stats<D>(a, rows_of_tile)[part_row + int64_t(lane) * rows_of_tile];
+    const float m = stats[0], ls = stats[1];
     float top = m;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
@@ -1224,7 +1228,7 @@ __global__ __launch_bounds__(256) void cache_join_kernel(CacheAttnArgs a, int ro
             const int s = s0 + first + i * kParts;
             const float fs = __shfl(f, s & 63);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] = s < a.splits ? __builtin_fmaf(fs, u[i][e / 2][e % 2], o[e]) : o[e];
+            for (int e = 0; e < 4; ++e) o[e] = s < a.splits ? __builtin_fmaf(fs, u[i][e], o[e]) : o[e];
         }
     }
 #pragma unroll
