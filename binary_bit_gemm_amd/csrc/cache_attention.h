@@ -830,9 +830,9 @@ __device__ __forceinline__ uint16_t* o_row(const CacheAttnArgs& a, const CacheWo
 }
 
 // Few rows (decoded tokens): the waves take tiles in turn.
-template <int D, int BITS, int NB>
+template <int D, int BITS>
 __global__ __launch_bounds__(256, 2) void cache_attention_kernel(CacheAttnArgs a) {
-    constexpr int kWaves = 4, kRows = 16 * NB;
+    constexpr int NB = 1, kWaves = 4, kRows = 16;
     constexpr int kPitch = D + 4;  // floats of a row: neighbouring rows 4 banks apart
     __shared__ __attribute__((aligned(16))) float lds_o[kWaves][kRows * kPitch];
     __shared__ float lds_m[kWaves][kRows], lds_l[kWaves][kRows];  // e (-inf: no key), and the sum
@@ -1039,26 +1039,30 @@ __device__ __forceinline__ f32x2_t* row_stats(const CacheAttnArgs& a, int rows_o
     return reinterpret_cast<f32x2_t*>(a.part + int64_t(a.batch) * a.cache.heads * a.row_tiles * a.splits * rows_of_tile * D);
 }
 
-// Many rows (trees, chunks): the waves share the tiles, through LDS, and each takes its own 16 NB rows.  A turn is kTurn tiles; the
-// copies of the next turn's are on their way meanwhile.
-template <int D, int BITS, int NB, int WAVES>
-__global__ __launch_bounds__(64 * WAVES, 2) void cache_attention_rows_kernel(CacheAttnArgs a) {
+// Many rows (trees, chunks): tiles go through LDS.  Four waves take 16 NB rows each, and as many the same rows on every other tile, so that two
+// waves work on a SIMD and a tile is read from LDS four times; what the two have is added at the end.  A turn is kTurn tiles; the copies
+// of the next turn's are on their way meanwhile.
+template <int D, int BITS, int NB, int ROW_WAVES>
+__global__ __launch_bounds__(512, 2) void cache_attention_rows_kernel(CacheAttnArgs a) {
     using L = LdsTile<D, BITS>;
-    constexpr int kRows = 16 * NB * WAVES;
-    constexpr int kTurn = D == 128 && BITS == 16 && WAVES == 4 ? 2 : 4;  // so that two workgroups of 4 waves fit a compute unit
+    constexpr int kWaves = 8, kRowWaves = ROW_WAVES, kKeyWaves = kWaves / kRowWaves;
+    constexpr int kRows = 16 * NB * kRowWaves;
+    constexpr int kTurn = 4;
     constexpr int kPitch = D + 4;  // floats of a result's row: neighbouring rows 4 banks apart
     constexpr int kSlab = 16 * kPitch * 4;
-    constexpr int kBytes = kTurn * L::kBytes > WAVES * kSlab ? kTurn * L::kBytes : WAVES * kSlab;
+    constexpr int kBytes = kTurn * L::kBytes > kWaves * kSlab ? kTurn * L::kBytes : kWaves * kSlab;
     // an array per buffer: the compiler then sees that a tile's reads do not depend on the copies landing in the other
     __shared__ __attribute__((aligned(1024))) unsigned char buf0[kBytes], buf1[kTurn * L::kBytes];
+    __shared__ f32x2_t stats[kWaves][16];
     const int lane = int(threadIdx.x) & 63;
     const int wave = __builtin_amdgcn_readfirstlane(int(threadIdx.x >> 6));
     const int q = lane >> 4, l16 = lane & 15;
     CacheRange r;
     if (!cache_range(r, a, kRows)) return;
+    const int row_wave = wave % kRowWaves, key_wave = wave / kRowWaves;
     CacheWork at = r.at;  // of the wave's rows
-    at.row0 += 16 * NB * wave;
-    at.rows = at.rows - 16 * NB * wave;
+    at.row0 += 16 * NB * row_wave;
+    at.rows = at.rows - 16 * NB * row_wave;
     at.rows = at.rows < 0 ? 0 : at.rows < 16 * NB ? at.rows : 16 * NB;
     CacheRowsState<D, BITS, NB> w;
     RawQueries<D, BITS, NB> raw;
@@ -1082,14 +1086,14 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_attention_rows_kernel(Cac
             };
             constexpr int kAll = kTurn * L::kCopies;
 #pragma unroll
-            for (int j = 0; j < (kAll + WAVES - 1) / WAVES; ++j) {
-                const int c = wave + j * WAVES, i = c / L::kCopies, in_tile = c % L::kCopies;
-                if (kAll % WAVES == 0 || c < kAll) copy_words<D, BITS>(to + i * L::kBytes, a, in_tile, place(2 * i + in_tile / (L::kCopies / 4) % 2));
+            for (int j = 0; j < (kAll + kWaves - 1) / kWaves; ++j) {
+                const int c = wave + j * kWaves, i = c / L::kCopies, in_tile = c % L::kCopies;
+                if (kAll % kWaves == 0 || c < kAll) copy_words<D, BITS>(to + i * L::kBytes, a, in_tile, place(2 * i + in_tile / (L::kCopies / 4) % 2));
             }
             if constexpr (BITS != 16) {
 #pragma unroll
-                for (int j = 0; j < 4 * kTurn / WAVES; ++j) {
-                    const int c = wave + j * WAVES, i = c / 4;
+                for (int j = 0; j < 4 * kTurn / kWaves; ++j) {
+                    const int c = wave + j * kWaves, i = c / 4;
                     copy_scales<D, BITS>(to + i * L::kBytes, a, c % 4, place(2 * i + c % 2));
                 }
             }
@@ -1111,7 +1115,7 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_attention_rows_kernel(Cac
                 copy(other, of_next, ok_next, t + kTurn);
             }
 #pragma unroll 1
-            for (int i = 0; i < kTurn; ++i) {
+            for (int i = key_wave; i < kTurn; i += kKeyWaves) {
                 if (t + i >= r.t1) break;
                 const unsigned char* const tile = cur + i * L::kBytes;
                 TileWords<D, BITS> words;
@@ -1149,30 +1153,44 @@ __global__ __launch_bounds__(64 * WAVES, 2) void cache_attention_rows_kernel(Cac
         start_rows(w, raw, a);
     }
     __syncthreads();  // the buffers have been read
-    // 16 rows at a time through the wave's part of LDS, so that neighbouring lanes store neighbouring columns
-    float* const slab = reinterpret_cast<float*>(buf0 + wave * kSlab);
+    // 16 rows at a time through the wave's part of LDS, so that neighbouring lanes store neighbouring columns, and what the waves with other keys
+    // of these rows have is added
+    float* const slab = reinterpret_cast<float*>(buf0) + wave * (kSlab / 4);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
         const float l = row_sum(w.l[nb]);
-        const float f = a.splits > 1 ? 1.f : l == 0.f ? 0.f : 1.f / l;
-        each_o(w, nb, [&](int j, int i, float v) __attribute__((always_inline)) { slab[l16 * kPitch + o_column<D, BITS>(j, 4 * q + i)] = v * f; });
-        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0); the wave's own writes, so no barrier
-        asm volatile("" ::: "memory");
-        const int64_t part_row = int64_t(r.group_of * a.splits + r.split) * kRows + 16 * NB * wave + 16 * nb;
-        for (int item = lane; item < 16 * (D / 4); item += 64) {
+        each_o(w, nb, [&](int j, int i, float v) __attribute__((always_inline)) { slab[l16 * kPitch + o_column<D, BITS>(j, 4 * q + i)] = v; });
+        if (q == 0) stats[wave][l16] = f32x2_t{l != 0.f ? w.e[nb] : kNegInf, l};  // (a NaN goes along)
+        __syncthreads();
+        const int64_t part_row = int64_t(r.group_of * a.splits + r.split) * kRows + 16 * NB * row_wave + 16 * nb;
+        for (int item = 64 * key_wave + lane; item < 16 * (D / 4); item += 64 * kKeyWaves) {
             const int row = item / (D / 4), col = 4 * (item % (D / 4));
             if (16 * nb + row >= at.rows) break;  // rows only grow
-            const f32x4_t v = *reinterpret_cast<const f32x4_t*>(slab + row * kPitch + col);
+            f32x2_t of[kKeyWaves];
+            float e = kNegInf, sum = 0.f;
+#pragma unroll
+            for (int k = 0; k < kKeyWaves; ++k) {
+                of[k] = stats[row_wave + k * kRowWaves][row];
+                e = fmaxf(e, of[k][0]);
+            }
+            f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < kKeyWaves; ++k) {
+                const f32x4_t u = *reinterpret_cast<const f32x4_t*>(reinterpret_cast<const float*>(buf0) + (row_wave + k * kRowWaves) * (kSlab / 4) + row * kPitch + col);
+                const float f = of[k][0] == kNegInf ? 0.f : __builtin_amdgcn_exp2f(of[k][0] - e);
+                sum = __builtin_fmaf(f, of[k][1], sum);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] = __builtin_fmaf(f, u[i], v[i]);
+            }
             if (a.splits == 1) {
-                *reinterpret_cast<u32x2_t*>(o_row(a, at, 16 * nb + row) + col) = u32x2_t{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+                const float f = sum == 0.f ? 0.f : 1.f / sum;
+                *reinterpret_cast<u32x2_t*>(o_row(a, at, 16 * nb + row) + col) = u32x2_t{pack_bf16(v[0] * f, v[1] * f), pack_bf16(v[2] * f, v[3] * f)};
             } else {
                 *reinterpret_cast<f32x4_t*>(a.part + (part_row + row) * D + col) = v;
+                if (col == 0) row_stats<D>(a, kRows)[part_row + row] = f32x2_t{e, sum};
             }
         }
-        if (a.splits > 1 && q == 0 && 16 * nb + l16 < at.rows)  // e (a NaN goes along) and the sum
-            row_stats<D>(a, kRows)[part_row + l16] = f32x2_t{l != 0.f ? w.e[nb] : kNegInf, l};
-        __builtin_amdgcn_s_waitcnt(0xC07F);  // the slab's reads are done
-        asm volatile("" ::: "memory");
+        if (nb + 1 < NB) __syncthreads();
     }
 }
 
@@ -1244,19 +1262,15 @@ template <int D, int BITS>
 hipError_t launch_cache_attention_as(const CacheAttnArgs& a, const CacheAttnPlan& plan, hipStream_t stream) {
     const unsigned grid = unsigned(a.row_tiles) * unsigned(a.splits) * unsigned(a.cache.heads) * unsigned(a.batch);
     if (!plan.share_tiles) {
-        if (plan.tile_rows == 16)
-            hipLaunchKernelGGL((cache_attention_kernel<D, BITS, 1>), dim3(grid), dim3(256), 0, stream, a);
-        else
-            hipLaunchKernelGGL((cache_attention_kernel<D, BITS, 2>), dim3(grid), dim3(256), 0, stream, a);
+        hipLaunchKernelGGL((cache_attention_kernel<D, BITS>), dim3(grid), dim3(256), 0, stream, a);
         return hipGetLastError();
     }
-    const dim3 block(64 * plan.waves);
-    if (plan.tile_rows == 64)
-        hipLaunchKernelGGL((cache_attention_rows_kernel<D, BITS, 1, 4>), dim3(grid), block, 0, stream, a);
-    else if (plan.tile_rows == 128)
-        hipLaunchKernelGGL((cache_attention_rows_kernel<D, BITS, 1, 8>), dim3(grid), block, 0, stream, a);
+    if (plan.tile_rows == 32)
+        hipLaunchKernelGGL((cache_attention_rows_kernel<D, BITS, 1, 2>), dim3(grid), dim3(512), 0, stream, a);
+    else if (plan.tile_rows == 64)
+        hipLaunchKernelGGL((cache_attention_rows_kernel<D, BITS, 1, 4>), dim3(grid), dim3(512), 0, stream, a);
     else
-        hipLaunchKernelGGL((cache_attention_rows_kernel<D, BITS, 2, 8>), dim3(grid), block, 0, stream, a);
+        hipLaunchKernelGGL((cache_attention_rows_kernel<D, BITS, 2, 4>), dim3(grid), dim3(512), 0, stream, a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || a.splits == 1) return e;
     const int64_t rows = int64_t(a.batch) * a.cache.heads * a.row_tiles * plan.tile_rows;

@@ -13,7 +13,8 @@ hipError_t launch_cache_attention_16(const CacheAttnArgs& a, const CacheAttnPlan
 
 namespace {
 
-constexpr int kTileKeys = 32, kMostSplits = 64;
+constexpr int kTileKeys = 32;
+constexpr int64_t kMostSplits = 64;
 
 // Few rows (up to 32): one workgroup per compute unit at most, of four tiles of 32 keys at least (a tile a wave; 16 bits, whose tiles are larger:
 // two), and past 12 ranges (24) of eight (four), since a join costs about 2 us: none below 16 tiles.  Measured, one token, 8 kv heads of 128, 8 bits
@@ -28,33 +29,28 @@ int64_t few_splits(int64_t groups, int64_t tiles, int bits) {
     return splits < most ? splits : most;
 }
 
-// Many rows, `rows` of a workgroup: an estimate (us) fitted to trees of 12, 27 and 64 tokens over 300 to 4000 keys, one and four requests of 32 / 8
-// heads: a start, a time per tile, and for ranges the join with its parts' way through memory.  It serves to choose: over those shapes the choice
-// is within 10% of the best of the three.  Measured (64 / 128 / 256 rows, us): 64 tokens, heads of 128, 8 bits: one request of 300 keys 15 / 16 / 21,
-// four of 1000 32 / 29 / 35, four of 4000 63 / 48 / 45.  More workgroups than compute units are not split further: two of 64 rows on one unit, 64
-// tokens over 4000 keys in 16 ranges rather than 8, took 31 us for 27.
-double many_us(int rows, int head_dim, int64_t groups, int64_t tiles, int64_t splits) {
-    const bool wide = head_dim == 128;
-    const double start = rows == 64 ? 7 : rows == 128 ? 11 : 16;
-    const double tile = rows == 64 ? (wide ? 0.95 : 0.74) : rows == 128 ? (wide ? 1.0 : 0.84) : (wide ? 1.35 : 1.17);
-    const double wgs = double(groups) * double(splits), turns = wgs / kComputeUnits;
-    const double load = turns <= 1 ? 1 : rows == 64 ? 0.8 * turns : double(int64_t(turns + 0.999));  // two of 64 rows share a unit
-    const double join = splits > 1 ? 3.5 + wgs * rows * (head_dim + 2) * 8 / 8e6 : 0;
-    return start + double(tiles_of(tiles, splits)) * tile * (load < 1 ? 1 : load) + join;
+// Many rows: one workgroup per compute unit at most, of two tiles at least, where that takes eight tiles or more off each; otherwise the join (3.5 us
+// and the parts' way through memory) costs more than it saves.  Measured, trees of 12 over 300 keys, 8 kv heads of 128, 8 bits (us by ranges) 1:
+// 12.4, 5: 10.8; of 64 over 4000 keys 2: 36, 4: 26, 8: 20.6.
+int64_t many_splits(int64_t groups, int64_t tiles) {
+    int64_t splits = kComputeUnits / groups;
+    splits = splits < tiles / 2 ? splits : tiles / 2;
+    splits = splits < kMostSplits ? splits : kMostSplits;
+    return splits > 1 && tiles - tiles_of(tiles, splits) >= 8 ? splits : 1;
 }
 
 }  // namespace
 
 // may_split false: no workspace to split with.
-//   LOWBIT_CACHE_ATTENTION=few|many64|many128|many256 in the environment forces the kernel (A/B runs and tests).
+//   LOWBIT_CACHE_ATTENTION=few|many32|many64|many128 in the environment forces the kernel (A/B runs and tests).
 CacheAttnPlan plan_cache_attention(const CacheAttnArgs& a, bool may_split) {
     CacheAttnPlan p{};
     const int64_t rows = int64_t(a.q_len) * a.group, heads = int64_t(a.batch) * a.cache.heads, tiles = tiles_of(a.kv_len, kTileKeys);
-    p.share_tiles = rows > 32;
+    p.share_tiles = rows > 16;
     int only = 0;
     if (const char* force = std::getenv("LOWBIT_CACHE_ATTENTION")) {
         if (std::strcmp(force, "few") == 0) p.share_tiles = false;
-        for (const int r : {64, 128, 256})
+        for (const int r : {32, 64, 128})
             if (std::strncmp(force, "many", 4) == 0 && std::atoi(force + 4) == r) {
                 p.share_tiles = true;
                 only = r;
@@ -62,28 +58,22 @@ CacheAttnPlan plan_cache_attention(const CacheAttnArgs& a, bool may_split) {
     }
     int64_t splits = 1;
     if (!p.share_tiles) {
-        p.tile_rows = rows <= 16 ? 16 : 32;
-        p.waves = 4;
+        p.tile_rows = 16;
         if (may_split && heads * tiles_of(rows, p.tile_rows) > 0) splits = few_splits(heads * tiles_of(rows, p.tile_rows), tiles, a.cache.bits);
     } else {
-        double best = 0;
-        for (const int r : {64, 128, 256}) {
-            if (only != 0 ? r != only : r > 64 && rows <= r / 2) continue;
-            const int64_t groups = heads * tiles_of(rows, r);
-            for (const int64_t s : {1, 2, 3, 4, 6, 8, 10, 12, 16, 20, 24, 32, 40, 48, 64}) {
-                if (s > 1 && (!may_split || s > tiles || groups * s > kComputeUnits)) break;
-                const double us = many_us(r, a.cache.head_dim, groups, tiles, s);
-                if (p.tile_rows == 0 || us < best) {
-                    best = us;
-                    p.tile_rows = r;
-                    splits = s;
-                }
-            }
+        // 128 rows of a workgroup read a tile from LDS for twice the rows; 64 start and end sooner: 128 where 64 would have more than 20 tiles.
+        // Measured (64 / 128 rows, us; 8 kv heads of 128, 8 bits; in brackets tiles of a workgroup of 64): 64 tokens, one request of 4000 keys
+        // [16] 20.6 / 21.7, four of 1000 [16] 23.7 / 25.2, four of 4000 [63] 51 / 45; 27 tokens in 4 bits, heads of 64, three of 8191 [26] 22.3 / 19.4.
+        p.tile_rows = only == 32 || (only == 0 && rows <= 32) ? 32 : 64;
+        const int64_t groups = heads * tiles_of(rows, p.tile_rows);
+        splits = may_split && groups > 0 ? many_splits(groups, tiles) : 1;
+        if (only != 0 ? only == 128 : rows > 64 && tiles_of(tiles, splits) > 20) {
+            p.tile_rows = 128;
+            splits = may_split && groups > 0 ? many_splits(heads * tiles_of(rows, 128), tiles) : 1;
         }
-        p.waves = p.tile_rows == 64 ? 4 : 8;
     }
     p.row_tiles = int(tiles_of(rows, p.tile_rows));
-    p.splits = splits < 1 ? 1 : splits < kMostSplits ? int(splits) : kMostSplits;
+    p.splits = splits < 1 ? 1 : splits < kMostSplits ? int(splits) : int(kMostSplits);
     const int64_t parts = heads * p.row_tiles * p.splits * p.tile_rows;
     p.bytes = p.splits > 1 ? kWorkspaceCounterBytes + size_t(parts) * (size_t(a.cache.head_dim) + 2) * 4u : 0;
     return p;
@@ -100,7 +90,7 @@ hipError_t launch_cache_attention(CacheAttnArgs a, const CacheAttnPlan& plan, vo
     if (e == hipSuccess && trace_enabled())
         std::fprintf(stderr, "lowbit: cache_attention %s rows=%d splits=%d grid=%lld block=%d problem=%dx%dx%dx%d kv_heads=%d dim=%d bits=%d page=%d%s\n",
                      plan.share_tiles ? "many" : "few", plan.tile_rows, a.splits,
-                     (long long)(int64_t(a.row_tiles) * a.splits * a.cache.heads * a.batch), 64 * plan.waves, a.batch, a.q_len, a.kv_len, a.cache.heads * a.group, a.cache.heads, a.cache.head_dim, a.cache.bits, 1 << a.cache.page_shift,
+                     (long long)(int64_t(a.row_tiles) * a.splits * a.cache.heads * a.batch), plan.share_tiles ? 512 : 256, a.batch, a.q_len, a.kv_len, a.cache.heads * a.group, a.cache.heads, a.cache.head_dim, a.cache.bits, 1 << a.cache.page_shift,
                      a.tree != nullptr ? " tree" : "");
     return e;
 }

@@ -257,8 +257,7 @@ struct CacheAttnArgs {
 };
 struct CacheAttnPlan {
     bool share_tiles;  // many rows: the waves share the tiles and split the rows; few: the other way round
-    int tile_rows;     // of a workgroup: 16 or 32 (few), 64, 128 or 256 (many)
-    int waves;         // of a workgroup: 4, or 8 with 128 rows or more
+    int tile_rows;     // of a workgroup: 16 or 32 (few), 64 or 128 (many)
     int row_tiles, splits;
     size_t bytes;  // of workspace (0: none)
 };

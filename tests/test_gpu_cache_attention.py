@@ -119,9 +119,9 @@ def problem_of(lens, q_lens, hq, hk, dim, bits, page, tree=None, seed=0):
     return Problem(lens, q_lens, hq, hk, dim, bits, page, tree=tree, seed=seed)
 
 
-@pytest.fixture(params=["few", "many64", "many128", "many256", "auto"])
+@pytest.fixture(params=["few", "many32", "many64", "many128", "auto"])
 def kernel(request, monkeypatch):
-    """Each of the kernels in turn (many rows: 64, 128 and 256 per workgroup), and the one that the library takes."""
+    """Each of the kernels in turn (many rows: 32, 64 and 128 per workgroup), and the one that the library takes."""
     if request.param != "auto":
         monkeypatch.setenv("LOWBIT_CACHE_ATTENTION", request.param)
     return request.param
