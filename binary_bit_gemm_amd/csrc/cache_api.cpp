@@ -6,7 +6,7 @@
 
 #include "../../include/lowbit.h"
 #include "host_checks.h"
-#include "lowbit_internal.h"
+#include "decode_internal.h"
 
 namespace {
 

@@ -1,11 +1,12 @@
 // Attention of new or drafted tokens over a paged, quantised cache: O = softmax(scale * Q K^T over the allowed keys) V.
 //
-// Row r of a kv head's problem is new token r / G of its q head r % G (G q heads share a kv head).  A workgroup takes 16 NB
-// rows and a range of the keys; its four waves take tiles of 32 keys in turn, each with its own running maximum and sums, joined at the
-// end (in wave order, then the key ranges in order: results do not depend on timing).
+// Row r of a kv head's problem is new token r / G of its q head r % G (G q heads share a kv head).  A workgroup takes a tile of the rows
+// and a range of the keys; its waves take tiles of 32 keys with their own running maximum and sums, joined at the
+// end (in wave order, then the key ranges in order: results do not depend on timing).  Two kernels, chosen in cache_attention.hip:
+//   up to 16 rows: codes go from memory straight into the registers that the matrix cores read, two tiles of a wave on their way;
+//   more: tiles go through LDS, read by as many waves as have rows.
 //
-// Codes go from memory straight into the registers that the matrix cores read, without LDS: the cache's layout
-// (kv_cache.h) is the operands' layout.  The products are computed transposed, S^T = K Q^T and O^T = V^T P^T, on 16x16x32
+// The cache's layout (kv_cache.h) is the operands' layout.  The products are computed transposed, S^T = K Q^T and O^T = V^T P^T, on 16x16x32
 // MFMAs: lane (q, l16) then holds scores of query row l16 for keys 4q .. 4q + 3 of each 16, and the probabilities
 // are already the second product's operand for its own keys.
 //   * A code is never converted: 8 or 4 bits between zeros are an fp16 subnormal, code * 2^-24 (or, 4 bits higher, 16 times
@@ -26,8 +27,8 @@
 #pragma once
 
 #include "kv_cache.h"
-#include "lowbit_device.h"
-#include "lowbit_internal.h"
+#include "decode_device.h"
+#include "decode_internal.h"
 
 namespace lowbit {
 namespace {
@@ -829,7 +830,13 @@ __device__ __forceinline__ uint16_t* o_row(const CacheAttnArgs& a, const CacheWo
     return a.o + int64_t(at.b) * a.o_batch + int64_t(tok) * a.o_token + int64_t(at.hk * a.group + g) * a.o_head;
 }
 
-// Few rows (decoded tokens): the waves take tiles in turn.
+// Up to 16 rows (decoded tokens): the waves take tiles in turn.
+//
+// Bound by the cache's bytes where there are many, one wave's chain of latencies where there are few: a start of 2.5 us (lengths, then the
+// table, then the first tile, each waiting for the last), a microsecond a tile and wave, 3 to 5 us for the join of split ranges.  Page
+// numbers come by scalar loads, so that waiting for one leaves the tiles' loads in flight; a vector load's wait drains them.  8 kv heads of 128 (us, kernel
+// and launch): 77 keys 5.5; 61 requests of up to 2050 keys, 8 bits, 36, 4.5 TB/s; one of 40,007 keys in 4 bits 20.8, 10.5 of them in the loop
+// at 4.4 TB/s.
 template <int D, int BITS>
 __global__ __launch_bounds__(256, 2) void cache_attention_kernel(CacheAttnArgs a) {
     constexpr int NB = 1, kWaves = 4, kRows = 16;
@@ -1041,7 +1048,12 @@ __device__ __forceinline__ f32x2_t* row_stats(const CacheAttnArgs& a, int rows_o
 
 // Many rows (trees, chunks): tiles go through LDS.  Four waves take 16 NB rows each, and as many the same rows on every other tile, so that two
 // waves work on a SIMD and a tile is read from LDS four times; what the two have is added at the end.  A turn is kTurn tiles; the copies
-// of the next turn's are on their way meanwhile.
+// of the next turn's are on their way meanwhile, each wave-wide copy of 1 KB with neighbouring lanes on neighbouring 16 bytes.
+//
+// Bound by vector instructions at 4 bits (a score costs five, a weight six beside the exponential; matrix cores under a third) and by one wave's
+// chain through LDS, matrix cores and exponentials otherwise: two waves of a SIMD overlap about half of it.  Eight waves with rows of their own (128 or
+// 256 rows) read each tile twice as often and wrote twice the parts: trees of 64 over 4 x 4099 keys in 16 bits 41.4 us, here 40; of 27 over
+// 3 x 8191 in 4 bits 21.9, here 19.4; of 64 over 4000 in 8 bits 27.5, here 20.5.  Reading the next tile's keys before this tile's exponentials gained nothing.
 template <int D, int BITS, int NB, int ROW_WAVES>
 __global__ __launch_bounds__(512, 2) void cache_attention_rows_kernel(CacheAttnArgs a) {
     using L = LdsTile<D, BITS>;

@@ -3,7 +3,7 @@
 #include <cstdlib>
 #include <cstring>
 
-#include "lowbit_internal.h"
+#include "decode_internal.h"
 
 namespace lowbit {
 
@@ -16,7 +16,7 @@ namespace {
 constexpr int kTileKeys = 32;
 constexpr int64_t kMostSplits = 64;
 
-// Few rows (up to 32): one workgroup per compute unit at most, of four tiles of 32 keys at least (a tile a wave; 16 bits, whose tiles are larger:
+// Up to 16 rows: one workgroup per compute unit at most, of four tiles of 32 keys at least (a tile a wave; 16 bits, whose tiles are larger:
 // two), and past 12 ranges (24) of eight (four), since a join costs about 2 us: none below 16 tiles.  Measured, one token, 8 kv heads of 128, 8 bits
 // (us by ranges): 300 keys 1: 7.1; 700 keys 1: 9.2, 6: 8.6; 1500 keys 3: 10.7, 12: 9.2, 16: 9.4; 3000 keys 7: 10.8, 12: 10.0, 32: 10.8; 16 bits 1500
 // keys 3: 14.7, 24: 10.5.

@@ -195,11 +195,6 @@ __device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t rs, void* lds_wave_
                                             soff, 0, 0);
 }
 
-// The same with 4 bytes a lane (at lds_wave_base + 4 * i).
-__device__ __forceinline__ void dma4(__amdgpu_buffer_rsrc_t rs, void* lds_wave_base, uint32_t voff, int soff) {
-    __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)lds_wave_base, 4, voff, soff, 0, 0);
-}
-
 // Which 16-byte chunk of a row's K run lane quarter q holds for 16x16x32 MFMA ks (any order will do that both operands
 // share): the quarters of lanes l and l + 16 then read one 32-byte block.
 __device__ __forceinline__ int k_chunk(int ks, int q) { return 8 * (ks / 2) + 4 * (q >> 1) + (q & 1) + 2 * (ks % 2); }

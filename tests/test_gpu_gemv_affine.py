@@ -92,3 +92,58 @@ def test_no_rows_and_no_elements():
     r = torch.randn(2, 32).bfloat16().cuda()
     assert (lb.gemv_affine(none, w[:, :0].contiguous(), e, e, 64) == 0).all()
     assert torch.equal(lb.gemv_affine(none, w[:, :0].contiguous(), e, e, 64, residual=r), r)
+
+
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("M,N,K,g", [(3, 48, 192, 64), (16, 32, 64, 64), (5, 32, 1088, 64), (9, 64, 256, 128), (1, 32, 320, 64)])
+def test_infinities_and_nan_stay_in_their_row_and_column(M, N, K, g, swiglu):
+    """A NaN in a row of X reaches that row of Y, one in a weight row's last scale that column: a K that ends inside a step, whose
+    reads go past the row, included."""
+    x, levels, w, s, b = make(M, 2 * N if swiglu else N, K, g, seed=2)
+    clean = lb.gemv_affine(x, w, s, b, g, swiglu=swiglu)
+    x[M - 1, K - 1] = float("nan")
+    s[N - 2, -1] = float("inf")
+    b[5, 0] = float("nan")
+    s[7, 0] = float("nan")
+    got = lb.gemv_affine(x, w, s, b, g, swiglu=swiglu)
+    rows, cols = torch.ones(M, dtype=torch.bool), torch.ones(N, dtype=torch.bool)
+    rows[M - 1] = False
+    cols[[5, 7, N - 2]] = False
+    assert torch.equal(got[rows.cuda()][:, cols.cuda()], clean[rows.cuda()][:, cols.cuda()])
+    assert got[M - 1].isnan().all() and got[:, [5, 7]].isnan().all() and not got[:, N - 2].isfinite().any()
+
+
+def test_captured_and_on_another_stream():
+    """A graph of gate, up and down products replayed with new inputs and eager work between, and the same on a stream of one's own."""
+    M, K, N, g = 3, 256, 320, 64
+    x, _, w1, s1, b1 = make(M, 2 * N, K, g, seed=3)
+    _, _, w2, s2, b2 = make(1, K, N, g, seed=4)
+    step = lambda x: lb.gemv_affine(lb.gemv_affine(x, w1, s1, b1, g, swiglu=True), w2, s2, b2, g, residual=x)  # noqa: E731
+    step(x)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(x)
+    stream = torch.cuda.Stream()
+    for i in range(4):
+        x.copy_(torch.randn(M, K, generator=torch.Generator().manual_seed(20 + i)).bfloat16())
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, step(x))
+        with torch.cuda.stream(stream):
+            stream.wait_stream(torch.cuda.default_stream())
+            other = step(x)
+        torch.cuda.synchronize()
+        assert torch.equal(other, out)
+
+
+@pytest.mark.parametrize("M,swiglu,residual", [(1, False, False), (7, True, False), (16, False, True)])
+def test_launch_log(M, swiglu, residual, capfd, monkeypatch):
+    x, _, w, s, b = make(M, 96 if swiglu else 48, 256, 64)
+    r = torch.zeros(M, 48, dtype=torch.bfloat16, device="cuda") if residual else None
+    monkeypatch.setenv("LOWBIT_TRACE", "1")
+    capfd.readouterr()
+    lb.gemv_affine(x, w, s, b, 64, swiglu=swiglu, residual=r)
+    torch.cuda.synchronize()
+    lines = [t for t in capfd.readouterr().err.splitlines() if t.startswith("lowbit: gemv_affine ")]
+    assert len(lines) == 1 and f"problem={M}x48x256" in lines[0] and lines[0].endswith("swiglu" if swiglu else "residual" if residual else "x256")
