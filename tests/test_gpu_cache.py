@@ -159,3 +159,24 @@ def test_nothing_to_do():
     x = rows(3, 2, 64)
     lb.cache_write(empty, x, x, torch.zeros(3, dtype=torch.int32, device="cuda"))
     assert (lb.cache_read(empty, torch.zeros(3, dtype=torch.int32, device="cuda"))[0] == 0).all()
+
+
+@pytest.mark.parametrize("bits", [4, 8])
+def test_more_rows_than_one_grid(bits):
+    """A head per 4099 and more blocks of tokens than workgroups are launched for: each takes several turns."""
+    tokens, heads, dim, page = 8300, 4099, 64, 16
+    pages = -(-tokens // page)
+    assert -(-tokens // 32) * heads > 1 << 20
+    one = rows(tokens, 1, dim, 12)
+    slots = torch.arange(tokens, dtype=torch.int32, device="cuda")
+    cache = lb.kv_cache(pages, heads, dim, bits, page)
+    lb.cache_write(cache, one.expand(-1, heads, -1), one.flip(0).contiguous().expand(-1, heads, -1), slots)
+    want = [read_back(x, bits) for x in (one, one.flip(0))]
+    for at in (torch.arange(40), torch.arange(tokens - 40, tokens), torch.randint(0, tokens, (40,), generator=torch.Generator().manual_seed(1))):
+        for got, w in zip(lb.cache_read(cache, at.to(torch.int32).cuda()), want):
+            assert (got == got[:, :1]).all()
+            same(got[:, :1], w[at])
+    out = torch.zeros(tokens, heads, dim, dtype=torch.bfloat16, device="cuda")
+    k, _ = lb.cache_read(cache, slots, k_out=out, v_out=torch.zeros_like(out))
+    assert (k == k[:, :1]).all()
+    same(k[:, :1], want[0])

@@ -321,3 +321,22 @@ def test_refusals_of_the_binding():
     long = torch.zeros(1, 65, 4, 64, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(lb.LowbitError):
         lb.cache_attention(long, p.cache, p.table, lens, tree=torch.ones(1, 65, dtype=torch.int64, device="cuda"))
+
+
+@pytest.mark.parametrize("bits", [4, 8, 16])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_nan_and_infinities_in_queries_stay_in_their_row(dim, bits, kernel):
+    p = Problem([150], [6], 4, 2, dim, bits, 16, seed=31)
+    whole = p.q.clone()
+    p.q[0, 1, 2, 3] = NAN
+    p.q[0, 4, 0, 0] = INF
+    got = p.call()
+    assert got[0, 1, 2].isnan().all() and not got[0, 4, 0].isfinite().any()
+    got[0, 1, 2], got[0, 4, 0] = 0, 0
+    p.q = whole
+    clean = p.call()
+    p.check(clean)
+    clean[0, 1, 2], clean[0, 4, 0] = 0, 0
+    for b, h in [(0, h) for h in range(4)]:
+        bound = torch.from_numpy(p.wanted(1 / math.sqrt(dim))[b, h][1]).cuda()
+        assert ((got[b, :, h].double() - clean[b, :, h].double()).abs() <= 2 * bound).all()  # both lie within their bounds of the formula
