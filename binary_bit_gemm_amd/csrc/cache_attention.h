@@ -38,7 +38,6 @@ typedef _Float16 f16x8_t __attribute__((__vector_size__(8 * sizeof(_Float16))));
 
 constexpr float kNegInf = -__builtin_inff();
 constexpr int kCacheTile = 32;      // keys of a wave's tile
-constexpr int kMaxCacheSplits = 64;  // a lane per split in the join
 constexpr float kMostWeight = 0x1p12f;    // of p s 2^-e: past it e moves
 constexpr float kMostProbability = 0x1p70f;   // of p 2^-e, which values of scale 0 do not bound: times their smallest value it stays in fp32
 constexpr float kCodeUnit = 0x1p24f;    // 1 / the value of code 1 as an fp16
@@ -835,7 +834,7 @@ __device__ __forceinline__ uint16_t* o_row(const CacheAttnArgs& a, const CacheWo
 // Bound by the cache's bytes where there are many, one wave's chain of latencies where there are few: a start of 2.5 us (lengths, then the
 // table, then the first tile, each waiting for the last), a microsecond a tile and wave, 3 to 5 us for the join of split ranges.  Page
 // numbers come by scalar loads, so that waiting for one leaves the tiles' loads in flight; a vector load's wait drains them.  8 kv heads of 128 (us, kernel
-// and launch): 77 keys 5.5; 61 requests of up to 2050 keys, 8 bits, 36, 4.5 TB/s; one of 40,007 keys in 4 bits 20.8, 10.5 of them in the loop
+// and launch): 77 keys 5.5; 61 requests of up to 2050 keys, 8 bits, 36, 4.5 TB/s; one of 40,007 keys in 4 bits 20.5, 10.5 of them in the loop
 // at 4.4 TB/s.
 template <int D, int BITS>
 __global__ __launch_bounds__(256, 2) void cache_attention_kernel(CacheAttnArgs a) {
@@ -975,68 +974,71 @@ __global__ __launch_bounds__(256, 2) void cache_attention_kernel(CacheAttnArgs a
     __syncthreads();
     if (!last_split) return;
     if (threadIdx.x == 0) __hip_atomic_store(&a.counters[group_of], 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    // (row, 4 columns) per thread, with the ranges shared out over `parts` threads where threads are left over; kAhead loads in flight,
-    // the first of them while the rows' factors are worked out
+    // (row, 4 columns) per thread, with the ranges shared out over `parts` threads where threads are left over, kAhead of a thread's on their way; every
+    // thread works out its ranges' factors itself
     constexpr int kAhead = 16;
     int parts = 1;
     while (parts < 8 && 2 * parts * items <= 64 * kWaves) parts *= 2;
     const int span = (a.splits + parts - 1) / parts;
     const int first_item = int(threadIdx.x) % items, part = int(threadIdx.x) / items;  // (threads past items * parts have nothing)
-    f32x4_t u[kAhead];
-    auto fetch = [&](int item, int s0, int s1) __attribute__((always_inline)) {
-        const uint32_t from = uint32_t(item / (D / 4)) * kPart + 16u * uint32_t(item % (D / 4));
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i)  // a range past the last reads as zeros
-            u[i] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(
-                                                   part_rs, s0 + i < s1 ? uint32_t((s0 + i) * kRows) * kPart + from : 0xFFFFFF00u, 0, kSc1));
-    };
     const int s_end = (part + 1) * span < a.splits ? (part + 1) * span : a.splits;
-    if (part < parts) fetch(first_item, part * span, s_end);
-    float* const factors = &lds_o[0][0];  // [rows][splits], then the sums [rows], then the parts' sums
-    float* const totals = factors + kRows * kMaxCacheSplits;
-    f32x4_t* const sums = reinterpret_cast<f32x4_t*>(totals + kRows);  // [threads]
-    static_assert(kRows * kMaxCacheSplits + kRows + 4 * 64 * kWaves <= kWaves * kRows * kPitch, "they fit the waves' results");
-    for (int row = wave; row < at.rows; row += kWaves) {  // a lane per range
-        const uint32_t from = uint32_t(lane * kRows + row) * kPart + 4u * D;
-        const bool in = lane < a.splits;
-        const float m = in ? __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(part_rs, from, 0, kSc1)) : kNegInf;
-        const float l = in ? __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(part_rs, from + 4u, 0, kSc1)) : 0.f;
-        float top = m;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-        const float f = m == kNegInf ? 0.f : __builtin_amdgcn_exp2f(m - top);
-        float sum = m == kNegInf ? 0.f : f * l;
-#pragma unroll
-        for (int d = 1; d < 64; d *= 2) sum += __shfl_xor(sum, d);
-        if (in) factors[row * kMaxCacheSplits + lane] = f;
-        if (lane == 0) totals[row] = sum;
-    }
-    __syncthreads();
+    f32x4_t* const sums = reinterpret_cast<f32x4_t*>(&lds_o[0][0]);             // [threads], then their (e, sum)
+    f32x2_t* const stats = reinterpret_cast<f32x2_t*>(sums + 64 * kWaves);
+    static_assert(6 * 64 <= kRows * kPitch, "they fit the waves' results");
     for (int item = first_item; item < items && part < parts; item += 64 * kWaves) {  // more than one turn only with one part
         const int row = item / (D / 4);
+        const uint32_t from = uint32_t(row) * kPart, col = 16u * uint32_t(item % (D / 4));
+        float top = kNegInf, l = 0.f;
         f32x4_t v = {0.f, 0.f, 0.f, 0.f};
         for (int s0 = part * span; s0 < s_end; s0 += kAhead) {
-            if (item != first_item || s0 != part * span) fetch(item, s0, s_end);
+            f32x4_t u[kAhead];
+            f32x2_t st[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {  // a range past the last reads as zeros
+                const uint32_t at_range = s0 + i < s_end ? uint32_t((s0 + i) * kRows) * kPart + from : 0xFFFFFF00u - kPart;
+                st[i] = __builtin_bit_cast(f32x2_t, __builtin_amdgcn_raw_buffer_load_b64(part_rs, at_range + 4u * D, 0, kSc1));
+                u[i] = __builtin_bit_cast(f32x4_t, __builtin_amdgcn_raw_buffer_load_b128(part_rs, at_range + col, 0, kSc1));
+            }
+            float most = top;
 #pragma unroll
             for (int i = 0; i < kAhead; ++i) {
-                const float f = s0 + i < s_end ? factors[row * kMaxCacheSplits + s0 + i] : 0.f;
+                st[i][0] = s0 + i < s_end ? st[i][0] : kNegInf;
+                most = fmaxf(most, st[i][0]);
+            }
+            const float old = top == kNegInf ? 0.f : __builtin_amdgcn_exp2f(top - most);
+            l *= old;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] *= old;
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i) {
+                const float f = st[i][0] == kNegInf ? 0.f : __builtin_amdgcn_exp2f(st[i][0] - most);
+                l = __builtin_fmaf(f, st[i][1], l);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(f, u[i][e], v[e]);
             }
+            top = most;
         }
-        if (parts == 1)
-            store4(row, 4 * (item % (D / 4)), v, totals[row]);
-        else
+        if (parts == 1) {
+            store4(row, 4 * (item % (D / 4)), v, l);
+        } else {
             sums[part * items + item] = v;
+            stats[part * items + item] = f32x2_t{top, l};
+        }
     }
     if (parts == 1) return;
     __syncthreads();
     if (int(threadIdx.x) < items) {
-        f32x4_t v = sums[first_item];
-        for (int i = 1; i < parts; ++i)
+        float top = kNegInf, l = 0.f;
+        for (int i = 0; i < parts; ++i) top = fmaxf(top, stats[i * items + first_item][0]);
+        f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < parts; ++i) {
+            const f32x2_t st = stats[i * items + first_item];
+            const float f = st[0] == kNegInf ? 0.f : __builtin_amdgcn_exp2f(st[0] - top);
+            l = __builtin_fmaf(f, st[1], l);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += sums[i * items + first_item][e];
-        store4(first_item / (D / 4), 4 * (first_item % (D / 4)), v, totals[first_item / (D / 4)]);
+            for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(f, sums[i * items + first_item][e], v[e]);
+        }
+        store4(first_item / (D / 4), 4 * (first_item % (D / 4)), v, l);
     }
 }
 
