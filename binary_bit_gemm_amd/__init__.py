@@ -824,8 +824,8 @@ def cache_attention(q, cache: KVCache, page_table, key_lens, q_lens=None, tree=N
     tokens' among them (cache_write puts them there first).  Every new token takes the keys before the new ones and, of those, the ones up to
     itself, or where bit i of tree[b, t] (int64 [batch, q_len], q_len <= 64) is set: a tree of drafted tokens, each with its
     ancestors and itself.  q_lens int32 [batch]: requests with fewer new tokens than q_len; rows of `out` past them are left as they
-    were (zeros where the output is made here).  kv_len: the most keys a request has in this call, if that is less than the table holds (it only
-    chooses how the keys are split).  scale: 1 / sqrt(head_dim) by default.
+    were (zeros where the output is made here).  kv_len: the most keys a request has in this call, if that is less than the table holds (it
+    chooses how the keys are split; a longer key_lens counts as kv_len).  scale: 1 / sqrt(head_dim) by default.
 
     `workspace`: an optional device tensor of at least cache_attention_workspace_size(q, cache, kv_len) bytes, zero-filled before its first use, with
     which few rows over many keys run split along the keys: pass one when decoding.  Reuse it between calls; do not
