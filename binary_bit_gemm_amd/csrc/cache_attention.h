@@ -3,7 +3,7 @@
 // Row r of a kv head's problem is new token r / G of its q head r % G (G q heads share a kv head).  A workgroup takes a tile of the rows
 // and a range of the keys; its waves take tiles of 32 keys with their own running maximum and sums, joined at the
 // end (in wave order, then the key ranges in order: results do not depend on timing).  Two kernels, chosen in cache_attention.hip:
-//   up to 16 rows: codes go from memory straight into the registers that the matrix cores read, two tiles of a wave on their way;
+//   up to 16 rows: codes go from memory straight into the registers that the matrix cores read;
 //   more: tiles go through LDS, read by as many waves as have rows.
 //
 // The cache's layout (kv_cache.h) is the operands' layout.  The products are computed transposed, S^T = K Q^T and O^T = V^T P^T, on 16x16x32
@@ -834,8 +834,8 @@ __device__ __forceinline__ uint16_t* o_row(const CacheAttnArgs& a, const CacheWo
 // Bound by the cache's bytes where there are many, one wave's chain of latencies where there are few: a start of 2.5 us (lengths, then the
 // table, then the first tile, each waiting for the last), a microsecond a tile and wave, 3 to 5 us for the join of split ranges.  Page
 // numbers come by scalar loads, so that waiting for one leaves the tiles' loads in flight; a vector load's wait drains them.  8 kv heads of 128 (us, kernel
-// and launch): 77 keys 5.5; 61 requests of up to 2050 keys, 8 bits, 36, 4.5 TB/s; one of 40,007 keys in 4 bits 20.5, 10.5 of them in the loop
-// at 4.4 TB/s.
+// and launch): 77 keys 5.4; 61 requests of up to 2050 keys, 8 bits, 34.8, 4.6 TB/s; one of 40,007 keys in 4 bits 19.3, half of them in the loop
+// at 4.5 TB/s.
 template <int D, int BITS>
 __global__ __launch_bounds__(256, 2) void cache_attention_kernel(CacheAttnArgs a) {
     constexpr int NB = 1, kWaves = 4, kRows = 16;
@@ -855,9 +855,9 @@ __global__ __launch_bounds__(256, 2) void cache_attention_kernel(CacheAttnArgs a
     RawQueries<D, BITS, NB> raw;
     load_queries(raw, a, at);
     int t = r.t0 + wave;
-    // A tile on its way or in work.  With 16 rows two of them: the next tile's loads run beside this one's work, and the registers of
-    // this one's keys (values) are loaded anew, for the tile after the next, as soon as its scores (products) are there.
-    constexpr int kSets = NB == 1 ? 2 : 1;
+    // A tile on its way or in work: its registers of keys (values) are loaded anew, for the wave's next tile, as soon as its scores (products) are
+    // there.  A second such set, two tiles on their way, cost more in registers than it hid: 4 bits, 40,007 keys 20.5 us, here 19.6; 8
+    // bits, 300 keys 7.1, here 6.7; 16 bits, whose tiles are larger and where it spilled, 1500 keys 10.6, here 9.4.
     struct Set {
         TileWords<D, BITS> k, v;
         KeyScales<D, BITS> ks, vs;
@@ -873,17 +873,14 @@ __global__ __launch_bounds__(256, 2) void cache_attention_kernel(CacheAttnArgs a
     };
     if (t < r.t1) {
         auto places = [&](int tile) __attribute__((always_inline)) { return tile_places(a, at, tile, r.end); };  // past the range: none
-        Set set[kSets];
-#pragma unroll
-        for (int i = 0; i < kSets; ++i) {
-            set[i].at = places(t + i * kWaves);
-            load_keys(set[i], set[i].at);
-            load_values(set[i], set[i].at);
-        }
-        Places ahead = places(t + kSets * kWaves);
+        Set s;
+        s.at = places(t);
+        load_keys(s, s.at);
+        load_values(s, s.at);
+        Places ahead = places(t + kWaves);
         start_rows(w, raw, a);
         const RowTokens<NB> rows = row_tokens<NB>(r, a, at);
-        auto step = [&](Set& s) __attribute__((always_inline)) {
+        do {
             TileScores<NB> x;
             TileWeights<D, BITS, NB> p;
             const bool whole = whole_tile(r, s.at, t);
@@ -902,16 +899,8 @@ __global__ __launch_bounds__(256, 2) void cache_attention_kernel(CacheAttnArgs a
             __builtin_amdgcn_sched_barrier(0);
             s.at = ahead;
             t += kWaves;
-            ahead = places(t + kSets * kWaves);
-        };
-        while (true) {
-            step(set[0]);
-            if (t >= r.t1) break;
-            if constexpr (kSets == 2) {
-                step(set[1]);
-                if (t >= r.t1) break;
-            }
-        }
+            ahead = places(t + kWaves);
+        } while (t < r.t1);
     } else {
         start_rows(w, raw, a);
     }

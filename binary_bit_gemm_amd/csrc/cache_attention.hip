@@ -18,12 +18,15 @@ constexpr int64_t kMostSplits = 64;
 
 // Up to 16 rows: one workgroup per compute unit at most, of four tiles of 32 keys at least (a tile a wave; 16 bits, whose tiles are larger:
 // two), and past 12 ranges (24) of eight (four), since a join costs about 2 us: none below 16 tiles.  Measured, one token, 8 kv heads of 128, 8 bits
-// (us by ranges): 300 keys 1: 7.1; 700 keys 1: 9.2, 6: 8.6; 1500 keys 3: 10.7, 12: 9.2, 16: 9.4; 3000 keys 7: 10.8, 12: 10.0, 32: 10.8; 16 bits 1500
-// keys 3: 14.7, 24: 10.5.
+// (us by ranges): 700 keys 1: 9.2, 6: 8.6; 1500 keys 3: 10.7, 12: 9.2, 16: 9.4; 3000 keys 7: 10.8, 12: 10.0, 32: 10.8; 16 bits 1500 keys 3: 14.7, 24:
+// 10.5 (all 0.3 to 1 us less since).
 int64_t few_splits(int64_t groups, int64_t tiles, int bits) {
     if (tiles < 16) return 1;
     const int64_t least = bits == 16 ? 2 : 4, small = bits == 16 ? 24 : 12;
     int64_t splits = kComputeUnits / groups;
+    // two on a unit at 4 bits, which keep vector units busier than memory, where ranges stay long and few: 16 requests of 6000 keys 30.1 us, 24.8
+    // with two; 8 of 4000 15.8, 14.5; one of 40,000 19.2, 19.5; at 8 bits 16 of 6000 33.7, 35.2
+    if (bits == 4 && splits <= 8 && tiles >= 28 * (splits < 1 ? 1 : splits)) splits = 2 * kComputeUnits / groups;
     splits = splits < tiles / least ? splits : tiles / least;
     const int64_t most = tiles / (2 * least) > small ? tiles / (2 * least) : small;
     return splits < most ? splits : most;
@@ -48,10 +51,10 @@ CacheAttnPlan plan_cache_attention(const CacheAttnArgs& a, bool may_split) {
     const int64_t rows = int64_t(a.q_len) * a.group, heads = int64_t(a.batch) * a.cache.heads, tiles = tiles_of(a.kv_len, kTileKeys);
     const int64_t few = may_split && heads > 0 ? few_splits(heads, tiles, a.cache.bits) : 1;
     // Up to 16 rows the kernel that feeds registers from memory starts and ends sooner and keeps more loads in flight; the one that shares tiles joins
-    // many ranges of many rows faster (a workgroup per four rows, not one for all), and has registers left at 16 bits.  Measured (us, few / many
-    // with 32 rows), 8 kv heads of 128: 8 bits, 4 rows over 16,000 keys 13.9 / 16.1, 32 requests of 4 rows over 4000 42 / 51, 16 rows over 2000
-    // 13.4 / 11.4, 12 over 16,000 18.3 / 16.4; 16 bits, 4 rows over 700 keys 9.9 / 10.2, over 3000 12.0 / 11.3, 16 over 2000 16.9 / 11.9.
-    p.share_tiles = rows > 16 || (rows > 8 && few > 8) || (a.cache.bits == 16 && (rows > 8 || tiles >= 64));
+    // many ranges of many rows faster (a workgroup per four rows, not one for all).  Measured (us, few / many with 32 rows), 8 kv heads of 128: 8 bits,
+    // 4 rows over 16,000 keys 13.9 / 16.1, 32 requests of 4 rows over 4000 42 / 51, 16 rows over 2000 13.4 / 11.4, 12 over 16,000 18.3 / 16.4; 16
+    // bits, 4 rows over 1500 keys 9.4 / 10.9, over 40,000 29.9 / 32.3, 16 over 2000 13.7 / 12.0, 12 over 16,000 21.0 / 20.4.
+    p.share_tiles = rows > 16 || (rows > 8 && few > 8);
     int only = 0;
     if (const char* force = std::getenv("LOWBIT_CACHE_ATTENTION")) {
         if (std::strcmp(force, "few") == 0) p.share_tiles = false;
