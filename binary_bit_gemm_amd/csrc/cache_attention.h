@@ -3,7 +3,7 @@
 // Row r of a kv head's problem is new token r / G of its q head r % G (G q heads share a kv head).  A workgroup takes a tile of the rows
 // and a range of the keys; its waves take tiles of 32 keys with their own running maximum and sums, joined at the
 // end (in wave order, then the key ranges in order: results do not depend on timing).  Two kernels, chosen in cache_attention.hip:
-//   up to 16 rows: codes go from memory straight into the registers that the matrix cores read;
+//   up to 16 rows of a workgroup: codes go from memory straight into the registers that the matrix cores read;
 //   more: tiles go through LDS, read by as many waves as have rows.
 //
 // The cache's layout (kv_cache.h) is the operands' layout.  The products are computed transposed, S^T = K Q^T and O^T = V^T P^T, on 16x16x32
@@ -829,7 +829,7 @@ __device__ __forceinline__ uint16_t* o_row(const CacheAttnArgs& a, const CacheWo
     return a.o + int64_t(at.b) * a.o_batch + int64_t(tok) * a.o_token + int64_t(at.hk * a.group + g) * a.o_head;
 }
 
-// Up to 16 rows (decoded tokens): the waves take tiles in turn.
+// 16 rows of a workgroup (decoded tokens, short caches): the waves take tiles in turn.
 //
 // Bound by the cache's bytes where there are many, one wave's chain of latencies where there are few: a start of 2.5 us (lengths, then the
 // table, then the first tile, each waiting for the last), a microsecond a tile and wave, 3 to 5 us for the join of split ranges.  Page

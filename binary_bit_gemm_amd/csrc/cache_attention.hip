@@ -49,12 +49,16 @@ int64_t many_splits(int64_t groups, int64_t tiles) {
 CacheAttnPlan plan_cache_attention(const CacheAttnArgs& a, bool may_split) {
     CacheAttnPlan p{};
     const int64_t rows = int64_t(a.q_len) * a.group, heads = int64_t(a.batch) * a.cache.heads, tiles = tiles_of(a.kv_len, kTileKeys);
-    const int64_t few = may_split && heads > 0 ? few_splits(heads, tiles, a.cache.bits) : 1;
+    const int64_t few_groups = heads * tiles_of(rows, 16);
+    const int64_t few = may_split && few_groups > 0 ? few_splits(few_groups, tiles, a.cache.bits) : 1;
     // Up to 16 rows the kernel that feeds registers from memory starts and ends sooner and keeps more loads in flight; the one that shares tiles joins
     // many ranges of many rows faster (a workgroup per four rows, not one for all).  Measured (us, few / many with 32 rows), 8 kv heads of 128: 8 bits,
     // 4 rows over 16,000 keys 13.9 / 16.1, 32 requests of 4 rows over 4000 42 / 51, 16 rows over 2000 13.4 / 11.4, 12 over 16,000 18.3 / 16.4; 16
     // bits, 4 rows over 1500 keys 9.4 / 10.9, over 40,000 29.9 / 32.3, 16 over 2000 13.7 / 12.0, 12 over 16,000 21.0 / 20.4.
-    p.share_tiles = rows > 16 || (rows > 8 && few > 8);
+    // Over short caches (32 tiles) it also takes more rows, 16 to a workgroup, up to two workgroups a unit: 64 rows over 300 keys 7.3 / 10.8, 256
+    // rows 7.4 / 11.4; four requests of 108 rows over 1000 keys 10.8 / 15.7; 16 of 108 over 300, 896 workgroups, 17.2 / 13.8.  Past that the two are
+    // within 10% of each other up to 2000 keys.
+    p.share_tiles = rows > 16 ? tiles > 32 || few_groups > 2 * kComputeUnits : rows > 8 && few > 8;
     int only = 0;
     if (const char* force = std::getenv("LOWBIT_CACHE_ATTENTION")) {
         if (std::strcmp(force, "few") == 0) p.share_tiles = false;
@@ -67,7 +71,7 @@ CacheAttnPlan plan_cache_attention(const CacheAttnArgs& a, bool may_split) {
     int64_t splits = 1;
     if (!p.share_tiles) {
         p.tile_rows = 16;
-        splits = rows <= 16 ? few : 1;
+        splits = few;
     } else {
         // 128 rows of a workgroup read a tile from LDS for twice the rows; 64 start and end sooner: 128 where 64 would have more than 20 tiles.
         // Measured (64 / 128 rows, us; 8 kv heads of 128, 8 bits; in brackets tiles of a workgroup of 64): 64 tokens, one request of 4000 keys

@@ -291,8 +291,8 @@ def test_a_workspace_too_small_is_not_used(kernel):
 
 
 @pytest.mark.parametrize("rows,keys,force,line", [
-    (1, 300, None, "few rows=16 splits=1 "), (1, 5000, None, "few rows=16 splits="), (5, 100, None, "many rows=32 splits=1 "),
-    (16, 500, None, "many rows=64 splits="), (64, 4000, None, "many rows="), (2, 100, "many128", "many rows=128 splits="), (40, 100, "few", "few rows=16 "),
+    (1, 300, None, "few rows=16 splits=1 "), (1, 5000, None, "few rows=16 splits="), (5, 100, None, "few rows=16 splits=1 "),
+    (16, 500, None, "few rows=16 splits="), (5, 2000, None, "many rows=32 splits="), (16, 2000, None, "many rows=64 splits="), (64, 4000, None, "many rows="), (2, 100, "many128", "many rows=128 splits="), (40, 100, "few", "few rows=16 "),
 ])
 def test_launch_log(rows, keys, force, line, capfd, monkeypatch):
     if force:
