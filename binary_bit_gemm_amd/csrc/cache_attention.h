@@ -20,7 +20,8 @@
 //   * Everything that a row sums (p, p s, p b) carries one factor 2^-e, which the division at the end takes out.  e is the largest score plus
 //     the power of two of its value's scale when it was last set, so that the weights p s lie in fp16's range; it
 //     stays as long as they are below 2^12 (which the tile's largest score and largest scale tell), and the sums with it.
-// 16-bit caches take the same path with bf16 operands and no scales.
+// 16-bit caches take the same path with bf16 operands and no scales; what divides a row is the sum of its rounded probabilities (a product with
+// ones), so that a row with one key, or one that outweighs all others, gives that key's value back.
 //
 // Rounding: p s to fp16 (2^-11 of each; 16 bits: p to bf16, 2^-8 of each) and O to bf16; all else is fp32.  fp16 holds 24 bits below its normal
 // range: a weight is off by 2^-25 of the row's largest at least, which shows only where one group's scales are 2^12 below the other's.
@@ -69,8 +70,8 @@ template <int D, int BITS, int NB>
 struct CacheRowsState {
     u32x4_t q[D / 32][NB];  // B operands (bf16, or fp16 times the row's power of two)
     f32x4_t o[D / 16][NB];  // O^T: lane (q, l16): row l16, columns column(j, 4q + i)
-    f32x4_t sum[NB];        // 8 bits: the sum of the rounded p s
-    float e[NB], l[NB];     // the row's exponent, the lane's own keys' sum of p 2^-e
+    f32x4_t sum[NB];        // 8 bits: the sum of the rounded p s; 16 bits: of the rounded p 2^-e
+    float e[NB], l[NB];     // the row's exponent, the lane's own keys' sum of p 2^-e (8 and 4 bits)
     uint32_t seen[NB];      // 1: the row has taken a key (e is 0 before)
     float low[NB][2];       // 4 bits: the lane's own keys' sum of p b 2^-e
     float gain[NB];         // scores in powers of two per unit of (scale * sum)
@@ -628,7 +629,7 @@ __device__ __forceinline__ void tile_weights(CacheRowsState<D, BITS, NB>& w, Til
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 y[kb][i] = __builtin_amdgcn_exp2f(x.s[kb][nb][i]);
-                w.l[nb] += y[kb][i];
+                if constexpr (BITS != 16) w.l[nb] += y[kb][i];
             }
 #pragma unroll
         for (int g = 0; g < kGroups; ++g)
@@ -655,8 +656,9 @@ __device__ __forceinline__ void tile_weights(CacheRowsState<D, BITS, NB>& w, Til
 // O += V^T P^T of a tile.
 template <int D, int BITS, int NB>
 __device__ __forceinline__ void tile_values(CacheRowsState<D, BITS, NB>& w, const TileWords<D, BITS>& v, const TileWeights<D, BITS, NB>& p) {
-    if constexpr (BITS == 8) {
-        const u32x4_t ones = {0x3C003C00u, 0x3C003C00u, 0x3C003C00u, 0x3C003C00u};
+    if constexpr (BITS != 4) {
+        constexpr uint32_t kOnes = BITS == 16 ? 0x3F803F80u : 0x3C003C00u;
+        const u32x4_t ones = {kOnes, kOnes, kOnes, kOnes};
 #pragma unroll
         for (int nb = 0; nb < NB; ++nb) w.sum[nb] = cache_mfma<BITS>(ones, p.p[nb][0], w.sum[nb]);
     }
@@ -802,6 +804,12 @@ __device__ __forceinline__ void trim_tile(CacheRowsState<D, BITS, NB>& w, TileSc
         }
 }
 
+// The sum that divides the lane's row in block nb (all lanes of the row have it).
+template <int D, int BITS, int NB>
+__device__ __forceinline__ float total_weight(const CacheRowsState<D, BITS, NB>& w, int nb) {
+    return BITS == 16 ? w.sum[nb][0] : row_sum(w.l[nb]);
+}
+
 // O of the lane's row in block nb: element [j][i], column o_column(j, 4q + i), as a number.
 template <int D, int BITS, int NB, class F>
 __device__ __forceinline__ void each_o(const CacheRowsState<D, BITS, NB>& w, int nb, F f) {
@@ -911,7 +919,7 @@ __global__ __launch_bounds__(256, 2) void cache_attention_kernel(CacheAttnArgs a
         each_o(w, nb, [&](int j, int i, float v) __attribute__((always_inline)) {
             lds_o[wave][(16 * nb + l16) * kPitch + o_column<D, BITS>(j, 4 * q + i)] = v;
         });
-        const float l = row_sum(w.l[nb]);
+        const float l = total_weight(w, nb);
         if (q == 0) {
             lds_m[wave][16 * nb + l16] = l != 0.f ? w.e[nb] : kNegInf;  // (a NaN goes along)
             lds_l[wave][16 * nb + l16] = l;
@@ -1161,7 +1169,7 @@ __global__ __launch_bounds__(512, 2) void cache_attention_rows_kernel(CacheAttnA
     float* const slab = reinterpret_cast<float*>(buf0) + wave * (kSlab / 4);
 #pragma unroll
     for (int nb = 0; nb < NB; ++nb) {
-        const float l = row_sum(w.l[nb]);
+        const float l = total_weight(w, nb);
         each_o(w, nb, [&](int j, int i, float v) __attribute__((always_inline)) { slab[l16 * kPitch + o_column<D, BITS>(j, 4 * q + i)] = v; });
         if (q == 0) stats[wave][l16] = f32x2_t{l != 0.f ? w.e[nb] : kNegInf, l};  // (a NaN goes along)
         __syncthreads();

@@ -470,7 +470,7 @@ int lowbit_cache_read(const lowbit_cache* cache, void* k, void* v, int64_t token
  *   A row that takes no key gets zeros.  Slots that no row takes may hold anything; a NaN in a key or value reaches the rows that take it,
  * an infinite value too (as an infinity or, where its weight underflows, a NaN).
  * Scores, softmax statistics and sums are fp32; a probability times its value's scale is rounded to fp16 (16 bits: the
- * probability to bf16) for the second product, O to bf16 once.  At 8 and 4 bits fp32's range holds what arises on the way for rows of V whose
+ * probability to bf16, and the sum that divides is of the rounded ones) for the second product, O to bf16 once.  At 8 and 4 bits fp32's range holds what arises on the way for rows of V whose
  * largest magnitudes lie between 2^-50 and 2^30 (or are 0), and scores inside it.  Deterministic.
  *   workspace  as for lowbit_attention: lowbit_cache_attention_workspace_size(problem) bytes (0: none), 16-byte aligned,
  *          zero-filled before its first use, shared by calls that do not run at once; with none or too little the keys are not split

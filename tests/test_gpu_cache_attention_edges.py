@@ -340,3 +340,21 @@ def test_nan_and_infinities_in_queries_stay_in_their_row(dim, bits, kernel):
     for b, h in [(0, h) for h in range(4)]:
         bound = torch.from_numpy(p.wanted(1 / math.sqrt(dim))[b, h][1]).cuda()
         assert ((got[b, :, h].double() - clean[b, :, h].double()).abs() <= 2 * bound).all()  # both lie within their bounds of the formula
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+def test_one_key_gives_its_value_back_at_16_bits(dim, kernel):
+    """Probabilities are divided by the sum of what they were rounded to: a row with one key, or with one whose score is past the others' by more than
+    fp32's range, has p v / p, two fp32 roundings away from the bf16 v, and so v itself."""
+    p = Problem([1, 1, 33, 2500], [1, 1, 1, 1], 8, 2, dim, 16, 16, seed=32)
+    at = {0: 0, 1: 0, 2: 20, 3: 1777}
+    for b, j in at.items():
+        p.k[b][:] = 0
+        for h in range(2):  # its head's queries all lie about along it, others score 0
+            p.q[b, 0, 4 * h:4 * h + 4] = (p.q[b, 0, 4 * h] * torch.tensor([1.0, 1.01, 1.3, 2.7], device="cuda")[:, None]).bfloat16()
+            p.k[b][j, h] = (p.q[b, 0, 4 * h].float().cpu() * 40).bfloat16()
+    p.write()
+    for ws in ("enough", None):
+        got = p.call(ws)
+        for b, j in at.items():
+            assert torch.equal(got[b, 0].cpu(), p.v[b][j].repeat_interleave(4, 0)), f"request {b}"
