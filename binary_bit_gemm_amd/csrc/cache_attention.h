@@ -765,9 +765,9 @@ __device__ __forceinline__ bool whole_tile(const CacheRange& r, const Places& pl
     return kCacheTile * (t + 1) <= r.first && place.ok0 && place.ok1;
 }
 
-// A tile with keys that some row leaves out or that are not there: their scores to -inf.  Scales of keys that are not there may be anything;
-// those of the others may be NaN (or infinite), which is for the rows that take the key alone, and zero in a product does not silence it: both
-// become zeros, and the sums of those rows NaN.
+// A tile with keys that some row leaves out or that are not there: their scores to -inf.  Scales (and smallest values) of keys that are not there
+// may be anything; those of the others may be NaN or infinite, which is for the rows that take the key alone, and zero in a product does not
+// silence it: both become zeros, and the sums of those rows NaN.
 template <int D, int BITS, int NB>
 __device__ __forceinline__ void trim_tile(CacheRowsState<D, BITS, NB>& w, TileScores<NB>& x, KeyScales<D, BITS>& vs, uint32_t live,
                                           const uint32_t (&allowed)[NB]) {
@@ -792,7 +792,9 @@ __device__ __forceinline__ void trim_tile(CacheRowsState<D, BITS, NB>& w, TileSc
                     uint32_t& word = vs.w[kb][BITS == 8 ? i / 2 : i * kGroups + g];
                     const int up = BITS == 8 && i % 2 ? 16 : 0;                       // the scale's half of the word
                     const uint32_t half = BITS == 4 ? ~0u : up != 0 ? 0xFFFF0000u : 0xFFFFu;  // what goes with it
-                    const uint32_t odd = (word & (0x7F80u << up)) == (0x7F80u << up) ? ~0u : 0u;
+                    bool no_number = (word & (0x7F80u << up)) == (0x7F80u << up);
+                    if constexpr (BITS == 4) no_number = no_number || (word & 0x7F800000u) == 0x7F800000u;
+                    const uint32_t odd = no_number ? ~0u : 0u;
                     word &= ~half | (taken_mask(there, kb, i) & ~odd);
 #pragma unroll
                     for (int nb = 0; nb < NB; ++nb) {

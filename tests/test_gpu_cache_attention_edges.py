@@ -358,3 +358,28 @@ def test_one_key_gives_its_value_back_at_16_bits(dim, kernel):
         got = p.call(ws)
         for b, j in at.items():
             assert torch.equal(got[b, 0].cpu(), p.v[b][j].repeat_interleave(4, 0)), f"request {b}"
+
+
+@pytest.mark.parametrize("low", [INF, -INF, NAN])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_smallest_values_that_are_not_finite_stay_with_the_rows_that_take_them(dim, low, kernel):
+    """4 bits: a drafted token that no row takes, whose slot holds anything (a scale that is a number, a smallest value that is none), and one that
+    some rows take: all others as if the two held zeros."""
+    nodes, n = 20, 73
+    tree = [t & ~(1 << 19) for t in random_tree(nodes, 6)]  # nobody takes token 19, not even itself
+    tree[9] |= 1 << 4
+    p = Problem([n], [nodes], 4, 2, dim, 4, 16, tree=[tree], seed=33)
+    base = n - nodes
+    for token in (4, 19):
+        key = base + token
+        slot = int(p.table[0, key // p.page]), key % p.page
+        p.cache.v_scales[slot[0], :, slot[1], :, 1] = low
+        if token == 19:
+            p.cache.k_scales[slot[0], :, slot[1], :, 1] = low
+    got = p.call()
+    none = p.call(workspace=None)
+    takes = np.array([(t >> 4) & 1 for t in tree], bool)
+    assert takes.any() and not takes.all()
+    for o in (got, none):
+        p.check(o, rows=lambda b: ~takes)
+        assert not o[0, torch.from_numpy(takes).cuda()].isfinite().any()
