@@ -16,7 +16,10 @@
 //     8 bits, codes u = c + 128:  sum q c = sum q u - 128 sum q, the second term being where the sums start from;
 //       sum p s c = sum p s u - 128 sum p s, with the same rounded p s (a product with ones).
 //     4 bits, x = s u + b per group: s (q.u) + b sum q for the scores, sum p s u + sum p b for the values (the latter in fp32).
-//   * Q is a power of two per row (2^14 over its largest exponent) times fp16: exact for bf16 elements down to 2^-28 of the largest.
+//   * Q is a power of two per row (2^14 over its largest exponent) times fp16: exact for bf16 elements down to 2^-28 of the largest (4 bits, every
+//     other pair, which carries 1/16: 2^-24).  What takes it back, scale * log2(e) * 2^(E + 10) for a largest exponent E, is one fp32 factor: finite
+//     while scale |q| is below 2^117, and with a key's scale while scale |q| |k| is.  A second factor for rows past that, behind a branch
+//     that all rows of a wave share, cost every call 1% (a loop of its own for such waves 2 to 6%, in registers).
 //   * Everything that a row sums (p, p s, p b) carries one factor 2^-e, which the division at the end takes out.  e is the largest score plus
 //     the power of two of its value's scale when it was last set, so that the weights p s lie in fp16's range; it
 //     stays as long as they are below 2^12 (which the tile's largest score and largest scale tell), and the sums with it.

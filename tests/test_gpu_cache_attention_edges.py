@@ -383,3 +383,20 @@ def test_smallest_values_that_are_not_finite_stay_with_the_rows_that_take_them(d
     for o in (got, none):
         p.check(o, rows=lambda b: ~takes)
         assert not o[0, torch.from_numpy(takes).cuda()].isfinite().any()
+
+
+@pytest.mark.parametrize("bits", [4, 8, 16])
+@pytest.mark.parametrize("q_scale,k_scale", [(2.0 ** 118, 2.0 ** -116), (2.0 ** 118, 2.0 ** -8), (2.0 ** -120, 2.0 ** 119)])
+def test_queries_near_the_ends_of_the_range(q_scale, k_scale, bits, kernel):
+    """Scale times the largest |q| (4.5 standard deviations and less) up to 2^117, with keys that make scores of ordinary size, or so large that one key
+    takes all; the largest |q| below 2^-117 (elements are kept out of bf16's subnormal range); then with a token of ordinary queries beside the large
+    ones, whose scores are tiny."""
+    p = Problem([400], [4], 4, 2, 128, bits, 64, seed=34)
+    away = lambda x, s: (x.float().sign() * x.float().abs().clamp(min=2.0 ** -5) * s).bfloat16()  # noqa: E731
+    p.q, p.k[0] = away(p.q, q_scale), away(p.k[0], k_scale)
+    p.write()
+    p.check(p.call())
+    p.answers.clear()
+    if q_scale > 1:
+        p.q[0, 2] = (p.q[0, 2].float() / q_scale).bfloat16()  # scores of 2^-119: every key the same
+        p.check(p.call())
