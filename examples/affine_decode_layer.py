@@ -71,6 +71,7 @@ class Requests:
         order = torch.randperm(count * each, generator=torch.Generator().manual_seed(seed))
         self.table = order.view(count, each).to(torch.int32).cuda()
         self.filled = torch.zeros(count, dtype=torch.int32, device="cuda")
+        self.drafted = {}  # request -> keys and values of the tokens that verify() last took
 
     def slots(self, request, index):
         """Slots of tokens `index` (int64 tensor) of requests `request` (the same shape, or one)."""
@@ -122,20 +123,23 @@ def decode(layer, requests, x, workspace, out=None):
 
 def verify(layer, requests, r, x, tree, depth, workspace):
     """x: bf16 [drafted, dim], drafted tokens of request r; tree: int64 [drafted], bit i for ancestor i and the token itself; depth: int32 [drafted].
-    Their rows of the stream; the request's length stays (the caller keeps the accepted ones)."""
+    Their rows of the stream; the request's length stays (the caller keeps the accepted ones, with keep())."""
     n = x.shape[0]
     q, k, v = project(layer, x, requests.filled[r] + depth, layer.qkv)
     slots = requests.slots(r, requests.filled[r].long() + torch.arange(n, device="cuda"))
     lb.cache_write(requests.cache, k, v, slots)
+    requests.drafted[r] = k, v
     mixed = lb.cache_attention(q[None], requests.cache, requests.table[r:r + 1], requests.filled[r:r + 1] + n, tree=tree[None], workspace=workspace)
     return finish(layer, x, mixed)
 
 
 def keep(requests, r, path):
-    """The accepted drafted tokens (a path of the tree, int64 indices) to where the request's next tokens belong: rows as they read back."""
-    first = requests.filled[r].long()
-    keys, values = lb.cache_read(requests.cache, requests.slots(r, first + path))
-    lb.cache_write(requests.cache, keys, values, requests.slots(r, first + torch.arange(len(path), device="cuda")))
+    """The accepted ones of the tokens that verify() last took (a path of the tree, int64 indices) to where the request's next tokens belong: their keys
+    and values are written there once more.  Codes depend on these alone, so the rows are those that verify() attended, to the bit; rows
+    read back and written again would be quantised a second time."""
+    keys, values = (x[path] for x in requests.drafted[r])
+    slots = requests.slots(r, requests.filled[r].long() + torch.arange(len(path), device="cuda"))
+    lb.cache_write(requests.cache, keys, values, slots)
     requests.filled[r] += len(path)
 
 

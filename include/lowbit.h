@@ -443,6 +443,8 @@ int lowbit_attention(const lowbit_attention_problem* problem, void* workspace, s
  * that row out.  The slots of one call that are inside must differ from each other.
  * lowbit_cache_read -- the rows at slots[t] as bf16 (rounded once at 8 bits; at 4 bits s u + b to fp32, then to bf16; slots may
  * repeat).  Rows whose slot is outside the cache are left as they were.
+ * Codes and scales depend on a row's elements alone, so a row written to two slots is the same in both; a row read back and written again at 8 or 4
+ * bits is quantised a second time.  Rows to be moved (accepted drafted tokens) are written again from the k and v that they came from.
  */
 typedef struct lowbit_cache {
     void *k, *v, *k_scales, *v_scales;

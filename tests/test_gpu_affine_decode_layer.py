@@ -113,3 +113,26 @@ def test_decoding_as_a_graph(bits):
         assert torch.equal(out, want[i])
         m.stored(graphed, 1, 600)
     assert torch.equal(graphed.filled, eager.filled)
+
+
+@pytest.mark.parametrize("bits", [4, 8, 16])
+def test_kept_drafts_hold_what_was_verified(bits):
+    """Rows of accepted drafted tokens, once moved to their places, are the rows that verify() attended, to the bit: quantised once, from the same keys
+    and values."""
+    m = load()
+    layer = m.Layer(256, 4, 2, 512, seed=9)
+    requests = m.Requests(layer, 2, 300, bits)
+    gen = torch.Generator(device="cuda").manual_seed(10)
+    rows = lambda n: torch.randn(n, 256, generator=gen, device="cuda").bfloat16()  # noqa: E731
+    ws = m.scratch(layer, requests, 13)
+    for r, n in enumerate((40, 129)):
+        m.prompt(layer, requests, r, rows(n))
+    for turn in range(2):
+        for r in range(2):
+            tree, depth, path = m.draft(13, seed=11 + 2 * r + turn)
+            n = int(requests.filled[r])
+            m.verify(layer, requests, r, rows(13), tree, depth, ws)
+            drafted = m.stored(requests, r, n + 13)
+            m.keep(requests, r, path)
+            for was, now in zip(drafted, m.stored(requests, r, n + len(path))):
+                assert torch.equal(now[:n], was[:n]) and torch.equal(now[n:], was[n:][path])
