@@ -464,6 +464,8 @@ def _workspace(workspace, like):
     """(address, bytes) of an optional workspace."""
     if workspace is None:
         return 0, 0
+    if not isinstance(workspace, _TORCH.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
     if workspace.get_device() != like.get_device() or not workspace.is_contiguous():
         if not workspace.is_cuda or not workspace.is_contiguous():
             raise ValueError("workspace must be a contiguous device tensor")
@@ -702,7 +704,7 @@ class KVCache:
 
 def _fits(t, dtype, dev: int) -> bool:
     """Whether t is a contiguous tensor of that type on that device."""
-    return t.__class__.__name__ != "NoneType" and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
+    return isinstance(t, _TORCH.Tensor) and t.dtype is dtype and t.get_device() == dev and t.is_contiguous()
 
 
 def kv_cache(pages: int, kv_heads: int, head_dim: int, bits: int = 8, page_size: int = 64, device="cuda") -> KVCache:
@@ -733,7 +735,13 @@ def _row_strides(t, name: str, shape, dev: int):
     return token if shape[0] > 1 else 0, head if shape[1] > 1 else 0
 
 
+def _require_cache(cache) -> None:
+    if not isinstance(cache, KVCache):
+        raise TypeError("cache must be a KVCache")
+
+
 def _cache_rows(function: str, cache: KVCache, k, v, slots) -> None:
+    _require_cache(cache)
     like = cache.k
     dev = like.get_device()
     at = _plain(slots, _torch().int32, "slots", 1, like)
@@ -757,6 +765,7 @@ def cache_read(cache: KVCache, slots, k_out=None, v_out=None):
     is outside the cache are left as they were (zeros where the output is made here)."""
     if k_out is None or v_out is None:
         torch = _torch()
+        _require_cache(cache)
         _plain(slots, torch.int32, "slots", 1, cache.k)
         shape = (slots.shape[0], cache.shape[1], cache.shape[3])
         k_out, v_out = (torch.zeros(shape, dtype=torch.bfloat16, device=cache.k.device) if t is None else t for t in (k_out, v_out))
@@ -768,6 +777,7 @@ def _cache_attention_problem(q, cache, page_table, key_lens, q_lens, tree, kv_le
     torch = _torch()
     int32 = torch.int32
     _heads(q, "q", 4)
+    _require_cache(cache)
     B, Lq, Hq, D = shape = q.shape
     _, _, page, dim = cache.shape
     dev = q.get_device()

@@ -400,3 +400,21 @@ def test_queries_near_the_ends_of_the_range(q_scale, k_scale, bits, kernel):
     if q_scale > 1:
         p.q[0, 2] = (p.q[0, 2].float() / q_scale).bfloat16()  # scores of 2^-119: every key the same
         p.check(p.call())
+
+
+def test_arguments_that_are_no_tensors_are_type_errors():
+    p = Problem([100], [2], 4, 2, 64, 8, 16, seed=39)
+    lens, c = ints([100]), p.cache
+    slots = ints([0, 1])
+    x = torch.zeros(2, 2, 64, dtype=torch.bfloat16, device="cuda")
+    for call in (lambda: lb.cache_attention(p.q, c, [[1]], lens), lambda: lb.cache_attention(p.q, c, p.table, [100]),
+                 lambda: lb.cache_attention(p.q, c, p.table, 100), lambda: lb.cache_attention(p.q, None, p.table, lens),
+                 lambda: lb.cache_attention(p.q, c.k, p.table, lens), lambda: lb.cache_attention(p.q, c, p.table, lens, workspace=4096),
+                 lambda: lb.cache_attention(p.q, c, p.table, lens, q_lens=[2]), lambda: lb.cache_attention(p.q, c, p.table, lens, tree=[[1, 3]]),
+                 lambda: lb.cache_attention(p.q, c, p.table, lens, out="q"), lambda: lb.cache_attention("q", c, p.table, lens),
+                 lambda: lb.cache_attention_workspace_size(p.q, c.k, 100), lambda: lb.KVCache(c.k, None, c.k_scales, c.v_scales),
+                 lambda: lb.KVCache(c.k, 5, c.k_scales, c.v_scales), lambda: lb.KVCache(c.k, c.v, [1.0], c.v_scales), lambda: lb.KVCache(c.k, c.v),
+                 lambda: lb.cache_write(c.k, x, x, slots), lambda: lb.cache_write(c, x, None, slots), lambda: lb.cache_write(c, x, x, [0, 1]),
+                 lambda: lb.cache_read(None, slots), lambda: lb.cache_read(c, [0, 1]), lambda: lb.cache_read(c, slots, k_out=3)):
+        with pytest.raises(TypeError):
+            call()
