@@ -785,11 +785,16 @@ def _cache_attention_problem(q, cache, page_table, key_lens, q_lens, tree, kv_le
         raise ValueError(f"q must be [batch, q_len, q_heads, {dim}], got {tuple(shape)}")
     if cache.k.get_device() != dev:
         raise ValueError(f"cache must be on {q.device}, got {cache.k.device}")
-    pt = pk = pq = ptree = po = pages = 0
+    pt = pk = pq = ptree = po = of_row = 0
     if page_table is not None:
-        pt = page_table.data_ptr() if _fits(page_table, int32, dev) and page_table.dim() == 2 else _plain(page_table, int32, "page_table", 2, q)
+        if not (isinstance(page_table, torch.Tensor) and page_table.dtype is int32 and page_table.dim() == 2 and page_table.get_device() == dev):
+            _plain(page_table, int32, "page_table", 2, q)
+        pt = page_table.data_ptr()
         pk = key_lens.data_ptr() if _fits(key_lens, int32, dev) and key_lens.dim() == 1 else _plain(key_lens, int32, "key_lens", 1, q)
         rows, pages = page_table.shape
+        of_row, of_page = page_table.stride()
+        if of_page != 1 and pages > 1:
+            raise ValueError("page_table must be contiguous along the pages")
         if rows != B or key_lens.shape[0] != B:
             raise ValueError(f"page_table must be [{B}, pages] and key_lens [{B}]")
         if kv_len is None:
@@ -818,7 +823,7 @@ def _cache_attention_problem(q, cache, page_table, key_lens, q_lens, tree, kv_le
         qt = ot = 0
     if Hq <= 1:
         qh = oh = 0
-    return _CACHE_ATTENTION_PROBLEM.pack(*cache._fields(), q.data_ptr(), po, pt, pk, pq, ptree, B, Lq, kv_len, qb, qt, qh, ob, ot, oh, pages, Hq,
+    return _CACHE_ATTENTION_PROBLEM.pack(*cache._fields(), q.data_ptr(), po, pt, pk, pq, ptree, B, Lq, kv_len, qb, qt, qh, ob, ot, oh, of_row if B > 1 else 0, Hq,
                                          scale if scale is not None else D ** -0.5)
 
 
@@ -830,11 +835,11 @@ def cache_attention_workspace_size(q, cache: KVCache, kv_len: int) -> int:
 def cache_attention(q, cache: KVCache, page_table, key_lens, q_lens=None, tree=None, kv_len: Optional[int] = None, scale=None, out=None,
                     workspace=None):
     """Attention of each request's last tokens over its keys and values in the cache, in bf16 (lowbit_cache_attention): q [batch, q_len,
-    q_heads, head_dim] (any strides of whole 16-byte pieces), page_table int32 [batch, pages of a request], key_lens int32 [batch]: keys, the new
-    tokens' among them (cache_write puts them there first).  Every new token takes the keys before the new ones and, of those, the ones up to
-    itself, or where bit i of tree[b, t] (int64 [batch, q_len], q_len <= 64) is set: a tree of drafted tokens, each with its
-    ancestors and itself.  q_lens int32 [batch]: requests with fewer new tokens than q_len; rows of `out` past them are left as they
-    were (zeros where the output is made here).  kv_len: the most keys a request has in this call, if that is less than the table holds (it
+    q_heads, head_dim] (any strides of whole 16-byte pieces), page_table int32 [batch, pages of a request] (rows at any stride, e.g. part of a wider
+    table), key_lens int32 [batch]: keys, the new tokens' among them (cache_write puts them there first).  Every new token takes the keys before
+    the new ones and, of those, the ones up to itself, or where bit i of tree[b, t] (int64 [batch, q_len], q_len <= 64) is set: a tree of drafted
+    tokens, each with its ancestors and itself.  q_lens int32 [batch]: requests with fewer new tokens than q_len; rows of `out` past them are left
+    as they were (zeros where the output is made here).  kv_len: the most keys a request has in this call, if that is less than the table holds (it
     chooses how the keys are split; a longer key_lens counts as kv_len).  scale: 1 / sqrt(head_dim) by default.
 
     `workspace`: an optional device tensor of at least cache_attention_workspace_size(q, cache, kv_len) bytes, zero-filled before its first use, with

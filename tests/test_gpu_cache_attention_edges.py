@@ -418,3 +418,23 @@ def test_arguments_that_are_no_tensors_are_type_errors():
                  lambda: lb.cache_read(None, slots), lambda: lb.cache_read(c, [0, 1]), lambda: lb.cache_read(c, slots, k_out=3)):
         with pytest.raises(TypeError):
             call()
+
+
+def test_part_of_a_wider_table(kernel):
+    """The first pages of every request's row of a table, and rows of a transposed one, which lie apart."""
+    p = Problem([200, 150], [2, 2], 4, 2, 64, 8, 16, seed=38)
+    want = p.call(workspace=None)
+    pages = p.table.shape[1]
+    wide = torch.full((2, pages + 9), -1, dtype=torch.int32, device="cuda")
+    wide[:, :pages] = p.table
+    lens = ints(p.lens)
+    assert torch.equal(lb.cache_attention(p.q, p.cache, wide[:, :pages], lens, kv_len=200), want)
+    assert torch.equal(lb.cache_attention(p.q[1:], p.cache, wide[1:, :pages], lens[1:], kv_len=200), want[1:])
+    every = torch.full((4, pages), -1, dtype=torch.int32, device="cuda")
+    every[::2] = p.table
+    assert torch.equal(lb.cache_attention(p.q, p.cache, every[::2], lens, kv_len=200), want)
+    both = p.q[:1].expand(2, -1, -1, -1)
+    one = lb.cache_attention(both, p.cache, p.table[:1].expand(2, -1), lens[:1].expand(2).contiguous(), kv_len=200)
+    assert torch.equal(one[0], one[1]) and torch.equal(one[:1], want[:1])
+    with pytest.raises(ValueError, match="page_table"):
+        lb.cache_attention(p.q, p.cache, p.table.t().contiguous().t(), lens, kv_len=200)
