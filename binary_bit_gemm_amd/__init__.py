@@ -656,6 +656,7 @@ def attention(q, k, v, key_mask=None, key_lens=None, causal: bool = False, q_sta
 
 # ---- decoding: a paged cache, attention over it, matrix-vector products ----
 
+CACHE_ATTENTION_WORKSPACE_BYTES = 17043456  # LOWBIT_CACHE_ATTENTION_WORKSPACE_BYTES: enough for every call
 _CACHE = struct.Struct("@4Pq4i0q")  # lowbit_cache of include/lowbit.h
 _CACHE_ATTENTION_PROBLEM = struct.Struct("@4Pq4i6P10qif0q")  # lowbit_cache_attention_problem
 
@@ -828,7 +829,8 @@ def _cache_attention_problem(q, cache, page_table, key_lens, q_lens, tree, kv_le
 
 
 def cache_attention_workspace_size(q, cache: KVCache, kv_len: int) -> int:
-    """Bytes of workspace that cache_attention can use for q and this many keys at most (0: none)."""
+    """Bytes of workspace that cache_attention can use for q and this many keys at most (0: none).  Fewer requests can use more (their keys
+    are split further): CACHE_ATTENTION_WORKSPACE_BYTES cover every call."""
     return int(lib().lowbit_cache_attention_workspace_size(_cache_attention_problem(q, cache, None, None, None, None, kv_len, None, None)))
 
 
@@ -843,8 +845,8 @@ def cache_attention(q, cache: KVCache, page_table, key_lens, q_lens=None, tree=N
     chooses how the keys are split; a longer key_lens counts as kv_len).  scale: 1 / sqrt(head_dim) by default.
 
     `workspace`: an optional device tensor of at least cache_attention_workspace_size(q, cache, kv_len) bytes, zero-filled before its first use, with
-    which few rows over many keys run split along the keys: pass one when decoding.  Reuse it between calls; do not
-    share it between calls that run concurrently."""
+    which few rows over many keys run split along the keys: pass one when decoding (one of CACHE_ATTENTION_WORKSPACE_BYTES where batches change).
+    Reuse it between calls; do not share it between calls that run concurrently."""
     if page_table is None or key_lens is None:
         raise TypeError("page_table and key_lens must be int32 tensors")
     if out is None:

@@ -3,6 +3,7 @@
 #include <cstdlib>
 #include <cstring>
 
+#include "../../include/lowbit.h"
 #include "decode_internal.h"
 
 namespace lowbit {
@@ -15,6 +16,8 @@ namespace {
 
 constexpr int kTileKeys = 32;
 constexpr int64_t kMostSplits = 64;
+// Split workgroups are at most one a compute unit, of 128 rows, or (4 bits) two of 16.
+static_assert(LOWBIT_CACHE_ATTENTION_WORKSPACE_BYTES == kWorkspaceCounterBytes + kComputeUnits * 128 * (128 + 2) * 4, "the largest plan");
 
 // Up to 16 rows: one workgroup per compute unit at most, of four tiles of 32 keys at least (a tile a wave; 16 bits, whose tiles are larger:
 // two), and past 12 ranges (24) of eight (four), since a join costs about 2 us: none below 16 tiles.  Measured, one token, 8 kv heads of 128, 8 bits

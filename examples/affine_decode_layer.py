@@ -181,10 +181,10 @@ def draft(tokens, seed=0):
 
 
 def scratch(layer, requests, rows):
+    """A workspace for one token of any number of requests, or any number of drafted tokens of one, up to `rows`."""
     q = torch.empty(rows, 1, layer.heads, 128, dtype=torch.bfloat16, device="cuda")
     capacity = requests.table.shape[1] * requests.cache.shape[2]
-    need = max(lb.cache_attention_workspace_size(q, requests.cache, capacity),
-               lb.cache_attention_workspace_size(q.transpose(0, 1), requests.cache, capacity))
+    need = max(lb.cache_attention_workspace_size(x, requests.cache, capacity) for n in range(1, rows + 1) for x in (q[:n], q[:n].transpose(0, 1)))
     return torch.zeros(max(need, 16), dtype=torch.uint8, device="cuda")
 
 

@@ -477,7 +477,8 @@ int lowbit_cache_read(const lowbit_cache* cache, void* k, void* v, int64_t token
  * 2^117 (past it the row can be NaN).  Deterministic.
  *   workspace  as for lowbit_attention: lowbit_cache_attention_workspace_size(problem) bytes (0: none), 16-byte aligned,
  *          zero-filled before its first use, shared by calls that do not run at once; with none or too little the keys are not split
- *          across workgroups.
+ *          across workgroups.  That size can grow as a batch shrinks (its keys are split further): a program whose batch changes keeps
+ *          LOWBIT_CACHE_ATTENTION_WORKSPACE_BYTES, which cover every call, or the largest size over the batches that it will have.
  * Meant for few new tokens; a prompt's long chunks go through lowbit_cache_read and lowbit_attention.
  * page_table, key_lens and q_lens need 4-byte alignment, tree 8, q, o and workspace 16.
  */
@@ -495,6 +496,7 @@ typedef struct lowbit_cache_attention_problem {
     float scale;
 } lowbit_cache_attention_problem;
 
+#define LOWBIT_CACHE_ATTENTION_WORKSPACE_BYTES 17043456
 size_t lowbit_cache_attention_workspace_size(const lowbit_cache_attention_problem* problem);
 int lowbit_cache_attention(const lowbit_cache_attention_problem* problem, void* workspace, size_t workspace_bytes, void* stream);
 

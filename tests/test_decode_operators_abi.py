@@ -175,3 +175,21 @@ def test_under_sanitizers():
     out = r.stdout + r.stderr
     assert r.returncode == 0, out[-4000:]
     assert "ERROR: AddressSanitizer" not in out and "runtime error:" not in out, out[-4000:]
+
+
+def test_a_workspace_for_every_call():
+    """LOWBIT_CACHE_ATTENTION_WORKSPACE_BYTES covers any call (the size that one call can use falls as a batch grows), and no more than that is asked for."""
+    size = lambda **kw: int(_lib.lib().lowbit_cache_attention_workspace_size(problem(**kw)))  # noqa: E731
+    most = 0
+    for batch in (1, 2, 5, 8, 17, 31, 64, 128, 255, 256, 300):
+        for q_len in (1, 2, 4, 5, 16, 17, 27, 32, 33, 64, 128, 500):
+            for kv_len in (300, 1000, 2100, 16000, 40007, 1 << 22):
+                for hq, hk in ((1, 1), (32, 8), (16, 2), (64, 1)):
+                    for dim in (64, 128):
+                        for bits in (4, 8, 16):
+                            n = size(batch=batch, q_len=q_len, kv_len=kv_len, q_heads=hq, heads=hk, dim=dim, bits=bits, q_head=128, o_head=128)
+                            assert n <= lb.CACHE_ATTENTION_WORKSPACE_BYTES, (batch, q_len, kv_len, hq, hk, dim, bits, n)
+                            most = max(most, n)
+    assert most == lb.CACHE_ATTENTION_WORKSPACE_BYTES
+    with open(os.path.join(ROOT, "include", "lowbit.h")) as f:
+        assert f"#define LOWBIT_CACHE_ATTENTION_WORKSPACE_BYTES {lb.CACHE_ATTENTION_WORKSPACE_BYTES}\n" in f.read()

@@ -136,3 +136,16 @@ def test_kept_drafts_hold_what_was_verified(bits):
             m.keep(requests, r, path)
             for was, now in zip(drafted, m.stored(requests, r, n + len(path))):
                 assert torch.equal(now[:n], was[:n]) and torch.equal(now[n:], was[n:][path])
+
+
+def test_scratch_serves_fewer_requests():
+    """The layer's workspace is enough for every number of requests and drafted tokens up to its rows: what a call can use grows as a batch shrinks."""
+    m = load()
+    layer = m.Layer(128, 8, 8, 128)
+    requests = m.Requests(layer, 1, 4200, 8)
+    size = m.scratch(layer, requests, 7).numel()
+    assert size <= m.lb.CACHE_ATTENTION_WORKSPACE_BYTES
+    for rows in range(1, 8):
+        q = torch.empty(rows, 1, 8, 128, dtype=torch.bfloat16, device="cuda")
+        for x in (q, q.transpose(0, 1)):
+            assert m.lb.cache_attention_workspace_size(x, requests.cache, 4200) <= size
