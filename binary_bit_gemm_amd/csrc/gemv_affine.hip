@@ -228,8 +228,8 @@ hipError_t launch_rows(const GemvArgs& a, hipStream_t stream) {
     hipLaunchKernelGGL(kernel, dim3(grid), dim3(unsigned(64 * waves)), bytes, stream, a);
     e = hipGetLastError();
     if (e == hipSuccess && trace_enabled())
-        std::fprintf(stderr, "lowbit: gemv_affine rows=%d waves=%d g=%d grid=%u block=%d lds=%u problem=%dx%dx%d%s\n", 4 * MQ, waves, G, grid,
-                     64 * waves, bytes, a.M, a.N, a.K, SWIGLU ? " swiglu" : a.R != nullptr ? " residual" : "");
+        std::fprintf(stderr, "lowbit: gemv_affine rows=%d waves=%d g=%d grid=%u block=%d lds=%u problem=%dx%dx%d%s%s\n", 4 * MQ, waves, G, grid,
+                     64 * waves, bytes, a.M, a.N, a.K, SWIGLU ? " swiglu" : "", a.R != nullptr ? " residual" : "");
     return e;
 }
 

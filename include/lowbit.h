@@ -531,7 +531,7 @@ int lowbit_check_gemm_args(const void* X, const uint32_t* W, const void* S, cons
  *   lowbit: cache_attention <few|many> rows=<of a workgroup> splits=<of the keys> grid=<workgroups> block=<threads>
  *           problem=<batch>x<q_len>x<kv_len>x<q_heads> kv_heads=<kv_heads> dim=<head_dim> bits=<bits> page=<page_size>[ tree]
  *   lowbit: gemv_affine rows=<of X, in fours> waves=<of a workgroup> g=<g> grid=<workgroups> block=<threads> lds=<dynamic LDS bytes>
- *           problem=<M>x<N>x<K>[ swiglu| residual] */
+ *           problem=<M>x<N>x<K>[ swiglu][ residual] */
 const char* lowbit_gemm_variant(int64_t M, int64_t N, int64_t K, int g, int bits);
 
 /* Human-readable text for a status code. */

@@ -147,3 +147,14 @@ def test_launch_log(M, swiglu, residual, capfd, monkeypatch):
     torch.cuda.synchronize()
     lines = [t for t in capfd.readouterr().err.splitlines() if t.startswith("lowbit: gemv_affine ")]
     assert len(lines) == 1 and f"problem={M}x48x256" in lines[0] and lines[0].endswith("swiglu" if swiglu else "residual" if residual else "x256")
+
+
+def test_launch_log_names_both_forms(capfd, monkeypatch):
+    x, _, w, s, b = make(2, 96, 256, 64)
+    r = torch.zeros(2, 48, dtype=torch.bfloat16, device="cuda")
+    monkeypatch.setenv("LOWBIT_TRACE", "1")
+    capfd.readouterr()
+    lb.gemv_affine(x, w, s, b, 64, swiglu=True, residual=r)
+    torch.cuda.synchronize()
+    lines = [t for t in capfd.readouterr().err.splitlines() if t.startswith("lowbit: gemv_affine ")]
+    assert len(lines) == 1 and lines[0].endswith("problem=2x48x256 swiglu residual")
