@@ -438,3 +438,30 @@ def test_part_of_a_wider_table(kernel):
     assert torch.equal(one[0], one[1]) and torch.equal(one[:1], want[:1])
     with pytest.raises(ValueError, match="page_table"):
         lb.cache_attention(p.q, p.cache, p.table.t().contiguous().t(), lens, kv_len=200)
+
+
+@pytest.mark.parametrize("bits", [4, 8, 16])
+@pytest.mark.parametrize("scale", [0.02, 0.5, 1.0])
+def test_scales_other_than_the_default(scale, bits, kernel):
+    for dim, lens, new in ((64, [90, 7], [3, 2]), (128, [700], [5]), (128, [1, 60], [1, 1])):
+        p = Problem(lens, new, 4, 2, dim, bits, 32, seed=35)
+        for ws in ("enough", None):
+            p.check(p.call(ws, scale=scale), scale=scale)
+
+
+@pytest.mark.parametrize("bits", [4, 8, 16])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_trees_of_unequal_sizes(dim, bits, kernel):
+    """Requests with fewer drafted tokens than the tree has rows, bits set past a request's last token (which say nothing), no drafted token at all,
+    more of them than keys; rows past the last are left as they were."""
+    nodes, q_lens, lens = 40, [40, 7, 0, 23, 33], [300, 77, 50, 23, 12]
+    tree = [random_tree(nodes, s) for s in range(5)]
+    p = Problem(lens, q_lens, 4, 2, dim, bits, 16, tree=tree, seed=36)
+    clean = p.call(out=torch.full_like(p.q, 3.0))
+    p.check(clean)
+    p.tree = [[t | (0xFFFFFFFFFFFFFFFF << n & 0xFFFFFFFFFFFFFFFF) for t in row] for row, n in zip(tree, q_lens)]
+    for ws in ("enough", None):
+        got = p.call(ws, out=torch.full_like(p.q, 3.0))
+        p.check(got)
+        for b, n in enumerate(q_lens):
+            assert (got[b, n:] == 3).all()

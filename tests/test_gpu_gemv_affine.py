@@ -158,3 +158,19 @@ def test_launch_log_names_both_forms(capfd, monkeypatch):
     torch.cuda.synchronize()
     lines = [t for t in capfd.readouterr().err.splitlines() if t.startswith("lowbit: gemv_affine ")]
     assert len(lines) == 1 and lines[0].endswith("problem=2x48x256 swiglu residual")
+
+
+@pytest.mark.parametrize("M,N,K,g", SHAPES)
+def test_swiglu_and_a_residual_together(M, N, K, g):
+    x, levels, w, s, b = make(M, 2 * N, K, g, seed=5)
+    y, bound = products(x, levels, s, b, g)
+    gate, up, eg, eu = y[:, :N], y[:, N:], bound[:, :N], bound[:, N:]
+    silu = gate / (1 + np.exp(-gate))
+    r = (torch.randn(M, N, generator=torch.Generator().manual_seed(10)) * 3).bfloat16().cuda()
+    want = silu * up + r.double().cpu().numpy()
+    off = np.abs(up) * 1.1 * eg + np.abs(silu) * eu + 1.1 * eg * eu + 2.0 ** -20 * np.abs(silu * up) + 2.0 ** -24 * np.abs(want)
+    got = lb.gemv_affine(x, w, s, b, g, residual=r, swiglu=True)
+    check(got, want, off)
+    out = r.clone()
+    assert lb.gemv_affine(x, w, s, b, g, residual=out, swiglu=True, out=out) is out  # in place
+    assert torch.equal(out, got)
