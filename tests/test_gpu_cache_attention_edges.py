@@ -465,3 +465,17 @@ def test_trees_of_unequal_sizes(dim, bits, kernel):
         p.check(got)
         for b, n in enumerate(q_lens):
             assert (got[b, n:] == 3).all()
+
+
+def test_pages_named_twice_change_their_request_alone(kernel):
+    """A table that names a page of the common prefix twice for request 0; request 1 keeps the shared prefix."""
+    p = Problem([128, 128], [4, 4], 4, 2, 128, 8, 32, seed=37)
+    p.table[1, :2] = p.table[0, :2]
+    for x in (p.k, p.v):
+        x[1][:64] = x[0][:64]
+    p.check(p.call())
+    p.answers.clear()
+    p.table[0, 1] = p.table[0, 0]
+    for x in (p.k, p.v):
+        x[0] = torch.cat([x[0][:32], x[0][:32], x[0][64:]])
+    p.check(p.call())
