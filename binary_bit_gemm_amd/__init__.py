@@ -864,7 +864,8 @@ def cache_attention(q, cache: KVCache, page_table, key_lens, q_lens=None, tree=N
 
 def gemv_affine(x, words, scales, biases, g: int, residual=None, swiglu: bool = False, out=None):
     """gemm_affine for up to 16 rows (lowbit_gemv_affine): Y = X . W^T (+ residual), W = S * u + B with `words` from pack_u4.  swiglu: words,
-    scales and biases hold 2N rows, gate then up, and Y = silu(X . Wg^T) * (X . Wu^T) (+ residual).  residual bf16 [M, N], may be `out`."""
+    scales and biases hold 2N rows, gate then up, and Y = silu(X . Wg^T) * (X . Wu^T) (+ residual).  residual bf16 [M, N], may be `out`.  An
+    infinite element of x leaves its row of Y without a finite number."""
     torch = _torch()
     _require(x, torch.bfloat16, "x")
     M, K = x.shape

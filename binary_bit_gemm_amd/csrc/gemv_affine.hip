@@ -14,7 +14,7 @@
 //     (2, 6), (3, 7) of a word, and X's operand is permuted to that order.  Per group
 //         S sum x u + B sum x = S sum x (128 + u) + (B - 128 S) sum x,
 //     with sum x from the matrix cores too (a product with ones).  Both sums are fp32, S and B multiply after them: no
-//     weight is rounded.
+//     weight is rounded.  (With an infinite x the two terms are infinities of opposite signs: NaN.)
 // Launch included: 1 x 9728 x 2560 with gate and up rows 8.1 us (28 MB, 3.5 TB/s), 1 x 2560 x 9728 with a residual 6.7 us, 11 x 2560 x 4096 5.0 us.
 #include <atomic>
 #include <cstdio>

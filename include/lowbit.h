@@ -507,7 +507,10 @@ int lowbit_cache_attention(const lowbit_cache_attention_problem* problem, void* 
  *       lowbit_gemm_swiglu.
  *   residual  device bf16 [M, N] or NULL; may be Y itself.
  * Other arguments, checks and errors as lowbit_gemm_affine; M > 16 returns LOWBIT_E_UNSUPPORTED.  Sums are fp32 with no weight
- * rounded, Y is rounded to bf16 once (the last bits can differ from lowbit_gemm_affine's).
+ * rounded, Y is rounded to bf16 once (the last bits can differ from lowbit_gemm_affine's).  A group's part is S sum x (128 + u) +
+ * (B - 128 S) sum x: 143 times a group's sum of |x|, and |S| times that, have to lie inside fp32's range, and an infinite element of X gives its row
+ * of Y NaN or infinities whatever sign the formula's would have (lowbit_gemm_affine, whose terms are sum 16 u x and B sum x: 240 times,
+ * and likewise).
  */
 int lowbit_gemv_affine(const void* X, const uint32_t* W, const void* S, const void* B, const void* residual, void* Y, int64_t M,
                        int64_t N, int64_t K, int g, int swiglu, void* stream);

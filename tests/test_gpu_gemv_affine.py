@@ -174,3 +174,20 @@ def test_swiglu_and_a_residual_together(M, N, K, g):
     out = r.clone()
     assert lb.gemv_affine(x, w, s, b, g, residual=out, swiglu=True, out=out) is out  # in place
     assert torch.equal(out, got)
+
+
+@pytest.mark.parametrize("M,N,K,g", [(1, 32, 320, 64), (3, 48, 256, 128), (11, 16, 2560, 64), (16, 32, 192, 64)])
+def test_large_and_infinite_activations(M, N, K, g):
+    """Elements up to 2^110 (143 times a group of 128 of them is below 2^125): sums stay finite and right.  An infinite one leaves its row of Y without a
+    number, and the other rows as they were to the bit."""
+    x, levels, w, s, b = make(M, N, K, g, seed=6)
+    clean = lb.gemv_affine(x, w, s, b, g)
+    big = (x.float() * 2.0 ** 107).bfloat16()  # exact: a power of two; randn stays below 2^3
+    assert float(big.abs().max()) < 2.0 ** 110
+    y, bound = products(big, levels, s, b, g)
+    check(lb.gemv_affine(big, w, s, b, g), y, bound)
+    for value in (float("inf"), -float("inf")):
+        odd = x.clone()
+        odd[M - 1, K // 2] = value
+        got = lb.gemv_affine(odd, w, s, b, g)
+        assert torch.equal(got[:M - 1], clean[:M - 1]) and not got[M - 1].isfinite().any()
