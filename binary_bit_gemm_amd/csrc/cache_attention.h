@@ -28,6 +28,9 @@
 //
 // Rounding: p s to fp16 (2^-11 of each; 16 bits: p to bf16, 2^-8 of each) and O to bf16; all else is fp32.  fp16 holds 24 bits below its normal
 // range: a weight is off by 2^-25 of the row's largest at least, which shows only where one group's scales are 2^12 below the other's.
+// A 16-bit cache's values are bf16 and a matrix instruction takes both operands in one type, so p has bf16's 8 bits there, as in lowbit_attention; a
+// second product with what that rounding leaves would double the value products.  Trees of 64 over 4 x 4099 keys: 0.0023 of O's norm off
+// the formula in 64 bits, 0.0017 of it by the rounding of O; at 8 and 4 bits 0.0017 and 0.0018.
 #pragma once
 
 #include "kv_cache.h"
@@ -847,8 +850,9 @@ __device__ __forceinline__ uint16_t* o_row(const CacheAttnArgs& a, const CacheWo
 // Bound by the cache's bytes where there are many, one wave's chain of latencies where there are few: a start of 2.5 us (lengths, then the
 // table, then the first tile, each waiting for the last), a microsecond a tile and wave, 3 to 5 us for the join of split ranges.  Page
 // numbers come by scalar loads, so that waiting for one leaves the tiles' loads in flight; a vector load's wait drains them.  8 kv heads of 128 (us, kernel
-// and launch): 77 keys 5.4; 61 requests of up to 2050 keys, 8 bits, 34.8, 4.6 TB/s; one of 40,007 keys in 4 bits 19.3, half of them in the loop
-// at 4.5 TB/s.
+// and launch, the cache from HBM): 61 requests of 1025 to 2050 keys, 8 bits, 40.9 (201 MB, 4.9 TB/s); one of 40,007 keys in 4 bits 20.1 (46 MB), half
+// of them in the loop; four of 2050 to 4099 in 8 bits 13.3.  Replayed, with the cache or part of it left in the last-level cache: 34.6, 19.2 and 11.4;
+// one of 77 keys 5.2.
 template <int D, int BITS>
 __global__ __launch_bounds__(256, 2) void cache_attention_kernel(CacheAttnArgs a) {
     constexpr int NB = 1, kWaves = 4, kRows = 16;

@@ -21,8 +21,9 @@ static_assert(LOWBIT_CACHE_ATTENTION_WORKSPACE_BYTES == kWorkspaceCounterBytes +
 
 // Up to 16 rows: one workgroup per compute unit at most, of four tiles of 32 keys at least (a tile a wave; 16 bits, whose tiles are larger:
 // two), and past 12 ranges (24) of eight (four), since a join costs about 2 us: none below 16 tiles.  Measured, one token, 8 kv heads of 128, 8 bits
-// (us by ranges): 700 keys 1: 9.2, 6: 8.6; 1500 keys 3: 10.7, 12: 9.2, 16: 9.4; 3000 keys 7: 10.8, 12: 10.0, 32: 10.8; 16 bits 1500 keys 3: 14.7, 24:
-// 10.5 (all 0.3 to 1 us less since).
+// (us by ranges): 700 keys 1: 8.7, 6: 8.2; 1500 keys 3: 10.1, 12: 8.7, 16: 9.0; 3000 keys 7: 10.2, 12: 9.4, 32: 10.6; 16 bits 1500 keys 3: 12.3, 24: 9.4.
+// Ranges come in whole numbers per unit, so past half as many groups as units keys are not split, and units are left over: with 8 kv heads 16 requests
+// over 16,000 keys take 93 us in 8 bits (178 in 16, 54 in 4), 17 take 135 (202, 66), 32 take 175 (340, 109); over 4000 25, 29 and 40.
 int64_t few_splits(int64_t groups, int64_t tiles, int bits) {
     if (tiles < 16) return 1;
     const int64_t least = bits == 16 ? 2 : 4, small = bits == 16 ? 24 : 12;
@@ -36,8 +37,8 @@ int64_t few_splits(int64_t groups, int64_t tiles, int bits) {
 }
 
 // Many rows: one workgroup per compute unit at most, of two tiles at least, where that takes eight tiles or more off each; otherwise the join (3.5 us
-// and the parts' way through memory) costs more than it saves.  Measured, trees of 12 over 300 keys, 8 kv heads of 128, 8 bits (us by ranges) 1:
-// 12.4, 5: 10.8; of 64 over 4000 keys 2: 36, 4: 26, 8: 20.6.
+// and the parts' way through memory) costs more than it saves.  Measured, trees of 12 over 300 keys, 8 kv heads of 128, 8 bits, 64 rows (us by ranges) 1:
+// 12.9, 5: 10.2; of 64 over 4000 keys 2: 46, 4: 28, 8: 19.9.  The same whole numbers: trees of 16 over 4000 keys, 64 rows a tile, 16 requests 50 us, 17 80.
 int64_t many_splits(int64_t groups, int64_t tiles) {
     int64_t splits = kComputeUnits / groups;
     splits = splits < tiles / 2 ? splits : tiles / 2;
@@ -56,8 +57,9 @@ CacheAttnPlan plan_cache_attention(const CacheAttnArgs& a, bool may_split) {
     const int64_t few = may_split && few_groups > 0 ? few_splits(few_groups, tiles, a.cache.bits) : 1;
     // Up to 16 rows the kernel that feeds registers from memory starts and ends sooner and keeps more loads in flight; the one that shares tiles joins
     // many ranges of many rows faster (a workgroup per four rows, not one for all).  Measured (us, few / many with 32 rows), 8 kv heads of 128: 8 bits,
-    // 4 rows over 16,000 keys 13.9 / 16.1, 32 requests of 4 rows over 4000 42 / 51, 16 rows over 2000 13.4 / 11.4, 12 over 16,000 18.3 / 16.4; 16
-    // bits, 4 rows over 1500 keys 9.4 / 10.9, over 40,000 29.9 / 32.3, 16 over 2000 13.7 / 12.0, 12 over 16,000 21.0 / 20.4.
+    // 4 rows over 16,000 keys 13.0 / 16.2, 32 requests of 4 rows over 4000 40 / 51; 16 bits, 4 rows over 1500 keys 9.3 / 10.9, over 40,000 30.6 / 32.0, 16
+    // over 2000 13.6 / 12.0, 12 over 16,000 21.0 / 20.6.  At 8 bits the two are close with more than 8 rows: 16 over 2000 10.8 / 11.4, 12 over 16,000
+    // 16.6 / 17.1.
     // Over short caches (32 tiles) it also takes more rows, 16 to a workgroup, up to two workgroups a unit: 64 rows over 300 keys 7.3 / 10.8, 256
     // rows 7.4 / 11.4; four requests of 108 rows over 1000 keys 10.8 / 15.7; 16 of 108 over 300, 896 workgroups, 17.2 / 13.8.  Past that the two are
     // within 10% of each other up to 2000 keys.
@@ -78,7 +80,7 @@ CacheAttnPlan plan_cache_attention(const CacheAttnArgs& a, bool may_split) {
     } else {
         // 128 rows of a workgroup read a tile from LDS for twice the rows; 64 start and end sooner: 128 where 64 would have more than 20 tiles.
         // Measured (64 / 128 rows, us; 8 kv heads of 128, 8 bits; in brackets tiles of a workgroup of 64): 64 tokens, one request of 4000 keys
-        // [16] 20.6 / 21.7, four of 1000 [16] 23.7 / 25.2, four of 4000 [63] 51 / 45; 27 tokens in 4 bits, heads of 64, three of 8191 [26] 22.3 / 19.4.
+        // [16] 19.9 / 21.5, four of 1000 [16] 22.8 / 24.3, four of 4000 [63] 50 / 43; 27 tokens in 4 bits, heads of 64, three of 8191 [26] 21.9 / 20.8.
         p.tile_rows = only == 32 || (only == 0 && rows <= 32) ? 32 : 64;
         const int64_t groups = heads * tiles_of(rows, p.tile_rows);
         splits = may_split && groups > 0 ? many_splits(groups, tiles) : 1;

@@ -15,7 +15,11 @@
 //         S sum x u + B sum x = S sum x (128 + u) + (B - 128 S) sum x,
 //     with sum x from the matrix cores too (a product with ones).  Both sums are fp32, S and B multiply after them: no
 //     weight is rounded.  (With an infinite x the two terms are infinities of opposite signs: NaN.)
-// Launch included: 1 x 9728 x 2560 with gate and up rows 8.1 us (28 MB, 3.5 TB/s), 1 x 2560 x 9728 with a residual 6.7 us, 11 x 2560 x 4096 5.0 us.
+// Launch included, us with the weights from HBM (left in the last-level cache by the pass before): 1 x 9728 x 2560 with gate and up rows 11.7 (8.1;
+// 28 MB, 2.4 TB/s), 1 x 2560 x 9728 with a residual 8.6 (6.8), 11 x 2560 x 4096 6.5 (5.1).  A wave waits for memory once per turn of kSteps: all
+// four waves of the first take a second turn for a single step, twelve of the second's sixteen and two of the third's fifteen do.
+// lowbit_gemm_affine's tile kernel, weights from HBM, at 1 as at 16 rows: 19456 x 2560 23.5 (here 10.6 with 1 row, 16.9 with 16), 2560 x 9728 46.5
+// (8.3, 12.7), 2560 x 4096 23.0 (5.1, 6.7).
 #include <atomic>
 #include <cstdio>
 

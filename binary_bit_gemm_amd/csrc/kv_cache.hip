@@ -10,9 +10,13 @@
 // Bound by memory (every element read once and written once) or, for a few tokens, by the launch and the two loads that wait for each other (the
 // slot, then the row).  8 elements per lane: 16 or 8 lanes hold a token's row of a head.  A wave takes keys and values of its rows together: one
 // look at the slot, twice the loads in flight; maxima meet by operand routing within 16 lanes, and codes cost one division a row.  With a wave for
-// keys and another for values, exchanges through shared memory and a division an element, the first and the last of these took 21 and 10 us:
-//   16,510 tokens of 8 heads of 128 read back from 4 bits: 15.9 us, 5.3 TB/s; 1 token of 61 requests written, 8 bits: 3.5 us;
-//   4,084 tokens of 16 heads of 64 written in 8 bits: 7.4 us, 3.4 TB/s.
+// keys and another for values, exchanges through shared memory and a division an element, 16,510 tokens read from 4 bits and 4,084 of 16 heads of 64
+// written in 8 took 21 and 10 us with their data in the last-level cache, where they take 15.3 and 6.4.
+// Measured, 8 heads of 128, everything from and to HBM, launch included (us at 16, 8 and 4 bits; with what the last pass left in the caches):
+//   61 tokens written 2.0, 2.6, 2.8, read 2.0, 2.1, 2.2;
+//   4,084 tokens written 9.9, 8.2, 8.5 (6.4, 6.3, 6.9), read 9.9, 7.9, 7.6 (5.2, 5.4, 6.0);
+//   16,510 tokens written 28.3, 24.3, 24.9 (21.2, 20.0, 21.5), read 27.8, 23.1, 21.8 (20.9, 16.8, 15.3): 135, 102 and 87 MB, 4.8, 4.2 and 3.5 TB/s
+//   written, 4.9, 4.4 and 4.0 read.
 #include "kv_cache.h"
 #include "lowbit_device.h"
 #include "decode_internal.h"

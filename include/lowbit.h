@@ -472,9 +472,11 @@ int lowbit_cache_read(const lowbit_cache* cache, void* k, void* v, int64_t token
  *   A row that takes no key gets zeros.  Slots that no row takes may hold anything; a NaN in a key or value reaches the rows that take it,
  * an infinite value too (as an infinity or, where its weight underflows, a NaN).
  * Scores, softmax statistics and sums are fp32; a probability times its value's scale is rounded to fp16 (16 bits: the
- * probability to bf16, and the sum that divides is of the rounded ones) for the second product, O to bf16 once.  At 8 and 4 bits fp32's range holds what arises on the way for rows of V whose
- * largest magnitudes lie between 2^-50 and 2^30 (or are 0), where scale times a row's largest |q|, and that times its keys' largest |k|, are below
- * 2^117 (past it the row can be NaN).  Deterministic.
+ * probability to bf16, and the sum that divides is of the rounded ones) for the second product, O to bf16 once.  At 8 and 4 bits q is held
+ * in fp16 times a power of two per row (elements 2^28 below the row's largest, at 4 bits 2^24, lose bits), and at 4 bits a group of V whose
+ * scales lie 2^12 and more below the other group's keeps fewer bits (2^-25 of the row's largest weight).  fp32's range holds what arises on the
+ * way there for rows of V whose largest magnitudes lie between 2^-50 and 2^30 (or are 0), where scale times a row's largest |q|, and that times its
+ * keys' largest |k|, are below 2^117 (past it the row can be NaN).  Deterministic.
  *   workspace  as for lowbit_attention: lowbit_cache_attention_workspace_size(problem) bytes (0: none), 16-byte aligned,
  *          zero-filled before its first use, shared by calls that do not run at once; with none or too little the keys are not split
  *          across workgroups.  That size can grow as a batch shrinks (its keys are split further): a program whose batch changes keeps
