@@ -106,7 +106,7 @@ def gemm_affine(x, words, scales, biases, g: int, out=None, workspace=None):
     """Y = X . W^T with affine 4-bit groups W = S * q + B (lowbit_gemm_affine): `words` from
     pack_u4, `scales` and `biases` fp16 [N, K/g].  `workspace`: an optional zero-filled device
     tensor of at least affine_workspace_size(M, N, K, g) bytes (lowbit_gemm_affine_ex), with which
-    shapes whose tile grid leaves compute units idle split K across workgroups."""
+    shapes whose tile grid leaves compute units idle split K across workgroups.  Up to 16 rows: gemv_affine is faster."""
     torch = _torch()
     _require(x, torch.bfloat16, "x")
     _require(words, torch.int32, "words")
@@ -763,7 +763,8 @@ def cache_write(cache: KVCache, k, v, slots) -> None:
 
 def cache_read(cache: KVCache, slots, k_out=None, v_out=None):
     """The rows at `slots` (int32 [tokens]) as bf16 [tokens, kv_heads, head_dim] (lowbit_cache_read): (k_out, v_out).  Rows whose slot
-    is outside the cache are left as they were (zeros where the output is made here)."""
+    is outside the cache are left as they were (zeros where the output is made here).  At 8 and 4 bits a row read back and written again is
+    quantised a second time."""
     if k_out is None or v_out is None:
         torch = _torch()
         _require_cache(cache)

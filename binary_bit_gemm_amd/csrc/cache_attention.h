@@ -28,7 +28,8 @@
 //
 // Rounding: p s to fp16 (2^-11 of each; 16 bits: p to bf16, 2^-8 of each) and O to bf16; all else is fp32.  fp16 holds 24 bits below its normal
 // range: a weight is off by 2^-25 of the row's largest at least, which shows only where one group's scales are 2^12 below the other's.
-// A 16-bit cache's values are bf16 and a matrix instruction takes both operands in one type, so p has bf16's 8 bits there, as in lowbit_attention; a
+// A 16-bit cache's values are bf16 and a matrix instruction takes both operands in one type, so p has bf16's 8 bits there, as in lowbit_attention: with
+// the sum taken of the rounded ones O is off by 2^-8 sum p |v - O| at most, nothing where one key has the weight.  A
 // second product with what that rounding leaves would double the value products.  Trees of 64 over 4 x 4099 keys: 0.0023 of O's norm off
 // the formula in 64 bits, 0.0017 of it by the rounding of O; at 8 and 4 bits 0.0017 and 0.0018.
 #pragma once

@@ -288,7 +288,7 @@ int lowbit_gemm_residual(const void* X, const uint32_t* W, const void* S, const 
  * matrix cores against an all-ones operand), is added in fp32; Y is rounded to bf16 once.
  * g = 64 or 128 (g = 32 returns LOWBIT_E_UNSUPPORTED).  A null or unaligned B with K > 0 returns
  * LOWBIT_E_INVALID / LOWBIT_E_ALIGN; other checks as lowbit_gemm with bits = 4.  K = 0 gives
- * Y = 0.  Runs on the 16x16-block tile kernel at every M.
+ * Y = 0.  Runs on the 16x16-block tile kernel at every M; lowbit_gemv_affine is faster for up to 16 rows.
  */
 int lowbit_gemm_affine(const void* X, const uint32_t* W, const void* S, const void* B, void* Y,
                        int64_t M, int64_t N, int64_t K, int g, void* stream);
